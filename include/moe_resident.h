@@ -47,7 +47,7 @@ typedef enum {
     MOE_ECUDA = 2,         /* a CUDA runtime call or launch failed */
     MOE_ENOMEM = 3,        /* workspace smaller than the matching *_workspace_bytes() */
     MOE_ETIMEOUT = 4,      /* device error word: a bounded wait in a kernel ran out */
-    MOE_EDEVICE = 5,       /* device error word: bad slot id / NaN scale / bad table */
+    MOE_EDEVICE = 5,       /* device error word: bad slot id / NaN scale / bad table / bad page */
     MOE_EUNSUPPORTED = 6,  /* a size past a documented limit */
     MOE_EIO = 7            /* a file could not be read or written (demand history) */
 } moe_status;
@@ -60,6 +60,8 @@ typedef enum {
 #define MOE_DEV_TIMEOUT     0x4u   /* a pipeline wait gave up after its limit */
 #define MOE_DEV_BAD_TABLE   0x8u   /* slot_of / owner tables inconsistent (re-plan, ring) */
 #define MOE_DEV_RESIDENT    0x10u  /* ring install of an expert that is already resident */
+#define MOE_DEV_BAD_PAGE    0x20u  /* key/value cache: a row, page id, path or lane length out of range */
+#define MOE_DEV_NAN_KV      0x40u  /* moe_kv_write met a key or value vector that is not finite */
 
 /*
  * The shared slot arena (README item 1: a single arena serves every layer).
@@ -371,6 +373,131 @@ moe_status moe_hot_read_sync(const uint64_t* store, const uint64_t* demand, cons
                              int32_t* slot_of, int32_t* owner, const moe_arena* arena, int layer, int L, int E,
                              float threshold, int32_t* budget, int32_t* swap, void* stream);
 
+/*
+ * Paged key/value cache of one attention layer in 8 bits, and attention of
+ * drafted tokens over it: the half of a decode step that stands in front of
+ * the routed experts. (The TideLM README keeps an 8-bit KV cache in a pool of
+ * pages shared by the lanes and checks drafted tokens; it gives no layout and
+ * no formula, so the format below is this library's own.)
+ *
+ * A cache row holds one token's keys and values. Every (row, head) vector x of
+ * head_dim values is head_dim e4m3 codes and one e8m0 scale byte s:
+ *   e    = the smallest integer in [-100, 120] with max|x| <= 448 * 2^e,
+ *          0 for a zero vector
+ *   code = e4m3(x * 2^-e)     (round to nearest, ties to even)
+ *   s    = e + 127;           the vector stands for code * 2^(s - 127)
+ * A power of two costs a floating-point code no precision, makes quantising
+ * and reading back exact up to the one rounding, and lets a kernel fold the
+ * scale into an exponent. A vector with a value that is not finite is stored
+ * as s = 255 and zero codes; it stands for NaN throughout, and never puts a
+ * NaN code beside finite ones.
+ *
+ * Passed by HOST pointer; k/v pointers are device memory, contiguous:
+ *   codes  [n_pages, n_kv_heads, page_size, head_dim] bytes, 16-byte aligned
+ *   scales [n_pages, n_kv_heads, page_size] bytes, 16-byte aligned
+ * Row i of a lane is row i % page_size of page page_table[lane, i / page_size].
+ * Codes 0x7F / 0xFF (NaN) are not written by this library and must not occur
+ * in rows that a call reads.
+ * Limits: page_size a power of two, 16..1024; head_dim 64, 128 or 256;
+ * 1 <= n_kv_heads <= 1024; n_pages * n_kv_heads * page_size < 2^31.
+ */
+typedef struct {
+    void*    k_codes;
+    void*    v_codes;
+    uint8_t* k_scales;
+    uint8_t* v_scales;
+    int32_t  n_pages;
+    int32_t  n_kv_heads;
+    int32_t  page_size;
+    int32_t  head_dim;
+} moe_kv_cache;
+
+/* Element types of the floating-point side of moe_kv_write and moe_kv_read. */
+#define MOE_BF16 0
+#define MOE_FP16 1
+#define MOE_FP32 2
+
+/*
+ * Quantises the keys and values of T tokens into their cache rows.
+ * k, v [T, n_kv_heads, head_dim] of `dtype`, the last axis contiguous, token
+ * and head strides in elements (so both may be parts of one projection's
+ * output); pointers 16-byte aligned and strides multiples of 16 bytes
+ * (MOE_EINVAL). slots int64 [T]: token t goes to row slots[t] % page_size of
+ * page slots[t] / page_size; -1 skips the token. Another slot outside the
+ * cache is skipped and sets MOE_DEV_BAD_PAGE; a vector that is not finite sets
+ * MOE_DEV_NAN_KV. Two tokens with one slot: either may win.
+ * T = 0 returns MOE_OK without a launch; T * n_kv_heads <= 2^27.
+ */
+moe_status moe_kv_write(const void* k, const void* v, int dtype, int64_t k_token_stride, int64_t k_head_stride,
+                        int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots, int T,
+                        const moe_kv_cache* cache, void* stream);
+
+/*
+ * Reads cache rows back: for lane b and 0 <= i < cu_rows[b+1] - cu_rows[b],
+ *   k_out[cu_rows[b] + i], v_out[...] = the values of row starts[b] + i of lane b
+ * cast once to `dtype` (exact in bf16 and fp32, and in fp16 inside its range). k_out, v_out
+ * [n_rows, n_kv_heads, head_dim] contiguous, 16-byte aligned. page_table int32
+ * [lanes, table_width]; starts int32 [lanes] or NULL (0); cu_rows int32
+ * [lanes + 1], ascending from 0 to n_rows. A row outside the table or a page
+ * id outside the cache reads as NaN and sets MOE_DEV_BAD_PAGE.
+ * n_rows = 0 returns MOE_OK without a launch. Limits: lanes <= 65,536,
+ * n_rows * n_kv_heads <= 2^27.
+ */
+moe_status moe_kv_read(const moe_kv_cache* cache, const int32_t* page_table, int table_width, int lanes,
+                       const int32_t* starts, const int32_t* cu_rows, int n_rows, int dtype, void* k_out, void* v_out,
+                       void* stream);
+
+/*
+ * Keeps the accepted path of a checked tree: in every lane b, for i <
+ * n_keep[b], row prefix[b] + path[b, i] moves to row prefix[b] + i (codes and
+ * scales, in place, every source read before it is overwritten). path int32
+ * [lanes, path_width], each lane's first n_keep[b] entries ascending from >= 0;
+ * n_keep[b] <= 0 leaves the lane alone. A lane with a path that is not
+ * ascending, or with a row outside its table or the cache, is left alone and
+ * sets MOE_DEV_BAD_PAGE. Lanes share no rows that move.
+ * Limits: lanes <= 65,536, path_width <= 4096.
+ */
+moe_status moe_kv_keep(const moe_kv_cache* cache, const int32_t* page_table, int table_width, int lanes,
+                       const int32_t* prefix, const int32_t* path, int path_width, const int32_t* n_keep,
+                       void* stream);
+
+/*
+ * Attention of the tree nodes of every lane over the lane's cache rows. Lane b
+ * has n = cu_nodes[b+1] - cu_nodes[b] nodes (drafted tokens; one for a plain
+ * decode step, none for a lane that waits) whose rows are the last n of its
+ * kv_len[b] rows, already written; node t's queries are q[cu_nodes[b] + t]. It
+ * sees the rows j < prefix = kv_len[b] - n, and row prefix + i where bit i % 32
+ * of word i / 32 of tree_mask[cu_nodes[b] + t] is set (set a node's own bit to
+ * have it see itself). Without a mask (NULL) it sees the rows up to its own: a
+ * chain of drafted tokens, a single token, a chunk of a prompt.
+ *   score[j] = scale * q . k[j],   p = softmax of the scores of the rows seen
+ *   out      = sum_j p[j] v[j],    lse = log sum_j exp(score[j])
+ * A node that sees no row gets zeros and lse = -inf. Rows that a node does not
+ * see never touch its result, whatever they hold.
+ * q bf16 [n_nodes, n_q_heads, head_dim], last axis contiguous, strides in
+ * elements (multiples of 8), 16-byte aligned; query head h reads kv head
+ * h / (n_q_heads / n_kv_heads). page_table int32 [lanes, table_width] (entries
+ * past a lane's rows are not read); kv_len int32 [lanes]; cu_nodes int32
+ * [lanes + 1] ascending from 0 to n_nodes; tree_mask int32 [n_nodes,
+ * mask_words] or NULL; max_nodes: an upper bound on a lane's nodes (host
+ * value; with a mask, at most 32 * mask_words). out bf16 [n_nodes, n_q_heads,
+ * head_dim] contiguous, 16-byte aligned; lse fp32 [n_nodes, n_q_heads] or NULL.
+ * A lane with more than max_nodes nodes, fewer rows than nodes or more rows
+ * than its table holds sets MOE_DEV_BAD_PAGE and gets zeros and -inf. A page
+ * id outside the cache sets it too; page 0 is read in its place.
+ * workspace: >= moe_tree_attention_workspace_bytes(...), 16-byte aligned; its
+ * contents need not be kept or cleared between calls. Calls that overlap on
+ * the GPU need one each.
+ * scale > 0. n_nodes = 0 returns MOE_OK without a launch. Limits: lanes <= 4096, n_q_heads a
+ * multiple of n_kv_heads and at most 1024, max_nodes <= 65,536, mask_words <= 2048.
+ */
+size_t     moe_tree_attention_workspace_bytes(int n_nodes, int n_q_heads, int n_kv_heads, int head_dim, int lanes);
+moe_status moe_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int n_nodes,
+                              int n_q_heads, const moe_kv_cache* cache, const int32_t* page_table, int table_width,
+                              int lanes, const int32_t* kv_len, const int32_t* cu_nodes, int max_nodes,
+                              const int32_t* tree_mask, int mask_words, float scale, void* out, float* lse,
+                              void* workspace, size_t ws_bytes, void* stream);
+
 /* Workspace sizes (bytes) for the calls above. */
 size_t moe_workspace_bytes(int T, int k, int d, int ffn, int E, int n_slots);
 size_t moe_replan_workspace_bytes(int L, int E);
@@ -413,7 +540,7 @@ moe_status moe_device_status(void* stream, uint32_t* bits);
 
 /*
  * Bound on every wait inside the library's pipelined kernels (the expert
- * FFN's GEMMs and the tensor-core router), in nanoseconds of wall-clock time
+ * FFN's GEMMs, the tensor-core router and tree attention), in nanoseconds of wall-clock time
  * counted from the wait's first failed try; ns = 0 restores the default, 2 s.
  * A healthy wait ends in microseconds; the bound exists so that a broken
  * pipeline cannot hang the GPU (failure detection in the spirit of the

@@ -25,6 +25,8 @@ LIB_PATH = os.path.join(_PKG, "libmoe_resident.so")
 
 MOE_OK, MOE_EINVAL, MOE_ECUDA, MOE_ENOMEM, MOE_ETIMEOUT, MOE_EDEVICE, MOE_EUNSUPPORTED, MOE_EIO = range(8)
 MOE_DEV_BAD_SLOT, MOE_DEV_NAN_SCALE, MOE_DEV_TIMEOUT, MOE_DEV_BAD_TABLE, MOE_DEV_RESIDENT = 0x1, 0x2, 0x4, 0x8, 0x10
+MOE_DEV_BAD_PAGE, MOE_DEV_NAN_KV = 0x20, 0x40
+MOE_BF16, MOE_FP16, MOE_FP32 = range(3)
 
 # Every symbol the header declares (checked by the CPU test suite).
 EXPORTS = ("moe_route_resident", "moe_route_resident_noalloc", "moe_demand_accumulate", "moe_hot_miss_select", "moe_expert_ffn_mxfp4",
@@ -33,7 +35,8 @@ EXPORTS = ("moe_route_resident", "moe_route_resident_noalloc", "moe_demand_accum
            "moe_profile_kernel_count", "moe_profile_read", "moe_profile_reset", "moe_demand_decay",
            "moe_demand_save", "moe_demand_load", "moe_hot_ring_create", "moe_hot_ring_step", "moe_hot_ring_destroy",
            "moe_hot_read_sync", "moe_renormalise_weights", "moe_expert_ffn_prefetch", "moe_set_wait_limit",
-           "moe_get_wait_limit", "moe_wait_selftest", "moe_arena_refill")
+           "moe_get_wait_limit", "moe_wait_selftest", "moe_arena_refill", "moe_kv_write", "moe_kv_read", "moe_kv_keep",
+           "moe_tree_attention", "moe_tree_attention_workspace_bytes")
 
 
 class MoeError(RuntimeError):
@@ -48,6 +51,13 @@ class MoeArena(ctypes.Structure):
                 ("d", ctypes.c_int32), ("ffn", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("off_gu_codes", ctypes.c_int64), ("off_gu_scales", ctypes.c_int64),
                 ("off_dn_codes", ctypes.c_int64), ("off_dn_scales", ctypes.c_int64)]
+
+
+class MoeKvCache(ctypes.Structure):
+    """Mirror of ``moe_kv_cache`` (passed by host pointer)."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 _P, _I, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
@@ -101,12 +111,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.moe_wait_selftest.argtypes = [_P]
     L.moe_arena_refill.argtypes = [ctypes.POINTER(MoeArena), ctypes.POINTER(ctypes.c_void_p), _I, _P, _P, _P, _P,
                                    _P, ctypes.POINTER(ctypes.c_int32)]
+    _I64, _KV = ctypes.c_int64, ctypes.POINTER(MoeKvCache)
+    L.moe_kv_write.argtypes = [_P, _P, _I, _I64, _I64, _I64, _I64, _P, _I, _KV, _P]
+    L.moe_kv_read.argtypes = [_KV, _P, _I, _I, _P, _P, _I, _I, _P, _P, _P]
+    L.moe_kv_keep.argtypes = [_KV, _P, _I, _I, _P, _P, _I, _P, _P]
+    L.moe_tree_attention_workspace_bytes.restype = _SZ
+    L.moe_tree_attention_workspace_bytes.argtypes = [_I, _I, _I, _I, _I]
+    L.moe_tree_attention.argtypes = [_P, _I64, _I64, _I, _I, _KV, _P, _I, _I, _P, _P, _I, _P, _I, _F, _P, _P, _P, _SZ, _P]
     for name in ("moe_route_resident", "moe_route_resident_noalloc", "moe_demand_accumulate", "moe_hot_miss_select",
                  "moe_expert_ffn_mxfp4",
                  "moe_arena_replan", "moe_ring_install", "moe_device_status", "moe_profile_enable",
                  "moe_profile_read", "moe_demand_decay", "moe_demand_save", "moe_demand_load", "moe_hot_ring_create",
                  "moe_hot_ring_step", "moe_hot_ring_destroy", "moe_hot_read_sync", "moe_renormalise_weights",
-                 "moe_expert_ffn_prefetch", "moe_set_wait_limit", "moe_wait_selftest", "moe_arena_refill"):
+                 "moe_expert_ffn_prefetch", "moe_set_wait_limit", "moe_wait_selftest", "moe_arena_refill",
+                 "moe_kv_write", "moe_kv_read", "moe_kv_keep", "moe_tree_attention"):
         L[name].restype = _I
     _lib = L
     return L
@@ -359,3 +377,115 @@ def moe_renormalise_weights(sel_slot, sel_w, stream=None) -> None:
     T, k = sel_w.shape
     _check("moe_renormalise_weights", load().moe_renormalise_weights(_ptr(sel_slot), _ptr(sel_w), T, k,
                                                                      _stream(stream)))
+
+
+# ------------------------------------------------------------------ paged 8-bit key/value cache and tree attention
+
+_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32}
+
+
+class KvCache:
+    """The paged 8-bit key/value cache of one attention layer (format: the header's ``moe_kv_cache``).
+
+    ``k_codes``, ``v_codes``: e4m3 codes [n_pages, n_kv_heads, page_size, head_dim] (uint8 or float8_e4m3fn);
+    ``k_scales``, ``v_scales``: e8m0 scale bytes uint8 [n_pages, n_kv_heads, page_size]. All contiguous, on the GPU.
+    """
+
+    def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor):
+        if k_codes.dim() != 4 or v_codes.shape != k_codes.shape or any(
+                s.shape != k_codes.shape[:3] or s.dtype != torch.uint8 for s in (k_scales, v_scales)):
+            raise ValueError("codes [pages, heads, rows, dim], scales uint8 [pages, heads, rows]")
+        if k_codes.element_size() != 1 or v_codes.element_size() != 1:
+            raise ValueError("codes are one byte each")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k_codes.shape
+        self._st = MoeKvCache(_ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), *k_codes.shape)
+        self._ref = ctypes.byref(self._st)
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device="cuda") -> "KvCache":
+        """A cache of zero vectors."""
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        codes = [torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.full(shape[:3], 127, dtype=torch.uint8, device=device) for _ in range(2)]
+        return cls(*codes, *scales)
+
+    def rows(self, x: torch.Tensor, what: str) -> None:
+        """Raises unless x is [tokens, n_kv_heads, head_dim] with a contiguous last axis, on the GPU."""
+        if x.dim() != 3 or x.shape[1] != self.n_kv_heads or x.shape[2] != self.head_dim or x.stride(2) != 1 or not x.is_cuda:
+            raise ValueError(f"{what}: expected a CUDA tensor [tokens, {self.n_kv_heads}, {self.head_dim}] with a contiguous last axis")
+
+
+def _of(t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str):
+    """Pointer of a contiguous CUDA tensor of this type and shape."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    return _ptr(t)
+
+
+def moe_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: KvCache, stream=None) -> None:
+    """Quantise the keys and values of T tokens [T, n_kv_heads, head_dim] (bf16, fp16 or fp32; any token and head
+    strides of whole 16 bytes) into cache rows slots int64 [T] (page * page_size + row; -1 skips the token)."""
+    cache.rows(k, "k")
+    cache.rows(v, "v")
+    T = k.shape[0]
+    if v.shape[0] != T or v.dtype != k.dtype or k.dtype not in _DTYPES:
+        raise ValueError("k and v: one length and one type of bf16, fp16, fp32")
+    _check("moe_kv_write", load().moe_kv_write(
+        k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+        _of(slots, torch.int64, (T,), "slots"), T, cache._ref, _stream(stream)))
+
+
+def moe_kv_read(cache: KvCache, page_table: torch.Tensor, starts, cu_rows: torch.Tensor, k_out: torch.Tensor,
+                v_out: torch.Tensor, stream=None) -> None:
+    """Read rows starts[b] .. of every lane b back into k_out, v_out [n_rows, n_kv_heads, head_dim] (bf16, fp16 or
+    fp32): lane b's rows go to cu_rows[b] .. cu_rows[b + 1] (see the header). starts may be None (row 0)."""
+    lanes, width = page_table.shape
+    n = k_out.shape[0]
+    if k_out.dtype not in _DTYPES:
+        raise ValueError("k_out: bf16, fp16 or fp32")
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    _check("moe_kv_read", load().moe_kv_read(
+        cache._ref, _of(page_table, torch.int32, (lanes, width), "page_table"), width, lanes,
+        None if starts is None else _of(starts, torch.int32, (lanes,), "starts"),
+        _of(cu_rows, torch.int32, (lanes + 1,), "cu_rows"), n, _DTYPES[k_out.dtype],
+        _of(k_out, k_out.dtype, shape, "k_out"), _of(v_out, k_out.dtype, shape, "v_out"), _stream(stream)))
+
+
+def moe_kv_keep(cache: KvCache, page_table: torch.Tensor, prefix: torch.Tensor, path: torch.Tensor,
+                n_keep: torch.Tensor, stream=None) -> None:
+    """Move the rows of each lane's accepted path, prefix[b] + path[b, i], to prefix[b] + i for i < n_keep[b], in
+    place (int32 [lanes], [lanes, path_width], [lanes]; see the header)."""
+    lanes, width = page_table.shape
+    _check("moe_kv_keep", load().moe_kv_keep(
+        cache._ref, _of(page_table, torch.int32, (lanes, width), "page_table"), width, lanes,
+        _of(prefix, torch.int32, (lanes,), "prefix"), _of(path, torch.int32, (lanes, path.shape[1]), "path"),
+        path.shape[1], _of(n_keep, torch.int32, (lanes,), "n_keep"), _stream(stream)))
+
+
+def moe_tree_attention_workspace_bytes(n_nodes: int, n_q_heads: int, n_kv_heads: int, head_dim: int, lanes: int) -> int:
+    return int(load().moe_tree_attention_workspace_bytes(n_nodes, n_q_heads, n_kv_heads, head_dim, lanes))
+
+
+def moe_tree_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, kv_len: torch.Tensor,
+                       cu_nodes: torch.Tensor, max_nodes: int, tree_mask, scale: float, out: torch.Tensor,
+                       workspace: torch.Tensor, lse: torch.Tensor | None = None, stream=None) -> None:
+    """Attention of every lane's tree nodes over its cache rows (see the header).
+
+    q bf16 [n_nodes, n_q_heads, head_dim] (strided); kv_len int32 [lanes] (the nodes' rows included); cu_nodes int32
+    [lanes + 1]; max_nodes: host bound on a lane's nodes; tree_mask int32 [n_nodes, words] or None (each node sees
+    the rows up to its own); out bf16 like q, contiguous; lse fp32 [n_nodes, n_q_heads] or None.
+    """
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_cuda or q.shape[2] != cache.head_dim or q.stride(2) != 1:
+        raise ValueError(f"q: expected a bf16 CUDA tensor [nodes, heads, {cache.head_dim}] with a contiguous last axis")
+    n, heads = q.shape[0], q.shape[1]
+    lanes, width = page_table.shape
+    words = 0 if tree_mask is None else tree_mask.shape[1]
+    _check("moe_tree_attention", load().moe_tree_attention(
+        q.data_ptr(), q.stride(0), q.stride(1), n, heads, cache._ref,
+        _of(page_table, torch.int32, (lanes, width), "page_table"), width, lanes,
+        _of(kv_len, torch.int32, (lanes,), "kv_len"), _of(cu_nodes, torch.int32, (lanes + 1,), "cu_nodes"), max_nodes,
+        None if tree_mask is None else _of(tree_mask, torch.int32, (n, words), "tree_mask"), words, scale,
+        _of(out, torch.bfloat16, (n, heads, cache.head_dim), "out"),
+        None if lse is None else _of(lse, torch.float32, (n, heads), "lse"), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))

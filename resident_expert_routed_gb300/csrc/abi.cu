@@ -128,7 +128,8 @@ moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_E
 // ------------------------------------------------------------------ optional per-launch event timing
 const char* const kKernelNames[MK_COUNT] = {"router_logits_partial", "route_select", "demand_accumulate",
                                             "hot_miss_select", "ffn_plan", "ffn_pack", "ffn_gemm_gate_up",
-                                            "ffn_gemm_down", "ffn_combine", "arena_replan", "ring_install"};
+                                            "ffn_gemm_down", "ffn_combine", "arena_replan", "ring_install", "kv_write",
+                                            "kv_read", "kv_keep", "tree_attention", "tree_attention_join"};
 struct ProfRec {
     int kind;
     cudaEvent_t a, b;
@@ -212,7 +213,7 @@ const char* moe_status_str(moe_status s) {
         case MOE_ECUDA: return "CUDA error";
         case MOE_ENOMEM: return "workspace too small";
         case MOE_ETIMEOUT: return "device wait timed out";
-        case MOE_EDEVICE: return "device reported bad data (slot id, scale byte or table)";
+        case MOE_EDEVICE: return "device reported bad data (slot id, scale byte, table or page)";
         case MOE_EUNSUPPORTED: return "size beyond a documented limit";
         case MOE_EIO: return "file could not be read or written";
     }

@@ -406,6 +406,13 @@ cudaError_t launch_replan(const unsigned long long* demand, int n, int n_main, i
 cudaError_t launch_ring_install(int32_t* slot_of, int32_t* owner, int ring_slot, int flat, cudaStream_t s,
                                 uint32_t* err);
 
+// Paged key/value cache (kv_cache.cu): the limits and alignment every call relies on.
+moe_status kv_cache_status(const moe_kv_cache* c);
+// One e8m0 scale byte as a float factor, 2^(s - 127); 255 is NaN.
+MOE_DEV float e8m0_to_float(uint32_t s) {
+    return s == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(s ? s << 23 : 0x00400000u);
+}
+
 // Programmatic dependent launch. Every kernel of the library is launched with
 // moe_launch (programmatic stream serialisation allowed) and starts with
 // pdl_trigger() then, after any prologue that touches no input, pdl_wait()
@@ -444,7 +451,8 @@ int moe_sm_count();
 // Kernel kinds for the optional per-launch event timing (abi.cu).
 enum MoeKernelKind {
     MK_ROUTER_LOGITS = 0, MK_ROUTE_SELECT, MK_DEMAND, MK_HOT_MISS, MK_PLAN, MK_PACK, MK_GEMM_GATE_UP,
-    MK_GEMM_DOWN, MK_COMBINE, MK_REPLAN, MK_RING, MK_COUNT
+    MK_GEMM_DOWN, MK_COMBINE, MK_REPLAN, MK_RING, MK_KV_WRITE, MK_KV_READ, MK_KV_KEEP, MK_ATTENTION, MK_ATTENTION_JOIN,
+    MK_COUNT
 };
 void moe_prof_begin(int kind, cudaStream_t s);
 void moe_prof_end(int kind, cudaStream_t s);
