@@ -1,7 +1,50 @@
 // Attention of drafted tokens over the paged 8-bit key/value cache.
+//
+// For the rows r = (node, query head) of one kv head and the cache rows j:
+//   s[r,j] = scale log2(e) q_r . k_j        (k_j = codes * 2^ek_j)
+//   out[r] = sum_j 2^s[r,j] v_j / sum_j 2^s[r,j]      (v_j = codes * 2^ev_j)
+// over the j that r sees. Both products run on the tensor cores on the codes
+// as they lie in the cache (tcgen05 kind::f8f6f4, e4m3 x e4m3, fp32
+// accumulators in TMEM): no byte of the cache is converted or scaled outside
+// the MMA, so TMA moves it from HBM to the operand buffers untouched.
+//   - The other operand is split in two e4m3 parts. A bf16 query has 8
+//     significant bits and e4m3 has 4: with its row scaled by a power of two to
+//     128 <= max|q| < 256, hi = e4m3(q), lo = e4m3(q - hi) hold it exactly down
+//     to 2^-9 of the row's maximum and within 2^-17 of the maximum below. The
+//     probabilities likewise: hi + lo carry 8 significant bits, as bf16 would.
+//   - The scale of a key row multiplies its column of scores; the scale of a
+//     value row is added to the exponent: s' = s + ev_j, p = 2^(s' - m + 8), with
+//     m the row's maximum of s' in the tile, so that p <= 256 and hi + lo reach 2^-18
+//     below it whatever the rows' scales; the sum of weights gets p 2^-ev_j.
+//   - Every tile of 128 cache rows has its own m: tiles do not wait for one
+//     another, and a large weight early on cannot flush the weights of later tiles.
+//
+// Orientation: cache rows are the MMA's M (128), tree rows its N (2R for S, R for
+// O: hi and lo of the queries side by side; those of the probabilities
+// accumulate), so a single token costs N = 16 and a wide tree 64, and nothing
+// is padded to 128:
+//   S^T[128 rows, 2R] = K[128, D] Q^T           O^T[D, R] = V^T[D, 128] P^T[128, R]
+//
+// Work: the (lane, kv head, tile of R tree rows) units, each a run of cache
+// tiles, are laid end to end and cut into equal parts, one per CTA. A unit that one
+// CTA does whole is written at once; the others leave their parts (output, maximum, sum)
+// in the workspace and tree_attention_join adds them up in order.
+//
+// Roles (512 threads):
+//   warps 0-3, 4-7   softmax of even and odd tiles; a thread is a cache row
+//   warps 8-11       merge: adds each tile's O^T to fp32 registers at the row's
+//                    running maximum, divides and stores
+//   warp 12          TMA: one copy per page of codes, bulk copies of scales
+//   warp 13          MMA issue (one lane), TMEM
+//   warps 14-15      queries of the next unit: split and laid out
+// Waits are bounded as in the expert GEMMs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <mutex>
+
+#include <cudaTypedefs.h>
 
 #include "common.cuh"
 
@@ -19,117 +62,984 @@ struct AttnArgs {
     int max_nodes;
     const int32_t* mask;
     int mask_words;
-    float scale;
+    float scale_log2;                            // scale * log2(e)
     __nv_bfloat16* out;
     float* lse;
+    uint8_t* ws;
     uint32_t* err;
+    uint64_t wait_ns;
 };
 
-MOE_DEV float2 e4m3x2_to_float2(uint32_t w) {
-    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3)));
+struct AttnMaps {
+    CUtensorMap k, v;                            // (head_dim, rows) bytes, box min(head_dim, 128) x min(page, 128) rows
+};
+
+constexpr int TILE = 128;                        // cache rows a tile
+constexpr int ATTN_THREADS = 512;
+constexpr int LANE_CACHE = 512;                  // lanes whose facts are kept in shared memory
+
+// What the join needs, at the start of the workspace: the cut, and for each CTA the unit that its part begins in.
+struct JoinHead {
+    int64_t total;                               // tiles in all
+    int32_t parts;                               // CTAs with work
+    int32_t pad;
+};
+struct JoinUnit {
+    int64_t first, end;                          // the unit's tiles in the whole run
+    int32_t node0, rows, head, row0;             // first node of the lane, tree rows of the unit, kv head, first row in the lane
+};
+constexpr size_t JOIN_UNITS = 256;               // byte offset of JoinUnit[CTAs]
+
+__host__ __device__ constexpr size_t part_floats(int R, int D) { return (size_t)R * (D + 2); }
+__host__ __device__ inline size_t parts_offset(int ctas) { return (JOIN_UNITS + (size_t)ctas * sizeof(JoinUnit) + 255) / 256 * 256; }
+
+template <int D, int R>
+struct Cfg {
+    static constexpr int ROWB = D >= 128 ? 128 : 64;          // bytes of an operand row: one swizzle atom
+    static constexpr int PANELS = D / ROWB;
+    static constexpr int PANEL = TILE * ROWB;
+    static constexpr int SLOT = TILE * D;
+    static constexpr int NS = D == 64 ? 12 : D == 128 ? 8 : 5;    // ring of key and value tiles
+    static constexpr int NSC = 4;                             // ring of scale tiles (128 key bytes, 128 value bytes)
+    static constexpr int PBUF = 2 * TILE * R;
+    static constexpr int QBUF = 2 * R * D;
+    static constexpr int MB = D == 256 ? 2 : 1;               // M blocks of O^T
+    static constexpr int OFF_RING = 0;
+    static constexpr int OFF_P = OFF_RING + NS * SLOT;
+    static constexpr int OFF_Q = OFF_P + 2 * PBUF;
+    static constexpr int OFF_SC = OFF_Q + 2 * QBUF;
+    static constexpr int OFF_F = OFF_SC + NSC * 256;          // floats from here
+    static constexpr int F_FAC = 0;                           // [2 groups][4 warps][3][R]: offset, alpha, beta
+    static constexpr int F_WMAX = F_FAC + 2 * 4 * 3 * R;      // [2][4][R]
+    static constexpr int F_MT = F_WMAX + 2 * 4 * R;           // [4][R] tile maxima for the merge
+    static constexpr int F_MFAC = F_MT + 4 * R;               // [4 warps][2][R]
+    static constexpr int F_QF = F_MFAC + 4 * 2 * R;           // [4][R] 2^-a of the queries' rows
+    static constexpr int F_L = F_QF + 4 * R;                  // [2][4][R] sums at a part's end
+    static constexpr int F_M = F_L + 2 * 4 * R;               // [2][R] their maxima
+    static constexpr int F_END = F_M + 2 * R;
+    static constexpr int OFF_LANE = OFF_F + F_END * 4;        // int n0, n, len [LANE_CACHE]
+    static constexpr int OFF_SCAN = OFF_LANE + 3 * LANE_CACHE * 4;
+    static constexpr int OFF_BAR = OFF_SCAN + 32 * 8 + 64;
+    // full, empty [NS]; scale full, empty [NSC]; sfull, pfull, ofull, ofree, wmax [2]; qfull, qfree [2]; lfull, lfree, drain
+    static constexpr int N_BARS = 2 * NS + 2 * NSC + 14 + 3;
+    static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
+    static constexpr int SMEM = OFF_MISC + 16 + 1024;
+    static constexpr int TMEM_O = 4 * R;
+    static constexpr int TMEM_USED = 4 * R + 2 * R * MB;
+    static constexpr int TMEM_COLS = TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
+    static_assert(TMEM_USED <= 512 && SMEM <= 227 * 1024, "TMEM, shared memory");
+    static_assert(OFF_F % 16 == 0 && OFF_SCAN % 8 == 0 && OFF_BAR % 8 == 0, "alignment");
+    static_assert(R == 16 || R == 32 || R == 64, "R");
+};
+
+// ------------------------------------------------------------------ small device pieces
+
+MOE_DEV float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+typedef unsigned long long f32x2;
+MOE_DEV f32x2 pack2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+MOE_DEV float2 unpack2(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+MOE_DEV f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+MOE_DEV f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+MOE_DEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// Maximum over the warp, in every lane (NaN inputs are passed over).
+MOE_DEV float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
-// One block per (node, query head): a thread scores one row of a tile of 128,
-// the block joins the running maximum and sum, and a thread then adds up its
-// columns of the output.
-__global__ void __launch_bounds__(128) tree_attention(const AttnArgs a) {
-    __shared__ float qs[256];
-    __shared__ float ps[128];
-    __shared__ int64_t rows[128];
-    __shared__ float red[4];
+MOE_DEV void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// kind::f8f6f4, e4m3 x e4m3 -> fp32; the last two say whether A and B lie with M and N (instead of K) contiguous.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n, int a_mn, int b_mn) {
+    return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// Shared-memory matrix descriptor without its address: swizzle 2 = 128 B, 4 = 64 B, 6 = 32 B, 0 = none; `group` =
+// bytes from one group of eight rows (of the strided axis) to the next. Every operand here is one
+// atom wide on its contiguous axis, so the group stride is the only one in use: both offset fields hold it.
+__host__ __device__ constexpr uint64_t desc_base(int swizzle, int group) {
+    return ((uint64_t)(group >> 4) << 16) | ((uint64_t)(group >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)swizzle << 61);
+}
+MOE_DEV uint64_t desc_at(uint64_t base, uint32_t saddr) { return base | (uint64_t)((saddr >> 4) & 0x3FFFu); }
+
+// A lane's facts. A lane that does not fit (see the header) has no rows, and its outputs become zeros.
+struct Lane {
+    int n0, n, len;
+};
+MOE_DEV Lane lane_facts(const AttnArgs& a, int b, bool* bad) {
+    Lane l;
+    l.n0 = a.cu[b];
+    l.n = a.cu[b + 1] - l.n0;
+    l.len = a.kv_len[b];
+    *bad = false;
+    if (l.n0 < 0 || l.n < 0 || l.n > a.n_nodes - l.n0) {      // row counts that would lead out of q and out
+        *bad = true;
+        l.n0 = l.n = l.len = 0;
+    } else if (l.n > 0 && (l.n > a.max_nodes || l.len < l.n ||
+                           (((int64_t)l.len + (1 << a.page_shift) - 1) >> a.page_shift) > a.width)) {
+        *bad = true;
+        l.len = 0;
+    }
+    return l;
+}
+
+// One CTA's way through its part of the run: the unit it is in and the tile within it.
+template <int R>
+struct Walk {
+    int b, h, rt, t, tiles, nrt;
+    Lane l;
+
+    MOE_DEV void enter(const AttnArgs& a, const int* facts) {
+        if (b < LANE_CACHE) {
+            l.n0 = facts[b];
+            l.n = facts[LANE_CACHE + b];
+            l.len = facts[2 * LANE_CACHE + b];
+        } else {
+            bool bad;
+            l = lane_facts(a, b, &bad);
+        }
+        tiles = l.len > 0 ? (l.len + TILE - 1) / TILE : 1;
+        nrt = l.n > 0 ? (l.n * a.group + R - 1) / R : 1;
+    }
+    MOE_DEV void start(const AttnArgs& a, const int* facts, int lane, int64_t offset) {
+        b = lane;
+        enter(a, facts);
+        const int u = (int)(offset / tiles);
+        t = (int)(offset - (int64_t)u * tiles);
+        h = u / nrt;
+        rt = u - h * nrt;
+    }
+    // past n tiles, which do not lead out of the unit; more: whether tiles are left after them
+    MOE_DEV void advance(const AttnArgs& a, const int* facts, int n, bool more) {
+        t += n;
+        if (t < tiles || !more) return;
+        t = 0;
+        if (++rt < nrt) return;
+        rt = 0;
+        if (++h < a.c.n_kv_heads) return;
+        h = 0;
+        do {
+            ++b;
+            enter(a, facts);
+        } while (l.n == 0 && b + 1 < a.lanes);
+    }
+    MOE_DEV int rows(const AttnArgs& a) const {               // tree rows of this unit
+        const int left = l.n * a.group - rt * R;
+        return left < R ? left : R;
+    }
+};
+
+template <int D, int R>
+__global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
+    using C = Cfg<D, R>;
+    constexpr int NS = C::NS, NSC = C::NSC;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* empty = full + NS;
+    uint64_t* scfull = empty + NS;
+    uint64_t* scempty = scfull + NSC;
+    uint64_t* sfull = scempty + NSC;             // [2] S of a tile is ready
+    uint64_t* pfull = sfull + 2;                 // [2] P is written (and S has been read)
+    uint64_t* ofull = pfull + 2;                 // [2] O of a tile is ready (and P has been read)
+    uint64_t* ofree = ofull + 2;                 // [2] the merge has read O
+    uint64_t* wmaxb = ofree + 2;                 // [2] the four warps of a softmax group have their maxima
+    uint64_t* qfull = wmaxb + 2;                 // [2]
+    uint64_t* qfree = qfull + 2;                 // [2]
+    uint64_t* lfull = qfree + 2;                 // the sums of a part are written
+    uint64_t* lfree = lfull + 1;                 // ... and read
+    uint64_t* drain = lfree + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+    float* F = reinterpret_cast<float*>(smem + C::OFF_F);
+    int* facts = reinterpret_cast<int*>(smem + C::OFF_LANE);
+    unsigned long long* scratch = reinterpret_cast<unsigned long long*>(smem + C::OFF_SCAN);
+    int64_t* begin_off = reinterpret_cast<int64_t*>(smem + C::OFF_SCAN + 256);       // where this CTA's part begins
+    int* begin_lane = reinterpret_cast<int*>(smem + C::OFF_SCAN + 264);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int H = a.c.n_kv_heads, G = a.group;
     pdl_trigger();
+    if (tid == 0) {
+        for (int s = 0; s < NS; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+        for (int s = 0; s < NSC; ++s) { mbar_init(&scfull[s], 1); mbar_init(&scempty[s], 4); }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sfull[s], 1); mbar_init(&pfull[s], 4); mbar_init(&ofull[s], 1); mbar_init(&ofree[s], 4);
+            mbar_init(&wmaxb[s], 4); mbar_init(&qfull[s], 2); mbar_init(&qfree[s], 1);
+        }
+        mbar_init(lfull, 8); mbar_init(lfree, 4); mbar_init(drain, 1);
+        *abort_flag = 0;
+        *begin_lane = 0;
+        *begin_off = 0;
+        fence_barrier_init();
+        prefetch_tmap(&maps.k);
+        prefetch_tmap(&maps.v);
+    }
+    if (warp == 13) { tmem_alloc(tmem_slot, C::TMEM_COLS); tmem_relinquish(); }
     pdl_wait();
-    const int node = blockIdx.x, qh = blockIdx.y, h = qh / a.group;
-    const int D = a.c.head_dim, tid = threadIdx.x;
-    int lo = 0, hi = a.lanes;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu[mid] <= node) lo = mid; else hi = mid;
-    }
-    const int n = a.cu[lo + 1] - a.cu[lo], t = node - a.cu[lo];
-    int len = a.kv_len[lo];
-    if (n > a.max_nodes || len < n || ((int64_t)len + (1 << a.page_shift) - 1) >> a.page_shift > a.width) {
-        if (tid == 0) record_error(a.err, MOE_DEV_BAD_PAGE);
-        len = 0;
-    }
-    const int prefix = len - n;
-    for (int d = tid; d < D; d += 128)
-        qs[d] = __bfloat162float(a.q[node * a.q_token_stride + qh * a.q_head_stride + d]);
-    const uint8_t* kc = static_cast<const uint8_t*>(a.c.k_codes);
-    const uint8_t* vc = static_cast<const uint8_t*>(a.c.v_codes);
-    float m = -INFINITY, l = 0.0f, acc[2] = {0.0f, 0.0f};
-    for (int j0 = 0; j0 < len; j0 += 128) {
-        __syncthreads();
-        const int j = j0 + tid;
-        float s = -INFINITY;
-        int64_t row = 0;
-        if (j < len) {
-            int page = a.table[(int64_t)lo * a.width + (j >> a.page_shift)];
-            if (page < 0 || page >= a.c.n_pages) {
-                record_error(a.err, MOE_DEV_BAD_PAGE);
-                page = 0;
+
+    // ---------------------------------------------------------------- the cut
+    auto work_of = [&](const Lane& l) -> unsigned long long {
+        if (l.n == 0) return 0ull;
+        const unsigned long long tiles = l.len > 0 ? (l.len + TILE - 1) / TILE : 1;
+        return (unsigned long long)H * ((l.n * G + R - 1) / R) * tiles;
+    };
+    unsigned long long total = 0, mine = 0, incl = 0;
+    for (int b0 = 0; b0 < a.lanes; b0 += ATTN_THREADS) {
+        const int b = b0 + tid;
+        Lane l{0, 0, 0};
+        if (b < a.lanes) {
+            bool bad;
+            l = lane_facts(a, b, &bad);
+            if (bad && blockIdx.x == 0) record_error(a.err, MOE_DEV_BAD_PAGE);
+            if (b < LANE_CACHE) {
+                facts[b] = l.n0;
+                facts[LANE_CACHE + b] = l.n;
+                facts[2 * LANE_CACHE + b] = l.len;
             }
-            row = (((int64_t)page * a.c.n_kv_heads + h) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
-            const int i = j - prefix;
-            const bool sees = i < 0 || (a.mask ? (a.mask[(int64_t)node * a.mask_words + (i >> 5)] >> (i & 31)) & 1 : i <= t);
-            if (sees) {
-                float dot = 0.0f;
-                for (int d = 0; d < D; d += 4) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t*>(kc + row * D + d);
-                    const float2 x = e4m3x2_to_float2(w), y = e4m3x2_to_float2(w >> 16);
-                    dot += x.x * qs[d] + x.y * qs[d + 1] + y.x * qs[d + 2] + y.y * qs[d + 3];
-                }
-                s = dot * e8m0_to_float(a.c.k_scales[row]) * a.scale;
-            } else {
-                row = -1;                                     // not seen: its values take no part
+        }
+        mine = work_of(l);
+        unsigned long long sum;
+        incl = block_inclusive_scan_u64(mine, scratch, &sum) + total;
+        total += sum;
+    }
+    const int parts = total < gridDim.x ? (int)total : (int)gridDim.x;
+    const bool active = (int)blockIdx.x < parts;
+    const int64_t first = active ? (int64_t)(total * blockIdx.x / parts) : 0;
+    const int64_t count = active ? (int64_t)(total * (blockIdx.x + 1) / parts) - first : 0;
+    if (active) {
+        if (a.lanes <= ATTN_THREADS) {
+            const unsigned long long excl = incl - mine;
+            if ((unsigned long long)first >= excl && (unsigned long long)first < incl) {
+                *begin_lane = tid;
+                *begin_off = first - (int64_t)excl;
             }
         } else {
-            row = -1;
-        }
-        rows[tid] = row;
-        float mx = s;                                         // NaN scores pass by the maximum and reach the sum
-        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-        if ((tid & 31) == 0) red[tid >> 5] = mx;
-        __syncthreads();
-        const float mn = fmaxf(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), m);
-        const float ref = mn == -INFINITY ? 0.0f : mn;
-        const float alpha = expf(m - ref);
-        const float p = row < 0 ? 0.0f : expf(s - ref);
-        ps[tid] = p;
-        m = mn;
-        __syncthreads();
-        float sum = 0.0f;
-        for (int i = 0; i < 128; ++i) sum += ps[i];
-        l = l * alpha + sum;
-        for (int k = 0; k < 2; ++k) {
-            const int d = tid + 128 * k;
-            if (d >= D) break;
-            float o = 0.0f;
-            for (int i = 0; i < 128; ++i)
-                if (rows[i] >= 0) {
-                    const __half v = __half(__nv_cvt_fp8_to_halfraw(vc[rows[i] * D + d], __NV_E4M3));
-                    o += ps[i] * __half2float(v) * e8m0_to_float(a.c.v_scales[rows[i]]);
+            unsigned long long before = 0;
+            for (int b0 = 0; b0 < a.lanes; b0 += ATTN_THREADS) {
+                const int b = b0 + tid;
+                bool bad;
+                mine = b < a.lanes ? work_of(lane_facts(a, b, &bad)) : 0ull;
+                unsigned long long sum;
+                incl = block_inclusive_scan_u64(mine, scratch, &sum) + before;
+                const unsigned long long excl = incl - mine;
+                if ((unsigned long long)first >= excl && (unsigned long long)first < incl) {
+                    *begin_lane = b;
+                    *begin_off = first - (int64_t)excl;
                 }
-            acc[k] = acc[k] * alpha + o;
+                before += sum;
+            }
         }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    for (int k = 0; k < 2; ++k) {
-        const int d = tid + 128 * k;
-        if (d < D) a.out[((int64_t)node * a.n_q_heads + qh) * D + d] = __float2bfloat16_rn(acc[k] * inv);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    Walk<R> w;
+    w.start(a, facts, active ? *begin_lane : 0, active ? *begin_off : 0);
+    if (tid == 0) {
+        if (blockIdx.x == 0) *reinterpret_cast<JoinHead*>(a.ws) = JoinHead{(int64_t)total, parts, 0};
+        if (active)
+            reinterpret_cast<JoinUnit*>(a.ws + JOIN_UNITS)[blockIdx.x] =
+                JoinUnit{first - w.t, first - w.t + w.tiles, w.l.n0, w.rows(a), w.h, w.rt * R};
     }
-    if (a.lse && tid == 0) a.lse[(int64_t)node * a.n_q_heads + qh] = l == 0.0f ? -INFINITY : m + logf(l);
+    int64_t left = count;
+    uint32_t issued = 0, sc_issued = 0;              // ring fills, by the producer's lane 0
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ softmax
+        const int g = warp >> 2, wl = warp & 3;      // group, warp in it
+        const int j = tid & 127;                     // this thread's row of the tile
+        const uint32_t trow = tmem + ((uint32_t)(wl * 32) << 16) + g * 2 * R;
+        float* fac = F + C::F_FAC + (g * 4 + wl) * 3 * R;
+        float* wmax = F + C::F_WMAX + g * 4 * R;
+        uint32_t i = 0, k = 0;                       // tile of the CTA; tile of this group
+        uint32_t piece = 0;
+        constexpr int RL = R > 32 ? 2 : 1;           // rows a lane keeps maxima for: lane, lane + 32
+        bool ok = true;
+        while (left > 0 && ok) {
+            const int nt = left < w.tiles - w.t ? (int)left : w.tiles - w.t;
+            f32x2 l2[R / 2];
+            float M[RL];
+#pragma unroll
+            for (int r = 0; r < R / 2; ++r) l2[r] = 0ull;
+#pragma unroll
+            for (int r = 0; r < RL; ++r) M[r] = -INFINITY;
+            const float* qf = F + C::F_QF + (piece & 3) * R;
+            const int prefix = w.l.len - w.l.n;
+            for (int t = w.t; t < w.t + nt; ++t, ++i) {
+                if ((int)(i & 1) != g) continue;
+                const int j0 = t * TILE;
+                const int valid = w.l.len - j0;      // rows of the tile that exist (can be <= 0 or > 128)
+                const bool masked = j0 + TILE > prefix;
+                // what this row is to each tree row
+                uint64_t sees = ~0ull;
+                if (masked) {
+                    const int n = j0 + j - prefix;
+                    if (j >= valid) {
+                        sees = 0ull;
+                    } else if (n >= 0) {
+                        sees = 0ull;
+                        const int row0 = w.rt * R, last = (row0 + w.rows(a) - 1) / G;
+                        for (int t1 = row0 / G; t1 <= last; ++t1) {
+                            const bool see = a.mask ? (a.mask[(int64_t)(w.l.n0 + t1) * a.mask_words + (n >> 5)] >> (n & 31)) & 1
+                                                    : n <= t1;
+                            if (!see) continue;
+                            int lo = t1 * G - row0, hi = lo + G;
+                            lo = lo < 0 ? 0 : lo;
+                            hi = hi > R ? R : hi;
+                            sees |= (hi == 64 ? ~0ull : (1ull << hi) - 1ull) & ~((1ull << lo) - 1ull);
+                        }
+                    }
+                }
+                const int sc = (int)(i % NSC);
+                if (!warp_wait(&scfull[sc], (i / NSC) & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                const uint32_t ks = smem[C::OFF_SC + sc * 256 + j], vs = smem[C::OFF_SC + sc * 256 + TILE + j];
+                const uint32_t four = *reinterpret_cast<const uint32_t*>(smem + C::OFF_SC + sc * 256 + TILE + lane * 4);
+                const uint32_t most = __vmaxu4(four, four >> 16), least = __vminu4(four, __byte_perm(four, 0, 0x1032));
+                const bool wide = __reduce_max_sync(0xFFFFFFFFu, max(most & 255u, (most >> 8) & 255u)) >
+                                  __reduce_min_sync(0xFFFFFFFFu, min(least & 255u, (least >> 8) & 255u)) + 104u;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&scempty[sc]);
+                const float cj = a.scale_log2 * e8m0_to_float(ks);
+                const float ev = vs == 255u ? __uint_as_float(0x7FC00000u) : (float)((int)vs - 127);
+                const f32x2 cj2 = pack2(cj, cj), ev2 = pack2(ev, ev);
+                if (!warp_wait(&sfull[g], k & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                tc_fence_after();
+                // s' of 16 tree rows, as 8 pairs
+                auto scores = [&](int c0, f32x2 (&x)[8]) {
+                    uint32_t hi[16], lo[16];
+                    tc_ld_x16(trow + c0, hi);
+                    tc_ld_x16(trow + R + c0, lo);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const f32x2 f = *reinterpret_cast<const f32x2*>(qf + c0 + 2 * q);
+                        const f32x2 s = add2(pack2(__uint_as_float(hi[2 * q]), __uint_as_float(hi[2 * q + 1])),
+                                             pack2(__uint_as_float(lo[2 * q]), __uint_as_float(lo[2 * q + 1])));
+                        x[q] = fma2(mul2(s, f), cj2, ev2);
+                    }
+                    if (masked) {
+                        const uint32_t bits = (uint32_t)(sees >> c0);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const float2 s = unpack2(x[q]);
+                            x[q] = pack2((bits >> (2 * q)) & 1 ? s.x : -INFINITY, (bits >> (2 * q + 1)) & 1 ? s.y : -INFINITY);
+                        }
+                    }
+                };
+                // one pass keeps the scores of up to 32 tree rows in registers; for 64 they are read from TMEM twice
+                constexpr bool KEEP = R <= 32;
+                f32x2 kept[KEEP ? R / 2 : 8];
+                float mine_max[RL];
+#pragma unroll
+                for (int r = 0; r < RL; ++r) mine_max[r] = -INFINITY;
+#pragma unroll
+                for (int c0 = 0; c0 < R; c0 += 16) {
+                    f32x2 x[8];
+                    scores(c0, x);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float2 s = unpack2(x[q]);
+                        const float m0 = warp_max(s.x), m1 = warp_max(s.y);
+                        const int r = c0 + 2 * q;
+                        if (lane == (r & 31)) mine_max[r / 32] = m0;
+                        if (lane == ((r + 1) & 31)) mine_max[r / 32] = m1;
+                        if (KEEP) kept[c0 / 2 + q] = x[q];
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < RL; ++r)
+                    if (R >= 32 || lane < R) wmax[wl * R + r * 32 + lane] = mine_max[r];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&wmaxb[g]);
+                // P of this group's previous tile has been read (its O is complete)
+                if (k > 0 && !warp_wait(&ofull[g], (k - 1) & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                if (!warp_wait(&wmaxb[g], k & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+#pragma unroll
+                for (int r = 0; r < RL; ++r) {
+                    const int row = r * 32 + lane;
+                    if (R < 32 && lane >= R) break;
+                    const float m = fmaxf(fmaxf(wmax[row], wmax[R + row]), fmaxf(wmax[2 * R + row], wmax[3 * R + row]));
+                    const float Mn = fmaxf(M[r], m);
+                    const bool none = m == -INFINITY;
+                    fac[row] = none ? 0.0f : 8.0f - m;
+                    fac[R + row] = M[r] == -INFINITY ? 0.0f : ex2(M[r] - Mn);
+                    fac[2 * R + row] = none ? 0.0f : ex2(m - Mn);
+                    M[r] = Mn;
+                    if (wl == 0) F[C::F_MT + (i & 3) * R + row] = m;
+                }
+                __syncwarp();
+                if (valid < TILE) {
+                    // rows past the lane's end hold anything: their values are cleared, so that 0 * NaN does not arise
+                    const uint32_t f = 2 * i + 1;
+                    if (!warp_wait(&full[f % NS], (f / NS) & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                    if (j >= valid)
+#pragma unroll
+                        for (int p = 0; p < C::PANELS; ++p)
+#pragma unroll
+                            for (int q = 0; q < C::ROWB / 16; ++q)
+                                *reinterpret_cast<uint4*>(smem + C::OFF_RING + (f % NS) * C::SLOT + p * C::PANEL + j * C::ROWB + q * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                }
+                // Weight of this row in the sums: p 2^-ev (a row without a valid scale is not seen, or p is NaN). With
+                // value scales more than 2^104 apart p could underflow in a row that matters to the sum: the
+                // weight then gets an exponential of its own.
+                const int evi = vs == 255u ? 0 : (int)vs - 127;
+                const float wj = exp2_int(-evi), evf = (float)evi;
+                const f32x2 wj2 = pack2(wj, wj);
+                uint8_t* P = smem + C::OFF_P + g * C::PBUF;
+#pragma unroll
+                for (int c0 = 0; c0 < R; c0 += 16) {
+                    f32x2 x[8];
+                    if (KEEP) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) x[q] = kept[c0 / 2 + q];
+                    } else {
+                        scores(c0, x);
+                    }
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int r = c0 + 2 * q;
+                        const float2 s = unpack2(add2(x[q], *reinterpret_cast<const f32x2*>(fac + r)));
+                        const float p0 = ex2(s.x), p1 = ex2(s.y);
+                        const f32x2 al = *reinterpret_cast<const f32x2*>(fac + R + r), be = *reinterpret_cast<const f32x2*>(fac + 2 * R + r);
+                        l2[r / 2] = wide ? fma2(pack2(ex2(s.x - evf), ex2(s.y - evf)), be, mul2(l2[r / 2], al))
+                                         : fma2(pack2(p0, p1), mul2(be, wj2), mul2(l2[r / 2], al));
+                        // p <= 256 in fp16 (11 bits), its leading 4 bits, and 4 bits of what is left (exact differences)
+                        const __half2 ph = __floats2half2_rn(p0, p1);
+                        const __nv_fp8x2_storage_t h8 = __nv_cvt_halfraw2_to_fp8x2(ph, __NV_SATFINITE, __NV_E4M3);
+                        const __half2 rest = __hsub2(ph, __half2(__nv_cvt_fp8x2_to_halfraw2(h8, __NV_E4M3)));
+                        const __nv_fp8x2_storage_t l8 = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
+                        if (q & 1) {
+                            hi[q / 2] |= (uint32_t)h8 << 16;
+                            lo[q / 2] |= (uint32_t)l8 << 16;
+                        } else {
+                            hi[q / 2] = h8;
+                            lo[q / 2] = l8;
+                        }
+                    }
+                    const int swz = R == 64 ? (j >> 1) & 3 : R == 32 ? (j >> 2) & 1 : 0;
+                    uint8_t* at = P + j * R + (((c0 / 16) ^ swz) << 4);
+                    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(at + TILE * R) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pfull[g]);
+                ++k;
+            }
+            if (!ok) break;
+            // the part's sums over this group's rows, for the merge
+            if (piece > 0 && !warp_wait(lfree, (piece - 1) & 1, abort_flag, a.wait_ns)) break;
+            float v[R];
+#pragma unroll
+            for (int r = 0; r < R / 2; ++r) {
+                const float2 p = unpack2(l2[r]);
+                v[2 * r] = p.x;
+                v[2 * r + 1] = p.y;
+            }
+            // halve the rows while the lanes are paired: lane ends with the sums of its R / 32 rows
+            int n = R;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                if (n > 1) {
+                    n /= 2;
+#pragma unroll
+                    for (int r = 0; r < R / 2; ++r) {
+                        if (r >= n) break;
+                        const bool up = lane & off;
+                        const float keep = up ? v[r + n] : v[r], send = up ? v[r] : v[r + n];
+                        v[r] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, off);
+                    }
+                } else {
+                    v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], off);
+                }
+            }
+            float* ls = F + C::F_L + (g * 4 + wl) * R;
+            if (R == 64) { ls[2 * lane] = v[0]; ls[2 * lane + 1] = v[R > 32 ? 1 : 0]; }
+            else if (R == 32) ls[lane] = v[0];
+            else if ((lane & 1) == 0) ls[lane >> 1] = v[0];
+            if (wl == 0)
+#pragma unroll
+                for (int r = 0; r < RL; ++r)
+                    if (R >= 32 || lane < R) F[C::F_M + g * R + r * 32 + lane] = M[r];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(lfull);
+            left -= nt;
+            w.advance(a, facts, nt, left > 0);
+            ++piece;
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------------------ merge
+        const int wl = warp & 3;
+        constexpr int RL = R > 32 ? 2 : 1;
+        float* fac = F + C::F_MFAC + wl * 2 * R;
+        const bool on = D >= 128 || lane < 16;       // M = 64 leaves 16 rows in each quarter of the lanes
+        const int d0 = D >= 128 ? wl * 32 + lane : wl * 16 + (lane & 15);
+        uint32_t i = 0, piece = 0;
+        bool ok = true;
+        while (left > 0 && ok) {
+            const int nt = left < w.tiles - w.t ? (int)left : w.tiles - w.t;
+            f32x2 acc[C::MB * R / 2];
+            float M[RL];
+#pragma unroll
+            for (int r = 0; r < C::MB * R / 2; ++r) acc[r] = 0ull;
+#pragma unroll
+            for (int r = 0; r < RL; ++r) M[r] = -INFINITY;
+            for (int t = 0; t < nt; ++t, ++i) {
+                const int ob = i & 1;
+                if (!warp_wait(&ofull[ob], (i >> 1) & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll
+                for (int r = 0; r < RL; ++r) {
+                    const int row = r * 32 + lane;
+                    if (R < 32 && lane >= R) break;
+                    const float m = F[C::F_MT + (i & 3) * R + row];
+                    const float Mn = fmaxf(M[r], m);
+                    fac[row] = M[r] == -INFINITY ? 0.0f : ex2(M[r] - Mn);
+                    fac[R + row] = m == -INFINITY ? 0.0f : ex2(m - Mn);
+                    M[r] = Mn;
+                }
+                __syncwarp();
+                const uint32_t orow = tmem + ((uint32_t)(wl * 32) << 16) + C::TMEM_O + ob * C::MB * R;
+#pragma unroll
+                for (int c0 = 0; c0 < C::MB * R; c0 += 16) {
+                    uint32_t o[16];
+                    tc_ld_x16(orow + c0, o);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int r = (c0 + 2 * q) % R;
+                        const f32x2 al = *reinterpret_cast<const f32x2*>(fac + r), be = *reinterpret_cast<const f32x2*>(fac + R + r);
+                        f32x2& x = acc[c0 / 2 + q];
+                        x = fma2(pack2(__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1])), be, mul2(x, al));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ofree[ob]);
+            }
+            if (!ok || !warp_wait(lfull, piece & 1, abort_flag, a.wait_ns)) break;
+            float L[RL];
+#pragma unroll
+            for (int r = 0; r < RL; ++r) {
+                const int row = r * 32 + lane;
+                L[r] = 0.0f;
+                if (R < 32 && lane >= R) break;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float m = F[C::F_M + g * R + row];
+                    const float* ls = F + C::F_L + g * 4 * R + row;
+                    const float s = (ls[0] + ls[R]) + (ls[2 * R] + ls[3 * R]);
+                    L[r] += s * (m == -INFINITY ? 0.0f : ex2(m - M[r]));     // s may be NaN
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(lfree);
+            const int rows = w.rows(a), row0 = w.rt * R;
+            const bool whole = nt == w.tiles;
+            if (whole) {
+                // out = acc / L; lse = ln 2 (M - 8 + log2 L): p carries 2^8
+#pragma unroll
+                for (int r = 0; r < RL; ++r) {
+                    const int row = r * 32 + lane;
+                    if (row >= rows) break;
+                    fac[row] = L[r] == 0.0f ? 0.0f : 1.0f / L[r];
+                    if (wl == 0 && a.lse) {
+                        const int tr = row0 + row, node = tr / G;
+                        a.lse[(int64_t)(w.l.n0 + node) * a.n_q_heads + w.h * G + tr - node * G] =
+                            L[r] == 0.0f ? -INFINITY : (M[r] - 8.0f + log2f(L[r])) * 0.69314718055994531f;
+                    }
+                }
+                __syncwarp();
+                int node = row0 / G, sub = row0 - node * G;
+                __nv_bfloat16* out = a.out + ((int64_t)(w.l.n0 + node) * a.n_q_heads + w.h * G + sub) * D + d0;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    if (r >= rows) break;
+                    const float inv = fac[r];
+                    if (on)
+#pragma unroll
+                        for (int m = 0; m < C::MB; ++m) {
+                            const float2 x = unpack2(acc[m * R / 2 + r / 2]);
+                            // a node that sees nothing: zeros (its products are zeros too)
+                            out[m * 128] = __float2bfloat16_rn(((r & 1) ? x.y : x.x) * inv);
+                        }
+                    out += D;
+                    if (++sub == G) { sub = 0; out += (int64_t)(a.n_q_heads - G) * D; }
+                }
+            } else {
+                const int slot = 2 * blockIdx.x + (left == count ? 0 : 1);
+                float* part = reinterpret_cast<float*>(a.ws + parts_offset(gridDim.x)) + (size_t)slot * part_floats(R, D);
+                if (on)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        if (r >= rows) break;
+#pragma unroll
+                        for (int m = 0; m < C::MB; ++m) {
+                            const float2 x = unpack2(acc[m * R / 2 + r / 2]);
+                            part[r * D + m * 128 + d0] = (r & 1) ? x.y : x.x;
+                        }
+                    }
+                if (wl == 0)
+#pragma unroll
+                    for (int r = 0; r < RL; ++r)
+                        if (r * 32 + lane < rows) {
+                            part[R * D + r * 32 + lane] = M[r];
+                            part[R * D + R + r * 32 + lane] = L[r];
+                        }
+            }
+            __syncwarp();
+            left -= nt;
+            w.advance(a, facts, nt, left > 0);
+            ++piece;
+        }
+    } else if (warp == 12) {
+        // ------------------------------------------------------------ TMA
+        const int P = 1 << a.page_shift, rows_a_page = P < TILE ? P : TILE;
+        const int ppt = TILE / rows_a_page;          // copies a tile
+        uint32_t i = 0;
+        bool ok = true;
+        // this lane's page of tile t: its id, or -1 past the lane's rows
+        auto page_of = [&](int t) -> int {
+            const int64_t at = (int64_t)t * TILE + lane * rows_a_page;
+            if (lane >= ppt || at >= w.l.len) return -1;
+            int p = a.table[(int64_t)w.b * a.width + (at >> a.page_shift)];
+            if (p < 0 || p >= a.c.n_pages) {
+                record_error(a.err, MOE_DEV_BAD_PAGE);
+                p = 0;
+            }
+            return p;
+        };
+        while (left > 0 && ok) {
+            const int nt = left < w.tiles - w.t ? (int)left : w.tiles - w.t;
+            int page = page_of(w.t);
+            for (int t = w.t; t < w.t + nt; ++t, ++i) {
+                const int cur = page;
+                if (t + 1 < w.t + nt) page = page_of(t + 1);
+                const uint32_t copies = __popc(__ballot_sync(0xFFFFFFFFu, cur >= 0));
+                const int row = (cur * H + w.h) * P + ((t * TILE) & (P - 1) & ~(rows_a_page - 1));
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const uint32_t f = 2 * i + v, s = f % NS;
+                    if (!warp_wait(&empty[s], ((f / NS) & 1) ^ 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                    if (v == 0) {
+                        const uint32_t sc = i % NSC;
+                        if (!warp_wait(&scempty[sc], ((i / NSC) & 1) ^ 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                        if (lane == 0) mbar_arrive_expect_tx(&scfull[sc], copies * 2 * rows_a_page);
+                        ++sc_issued;
+                        __syncwarp();
+                        if (cur >= 0) {
+                            uint8_t* dst = smem + C::OFF_SC + sc * 256 + lane * rows_a_page;
+                            bulk_load(dst, a.c.k_scales + row, rows_a_page, &scfull[sc]);
+                            bulk_load(dst + TILE, a.c.v_scales + row, rows_a_page, &scfull[sc]);
+                        }
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&full[s], copies * rows_a_page * D);
+                    ++issued;
+                    __syncwarp();
+                    if (cur >= 0)
+#pragma unroll
+                        for (int p = 0; p < C::PANELS; ++p)
+                            tma_load_2d(smem + C::OFF_RING + s * C::SLOT + p * C::PANEL + lane * rows_a_page * C::ROWB,
+                                        v ? &maps.v : &maps.k, &full[s], p * 128, row);
+                }
+                if (!ok) break;
+            }
+            left -= nt;
+            w.advance(a, facts, nt, left > 0);
+        }
+    } else if (warp == 13) {
+        // ------------------------------------------------------------ MMA issue
+        if (lane == 0) {
+            constexpr uint64_t KD = desc_base(C::ROWB == 128 ? 2 : 4, 8 * C::ROWB);       // K, Q (by K) and V (by M): one atom, 8 rows
+            constexpr uint64_t PD = desc_base(R == 64 ? 4 : R == 32 ? 6 : 0, 8 * R);
+            constexpr uint32_t ID_S = idesc_e4m3(128, 2 * R, 0, 0), ID_O = idesc_e4m3(D < 128 ? 64 : 128, R, 1, 1);
+            const uint32_t ring = smem_u32(smem + C::OFF_RING);
+            uint32_t i = 0, piece = 0;
+            bool ok = true;
+            auto pv = [&](uint32_t n) -> bool {                       // O of tile n
+                const int ob = n & 1;
+                const uint32_t u = n >> 1, f = 2 * n + 1, s = f % NS;
+                if (!mbar_wait(&pfull[ob], u & 1, abort_flag, a.wait_ns) || !mbar_wait(&full[s], (f / NS) & 1, abort_flag, a.wait_ns) ||
+                    !mbar_wait(&ofree[ob], (u & 1) ^ 1, abort_flag, a.wait_ns))
+                    return false;
+                tc_fence_after();
+                const uint32_t va = ring + s * C::SLOT, pa = smem_u32(smem + C::OFF_P + ob * C::PBUF);
+#pragma unroll
+                for (int m = 0; m < C::MB; ++m)
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)                     // 4 steps of 32 rows with hi, 4 with lo
+                        tc_mma_f8(tmem + C::TMEM_O + (ob * C::MB + m) * R, desc_at(KD, va + m * C::PANEL + (kk & 3) * 32 * C::ROWB),
+                                  desc_at(PD, pa + (kk >> 2) * TILE * R + (kk & 3) * 32 * R), ID_O, kk ? 1u : 0u);
+                tc_commit(&empty[s]);
+                tc_commit(&ofull[ob]);
+                return true;
+            };
+            while (left > 0 && ok) {
+                const int nt = left < w.tiles - w.t ? (int)left : w.tiles - w.t;
+                const uint32_t qb = piece & 1;
+                if (!mbar_wait(&qfull[qb], (piece >> 1) & 1, abort_flag, a.wait_ns)) break;
+                const uint32_t qa = smem_u32(smem + C::OFF_Q + qb * C::QBUF);
+                for (int t = 0; t < nt; ++t, ++i) {
+                    const uint32_t f = 2 * i, s = f % NS;
+                    if (!mbar_wait(&full[s], (f / NS) & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t ka = ring + s * C::SLOT;
+#pragma unroll
+                    for (int kk = 0; kk < D / 32; ++kk) {
+                        constexpr int STEPS = C::ROWB / 32;
+                        tc_mma_f8(tmem + (i & 1) * 2 * R, desc_at(KD, ka + (kk / STEPS) * C::PANEL + (kk % STEPS) * 32),
+                                  desc_at(KD, qa + (kk / STEPS) * 2 * R * C::ROWB + (kk % STEPS) * 32), ID_S, kk ? 1u : 0u);
+                    }
+                    tc_commit(&empty[s]);
+                    tc_commit(&sfull[i & 1]);
+                    if (t == nt - 1) tc_commit(&qfree[qb]);
+                    if (i > 0 && !pv(i - 1)) { ok = false; break; }     // also: S of tile i - 1 has been read before tile i + 1
+                }
+                left -= nt;
+                ++piece;
+                w.advance(a, facts, nt, left > 0);
+            }
+            if (ok && left <= 0 && i > 0) (void)pv(i - 1);
+        }
+    } else {
+        // ------------------------------------------------------------ queries
+        constexpr int LPR = D / 8, RPW = 32 / LPR;                    // lanes a row, rows a warp takes at once
+        const int part = lane % LPR, sub = lane / LPR;
+        uint32_t piece = 0;
+        while (left > 0) {
+            const int nt = left < w.tiles - w.t ? (int)left : w.tiles - w.t;
+            const uint32_t qb = piece & 1;
+            if (!warp_wait(&qfree[qb], ((piece >> 1) & 1) ^ 1, abort_flag, a.wait_ns)) break;
+            const int rows = w.rows(a), row0 = w.rt * R;
+            uint8_t* Q = smem + C::OFF_Q + qb * C::QBUF;
+            float* qf = F + C::F_QF + (piece & 3) * R;
+#pragma unroll 4
+            for (int r0 = (warp - 14) * RPW; r0 < R; r0 += 2 * RPW) {
+                const int r = r0 + sub;
+                uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                if (r < rows) {
+                    const int node = (row0 + r) / G, qh = w.h * G + (row0 + r) - node * G;
+                    raw = *reinterpret_cast<const uint4*>(a.q + (w.l.n0 + node) * a.q_token_stride + qh * a.q_head_stride + part * 8);
+                }
+                const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+                float x[8];
+                uint32_t key = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[2 * e] = __uint_as_float(in[e] << 16);
+                    x[2 * e + 1] = __uint_as_float(in[e] & 0xFFFF0000u);
+                    key = max(key, max((in[e] << 16) & 0x7FFFFFFFu, in[e] & 0x7FFF0000u));   // |x| as integers
+                }
+#pragma unroll
+                for (int off = LPR / 2; off > 0; off >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, off));
+                int up = key ? 7 - floor_log2_pos(__uint_as_float(key)) : 0;
+                up = up > 120 ? 120 : (up < -120 ? -120 : up);
+                const float gain = exp2_int(up);
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x0 = x[2 * e] * gain, x1 = x[2 * e + 1] * gain;
+                    const __nv_fp8x2_storage_t h8 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+                    const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h8, __NV_E4M3)));
+                    const __nv_fp8x2_storage_t l8 =
+                        __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y), __NV_SATFINITE, __NV_E4M3);
+                    if (e & 1) { hi[e / 2] |= (uint32_t)h8 << 16; lo[e / 2] |= (uint32_t)l8 << 16; }
+                    else { hi[e / 2] = h8; lo[e / 2] = l8; }
+                }
+                // a row that is not finite: its scores become NaN
+                if (part == 0) qf[r] = key >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : exp2_int(-up);
+                const int byte = part * 8, panel = byte / C::ROWB, in_row = byte % C::ROWB;
+                auto place = [&](int row) {
+                    const int swz = C::ROWB == 128 ? row & 7 : (row >> 1) & 3;
+                    return Q + panel * 2 * R * C::ROWB + row * C::ROWB + (((in_row >> 4) ^ swz) << 4) + (in_row & 15);
+                };
+                *reinterpret_cast<uint2*>(place(r)) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(place(R + r)) = make_uint2(lo[0], lo[1]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&qfull[qb]);
+            left -= nt;
+            ++piece;
+            w.advance(a, facts, nt, left > 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {                               // final after the barrier: nothing new is issued past it
+        if (warp == 12 && lane == 0) {
+            drain_stage_fills(full, NS, issued);
+            drain_stage_fills(scfull, NSC, sc_issued);
+        }
+        if (warp == 13 && lane == 0) tc_drain(drain);
+        tc_fence_before();
+        __syncthreads();
+    }
+    if (warp == 13) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+    if (tid == 0 && *abort_flag) record_error(a.err, MOE_DEV_TIMEOUT);
 }
+
+// ------------------------------------------------------------------ join
+
+// One warp per tree row of a unit that several CTAs share; blockIdx.x is the
+// second of them (the first whose part begins inside the unit). The parts are
+// added in the order of the cache rows, so the result does not depend on the order
+// in which they were done.
+constexpr int JOIN_WARPS = 8;
+
+template <int D, int R>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) tree_attention_join(const AttnArgs a, int ctas) {
+    pdl_trigger();
+    pdl_wait();
+    const JoinHead head = *reinterpret_cast<const JoinHead*>(a.ws);
+    const int c = blockIdx.x + 1;
+    if (c >= head.parts) return;
+    const JoinUnit u = reinterpret_cast<const JoinUnit*>(a.ws + JOIN_UNITS)[c];
+    auto begin = [&](int k) { return (int64_t)((unsigned long long)head.total * k / head.parts); };
+    if (begin(c) <= u.first || begin(c - 1) > u.first) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = blockIdx.y * JOIN_WARPS + warp;
+    if (r >= u.rows) return;
+    // the last CTA whose part begins before the unit's end: total k < end parts
+    const int last = (int)(((unsigned long long)u.end * head.parts - 1) / head.total);
+    const float* parts = reinterpret_cast<const float*>(a.ws + parts_offset(ctas));
+    const int before = begin(c - 1) < u.first;       // that CTA comes to the unit from another one
+    auto part = [&](int k) { return parts + (size_t)(2 * k + (k == c - 1 ? before : 0)) * part_floats(R, D); };
+    float M = -INFINITY;
+    for (int k = c - 1 + lane; k <= last; k += 32) M = fmaxf(M, part(k)[R * D + r]);
+    M = warp_max(M);
+    constexpr int V = D / 32;                        // columns a lane
+    float acc[V] = {}, L = 0.0f;
+#pragma unroll 4
+    for (int k = c - 1; k <= last; ++k) {
+        const float* p = part(k);
+        const float m = p[R * D + r];
+        const float f = m == -INFINITY ? 0.0f : ex2(m - M);
+        L += f * p[R * D + R + r];                   // NaN stays, also with a weight of zero
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] += f * p[r * D + e * 32 + lane];
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    const int tr = u.row0 + r, node = tr / a.group;
+    const int64_t at = (int64_t)(u.node0 + node) * a.n_q_heads + u.head * a.group + tr - node * a.group;
+#pragma unroll
+    for (int e = 0; e < V; ++e) a.out[at * D + e * 32 + lane] = __float2bfloat16_rn(acc[e] * inv);
+    if (a.lse && lane == 0) a.lse[at] = L == 0.0f ? -INFINITY : (M - 8.0f + log2f(L)) * 0.69314718055994531f;
+}
+
+// ------------------------------------------------------------------ host side
 
 int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
 
-size_t attention_workspace() { return 256; }
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+cudaError_t codes_map(CUtensorMap* m, const void* base, const moe_kv_cache& c) {
+    auto enc = encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.n_pages * c.n_kv_heads * c.page_size};
+    const cuuint64_t strides[1] = {(cuuint64_t)c.head_dim};
+    const cuuint32_t box[2] = {(cuuint32_t)(c.head_dim < 128 ? c.head_dim : 128), (cuuint32_t)(c.page_size < TILE ? c.page_size : TILE)};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, c.head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+constexpr int max_rows(int D) { return D == 256 ? 32 : 64; }  // R: shared memory holds 64 tree rows of up to 128 values
+
+template <int D, int R>
+cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
+    using C = Cfg<D, R>;
+    AttnMaps maps;
+    cudaError_t e = codes_map(&maps.k, a.c.k_codes, a.c);
+    if (e == cudaSuccess) e = codes_map(&maps.v, a.c.v_codes, a.c);
+    if (e != cudaSuccess) return e;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+        e = cudaFuncSetAttribute(tree_attention<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
+    const int ctas = moe_sm_count();
+    moe_prof_begin(MK_ATTENTION, s);
+    e = moe_launch(tree_attention<D, R>, dim3((unsigned)ctas), dim3(ATTN_THREADS), C::SMEM, s, maps, a);
+    moe_prof_end(MK_ATTENTION, s);
+    if (e != cudaSuccess || ctas < 2) return e;
+    moe_prof_begin(MK_ATTENTION_JOIN, s);
+    e = moe_launch(tree_attention_join<D, R>, dim3((unsigned)(ctas - 1), R / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0, s, a, ctas);
+    moe_prof_end(MK_ATTENTION_JOIN, s);
+    return e;
+}
+
+// The tile of tree rows: the smallest that takes a lane's rows of one kv head at once.
+template <int D>
+cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
+    const int64_t rows = (int64_t)(a.max_nodes < a.n_nodes ? a.max_nodes : a.n_nodes) * a.group;
+    if (rows <= 16) return launch<D, 16>(a, s);
+    if (rows <= 32 || max_rows(D) == 32) return launch<D, 32>(a, s);
+    return launch<D, max_rows(D)>(a, s);
+}
 
 }  // namespace
 
 size_t moe_tree_attention_workspace_bytes(int n_nodes, int n_q_heads, int n_kv_heads, int head_dim, int lanes) {
     if (n_nodes < 1 || n_q_heads < 1 || n_kv_heads < 1 || head_dim < 1 || lanes < 1) return 0;
-    return attention_workspace();
+    const int ctas = moe_sm_count();
+    return parts_offset(ctas) + (size_t)2 * ctas * part_floats(max_rows(head_dim), head_dim) * sizeof(float);
 }
 
 moe_status moe_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int n_nodes, int n_q_heads,
@@ -169,13 +1079,15 @@ moe_status moe_tree_attention(const void* q, int64_t q_token_stride, int64_t q_h
     a.max_nodes = max_nodes;
     a.mask = tree_mask;
     a.mask_words = mask_words;
-    a.scale = scale;
+    a.scale_log2 = scale * 1.4426950408889634f;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
+    a.ws = static_cast<uint8_t*>(workspace);
     a.err = err;
-    moe_prof_begin(MK_ATTENTION, s);
-    const cudaError_t e = moe_launch(tree_attention, dim3((unsigned)n_nodes, (unsigned)n_q_heads), dim3(128), 0, s, a);
-    moe_prof_end(MK_ATTENTION, s);
-    moe_count_launches(1);
+    a.wait_ns = moe_wait_limit_ns();
+    const cudaError_t e = cache->head_dim == 64    ? launch_rows<64>(a, s)
+                          : cache->head_dim == 128 ? launch_rows<128>(a, s)
+                                                   : launch_rows<256>(a, s);
+    moe_count_launches(2);
     return e == cudaSuccess ? MOE_OK : MOE_ECUDA;
 }
