@@ -15,39 +15,36 @@
 //     have: hi = e5m2(p), which is the upper byte of p in fp16 (rounded by an
 //     integer add), lo = e4m3 of the rest.
 //   - The scale of a key row multiplies its column of scores; the scale of a
-//     value row is added to the exponent: s' = s + ev_j, p = 2^(s' - m + 8), so
+//     value row is added to the exponent: s' = s + ev_j, p = 2^(s' - m + 6), so
 //     values of any size keep their precision; the sum of weights gets p 2^-ev_j.
 //   - m is a running reference, not each tile's maximum: it is the maximum of s'
-//     when it is set, and stays until a score passes it by 2^3.5 (p would pass what lo can
+//     when it is set, and stays until a score passes it by 2^5.5 (p would pass what lo can
 //     hold); then it is set again and what has been added up is scaled down. Most tiles
 //     so need no maximum at all: one compare, a vote, no reduction over the rows.
-//     Weights below 2^-25 of the largest are dropped, the rest keep at least the 3 bits of
-//     hi, which is unbiased.
+//     Weights below 2^-23 of the largest are dropped, the rest keep at least the 3 bits of
+//     hi, rounded to nearest.
 //
-// Orientation: cache rows are the MMA's M (128), tree rows its N (2R for S, R for
-// O: hi and lo of the queries side by side; those of the probabilities
-// accumulate), so a single token costs N = 16 and a wide tree 64, and nothing
-// is padded to 128:
-//   S^T[128 rows, 2R] = K[128, D] Q^T           O^T[D, R] += V^T[D, 128] P^T[128, R]
+// Orientation: cache rows are the MMA's M (128), tree rows its N, so a single
+// token costs N = 16 and a wide tree 64 or 128, and nothing is padded to 128;
+// hi and lo accumulate:
+//   S^T[128 rows, R] = K[128, D] Q^T            O^T[D, R] += V^T[D, 128] P^T[128, R]
 // A thread of a softmax group is a cache row: the rows' scales are its own
 // registers, the sums of weights are kept per thread and added up once at the end.
 //
-// Two softmax groups of four warps. Up to R tree rows (R = 16, 32, 64; 32 at
-// head_dim 256) they take the tiles of 128 cache rows in turn, each with an O of
-// its own; above, PAIR, both take every tile, each for R of 2R tree rows, so that the
-// cache is read once for twice the rows.
+// Two softmax groups take the tiles of 128 cache rows in turn, each with an O of
+// its own, four warps for up to 32 tree rows and eight for 64 (32 tree rows are what a
+// thread can hold next to their sums).
 //
 // Work: the (lane, kv head, tile of tree rows) units, each a run of cache
 // tiles, are laid end to end and cut into equal parts, one per CTA. A unit that one
 // CTA does whole is written at once; the others leave their parts (output, maximum, sum)
 // in the workspace and tree_attention_join adds them up in order.
 //
-// Roles (512 threads):
-//   warps 0-3, 4-7   softmax groups
-//   warps 8-11       the next unit's queries (split and laid out), a finished unit's output
-//   warp 12          TMA, one copy per page
-//   warp 13          MMA issue, TMEM
-//   warp 14          the rows' scales
+// Roles: 8 or 16 warps of softmax, then
+//   four warps       the next unit's queries (split and laid out), a finished unit's output
+//   a warp           TMA, one copy per page
+//   a warp           MMA issue, TMEM
+//   a warp           the rows' scales
 // Waits are bounded as in the expert GEMMs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -86,8 +83,7 @@ struct AttnMaps {
 };
 
 constexpr int TILE = 128;                        // cache rows a tile
-constexpr int ATTN_THREADS = 512;
-constexpr int LANE_CACHE = 512;                  // lanes whose facts are kept in shared memory
+constexpr int LANE_CACHE = 256;                  // lanes whose facts are kept in shared memory
 
 // What the join needs, at the start of the workspace: the cut, and for each CTA the unit that its part begins in.
 struct JoinHead {
@@ -101,45 +97,64 @@ struct JoinUnit {
 };
 constexpr size_t JOIN_UNITS = 256;               // byte offset of JoinUnit[CTAs]
 
-__host__ __device__ constexpr size_t part_floats(int RU, int D) { return (size_t)RU * (D + 2); }
+__host__ __device__ constexpr size_t part_floats(int R, int D) { return (size_t)R * (D + 2); }
 __host__ __device__ inline size_t parts_offset(int ctas) { return (JOIN_UNITS + (size_t)ctas * sizeof(JoinUnit) + 255) / 256 * 256; }
 
-template <int D, int R, bool PAIR>
+// First tile of part k: total / parts tiles each, one more in the first total % parts. (64-bit divisions only where needed.)
+MOE_DEV int64_t part_begin(unsigned long long total, int parts, int k) {
+    const unsigned long long each = total >> 32 ? total / parts : (uint32_t)total / (uint32_t)parts;
+    const int more = (int)(total - each * parts);
+    return (int64_t)(each * k) + (k < more ? k : more);
+}
+// The part that holds tile x.
+MOE_DEV int part_of(unsigned long long total, int parts, unsigned long long x) {
+    const unsigned long long each = total / parts, more = total - each * parts;
+    return (int)(x < more * (each + 1) ? x / (each + 1) : more + (x - more * (each + 1)) / each);
+}
+
+template <int D, int R>                          // R: tree rows of a unit
 struct Cfg {
-    static constexpr int RU = PAIR ? 2 * R : R;               // tree rows of a unit
+    static constexpr int RH = R < 32 ? R : 32;                // tree rows of a softmax warpgroup: its threads' registers
+    static constexpr int HALVES = R / RH;                     // warpgroups of a softmax group
+    static constexpr int SW = 8 * HALVES;                     // softmax warps, of two groups
+    static constexpr int THREADS = (SW + 8) * 32;             // then four of queries and outputs, TMA, MMA, scales, one idle
     static constexpr int ROWB = D >= 128 ? 128 : 64;          // bytes of an operand row: one swizzle atom
     static constexpr int PANELS = D / ROWB;
     static constexpr int PANEL = TILE * ROWB;
     static constexpr int SLOT = TILE * D;
-    static constexpr int QROWS = 2 * RU;                      // hi and lo of each half's rows
-    static constexpr int QBUFS = PAIR ? 1 : 2;                // PAIR: its 2R rows leave room for one
+    static constexpr int QROWS = 2 * R;                       // hi, then lo
     static constexpr int QBUF = QROWS * D;
     static constexpr int PBUF = 2 * TILE * R;
-    // ring of key and value tiles: what fits, 8 tiles of 16 KB at most (more measured no faster)
-    static constexpr int NS = D == 64 ? 12 : D == 128 ? 8 : R == 16 ? 5 : PAIR ? 5 : 5;
+    static constexpr int SB = 4;                              // buffers of S
+    static constexpr int NS = D == 64 ? 16 : D == 256 ? 5 : R == 64 ? 9 : R == 32 ? 11 : 12;      // ring of key and value tiles: what fits
     static constexpr int NSC = 4;                             // ring of scale tiles (128 key bytes, 128 value bytes)
     static constexpr int MB = D == 256 ? 2 : 1;               // M blocks of O^T
     static constexpr int OFF_RING = 0;
     static constexpr int OFF_P = OFF_RING + NS * SLOT;
     static constexpr int OFF_Q = OFF_P + 2 * PBUF;
-    static constexpr int OFF_SC = OFF_Q + QBUFS * QBUF;
+    static constexpr int OFF_SC = OFF_Q + 2 * QBUF;
     static constexpr int OFF_F = OFF_SC + NSC * 256;          // floats from here
     static constexpr int F_O = 0;                             // [2 groups][R] 8 - m, as added to s'
     static constexpr int F_AL = F_O + 2 * R;                  // [2][R] scale-down of what has been added up
-    static constexpr int F_WMAX = F_AL + 2 * R;               // [2][4 warps][R]
-    static constexpr int F_QF = F_WMAX + 8 * R;               // [4][RU] 2^-a of the queries' rows
-    static constexpr int F_L = F_QF + 4 * RU;                 // [2][4][R] sums at a part's end
+    static constexpr int F_WMAX = F_AL + 2 * R;               // [2 groups][HALVES][2][4 warps][RH]
+    static constexpr int F_QF = F_WMAX + 16 * R;              // [4][R] 2^-a of the queries' rows
+    static constexpr int F_QU = F_QF + 4 * R;                // [4][2] 2^-a of all rows of a unit; whether the rows' differ instead
+    static constexpr int F_QX = F_QU + 8;                     // [largest, smallest][unit parity][4 warps] |q| of the rows, as bits
+    static constexpr int F_L = F_QX + 16;                 // [2][4][R] sums at a part's end
     static constexpr int F_M = F_L + 8 * R;                   // [2][R] their references
-    static constexpr int F_ST = F_M + 2 * R;                  // [4 warps][2][RU] factors of the output
-    static constexpr int F_END = F_ST + 8 * RU;
+    static constexpr int F_ST = F_M + 2 * R;                  // [4 warps][2][R] factors of the output
+    static constexpr int F_END = F_ST + 8 * R;
     static constexpr int OFF_LANE = OFF_F + F_END * 4;        // int n0, n, len [LANE_CACHE]
     static constexpr int OFF_SCAN = OFF_LANE + 3 * LANE_CACHE * 4;
     static constexpr int OFF_BAR = OFF_SCAN + 32 * 8 + 64;
-    // full, empty [NS]; scale full, empty [NSC]; sfull, pfull, pfree, vote, maxima, qfull, qfree, ofull, ofree [2]; lfull, lfree, drain
-    static constexpr int N_BARS = 2 * NS + 2 * NSC + 18 + 3;
-    static constexpr int OFF_MISC = (OFF_BAR + N_BARS * 8 + 15) / 16 * 16;     // tmem slot, abort flag, votes [2][2][4]
-    static constexpr int SMEM = OFF_MISC + 16 + 64 + 1024;
-    static constexpr int TMEM_O = 4 * R;                      // after S of both groups: O [group][unit parity][MB][R]
+    // full, empty [NS]; scale full, empty [NSC]; sfull, vote, maxima [4]; pfull, pfree, qfull, qfree, ofull, ofree [2];
+    // lfull, lfree, qmax, drain
+    static constexpr int N_BARS = 2 * NS + 2 * NSC + 12 + 12 + 4;
+    static constexpr int OFF_MISC = (OFF_BAR + N_BARS * 8 + 15) / 16 * 16;     // tmem slot, abort flag, votes [4 warpgroups][2][4]
+    static constexpr int SMEM = OFF_MISC + 16 + 128 + 1024;
+    // Tiles whose S may be under way: the buffers, and (an odd ring) not past a slot whose values are still to be used
+    static constexpr int LOOK = NS % 2 && NS / 2 + 1 < SB ? NS / 2 + 1 : SB;
+    static constexpr int TMEM_O = 4 * R;                      // after S (4 R columns): O [group][unit parity][MB][R]
     static constexpr int TMEM_USED = 4 * R + 4 * R * MB;
     static constexpr int TMEM_COLS = TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
     static_assert(TMEM_USED <= 512 && SMEM <= 227 * 1024, "TMEM, shared memory");
@@ -147,7 +162,7 @@ struct Cfg {
     static_assert(R == 16 || R == 32 || R == 64, "R");
 };
 
-constexpr float P_EXP = 8.0f;                    // p = 2^8 at the reference
+constexpr float P_EXP = 6.0f;                    // p = 2^6 at the reference
 constexpr float P_EXP_MAX = 11.5f;               // above it, lo = e4m3(p - hi) could pass 448
 
 // ------------------------------------------------------------------ small device pieces
@@ -190,6 +205,19 @@ MOE_DEV float warp_max(float v) {
     return r;
 }
 
+// Whether the phase with this parity is over, without waiting.
+MOE_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 MOE_DEV void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -198,6 +226,10 @@ MOE_DEV void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t
         ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+
+// Moves registers between the warpgroups of a block of 768 threads launched with 80 each: 4 x 96 + 56 + 40 = 6 x 80.
+template <int N> MOE_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> MOE_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // kind::f8f6f4, e4m3 x e4m3 (or x e5m2) -> fp32; a_mn, b_mn: whether A and B lie with M and N (instead of K) contiguous.
 __host__ __device__ constexpr uint32_t idesc_f8(int m, int n, int a_mn, int b_mn, int b_e5m2) {
@@ -218,9 +250,31 @@ MOE_DEV void tc_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
                  : "r"(taddr));
 }
 
-// Moves registers between the warpgroups of a block of 512 threads launched with 128 each: 2 x 184 + 80 + 64 = 4 x 128.
-template <int N> MOE_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> MOE_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// N consecutive columns of this lane of TMEM, complete on return. One wide load, not several: beside running
+// MMAs each wait costs 250 to 400 clocks.
+MOE_DEV void tc_load(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+MOE_DEV void tc_load(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
 
 // Shared-memory matrix descriptor without its address: swizzle 2 = 128 B, 4 = 64 B, 6 = 32 B, 0 = none; `group` =
 // bytes from one group of eight rows (of the strided axis) to the next. Every operand here is one
@@ -272,7 +326,7 @@ struct Walk {
     MOE_DEV void start(const AttnArgs& a, const int* facts, int lane, int64_t offset) {
         b = lane;
         enter(a, facts);
-        const int u = (int)(offset / tiles);
+        const int u = offset >> 32 ? (int)(offset / tiles) : (int)((uint32_t)offset / (uint32_t)tiles);
         t = (int)(offset - (int64_t)u * tiles);
         h = u / nrt;
         rt = u - h * nrt;
@@ -297,10 +351,10 @@ struct Walk {
     }
 };
 
-template <int D, int R, bool PAIR>
-__global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
-    using C = Cfg<D, R, PAIR>;
-    constexpr int RU = C::RU;
+template <int D, int R>
+__global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
+    using C = Cfg<D, R>;
+    constexpr int RH = C::RH, SW = C::SW, ATTN_THREADS = C::THREADS;
     constexpr int NS = C::NS, NSC = C::NSC;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -308,21 +362,22 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
     uint64_t* empty = full + NS;
     uint64_t* scfull = empty + NS;
     uint64_t* scempty = scfull + NSC;
-    uint64_t* sfull = scempty + NSC;             // [2 groups] S of a tile is ready
-    uint64_t* pfull = sfull + 2;                 // [2] P is written (and S has been read)
+    uint64_t* sfull = scempty + NSC;             // [SB] S of a tile is ready
+    uint64_t* pfull = sfull + 4;                 // [2 groups] P is written (and S has been read)
     uint64_t* pfree = pfull + 2;                 // [2] P has been read (and added to O)
-    uint64_t* vote = pfree + 2;                  // [2] the group's four warps have compared a tile's scores
-    uint64_t* maxima = vote + 2;                 // [2] ... have written a tile's maxima
-    uint64_t* qfull = maxima + 2;                // [QBUFS]
+    uint64_t* vote = pfree + 2;                  // [warpgroups] the four warps have compared a tile's scores
+    uint64_t* maxima = vote + 4;                 // [warpgroups] ... have written a tile's maxima
+    uint64_t* qfull = maxima + 4;                // [2]
     uint64_t* qfree = qfull + 2;
     uint64_t* ofull = qfree + 2;                 // [2] O of a part is complete
     uint64_t* ofree = ofull + 2;                 // [2] ... and has been read
     uint64_t* lfull = ofree + 2;                 // the sums of a part are written
     uint64_t* lfree = lfull + 1;                 // ... and read
-    uint64_t* drain = lfree + 1;
+    uint64_t* qmax = lfree + 1;                  // the four query warps have their maxima
+    uint64_t* drain = qmax + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-    volatile int* votes = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);       // [2 groups][2][4 warps]
+    volatile int* votes = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);       // [warpgroups][2][4 warps]
     float* F = reinterpret_cast<float*>(smem + C::OFF_F);
     int* facts = reinterpret_cast<int*>(smem + C::OFF_LANE);
     unsigned long long* scratch = reinterpret_cast<unsigned long long*>(smem + C::OFF_SCAN);
@@ -334,12 +389,13 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
     pdl_trigger();
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-        for (int s = 0; s < NSC; ++s) { mbar_init(&scfull[s], 1); mbar_init(&scempty[s], PAIR ? 8 : 4); }
+        for (int s = 0; s < NSC; ++s) { mbar_init(&scfull[s], 1); mbar_init(&scempty[s], SW / 2); }
+        for (int s = 0; s < 4; ++s) { mbar_init(&sfull[s], 1); mbar_init(&vote[s], 4); mbar_init(&maxima[s], 4); }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&sfull[s], 1); mbar_init(&pfull[s], 4); mbar_init(&pfree[s], 1); mbar_init(&vote[s], 4); mbar_init(&maxima[s], 4);
-            mbar_init(&qfull[s], 4); mbar_init(&qfree[s], 1); mbar_init(&ofull[s], 1); mbar_init(&ofree[s], 4);
+            mbar_init(&pfull[s], SW / 2); mbar_init(&pfree[s], 1); mbar_init(&qfull[s], 4); mbar_init(&qfree[s], 1);
+            mbar_init(&ofull[s], 1); mbar_init(&ofree[s], 4);
         }
-        mbar_init(lfull, 8); mbar_init(lfree, 4); mbar_init(drain, 1);
+        mbar_init(lfull, SW); mbar_init(lfree, 4); mbar_init(qmax, 4); mbar_init(drain, 1);
         *abort_flag = 0;
         *begin_lane = 0;
         *begin_off = 0;
@@ -347,14 +403,14 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
         prefetch_tmap(&maps.k);
         prefetch_tmap(&maps.v);
     }
-    if (warp == 13) { tmem_alloc(tmem_slot, C::TMEM_COLS); tmem_relinquish(); }
+    if (warp == SW + 5) { tmem_alloc(tmem_slot, C::TMEM_COLS); tmem_relinquish(); }
     pdl_wait();
 
     // ---------------------------------------------------------------- the cut
     auto work_of = [&](const Lane& l) -> unsigned long long {
         if (l.n == 0) return 0ull;
         const unsigned long long tiles = l.len > 0 ? (l.len + TILE - 1) / TILE : 1;
-        return (unsigned long long)H * ((l.n * G + RU - 1) / RU) * tiles;
+        return (unsigned long long)H * ((l.n * G + R - 1) / R) * tiles;
     };
     unsigned long long total = 0, mine = 0, incl = 0;
     for (int b0 = 0; b0 < a.lanes; b0 += ATTN_THREADS) {
@@ -377,8 +433,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
     }
     const int parts = total < gridDim.x ? (int)total : (int)gridDim.x;
     const bool active = (int)blockIdx.x < parts;
-    const int64_t first = active ? (int64_t)(total * blockIdx.x / parts) : 0;
-    const int64_t count = active ? (int64_t)(total * (blockIdx.x + 1) / parts) - first : 0;
+    const int64_t first = active ? part_begin(total, parts, blockIdx.x) : 0;
+    const int64_t count = active ? part_begin(total, parts, blockIdx.x + 1) - first : 0;
     if (active) {
         if (a.lanes <= ATTN_THREADS) {
             const unsigned long long excl = incl - mine;
@@ -407,64 +463,61 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    Walk<RU> w;
+    Walk<R> w;
     w.start(a, facts, active ? *begin_lane : 0, active ? *begin_off : 0);
     if (tid == 0) {
         if (blockIdx.x == 0) *reinterpret_cast<JoinHead*>(a.ws) = JoinHead{(int64_t)total, parts, 0};
         if (active)
             reinterpret_cast<JoinUnit*>(a.ws + JOIN_UNITS)[blockIdx.x] =
-                JoinUnit{first - w.t, first - w.t + w.tiles, w.l.n0, w.rows(a), w.h, w.rt * RU};
+                JoinUnit{first - w.t, first - w.t + w.tiles, w.l.n0, w.rows(a), w.h, w.rt * R};
     }
     int64_t left = count;
     uint32_t issued = 0;                             // ring fills, by the producer
 
-    if (warp < 8) {
+    if (warp < SW) {
         // ------------------------------------------------------------ softmax
-        if constexpr (R == 64) regs_up<184>();
-        const int g = warp >> 2, wl = warp & 3;      // group, warp in it
+        if constexpr (R == 64) regs_up<96>();
+        const int wg = warp >> 2, wl = warp & 3;     // warpgroup, warp in it
+        const int g = wg / C::HALVES, h = wg % C::HALVES;             // group, which of its tree rows
         const int j = tid & 127;                     // this thread's row of the tile
-        const uint32_t trow = tmem + ((uint32_t)(wl * 32) << 16) + g * 2 * R;
-        float* off = F + C::F_O + g * R;
-        float* alpha = F + C::F_AL + g * R;
-        float* wmax = F + C::F_WMAX + g * 4 * R;
+        const uint32_t trow = tmem + ((uint32_t)(wl * 32) << 16) + h * RH;
+        float* off = F + C::F_O + g * R + h * RH;
+        float* alpha = F + C::F_AL + g * R + h * RH;
         uint32_t i = 0, k = 0, sets = 0, polls = 0, piece = 0;       // tile of the CTA; of this group; references set; votes; part
-        constexpr int RL = R > 32 ? 2 : 1;           // tree rows a lane keeps the reference of: lane, lane + 32
         bool ok = true;
         while (left > 0 && ok) {
             const int nt = left < w.tiles - w.t ? (int)left : w.tiles - w.t;
-            f32x2 l2[R / 2];
-            float M[RL];
+            f32x2 l2[RH / 2];
+            float M = -INFINITY;                     // reference of tree row `lane`
 #pragma unroll
-            for (int r = 0; r < R / 2; ++r) l2[r] = 0ull;
-#pragma unroll
-            for (int r = 0; r < RL; ++r) M[r] = -INFINITY;
-            const float* qf = F + C::F_QF + (piece & 3) * RU + (PAIR ? g * R : 0);
+            for (int r = 0; r < RH / 2; ++r) l2[r] = 0ull;
+            const float* qf = F + C::F_QF + (piece & 3) * R + h * RH;
             const int prefix = w.l.len - w.l.n;
-            const int row0 = w.rt * RU + (PAIR ? g * R : 0);         // this group's tree rows in the lane
+            const int row0 = w.rt * R + h * RH;      // this warpgroup's tree rows in the lane
             uint32_t ev_most = 0;                    // largest value scale seen so far
             bool set = true;                         // the reference is to be set (a part's first tile)
             for (int t = w.t; t < w.t + nt; ++t, ++i) {
-                if (!PAIR && (int)(i & 1) != g) continue;
+                if ((int)(i & 1) != g) continue;
                 const int j0 = t * TILE;
                 const int valid = w.l.len - j0;      // rows of the tile that exist (can be <= 0 or > 128)
                 const bool masked = j0 + TILE > prefix;
                 // what this row is to each tree row
-                uint64_t sees = ~0ull;
+                uint32_t sees = ~0u;
                 if (masked) {
                     const int n = j0 + j - prefix;
                     if (j >= valid) {
-                        sees = 0ull;
+                        sees = 0u;
                     } else if (n >= 0) {
-                        sees = 0ull;
-                        const int end = w.l.n * G < row0 + R ? w.l.n * G : row0 + R;
+                        sees = 0u;
+                        const int end = w.l.n * G < row0 + RH ? w.l.n * G : row0 + RH;
                         for (int t1 = row0 / G; t1 * G < end; ++t1) {
                             const bool see = a.mask ? (a.mask[(int64_t)(w.l.n0 + t1) * a.mask_words + (n >> 5)] >> (n & 31)) & 1
                                                     : n <= t1;
                             if (!see) continue;
                             int lo = t1 * G - row0, hi = lo + G;
                             lo = lo < 0 ? 0 : lo;
-                            hi = hi > R ? R : hi;
-                            sees |= (hi == 64 ? ~0ull : (1ull << hi) - 1ull) & ~((1ull << lo) - 1ull);
+                            hi = hi > RH ? RH : hi;
+                            sees |= (hi == 32 ? ~0u : (1u << hi) - 1u) & ~((1u << lo) - 1u);
                         }
                     }
                 }
@@ -480,102 +533,120 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
                 // Value scales more than 2^104 apart: p could underflow in a row that matters to the sum of
                 // weights, p 2^-ev; its weight then gets an exponential of its own.
                 const bool wide = ev_most > __reduce_min_sync(0xFFFFFFFFu, min(least & 255u, (least >> 8) & 255u)) + 104u;
-                const float cj = a.scale_log2 * e8m0_to_float(ks);
                 const int evi = vs == 255u ? 0 : (int)vs - 127;
                 const float ev = vs == 255u ? __uint_as_float(0x7FC00000u) : (float)evi;
-                const f32x2 cj2 = pack2(cj, cj), ev2 = pack2(ev, ev);
-                if (!warp_wait(&sfull[g], k & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                const f32x2 ev2 = pack2(ev, ev);
+                const uint32_t sb = i % C::SB;
+                if (!warp_wait(&sfull[sb], (i / C::SB) & 1, abort_flag, a.wait_ns)) { ok = false; break; }
                 tc_fence_after();
-                // y = s' (+ off: the exponent of p); rows not seen are -inf
-                f32x2 y[R / 2];
-                auto scores = [&](bool with_off) {
+                const uint32_t srow = trow + sb * R;
+                const float2 unit = *reinterpret_cast<const float2*>(F + C::F_QU + (piece & 3) * 2);
+                const bool rowwise = unit.y != 0.0f;
+                const float cj = a.scale_log2 * e8m0_to_float(ks) * unit.x;
+                const f32x2 cj2 = pack2(cj, cj);
+                // One pass over the tile, a second one where a score has passed the limit
+                f32x2 y[RH / 2];                     // s' + off, the exponent of p, then p; rows not seen are -inf
+                bool setting = set;
+                for (;;) {
+                    {
+                        uint32_t s[RH];
+                        tc_load(srow, s);
 #pragma unroll
-                    for (int c0 = 0; c0 < R; c0 += 8) {
-                        uint32_t hi[8], lo[8];
-                        tc_ld_x8(trow + c0, hi);
-                        tc_ld_x8(trow + R + c0, lo);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const f32x2 f = *reinterpret_cast<const f32x2*>(qf + c0 + 2 * q);
-                            const f32x2 o = *reinterpret_cast<const f32x2*>(off + c0 + 2 * q);
-                            const f32x2 s = add2(pack2(__uint_as_float(hi[2 * q]), __uint_as_float(hi[2 * q + 1])),
-                                                 pack2(__uint_as_float(lo[2 * q]), __uint_as_float(lo[2 * q + 1])));
-                            y[c0 / 2 + q] = fma2(mul2(s, f), cj2, with_off ? add2(ev2, o) : ev2);
-                        }
+                        for (int q = 0; q < RH / 2; ++q) y[q] = pack2(__uint_as_float(s[2 * q]), __uint_as_float(s[2 * q + 1]));
                     }
+                    if (rowwise) {
+#pragma unroll
+                        for (int q = 0; q < RH / 2; ++q) y[q] = mul2(y[q], *reinterpret_cast<const f32x2*>(qf + 2 * q));
+                    }
+#pragma unroll
+                    for (int q = 0; q < RH / 2; ++q) y[q] = fma2(y[q], cj2, ev2);
                     if (masked) {
 #pragma unroll
-                        for (int q = 0; q < R / 2; ++q) {
+                        for (int q = 0; q < RH / 2; ++q) {
                             const float2 s = unpack2(y[q]);
                             y[q] = pack2((sees >> (2 * q)) & 1 ? s.x : -INFINITY, (sees >> (2 * q + 1)) & 1 ? s.y : -INFINITY);
                         }
                     }
-                };
-                auto set_reference = [&]() -> bool {
-                    // the tile's maximum of s' in every tree row, over the group's 128 threads
-                    float mine[RL];
+                    if (setting) {
+                        // The tile's maximum of s' in every tree row, over the warpgroup's 128 threads. Rows are halved while
+                        // lanes are paired: lane l ends with row l (of 16: l / 2). Shuffles, not redux.sync: its
+                        // results come one by one through the uniform registers (100 clocks each).
+                        float* wmax = F + C::F_WMAX + (wg * 2 + (sets & 1)) * 4 * RH;
+                        constexpr int HALF = RH / 2;
+                        float v[HALF];
 #pragma unroll
-                    for (int r = 0; r < RL; ++r) mine[r] = -INFINITY;
+                        for (int r = 0; r < HALF; r += 2) {
+                            const float2 x0 = unpack2(y[r / 2]), x1 = unpack2(y[(r + HALF) / 2]);
+                            const bool up = lane & 16;
+                            v[r] = fmaxf(up ? x1.x : x0.x, __shfl_xor_sync(0xFFFFFFFFu, up ? x0.x : x1.x, 16));
+                            v[r + 1] = fmaxf(up ? x1.y : x0.y, __shfl_xor_sync(0xFFFFFFFFu, up ? x0.y : x1.y, 16));
+                        }
+                        int n = HALF;
 #pragma unroll
-                    for (int q = 0; q < R / 2; ++q) {
-                        const float2 s = unpack2(y[q]);
-                        const float m0 = warp_max(s.x), m1 = warp_max(s.y);
-                        if (lane == ((2 * q) & 31)) mine[q / 16] = m0;
-                        if (lane == ((2 * q + 1) & 31)) mine[q / 16] = m1;
+                        for (int o = 8; o > 0; o >>= 1) {
+                            n /= 2;
+                            const bool up = lane & o;
+#pragma unroll
+                            for (int r = 0; r < HALF / 2; ++r) {
+                                if (r >= n) break;
+                                v[r] = fmaxf(up ? v[r + n] : v[r], __shfl_xor_sync(0xFFFFFFFFu, up ? v[r] : v[r + n], o));
+                            }
+                            if (n == 0) v[0] = fmaxf(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], o));
+                        }
+                        wmax[wl * RH + (RH < 32 ? lane >> 1 : lane)] = v[0];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&maxima[wg]);
+                        if (!warp_wait(&maxima[wg], sets & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                        ++sets;
+                        if (RH == 32 || lane < RH) { // every warp writes the same factors
+                            const float m = fmaxf(fmaxf(wmax[lane], wmax[RH + lane]), fmaxf(wmax[2 * RH + lane], wmax[3 * RH + lane]));
+                            const float Mn = fmaxf(M, m);
+                            // a row that has seen nothing: the first score it sees passes any limit
+                            off[lane] = Mn == -INFINITY ? 1e30f : P_EXP - Mn;
+                            alpha[lane] = M == -INFINITY ? 0.0f : ex2(M - Mn);
+                            M = Mn;
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int q = 0; q < RH / 2; ++q) l2[q] = mul2(l2[q], *reinterpret_cast<const f32x2*>(alpha + 2 * q));
                     }
-#pragma unroll
-                    for (int r = 0; r < RL; ++r)
-                        if (R >= 32 || lane < R) wmax[wl * R + r * 32 + lane] = mine[r];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&maxima[g]);
-                    if (!warp_wait(&maxima[g], sets & 1, abort_flag, a.wait_ns)) return false;
-                    ++sets;
-                    // every warp writes the same factors
-#pragma unroll
-                    for (int r = 0; r < RL; ++r) {
-                        if (R < 32 && lane >= R) break;
-                        const int row = r * 32 + lane;
-                        const float m = fmaxf(fmaxf(wmax[row], wmax[R + row]), fmaxf(wmax[2 * R + row], wmax[3 * R + row]));
-                        const float Mn = fmaxf(M[r], m);
-                        // a row that has seen nothing: the first score it sees passes any limit
-                        off[row] = Mn == -INFINITY ? 1e30f : P_EXP - Mn;
-                        alpha[row] = M[r] == -INFINITY ? 0.0f : ex2(M[r] - Mn);
-                        M[r] = Mn;
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int q = 0; q < R / 2; ++q) {
-                        y[q] = add2(y[q], *reinterpret_cast<const f32x2*>(off + 2 * q));
-                        l2[q] = mul2(l2[q], *reinterpret_cast<const f32x2*>(alpha + 2 * q));
-                    }
-                    return true;
-                };
-                const bool first = set;
-                scores(!first);
-                if (first) {
-                    if (!set_reference()) { ok = false; break; }
-                    set = false;
-                } else {
                     float top = -INFINITY;
 #pragma unroll
-                    for (int q = 0; q < R / 2; ++q) {
-                        const float2 s = unpack2(y[q]);
-                        top = fmaxf(top, fmaxf(s.x, s.y));
+                    for (int q = 0; q < RH / 2; q += 2) {
+                        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(off + 2 * q);
+                        y[q] = add2(y[q], o.x);
+                        y[q + 1] = add2(y[q + 1], o.y);
+                        const float2 s0 = unpack2(y[q]), s1 = unpack2(y[q + 1]);
+                        top = fmaxf(top, fmaxf(fmaxf(s0.x, s0.y), fmaxf(s1.x, s1.y)));
                     }
-                    const bool over = __any_sync(0xFFFFFFFFu, top > P_EXP_MAX);
-                    if (lane == 0) {
-                        votes[g * 4 + wl] = over;
-                        mbar_arrive(&vote[g]);
+                    if (!setting) {
+                        const bool over = __any_sync(0xFFFFFFFFu, top > P_EXP_MAX);
+                        if (lane == 0) {
+                            votes[wg * 8 + (polls & 1) * 4 + wl] = over;
+                            mbar_arrive(&vote[wg]);
+                        }
                     }
-                }
-                // P of this group's previous tile has been read, and its O added up
-                if (k > 0 && !warp_wait(&pfree[g], (k - 1) & 1, abort_flag, a.wait_ns)) { ok = false; break; }
-                uint8_t* P = smem + C::OFF_P + g * C::PBUF + j * R;
-                auto write_p = [&]() {
+                    // P of this group's previous tile has been read, and its O added up
+                    if (k > 0 && !warp_wait(&pfree[g], (k - 1) & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                    if (setting && !set) {           // what has been added up is scaled down to the new reference
+                        tc_fence_after();
+                        const uint32_t orow = tmem + ((uint32_t)(wl * 32) << 16) + C::TMEM_O + (g * 2 + (piece & 1)) * C::MB * R + h * RH;
+                        for (int c0 = 0; c0 < C::MB * RH; c0 += 8) {
+                            const uint32_t at = orow + (c0 / RH) * R + c0 % RH;
+                            uint32_t o[8];
+                            tc_ld_x8(at, o);
+                            tc_wait_ld();
+                            const float* al = alpha + c0 % RH;
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * al[q]);
+                            tc_st_x8(at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
+                        }
+                        tc_wait_st();
+                    }
+                    uint8_t* P = smem + C::OFF_P + g * C::PBUF + j * R;
                     const int swz = R == 64 ? (j >> 1) & 3 : R == 32 ? (j >> 2) & 1 : 0;
 #pragma unroll
-                    for (int c0 = 0; c0 < R; c0 += 16) {
+                    for (int c0 = 0; c0 < RH; c0 += 16) {
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -583,9 +654,10 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
                             __nv_fp8x2_storage_t l8[2];
 #pragma unroll
                             for (int z = 0; z < 2; ++z) {
-                                const float2 s = unpack2(y[c0 / 2 + 2 * q + z]);
+                                f32x2& e = y[c0 / 2 + 2 * q + z];
+                                const float2 s = unpack2(e);
                                 const float p0 = ex2(s.x), p1 = ex2(s.y);
-                                if (!wide) y[c0 / 2 + 2 * q + z] = pack2(p0, p1);
+                                if (!wide) e = pack2(p0, p1);
                                 const __half2 ph = __floats2half2_rn(p0, p1);
                                 // p rounded to the upper byte of its fp16 pattern (p <= 2900: no carry out of it; NaN
                                 // stays in the rest), and the exact rest
@@ -596,47 +668,20 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
                             hi[q] = __byte_perm(up[0], up[1], 0x7531);
                             lo[q] = (uint32_t)l8[0] | ((uint32_t)l8[1] << 16);
                         }
-                        uint8_t* at = P + (((c0 / 16) ^ swz) << 4);
+                        uint8_t* at = P + (((h * (RH / 16) + c0 / 16) ^ swz) << 4);
                         *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *reinterpret_cast<uint4*>(at + TILE * R) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                };
-                write_p();
-                if (!first) {
-                    if (!warp_wait(&vote[g], polls & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                    if (setting) break;
+                    if (!warp_wait(&vote[wg], polls & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                    const volatile int* got = votes + wg * 8 + (polls & 1) * 4;
                     ++polls;
-                    if (votes[g * 4] | votes[g * 4 + 1] | votes[g * 4 + 2] | votes[g * 4 + 3]) {
-                        // a score has passed the limit: the reference is set again, and O scaled down to it
-                        scores(false);
-                        if (!set_reference()) { ok = false; break; }
-                        tc_fence_after();
-                        const uint32_t orow = tmem + ((uint32_t)(wl * 32) << 16) + C::TMEM_O + (g * 2 + (piece & 1)) * C::MB * R;
-                        for (int c0 = 0; c0 < C::MB * R; c0 += 8) {
-                            uint32_t o[8];
-                            tc_ld_x8(orow + c0, o);
-                            tc_wait_ld();
-                            const float* al = alpha + c0 % R;
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * al[q]);
-                            tc_st_x8(orow + c0, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
-                        }
-                        tc_wait_st();
-                        write_p();
-                    }
+                    if (!(got[0] | got[1] | got[2] | got[3])) break;
+                    setting = true;
                 }
-                if (wide) {
-#pragma unroll
-                    for (int q = 0; q < R / 2; ++q) {
-                        const float2 s = unpack2(y[q]);
-                        l2[q] = add2(l2[q], pack2(ex2(s.x - (float)evi), ex2(s.y - (float)evi)));
-                    }
-                } else {
-                    const float wj = exp2_int(-evi);
-                    const f32x2 wj2 = pack2(wj, wj);
-#pragma unroll
-                    for (int q = 0; q < R / 2; ++q) l2[q] = fma2(y[q], wj2, l2[q]);
-                }
-                if (valid < TILE && (!PAIR || g == 0)) {
+                if (!ok) break;
+                set = false;
+                if (valid < TILE && h == 0) {
                     // rows past the lane's end hold anything: their values are cleared, so that 0 * NaN does not arise
                     const uint32_t f = 2 * i + 1;
                     if (!warp_wait(&full[f % NS], (f / NS) & 1, abort_flag, a.wait_ns)) { ok = false; break; }
@@ -652,111 +697,163 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&pfull[g]);
+                if (wide) {
+#pragma unroll
+                    for (int q = 0; q < RH / 2; ++q) {
+                        const float2 s = unpack2(y[q]);
+                        l2[q] = add2(l2[q], pack2(ex2(s.x - (float)evi), ex2(s.y - (float)evi)));
+                    }
+                } else {
+                    const float wj = exp2_int(-evi);
+                    const f32x2 wj2 = pack2(wj, wj);
+#pragma unroll
+                    for (int q = 0; q < RH / 2; ++q) l2[q] = fma2(y[q], wj2, l2[q]);
+                }
                 ++k;
             }
             if (!ok) break;
             // the part's sums over this group's rows
             if (piece > 0 && !warp_wait(lfree, (piece - 1) & 1, abort_flag, a.wait_ns)) break;
-            float v[R];
+            float v[RH];
 #pragma unroll
-            for (int r = 0; r < R / 2; ++r) {
+            for (int r = 0; r < RH / 2; ++r) {
                 const float2 p = unpack2(l2[r]);
                 v[2 * r] = p.x;
                 v[2 * r + 1] = p.y;
             }
-            // halve the rows while the lanes are paired: a lane ends with the sums of its R / 32 rows
-            int n = R;
+            int n = RH;                              // as for the maxima
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
-                if (n > 1) {
-                    n /= 2;
+                n /= 2;
+                const bool up = lane & o;
 #pragma unroll
-                    for (int r = 0; r < R / 2; ++r) {
-                        if (r >= n) break;
-                        const bool up = lane & o;
-                        const float keep = up ? v[r + n] : v[r], send = up ? v[r] : v[r + n];
-                        v[r] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
-                    }
-                } else {
-                    v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+                for (int r = 0; r < RH / 2; ++r) {
+                    if (r >= n) break;
+                    v[r] = (up ? v[r + n] : v[r]) + __shfl_xor_sync(0xFFFFFFFFu, up ? v[r] : v[r + n], o);
                 }
+                if (n == 0) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
             }
-            float* ls = F + C::F_L + (g * 4 + wl) * R;
-            if (R == 64) { ls[2 * lane] = v[0]; ls[2 * lane + 1] = v[R > 32 ? 1 : 0]; }
-            else if (R == 32) ls[lane] = v[0];
-            else if ((lane & 1) == 0) ls[lane >> 1] = v[0];
-            if (wl == 0)
-#pragma unroll
-                for (int r = 0; r < RL; ++r)
-                    if (R >= 32 || lane < R) F[C::F_M + g * R + r * 32 + lane] = M[r];
+            F[C::F_L + (g * 4 + wl) * R + h * RH + (RH < 32 ? lane >> 1 : lane)] = v[0];
+            if (wl == 0 && (RH == 32 || lane < RH)) F[C::F_M + g * R + h * RH + lane] = M;
             __syncwarp();
             if (lane == 0) mbar_arrive(lfull);
             left -= nt;
             w.advance(a, facts, nt, left > 0);
             ++piece;
         }
-    } else if (warp < 12) {
+    } else if (warp < SW + 4) {
         // ------------------------------------------------------------ queries and outputs
-        if constexpr (R == 64) regs_down<80>();
+        if constexpr (R == 64) regs_down<56>();
         const int wl = warp & 3;
         // the queries of the next unit; all loads of a batch are under way before the first is used
-        Walk<RU> wq = w;
+        Walk<R> wq = w;
         int64_t qleft = left;
         uint32_t qpiece = 0;
+        const int row_step = 4 * (32 / (D / 8));     // tree rows the four warps take at once
         auto convert = [&]() -> bool {
             constexpr int LPR = D / 8, RPW = 32 / LPR;                // lanes a row, rows a warp takes at once
-            constexpr int ITER = RU / (4 * RPW) > 0 ? RU / (4 * RPW) : 1, BATCH = ITER < 8 ? ITER : 8;
+            constexpr int ITER = R / (4 * RPW) > 0 ? R / (4 * RPW) : 1;
             const int part = lane % LPR, sub = lane / LPR;
-            const uint32_t qb = qpiece % C::QBUFS;
-            const int rows = wq.rows(a), row0 = wq.rt * RU;
+            const uint32_t qb = qpiece & 1;
+            const int rows = wq.rows(a), row0 = wq.rt * R;
             uint8_t* Q = smem + C::OFF_Q + qb * C::QBUF;
-            float* qf = F + C::F_QF + (qpiece & 3) * RU;
-            for (int i0 = 0; i0 < ITER; i0 += BATCH) {
-                uint4 raw[BATCH];
+            float* qf = F + C::F_QF + (qpiece & 3) * R;
+            // up to eight rows a lane at a time, all loads under way before the first is used; more are read twice
+            constexpr int BATCH = ITER < 8 ? ITER : 8;
+            const int first = row0 + wl * RPW + sub, node0 = first / G, head0 = first - node0 * G;
+            int node = node0, head = head0;
+            uint4 raw[BATCH];
+            auto fetch = [&](int b0) {
 #pragma unroll
                 for (int b = 0; b < BATCH; ++b) {
-                    const int u = ((i0 + b) * 4 + wl) * RPW + sub;
                     raw[b] = make_uint4(0u, 0u, 0u, 0u);
-                    if (u < rows) {
-                        const int node = (row0 + u) / G, qh = wq.h * G + (row0 + u) - node * G;
-                        raw[b] = *reinterpret_cast<const uint4*>(a.q + (wq.l.n0 + node) * a.q_token_stride + qh * a.q_head_stride + part * 8);
-                    }
+                    if (((b0 + b) * 4 + wl) * RPW + sub < rows)
+                        raw[b] = *reinterpret_cast<const uint4*>(a.q + (wq.l.n0 + node) * a.q_token_stride + (wq.h * G + head) * a.q_head_stride + part * 8);
+                    node += row_step / G;
+                    head += row_step % G;
+                    if (head >= G) { head -= G; ++node; }
                 }
-                if (i0 == 0 && !warp_wait(&qfree[qb], ((qpiece / C::QBUFS) & 1) ^ 1, abort_flag, a.wait_ns)) return false;
+            };
+            // max |x| of each row (bf16 bits; NaN stays), and of the unit's rows the largest and the smallest but zero
+            uint32_t* keys = reinterpret_cast<uint32_t*>(qf);
+            uint32_t most = 0, least = 0x7FFFu;
+#pragma unroll
+            for (int b0 = 0; b0 < ITER; b0 += BATCH) {
+                fetch(b0);
 #pragma unroll
                 for (int b = 0; b < BATCH; ++b) {
-                    const int u = ((i0 + b) * 4 + wl) * RPW + sub;
-                    const uint32_t in[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
-                    uint32_t key = 0;                                 // max |x|: bit patterns order as integers
+                    auto abs2 = [](uint32_t v) {
+                        v &= 0x7FFF7FFFu;
+                        return *reinterpret_cast<const __nv_bfloat162*>(&v);
+                    };
+                    __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(abs2(raw[b].x), abs2(raw[b].y)), __hmax2_nan(abs2(raw[b].z), abs2(raw[b].w)));
+                    m = __hmax2_nan(m, __lowhigh2highlow(m));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) key = max(key, max((in[e] << 16) & 0x7FFFFFFFu, in[e] & 0x7FFF0000u));
+                    for (int o = LPR / 2; o > 0; o >>= 1) m = __hmax2_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                    const uint32_t key = *reinterpret_cast<const uint32_t*>(&m) & 0xFFFFu;
+                    const int u = ((b0 + b) * 4 + wl) * RPW + sub;
+                    if (part == 0 && u < R) keys[u] = key;
+                    most = max(most, key);
+                    if (key) least = min(least, key);
+                }
+            }
+            uint32_t* qx = reinterpret_cast<uint32_t*>(F + C::F_QX);
+            most = __reduce_max_sync(0xFFFFFFFFu, most);
+            least = __reduce_min_sync(0xFFFFFFFFu, least);
+            if (lane == 0) {
+                qx[(qpiece & 1) * 4 + wl] = most;
+                qx[8 + (qpiece & 1) * 4 + wl] = least;
+                mbar_arrive(qmax);
+            }
+            if (!warp_wait(qmax, qpiece & 1, abort_flag, a.wait_ns)) return false;
 #pragma unroll
-                    for (int o = LPR / 2; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, o));
-                    int up = key ? 7 - floor_log2_pos(__uint_as_float(key)) : 0;
-                    up = up > 120 ? 120 : (up < -120 ? -120 : up);
+            for (int q = 0; q < 4; ++q) {
+                most = max(most, qx[(qpiece & 1) * 4 + q]);
+                least = min(least, qx[8 + (qpiece & 1) * 4 + q]);
+            }
+            // Rows within 2^4 of one another share one power of two, and the scores need no factor of their row's;
+            // the smallest rows' low parts then end 2^-13 below their own maximum. (Subnormal rows count as 2^-126.)
+            auto up_of = [](uint32_t k) {            // 2^up * maximum is in [128, 256)
+                const int up = k ? 134 - (int)(k >> 7) : 0;
+                return up > 120 ? 120 : (up < -120 ? -120 : up);
+            };
+            const int unit_up = up_of(most);
+            const bool rowwise = most >= 0x7F80u || (least < most && up_of(least) - unit_up > 4);
+            if (!warp_wait(&qfree[qb], ((qpiece >> 1) & 1) ^ 1, abort_flag, a.wait_ns)) return false;
+            if (wl == 0 && lane == 0)
+                *reinterpret_cast<float2*>(F + C::F_QU + (qpiece & 3) * 2) = make_float2(rowwise ? 1.0f : exp2_int(-unit_up), rowwise ? 1.0f : 0.0f);
+            const int byte = part * 8, panel = byte / C::ROWB, in_row = byte % C::ROWB;
+            node = node0;
+            head = head0;
+#pragma unroll
+            for (int b0 = 0; b0 < ITER; b0 += BATCH) {
+                if (ITER > BATCH) fetch(b0);
+#pragma unroll
+                for (int b = 0; b < BATCH; ++b) {
+                    const int u = ((b0 + b) * 4 + wl) * RPW + sub;
+                    const uint32_t key = rowwise && u < R ? keys[u] : 0u;
+                    __syncwarp();
+                    const int up = rowwise ? up_of(key) : unit_up;
                     const float gain = exp2_int(up);
-                    uint32_t hi[2], lo[2];
+                    const f32x2 gain2 = pack2(gain, gain);
+                    const uint32_t in[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+                    uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float x0 = __uint_as_float(in[e] << 16) * gain, x1 = __uint_as_float(in[e] & 0xFFFF0000u) * gain;
-                        const __nv_fp8x2_storage_t h8 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-                        const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h8, __NV_E4M3)));
-                        const __nv_fp8x2_storage_t l8 =
-                            __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y), __NV_SATFINITE, __NV_E4M3);
-                        if (e & 1) { hi[e / 2] |= (uint32_t)h8 << 16; lo[e / 2] |= (uint32_t)l8 << 16; }
-                        else { hi[e / 2] = h8; lo[e / 2] = l8; }
+                        // a scaled bf16 value is exact in fp16 (down to 2^-16, far below what lo resolves)
+                        const float2 x = unpack2(mul2(pack2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xFFFF0000u)), gain2));
+                        const __half2 xh = __floats2half2_rn(x.x, x.y);
+                        hi[e] = __nv_cvt_halfraw2_to_fp8x2(xh, __NV_SATFINITE, __NV_E4M3);
+                        const __half2 rest = __hsub2(xh, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3)));
+                        lo[e] = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
                     }
-                    if (u < RU) {
+                    if (u < R) {
                         // a row that is not finite: its scores become NaN
-                        if (part == 0) qf[u] = key >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : exp2_int(-up);
-                        const int byte = part * 8, panel = byte / C::ROWB, in_row = byte % C::ROWB;
-                        auto place = [&](int row) {
-                            const int swz = C::ROWB == 128 ? row & 7 : (row >> 1) & 3;
-                            return Q + panel * C::QROWS * C::ROWB + row * C::ROWB + (((in_row >> 4) ^ swz) << 4) + (in_row & 15);
-                        };
-                        const int row = (u / R) * 2 * R + u % R;
-                        *reinterpret_cast<uint2*>(place(row)) = make_uint2(hi[0], hi[1]);
-                        *reinterpret_cast<uint2*>(place(row + R)) = make_uint2(lo[0], lo[1]);
+                        if (rowwise && part == 0) qf[u] = key >= 0x7F80u ? __uint_as_float(0x7FC00000u) : exp2_int(-up);
+                        const int swz = C::ROWB == 128 ? u & 7 : (u >> 1) & 3;     // the same for row R + u
+                        uint8_t* at = Q + panel * C::QROWS * C::ROWB + u * C::ROWB + (((in_row >> 4) ^ swz) << 4) + (in_row & 15);
+                        *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(hi[0], hi[1], 0x5410), __byte_perm(hi[2], hi[3], 0x5410));
+                        *reinterpret_cast<uint2*>(at + R * C::ROWB) = make_uint2(__byte_perm(lo[0], lo[1], 0x5410), __byte_perm(lo[2], lo[3], 0x5410));
                     }
                 }
             }
@@ -770,8 +867,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
             return true;
         };
 
-        constexpr int RL = RU > 32 ? RU / 32 : 1;    // tree rows a lane looks after
-        float* st = F + C::F_ST + wl * 2 * RU;
+        constexpr int RL = R > 32 ? R / 32 : 1;    // tree rows a lane looks after
+        float* st = F + C::F_ST + wl * 2 * R;
         const bool on = D >= 128 || lane < 16;       // M = 64 leaves 16 rows in each quarter of the lanes
         const int d0 = D >= 128 ? wl * 32 + lane : wl * 16 + (lane & 15);
         uint32_t i0 = 0, piece = 0;                  // the part's first tile
@@ -782,31 +879,25 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
             const uint32_t ob = piece & 1;
             if (!warp_wait(lfull, piece & 1, abort_flag, a.wait_ns) || !warp_wait(&ofull[ob], (piece >> 1) & 1, abort_flag, a.wait_ns)) break;
             tc_fence_after();
-            const int rows = w.rows(a), row0 = w.rt * RU;
+            const int rows = w.rows(a), row0 = w.rt * R;
             const bool whole = nt == w.tiles;
             // a group without a tile in this part has no O
-            const bool has0 = PAIR || nt > 1 || (i0 & 1) == 0, has1 = !PAIR && (nt > 1 || (i0 & 1) == 1);
+            const bool has0 = nt > 1 || (i0 & 1) == 0, has1 = nt > 1 || (i0 & 1) == 1;
             float* part = reinterpret_cast<float*>(a.ws + parts_offset(gridDim.x)) +
-                          (size_t)(2 * blockIdx.x + (left == count ? 0 : 1)) * part_floats(RU, D);
+                          (size_t)(2 * blockIdx.x + (left == count ? 0 : 1)) * part_floats(R, D);
 #pragma unroll
             for (int r = 0; r < RL; ++r) {
                 const int u = r * 32 + lane;
                 if (u >= rows) break;
-                const int g0 = PAIR ? u / R : 0, row = PAIR ? u % R : u;
                 auto sum = [&](int g) {
-                    const float* ls = F + C::F_L + g * 4 * R + row;
+                    const float* ls = F + C::F_L + g * 4 * R + u;
                     return (ls[0] + ls[R]) + (ls[2 * R] + ls[3 * R]);
                 };
-                float M = F[C::F_M + g0 * R + row], L = sum(g0), f0 = 1.0f, f1 = 0.0f;
-                if (!PAIR) {
-                    const float M0 = M, M1 = F[C::F_M + R + row];
-                    M = fmaxf(M0, M1);
-                    f0 = M0 == -INFINITY ? 0.0f : ex2(M0 - M);
-                    f1 = M1 == -INFINITY ? 0.0f : ex2(M1 - M);
-                    L = L * f0 + sum(1) * f1;                         // sums may be NaN
-                }
+                const float M0 = F[C::F_M + u], M1 = F[C::F_M + R + u], M = fmaxf(M0, M1);
+                float f0 = M0 == -INFINITY ? 0.0f : ex2(M0 - M), f1 = M1 == -INFINITY ? 0.0f : ex2(M1 - M);
+                const float L = sum(0) * f0 + sum(1) * f1;            // sums may be NaN
                 if (whole) {
-                    // out = O / L; lse = ln 2 (M - 8 + log2 L): p carries 2^8
+                    // out = O / L; lse = ln 2 (M - 6 + log2 L): p carries 2^6
                     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
                     f0 *= inv;
                     f1 *= inv;
@@ -816,11 +907,11 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
                             L == 0.0f ? -INFINITY : (M - P_EXP + log2f(L)) * 0.69314718055994531f;
                     }
                 } else if (wl == 0) {
-                    part[RU * D + u] = M;
-                    part[RU * D + RU + u] = L;
+                    part[R * D + u] = M;
+                    part[R * D + R + u] = L;
                 }
                 st[u] = f0;
-                st[RU + u] = f1;
+                st[R + u] = f1;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(lfree);
@@ -831,15 +922,14 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
                 float x[C::MB][8];
 #pragma unroll
                 for (int m = 0; m < C::MB; ++m) {
-                    const int c = PAIR ? c0 % R : c0, g0 = PAIR ? c0 / R : 0;
                     uint32_t o0[8], o1[8];
-                    if (has0) tc_ld_x8(orow + ((g0 * 2 + ob) * C::MB + m) * R + c, o0);
-                    if (has1) tc_ld_x8(orow + ((2 + ob) * C::MB + m) * R + c, o1);
+                    if (has0) tc_ld_x8(orow + (ob * C::MB + m) * R + c0, o0);
+                    if (has1) tc_ld_x8(orow + ((2 + ob) * C::MB + m) * R + c0, o1);
                     tc_wait_ld();
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         x[m][q] = has0 ? __uint_as_float(o0[q]) * st[c0 + q] : 0.0f;
-                        if (has1) x[m][q] = fmaf(__uint_as_float(o1[q]), st[RU + c0 + q], x[m][q]);
+                        if (has1) x[m][q] = fmaf(__uint_as_float(o1[q]), st[R + c0 + q], x[m][q]);
                     }
                 }
 #pragma unroll
@@ -864,10 +954,10 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
             ++piece;
         }
     } else {
-        if constexpr (R == 64) regs_down<64>();
+        if constexpr (R == 64) regs_down<40>();
         const int P = 1 << a.page_shift;
         // the cache row of this unit's head at lane row `at` (its page's first one is at / P * P), -1 past the end
-        auto row_of = [&](const Walk<RU>& x, int64_t at, bool tell) -> int {
+        auto row_of = [&](const Walk<R>& x, int64_t at, bool tell) -> int {
             if (at >= x.l.len) return -1;
             int p = a.table[(int64_t)x.b * a.width + (at >> a.page_shift)];
             if (p < 0 || p >= a.c.n_pages) {
@@ -876,7 +966,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
             }
             return (p * H + x.h) * P + (int)(at & (P - 1));
         };
-        if (warp == 12) {
+        if (warp == SW + 4) {
             // -------------------------------------------------------- TMA: lane l copies the tile's l-th page (or 128 rows of it)
             const int rows_a_page = P < TILE ? P : TILE;
             auto place = [&]() { return lane * rows_a_page < TILE ? row_of(w, (int64_t)w.t * TILE + lane * rows_a_page, true) : -1; };
@@ -904,111 +994,113 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
                                         v ? &maps.v : &maps.k, &full[s], p * 128, row);
                 }
             }
-        } else if (warp == 13) {
+        } else if (warp == SW + 5) {
             // -------------------------------------------------------- MMA issue. The loop is uniform over the warp and one elected
             // lane issues, so that descriptors stay in uniform registers (39 clocks an MMA of N = 16 against 120
             // from a loop that one lane runs).
             constexpr uint64_t KD = desc_base(C::ROWB == 128 ? 2 : 4, 8 * C::ROWB);       // K, Q (along K) and V (along M): one atom, 8 rows
             constexpr uint64_t PD = desc_base(R == 64 ? 4 : R == 32 ? 6 : 0, 8 * R);
-            constexpr uint32_t ID_S = idesc_f8(128, 2 * R, 0, 0, 0);
+            constexpr uint32_t ID_S = idesc_f8(128, R, 0, 0, 0);
             constexpr uint32_t ID_HI = idesc_f8(D < 128 ? 64 : 128, R, 1, 1, 1), ID_LO = idesc_f8(D < 128 ? 64 : 128, R, 1, 1, 0);
             const uint32_t base = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             const uint64_t ring = desc_at(KD, smem_u32(smem + C::OFF_RING));
             const uint64_t qd = desc_at(KD, smem_u32(smem + C::OFF_Q)), pd = desc_at(PD, smem_u32(smem + C::OFF_P));
-            uint32_t i = 0, piece = 0;
-            // the tile before: its part, its place in it, whether it ends it
-            uint32_t pp = 0, pt = 0, plast = 0;
-            bool ok = true;
-            auto qk = [&](uint32_t s, uint32_t qb, uint32_t g, bool done, bool last) {
-                const uint64_t kd = ring + (uint64_t)(s * (C::SLOT >> 4)), q = qd + (uint64_t)(qb * (C::QBUF >> 4) + (PAIR ? g * (2 * R * C::ROWB >> 4) : 0));
+            // S of tile i = K (Q hi)^T + K (Q lo)^T; `last` of its part
+            auto qk = [&](uint32_t i, uint32_t qb, bool last) {
+                const uint32_t s = (2 * i) % NS;
+                const uint64_t kd = ring + (uint64_t)(s * (C::SLOT >> 4)), q = qd + (uint64_t)(qb * (C::QBUF >> 4));
+                const uint32_t d = base + (i % C::SB) * R;
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 32; ++kk) {
-                        constexpr int STEPS = C::ROWB / 32;
-                        tc_mma_f8(base + g * 2 * R, kd + (((kk / STEPS) * C::PANEL + (kk % STEPS) * 32) >> 4),
-                                  q + (((kk / STEPS) * C::QROWS * C::ROWB + (kk % STEPS) * 32) >> 4), ID_S, kk ? 1u : 0u);
+                    for (int kk = 0; kk < 2 * D / 32; ++kk) {
+                        constexpr int STEPS = C::ROWB / 32, HALF = D / 32;
+                        const int k = kk % HALF;
+                        tc_mma_f8(d, kd + (((k / STEPS) * C::PANEL + (k % STEPS) * 32) >> 4),
+                                  q + (((k / STEPS) * C::QROWS * C::ROWB + (kk / HALF) * R * C::ROWB + (k % STEPS) * 32) >> 4), ID_S,
+                                  kk ? 1u : 0u);
                     }
-                    if (done) tc_commit(&empty[s]);
-                    tc_commit(&sfull[g]);
-                    if (done && last) tc_commit(&qfree[qb]);
+                    tc_commit(&empty[s]);
+                    tc_commit(&sfull[i % C::SB]);
+                    if (last) tc_commit(&qfree[qb]);
                 }
                 __syncwarp();
             };
-            auto pv = [&](uint32_t n, uint32_t g, bool done, bool ends) {                  // adds tile n to group g's O
-                const uint32_t s = (2 * n + 1) % NS;
+            // O of the tile's group += tile n; fresh: the group's first of the part, ends: the part's last
+            auto pv = [&](uint32_t n, uint32_t part, bool fresh, bool ends) {
+                const uint32_t g = n & 1, s = (2 * n + 1) % NS;
                 const uint64_t vd = ring + (uint64_t)(s * (C::SLOT >> 4)), p = pd + (uint64_t)(g * (C::PBUF >> 4));
-                const uint32_t fresh = PAIR ? pt == 0 : pt < 2;
-                const uint32_t o = base + C::TMEM_O + (g * 2 + (pp & 1)) * C::MB * R;
+                const uint32_t o = base + C::TMEM_O + (g * 2 + (part & 1)) * C::MB * R;
+                const uint32_t add = fresh ? 0u : 1u;
                 if (elect_one()) {
 #pragma unroll
                     for (int m = 0; m < C::MB; ++m)
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)                 // four steps of 32 rows with hi, four with lo
                             tc_mma_f8(o + m * R, vd + ((m * C::PANEL + (kk & 3) * 32 * C::ROWB) >> 4),
-                                      p + (((kk >> 2) * TILE * R + (kk & 3) * 32 * R) >> 4), kk < 4 ? ID_HI : ID_LO, kk ? 1u : fresh ^ 1u);
-                    if (done) tc_commit(&empty[s]);
+                                      p + (((kk >> 2) * TILE * R + (kk & 3) * 32 * R) >> 4), kk < 4 ? ID_HI : ID_LO, kk ? 1u : add);
+                    tc_commit(&empty[s]);
                     tc_commit(&pfree[g]);
-                    if (ends) tc_commit(&ofull[pp & 1]);
+                    if (ends) tc_commit(&ofull[part & 1]);
                 }
                 __syncwarp();
             };
-            auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = warp_wait(bar, parity, abort_flag, a.wait_ns); };
-            auto before_pv = [&](uint32_t n) {                         // the values, and room for the part's first O
-                const uint32_t f = 2 * n + 1;
-                return wait(&full[f % NS], (f / NS) & 1) && (pt > 0 || wait(&ofree[pp & 1], ((pp >> 1) & 1) ^ 1));
+            // Whatever is ready is issued: a finished P frees its values' place in the ring, the next keys keep the softmax
+            // groups supplied (waiting for either in turn holds up the other).
+            auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_test(bar, parity)) != 0; };
+            auto tiles_of = [&](const Walk<R>& x, int64_t rest) {
+                return __shfl_sync(0xFFFFFFFFu, rest < x.tiles - x.t ? (int)rest : x.tiles - x.t, 0);
             };
-            while (left > 0 && ok) {
-                const int nt = __shfl_sync(0xFFFFFFFFu, left < w.tiles - w.t ? (int)left : w.tiles - w.t, 0);
-                const uint32_t qb = piece % C::QBUFS;
-                if (!wait(&qfull[qb], (piece / C::QBUFS) & 1)) break;
-                for (int t = 0; t < nt; ++t, ++i) {
-                    const uint32_t f = 2 * i, s = f % NS;
-                    if (!wait(&full[s], (f / NS) & 1)) break;
-                    if constexpr (PAIR) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (i > 0 && !wait(&pfull[h], (i - 1) & 1)) break;       // S of the tile before has been read
-                            tc_fence_after();
-                            qk(s, qb, h, h == 1, t == nt - 1);
-                            if (i > 0) {
-                                if (h == 0 && !before_pv(i - 1)) break;
-                                tc_fence_after();
-                                pv(i - 1, h, h == 1, h == 1 && plast);
-                            }
-                        }
-                        if (!ok) break;
-                    } else {
-                        tc_fence_after();
-                        qk(s, qb, i & 1, true, t == nt - 1);
-                        if (i > 0) {                                   // also: S of tile i - 1 has been read before tile i + 1
-                            if (!wait(&pfull[(i - 1) & 1], ((i - 1) >> 1) & 1) || !before_pv(i - 1)) break;
-                            tc_fence_after();
-                            pv(i - 1, (i - 1) & 1, true, plast);
-                        }
-                    }
-                    pp = piece;
-                    pt = t;
-                    plast = t == nt - 1;
-                }
-                if (!ok) break;
-                left -= nt;
-                ++piece;
-                w.advance(a, facts, nt, left > 0);
-            }
-            if (ok && i > 0) {
-                if constexpr (PAIR) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (!wait(&pfull[h], (i - 1) & 1) || (h == 0 && !before_pv(i - 1))) break;
-                        tc_fence_after();
-                        pv(i - 1, h, h == 1, h == 1);
-                    }
-                } else if (wait(&pfull[(i - 1) & 1], ((i - 1) >> 1) & 1) && before_pv(i - 1)) {
+            Walk<R> wv = w;                         // the tile whose O is added next, on its own way through the parts
+            int64_t vleft = left;
+            uint32_t i = 0, n = 0, piece = 0, vpart = 0;
+            int nt = left > 0 ? tiles_of(w, left) : 0, t = 0, vnt = nt, vt = 0;
+            uint32_t idle = 0;
+            uint64_t since = 0;
+            while (vnt > 0) {
+                bool moved = false;
+                const uint32_t vf = 2 * n + 1;
+                if (n < i && ready(&pfull[n & 1], (n >> 1) & 1) && ready(&full[vf % NS], (vf / NS) & 1) &&
+                    (vt > 0 || ready(&ofree[vpart & 1], ((vpart >> 1) & 1) ^ 1))) {
                     tc_fence_after();
-                    pv(i - 1, (i - 1) & 1, true, true);
+                    pv(n, vpart, vt < 2, vt == vnt - 1);
+                    ++n;
+                    if (++vt == vnt) {
+                        vleft -= vnt;
+                        ++vpart;
+                        vt = 0;
+                        wv.advance(a, facts, vnt, vleft > 0);
+                        vnt = vleft > 0 ? tiles_of(wv, vleft) : 0;
+                    }
+                    moved = true;
+                }
+                // S of tile i - SB has been read: its O, or a later one, has been added
+                const uint32_t kf = 2 * i;
+                if (nt > 0 && i < n + C::LOOK && (t > 0 || ready(&qfull[piece & 1], (piece >> 1) & 1)) &&
+                    ready(&full[kf % NS], (kf / NS) & 1)) {
+                    tc_fence_after();
+                    qk(i, piece & 1, t == nt - 1);
+                    ++i;
+                    if (++t == nt) {
+                        left -= nt;
+                        ++piece;
+                        t = 0;
+                        w.advance(a, facts, nt, left > 0);
+                        nt = left > 0 ? tiles_of(w, left) : 0;
+                    }
+                    moved = true;
+                }
+                if (moved) {
+                    idle = 0;
+                } else {                             // bounded, as every wait
+                    if ((++idle & 255u) == 0) {
+                        const uint64_t now = global_timer_ns();
+                        if (idle == 256) since = now;
+                        else if (now - since >= a.wait_ns) *abort_flag = 1;
+                        if (__any_sync(0xFFFFFFFFu, *abort_flag)) break;
+                    }
                 }
             }
-        } else if (warp == 14) {
+        } else if (warp == SW + 6) {
             // -------------------------------------------------------- scales: a lane takes four rows; pages are looked up two tiles
             // ahead and scales read one ahead
             auto place = [&]() { return row_of(w, (int64_t)w.t * TILE + lane * 4, false); };
@@ -1048,12 +1140,12 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
     tc_fence_before();
     __syncthreads();
     if (*abort_flag) {                               // final after the barrier: nothing new is issued past it
-        if (warp == 12 && lane == 0) drain_stage_fills(full, NS, issued);
-        if (warp == 13 && elect_one()) tc_drain(drain);
+        if (warp == SW + 4 && lane == 0) drain_stage_fills(full, NS, issued);
+        if (warp == SW + 5 && elect_one()) tc_drain(drain);
         tc_fence_before();
         __syncthreads();
     }
-    if (warp == 13) {
+    if (warp == SW + 5) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
     }
@@ -1068,7 +1160,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) tree_attention(const __grid_c
 // in which they were done.
 constexpr int JOIN_WARPS = 8;
 
-template <int D, int RU>
+template <int D, int R>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_attention_join(const AttnArgs a, int ctas) {
     pdl_trigger();
     pdl_wait();
@@ -1076,27 +1168,26 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_attention_join(const Att
     const int c = blockIdx.x + 1;
     if (c >= head.parts) return;
     const JoinUnit u = reinterpret_cast<const JoinUnit*>(a.ws + JOIN_UNITS)[c];
-    auto begin = [&](int k) { return (int64_t)((unsigned long long)head.total * k / head.parts); };
+    auto begin = [&](int k) { return part_begin(head.total, head.parts, k); };
     if (begin(c) <= u.first || begin(c - 1) > u.first) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = blockIdx.y * JOIN_WARPS + warp;
     if (r >= u.rows) return;
-    // the last CTA whose part begins before the unit's end: total k < end parts
-    const int last = (int)(((unsigned long long)u.end * head.parts - 1) / head.total);
+    const int last = part_of(head.total, head.parts, u.end - 1);
     const float* parts = reinterpret_cast<const float*>(a.ws + parts_offset(ctas));
     const int before = begin(c - 1) < u.first;       // that CTA comes to the unit from another one
-    auto part = [&](int k) { return parts + (size_t)(2 * k + (k == c - 1 ? before : 0)) * part_floats(RU, D); };
+    auto part = [&](int k) { return parts + (size_t)(2 * k + (k == c - 1 ? before : 0)) * part_floats(R, D); };
     float M = -INFINITY;
-    for (int k = c - 1 + lane; k <= last; k += 32) M = fmaxf(M, part(k)[RU * D + r]);
+    for (int k = c - 1 + lane; k <= last; k += 32) M = fmaxf(M, part(k)[R * D + r]);
     M = warp_max(M);
     constexpr int V = D / 32;                        // columns a lane
     float acc[V] = {}, L = 0.0f;
 #pragma unroll 4
     for (int k = c - 1; k <= last; ++k) {
         const float* p = part(k);
-        const float m = p[RU * D + r];
+        const float m = p[R * D + r];
         const float f = m == -INFINITY ? 0.0f : ex2(m - M);
-        L += f * p[RU * D + RU + r];                   // NaN stays, also with a weight of zero
+        L += f * p[R * D + R + r];                   // NaN stays, also with a weight of zero
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] += f * p[r * D + e * 32 + lane];
     }
@@ -1138,11 +1229,11 @@ cudaError_t codes_map(CUtensorMap* m, const void* base, const moe_kv_cache& c) {
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-constexpr int max_unit(int D) { return D == 256 ? 64 : 128; }        // RU: two halves of the widest R
+constexpr int max_unit(int D) { return D == 256 ? 32 : 64; }         // R: what shared memory holds
 
-template <int D, int R, bool PAIR>
+template <int D, int R>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
-    using C = Cfg<D, R, PAIR>;
+    using C = Cfg<D, R>;
     AttnMaps maps;
     cudaError_t e = codes_map(&maps.k, a.c.k_codes, a.c);
     if (e == cudaSuccess) e = codes_map(&maps.v, a.c.v_codes, a.c);
@@ -1151,33 +1242,30 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        e = cudaFuncSetAttribute(tree_attention<D, R, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        e = cudaFuncSetAttribute(tree_attention<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
     const int ctas = moe_sm_count();
     moe_prof_begin(MK_ATTENTION, s);
-    e = moe_launch(tree_attention<D, R, PAIR>, dim3((unsigned)ctas), dim3(ATTN_THREADS), C::SMEM, s, maps, a);
+    e = moe_launch(tree_attention<D, R>, dim3((unsigned)ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
     moe_prof_end(MK_ATTENTION, s);
     if (e != cudaSuccess || ctas < 2) return e;
     moe_prof_begin(MK_ATTENTION_JOIN, s);
-    e = moe_launch(tree_attention_join<D, C::RU>, dim3((unsigned)(ctas - 1), C::RU / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0, s, a, ctas);
+    e = moe_launch(tree_attention_join<D, R>, dim3((unsigned)(ctas - 1), R / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0, s, a, ctas);
     moe_prof_end(MK_ATTENTION_JOIN, s);
     return e;
 }
 
-// The tile of tree rows: the smallest that takes a lane's rows of one kv head at once.
+// The tile of tree rows: the smallest that takes a lane's rows of one kv head at once, else the largest. (Two groups
+// on one tile for twice the rows read the cache once where two units read it twice, but above 64 rows the softmax
+// bounds, not the reading: 3 % faster with 128 rows in every lane, 8 % slower with uneven trees.)
 template <int D>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
     const int64_t rows = (int64_t)(a.max_nodes < a.n_nodes ? a.max_nodes : a.n_nodes) * a.group;
-    if (rows <= 16) return launch<D, 16, false>(a, s);
-    if (rows <= 32) return launch<D, 32, false>(a, s);
-    if constexpr (D == 256) {
-        return launch<D, 32, true>(a, s);
-    } else {
-        if (rows <= 64) return launch<D, 64, false>(a, s);
-        return launch<D, 64, true>(a, s);
-    }
+    if (rows <= 16) return launch<D, 16>(a, s);
+    if (rows <= 32 || D == 256) return launch<D, 32>(a, s);
+    return launch<D, max_unit(D)>(a, s);
 }
 
 }  // namespace
