@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -111,7 +112,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.moe_wait_selftest.argtypes = [_P]
     L.moe_arena_refill.argtypes = [ctypes.POINTER(MoeArena), ctypes.POINTER(ctypes.c_void_p), _I, _P, _P, _P, _P,
                                    _P, ctypes.POINTER(ctypes.c_int32)]
-    _I64, _KV = ctypes.c_int64, ctypes.POINTER(MoeKvCache)
+    _I64, _KV = ctypes.c_int64, _P          # a cache goes by pointer: a MoeKvCache by reference, or its bytes
     L.moe_kv_write.argtypes = [_P, _P, _I, _I64, _I64, _I64, _I64, _P, _I, _KV, _P]
     L.moe_kv_read.argtypes = [_KV, _P, _I, _I, _P, _P, _I, _I, _P, _P, _P]
     L.moe_kv_keep.argtypes = [_KV, _P, _I, _I, _P, _P, _I, _P, _P]
@@ -143,12 +144,14 @@ def _ptr(t, host_ok: bool = False):
         raise ValueError("expected a CUDA tensor" + (" or a pinned host tensor" if host_ok else ""))
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """Handle of a stream, or of the current one of the current device (without building a Stream object: 3 us)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 @dataclass
@@ -384,23 +387,28 @@ def moe_renormalise_weights(sel_slot, sel_w, stream=None) -> None:
 _DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32}
 
 
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_CACHE_BYTES = struct.Struct("=4Q4i")              # the layout of moe_kv_cache
+
+
 class KvCache:
     """The paged 8-bit key/value cache of one attention layer (format: the header's ``moe_kv_cache``).
 
     ``k_codes``, ``v_codes``: e4m3 codes [n_pages, n_kv_heads, page_size, head_dim] (uint8 or float8_e4m3fn);
     ``k_scales``, ``v_scales``: e8m0 scale bytes uint8 [n_pages, n_kv_heads, page_size]. All contiguous, on the GPU.
     """
+    __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "n_pages", "n_kv_heads", "page_size", "head_dim", "_st")
 
     def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor):
-        if k_codes.dim() != 4 or v_codes.shape != k_codes.shape or any(
-                s.shape != k_codes.shape[:3] or s.dtype != torch.uint8 for s in (k_scales, v_scales)):
-            raise ValueError("codes [pages, heads, rows, dim], scales uint8 [pages, heads, rows]")
-        if k_codes.element_size() != 1 or v_codes.element_size() != 1:
-            raise ValueError("codes are one byte each")
+        shape = k_codes.shape
+        if len(shape) != 4 or v_codes.shape != shape or k_scales.shape != shape[:3] or v_scales.shape != shape[:3]:
+            raise ValueError("codes [pages, heads, rows, dim], scales [pages, heads, rows]")
+        if (k_codes.dtype not in _CODES or v_codes.dtype not in _CODES or k_scales.dtype is not torch.uint8 or
+                v_scales.dtype is not torch.uint8):
+            raise ValueError("codes are uint8 or float8_e4m3fn, scales uint8")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
-        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k_codes.shape
-        self._st = MoeKvCache(_ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), *k_codes.shape)
-        self._ref = ctypes.byref(self._st)
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = shape
+        self._st = _CACHE_BYTES.pack(_ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), *shape)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device="cuda") -> "KvCache":
@@ -410,15 +418,18 @@ class KvCache:
         scales = [torch.full(shape[:3], 127, dtype=torch.uint8, device=device) for _ in range(2)]
         return cls(*codes, *scales)
 
-    def rows(self, x: torch.Tensor, what: str) -> None:
-        """Raises unless x is [tokens, n_kv_heads, head_dim] with a contiguous last axis, on the GPU."""
-        if x.dim() != 3 or x.shape[1] != self.n_kv_heads or x.shape[2] != self.head_dim or x.stride(2) != 1 or not x.is_cuda:
-            raise ValueError(f"{what}: expected a CUDA tensor [tokens, {self.n_kv_heads}, {self.head_dim}] with a contiguous last axis")
+
+def _rows(x: torch.Tensor, cache: KvCache, what: str) -> None:
+    """Raises unless x is [tokens, n_kv_heads, head_dim] with a contiguous last axis, on the GPU."""
+    shape = x.shape
+    if (len(shape) != 3 or shape[1] != cache.n_kv_heads or shape[2] != cache.head_dim or x.stride(2) != 1 or
+            not x.is_cuda):
+        raise ValueError(f"{what}: expected a CUDA tensor [tokens, {cache.n_kv_heads}, {cache.head_dim}] with a contiguous last axis")
 
 
-def _of(t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str):
-    """Pointer of a contiguous CUDA tensor of this type and shape."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
+def _ints(t: torch.Tensor, shape: tuple, what: str, dtype=torch.int32):
+    """Pointer of a contiguous CUDA tensor of integers (or of another type) of this shape."""
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     return _ptr(t)
 
@@ -426,14 +437,18 @@ def _of(t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str):
 def moe_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: KvCache, stream=None) -> None:
     """Quantise the keys and values of T tokens [T, n_kv_heads, head_dim] (bf16, fp16 or fp32; any token and head
     strides of whole 16 bytes) into cache rows slots int64 [T] (page * page_size + row; -1 skips the token)."""
-    cache.rows(k, "k")
-    cache.rows(v, "v")
+    _rows(k, cache, "k")
+    _rows(v, cache, "v")
     T = k.shape[0]
-    if v.shape[0] != T or v.dtype != k.dtype or k.dtype not in _DTYPES:
+    dtype = _DTYPES.get(k.dtype)
+    if dtype is None or v.dtype is not k.dtype or v.shape[0] != T:
         raise ValueError("k and v: one length and one type of bf16, fp16, fp32")
-    _check("moe_kv_write", load().moe_kv_write(
-        k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-        _of(slots, torch.int64, (T,), "slots"), T, cache._ref, _stream(stream)))
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    st = (_lib or load()).moe_kv_write(k.data_ptr(), v.data_ptr(), dtype, kt, kh, vt, vh,
+                                       _ints(slots, (T,), "slots", torch.int64), T, cache._st, _stream(stream))
+    if st:
+        _check("moe_kv_write", st)
 
 
 def moe_kv_read(cache: KvCache, page_table: torch.Tensor, starts, cu_rows: torch.Tensor, k_out: torch.Tensor,
@@ -442,14 +457,16 @@ def moe_kv_read(cache: KvCache, page_table: torch.Tensor, starts, cu_rows: torch
     fp32): lane b's rows go to cu_rows[b] .. cu_rows[b + 1] (see the header). starts may be None (row 0)."""
     lanes, width = page_table.shape
     n = k_out.shape[0]
-    if k_out.dtype not in _DTYPES:
+    dtype = _DTYPES.get(k_out.dtype)
+    if dtype is None:
         raise ValueError("k_out: bf16, fp16 or fp32")
     shape = (n, cache.n_kv_heads, cache.head_dim)
-    _check("moe_kv_read", load().moe_kv_read(
-        cache._ref, _of(page_table, torch.int32, (lanes, width), "page_table"), width, lanes,
-        None if starts is None else _of(starts, torch.int32, (lanes,), "starts"),
-        _of(cu_rows, torch.int32, (lanes + 1,), "cu_rows"), n, _DTYPES[k_out.dtype],
-        _of(k_out, k_out.dtype, shape, "k_out"), _of(v_out, k_out.dtype, shape, "v_out"), _stream(stream)))
+    st = (_lib or load()).moe_kv_read(
+        cache._st, _ints(page_table, (lanes, width), "page_table"), width, lanes,
+        None if starts is None else _ints(starts, (lanes,), "starts"), _ints(cu_rows, (lanes + 1,), "cu_rows"), n, dtype,
+        _ints(k_out, shape, "k_out", k_out.dtype), _ints(v_out, shape, "v_out", k_out.dtype), _stream(stream))
+    if st:
+        _check("moe_kv_read", st)
 
 
 def moe_kv_keep(cache: KvCache, page_table: torch.Tensor, prefix: torch.Tensor, path: torch.Tensor,
@@ -457,10 +474,12 @@ def moe_kv_keep(cache: KvCache, page_table: torch.Tensor, prefix: torch.Tensor, 
     """Move the rows of each lane's accepted path, prefix[b] + path[b, i], to prefix[b] + i for i < n_keep[b], in
     place (int32 [lanes], [lanes, path_width], [lanes]; see the header)."""
     lanes, width = page_table.shape
-    _check("moe_kv_keep", load().moe_kv_keep(
-        cache._ref, _of(page_table, torch.int32, (lanes, width), "page_table"), width, lanes,
-        _of(prefix, torch.int32, (lanes,), "prefix"), _of(path, torch.int32, (lanes, path.shape[1]), "path"),
-        path.shape[1], _of(n_keep, torch.int32, (lanes,), "n_keep"), _stream(stream)))
+    path_width = path.shape[1]
+    st = (_lib or load()).moe_kv_keep(
+        cache._st, _ints(page_table, (lanes, width), "page_table"), width, lanes, _ints(prefix, (lanes,), "prefix"),
+        _ints(path, (lanes, path_width), "path"), path_width, _ints(n_keep, (lanes,), "n_keep"), _stream(stream))
+    if st:
+        _check("moe_kv_keep", st)
 
 
 def moe_tree_attention_workspace_bytes(n_nodes: int, n_q_heads: int, n_kv_heads: int, head_dim: int, lanes: int) -> int:
@@ -476,16 +495,18 @@ def moe_tree_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor
     [lanes + 1]; max_nodes: host bound on a lane's nodes; tree_mask int32 [n_nodes, words] or None (each node sees
     the rows up to its own); out bf16 like q, contiguous; lse fp32 [n_nodes, n_q_heads] or None.
     """
-    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_cuda or q.shape[2] != cache.head_dim or q.stride(2) != 1:
+    shape = q.shape
+    if len(shape) != 3 or q.dtype is not torch.bfloat16 or not q.is_cuda or shape[2] != cache.head_dim or q.stride(2) != 1:
         raise ValueError(f"q: expected a bf16 CUDA tensor [nodes, heads, {cache.head_dim}] with a contiguous last axis")
-    n, heads = q.shape[0], q.shape[1]
+    n, heads, _ = shape
+    qt, qh, _ = q.stride()
     lanes, width = page_table.shape
     words = 0 if tree_mask is None else tree_mask.shape[1]
-    _check("moe_tree_attention", load().moe_tree_attention(
-        q.data_ptr(), q.stride(0), q.stride(1), n, heads, cache._ref,
-        _of(page_table, torch.int32, (lanes, width), "page_table"), width, lanes,
-        _of(kv_len, torch.int32, (lanes,), "kv_len"), _of(cu_nodes, torch.int32, (lanes + 1,), "cu_nodes"), max_nodes,
-        None if tree_mask is None else _of(tree_mask, torch.int32, (n, words), "tree_mask"), words, scale,
-        _of(out, torch.bfloat16, (n, heads, cache.head_dim), "out"),
-        None if lse is None else _of(lse, torch.float32, (n, heads), "lse"), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    st = (_lib or load()).moe_tree_attention(
+        q.data_ptr(), qt, qh, n, heads, cache._st, _ints(page_table, (lanes, width), "page_table"), width, lanes,
+        _ints(kv_len, (lanes,), "kv_len"), _ints(cu_nodes, (lanes + 1,), "cu_nodes"), max_nodes,
+        None if tree_mask is None else _ints(tree_mask, (n, words), "tree_mask"), words, scale,
+        _ints(out, shape, "out", torch.bfloat16), None if lse is None else _ints(lse, (n, heads), "lse", torch.float32),
+        _ptr(workspace), workspace.nbytes, _stream(stream))
+    if st:
+        _check("moe_tree_attention", st)

@@ -36,7 +36,7 @@
 // thread can hold next to their sums).
 //
 // Work: the (lane, kv head, tile of tree rows) units, each a run of cache
-// tiles, are laid end to end and cut into equal parts, one per CTA. A unit that one
+// tiles, are laid end to end and cut into equal parts, one per CTA. (A few tiles are added for each unit.) A unit that one
 // CTA does whole is written at once; the others leave their parts (output, maximum, sum)
 // in the workspace and tree_attention_join adds them up in order.
 //
@@ -45,11 +45,15 @@
 //   a warp           TMA, one copy per page
 //   a warp           MMA issue, TMEM
 //   a warp           the rows' scales
-// Waits are bounded as in the expert GEMMs.
+//   a warp           what the join has to know, then the watchdog
+// Waits are bounded as in the expert GEMMs, by a watchdog warp. Loops that run beside the softmax are kept short and
+// rolled: their instructions compete with its unrolled ones for the instruction cache (TMA and scale loops unrolled
+// by four and eight cost a third of the rate).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <climits>
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -85,28 +89,28 @@ struct AttnMaps {
 constexpr int TILE = 128;                        // cache rows a tile
 constexpr int LANE_CACHE = 256;                  // lanes whose facts are kept in shared memory
 
-// What the join needs, at the start of the workspace: the cut, and for each CTA the unit that its part begins in.
-struct JoinHead {
-    int64_t total;                               // tiles in all
-    int32_t parts;                               // CTAs with work
-    int32_t pad;
-};
+// A unit costs this many tiles beside its own: its queries, its first reference, its output (which grow with R). The parts
+// are cut evenly in tiles and unit costs (below four tiles a CTA in tiles alone: there the longest part counts).
+__host__ __device__ constexpr int unit_cost(int R) { return R / 8; }
+
+// What the join needs, at the start of the workspace: for each CTA the unit that its part begins in.
 struct JoinUnit {
-    int64_t first, end;                          // the unit's tiles in the whole run
+    int32_t join;                                // 1: its part is the second of the unit, whose parts are
+    int32_t first, last;                         // those of CTAs first .. last,
+    int32_t second;                              // the first of them its CTA's second part (else its first)
     int32_t node0, rows, head, row0;             // first node of the lane, tree rows of the unit, kv head, first row in the lane
 };
-constexpr size_t JOIN_UNITS = 256;               // byte offset of JoinUnit[CTAs]
 
 __host__ __device__ constexpr size_t part_floats(int R, int D) { return (size_t)R * (D + 2); }
-__host__ __device__ inline size_t parts_offset(int ctas) { return (JOIN_UNITS + (size_t)ctas * sizeof(JoinUnit) + 255) / 256 * 256; }
+__host__ __device__ inline size_t parts_offset(int ctas) { return ((size_t)ctas * sizeof(JoinUnit) + 255) / 256 * 256; }
 
-// First tile of part k: total / parts tiles each, one more in the first total % parts. (64-bit divisions only where needed.)
+// Where part k begins: total / parts each, one more in the first total % parts. (64-bit divisions only where needed.)
 MOE_DEV int64_t part_begin(unsigned long long total, int parts, int k) {
     const unsigned long long each = total >> 32 ? total / parts : (uint32_t)total / (uint32_t)parts;
     const int more = (int)(total - each * parts);
     return (int64_t)(each * k) + (k < more ? k : more);
 }
-// The part that holds tile x.
+// The part that x is in.
 MOE_DEV int part_of(unsigned long long total, int parts, unsigned long long x) {
     const unsigned long long each = total / parts, more = total - each * parts;
     return (int)(x < more * (each + 1) ? x / (each + 1) : more + (x - more * (each + 1)) / each);
@@ -114,10 +118,10 @@ MOE_DEV int part_of(unsigned long long total, int parts, unsigned long long x) {
 
 template <int D, int R>                          // R: tree rows of a unit
 struct Cfg {
-    static constexpr int RH = R < 32 ? R : 32;                // tree rows of a softmax warpgroup: its threads' registers
+    static constexpr int RH = R == 64 ? 32 : 16;                // tree rows of a softmax warpgroup: its threads' registers
     static constexpr int HALVES = R / RH;                     // warpgroups of a softmax group
     static constexpr int SW = 8 * HALVES;                     // softmax warps, of two groups
-    static constexpr int THREADS = (SW + 8) * 32;             // then four of queries and outputs, TMA, MMA, scales, one idle
+    static constexpr int THREADS = (SW + 8) * 32;             // then four of queries and outputs, TMA, MMA, scales, join
     static constexpr int ROWB = D >= 128 ? 128 : 64;          // bytes of an operand row: one swizzle atom
     static constexpr int PANELS = D / ROWB;
     static constexpr int PANEL = TILE * ROWB;
@@ -126,14 +130,15 @@ struct Cfg {
     static constexpr int QBUF = QROWS * D;
     static constexpr int PBUF = 2 * TILE * R;
     static constexpr int SB = 4;                              // buffers of S
-    static constexpr int NS = D == 64 ? 16 : D == 256 ? 5 : R == 64 ? 9 : R == 32 ? 11 : 12;      // ring of key and value tiles: what fits
-    static constexpr int NSC = 4;                             // ring of scale tiles (128 key bytes, 128 value bytes)
+    static constexpr int NS = D == 64 ? 16 : D == 256 ? 5 : R == 64 ? 8 : R == 32 ? 11 : 12;      // ring of key and value tiles: what fits
+    static constexpr int NSC = 8;                             // ring of the rows' scales:
+    static constexpr int SC_BYTES = 2 * TILE + 16;            // key bytes, value bytes, largest and smallest value exponent
     static constexpr int MB = D == 256 ? 2 : 1;               // M blocks of O^T
     static constexpr int OFF_RING = 0;
     static constexpr int OFF_P = OFF_RING + NS * SLOT;
     static constexpr int OFF_Q = OFF_P + 2 * PBUF;
     static constexpr int OFF_SC = OFF_Q + 2 * QBUF;
-    static constexpr int OFF_F = OFF_SC + NSC * 256;          // floats from here
+    static constexpr int OFF_F = OFF_SC + NSC * SC_BYTES;          // floats from here
     static constexpr int F_O = 0;                             // [2 groups][R] 8 - m, as added to s'
     static constexpr int F_AL = F_O + 2 * R;                  // [2][R] scale-down of what has been added up
     static constexpr int F_WMAX = F_AL + 2 * R;               // [2 groups][HALVES][2][4 warps][RH]
@@ -142,15 +147,31 @@ struct Cfg {
     static constexpr int F_QX = F_QU + 8;                     // [largest, smallest][unit parity][4 warps] |q| of the rows, as bits
     static constexpr int F_L = F_QX + 16;                 // [2][4][R] sums at a part's end
     static constexpr int F_M = F_L + 8 * R;                   // [2][R] their references
-    static constexpr int F_ST = F_M + 2 * R;                  // [4 warps][2][R] factors of the output
-    static constexpr int F_END = F_ST + 8 * R;
+    static constexpr int F_ST = F_M + 2 * R;                  // [4 warps][3][R] factors of the output, and its rows' places (int)
+    static constexpr int F_END = F_ST + 12 * R;
     static constexpr int OFF_LANE = OFF_F + F_END * 4;        // int n0, n, len [LANE_CACHE]
     static constexpr int OFF_SCAN = OFF_LANE + 3 * LANE_CACHE * 4;
-    static constexpr int OFF_BAR = OFF_SCAN + 32 * 8 + 64;
-    // full, empty [NS]; scale full, empty [NSC]; sfull, vote, maxima [4]; pfull, pfree, qfull, qfree, ofull, ofree [2];
-    // lfull, lfree, qmax, drain
-    static constexpr int N_BARS = 2 * NS + 2 * NSC + 12 + 12 + 4;
-    static constexpr int OFF_MISC = (OFF_BAR + N_BARS * 8 + 15) / 16 * 16;     // tmem slot, abort flag, votes [4 warpgroups][2][4]
+    static constexpr int OFF_BAR = OFF_SCAN + 2 * 32 * 8 + 64;       // two sums, Cut
+    // barriers, as byte offsets
+    static constexpr int B_FULL = OFF_BAR;                    // [NS] a tile of keys or values has arrived
+    static constexpr int B_EMPTY = B_FULL + 8 * NS;           // [NS] ... has been used
+    static constexpr int B_SCFULL = B_EMPTY + 8 * NS;         // [NSC] the scales of a tile are there
+    static constexpr int B_SCEMPTY = B_SCFULL + 8 * NSC;      // [NSC] ... have been read
+    static constexpr int B_SFULL = B_SCEMPTY + 8 * NSC;       // [SB] S of a tile is ready
+    static constexpr int B_VOTE = B_SFULL + 8 * SB;           // [4 warpgroups] the four warps have compared a tile's scores
+    static constexpr int B_MAXIMA = B_VOTE + 32;              // [4 warpgroups] ... have written a tile's maxima
+    static constexpr int B_PFULL = B_MAXIMA + 32;             // [2 groups] P is written (and S has been read)
+    static constexpr int B_PFREE = B_PFULL + 16;              // [2] P has been read (and added to O)
+    static constexpr int B_QFULL = B_PFREE + 16;              // [2] the queries of a part are there
+    static constexpr int B_QFREE = B_QFULL + 16;              // [2] ... have been used
+    static constexpr int B_OFULL = B_QFREE + 16;              // [2] O of a part is complete
+    static constexpr int B_OFREE = B_OFULL + 16;              // [2] ... and has been read
+    static constexpr int B_LFULL = B_OFREE + 16;              // the sums of a part are written
+    static constexpr int B_LFREE = B_LFULL + 8;               // ... and read
+    static constexpr int B_QMAX = B_LFREE + 8;                // the four query warps have their maxima
+    static constexpr int B_DONE = B_QMAX + 8;                 // the block's last output is written
+    static constexpr int B_DRAIN = B_DONE + 8;
+    static constexpr int OFF_MISC = (B_DRAIN + 8 + 15) / 16 * 16;     // tmem slot, abort flag, votes [4 warpgroups][2][4]
     static constexpr int SMEM = OFF_MISC + 16 + 128 + 1024;
     // Tiles whose S may be under way: the buffers, and (an odd ring) not past a slot whose values are still to be used
     static constexpr int LOOK = NS % 2 && NS / 2 + 1 < SB ? NS / 2 + 1 : SB;
@@ -205,17 +226,66 @@ MOE_DEV float warp_max(float v) {
     return r;
 }
 
-// Whether the phase with this parity is over, without waiting.
-MOE_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
+// The barrier and copy instructions of common.cuh on 32-bit shared-memory addresses: one register holds the base, the
+// rest is an immediate. (Registers bound this kernel; a table of 64-bit pointers costs it dozens.)
+MOE_DEV bool test_at(uint32_t bar, uint32_t parity) {         // without waiting
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
+}
+MOE_DEV bool try_at(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+MOE_DEV bool try_at_for(uint32_t bar, uint32_t parity, uint32_t ns) {       // asleep for about ns at most
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(ns)
+        : "memory");
+    return ok != 0;
+}
+MOE_DEV uint32_t stopped(uint32_t stop) {
+    uint32_t v;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(stop) : "memory");
+    return v;
+}
+MOE_DEV void stop_all(uint32_t stop) { asm volatile("st.volatile.shared.u32 [%0], 1;" ::"r"(stop) : "memory"); }
+// A wait of a whole warp, with the same outcome in every lane: false when the block has been stopped. The watchdog warp bounds all
+// of a block's waits in one place: a bound in each of some thirty inlined waits drives the kernel out of the instruction cache.
+MOE_DEV bool warp_wait_at(uint32_t bar, uint32_t parity, uint32_t stop) {
+    while (!__all_sync(0xFFFFFFFFu, try_at(bar, parity)))
+        if (__any_sync(0xFFFFFFFFu, stopped(stop))) return false;
+    return true;
+}
+MOE_DEV void arrive_at(uint32_t bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory"); }
+MOE_DEV void arrive_expect_tx_at(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+MOE_DEV void commit_at(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+MOE_DEV void tma_load_at(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
 }
 
 MOE_DEV void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -227,7 +297,7 @@ MOE_DEV void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t
         : "memory");
 }
 
-// Moves registers between the warpgroups of a block of 768 threads launched with 80 each: 4 x 96 + 56 + 40 = 6 x 80.
+// Moves registers between warpgroups: of 768 threads launched with 80 each (R = 64), 4 x 96 + 56 + 40 = 6 x 80.
 template <int N> MOE_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> MOE_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
@@ -305,100 +375,211 @@ MOE_DEV Lane lane_facts(const AttnArgs& a, int b, bool* bad) {
     return l;
 }
 
-// One CTA's way through its part of the run: the unit it is in and the tile within it.
-template <int R>                                 // R: tree rows of a unit
-struct Walk {
-    int b, h, rt, t, tiles, nrt;
-    Lane l;
+// This CTA's part: its first lane, unit of the lane and tile of the unit, its number of tiles.
+struct Cut {
+    int lane, unit, t, count;
+    unsigned long long unit_at, before, next;        // that unit's first place in the run; tiles before the part, before the next one
+    unsigned long long total;                        // of the run: tiles and unit costs
+    int cost, parts;
+};
 
-    MOE_DEV void enter(const AttnArgs& a, const int* facts) {
-        if (b < LANE_CACHE) {
-            l.n0 = facts[b];
-            l.n = facts[LANE_CACHE + b];
-            l.len = facts[2 * LANE_CACHE + b];
-        } else {
-            bool bad;
-            l = lane_facts(a, b, &bad);
-        }
-        tiles = l.len > 0 ? (l.len + TILE - 1) / TILE : 1;
-        nrt = l.n > 0 ? (l.n * a.group + R - 1) / R : 1;
+// Inclusive sums over the block's threads of two values, and their totals. scratch: 64 values. One barrier, after one that
+// lets scratch be written again.
+MOE_DEV void scan2(unsigned long long& x, unsigned long long& y, unsigned long long* scratch, unsigned long long* tx, unsigned long long* ty) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long a = __shfl_up_sync(0xFFFFFFFFu, x, o), b = __shfl_up_sync(0xFFFFFFFFu, y, o);
+        if (lane >= o) { x += a; y += b; }
     }
-    MOE_DEV void start(const AttnArgs& a, const int* facts, int lane, int64_t offset) {
-        b = lane;
-        enter(a, facts);
-        const int u = offset >> 32 ? (int)(offset / tiles) : (int)((uint32_t)offset / (uint32_t)tiles);
-        t = (int)(offset - (int64_t)u * tiles);
-        h = u / nrt;
-        rt = u - h * nrt;
+    __syncthreads();
+    if (lane == 31) { scratch[wid] = x; scratch[32 + wid] = y; }
+    __syncthreads();
+    unsigned long long sx = lane < nw ? scratch[lane] : 0ull, sy = lane < nw ? scratch[32 + lane] : 0ull;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long a = __shfl_up_sync(0xFFFFFFFFu, sx, o), b = __shfl_up_sync(0xFFFFFFFFu, sy, o);
+        if (lane >= o) { sx += a; sy += b; }
+    }
+    *tx = __shfl_sync(0xFFFFFFFFu, sx, 31);
+    *ty = __shfl_sync(0xFFFFFFFFu, sy, 31);
+    const unsigned long long bx = __shfl_sync(0xFFFFFFFFu, sx, wid - 1 & 31), by = __shfl_sync(0xFFFFFFFFu, sy, wid - 1 & 31);
+    if (wid > 0) { x += bx; y += by; }
+}
+
+// One CTA's way through its part of the run: the unit it is in and the tile within it.
+struct Walk {
+    int b, h, rt, t, tiles, nrt;                     // lane, kv head, tile of tree rows, cache tile; tiles of the unit, units of a head
+};
+template <int R>                                     // R: tree rows of a unit
+struct Walker {
+    const AttnArgs& a;
+    const int* facts;
+
+    MOE_DEV Lane lane(int b) const {
+        if (b < LANE_CACHE) return Lane{facts[b], facts[LANE_CACHE + b], facts[2 * LANE_CACHE + b]};
+        bool bad;
+        return lane_facts(a, b, &bad);
+    }
+    MOE_DEV void enter(Walk& w) const {
+        const Lane l = lane(w.b);
+        w.tiles = l.len > 0 ? (l.len + TILE - 1) / TILE : 1;
+        w.nrt = l.n > 0 ? (l.n * a.group + R - 1) / R : 1;
+    }
+    MOE_DEV Walk start(int b, int u, int tile) const {
+        Walk w;
+        w.b = b;
+        enter(w);
+        w.t = tile;
+        w.h = u / w.nrt;
+        w.rt = u - w.h * w.nrt;
+        return w;
     }
     // past n tiles, which do not lead out of the unit; more: whether tiles are left after them
-    MOE_DEV void advance(const AttnArgs& a, const int* facts, int n, bool more) {
-        t += n;
-        if (t < tiles || !more) return;
-        t = 0;
-        if (++rt < nrt) return;
-        rt = 0;
-        if (++h < a.c.n_kv_heads) return;
-        h = 0;
-        do {
-            ++b;
-            enter(a, facts);
-        } while (l.n == 0 && b + 1 < a.lanes);
+    MOE_DEV void advance(Walk& w, int n, bool more) const {
+        w.t += n;
+        if (w.t < w.tiles || !more) return;
+        w.t = 0;
+        if (++w.rt < w.nrt) return;
+        w.rt = 0;
+        if (++w.h < a.c.n_kv_heads) return;
+        w.h = 0;
+        do ++w.b; while (lane(w.b).n == 0 && w.b + 1 < a.lanes);
+        enter(w);
     }
-    MOE_DEV int rows(const AttnArgs& a) const {               // tree rows of this unit
-        const int left = l.n * a.group - rt * R;
+    MOE_DEV int rows(const Walk& w) const {                   // tree rows of this unit
+        const int left = lane(w.b).n * a.group - w.rt * R;
         return left < R ? left : R;
     }
 };
 
+// The cut: every CTA adds up all lanes' tiles and finds its own part. A function of its own, so that nothing of it is
+// live in the roles.
+template <int R>
+__device__ __noinline__ void cut_run(const AttnArgs& a, int* facts, unsigned long long* scratch, Cut* here) {
+    const int tid = threadIdx.x, H = a.c.n_kv_heads, G = a.group;
+    // tiles and units of this thread's lane of a round, and of the lanes before it
+    unsigned long long tiles_all = 0, units_all = 0, tiles_in = 0, units_in = 0;
+    uint32_t units = 0, tiles = 0;
+    auto scan_lanes = [&](int b0, bool tell) {
+        const int b = b0 + tid;
+        Lane l{0, 0, 0};
+        if (b < a.lanes) {
+            bool bad;
+            l = lane_facts(a, b, &bad);
+            if (bad && tell && blockIdx.x == 0) record_error(a.err, MOE_DEV_BAD_PAGE);
+            if (b < LANE_CACHE) {
+                facts[b] = l.n0;
+                facts[LANE_CACHE + b] = l.n;
+                facts[2 * LANE_CACHE + b] = l.len;
+            }
+        }
+        units = l.n > 0 ? H * ((l.n * G + R - 1) / R) : 0;
+        tiles = l.len > 0 ? (l.len + TILE - 1) / TILE : 1;
+        unsigned long long x = (unsigned long long)units * tiles, y = units, tx, ty;
+        scan2(x, y, scratch, &tx, &ty);
+        tiles_in = tiles_all + x - (unsigned long long)units * tiles;
+        units_in = units_all + y - units;
+        tiles_all += tx;
+        units_all += ty;
+    };
+    for (int b0 = 0; b0 < a.lanes; b0 += (int)blockDim.x) scan_lanes(b0, true);
+    const unsigned long long n_tiles = tiles_all;
+    const int cost = n_tiles > 4ull * gridDim.x ? unit_cost(R) : 0;
+    const unsigned long long total = n_tiles + cost * units_all;
+    const int parts = n_tiles < gridDim.x ? (int)n_tiles : (int)gridDim.x;
+    const bool active = (int)blockIdx.x < parts;
+    const unsigned long long first = active ? part_begin(total, parts, blockIdx.x) : 0;
+    const unsigned long long next = active ? part_begin(total, parts, blockIdx.x + 1) : 0;
+    auto locate = [&](int b0) {                      // by the thread whose lane it is in
+        const unsigned long long at = tiles_in + cost * units_in, size = (unsigned long long)units * (tiles + cost);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const unsigned long long x = z ? next : first;
+            if (x < at || x >= at + size) continue;
+            const unsigned long long off = x - at;
+            const uint32_t each = tiles + cost, u = off >> 32 ? (uint32_t)(off / each) : (uint32_t)off / each;
+            const uint32_t in = (uint32_t)(off - (unsigned long long)u * each), tile = in > (uint32_t)cost ? in - cost : 0;
+            const unsigned long long before = tiles_in + (unsigned long long)u * tiles + tile;
+            if (z == 0) {
+                here->lane = b0 + tid;
+                here->unit = (int)u;
+                here->t = (int)tile;
+                here->unit_at = at + (unsigned long long)u * each;
+                here->before = before;
+            }
+            else here->next = before;
+        }
+    };
+    if (active) {
+        if (a.lanes <= (int)blockDim.x) {
+            locate(0);
+        } else {
+            tiles_all = units_all = 0;
+            for (int b0 = 0; b0 < a.lanes; b0 += (int)blockDim.x) {
+                scan_lanes(b0, false);
+                locate(b0);
+            }
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        if (!active) here->lane = here->unit = here->t = here->count = 0;
+        else here->count = (int)((next == total ? n_tiles : here->next) - here->before);      // of at most 2^31 rows
+        here->total = total;
+        here->cost = cost;
+        here->parts = parts;
+    }
+}
+
+// What the join has to know of this part.
+template <int R>
+__device__ __noinline__ void tell_join(const AttnArgs& a, const int* facts, const Cut* here) {
+    const Walker<R> walk{a, facts};
+    const Walk w = walk.start(here->lane, here->unit, here->t);
+    JoinUnit u{0, 0, 0, 0, walk.lane(w.b).n0, walk.rows(w), w.h, w.rt * R};
+    if (here->count > 0 && w.t > 0) {
+        u.first = part_of(here->total, here->parts, here->unit_at + here->cost);
+        u.last = part_of(here->total, here->parts, here->unit_at + here->cost + w.tiles - 1);
+        u.second = (unsigned long long)part_begin(here->total, here->parts, u.first) < here->unit_at;
+        u.join = u.first == (int)blockIdx.x - 1;
+    }
+    reinterpret_cast<JoinUnit*>(a.ws)[blockIdx.x] = u;
+}
+
 template <int D, int R>
-__global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
+__global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __grid_constant__ AttnMaps maps,
+                                                                          const __grid_constant__ AttnArgs a) {
     using C = Cfg<D, R>;
-    constexpr int RH = C::RH, SW = C::SW, ATTN_THREADS = C::THREADS;
+    constexpr int RH = C::RH, SW = C::SW;
     constexpr int NS = C::NS, NSC = C::NSC;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-    uint64_t* empty = full + NS;
-    uint64_t* scfull = empty + NS;
-    uint64_t* scempty = scfull + NSC;
-    uint64_t* sfull = scempty + NSC;             // [SB] S of a tile is ready
-    uint64_t* pfull = sfull + 4;                 // [2 groups] P is written (and S has been read)
-    uint64_t* pfree = pfull + 2;                 // [2] P has been read (and added to O)
-    uint64_t* vote = pfree + 2;                  // [warpgroups] the four warps have compared a tile's scores
-    uint64_t* maxima = vote + 4;                 // [warpgroups] ... have written a tile's maxima
-    uint64_t* qfull = maxima + 4;                // [2]
-    uint64_t* qfree = qfull + 2;
-    uint64_t* ofull = qfree + 2;                 // [2] O of a part is complete
-    uint64_t* ofree = ofull + 2;                 // [2] ... and has been read
-    uint64_t* lfull = ofree + 2;                 // the sums of a part are written
-    uint64_t* lfree = lfull + 1;                 // ... and read
-    uint64_t* qmax = lfree + 1;                  // the four query warps have their maxima
-    uint64_t* drain = qmax + 1;
+    const uint32_t base = smem_u32(smem), stop = base + C::OFF_MISC + 4;
+    auto bar = [&](int offset, uint32_t i = 0) { return base + offset + 8 * i; };
+    auto bar_ptr = [&](int offset) { return reinterpret_cast<uint64_t*>(smem + offset); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+    volatile uint32_t* progress = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 8);      // tiles done; parts out
     volatile int* votes = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);       // [warpgroups][2][4 warps]
     float* F = reinterpret_cast<float*>(smem + C::OFF_F);
     int* facts = reinterpret_cast<int*>(smem + C::OFF_LANE);
     unsigned long long* scratch = reinterpret_cast<unsigned long long*>(smem + C::OFF_SCAN);
-    int64_t* begin_off = reinterpret_cast<int64_t*>(smem + C::OFF_SCAN + 256);       // where this CTA's part begins
-    int* begin_lane = reinterpret_cast<int*>(smem + C::OFF_SCAN + 264);
+    Cut* here = reinterpret_cast<Cut*>(smem + C::OFF_SCAN + 512);
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const int H = a.c.n_kv_heads, G = a.group;
     pdl_trigger();
     if (tid == 0) {
-        for (int s = 0; s < NS; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-        for (int s = 0; s < NSC; ++s) { mbar_init(&scfull[s], 1); mbar_init(&scempty[s], SW / 2); }
-        for (int s = 0; s < 4; ++s) { mbar_init(&sfull[s], 1); mbar_init(&vote[s], 4); mbar_init(&maxima[s], 4); }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&pfull[s], SW / 2); mbar_init(&pfree[s], 1); mbar_init(&qfull[s], 4); mbar_init(&qfree[s], 1);
-            mbar_init(&ofull[s], 1); mbar_init(&ofree[s], 4);
-        }
-        mbar_init(lfull, SW); mbar_init(lfree, 4); mbar_init(qmax, 4); mbar_init(drain, 1);
+        auto init = [&](int offset, int n, int arrivals) {
+            for (int i = 0; i < n; ++i) mbar_init(bar_ptr(offset) + i, arrivals);
+        };
+        init(C::B_FULL, NS, 1); init(C::B_EMPTY, NS, 1); init(C::B_SCFULL, NSC, 1); init(C::B_SCEMPTY, NSC, SW / 2);
+        init(C::B_SFULL, C::SB, 1); init(C::B_VOTE, 4, 4); init(C::B_MAXIMA, 4, 4); init(C::B_PFULL, 2, SW / 2); init(C::B_PFREE, 2, 1);
+        init(C::B_QFULL, 2, 4); init(C::B_QFREE, 2, 1); init(C::B_OFULL, 2, 1); init(C::B_OFREE, 2, 4);
+        init(C::B_LFULL, 1, SW); init(C::B_LFREE, 1, 4); init(C::B_QMAX, 1, 4); init(C::B_DONE, 1, 1); init(C::B_DRAIN, 1, 1);
         *abort_flag = 0;
-        *begin_lane = 0;
-        *begin_off = 0;
+        progress[0] = progress[1] = 0;
         fence_barrier_init();
         prefetch_tmap(&maps.k);
         prefetch_tmap(&maps.v);
@@ -407,71 +588,15 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
     pdl_wait();
 
     // ---------------------------------------------------------------- the cut
-    auto work_of = [&](const Lane& l) -> unsigned long long {
-        if (l.n == 0) return 0ull;
-        const unsigned long long tiles = l.len > 0 ? (l.len + TILE - 1) / TILE : 1;
-        return (unsigned long long)H * ((l.n * G + R - 1) / R) * tiles;
-    };
-    unsigned long long total = 0, mine = 0, incl = 0;
-    for (int b0 = 0; b0 < a.lanes; b0 += ATTN_THREADS) {
-        const int b = b0 + tid;
-        Lane l{0, 0, 0};
-        if (b < a.lanes) {
-            bool bad;
-            l = lane_facts(a, b, &bad);
-            if (bad && blockIdx.x == 0) record_error(a.err, MOE_DEV_BAD_PAGE);
-            if (b < LANE_CACHE) {
-                facts[b] = l.n0;
-                facts[LANE_CACHE + b] = l.n;
-                facts[2 * LANE_CACHE + b] = l.len;
-            }
-        }
-        mine = work_of(l);
-        unsigned long long sum;
-        incl = block_inclusive_scan_u64(mine, scratch, &sum) + total;
-        total += sum;
-    }
-    const int parts = total < gridDim.x ? (int)total : (int)gridDim.x;
-    const bool active = (int)blockIdx.x < parts;
-    const int64_t first = active ? part_begin(total, parts, blockIdx.x) : 0;
-    const int64_t count = active ? part_begin(total, parts, blockIdx.x + 1) - first : 0;
-    if (active) {
-        if (a.lanes <= ATTN_THREADS) {
-            const unsigned long long excl = incl - mine;
-            if ((unsigned long long)first >= excl && (unsigned long long)first < incl) {
-                *begin_lane = tid;
-                *begin_off = first - (int64_t)excl;
-            }
-        } else {
-            unsigned long long before = 0;
-            for (int b0 = 0; b0 < a.lanes; b0 += ATTN_THREADS) {
-                const int b = b0 + tid;
-                bool bad;
-                mine = b < a.lanes ? work_of(lane_facts(a, b, &bad)) : 0ull;
-                unsigned long long sum;
-                incl = block_inclusive_scan_u64(mine, scratch, &sum) + before;
-                const unsigned long long excl = incl - mine;
-                if ((unsigned long long)first >= excl && (unsigned long long)first < incl) {
-                    *begin_lane = b;
-                    *begin_off = first - (int64_t)excl;
-                }
-                before += sum;
-            }
-        }
-    }
+    cut_run<R>(a, facts, scratch, here);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    Walk<R> w;
-    w.start(a, facts, active ? *begin_lane : 0, active ? *begin_off : 0);
-    if (tid == 0) {
-        if (blockIdx.x == 0) *reinterpret_cast<JoinHead*>(a.ws) = JoinHead{(int64_t)total, parts, 0};
-        if (active)
-            reinterpret_cast<JoinUnit*>(a.ws + JOIN_UNITS)[blockIdx.x] =
-                JoinUnit{first - w.t, first - w.t + w.tiles, w.l.n0, w.rows(a), w.h, w.rt * R};
-    }
-    int64_t left = count;
+    const int count = here->count;
+    const Walker<R> walk{a, facts};
+    Walk w = walk.start(here->lane, here->unit, here->t);
+    int left = count;
     uint32_t issued = 0;                             // ring fills, by the producer
 
     if (warp < SW) {
@@ -486,20 +611,21 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
         uint32_t i = 0, k = 0, sets = 0, polls = 0, piece = 0;       // tile of the CTA; of this group; references set; votes; part
         bool ok = true;
         while (left > 0 && ok) {
-            const int nt = left < w.tiles - w.t ? (int)left : w.tiles - w.t;
+            const int nt = left < w.tiles - w.t ? left : w.tiles - w.t;
             f32x2 l2[RH / 2];
             float M = -INFINITY;                     // reference of tree row `lane`
 #pragma unroll
             for (int r = 0; r < RH / 2; ++r) l2[r] = 0ull;
             const float* qf = F + C::F_QF + (piece & 3) * R + h * RH;
-            const int prefix = w.l.len - w.l.n;
+            const Lane ln = walk.lane(w.b);
+            const int len = ln.len, prefix = ln.len - ln.n;
             const int row0 = w.rt * R + h * RH;      // this warpgroup's tree rows in the lane
-            uint32_t ev_most = 0;                    // largest value scale seen so far
+            float ev_most = -INFINITY;               // largest value exponent seen so far
             bool set = true;                         // the reference is to be set (a part's first tile)
             for (int t = w.t; t < w.t + nt; ++t, ++i) {
                 if ((int)(i & 1) != g) continue;
                 const int j0 = t * TILE;
-                const int valid = w.l.len - j0;      // rows of the tile that exist (can be <= 0 or > 128)
+                const int valid = len - j0;      // rows of the tile that exist (can be <= 0 or > 128)
                 const bool masked = j0 + TILE > prefix;
                 // what this row is to each tree row
                 uint32_t sees = ~0u;
@@ -509,9 +635,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                         sees = 0u;
                     } else if (n >= 0) {
                         sees = 0u;
-                        const int end = w.l.n * G < row0 + RH ? w.l.n * G : row0 + RH;
+                        const Lane ln = walk.lane(w.b);
+                        const int end = ln.n * G < row0 + RH ? ln.n * G : row0 + RH;
                         for (int t1 = row0 / G; t1 * G < end; ++t1) {
-                            const bool see = a.mask ? (a.mask[(int64_t)(w.l.n0 + t1) * a.mask_words + (n >> 5)] >> (n & 31)) & 1
+                            const bool see = a.mask ? (a.mask[(int64_t)(ln.n0 + t1) * a.mask_words + (n >> 5)] >> (n & 31)) & 1
                                                     : n <= t1;
                             if (!see) continue;
                             int lo = t1 * G - row0, hi = lo + G;
@@ -522,22 +649,21 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                     }
                 }
                 const int sc = (int)(i % NSC);
-                if (!warp_wait(&scfull[sc], (i / NSC) & 1, abort_flag, a.wait_ns)) { ok = false; break; }
-                const uint8_t* scales = smem + C::OFF_SC + sc * 256;
+                if (!warp_wait_at(bar(C::B_SCFULL, sc), (i / NSC) & 1, stop)) { ok = false; break; }
+                const uint8_t* scales = smem + C::OFF_SC + sc * C::SC_BYTES;
                 const uint32_t ks = scales[j], vs = scales[TILE + j];
-                const uint32_t four = *reinterpret_cast<const uint32_t*>(scales + TILE + lane * 4);
+                const float2 range = *reinterpret_cast<const float2*>(scales + 2 * TILE);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&scempty[sc]);
-                const uint32_t most = __vmaxu4(four, four >> 16), least = __vminu4(four, __byte_perm(four, 0, 0x1032));
-                ev_most = max(ev_most, __reduce_max_sync(0xFFFFFFFFu, max(most & 255u, (most >> 8) & 255u)));
+                if (lane == 0) arrive_at(bar(C::B_SCEMPTY, sc));
                 // Value scales more than 2^104 apart: p could underflow in a row that matters to the sum of
                 // weights, p 2^-ev; its weight then gets an exponential of its own.
-                const bool wide = ev_most > __reduce_min_sync(0xFFFFFFFFu, min(least & 255u, (least >> 8) & 255u)) + 104u;
-                const int evi = vs == 255u ? 0 : (int)vs - 127;
+                ev_most = fmaxf(ev_most, range.x);
+                const bool wide = ev_most > range.y + 104.0f;
+                const int evi = vs == 255u ? 0 : (int)vs - 127;       // a NaN row that is not seen weighs nothing
                 const float ev = vs == 255u ? __uint_as_float(0x7FC00000u) : (float)evi;
                 const f32x2 ev2 = pack2(ev, ev);
                 const uint32_t sb = i % C::SB;
-                if (!warp_wait(&sfull[sb], (i / C::SB) & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                if (!warp_wait_at(bar(C::B_SFULL, sb), (i / C::SB) & 1, stop)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t srow = trow + sb * R;
                 const float2 unit = *reinterpret_cast<const float2*>(F + C::F_QU + (piece & 3) * 2);
@@ -595,8 +721,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                         }
                         wmax[wl * RH + (RH < 32 ? lane >> 1 : lane)] = v[0];
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&maxima[wg]);
-                        if (!warp_wait(&maxima[wg], sets & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                        if (lane == 0) arrive_at(bar(C::B_MAXIMA, wg));
+                        if (!warp_wait_at(bar(C::B_MAXIMA, wg), sets & 1, stop)) { ok = false; break; }
                         ++sets;
                         if (RH == 32 || lane < RH) { // every warp writes the same factors
                             const float m = fmaxf(fmaxf(wmax[lane], wmax[RH + lane]), fmaxf(wmax[2 * RH + lane], wmax[3 * RH + lane]));
@@ -623,11 +749,11 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                         const bool over = __any_sync(0xFFFFFFFFu, top > P_EXP_MAX);
                         if (lane == 0) {
                             votes[wg * 8 + (polls & 1) * 4 + wl] = over;
-                            mbar_arrive(&vote[wg]);
+                            arrive_at(bar(C::B_VOTE, wg));
                         }
                     }
                     // P of this group's previous tile has been read, and its O added up
-                    if (k > 0 && !warp_wait(&pfree[g], (k - 1) & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                    if (k > 0 && !warp_wait_at(bar(C::B_PFREE, g), (k - 1) & 1, stop)) { ok = false; break; }
                     if (setting && !set) {           // what has been added up is scaled down to the new reference
                         tc_fence_after();
                         const uint32_t orow = tmem + ((uint32_t)(wl * 32) << 16) + C::TMEM_O + (g * 2 + (piece & 1)) * C::MB * R + h * RH;
@@ -673,7 +799,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                         *reinterpret_cast<uint4*>(at + TILE * R) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                     if (setting) break;
-                    if (!warp_wait(&vote[wg], polls & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                    if (!warp_wait_at(bar(C::B_VOTE, wg), polls & 1, stop)) { ok = false; break; }
                     const volatile int* got = votes + wg * 8 + (polls & 1) * 4;
                     ++polls;
                     if (!(got[0] | got[1] | got[2] | got[3])) break;
@@ -684,7 +810,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                 if (valid < TILE && h == 0) {
                     // rows past the lane's end hold anything: their values are cleared, so that 0 * NaN does not arise
                     const uint32_t f = 2 * i + 1;
-                    if (!warp_wait(&full[f % NS], (f / NS) & 1, abort_flag, a.wait_ns)) { ok = false; break; }
+                    if (!warp_wait_at(bar(C::B_FULL, f % NS), (f / NS) & 1, stop)) { ok = false; break; }
                     if (j >= valid)
 #pragma unroll
                         for (int p = 0; p < C::PANELS; ++p)
@@ -696,12 +822,13 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&pfull[g]);
+                if (lane == 0) arrive_at(bar(C::B_PFULL, g));
                 if (wide) {
+                    const float evf = (float)evi;
 #pragma unroll
                     for (int q = 0; q < RH / 2; ++q) {
                         const float2 s = unpack2(y[q]);
-                        l2[q] = add2(l2[q], pack2(ex2(s.x - (float)evi), ex2(s.y - (float)evi)));
+                        l2[q] = add2(l2[q], pack2(ex2(s.x - evf), ex2(s.y - evf)));
                     }
                 } else {
                     const float wj = exp2_int(-evi);
@@ -713,7 +840,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             }
             if (!ok) break;
             // the part's sums over this group's rows
-            if (piece > 0 && !warp_wait(lfree, (piece - 1) & 1, abort_flag, a.wait_ns)) break;
+            if (piece > 0 && !warp_wait_at(bar(C::B_LFREE), (piece - 1) & 1, stop)) break;
             float v[RH];
 #pragma unroll
             for (int r = 0; r < RH / 2; ++r) {
@@ -736,9 +863,9 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             F[C::F_L + (g * 4 + wl) * R + h * RH + (RH < 32 ? lane >> 1 : lane)] = v[0];
             if (wl == 0 && (RH == 32 || lane < RH)) F[C::F_M + g * R + h * RH + lane] = M;
             __syncwarp();
-            if (lane == 0) mbar_arrive(lfull);
+            if (lane == 0) arrive_at(bar(C::B_LFULL));
             left -= nt;
-            w.advance(a, facts, nt, left > 0);
+            walk.advance(w, nt, left > 0);
             ++piece;
         }
     } else if (warp < SW + 4) {
@@ -746,8 +873,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
         if constexpr (R == 64) regs_down<56>();
         const int wl = warp & 3;
         // the queries of the next unit; all loads of a batch are under way before the first is used
-        Walk<R> wq = w;
-        int64_t qleft = left;
+        Walk wq = w;
+        int qleft = left;
         uint32_t qpiece = 0;
         const int row_step = 4 * (32 / (D / 8));     // tree rows the four warps take at once
         auto convert = [&]() -> bool {
@@ -755,7 +882,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             constexpr int ITER = R / (4 * RPW) > 0 ? R / (4 * RPW) : 1;
             const int part = lane % LPR, sub = lane / LPR;
             const uint32_t qb = qpiece & 1;
-            const int rows = wq.rows(a), row0 = wq.rt * R;
+            const int rows = walk.rows(wq), row0 = wq.rt * R, n0 = walk.lane(wq.b).n0;
             uint8_t* Q = smem + C::OFF_Q + qb * C::QBUF;
             float* qf = F + C::F_QF + (qpiece & 3) * R;
             // up to eight rows a lane at a time, all loads under way before the first is used; more are read twice
@@ -768,7 +895,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                 for (int b = 0; b < BATCH; ++b) {
                     raw[b] = make_uint4(0u, 0u, 0u, 0u);
                     if (((b0 + b) * 4 + wl) * RPW + sub < rows)
-                        raw[b] = *reinterpret_cast<const uint4*>(a.q + (wq.l.n0 + node) * a.q_token_stride + (wq.h * G + head) * a.q_head_stride + part * 8);
+                        raw[b] = *reinterpret_cast<const uint4*>(a.q + (n0 + node) * a.q_token_stride + (wq.h * G + head) * a.q_head_stride + part * 8);
                     node += row_step / G;
                     head += row_step % G;
                     if (head >= G) { head -= G; ++node; }
@@ -803,9 +930,9 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             if (lane == 0) {
                 qx[(qpiece & 1) * 4 + wl] = most;
                 qx[8 + (qpiece & 1) * 4 + wl] = least;
-                mbar_arrive(qmax);
+                arrive_at(bar(C::B_QMAX));
             }
-            if (!warp_wait(qmax, qpiece & 1, abort_flag, a.wait_ns)) return false;
+            if (!warp_wait_at(bar(C::B_QMAX), qpiece & 1, stop)) return false;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 most = max(most, qx[(qpiece & 1) * 4 + q]);
@@ -819,7 +946,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             };
             const int unit_up = up_of(most);
             const bool rowwise = most >= 0x7F80u || (least < most && up_of(least) - unit_up > 4);
-            if (!warp_wait(&qfree[qb], ((qpiece >> 1) & 1) ^ 1, abort_flag, a.wait_ns)) return false;
+            if (!warp_wait_at(bar(C::B_QFREE, qb), ((qpiece >> 1) & 1) ^ 1, stop)) return false;
             if (wl == 0 && lane == 0)
                 *reinterpret_cast<float2*>(F + C::F_QU + (qpiece & 3) * 2) = make_float2(rowwise ? 1.0f : exp2_int(-unit_up), rowwise ? 1.0f : 0.0f);
             const int byte = part * 8, panel = byte / C::ROWB, in_row = byte % C::ROWB;
@@ -859,27 +986,28 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&qfull[qb]);
-            const int nt = qleft < wq.tiles - wq.t ? (int)qleft : wq.tiles - wq.t;
+            if (lane == 0) arrive_at(bar(C::B_QFULL, qb));
+            const int nt = qleft < wq.tiles - wq.t ? qleft : wq.tiles - wq.t;
             qleft -= nt;
             ++qpiece;
-            wq.advance(a, facts, nt, qleft > 0);
+            walk.advance(wq, nt, qleft > 0);
             return true;
         };
 
         constexpr int RL = R > 32 ? R / 32 : 1;    // tree rows a lane looks after
-        float* st = F + C::F_ST + wl * 2 * R;
+        float* st = F + C::F_ST + wl * 3 * R;
+        int* place = reinterpret_cast<int*>(st + 2 * R);
         const bool on = D >= 128 || lane < 16;       // M = 64 leaves 16 rows in each quarter of the lanes
         const int d0 = D >= 128 ? wl * 32 + lane : wl * 16 + (lane & 15);
         uint32_t i0 = 0, piece = 0;                  // the part's first tile
         if (left > 0) (void)convert();
         while (left > 0) {
-            const int nt = left < w.tiles - w.t ? (int)left : w.tiles - w.t;
+            const int nt = left < w.tiles - w.t ? left : w.tiles - w.t;
             if (qleft > 0 && !convert()) break;
             const uint32_t ob = piece & 1;
-            if (!warp_wait(lfull, piece & 1, abort_flag, a.wait_ns) || !warp_wait(&ofull[ob], (piece >> 1) & 1, abort_flag, a.wait_ns)) break;
+            if (!warp_wait_at(bar(C::B_LFULL), piece & 1, stop) || !warp_wait_at(bar(C::B_OFULL, ob), (piece >> 1) & 1, stop)) break;
             tc_fence_after();
-            const int rows = w.rows(a), row0 = w.rt * R;
+            const int rows = walk.rows(w), row0 = w.rt * R, n0 = walk.lane(w.b).n0;
             const bool whole = nt == w.tiles;
             // a group without a tile in this part has no O
             const bool has0 = nt > 1 || (i0 & 1) == 0, has1 = nt > 1 || (i0 & 1) == 1;
@@ -888,7 +1016,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
 #pragma unroll
             for (int r = 0; r < RL; ++r) {
                 const int u = r * 32 + lane;
-                if (u >= rows) break;
+                if (R < 32 && u >= R) break;
                 auto sum = [&](int g) {
                     const float* ls = F + C::F_L + g * 4 * R + u;
                     return (ls[0] + ls[R]) + (ls[2 * R] + ls[3 * R]);
@@ -896,104 +1024,114 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                 const float M0 = F[C::F_M + u], M1 = F[C::F_M + R + u], M = fmaxf(M0, M1);
                 float f0 = M0 == -INFINITY ? 0.0f : ex2(M0 - M), f1 = M1 == -INFINITY ? 0.0f : ex2(M1 - M);
                 const float L = sum(0) * f0 + sum(1) * f1;            // sums may be NaN
+                const int node = (row0 + u) / G, row = node * a.n_q_heads + row0 + u - node * G;      // of the lane and kv head
                 if (whole) {
                     // out = O / L; lse = ln 2 (M - 6 + log2 L): p carries 2^6
                     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
                     f0 *= inv;
                     f1 *= inv;
-                    if (wl == 0 && a.lse) {
-                        const int node = (row0 + u) / G;
-                        a.lse[(int64_t)(w.l.n0 + node) * a.n_q_heads + w.h * G + row0 + u - node * G] =
-                            L == 0.0f ? -INFINITY : (M - P_EXP + log2f(L)) * 0.69314718055994531f;
-                    }
-                } else if (wl == 0) {
+                    if (wl == 0 && a.lse && u < rows)
+                        a.lse[(int64_t)n0 * a.n_q_heads + w.h * G + row] = L == 0.0f ? -INFINITY : (M - P_EXP + log2f(L)) * 0.69314718055994531f;
+                } else if (wl == 0 && u < rows) {
                     part[R * D + u] = M;
                     part[R * D + R + u] = L;
                 }
+                // a group without a tile has no O: what lies there is read, and cleared below
                 st[u] = f0;
                 st[R + u] = f1;
+                place[u] = row * D;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(lfree);
-            int node = row0 / G, sub = row0 - node * G;
-            __nv_bfloat16* out = a.out + ((int64_t)(w.l.n0 + node) * a.n_q_heads + w.h * G + sub) * D + d0;
-            const uint32_t orow = tmem + ((uint32_t)(wl * 32) << 16) + C::TMEM_O;
-            for (int c0 = 0; c0 < rows; c0 += 8) {
-                float x[C::MB][8];
+            if (lane == 0) arrive_at(bar(C::B_LFREE));
+            __nv_bfloat16* out = a.out + ((int64_t)n0 * a.n_q_heads + w.h * G) * D + d0;
+            const uint32_t orow = tmem + ((uint32_t)(wl * 32) << 16) + C::TMEM_O + ob * C::MB * R;
+            for (int c0 = 0; c0 < rows; c0 += 16) {
 #pragma unroll
                 for (int m = 0; m < C::MB; ++m) {
-                    uint32_t o0[8], o1[8];
-                    if (has0) tc_ld_x8(orow + (ob * C::MB + m) * R + c0, o0);
-                    if (has1) tc_ld_x8(orow + ((2 + ob) * C::MB + m) * R + c0, o1);
+                    uint32_t o0[16], o1[16];
+                    tc_ld_x16(orow + m * R + c0, o0);
+                    tc_ld_x16(orow + (2 * C::MB + m) * R + c0, o1);
                     tc_wait_ld();
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        x[m][q] = has0 ? __uint_as_float(o0[q]) * st[c0 + q] : 0.0f;
-                        if (has1) x[m][q] = fmaf(__uint_as_float(o1[q]), st[R + c0 + q], x[m][q]);
-                    }
-                }
+                    for (int q = 0; q < 16; q += 4) {
+                        const float4 f0 = *reinterpret_cast<const float4*>(st + c0 + q), f1 = *reinterpret_cast<const float4*>(st + R + c0 + q);
+                        const int4 at = *reinterpret_cast<const int4*>(place + c0 + q);
+                        const float g0[4] = {f0.x, f0.y, f0.z, f0.w}, g1[4] = {f1.x, f1.y, f1.z, f1.w};
+                        const int to[4] = {at.x, at.y, at.z, at.w};
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    if (c0 + q >= rows) break;
-#pragma unroll
-                    for (int m = 0; m < C::MB; ++m) {
-                        if (!on) continue;
-                        if (whole) out[m * 128] = __float2bfloat16_rn(x[m][q]);
-                        else part[(c0 + q) * D + m * 128 + d0] = x[m][q];
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = (has0 ? __uint_as_float(o0[q + e]) * g0[e] : 0.0f) + (has1 ? __uint_as_float(o1[q + e]) * g1[e] : 0.0f);
+                            if (!on || c0 + q + e >= rows) continue;
+                            if (whole) out[to[e] + m * 128] = __float2bfloat16_rn(x);
+                            else part[(c0 + q + e) * D + m * 128 + d0] = x;
+                        }
                     }
-                    out += D;
-                    if (++sub == G) { sub = 0; out += (int64_t)(a.n_q_heads - G) * D; }
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ofree[ob]);
+            if (lane == 0) arrive_at(bar(C::B_OFREE, ob));
             i0 += nt;
             left -= nt;
-            w.advance(a, facts, nt, left > 0);
+            walk.advance(w, nt, left > 0);
             ++piece;
+            progress[1] = piece;
         }
+        __syncwarp();
+        if (wl == 0 && lane == 0) arrive_at(bar(C::B_DONE));           // the block's last work, or it has been stopped
     } else {
+        if (warp == SW + 7 && lane == 0) tell_join<R>(a, facts, here);       // (before registers are handed back: the call may use them)
+        __syncwarp();
         if constexpr (R == 64) regs_down<40>();
         const int P = 1 << a.page_shift;
-        // the cache row of this unit's head at lane row `at` (its page's first one is at / P * P), -1 past the end
-        auto row_of = [&](const Walk<R>& x, int64_t at, bool tell) -> int {
-            if (at >= x.l.len) return -1;
-            int p = a.table[(int64_t)x.b * a.width + (at >> a.page_shift)];
-            if (p < 0 || p >= a.c.n_pages) {
-                if (tell) record_error(a.err, MOE_DEV_BAD_PAGE);
-                p = 0;
-            }
-            return (p * H + x.h) * P + (int)(at & (P - 1));
+        // A warp of its own has few instructions a tile to spare (each waits for the one before: five clocks): within a part the
+        // way through the table is one add a tile. Ids are looked at when used, so that lookups stay under way;
+        // NONE is past the lane's rows.
+        constexpr int NONE = INT_MIN;
+        auto checked = [&](int page, bool tell) {
+            if (page >= 0 && page < a.c.n_pages) return page;
+            if (tell) record_error(a.err, MOE_DEV_BAD_PAGE);
+            return 0;
         };
         if (warp == SW + 4) {
             // -------------------------------------------------------- TMA: lane l copies the tile's l-th page (or 128 rows of it)
             const int rows_a_page = P < TILE ? P : TILE;
-            auto place = [&]() { return lane * rows_a_page < TILE ? row_of(w, (int64_t)w.t * TILE + lane * rows_a_page, true) : -1; };
-            int next = left > 0 ? place() : -1;
             bool ok = true;
-            for (uint32_t i = 0; left > 0 && ok; ++i) {
-                const int row = next;
-                --left;
-                if (left > 0) {                                       // the next tile's page, one tile ahead
-                    w.advance(a, facts, 1, true);
-                    next = place();
-                }
-                const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0)) * rows_a_page * D;
+            uint32_t f = 0, slot = 0, round = 1;     // fill of the ring, its slot, the parity of the slot's last use
+            while (left > 0 && ok) {
+                const int nt = left < w.tiles - w.t ? left : w.tiles - w.t;
+                const int first = w.t * TILE + lane * rows_a_page;
+                // past the part or the lane's rows, or no piece of a tile for this lane: nothing to copy
+                const int end = lane * rows_a_page >= TILE ? 0 : min(walk.lane(w.b).len, (w.t + nt) * TILE), hp = w.h * P;
+                const int32_t* table = a.table + (int64_t)w.b * a.width;
+                auto look = [&](int at) { return at < end ? table[at >> a.page_shift] : NONE; };
+                int page = look(first), page1 = look(first + TILE), page2 = look(first + 2 * TILE);
+                for (int d = 0; d < nt && ok; ++d) {
+                    const int at = first + d * TILE;
+                    const bool some = page != NONE;
+                    const int row = some ? checked(page, true) * H * P + hp + (at & (P - 1)) : 0;
+                    page = page1;
+                    page1 = page2;
+                    page2 = look(at + 3 * TILE);
+                    const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, some)) * rows_a_page * D;
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v) {
+                        if (!warp_wait_at(bar(C::B_EMPTY, slot), round, stop)) { ok = false; break; }
+                        if (lane == 0) arrive_expect_tx_at(bar(C::B_FULL, slot), bytes);
+                        ++f;
+                        __syncwarp();
+                        if (some)
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const uint32_t f = 2 * i + v, s = f % NS;
-                    if (!warp_wait(&empty[s], ((f / NS) & 1) ^ 1, abort_flag, a.wait_ns)) { ok = false; break; }
-                    if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
-                    ++issued;
-                    __syncwarp();
-                    if (row >= 0)
-#pragma unroll
-                        for (int p = 0; p < C::PANELS; ++p)
-                            tma_load_2d(smem + C::OFF_RING + s * C::SLOT + p * C::PANEL + lane * rows_a_page * C::ROWB,
-                                        v ? &maps.v : &maps.k, &full[s], p * 128, row);
+                            for (int q = 0; q < C::PANELS; ++q)
+                                tma_load_at(base + C::OFF_RING + slot * C::SLOT + q * C::PANEL + lane * rows_a_page * C::ROWB,
+                                            v ? &maps.v : &maps.k, bar(C::B_FULL, slot), q * 128, row);
+                        if (++slot == NS) { slot = 0; round ^= 1; }
+                    }
                 }
+                left -= nt;
+                walk.advance(w, nt, left > 0);
             }
+            issued = f;
         } else if (warp == SW + 5) {
             // -------------------------------------------------------- MMA issue. The loop is uniform over the warp and one elected
             // lane issues, so that descriptors stay in uniform registers (39 clocks an MMA of N = 16 against 120
@@ -1002,14 +1140,14 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             constexpr uint64_t PD = desc_base(R == 64 ? 4 : R == 32 ? 6 : 0, 8 * R);
             constexpr uint32_t ID_S = idesc_f8(128, R, 0, 0, 0);
             constexpr uint32_t ID_HI = idesc_f8(D < 128 ? 64 : 128, R, 1, 1, 1), ID_LO = idesc_f8(D < 128 ? 64 : 128, R, 1, 1, 0);
-            const uint32_t base = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             const uint64_t ring = desc_at(KD, smem_u32(smem + C::OFF_RING));
             const uint64_t qd = desc_at(KD, smem_u32(smem + C::OFF_Q)), pd = desc_at(PD, smem_u32(smem + C::OFF_P));
             // S of tile i = K (Q hi)^T + K (Q lo)^T; `last` of its part
             auto qk = [&](uint32_t i, uint32_t qb, bool last) {
                 const uint32_t s = (2 * i) % NS;
                 const uint64_t kd = ring + (uint64_t)(s * (C::SLOT >> 4)), q = qd + (uint64_t)(qb * (C::QBUF >> 4));
-                const uint32_t d = base + (i % C::SB) * R;
+                const uint32_t d = tm + (i % C::SB) * R;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 2 * D / 32; ++kk) {
@@ -1019,9 +1157,9 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                                   q + (((k / STEPS) * C::QROWS * C::ROWB + (kk / HALF) * R * C::ROWB + (k % STEPS) * 32) >> 4), ID_S,
                                   kk ? 1u : 0u);
                     }
-                    tc_commit(&empty[s]);
-                    tc_commit(&sfull[i % C::SB]);
-                    if (last) tc_commit(&qfree[qb]);
+                    commit_at(bar(C::B_EMPTY, s));
+                    commit_at(bar(C::B_SFULL, i % C::SB));
+                    if (last) commit_at(bar(C::B_QFREE, qb));
                 }
                 __syncwarp();
             };
@@ -1029,7 +1167,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             auto pv = [&](uint32_t n, uint32_t part, bool fresh, bool ends) {
                 const uint32_t g = n & 1, s = (2 * n + 1) % NS;
                 const uint64_t vd = ring + (uint64_t)(s * (C::SLOT >> 4)), p = pd + (uint64_t)(g * (C::PBUF >> 4));
-                const uint32_t o = base + C::TMEM_O + (g * 2 + (part & 1)) * C::MB * R;
+                const uint32_t o = tm + C::TMEM_O + (g * 2 + (part & 1)) * C::MB * R;
                 const uint32_t add = fresh ? 0u : 1u;
                 if (elect_one()) {
 #pragma unroll
@@ -1038,45 +1176,43 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                         for (int kk = 0; kk < 8; ++kk)                 // four steps of 32 rows with hi, four with lo
                             tc_mma_f8(o + m * R, vd + ((m * C::PANEL + (kk & 3) * 32 * C::ROWB) >> 4),
                                       p + (((kk >> 2) * TILE * R + (kk & 3) * 32 * R) >> 4), kk < 4 ? ID_HI : ID_LO, kk ? 1u : add);
-                    tc_commit(&empty[s]);
-                    tc_commit(&pfree[g]);
-                    if (ends) tc_commit(&ofull[part & 1]);
+                    commit_at(bar(C::B_EMPTY, s));
+                    commit_at(bar(C::B_PFREE, g));
+                    if (ends) commit_at(bar(C::B_OFULL, part & 1));
                 }
                 __syncwarp();
             };
             // Whatever is ready is issued: a finished P frees its values' place in the ring, the next keys keep the softmax
             // groups supplied (waiting for either in turn holds up the other).
-            auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_test(bar, parity)) != 0; };
-            auto tiles_of = [&](const Walk<R>& x, int64_t rest) {
-                return __shfl_sync(0xFFFFFFFFu, rest < x.tiles - x.t ? (int)rest : x.tiles - x.t, 0);
+            auto ready = [&](uint32_t at, uint32_t parity) { return __all_sync(0xFFFFFFFFu, test_at(at, parity)) != 0; };
+            auto tiles_of = [&](const Walk& x, int rest) {
+                return __shfl_sync(0xFFFFFFFFu, rest < x.tiles - x.t ? rest : x.tiles - x.t, 0);
             };
-            Walk<R> wv = w;                         // the tile whose O is added next, on its own way through the parts
-            int64_t vleft = left;
+            Walk wv = w;                         // the tile whose O is added next, on its own way through the parts
+            int vleft = left;
             uint32_t i = 0, n = 0, piece = 0, vpart = 0;
             int nt = left > 0 ? tiles_of(w, left) : 0, t = 0, vnt = nt, vt = 0;
-            uint32_t idle = 0;
-            uint64_t since = 0;
             while (vnt > 0) {
                 bool moved = false;
                 const uint32_t vf = 2 * n + 1;
-                if (n < i && ready(&pfull[n & 1], (n >> 1) & 1) && ready(&full[vf % NS], (vf / NS) & 1) &&
-                    (vt > 0 || ready(&ofree[vpart & 1], ((vpart >> 1) & 1) ^ 1))) {
+                if (n < i && ready(bar(C::B_PFULL, n & 1), (n >> 1) & 1) && ready(bar(C::B_FULL, vf % NS), (vf / NS) & 1) &&
+                    (vt > 0 || ready(bar(C::B_OFREE, vpart & 1), ((vpart >> 1) & 1) ^ 1))) {
                     tc_fence_after();
                     pv(n, vpart, vt < 2, vt == vnt - 1);
-                    ++n;
+                    progress[0] = ++n;
                     if (++vt == vnt) {
                         vleft -= vnt;
                         ++vpart;
                         vt = 0;
-                        wv.advance(a, facts, vnt, vleft > 0);
+                        walk.advance(wv, vnt, vleft > 0);
                         vnt = vleft > 0 ? tiles_of(wv, vleft) : 0;
                     }
                     moved = true;
                 }
                 // S of tile i - SB has been read: its O, or a later one, has been added
                 const uint32_t kf = 2 * i;
-                if (nt > 0 && i < n + C::LOOK && (t > 0 || ready(&qfull[piece & 1], (piece >> 1) & 1)) &&
-                    ready(&full[kf % NS], (kf / NS) & 1)) {
+                if (nt > 0 && i < n + C::LOOK && (t > 0 || ready(bar(C::B_QFULL, piece & 1), (piece >> 1) & 1)) &&
+                    ready(bar(C::B_FULL, kf % NS), (kf / NS) & 1)) {
                     tc_fence_after();
                     qk(i, piece & 1, t == nt - 1);
                     ++i;
@@ -1084,64 +1220,80 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                         left -= nt;
                         ++piece;
                         t = 0;
-                        w.advance(a, facts, nt, left > 0);
+                        walk.advance(w, nt, left > 0);
                         nt = left > 0 ? tiles_of(w, left) : 0;
                     }
                     moved = true;
                 }
-                if (moved) {
-                    idle = 0;
-                } else {                             // bounded, as every wait
-                    if ((++idle & 255u) == 0) {
-                        const uint64_t now = global_timer_ns();
-                        if (idle == 256) since = now;
-                        else if (now - since >= a.wait_ns) *abort_flag = 1;
-                        if (__any_sync(0xFFFFFFFFu, *abort_flag)) break;
-                    }
+                if (!moved && __any_sync(0xFFFFFFFFu, stopped(stop))) break;
+            }
+        } else if (warp == SW + 7) {
+            // -------------------------------------------------------- watchdog: stops the block when nothing has moved for the bound
+            uint32_t seen = 0;
+            uint64_t since = global_timer_ns();
+            while (!try_at_for(bar(C::B_DONE), 0, 20000) && !stopped(stop)) {
+                const uint32_t now_at = progress[0] + progress[1];
+                const uint64_t now = global_timer_ns();
+                if (now_at != seen) {
+                    seen = now_at;
+                    since = now;
+                } else if (now - since >= a.wait_ns) {
+                    stop_all(stop);
+                    break;
                 }
             }
-        } else if (warp == SW + 6) {
-            // -------------------------------------------------------- scales: a lane takes four rows; pages are looked up two tiles
-            // ahead and scales read one ahead
-            auto place = [&]() { return row_of(w, (int64_t)w.t * TILE + lane * 4, false); };
-            auto load = [&](int row, uint32_t& ks, uint32_t& vs) {
-                ks = vs = 0x7F7F7F7Fu;
-                if (row >= 0) {
-                    ks = *reinterpret_cast<const uint32_t*>(a.c.k_scales + row);
-                    vs = *reinterpret_cast<const uint32_t*>(a.c.v_scales + row);
+        } else {
+            // -------------------------------------------------------- scales: a lane takes four rows. Scales are under way four tiles
+            // ahead and pages another two: a tile takes 1,500 clocks and an access to loaded HBM several thousand.
+            bool ok = true;
+            uint32_t i = 0;
+            while (left > 0 && ok) {
+                const int nt = left < w.tiles - w.t ? left : w.tiles - w.t;
+                const int first = w.t * TILE + lane * 4, end = min(walk.lane(w.b).len, (w.t + nt) * TILE), hp = w.h * P;
+                const int32_t* table = a.table + (int64_t)w.b * a.width;
+                auto look = [&](int at) { return at < end ? table[at >> a.page_shift] : NONE; };
+                auto load = [&](int id, int at) {
+                    if (id == NONE) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                    const int row = checked(id, false) * H * P + hp + (at & (P - 1));
+                    return make_uint2(*reinterpret_cast<const uint32_t*>(a.c.k_scales + row), *reinterpret_cast<const uint32_t*>(a.c.v_scales + row));
+                };
+                int page[4], page4, page5;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) page[p] = look(first + p * TILE);
+                page4 = look(first + 4 * TILE);
+                page5 = look(first + 5 * TILE);
+                uint2 s0 = load(page[0], first), s1 = load(page[1], first + TILE), s2 = load(page[2], first + 2 * TILE), s3 = load(page[3], first + 3 * TILE);
+#pragma unroll 1
+                for (int d = 0; d < nt; ++d, ++i) {
+                    const int at = first + d * TILE;
+                    const uint32_t sc = i % NSC;
+                    if (!warp_wait_at(bar(C::B_SCEMPTY, sc), ((i / NSC) & 1) ^ 1, stop)) { ok = false; break; }
+                    uint8_t* dst = smem + C::OFF_SC + sc * C::SC_BYTES;
+                    reinterpret_cast<uint32_t*>(dst)[lane] = s0.x;
+                    reinterpret_cast<uint32_t*>(dst + TILE)[lane] = s0.y;
+                    const uint32_t hi = __vmaxu4(s0.y, s0.y >> 16), lo = __vminu4(s0.y, __byte_perm(s0.y, 0, 0x1032));
+                    const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(hi & 255u, (hi >> 8) & 255u));
+                    const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, min(lo & 255u, (lo >> 8) & 255u));
+                    if (lane == 0) *reinterpret_cast<float2*>(dst + 2 * TILE) = make_float2((float)most, (float)least);
+                    __syncwarp();
+                    if (lane == 0) arrive_at(bar(C::B_SCFULL, sc));
+                    s0 = s1;
+                    s1 = s2;
+                    s2 = s3;
+                    s3 = load(page4, at + 4 * TILE);
+                    page4 = page5;
+                    page5 = look(at + 6 * TILE);
                 }
-            };
-            uint32_t ks = 0, vs = 0, ks1 = 0, vs1 = 0;
-            int row1 = -1;
-            if (left > 0) load(place(), ks, vs);
-            if (left > 1) {
-                w.advance(a, facts, 1, true);
-                row1 = place();
-            }
-            for (uint32_t i = 0; left > 0; ++i) {
-                if (left > 1) load(row1, ks1, vs1);
-                if (left > 2) {
-                    w.advance(a, facts, 1, true);
-                    row1 = place();
-                }
-                const uint32_t sc = i % NSC;
-                if (!warp_wait(&scempty[sc], ((i / NSC) & 1) ^ 1, abort_flag, a.wait_ns)) break;
-                uint32_t* dst = reinterpret_cast<uint32_t*>(smem + C::OFF_SC + sc * 256);
-                dst[lane] = ks;
-                dst[32 + lane] = vs;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&scfull[sc]);
-                ks = ks1;
-                vs = vs1;
-                --left;
+                left -= nt;
+                walk.advance(w, nt, left > 0);
             }
         }
     }
     tc_fence_before();
     __syncthreads();
     if (*abort_flag) {                               // final after the barrier: nothing new is issued past it
-        if (warp == SW + 4 && lane == 0) drain_stage_fills(full, NS, issued);
-        if (warp == SW + 5 && elect_one()) tc_drain(drain);
+        if (warp == SW + 4 && lane == 0) drain_stage_fills(bar_ptr(C::B_FULL), NS, issued);
+        if (warp == SW + 5 && elect_one()) tc_drain(bar_ptr(C::B_DRAIN));
         tc_fence_before();
         __syncthreads();
     }
@@ -1164,26 +1316,19 @@ template <int D, int R>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_attention_join(const AttnArgs a, int ctas) {
     pdl_trigger();
     pdl_wait();
-    const JoinHead head = *reinterpret_cast<const JoinHead*>(a.ws);
-    const int c = blockIdx.x + 1;
-    if (c >= head.parts) return;
-    const JoinUnit u = reinterpret_cast<const JoinUnit*>(a.ws + JOIN_UNITS)[c];
-    auto begin = [&](int k) { return part_begin(head.total, head.parts, k); };
-    if (begin(c) <= u.first || begin(c - 1) > u.first) return;
+    const JoinUnit u = reinterpret_cast<const JoinUnit*>(a.ws)[blockIdx.x + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = blockIdx.y * JOIN_WARPS + warp;
-    if (r >= u.rows) return;
-    const int last = part_of(head.total, head.parts, u.end - 1);
+    if (!u.join || r >= u.rows) return;
     const float* parts = reinterpret_cast<const float*>(a.ws + parts_offset(ctas));
-    const int before = begin(c - 1) < u.first;       // that CTA comes to the unit from another one
-    auto part = [&](int k) { return parts + (size_t)(2 * k + (k == c - 1 ? before : 0)) * part_floats(R, D); };
+    auto part = [&](int k) { return parts + (size_t)(2 * k + (k == u.first ? u.second : 0)) * part_floats(R, D); };
     float M = -INFINITY;
-    for (int k = c - 1 + lane; k <= last; k += 32) M = fmaxf(M, part(k)[R * D + r]);
-    M = warp_max(M);
+    for (int k = u.first + lane; k <= u.last; k += 32) M = fmaxf(M, part(k)[R * D + r]);
     constexpr int V = D / 32;                        // columns a lane
     float acc[V] = {}, L = 0.0f;
-#pragma unroll 4
-    for (int k = c - 1; k <= last; ++k) {
+    M = warp_max(M);
+#pragma unroll 8
+    for (int k = u.first; k <= u.last; ++k) {
         const float* p = part(k);
         const float m = p[R * D + r];
         const float f = m == -INFINITY ? 0.0f : ex2(m - M);
