@@ -147,11 +147,13 @@ def _ptr(t, host_ok: bool = False):
     return t.data_ptr()
 
 
+_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     """Handle of a stream, or of the current one of the current device (without building a Stream object: 3 us)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream
+    return _raw_stream(_device()) if stream is None else stream.cuda_stream
 
 
 @dataclass
@@ -388,7 +390,18 @@ _DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE
 
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)
+_U8, _I32, _I64, _BF16, _F32 = torch.uint8, torch.int32, torch.int64, torch.bfloat16, torch.float32
 _CACHE_BYTES = struct.Struct("=4Q4i")              # the layout of moe_kv_cache
+
+
+def _at(t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str) -> int:
+    """Address of a contiguous CUDA tensor of this type and shape. (A small call's time is the host's: the checks of
+    these calls are written to be few.)"""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{what}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous CUDA tensor")
+    return t.data_ptr()
 
 
 class KvCache:
@@ -401,14 +414,13 @@ class KvCache:
 
     def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor):
         shape = k_codes.shape
-        if len(shape) != 4 or v_codes.shape != shape or k_scales.shape != shape[:3] or v_scales.shape != shape[:3]:
-            raise ValueError("codes [pages, heads, rows, dim], scales [pages, heads, rows]")
-        if (k_codes.dtype not in _CODES or v_codes.dtype not in _CODES or k_scales.dtype is not torch.uint8 or
-                v_scales.dtype is not torch.uint8):
-            raise ValueError("codes are uint8 or float8_e4m3fn, scales uint8")
+        if len(shape) != 4 or k_codes.dtype not in _CODES or v_codes.dtype not in _CODES:
+            raise ValueError("codes [pages, heads, rows, dim] of uint8 or float8_e4m3fn")
+        rows = shape[:3]
+        self._st = _CACHE_BYTES.pack(_at(k_codes, k_codes.dtype, shape, "k_codes"), _at(v_codes, v_codes.dtype, shape, "v_codes"),
+                                     _at(k_scales, _U8, rows, "k_scales"), _at(v_scales, _U8, rows, "v_scales"), *shape)
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = shape
-        self._st = _CACHE_BYTES.pack(_ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), *shape)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device="cuda") -> "KvCache":
@@ -419,34 +431,19 @@ class KvCache:
         return cls(*codes, *scales)
 
 
-def _rows(x: torch.Tensor, cache: KvCache, what: str) -> None:
-    """Raises unless x is [tokens, n_kv_heads, head_dim] with a contiguous last axis, on the GPU."""
-    shape = x.shape
-    if (len(shape) != 3 or shape[1] != cache.n_kv_heads or shape[2] != cache.head_dim or x.stride(2) != 1 or
-            not x.is_cuda):
-        raise ValueError(f"{what}: expected a CUDA tensor [tokens, {cache.n_kv_heads}, {cache.head_dim}] with a contiguous last axis")
-
-
-def _ints(t: torch.Tensor, shape: tuple, what: str, dtype=torch.int32):
-    """Pointer of a contiguous CUDA tensor of integers (or of another type) of this shape."""
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{what}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    return _ptr(t)
-
-
 def moe_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: KvCache, stream=None) -> None:
     """Quantise the keys and values of T tokens [T, n_kv_heads, head_dim] (bf16, fp16 or fp32; any token and head
     strides of whole 16 bytes) into cache rows slots int64 [T] (page * page_size + row; -1 skips the token)."""
-    _rows(k, cache, "k")
-    _rows(v, cache, "v")
-    T = k.shape[0]
-    dtype = _DTYPES.get(k.dtype)
-    if dtype is None or v.dtype is not k.dtype or v.shape[0] != T:
-        raise ValueError("k and v: one length and one type of bf16, fp16, fp32")
-    kt, kh, _ = k.stride()
-    vt, vh, _ = v.stride()
-    st = (_lib or load()).moe_kv_write(k.data_ptr(), v.data_ptr(), dtype, kt, kh, vt, vh,
-                                       _ints(slots, (T,), "slots", torch.int64), T, cache._st, _stream(stream))
+    shape, dtype = k.shape, _DTYPES.get(k.dtype)
+    if len(shape) != 3 or v.shape != shape or dtype is None or v.dtype is not k.dtype:
+        raise ValueError("k and v: one shape [tokens, heads, dim] and one type of bf16, fp16, fp32")
+    T, heads, dim = shape
+    kt, kh, k1 = k.stride()
+    vt, vh, v1 = v.stride()
+    if heads != cache.n_kv_heads or dim != cache.head_dim or k1 != 1 or v1 != 1 or not k.is_cuda or not v.is_cuda:
+        raise ValueError(f"k and v: expected CUDA tensors [tokens, {cache.n_kv_heads}, {cache.head_dim}] with a contiguous last axis")
+    st = (_lib or load()).moe_kv_write(k.data_ptr(), v.data_ptr(), dtype, kt, kh, vt, vh, _at(slots, _I64, (T,), "slots"),
+                                       T, cache._st, _raw_stream(_device()) if stream is None else stream.cuda_stream)
     if st:
         _check("moe_kv_write", st)
 
@@ -462,9 +459,9 @@ def moe_kv_read(cache: KvCache, page_table: torch.Tensor, starts, cu_rows: torch
         raise ValueError("k_out: bf16, fp16 or fp32")
     shape = (n, cache.n_kv_heads, cache.head_dim)
     st = (_lib or load()).moe_kv_read(
-        cache._st, _ints(page_table, (lanes, width), "page_table"), width, lanes,
-        None if starts is None else _ints(starts, (lanes,), "starts"), _ints(cu_rows, (lanes + 1,), "cu_rows"), n, dtype,
-        _ints(k_out, shape, "k_out", k_out.dtype), _ints(v_out, shape, "v_out", k_out.dtype), _stream(stream))
+        cache._st, _at(page_table, _I32, (lanes, width), "page_table"), width, lanes,
+        None if starts is None else _at(starts, _I32, (lanes,), "starts"), _at(cu_rows, _I32, (lanes + 1,), "cu_rows"), n, dtype,
+        _at(k_out, k_out.dtype, shape, "k_out"), _at(v_out, k_out.dtype, shape, "v_out"), _stream(stream))
     if st:
         _check("moe_kv_read", st)
 
@@ -476,8 +473,8 @@ def moe_kv_keep(cache: KvCache, page_table: torch.Tensor, prefix: torch.Tensor, 
     lanes, width = page_table.shape
     path_width = path.shape[1]
     st = (_lib or load()).moe_kv_keep(
-        cache._st, _ints(page_table, (lanes, width), "page_table"), width, lanes, _ints(prefix, (lanes,), "prefix"),
-        _ints(path, (lanes, path_width), "path"), path_width, _ints(n_keep, (lanes,), "n_keep"), _stream(stream))
+        cache._st, _at(page_table, _I32, (lanes, width), "page_table"), width, lanes, _at(prefix, _I32, (lanes,), "prefix"),
+        _at(path, _I32, (lanes, path_width), "path"), path_width, _at(n_keep, _I32, (lanes,), "n_keep"), _stream(stream))
     if st:
         _check("moe_kv_keep", st)
 
@@ -503,10 +500,10 @@ def moe_tree_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor
     lanes, width = page_table.shape
     words = 0 if tree_mask is None else tree_mask.shape[1]
     st = (_lib or load()).moe_tree_attention(
-        q.data_ptr(), qt, qh, n, heads, cache._st, _ints(page_table, (lanes, width), "page_table"), width, lanes,
-        _ints(kv_len, (lanes,), "kv_len"), _ints(cu_nodes, (lanes + 1,), "cu_nodes"), max_nodes,
-        None if tree_mask is None else _ints(tree_mask, (n, words), "tree_mask"), words, scale,
-        _ints(out, shape, "out", torch.bfloat16), None if lse is None else _ints(lse, (n, heads), "lse", torch.float32),
+        q.data_ptr(), qt, qh, n, heads, cache._st, _at(page_table, _I32, (lanes, width), "page_table"), width, lanes,
+        _at(kv_len, _I32, (lanes,), "kv_len"), _at(cu_nodes, _I32, (lanes + 1,), "cu_nodes"), max_nodes,
+        None if tree_mask is None else _at(tree_mask, _I32, (n, words), "tree_mask"), words, scale,
+        _at(out, _BF16, shape, "out"), None if lse is None else _at(lse, _F32, (n, heads), "lse"),
         _ptr(workspace), workspace.nbytes, _stream(stream))
     if st:
         _check("moe_tree_attention", st)

@@ -74,6 +74,7 @@ struct AttnArgs {
     int max_nodes;
     const int32_t* mask;
     int mask_words;
+    int whole;                                   // units are not cut: the table holds WHOLE_TILES tiles at most
     float scale_log2;                            // scale * log2(e)
     __nv_bfloat16* out;
     float* lse;
@@ -88,6 +89,10 @@ struct AttnMaps {
 
 constexpr int TILE = 128;                        // cache rows a tile
 constexpr int LANE_CACHE = 256;                  // lanes whose facts are kept in shared memory
+
+// Units of at most this many tiles are not cut between CTAs, and the join is not launched: a unit's tiles one after the other
+// take less than the join and its launch. Known on the host, from the rows that the page table can hold.
+constexpr int WHOLE_TILES = 8;
 
 // A unit costs this many tiles beside its own: its queries, its first reference, its output (which grow with R). The parts
 // are cut evenly in tiles and unit costs (below four tiles a CTA in tiles alone: there the longest part counts).
@@ -118,7 +123,7 @@ MOE_DEV int part_of(unsigned long long total, int parts, unsigned long long x) {
 
 template <int D, int R>                          // R: tree rows of a unit
 struct Cfg {
-    static constexpr int RH = R == 64 ? 32 : 16;                // tree rows of a softmax warpgroup: its threads' registers
+    static constexpr int RH = R < 32 ? R : 32;                // tree rows of a softmax warpgroup: its threads' registers
     static constexpr int HALVES = R / RH;                     // warpgroups of a softmax group
     static constexpr int SW = 8 * HALVES;                     // softmax warps, of two groups
     static constexpr int THREADS = (SW + 8) * 32;             // then four of queries and outputs, TMA, MMA, scales, join
@@ -219,13 +224,6 @@ MOE_DEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
-// Maximum over the warp, in every lane (NaN inputs are passed over).
-MOE_DEV float warp_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
-
 // The barrier and copy instructions of common.cuh on 32-bit shared-memory addresses: one register holds the base, the
 // rest is an immediate. (Registers bound this kernel; a table of 64-bit pointers costs it dozens.)
 MOE_DEV bool test_at(uint32_t bar, uint32_t parity) {         // without waiting
@@ -486,20 +484,21 @@ __device__ __noinline__ void cut_run(const AttnArgs& a, int* facts, unsigned lon
     for (int b0 = 0; b0 < a.lanes; b0 += (int)blockDim.x) scan_lanes(b0, true);
     const unsigned long long n_tiles = tiles_all;
     const int cost = n_tiles > 4ull * gridDim.x ? unit_cost(R) : 0;
-    const unsigned long long total = n_tiles + cost * units_all;
-    const int parts = n_tiles < gridDim.x ? (int)n_tiles : (int)gridDim.x;
+    const unsigned long long total = a.whole ? units_all : n_tiles + cost * units_all, pieces = a.whole ? units_all : n_tiles;
+    const int parts = pieces < gridDim.x ? (int)pieces : (int)gridDim.x;
     const bool active = (int)blockIdx.x < parts;
     const unsigned long long first = active ? part_begin(total, parts, blockIdx.x) : 0;
     const unsigned long long next = active ? part_begin(total, parts, blockIdx.x + 1) : 0;
     auto locate = [&](int b0) {                      // by the thread whose lane it is in
-        const unsigned long long at = tiles_in + cost * units_in, size = (unsigned long long)units * (tiles + cost);
+        const uint32_t each = a.whole ? 1 : tiles + cost;
+        const unsigned long long at = a.whole ? units_in : tiles_in + cost * units_in, size = (unsigned long long)units * each;
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
             const unsigned long long x = z ? next : first;
             if (x < at || x >= at + size) continue;
             const unsigned long long off = x - at;
-            const uint32_t each = tiles + cost, u = off >> 32 ? (uint32_t)(off / each) : (uint32_t)off / each;
-            const uint32_t in = (uint32_t)(off - (unsigned long long)u * each), tile = in > (uint32_t)cost ? in - cost : 0;
+            const uint32_t u = off >> 32 ? (uint32_t)(off / each) : (uint32_t)off / each;
+            const uint32_t in = (uint32_t)(off - (unsigned long long)u * each), tile = !a.whole && in > (uint32_t)cost ? in - cost : 0;
             const unsigned long long before = tiles_in + (unsigned long long)u * tiles + tile;
             if (z == 0) {
                 here->lane = b0 + tid;
@@ -1322,19 +1321,37 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_attention_join(const Att
     if (!u.join || r >= u.rows) return;
     const float* parts = reinterpret_cast<const float*>(a.ws + parts_offset(ctas));
     auto part = [&](int k) { return parts + (size_t)(2 * k + (k == u.first ? u.second : 0)) * part_floats(R, D); };
-    float M = -INFINITY;
-    for (int k = u.first + lane; k <= u.last; k += 32) M = fmaxf(M, part(k)[R * D + r]);
-    constexpr int V = D / 32;                        // columns a lane
-    float acc[V] = {}, L = 0.0f;
-    M = warp_max(M);
-#pragma unroll 8
-    for (int k = u.first; k <= u.last; ++k) {
-        const float* p = part(k);
-        const float m = p[R * D + r];
-        const float f = m == -INFINITY ? 0.0f : ex2(m - M);
-        L += f * p[R * D + R + r];                   // NaN stays, also with a weight of zero
+    constexpr int V = D / 32, AT_ONCE = D == 256 ? 4 : 8;      // columns a lane; parts whose loads are under way together
+    float acc[V] = {}, L = 0.0f, M = -INFINITY;
+#pragma unroll 1
+    for (int k0 = u.first; k0 <= u.last; k0 += AT_ONCE) {
+        float m[AT_ONCE], l[AT_ONCE], x[AT_ONCE][V], Mn = M;
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] += f * p[r * D + e * 32 + lane];
+        for (int k = 0; k < AT_ONCE; ++k) {
+            const float* p = part(k0 + k <= u.last ? k0 + k : u.last);
+            m[k] = p[R * D + r];
+            l[k] = p[R * D + R + r];
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[k][e] = p[r * D + e * 32 + lane];
+        }
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            if (k0 + k > u.last) { m[k] = -INFINITY; l[k] = 0.0f; }
+            Mn = fmaxf(Mn, m[k]);
+        }
+        const float f0 = M == -INFINITY ? 0.0f : ex2(M - Mn);
+        L *= f0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] *= f0;
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            const float f = m[k] == -INFINITY ? 0.0f : ex2(m[k] - Mn);
+            L += f * l[k];                           // NaN stays, also with a weight of zero
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (k0 + k <= u.last) acc[e] += f * x[k][e];
+        }
+        M = Mn;
     }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     const int tr = u.row0 + r, node = tr / a.group;
@@ -1395,10 +1412,12 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     moe_prof_begin(MK_ATTENTION, s);
     e = moe_launch(tree_attention<D, R>, dim3((unsigned)ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
     moe_prof_end(MK_ATTENTION, s);
-    if (e != cudaSuccess || ctas < 2) return e;
+    moe_count_launches(1);
+    if (e != cudaSuccess || ctas < 2 || a.whole) return e;
     moe_prof_begin(MK_ATTENTION_JOIN, s);
     e = moe_launch(tree_attention_join<D, R>, dim3((unsigned)(ctas - 1), R / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0, s, a, ctas);
     moe_prof_end(MK_ATTENTION_JOIN, s);
+    moe_count_launches(1);
     return e;
 }
 
@@ -1458,6 +1477,7 @@ moe_status moe_tree_attention(const void* q, int64_t q_token_stride, int64_t q_h
     a.max_nodes = max_nodes;
     a.mask = tree_mask;
     a.mask_words = mask_words;
+    a.whole = (int64_t)table_width * cache->page_size <= WHOLE_TILES * TILE;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
@@ -1467,6 +1487,5 @@ moe_status moe_tree_attention(const void* q, int64_t q_token_stride, int64_t q_h
     const cudaError_t e = cache->head_dim == 64    ? launch_rows<64>(a, s)
                           : cache->head_dim == 128 ? launch_rows<128>(a, s)
                                                    : launch_rows<256>(a, s);
-    moe_count_launches(2);
     return e == cudaSuccess ? MOE_OK : MOE_ECUDA;
 }
