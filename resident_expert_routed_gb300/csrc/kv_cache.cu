@@ -112,13 +112,13 @@ __global__ void __launch_bounds__(KV_THREADS) kv_write(const KvSide k, const KvS
 // moe_kv_read. A block takes a few rows; their places are looked up once (a
 // binary search over the lanes' row counts) and then every thread converts
 // 16-byte pieces of the output, neighbours next to each other.
-constexpr int READ_ROWS = 32;
+constexpr int READ_ROWS = 32, READ_UNROLL = 4;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(KV_THREADS) kv_read(const moe_kv_cache c, const int32_t* __restrict__ table, int width,
                                                       int lanes, const int32_t* __restrict__ starts,
                                                       const int32_t* __restrict__ cu, int n_rows, int rows_per_block,
-                                                      int page_shift, T* __restrict__ k_out, T* __restrict__ v_out,
+                                                      uint32_t by_heads, int page_shift, T* __restrict__ k_out, T* __restrict__ v_out,
                                                       uint32_t* err) {
     constexpr int EPC = 16 / sizeof(T), CPV = D / EPC;         // elements a piece, pieces a vector
     __shared__ int64_t base[READ_ROWS];                        // first cache row (head 0) of each of the block's rows
@@ -148,33 +148,44 @@ __global__ void __launch_bounds__(KV_THREADS) kv_read(const moe_kv_cache c, cons
     const uint8_t* scales = blockIdx.y ? c.v_scales : c.k_scales;
     T* out = (blockIdx.y ? v_out : k_out) + r0 * H * D;
     const int pieces = rows * H * CPV;
-    for (int i = threadIdx.x; i < pieces; i += KV_THREADS) {
-        const int vec = i / CPV, part = i % CPV;
-        const int row = vec / H, h = vec - row * H;
-        const int64_t b = base[row];
-        float f = __uint_as_float(0x7FC00000u);
-        uint32_t w[EPC / 4] = {};
-        if (b >= 0) {
+    for (int i0 = threadIdx.x; i0 < pieces; i0 += READ_UNROLL * KV_THREADS) {
+        uint32_t w[READ_UNROLL][EPC / 4];
+        uint32_t s[READ_UNROLL];
+#pragma unroll
+        for (int u = 0; u < READ_UNROLL; ++u) {                // all loads before the first use
+            const int i = i0 + u * KV_THREADS;
+            s[u] = 255u;
+            if (i >= pieces) continue;
+            const int vec = i / CPV, part = i % CPV;
+            const int row = H == 1 ? vec : (int)__umulhi((uint32_t)vec, by_heads), h = vec - row * H;
+            const int64_t b = base[row];
+            if (b < 0) continue;
             const int64_t at = b + ((int64_t)h << page_shift);
             if constexpr (EPC == 8) {
                 const uint2 q = *reinterpret_cast<const uint2*>(codes + at * D + part * 8);
-                w[0] = q.x;
-                w[1] = q.y;
+                w[u][0] = q.x;
+                w[u][1] = q.y;
             } else {
-                w[0] = *reinterpret_cast<const uint32_t*>(codes + at * D + part * 4);
+                w[u][0] = *reinterpret_cast<const uint32_t*>(codes + at * D + part * 4);
             }
-            f = e8m0_to_float(scales[at]);
+            s[u] = scales[at];
         }
-        uint4 o;
-        T* e = reinterpret_cast<T*>(&o);
 #pragma unroll
-        for (int q = 0; q < EPC / 2; ++q) {
-            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[q / 2] >> (16 * (q & 1))), __NV_E4M3);
-            const float2 p = __half22float2(__half2(hr));
-            e[2 * q] = from_float<T>(p.x * f);
-            e[2 * q + 1] = from_float<T>(p.y * f);
+        for (int u = 0; u < READ_UNROLL; ++u) {
+            const int i = i0 + u * KV_THREADS;
+            if (i >= pieces) break;
+            const float f = e8m0_to_float(s[u]);
+            uint4 o;
+            T* e = reinterpret_cast<T*>(&o);
+#pragma unroll
+            for (int q = 0; q < EPC / 2; ++q) {
+                const uint32_t two = s[u] == 255u ? 0u : w[u][q / 2] >> (16 * (q & 1));
+                const float2 p = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
+                e[2 * q] = from_float<T>(p.x * f);
+                e[2 * q + 1] = from_float<T>(p.y * f);
+            }
+            __stcs(reinterpret_cast<uint4*>(out + (int64_t)i * EPC), o);
         }
-        *reinterpret_cast<uint4*>(out + (int64_t)i * EPC) = o;
     }
 }
 
@@ -267,8 +278,10 @@ cudaError_t launch_read(const moe_kv_cache& c, const int32_t* table, int width, 
     rpb = rpb < 1 ? 1 : (rpb > READ_ROWS ? READ_ROWS : rpb);
     const dim3 grid((unsigned)((n_rows + rpb - 1) / rpb), 2);
     const int shift = log2_of(c.page_size);
+    // ceil(2^32 / heads): a product's upper half divides by the heads (vectors of a block: below 2^15)
+    const uint32_t by_heads = (uint32_t)((((uint64_t)1 << 32) + c.n_kv_heads - 1) / c.n_kv_heads);
     auto go = [&](auto kern) {
-        return moe_launch(kern, grid, dim3(KV_THREADS), 0, s, c, table, width, lanes, starts, cu, n_rows, rpb, shift,
+        return moe_launch(kern, grid, dim3(KV_THREADS), 0, s, c, table, width, lanes, starts, cu, n_rows, rpb, by_heads, shift,
                           static_cast<T*>(k_out), static_cast<T*>(v_out), err);
     };
     return c.head_dim == 64 ? go(kv_read<T, 64>) : c.head_dim == 128 ? go(kv_read<T, 128>) : go(kv_read<T, 256>);

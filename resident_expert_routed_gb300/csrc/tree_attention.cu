@@ -1242,8 +1242,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                 }
             }
         } else {
-            // -------------------------------------------------------- scales: a lane takes four rows. Scales are under way four tiles
-            // ahead and pages another two: a tile takes 1,500 clocks and an access to loaded HBM several thousand.
+            // -------------------------------------------------------- scales: a lane takes four rows. Scales are under way PF tiles
+            // ahead and pages another four: a tile takes 750 (head_dim 64) to 2,500 clocks (64 tree rows) and an access to
+            // loaded HBM some 5,500.
+            constexpr int PF = R == 64 ? 4 : 12, PG = 4;
             bool ok = true;
             uint32_t i = 0;
             while (left > 0 && ok) {
@@ -1256,32 +1258,34 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                     const int row = checked(id, false) * H * P + hp + (at & (P - 1));
                     return make_uint2(*reinterpret_cast<const uint32_t*>(a.c.k_scales + row), *reinterpret_cast<const uint32_t*>(a.c.v_scales + row));
                 };
-                int page[4], page4, page5;
+                int page[PG];
+                uint2 s[PF];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) page[p] = look(first + p * TILE);
-                page4 = look(first + 4 * TILE);
-                page5 = look(first + 5 * TILE);
-                uint2 s0 = load(page[0], first), s1 = load(page[1], first + TILE), s2 = load(page[2], first + 2 * TILE), s3 = load(page[3], first + 3 * TILE);
+                for (int p = 0; p < PF; ++p) s[p].x = (uint32_t)look(first + p * TILE);
+#pragma unroll
+                for (int p = 0; p < PF; ++p) s[p] = load((int)s[p].x, first + p * TILE);
+#pragma unroll
+                for (int p = 0; p < PG; ++p) page[p] = look(first + (PF + p) * TILE);
 #pragma unroll 1
                 for (int d = 0; d < nt; ++d, ++i) {
                     const int at = first + d * TILE;
                     const uint32_t sc = i % NSC;
                     if (!warp_wait_at(bar(C::B_SCEMPTY, sc), ((i / NSC) & 1) ^ 1, stop)) { ok = false; break; }
                     uint8_t* dst = smem + C::OFF_SC + sc * C::SC_BYTES;
-                    reinterpret_cast<uint32_t*>(dst)[lane] = s0.x;
-                    reinterpret_cast<uint32_t*>(dst + TILE)[lane] = s0.y;
-                    const uint32_t hi = __vmaxu4(s0.y, s0.y >> 16), lo = __vminu4(s0.y, __byte_perm(s0.y, 0, 0x1032));
+                    reinterpret_cast<uint32_t*>(dst)[lane] = s[0].x;
+                    reinterpret_cast<uint32_t*>(dst + TILE)[lane] = s[0].y;
+                    const uint32_t hi = __vmaxu4(s[0].y, s[0].y >> 16), lo = __vminu4(s[0].y, __byte_perm(s[0].y, 0, 0x1032));
                     const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(hi & 255u, (hi >> 8) & 255u));
                     const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, min(lo & 255u, (lo >> 8) & 255u));
                     if (lane == 0) *reinterpret_cast<float2*>(dst + 2 * TILE) = make_float2((float)most, (float)least);
                     __syncwarp();
                     if (lane == 0) arrive_at(bar(C::B_SCFULL, sc));
-                    s0 = s1;
-                    s1 = s2;
-                    s2 = s3;
-                    s3 = load(page4, at + 4 * TILE);
-                    page4 = page5;
-                    page5 = look(at + 6 * TILE);
+#pragma unroll
+                    for (int p = 0; p + 1 < PF; ++p) s[p] = s[p + 1];
+                    s[PF - 1] = load(page[0], at + PF * TILE);
+#pragma unroll
+                    for (int p = 0; p + 1 < PG; ++p) page[p] = page[p + 1];
+                    page[PG - 1] = look(at + (PF + PG) * TILE);
                 }
                 left -= nt;
                 walk.advance(w, nt, left > 0);
