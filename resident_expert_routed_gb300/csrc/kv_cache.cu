@@ -3,7 +3,10 @@
 // Format (include/moe_resident.h): per (row, head) vector head_dim e4m3 codes
 // and one e8m0 scale, 2^e with e the smallest exponent that keeps max|x| within
 // 448 * 2^e. The three calls only move and convert bytes, so HBM bounds the
-// large ones and the launch the small ones.
+// large ones and the launch the small ones. A code is rounded once, to nearest
+// (ties to even): scaling by a power of two is exact. Reading back multiplies
+// by that power in fp32, which is exact too (but below the smallest normal
+// fp16, and where a value of 2^127 and more leaves the type).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -43,8 +46,10 @@ struct KvSide {
 };
 
 // moe_kv_write. D / 16 lanes share a vector: 16 elements a lane, one 16-byte
-// store of codes, the maximum by shuffles within the group. blockIdx.y picks
-// keys or values.
+// store of codes, the maximum by shuffles within the group, so a vector is read
+// once and stays in registers. blockIdx.y picks keys or values. Measured (calls back
+// to back, 8 heads of 128, bf16): 8,192 rows 8.7 us (50.5 MB, 5.8 TB/s), one
+// row 1.5 us, a launch.
 template <typename T, int D>
 __global__ void __launch_bounds__(KV_THREADS) kv_write(const KvSide k, const KvSide v, const int64_t* __restrict__ slots,
                                                        int n_tokens, int H, int page_shift, int64_t n_rows, uint32_t* err) {
@@ -111,7 +116,10 @@ __global__ void __launch_bounds__(KV_THREADS) kv_write(const KvSide k, const KvS
 
 // moe_kv_read. A block takes a few rows; their places are looked up once (a
 // binary search over the lanes' row counts) and then every thread converts
-// 16-byte pieces of the output, neighbours next to each other.
+// 16-byte pieces of the output, neighbours next to each other, READ_UNROLL
+// pieces under way (one: 8.4 us for 7.8; eight: no faster). What is written is not read again
+// here, so it is stored as streaming. Measured (8 heads of 128, bf16): 8,192 rows
+// of one lane 7.8 us (50.5 MB, 6.5 TB/s).
 constexpr int READ_ROWS = 32, READ_UNROLL = 4;
 
 template <typename T, int D>
@@ -193,7 +201,8 @@ __global__ void __launch_bounds__(KV_THREADS) kv_read(const moe_kv_cache c, cons
 // takes the path in batches: all sources of a batch are read into registers,
 // then, after a barrier, written. Since the path ascends from >= 0, path[i] >=
 // i: the rows a batch writes are sources of this batch or of earlier ones
-// only, all read by then.
+// only, all read by then. The launch and four dependent loads (count, path, page,
+// codes) bound it: 2.9 us for one lane's 8 rows, 5.5 us for 64 lanes' paths.
 constexpr int KEEP_BATCH = 64;
 
 __global__ void __launch_bounds__(KV_THREADS) kv_keep(const moe_kv_cache c, const int32_t* __restrict__ table, int width,
@@ -274,7 +283,7 @@ template <typename T>
 cudaError_t launch_read(const moe_kv_cache& c, const int32_t* table, int width, int lanes, const int32_t* starts,
                         const int32_t* cu, int n_rows, void* k_out, void* v_out, uint32_t* err, cudaStream_t s) {
     const int per_row = c.n_kv_heads * c.head_dim / (16 / (int)sizeof(T));
-    int rpb = 8 * KV_THREADS / per_row;                        // about eight pieces a thread
+    int rpb = 8 * KV_THREADS / per_row;                        // about eight pieces a thread (4 and 16: slower)
     rpb = rpb < 1 ? 1 : (rpb > READ_ROWS ? READ_ROWS : rpb);
     const dim3 grid((unsigned)((n_rows + rpb - 1) / rpb), 2);
     const int shift = log2_of(c.page_size);

@@ -18,14 +18,15 @@
 //     value row is added to the exponent: s' = s + ev_j, p = 2^(s' - m + 6), so
 //     values of any size keep their precision; the sum of weights gets p 2^-ev_j.
 //   - m is a running reference, not each tile's maximum: it is the maximum of s'
-//     when it is set, and stays until a score passes it by 2^5.5 (p would pass what lo can
-//     hold); then it is set again and what has been added up is scaled down. Most tiles
+//     when it is set, and stays until a score passes it by 5.5 (p = 2^11.5 would pass what
+//     lo can hold); then it is set again and what has been added up is scaled down. Most tiles
 //     so need no maximum at all: one compare, a vote, no reduction over the rows.
 //     Weights below 2^-23 of the largest are dropped, the rest keep at least the 3 bits of
 //     hi, rounded to nearest.
+// Scores, sums, the accumulators O and the parts that the join adds up are fp32; the output is rounded to bf16 once.
 //
 // Orientation: cache rows are the MMA's M (128), tree rows its N, so a single
-// token costs N = 16 and a wide tree 64 or 128, and nothing is padded to 128;
+// token costs N = 16 and a wide tree 32 or 64, and nothing is padded to 128;
 // hi and lo accumulate:
 //   S^T[128 rows, R] = K[128, D] Q^T            O^T[D, R] += V^T[D, 128] P^T[128, R]
 // A thread of a softmax group is a cache row: the rows' scales are its own
@@ -38,7 +39,15 @@
 // Work: the (lane, kv head, tile of tree rows) units, each a run of cache
 // tiles, are laid end to end and cut into equal parts, one per CTA. (A few tiles are added for each unit.) A unit that one
 // CTA does whole is written at once; the others leave their parts (output, maximum, sum)
-// in the workspace and tree_attention_join adds them up in order.
+// in the workspace and tree_attention_join adds them up in order. One CTA an SM, so one long lane and many uneven
+// ones fill the machine alike.
+//
+// What bounds it (measured, a call's whole time; head_dim 128, 8 kv heads, 2,064 bytes of cache a row): up to 32 tree
+// rows HBM: one token in 64 lanes of uneven lengths up to 8,192 rows 106 us (543 MB, 5.1 TB/s; even lengths 5.8 TB/s),
+// a tree of 7 nodes in two lanes of 131,072 rows 111 us (541 MB). Of the 106 us the tile loop takes 90, the cut 3,
+// uneven SMs some 8, the join and its launch 5. With 64 tree rows the softmax's instructions: 2,500 clocks a tile
+// where HBM would allow 1,470 (trees of up to 16 nodes, 64 query heads, 32 lanes of up to 8,001 rows: 139 us). Below
+// some thousand rows the chain of one unit: 8.4 us for a lane of 300.
 //
 // Roles: 8 or 16 warps of softmax, then
 //   four warps       the next unit's queries (split and laid out), a finished unit's output
@@ -91,12 +100,16 @@ constexpr int TILE = 128;                        // cache rows a tile
 constexpr int LANE_CACHE = 256;                  // lanes whose facts are kept in shared memory
 
 // Units of at most this many tiles are not cut between CTAs, and the join is not launched: a unit's tiles one after the other
-// take less than the join and its launch. Known on the host, from the rows that the page table can hold.
+// take less than the join and its launch. Known on the host, from the rows that the page table can hold. (One token, 8 kv
+// heads of 128, us whole / cut: 300 rows 8.4 / 10.9 in one lane, 20.5 / 25.2 in 64; 1,000 rows 11.5 / 11.5 and 34.2 / 36.9;
+// 2,000 rows 16.8 / 14.0 and 57.3 / 55.0.)
 constexpr int WHOLE_TILES = 8;
 
 // A unit costs this many tiles beside its own: its queries, its first reference, its output (which grow with R). The parts
-// are cut evenly in tiles and unit costs (below four tiles a CTA in tiles alone: there the longest part counts).
-__host__ __device__ constexpr int unit_cost(int R) { return R / 8; }
+// are cut evenly in tiles and unit costs (below four tiles a CTA in tiles alone: there the longest part counts). Measured with
+// 0, R / 8, R / 4: trees of up to 16 nodes, 64 rows a unit, 205, 138, 147 us; 64 uneven lanes, 16 rows a unit, 109, 106, 109 us.
+constexpr int FULL_COST = 4, HALF_COST = 3;       // of a tile; with half of the unit's tree rows at most, where halves are other warps'
+__host__ __device__ constexpr int unit_cost(int R) { return FULL_COST * R / 8; }
 
 // What the join needs, at the start of the workspace: for each CTA the unit that its part begins in.
 struct JoinUnit {
@@ -144,7 +157,7 @@ struct Cfg {
     static constexpr int OFF_Q = OFF_P + 2 * PBUF;
     static constexpr int OFF_SC = OFF_Q + 2 * QBUF;
     static constexpr int OFF_F = OFF_SC + NSC * SC_BYTES;          // floats from here
-    static constexpr int F_O = 0;                             // [2 groups][R] 8 - m, as added to s'
+    static constexpr int F_O = 0;                             // [2 groups][R] P_EXP - m, as added to s'
     static constexpr int F_AL = F_O + 2 * R;                  // [2][R] scale-down of what has been added up
     static constexpr int F_WMAX = F_AL + 2 * R;               // [2 groups][HALVES][2][4 warps][RH]
     static constexpr int F_QF = F_WMAX + 16 * R;              // [4][R] 2^-a of the queries' rows
@@ -377,8 +390,8 @@ MOE_DEV Lane lane_facts(const AttnArgs& a, int b, bool* bad) {
 struct Cut {
     int lane, unit, t, count;
     unsigned long long unit_at, before, next;        // that unit's first place in the run; tiles before the part, before the next one
-    unsigned long long total;                        // of the run: tiles and unit costs
-    int cost, parts;
+    unsigned long long total;                        // of the run
+    int cost, weight, parts;                         // of a unit beside its tiles, of a tile of that unit; parts of the run
 };
 
 // Inclusive sums over the block's threads of two values, and their totals. scratch: 64 values. One barrier, after one that
@@ -456,9 +469,10 @@ struct Walker {
 template <int R>
 __device__ __noinline__ void cut_run(const AttnArgs& a, int* facts, unsigned long long* scratch, Cut* here) {
     const int tid = threadIdx.x, H = a.c.n_kv_heads, G = a.group;
-    // tiles and units of this thread's lane of a round, and of the lanes before it
-    unsigned long long tiles_all = 0, units_all = 0, tiles_in = 0, units_in = 0;
-    uint32_t units = 0, tiles = 0;
+    // this thread's lane of a round: units a head, tiles a unit, costs of a full unit's tile and of the last one's; sizes of
+    // the lanes before it, in the run's measure and in tiles
+    unsigned long long size_all = 0, tiles_all = 0, size_in = 0, tiles_in = 0, lane_size = 0, lane_tiles = 0;
+    uint32_t nrt = 0, tiles = 0, last = 0;
     auto scan_lanes = [&](int b0, bool tell) {
         const int b = b0 + tid;
         Lane l{0, 0, 0};
@@ -472,40 +486,64 @@ __device__ __noinline__ void cut_run(const AttnArgs& a, int* facts, unsigned lon
                 facts[2 * LANE_CACHE + b] = l.len;
             }
         }
-        units = l.n > 0 ? H * ((l.n * G + R - 1) / R) : 0;
+        nrt = (l.n * G + R - 1) / R;
         tiles = l.len > 0 ? (l.len + TILE - 1) / TILE : 1;
-        unsigned long long x = (unsigned long long)units * tiles, y = units, tx, ty;
+        last = Cfg<64, R>::HALVES > 1 && l.n * G - (int)(nrt - 1) * R <= R / 2 ? HALF_COST : FULL_COST;
+        lane_tiles = (unsigned long long)H * nrt * tiles;
+        lane_size = nrt == 0  ? 0
+                    : a.whole ? (unsigned long long)H * nrt
+                              : H * ((unsigned long long)tiles * ((nrt - 1) * FULL_COST + last) + (unsigned long long)nrt * unit_cost(R));
+        unsigned long long x = lane_size, y = lane_tiles, tx, ty;
         scan2(x, y, scratch, &tx, &ty);
-        tiles_in = tiles_all + x - (unsigned long long)units * tiles;
-        units_in = units_all + y - units;
-        tiles_all += tx;
-        units_all += ty;
+        size_in = size_all + x - lane_size;
+        tiles_in = tiles_all + y - lane_tiles;
+        size_all += tx;
+        tiles_all += ty;
     };
     for (int b0 = 0; b0 < a.lanes; b0 += (int)blockDim.x) scan_lanes(b0, true);
     const unsigned long long n_tiles = tiles_all;
-    const int cost = n_tiles > 4ull * gridDim.x ? unit_cost(R) : 0;
-    const unsigned long long total = a.whole ? units_all : n_tiles + cost * units_all, pieces = a.whole ? units_all : n_tiles;
+    const bool plain = !a.whole && n_tiles <= 4ull * gridDim.x;      // a tile is a tile
+    const uint32_t cost = a.whole || plain ? 0 : unit_cost(R), full = plain ? 1 : FULL_COST;
+    const unsigned long long total = plain ? n_tiles : size_all, pieces = a.whole ? size_all : n_tiles;
     const int parts = pieces < gridDim.x ? (int)pieces : (int)gridDim.x;
     const bool active = (int)blockIdx.x < parts;
     const unsigned long long first = active ? part_begin(total, parts, blockIdx.x) : 0;
     const unsigned long long next = active ? part_begin(total, parts, blockIdx.x + 1) : 0;
+    auto divide = [](unsigned long long x, unsigned long long y) { return (x | y) >> 32 ? (uint32_t)(x / y) : (uint32_t)x / (uint32_t)y; };
     auto locate = [&](int b0) {                      // by the thread whose lane it is in
-        const uint32_t each = a.whole ? 1 : tiles + cost;
-        const unsigned long long at = a.whole ? units_in : tiles_in + cost * units_in, size = (unsigned long long)units * each;
+        const unsigned long long at = plain ? tiles_in : size_in, size = plain ? lane_tiles : lane_size;
+        const uint32_t wl = plain ? 1 : last;
+        const uint32_t each = tiles * full + cost;                   // of a full unit; of all units of a head:
+        const unsigned long long head = (unsigned long long)(nrt - 1) * each + tiles * wl + cost;
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
             const unsigned long long x = z ? next : first;
             if (x < at || x >= at + size) continue;
             const unsigned long long off = x - at;
-            const uint32_t u = off >> 32 ? (uint32_t)(off / each) : (uint32_t)off / each;
-            const uint32_t in = (uint32_t)(off - (unsigned long long)u * each), tile = !a.whole && in > (uint32_t)cost ? in - cost : 0;
+            uint32_t u, tile = 0, w = wl;
+            unsigned long long in_lane;              // where the unit begins
+            if (a.whole) {
+                u = (uint32_t)off;
+                in_lane = off;
+            } else {
+                const uint32_t h = divide(off, head);
+                const unsigned long long rest = off - h * head;
+                uint32_t rt = divide(rest, each);
+                if (rt >= nrt - 1) rt = nrt - 1;
+                else w = full;
+                const uint32_t in = (uint32_t)(rest - (unsigned long long)rt * each);
+                if (in > cost) tile = (in - cost) / w;
+                u = h * nrt + rt;
+                in_lane = off - in;
+            }
             const unsigned long long before = tiles_in + (unsigned long long)u * tiles + tile;
             if (z == 0) {
                 here->lane = b0 + tid;
                 here->unit = (int)u;
                 here->t = (int)tile;
-                here->unit_at = at + (unsigned long long)u * each;
+                here->unit_at = at + in_lane;
                 here->before = before;
+                here->weight = (int)w;
             }
             else here->next = before;
         }
@@ -514,7 +552,7 @@ __device__ __noinline__ void cut_run(const AttnArgs& a, int* facts, unsigned lon
         if (a.lanes <= (int)blockDim.x) {
             locate(0);
         } else {
-            tiles_all = units_all = 0;
+            size_all = tiles_all = 0;
             for (int b0 = 0; b0 < a.lanes; b0 += (int)blockDim.x) {
                 scan_lanes(b0, false);
                 locate(b0);
@@ -523,10 +561,10 @@ __device__ __noinline__ void cut_run(const AttnArgs& a, int* facts, unsigned lon
     }
     __syncthreads();
     if (tid == 0) {
-        if (!active) here->lane = here->unit = here->t = here->count = 0;
+        if (!active) here->lane = here->unit = here->t = here->count = here->weight = 0;
         else here->count = (int)((next == total ? n_tiles : here->next) - here->before);      // of at most 2^31 rows
         here->total = total;
-        here->cost = cost;
+        here->cost = (int)cost;
         here->parts = parts;
     }
 }
@@ -538,8 +576,9 @@ __device__ __noinline__ void tell_join(const AttnArgs& a, const int* facts, cons
     const Walk w = walk.start(here->lane, here->unit, here->t);
     JoinUnit u{0, 0, 0, 0, walk.lane(w.b).n0, walk.rows(w), w.h, w.rt * R};
     if (here->count > 0 && w.t > 0) {
-        u.first = part_of(here->total, here->parts, here->unit_at + here->cost);
-        u.last = part_of(here->total, here->parts, here->unit_at + here->cost + w.tiles - 1);
+        // a part that begins within a tile's span has that tile
+        u.first = part_of(here->total, here->parts, here->unit_at + here->cost + here->weight - 1);
+        u.last = part_of(here->total, here->parts, here->unit_at + here->cost + (unsigned long long)w.tiles * here->weight - 1);
         u.second = (unsigned long long)part_begin(here->total, here->parts, u.first) < here->unit_at;
         u.join = u.first == (int)blockIdx.x - 1;
     }
@@ -619,10 +658,22 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             const Lane ln = walk.lane(w.b);
             const int len = ln.len, prefix = ln.len - ln.n;
             const int row0 = w.rt * R + h * RH;      // this warpgroup's tree rows in the lane
+            const int live = ln.n * G - row0;        // how many of them there are (more than RH: all; none or less: none)
             float ev_most = -INFINITY;               // largest value exponent seen so far
             bool set = true;                         // the reference is to be set (a part's first tile)
             for (int t = w.t; t < w.t + nt; ++t, ++i) {
                 if ((int)(i & 1) != g) continue;
+                if (C::HALVES > 1 && live <= 0) {    // the last unit of a lane: its first half has all the rows
+                    const int sc = (int)(i % NSC);
+                    if (!warp_wait_at(bar(C::B_SCFULL, sc), (i / NSC) & 1, stop)) { ok = false; break; }
+                    if (k > 0 && !warp_wait_at(bar(C::B_PFREE, g), (k - 1) & 1, stop)) { ok = false; break; }
+                    if (lane == 0) {
+                        arrive_at(bar(C::B_SCEMPTY, sc));
+                        arrive_at(bar(C::B_PFULL, g));
+                    }
+                    ++k;
+                    continue;
+                }
                 const int j0 = t * TILE;
                 const int valid = len - j0;      // rows of the tile that exist (can be <= 0 or > 128)
                 const bool masked = j0 + TILE > prefix;
@@ -772,6 +823,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                     const int swz = R == 64 ? (j >> 1) & 3 : R == 32 ? (j >> 2) & 1 : 0;
 #pragma unroll
                     for (int c0 = 0; c0 < RH; c0 += 16) {
+                        if (c0 >= live) break;       // what P then holds there becomes columns of O that nobody reads
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
