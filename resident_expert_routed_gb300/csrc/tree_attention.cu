@@ -149,14 +149,18 @@ struct Cfg {
     static constexpr int PBUF = 2 * TILE * R;
     static constexpr int SB = 4;                              // buffers of S
     static constexpr int NS = D == 64 ? 16 : D == 256 ? 5 : R == 64 ? 8 : R == 32 ? 11 : 12;      // ring of key and value tiles: what fits
-    static constexpr int NSC = 8;                             // ring of the rows' scales:
+    static constexpr int SA = 8;                              // tiles that scales are under way ahead, and page ids another as many
+    static constexpr int PT = 8;                              // tiles that the page ids of keys and values are under way ahead
+    static constexpr int NSC = 2 * SA;                        // ring of the rows' scales:
     static constexpr int SC_BYTES = 2 * TILE + 16;            // key bytes, value bytes, largest and smallest value exponent
     static constexpr int MB = D == 256 ? 2 : 1;               // M blocks of O^T
     static constexpr int OFF_RING = 0;
     static constexpr int OFF_P = OFF_RING + NS * SLOT;
     static constexpr int OFF_Q = OFF_P + 2 * PBUF;
     static constexpr int OFF_SC = OFF_Q + 2 * QBUF;
-    static constexpr int OFF_F = OFF_SC + NSC * SC_BYTES;          // floats from here
+    static constexpr int OFF_SID = OFF_SC + NSC * SC_BYTES;   // page ids, [2 SA][32]
+    static constexpr int OFF_TID = OFF_SID + 2 * SA * 128;    // [PT][8]
+    static constexpr int OFF_F = OFF_TID + PT * 32;           // floats from here
     static constexpr int F_O = 0;                             // [2 groups][R] P_EXP - m, as added to s'
     static constexpr int F_AL = F_O + 2 * R;                  // [2][R] scale-down of what has been added up
     static constexpr int F_WMAX = F_AL + 2 * R;               // [2 groups][HALVES][2][4 warps][RH]
@@ -272,6 +276,17 @@ MOE_DEV bool try_at_for(uint32_t bar, uint32_t parity, uint32_t ns) {       // a
         : "memory");
     return ok != 0;
 }
+MOE_DEV void cp_async_4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+MOE_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> MOE_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+MOE_DEV int read_at(uint32_t at) {
+    int v;
+    asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+MOE_DEV void write_at(uint32_t at, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
 MOE_DEV uint32_t stopped(uint32_t stop) {
     uint32_t v;
     asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(stop) : "memory");
@@ -1136,9 +1151,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
         if constexpr (R == 64) regs_down<40>();
         const int P = 1 << a.page_shift;
         // A warp of its own has few instructions a tile to spare (each waits for the one before: five clocks): within a part the
-        // way through the table is one add a tile. Ids are looked at when used, so that lookups stay under way;
-        // NONE is past the lane's rows.
-        constexpr int NONE = INT_MIN;
+        // way through the table is one add a tile. Ids are looked at when used, so that lookups stay under way.
         auto checked = [&](int page, bool tell) {
             if (page >= 0 && page < a.c.n_pages) return page;
             if (tell) record_error(a.err, MOE_DEV_BAD_PAGE);
@@ -1147,6 +1160,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
         if (warp == SW + 4) {
             // -------------------------------------------------------- TMA: lane l copies the tile's l-th page (or 128 rows of it)
             const int rows_a_page = P < TILE ? P : TILE;
+            const uint32_t ids = base + C::OFF_TID + (lane & 7) * 4;         // eight pages a tile at most: [PT][8]
             bool ok = true;
             uint32_t f = 0, slot = 0, round = 1;     // fill of the ring, its slot, the parity of the slot's last use
             while (left > 0 && ok) {
@@ -1155,16 +1169,25 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                 // past the part or the lane's rows, or no piece of a tile for this lane: nothing to copy
                 const int end = lane * rows_a_page >= TILE ? 0 : min(walk.lane(w.b).len, (w.t + nt) * TILE), hp = w.h * P;
                 const int32_t* table = a.table + (int64_t)w.b * a.width;
-                auto look = [&](int at) { return at < end ? table[at >> a.page_shift] : NONE; };
-                int page = look(first), page1 = look(first + TILE), page2 = look(first + 2 * TILE);
+                // Ids come PT tiles ahead through shared memory: a register handed from one to the next would wait for its load.
+                constexpr int PT = C::PT;
+                auto look = [&](int d) {
+                    const int at = first + d * TILE;
+                    if (d < nt && at < end) cp_async_4(ids + (d % PT) * 32, table + (at >> a.page_shift));
+                    cp_async_commit();
+                };
+                const bool few = nt < PT;            // then all at once
+#pragma unroll 1
+                for (int d = 0; d < (few ? nt : PT); ++d) look(d);
+#pragma unroll 1
                 for (int d = 0; d < nt && ok; ++d) {
                     const int at = first + d * TILE;
-                    const bool some = page != NONE;
-                    const int row = some ? checked(page, true) * H * P + hp + (at & (P - 1)) : 0;
-                    page = page1;
-                    page1 = page2;
-                    page2 = look(at + 3 * TILE);
+                    const bool some = at < end;
+                    if (few) cp_async_wait<0>(); else cp_async_wait<PT - 1>();
+                    int row = 0;
+                    if (some) row = checked(read_at(ids + (d % PT) * 32), true) * H * P + hp + (at & (P - 1));
                     const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, some)) * rows_a_page * D;
+                    look(d + PT);                    // into the place that has just been read
 #pragma unroll 1
                     for (int v = 0; v < 2; ++v) {
                         if (!warp_wait_at(bar(C::B_EMPTY, slot), round, stop)) { ok = false; break; }
@@ -1182,6 +1205,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                 left -= nt;
                 walk.advance(w, nt, left > 0);
             }
+            cp_async_wait<0>();
             issued = f;
         } else if (warp == SW + 5) {
             // -------------------------------------------------------- MMA issue. The loop is uniform over the warp and one elected
@@ -1294,54 +1318,67 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                 }
             }
         } else {
-            // -------------------------------------------------------- scales: a lane takes four rows. Scales are under way PF tiles
-            // ahead and pages another four: a tile takes 750 (head_dim 64) to 2,500 clocks (64 tree rows) and an access to
-            // loaded HBM some 5,500.
-            constexpr int PF = R == 64 ? 4 : 12, PG = 4;
+            // -------------------------------------------------------- scales: a lane takes four rows. Scales are under way A tiles
+            // ahead and page ids another A, both into shared memory (a register handed from one to the next waits for its load:
+            // a tile then takes an access): a tile takes 750 (head_dim 64) to 2,500 clocks (64 tree rows) and an
+            // access to loaded HBM some 5,500.
+            constexpr int A = C::SA;
+            const uint32_t ids = base + C::OFF_SID + lane * 4, sc0 = base + C::OFF_SC + lane * 4;
             bool ok = true;
             uint32_t i = 0;
             while (left > 0 && ok) {
                 const int nt = left < w.tiles - w.t ? left : w.tiles - w.t;
                 const int first = w.t * TILE + lane * 4, end = min(walk.lane(w.b).len, (w.t + nt) * TILE), hp = w.h * P;
                 const int32_t* table = a.table + (int64_t)w.b * a.width;
-                auto look = [&](int at) { return at < end ? table[at >> a.page_shift] : NONE; };
-                auto load = [&](int id, int at) {
-                    if (id == NONE) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                    const int row = checked(id, false) * H * P + hp + (at & (P - 1));
-                    return make_uint2(*reinterpret_cast<const uint32_t*>(a.c.k_scales + row), *reinterpret_cast<const uint32_t*>(a.c.v_scales + row));
-                };
-                int page[PG];
-                uint2 s[PF];
-#pragma unroll
-                for (int p = 0; p < PF; ++p) s[p].x = (uint32_t)look(first + p * TILE);
-#pragma unroll
-                for (int p = 0; p < PF; ++p) s[p] = load((int)s[p].x, first + p * TILE);
-#pragma unroll
-                for (int p = 0; p < PG; ++p) page[p] = look(first + (PF + p) * TILE);
-#pragma unroll 1
-                for (int d = 0; d < nt; ++d, ++i) {
+                auto look = [&](int d) {
                     const int at = first + d * TILE;
-                    const uint32_t sc = i % NSC;
-                    if (!warp_wait_at(bar(C::B_SCEMPTY, sc), ((i / NSC) & 1) ^ 1, stop)) { ok = false; break; }
-                    uint8_t* dst = smem + C::OFF_SC + sc * C::SC_BYTES;
-                    reinterpret_cast<uint32_t*>(dst)[lane] = s[0].x;
-                    reinterpret_cast<uint32_t*>(dst + TILE)[lane] = s[0].y;
-                    const uint32_t hi = __vmaxu4(s[0].y, s[0].y >> 16), lo = __vminu4(s[0].y, __byte_perm(s[0].y, 0, 0x1032));
+                    if (d < nt && at < end) cp_async_4(ids + (d % (2 * A)) * 128, table + (at >> a.page_shift));
+                };
+                auto load = [&](int d) {                     // its id has arrived
+                    if (d >= nt) return true;
+                    const uint32_t e = i + d, sc = e % NSC;
+                    if (!warp_wait_at(bar(C::B_SCEMPTY, sc), ((e / NSC) & 1) ^ 1, stop)) return false;
+                    const int at = first + d * TILE;
+                    const uint32_t dst = sc0 + sc * C::SC_BYTES;
+                    if (at < end) {
+                        const int row = checked(read_at(ids + (d % (2 * A)) * 128), false) * H * P + hp + (at & (P - 1));
+                        cp_async_4(dst, a.c.k_scales + row);
+                        cp_async_4(dst + TILE, a.c.v_scales + row);
+                    } else {
+                        write_at(dst, 0x7F7F7F7Fu);
+                        write_at(dst + TILE, 0x7F7F7F7Fu);
+                    }
+                    return true;
+                };
+                const int ahead = nt < A ? nt : A;
+#pragma unroll 1
+                for (int d = 0; d < ahead; ++d) look(d);
+                cp_async_commit();
+                cp_async_wait<0>();
+                // at d: scales of tile d + A and ids of tile d + 2 A are sent for, tile d is handed over; few tiles wait for all
+#pragma unroll 1
+                for (int d = -ahead; d < nt; ++d) {
+                    if (d >= 0) {
+                        if (nt < A) cp_async_wait<0>(); else cp_async_wait<A - 1>();
+                    }
+                    if (!load(d + ahead)) { ok = false; break; }
+                    look(d + 2 * A);
+                    cp_async_commit();
+                    if (d < 0) continue;
+                    const uint32_t sc = (i + d) % NSC;
+                    const uint32_t mine = read_at(sc0 + sc * C::SC_BYTES + TILE);
+                    const uint32_t hi = __vmaxu4(mine, mine >> 16), lo = __vminu4(mine, __byte_perm(mine, 0, 0x1032));
                     const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(hi & 255u, (hi >> 8) & 255u));
                     const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, min(lo & 255u, (lo >> 8) & 255u));
-                    if (lane == 0) *reinterpret_cast<float2*>(dst + 2 * TILE) = make_float2((float)most, (float)least);
+                    if (lane == 0) *reinterpret_cast<float2*>(smem + C::OFF_SC + sc * C::SC_BYTES + 2 * TILE) = make_float2((float)most, (float)least);
                     __syncwarp();
                     if (lane == 0) arrive_at(bar(C::B_SCFULL, sc));
-#pragma unroll
-                    for (int p = 0; p + 1 < PF; ++p) s[p] = s[p + 1];
-                    s[PF - 1] = load(page[0], at + PF * TILE);
-#pragma unroll
-                    for (int p = 0; p + 1 < PG; ++p) page[p] = page[p + 1];
-                    page[PG - 1] = look(at + (PF + PG) * TILE);
                 }
+                i += nt;
                 left -= nt;
                 walk.advance(w, nt, left > 0);
             }
+            cp_async_wait<0>();
         }
     }
     tc_fence_before();
