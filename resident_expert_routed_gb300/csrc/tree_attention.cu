@@ -43,11 +43,12 @@
 // ones fill the machine alike.
 //
 // What bounds it (measured, a call's whole time; head_dim 128, 8 kv heads, 2,064 bytes of cache a row): up to 32 tree
-// rows HBM: one token in 64 lanes of uneven lengths up to 8,192 rows 106 us (543 MB, 5.1 TB/s; even lengths 5.8 TB/s),
-// a tree of 7 nodes in two lanes of 131,072 rows 111 us (541 MB). Of the 106 us the tile loop takes 90, the cut 3,
-// uneven SMs some 8, the join and its launch 5. With 64 tree rows the softmax's instructions: 2,500 clocks a tile
-// where HBM would allow 1,470 (trees of up to 16 nodes, 64 query heads, 32 lanes of up to 8,001 rows: 139 us). Below
-// some thousand rows the chain of one unit: 8.4 us for a lane of 300.
+// rows HBM: one token in 64 lanes of uneven lengths up to 8,192 rows 95 us (543 MB, 5.7 TB/s; even lengths 6.4 TB/s,
+// head_dim 256 6.4, head_dim 64 4.1: there the copies' warp, 1,100 clocks a tile for four pages), a tree of 7 nodes in two
+// lanes of 131,072 rows 103 us (541 MB). Of the 95 us the tile loop takes 78, the cut 4, the first tile 4, the last
+// outputs, the join and its launch 6. With 64 tree rows the softmax's instructions and their latency: 2,200 clocks a
+// tile where HBM would allow 1,470 (trees of up to 16 nodes, 64 query heads, 32 lanes of up to 8,001 rows: 139 us).
+// Below some thousand rows the chain of one unit: 8.6 us for a lane of 300.
 //
 // Roles: 8 or 16 warps of softmax, then
 //   four warps       the next unit's queries (split and laid out), a finished unit's output
@@ -101,14 +102,16 @@ constexpr int LANE_CACHE = 256;                  // lanes whose facts are kept i
 
 // Units of at most this many tiles are not cut between CTAs, and the join is not launched: a unit's tiles one after the other
 // take less than the join and its launch. Known on the host, from the rows that the page table can hold. (One token, 8 kv
-// heads of 128, us whole / cut: 300 rows 8.4 / 10.9 in one lane, 20.5 / 25.2 in 64; 1,000 rows 11.5 / 11.5 and 34.2 / 36.9;
-// 2,000 rows 16.8 / 14.0 and 57.3 / 55.0.)
+// heads of 128, us whole / cut: 300 rows 8.6 / 10.7 in one lane, 19.3 / 24.2 in 64; 1,000 rows 12 / 11.7 and 34.5 / 36.0;
+// 2,000 rows 18.0 / 14.0 and 57.0 / 54.8.)
 constexpr int WHOLE_TILES = 8;
 
-// A unit costs this many tiles beside its own: its queries, its first reference, its output (which grow with R). The parts
-// are cut evenly in tiles and unit costs (below four tiles a CTA in tiles alone: there the longest part counts). Measured with
-// 0, R / 8, R / 4: trees of up to 16 nodes, 64 rows a unit, 205, 138, 147 us; 64 uneven lanes, 16 rows a unit, 109, 106, 109 us.
-constexpr int FULL_COST = 4, HALF_COST = 3;       // of a tile; with half of the unit's tree rows at most, where halves are other warps'
+// The run's measure: what a tile costs, and a tile of which half the unit's tree rows are missing, where the halves are
+// different warps' (the cache is then read as fast, the softmax does half the work; 2, 3, 4: trees of up to 10 nodes 133, 115,
+// 120 us). A unit costs R / 8 tiles beside its own: its queries, its first reference, its output (0, R / 8, R / 4: trees of up to
+// 16 nodes 210, 139, 144 us; 64 uneven lanes of one token 112, 95, 96 us). The parts are cut evenly in this measure; below four
+// tiles a CTA in tiles alone, as there the longest part counts.
+constexpr int FULL_COST = 4, HALF_COST = 3;
 __host__ __device__ constexpr int unit_cost(int R) { return FULL_COST * R / 8; }
 
 // What the join needs, at the start of the workspace: for each CTA the unit that its part begins in.
@@ -1514,9 +1517,12 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     return e;
 }
 
-// The tile of tree rows: the smallest that takes a lane's rows of one kv head at once, else the largest. (Two groups
-// on one tile for twice the rows read the cache once where two units read it twice, but above 64 rows the softmax
-// bounds, not the reading: 3 % faster with 128 rows in every lane, 8 % slower with uneven trees.)
+// The tile of tree rows: the smallest that takes a lane's rows of one kv head at once, else the largest. Measured, us,
+// taken / the other: 4 rows, 64 lanes of up to 8,192 rows, 16 / 32: 95 / 106. 28 rows, two lanes of 131,072, 32 / 64:
+// 103 / 110. Up to 128 rows, 32 lanes of up to 8,001, 64 / 32: 139 / 164. Up to 64 rows at head_dim 64, 32 lanes of up
+// to 8,000, 64 / 32: 153 / 187 (nine lanes of up to 2,047, their trees uneven: 35 / 31). Two groups on one tile for
+// twice the rows read the cache once where two units read it twice, but above 64 rows the softmax
+// bounds, not the reading: 3 % faster with 128 rows in every lane, 8 % slower with uneven trees.
 template <int D>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
     const int64_t rows = (int64_t)(a.max_nodes < a.n_nodes ? a.max_nodes : a.n_nodes) * a.group;

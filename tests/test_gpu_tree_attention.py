@@ -156,6 +156,19 @@ def test_uneven_long_lanes():
     run_and_check(Case([(20000, 2), (5, 3), (9000, 1), (0, 1), (777, 8)], 8, 2, 128, 32, seed=3), heads=[0, 7])
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_long_lanes_whose_last_units_are_short(D):
+    # 72, 8, 24, 128 and 96 tree rows a kv head: full units, and ones of which most rows are missing
+    run_and_check(Case([(9000, 9), (6500, 1), (0, 3), (7300, 16), (8100, 12)], 16, 2, D, 32, seed=D), heads=[0, 7, 15])
+
+
+@pytest.mark.parametrize("nodes", [2, 9])
+def test_more_lanes_than_a_block_has_threads(nodes):
+    rng = np.random.RandomState(nodes)
+    lanes = [(int(rng.randint(0, 1500 if b % 50 == 0 else 150)), int(rng.randint(0, nodes + 1))) for b in range(900)]
+    run_and_check(Case(lanes, 8, 2, 64, 16, seed=nodes), heads=[0, 5], lanes=set(range(0, 900, 25)) | {899})
+
+
 def test_nodes_that_see_nothing():
     c = Case([(0, 4), (0, 1), (200, 3), (0, 40)], 4, 2, 128, 16, seed=2)
     c.mask[1] = 0                         # of the first lane
