@@ -45,7 +45,7 @@
 // What bounds it (measured, a call's whole time; head_dim 128, 8 kv heads, 2,064 bytes of cache a row): up to 32 tree
 // rows HBM: one token in 64 lanes of uneven lengths up to 8,192 rows 95 us (543 MB, 5.7 TB/s; even lengths 6.4 TB/s,
 // head_dim 256 6.4, head_dim 64 4.1: there the copies' warp, 1,100 clocks a tile for four pages), a tree of 7 nodes in two
-// lanes of 131,072 rows 103 us (541 MB). Of the 95 us the tile loop takes 78, the cut 4, the first tile 4, the last
+// lanes of 131,072 rows 100 us (541 MB). Of the 95 us the tile loop takes 78, the cut 4, the first tile 4, the last
 // outputs, the join and its launch 6. With 64 tree rows the softmax's instructions and their latency: 2,200 clocks a
 // tile where HBM would allow 1,470 (trees of up to 16 nodes, 64 query heads, 32 lanes of up to 8,001 rows: 139 us).
 // Below some thousand rows the chain of one unit: 8.6 us for a lane of 300.
@@ -217,6 +217,11 @@ MOE_DEV float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+MOE_DEV float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 typedef unsigned long long f32x2;
 MOE_DEV f32x2 pack2(float a, float b) {
@@ -679,8 +684,9 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             const int live = ln.n * G - row0;        // how many of them there are (more than RH: all; none or less: none)
             float ev_most = -INFINITY;               // largest value exponent seen so far
             bool set = true;                         // the reference is to be set (a part's first tile)
-            for (int t = w.t; t < w.t + nt; ++t, ++i) {
-                if ((int)(i & 1) != g) continue;
+            const uint32_t i1 = i + nt;              // the part's tiles are taken in turn by the two groups
+            int t = w.t + (int)((i ^ (uint32_t)g) & 1);
+            for (i += (i ^ (uint32_t)g) & 1; i < i1; i += 2, t += 2) {
                 if (C::HALVES > 1 && live <= 0) {    // the last unit of a lane: its first half has all the rows
                     const int sc = (int)(i % NSC);
                     if (!warp_wait_at(bar(C::B_SCFULL, sc), (i / NSC) & 1, stop)) { ok = false; break; }
@@ -811,7 +817,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                         y[q] = add2(y[q], o.x);
                         y[q + 1] = add2(y[q + 1], o.y);
                         const float2 s0 = unpack2(y[q]), s1 = unpack2(y[q + 1]);
-                        top = fmaxf(top, fmaxf(fmaxf(s0.x, s0.y), fmaxf(s1.x, s1.y)));
+                        top = max3(max3(top, s0.x, s0.y), s1.x, s1.y);
                     }
                     if (!setting) {
                         const bool over = __any_sync(0xFFFFFFFFu, top > P_EXP_MAX);
@@ -908,6 +914,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                 ++k;
             }
             if (!ok) break;
+            i = i1;
             // the part's sums over this group's rows
             if (piece > 0 && !warp_wait_at(bar(C::B_LFREE), (piece - 1) & 1, stop)) break;
             float v[RH];
@@ -1519,7 +1526,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
 
 // The tile of tree rows: the smallest that takes a lane's rows of one kv head at once, else the largest. Measured, us,
 // taken / the other: 4 rows, 64 lanes of up to 8,192 rows, 16 / 32: 95 / 106. 28 rows, two lanes of 131,072, 32 / 64:
-// 103 / 110. Up to 128 rows, 32 lanes of up to 8,001, 64 / 32: 139 / 164. Up to 64 rows at head_dim 64, 32 lanes of up
+// 100 / 110. Up to 128 rows, 32 lanes of up to 8,001, 64 / 32: 139 / 164. Up to 64 rows at head_dim 64, 32 lanes of up
 // to 8,000, 64 / 32: 153 / 187 (nine lanes of up to 2,047, their trees uneven: 35 / 31). Two groups on one tile for
 // twice the rows read the cache once where two units read it twice, but above 64 rows the softmax
 // bounds, not the reading: 3 % faster with 128 rows in every lane, 8 % slower with uneven trees.
