@@ -1100,7 +1100,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                 const float M0 = F[C::F_M + u], M1 = F[C::F_M + R + u], M = fmaxf(M0, M1);
                 float f0 = M0 == -INFINITY ? 0.0f : ex2(M0 - M), f1 = M1 == -INFINITY ? 0.0f : ex2(M1 - M);
                 const float L = sum(0) * f0 + sum(1) * f1;            // sums may be NaN
-                const int node = (row0 + u) / G, row = node * a.n_q_heads + row0 + u - node * G;      // of the lane and kv head
+                const int node = (row0 + u) / G, row = node * a.n_q_heads + row0 + u - node * G;      // of the lane and kv head: 2^26 at most
                 if (whole) {
                     // out = O / L; lse = ln 2 (M - 6 + log2 L): p carries 2^6
                     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
@@ -1115,7 +1115,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                 // a group without a tile has no O: what lies there is read, and cleared below
                 st[u] = f0;
                 st[R + u] = f1;
-                place[u] = row * D;
+                place[u] = row;                  // in vectors of D: the offset in values can pass 32 bits
             }
             __syncwarp();
             if (lane == 0) arrive_at(bar(C::B_LFREE));
@@ -1138,7 +1138,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                         for (int e = 0; e < 4; ++e) {
                             const float x = (has0 ? __uint_as_float(o0[q + e]) * g0[e] : 0.0f) + (has1 ? __uint_as_float(o1[q + e]) * g1[e] : 0.0f);
                             if (!on || c0 + q + e >= rows) continue;
-                            if (whole) out[to[e] + m * 128] = __float2bfloat16_rn(x);
+                            if (whole) out[(int64_t)to[e] * D + m * 128] = __float2bfloat16_rn(x);
                             else part[(c0 + q + e) * D + m * 128 + d0] = x;
                         }
                     }
