@@ -7,22 +7,24 @@
 // as they lie in the cache (tcgen05 kind::f8f6f4, fp32 accumulators in TMEM):
 // no byte of the cache is converted or scaled outside the MMA, so TMA moves it
 // from HBM to the operand buffers untouched.
-//   - The other operand is split in two 8-bit parts. A bf16 query has 8
+//   - The other operand is split in 8-bit parts. A bf16 query has 8
 //     significant bits and e4m3 has 4: with its row scaled by a power of two to
 //     128 <= max|q| < 256, hi = e4m3(q), lo = e4m3(q - hi) hold it exactly down
 //     to 2^-9 of the row's maximum and within 2^-17 of the maximum below.
-//   - A probability p is hi + lo too, with 8 significant bits as bf16 would
-//     have: hi = e5m2(p), which is the upper byte of p in fp16 (rounded by an
-//     integer add), lo = e4m3 of the rest.
+//   - A probability p, rounded to fp16, is the sum of three e5m2: an e5m2 is the upper byte of an fp16, so hi is that
+//     byte of p, mid that of p - hi (rounded by an integer add), lo that of the rest. Together 10 significant bits,
+//     as long as lo's smallest, 2^-16, allows.
 //   - The scale of a key row multiplies its column of scores; the scale of a
-//     value row is added to the exponent: s' = s + ev_j, p = 2^(s' - m + 6), so
-//     values of any size keep their precision; the sum of weights gets p 2^-ev_j.
+//     value row is added to the exponent: s' = s + ev_j, p = 2^(s' - m + 11), so
+//     values of any size keep their precision; the sum of weights gets p 2^-ev_j (and 2^-16, for its range).
 //   - m is a running reference, not each tile's maximum: it is the maximum of s'
-//     when it is set, and stays until a score passes it by 5.5 (p = 2^11.5 would pass what
-//     lo can hold); then it is set again and what has been added up is scaled down. Most tiles
+//     when it is set, and stays until a score passes it by 4.9 (p = 2^15.9; fp16 ends at 2^16);
+//     then it is set again and what has been added up is scaled down. Most tiles
 //     so need no maximum at all: one compare, a vote, no reduction over the rows.
-//     Weights below 2^-23 of the largest are dropped, the rest keep at least the 3 bits of
-//     hi, rounded to nearest.
+//     A weight (2^s') is held to 2^-9 of itself, or to 2^-28 of the largest: weights that are small but many keep
+//     their share, 2^17 of one size to 2^-11 of the peak above them. (Two parts, e5m2 and e4m3, reach 2^-9 of a weight
+//     only down to 2^-8 of the largest, and equal weights below round the same way: up to 11 % of a tail's share was
+//     lost.)
 // Scores, sums, the accumulators O and the parts that the join adds up are fp32; the output is rounded to bf16 once.
 //
 // Orientation: cache rows are the MMA's M (128), tree rows its N, so a single
@@ -149,9 +151,9 @@ struct Cfg {
     static constexpr int SLOT = TILE * D;
     static constexpr int QROWS = 2 * R;                       // hi, then lo
     static constexpr int QBUF = QROWS * D;
-    static constexpr int PBUF = 2 * TILE * R;
+    static constexpr int PBUF = 3 * TILE * R;                 // hi, mid, lo
     static constexpr int SB = 4;                              // buffers of S
-    static constexpr int NS = D == 64 ? 16 : D == 256 ? 5 : R == 64 ? 8 : R == 32 ? 11 : 12;      // ring of key and value tiles: what fits
+    static constexpr int NS = D == 64 ? 16 : D == 256 ? (R == 32 ? 4 : 5) : R == 64 ? 7 : R == 32 ? 10 : 12;     // ring of key and value tiles: what fits
     static constexpr int SA = 8;                              // tiles that scales are under way ahead, and page ids another as many
     static constexpr int PT = 8;                              // tiles that the page ids of keys and values are under way ahead
     static constexpr int NSC = 2 * SA;                        // ring of the rows' scales:
@@ -200,16 +202,25 @@ struct Cfg {
     static constexpr int SMEM = OFF_MISC + 16 + 128 + 1024;
     // Tiles whose S may be under way: the buffers, and (an odd ring) not past a slot whose values are still to be used
     static constexpr int LOOK = NS % 2 && NS / 2 + 1 < SB ? NS / 2 + 1 : SB;
-    static constexpr int TMEM_O = 4 * R;                      // after S (4 R columns): O [group][unit parity][MB][R]
-    static constexpr int TMEM_USED = 4 * R + 4 * R * MB;
+    // O of the three parts of P in columns of their own where TMEM has room (they are added up with the output): one MMA of
+    // N = 3 R takes 32 rows, not three of N = R (us, so / three: one token in 64 uneven lanes 94.7 / 103.2, a tree of 7 nodes
+    // in two lanes of 131,072 rows 100.8 / 107.9).
+    static constexpr int PARTS = 4 * R + 4 * R * MB * 3 <= 512 ? 3 : 1;
+    static constexpr int OC = PARTS * R;                      // columns of one O block
+    static constexpr int TMEM_O = 4 * R;                      // after S (4 R columns): O [group][unit parity][MB][PARTS][R]
+    static constexpr int TMEM_USED = 4 * R + 4 * OC * MB;
     static constexpr int TMEM_COLS = TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
     static_assert(TMEM_USED <= 512 && SMEM <= 227 * 1024, "TMEM, shared memory");
     static_assert(OFF_F % 16 == 0 && OFF_SCAN % 8 == 0 && OFF_BAR % 8 == 0 && OFF_MISC % 16 == 0, "alignment");
     static_assert(R == 16 || R == 32 || R == 64, "R");
 };
 
-constexpr float P_EXP = 6.0f;                    // p = 2^6 at the reference
-constexpr float P_EXP_MAX = 11.5f;               // above it, lo = e4m3(p - hi) could pass 448
+constexpr float P_EXP = 11.0f;                   // p = 2^11 at the reference
+constexpr float P_EXP_MAX = 15.9f;               // below fp16's largest, 65,504
+// The sums of weights hold 2^(s - m + P_EXP - L_EXP), with value exponents of -100 to 120 in m: 2^99 at most for a row (so 2^28
+// rows do not overflow), 2^-125 for the largest weight at least. An exponential of its own is taken 2^26 larger, as
+// ex2 has no subnormal results.
+constexpr int L_EXP = 16, L_OWN = 26;
 
 // ------------------------------------------------------------------ small device pieces
 
@@ -341,6 +352,9 @@ __host__ __device__ constexpr uint32_t idesc_f8(int m, int n, int a_mn, int b_mn
            ((uint32_t)(m >> 4) << 24);
 }
 
+// 2^p down to the smallest subnormal, 2^-149.
+MOE_DEV float exp2_whole(int p) { return p >= -126 ? exp2_int(p) : __uint_as_float(p >= -149 ? 1u << (p + 149) : 0u); }
+
 // One lane of the (converged) warp.
 MOE_DEV bool elect_one() {
     uint32_t p;
@@ -380,11 +394,12 @@ MOE_DEV void tc_load(uint32_t taddr, uint32_t (&r)[32]) {
         : "memory");
 }
 
-// Shared-memory matrix descriptor without its address: swizzle 2 = 128 B, 4 = 64 B, 6 = 32 B, 0 = none; `group` =
-// bytes from one group of eight rows (of the strided axis) to the next. Every operand here is one
-// atom wide on its contiguous axis, so the group stride is the only one in use: both offset fields hold it.
-__host__ __device__ constexpr uint64_t desc_base(int swizzle, int group) {
-    return ((uint64_t)(group >> 4) << 16) | ((uint64_t)(group >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)swizzle << 61);
+// Shared-memory matrix descriptor without its address: swizzle 2 = 128 B, 4 = 64 B, 6 = 32 B, 0 = none; the two
+// strides in bytes. With a swizzle `lead` is from one atom of the contiguous axis to the next and `group` from one group of
+// eight rows (of the strided axis) to the next, without one the other way round. Operands that are one atom wide on
+// their contiguous axis hold the group stride in both.
+__host__ __device__ constexpr uint64_t desc_base(int swizzle, int lead, int group) {
+    return ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(group >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)swizzle << 61);
 }
 MOE_DEV uint64_t desc_at(uint64_t base, uint32_t saddr) { return base + (uint64_t)(saddr >> 4); }   // below 256 KB: no carry
 
@@ -830,8 +845,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                     if (k > 0 && !warp_wait_at(bar(C::B_PFREE, g), (k - 1) & 1, stop)) { ok = false; break; }
                     if (setting && !set) {           // what has been added up is scaled down to the new reference
                         tc_fence_after();
-                        const uint32_t orow = tmem + ((uint32_t)(wl * 32) << 16) + C::TMEM_O + (g * 2 + (piece & 1)) * C::MB * R + h * RH;
-                        for (int c0 = 0; c0 < C::MB * RH; c0 += 8) {
+                        const uint32_t orow = tmem + ((uint32_t)(wl * 32) << 16) + C::TMEM_O + (g * 2 + (piece & 1)) * C::MB * C::OC + h * RH;
+                        for (int c0 = 0; c0 < C::MB * C::PARTS * RH; c0 += 8) {
                             const uint32_t at = orow + (c0 / RH) * R + c0 % RH;
                             uint32_t o[8];
                             tc_ld_x8(at, o);
@@ -848,30 +863,34 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
 #pragma unroll
                     for (int c0 = 0; c0 < RH; c0 += 16) {
                         if (c0 >= live) break;       // what P then holds there becomes columns of O that nobody reads
-                        uint32_t hi[4], lo[4];
+                        uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            uint32_t up[2];
-                            __nv_fp8x2_storage_t l8[2];
+                            uint32_t a2[2], b2[2], c2[2];
 #pragma unroll
                             for (int z = 0; z < 2; ++z) {
                                 f32x2& e = y[c0 / 2 + 2 * q + z];
                                 const float2 s = unpack2(e);
                                 const float p0 = ex2(s.x), p1 = ex2(s.y);
                                 if (!wide) e = pack2(p0, p1);
+                                auto bits = [](__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); };
+                                auto halves = [](uint32_t x) { return *reinterpret_cast<const __half2*>(&x); };
+                                // hi is cut off (NaN, 0x7FFF, stays NaN), the rests are exact, mid and lo rounded to
+                                // nearest. No sum carries out of its half.
                                 const __half2 ph = __floats2half2_rn(p0, p1);
-                                // p rounded to the upper byte of its fp16 pattern (p <= 2900: no carry out of it; NaN
-                                // stays in the rest), and the exact rest
-                                up[z] = (*reinterpret_cast<const uint32_t*>(&ph) + 0x00800080u) & 0xFF00FF00u;
-                                l8[z] = __nv_cvt_halfraw2_to_fp8x2(__hsub2(ph, *reinterpret_cast<const __half2*>(&up[z])),
-                                                                   __NV_SATFINITE, __NV_E4M3);
+                                a2[z] = bits(ph);
+                                const __half2 r1 = __hsub2(ph, halves(a2[z] & 0xFF00FF00u));
+                                b2[z] = bits(r1) + 0x00800080u;
+                                c2[z] = bits(__hsub2(r1, halves(b2[z] & 0xFF00FF00u))) + 0x00800080u;
                             }
-                            hi[q] = __byte_perm(up[0], up[1], 0x7531);
-                            lo[q] = (uint32_t)l8[0] | ((uint32_t)l8[1] << 16);
+                            hi[q] = __byte_perm(a2[0], a2[1], 0x7531);
+                            mid[q] = __byte_perm(b2[0], b2[1], 0x7531);
+                            lo[q] = __byte_perm(c2[0], c2[1], 0x7531);
                         }
                         uint8_t* at = P + (((h * (RH / 16) + c0 / 16) ^ swz) << 4);
                         *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4*>(at + TILE * R) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        *reinterpret_cast<uint4*>(at + TILE * R) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                        *reinterpret_cast<uint4*>(at + 2 * TILE * R) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                     if (setting) break;
                     if (!warp_wait_at(bar(C::B_VOTE, wg), polls & 1, stop)) { ok = false; break; }
@@ -899,14 +918,15 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                 __syncwarp();
                 if (lane == 0) arrive_at(bar(C::B_PFULL, g));
                 if (wide) {
-                    const float evf = (float)evi;
+                    const float evf = (float)(evi - (L_OWN - L_EXP)), wj = exp2_int(-L_OWN);
+                    const f32x2 wj2 = pack2(wj, wj);
 #pragma unroll
                     for (int q = 0; q < RH / 2; ++q) {
                         const float2 s = unpack2(y[q]);
-                        l2[q] = add2(l2[q], pack2(ex2(s.x - evf), ex2(s.y - evf)));
+                        l2[q] = fma2(pack2(ex2(s.x - evf), ex2(s.y - evf)), wj2, l2[q]);
                     }
                 } else {
-                    const float wj = exp2_int(-evi);
+                    const float wj = exp2_whole(-evi - L_EXP);
                     const f32x2 wj2 = pack2(wj, wj);
 #pragma unroll
                     for (int q = 0; q < RH / 2; ++q) l2[q] = fma2(y[q], wj2, l2[q]);
@@ -1102,12 +1122,12 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                 const float L = sum(0) * f0 + sum(1) * f1;            // sums may be NaN
                 const int node = (row0 + u) / G, row = node * a.n_q_heads + row0 + u - node * G;      // of the lane and kv head: 2^26 at most
                 if (whole) {
-                    // out = O / L; lse = ln 2 (M - 6 + log2 L): p carries 2^6
-                    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+                    // out = O / (L 2^L_EXP); lse = ln 2 (M - P_EXP + L_EXP + log2 L): p carries 2^P_EXP, L 2^-L_EXP
+                    const float inv = L == 0.0f ? 0.0f : exp2_int(-L_EXP) / L;
                     f0 *= inv;
                     f1 *= inv;
                     if (wl == 0 && a.lse && u < rows)
-                        a.lse[(int64_t)n0 * a.n_q_heads + w.h * G + row] = L == 0.0f ? -INFINITY : (M - P_EXP + log2f(L)) * 0.69314718055994531f;
+                        a.lse[(int64_t)n0 * a.n_q_heads + w.h * G + row] = L == 0.0f ? -INFINITY : (M - (P_EXP - L_EXP) + log2f(L)) * 0.69314718055994531f;
                 } else if (wl == 0 && u < rows) {
                     part[R * D + u] = M;
                     part[R * D + R + u] = L;
@@ -1120,14 +1140,26 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             __syncwarp();
             if (lane == 0) arrive_at(bar(C::B_LFREE));
             __nv_bfloat16* out = a.out + ((int64_t)n0 * a.n_q_heads + w.h * G) * D + d0;
-            const uint32_t orow = tmem + ((uint32_t)(wl * 32) << 16) + C::TMEM_O + ob * C::MB * R;
+            const uint32_t orow = tmem + ((uint32_t)(wl * 32) << 16) + C::TMEM_O + ob * C::MB * C::OC;
             for (int c0 = 0; c0 < rows; c0 += 16) {
 #pragma unroll
                 for (int m = 0; m < C::MB; ++m) {
                     uint32_t o0[16], o1[16];
-                    tc_ld_x16(orow + m * R + c0, o0);
-                    tc_ld_x16(orow + (2 * C::MB + m) * R + c0, o1);
+                    tc_ld_x16(orow + m * C::OC + c0, o0);
+                    tc_ld_x16(orow + (2 * C::MB + m) * C::OC + c0, o1);
                     tc_wait_ld();
+#pragma unroll
+                    for (int z = 1; z < C::PARTS; ++z) {
+                        uint32_t x0[16], x1[16];
+                        tc_ld_x16(orow + m * C::OC + z * R + c0, x0);
+                        tc_ld_x16(orow + (2 * C::MB + m) * C::OC + z * R + c0, x1);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            o0[q] = __float_as_uint(__uint_as_float(o0[q]) + __uint_as_float(x0[q]));
+                            o1[q] = __float_as_uint(__uint_as_float(o1[q]) + __uint_as_float(x1[q]));
+                        }
+                    }
 #pragma unroll
                     for (int q = 0; q < 16; q += 4) {
                         const float4 f0 = *reinterpret_cast<const float4*>(st + c0 + q), f1 = *reinterpret_cast<const float4*>(st + R + c0 + q);
@@ -1221,10 +1253,12 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             // -------------------------------------------------------- MMA issue. The loop is uniform over the warp and one elected
             // lane issues, so that descriptors stay in uniform registers (39 clocks an MMA of N = 16 against 120
             // from a loop that one lane runs).
-            constexpr uint64_t KD = desc_base(C::ROWB == 128 ? 2 : 4, 8 * C::ROWB);       // K, Q (along K) and V (along M): one atom, 8 rows
-            constexpr uint64_t PD = desc_base(R == 64 ? 4 : R == 32 ? 6 : 0, 8 * R);
+            constexpr uint64_t KD = desc_base(C::ROWB == 128 ? 2 : 4, 8 * C::ROWB, 8 * C::ROWB);       // K, Q (along K) and V (along M): one atom, 8 rows
+            // P: 8 R bytes from eight cache rows to the next, TILE R from hi to mid to lo. (Without a swizzle the strides of
+            // the contiguous axis and of the groups stand in each other's fields.)
+            constexpr uint64_t PD = R == 16 ? desc_base(0, 8 * R, TILE * R) : desc_base(R == 64 ? 4 : 6, TILE * R, 8 * R);
             constexpr uint32_t ID_S = idesc_f8(128, R, 0, 0, 0);
-            constexpr uint32_t ID_HI = idesc_f8(D < 128 ? 64 : 128, R, 1, 1, 1), ID_LO = idesc_f8(D < 128 ? 64 : 128, R, 1, 1, 0);
+            constexpr uint32_t ID_PV = idesc_f8(D < 128 ? 64 : 128, C::OC, 1, 1, 1);
             const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             const uint64_t ring = desc_at(KD, smem_u32(smem + C::OFF_RING));
             const uint64_t qd = desc_at(KD, smem_u32(smem + C::OFF_Q)), pd = desc_at(PD, smem_u32(smem + C::OFF_P));
@@ -1252,15 +1286,15 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             auto pv = [&](uint32_t n, uint32_t part, bool fresh, bool ends) {
                 const uint32_t g = n & 1, s = (2 * n + 1) % NS;
                 const uint64_t vd = ring + (uint64_t)(s * (C::SLOT >> 4)), p = pd + (uint64_t)(g * (C::PBUF >> 4));
-                const uint32_t o = tm + C::TMEM_O + (g * 2 + (part & 1)) * C::MB * R;
+                const uint32_t o = tm + C::TMEM_O + (g * 2 + (part & 1)) * C::MB * C::OC;
                 const uint32_t add = fresh ? 0u : 1u;
                 if (elect_one()) {
 #pragma unroll
                     for (int m = 0; m < C::MB; ++m)
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)                 // four steps of 32 rows with hi, four with lo
-                            tc_mma_f8(o + m * R, vd + ((m * C::PANEL + (kk & 3) * 32 * C::ROWB) >> 4),
-                                      p + (((kk >> 2) * TILE * R + (kk & 3) * 32 * R) >> 4), kk < 4 ? ID_HI : ID_LO, kk ? 1u : add);
+                        for (int kk = 0; kk < 12 / C::PARTS; ++kk)     // four steps of 32 rows; with hi, with mid and with lo
+                            tc_mma_f8(o + m * C::OC, vd + ((m * C::PANEL + (kk & 3) * 32 * C::ROWB) >> 4),
+                                      p + (((kk >> 2) * TILE * R + (kk & 3) * 32 * R) >> 4), ID_PV, kk ? 1u : add);
                     commit_at(bar(C::B_EMPTY, s));
                     commit_at(bar(C::B_PFREE, g));
                     if (ends) commit_at(bar(C::B_OFULL, part & 1));
@@ -1456,12 +1490,12 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_attention_join(const Att
         }
         M = Mn;
     }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    const float inv = L == 0.0f ? 0.0f : exp2_int(-L_EXP) / L;
     const int tr = u.row0 + r, node = tr / a.group;
     const int64_t at = (int64_t)(u.node0 + node) * a.n_q_heads + u.head * a.group + tr - node * a.group;
 #pragma unroll
     for (int e = 0; e < V; ++e) a.out[at * D + e * 32 + lane] = __float2bfloat16_rn(acc[e] * inv);
-    if (a.lse && lane == 0) a.lse[at] = L == 0.0f ? -INFINITY : (M - P_EXP + log2f(L)) * 0.69314718055994531f;
+    if (a.lse && lane == 0) a.lse[at] = L == 0.0f ? -INFINITY : (M - (P_EXP - L_EXP) + log2f(L)) * 0.69314718055994531f;
 }
 
 // ------------------------------------------------------------------ host side

@@ -1,0 +1,116 @@
+"""Weights of tree attention far below the largest, value vectors of zeros and of very different size, against the
+definition in 64 bits.
+
+Bounds. A weight is held to 2^-9 of itself, or to 2^-28 of the largest weight times its value vector's scale, whichever
+is more; the scores and the sums are fp32 (2^-11 of the weights covers their roundings, and the queries'), and the
+output is rounded to bf16 once (half a unit: 2^-9). So
+  |out - o| <= 2^-9 |o| + (2^-9 + 2^-11) sum p |v| + 2^-28 max(p 2^ev) sum |codes|,
+each column for itself. A log sum is off by the rounding of the scores and the scale exponents that are
+added to them (at most 2^7: 2^-17 each) and a few 2^-22.
+"""
+import numpy as np
+import pytest
+import torch
+
+from tests import kv_reference as ref
+from tests.test_gpu_tree_attention import Case
+
+pytestmark = pytest.mark.gpu
+
+moe = pytest.importorskip("resident_expert_routed_gb300")
+
+
+def definition(q, k, codes, scales, see, scale):
+    """(out [n, D], lse [n], tolerance [n, D]) of one lane and head: q [n, D], k [L, D] values, codes and scales of v."""
+    v, unit = ref.values(codes, scales), 2.0 ** (scales.astype(np.float64) - 127)
+    c = np.abs(ref.E4M3[codes])
+    out, lse, tol = np.zeros(q.shape), np.full(len(q), -np.inf), np.zeros(q.shape)
+    for t in range(len(q)):
+        j = np.flatnonzero(see[t])
+        if not len(j):
+            continue
+        s = k[j] @ q[t] * scale
+        p = np.exp(s - s.max())
+        total = p.sum()
+        held = c[j].any(-1)                   # a vector of zeros adds to the sum of weights alone
+        most = (p * unit[j])[held].max(initial=0.0)
+        out[t], lse[t] = p @ v[j] / total, s.max() + np.log(total)
+        tol[t] = 2.0 ** -9 * np.abs(out[t]) + ((2.0 ** -9 + 2.0 ** -11) * (p @ np.abs(v[j])) + 2.0 ** -28 * most * c[j].sum(0)) / total
+    return out, lse, tol
+
+
+def check(c, got, lse, lanes=None):
+    k = ref.values(*c.pool[:2])
+    G = c.Hq // c.Hkv
+    for b, (p, n) in enumerate(c.lanes):
+        if lanes is not None and b not in lanes:
+            continue
+        see = ref.visible(n, p + n, c.mask, c.cu[b])
+        kb, codes, scales = (ref.lane_rows(x, c.table[b], p + n) for x in (k, *c.pool[2:]))
+        rows = slice(c.cu[b], c.cu[b + 1])
+        for h in range(c.Hq):
+            o, e, tol = definition(c.q_host[rows, h], kb[:, h // G], codes[:, h // G], scales[:, h // G], see, c.scale)
+            off = np.abs(got[rows, h] - o)
+            assert (off <= tol).all(), (b, h, float((off / np.maximum(tol, 1e-300)).max()))
+            none = np.isneginf(e)
+            assert np.array_equal(np.isneginf(lse[rows, h]), none)
+            mags = np.abs(c.q_host[rows, h]) @ np.abs(kb[:, h // G]).max(0) * c.scale
+            bound = 2.0 ** -16 + 2.0 ** -20 * np.abs(e[~none]) + c.D * 2.0 ** -24 * mags[~none]
+            assert (np.abs(lse[rows, h] - e)[~none] <= bound).all(), (b, h, np.abs(lse[rows, h] - e)[~none].max())
+    assert moe.moe_device_status() == (moe.MOE_OK, 0)
+
+
+# ------------------------------------------------------------------ small weights of one size
+
+@pytest.mark.parametrize("bits", [4.3, 8.9, 12.84, 13.5, 15.84, 16.3, 18.55])
+@pytest.mark.parametrize("D,G,nodes", [(128, 1, 1), (128, 4, 6), (128, 8, 8), (64, 8, 8), (256, 4, 7)])
+def test_a_flat_tail_below_a_peak(bits, D, G, nodes):
+    """Two peaks (one for each half of the work on a lane's tiles) before 8,190 rows of one weight each, 2^-bits of a
+    peak's; the tail's values have a column of their own. The tail's rows are one page, again and again."""
+    H, page, rows, lanes = 8, 128, 8192, 20
+    rng = np.random.RandomState(1)
+    kc = np.full((3, H, page, D), 0x38, np.uint8)                        # keys of ones, times 2^-8; a peak's are 2^-7
+    ks = np.full((3, H, page), 127 - 8, np.uint8)
+    ks[:2, :, 0] += 1
+    vc, vs = np.empty_like(kc), np.empty_like(ks)
+    x = rng.randn(3, H, page, D)
+    x[:, :, :, 0], x[:, :, :, 1] = 1.0, 0.0
+    x[:2, :, 0, 0], x[:2, :, 0, 1] = 0.0, 1.0
+    for i in range(3):
+        vc[i], vs[i] = ref.quantise(x[i])
+    table = np.full((lanes, rows // page), 2, np.int32)
+    table[:, 0], table[:, 1] = 0, 1
+    n, Hq = lanes * nodes, G * H
+    cu = np.arange(lanes + 1, dtype=np.int32) * nodes
+    mask = np.tile((1 << np.arange(nodes, dtype=np.int64)).astype(np.int32), lanes)[:, None]       # its own row, no other node's
+    scale = float(bits * np.log(2.0) / (D * 2.0 ** -8))
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    cache = moe.KvCache(dev(kc), dev(vc), dev(ks), dev(vs))
+    q = torch.ones((n, Hq, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.full((n, Hq, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((n, Hq), device="cuda")
+    ws = torch.empty(moe.moe_tree_attention_workspace_bytes(n, Hq, H, D, lanes), dtype=torch.uint8, device="cuda")
+    moe.moe_tree_attention(q, cache, dev(table), torch.full((lanes,), rows, dtype=torch.int32, device="cuda"), dev(cu), nodes, dev(mask),
+                           scale, out, ws, lse=lse)
+    got, gl = out.double().cpu().numpy().reshape(lanes, nodes, H, G, D), lse.double().cpu().numpy().reshape(lanes, nodes, H, G)
+    assert moe.moe_device_status() == (moe.MOE_OK, 0)
+    at, k = np.arange(rows), ref.values(kc, ks)
+    see = np.ones((nodes, rows), bool)
+    see[:, rows - nodes:] = np.eye(nodes, dtype=bool)
+    for h in range(H):
+        kl, cl, sl = (a[table[0, at // page], h, at % page] for a in (k, vc, vs))
+        o, e, tol = definition(np.ones((nodes, D)), kl, cl, sl, see, scale)
+        off = np.abs(got[:, :, h] - o[None, :, None, :])
+        assert (off <= tol[None, :, None, :]).all(), (h, float((off / tol[None, :, None, :]).max()))
+        # scores of up to 2^5: 2^-20 of them, and the tail's sum
+        assert (np.abs(gl[:, :, h] - e[None, :, None]) <= 2.0 ** -16 + 2.0 ** -20 * np.abs(e).max()).all()
+
+
+def test_a_value_row_that_is_large_in_one_column():
+    # the other columns hold what the small rows give, 2^13 below
+    c = Case([(900, 3), (300, 2)], 8, 2, 128, 32, seed=21)
+    for b, j in ((0, 5), (0, 700), (1, 290)):
+        page, at = c.row(b, j)
+        c.pool[2][page, :, at], c.pool[3][page, :, at] = 0, 127 + 6
+        c.pool[2][page, :, at, 17] = 0x78                                # 256
+    check(c, *c.gpu())
