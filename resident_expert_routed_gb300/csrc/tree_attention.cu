@@ -25,6 +25,9 @@
 //     their share, 2^17 of one size to 2^-11 of the peak above them. (Two parts, e5m2 and e4m3, reach 2^-9 of a weight
 //     only down to 2^-8 of the largest, and equal weights below round the same way: up to 11 % of a tail's share was
 //     lost.)
+//   - References hold a value exponent, so two of them can be 2^220 apart where the scores are not. The sum of weights,
+//     which holds the inverse, is taken from one to the other by the root of the factor, twice: 2^-220 is no
+//     fp32, its product with the sum is.
 // Scores, sums, the accumulators O and the parts that the join adds up are fp32; the output is rounded to bf16 once.
 //
 // Orientation: cache rows are the MMA's M (128), tree rows its N, so a single
@@ -167,7 +170,7 @@ struct Cfg {
     static constexpr int OFF_TID = OFF_SID + 2 * SA * 128;    // [PT][8]
     static constexpr int OFF_F = OFF_TID + PT * 32;           // floats from here
     static constexpr int F_O = 0;                             // [2 groups][R] P_EXP - m, as added to s'
-    static constexpr int F_AL = F_O + 2 * R;                  // [2][R] scale-down of what has been added up
+    static constexpr int F_AL = F_O + 2 * R;                  // [2][R] scale-down of what has been added up: its root
     static constexpr int F_WMAX = F_AL + 2 * R;               // [2 groups][HALVES][2][4 warps][RH]
     static constexpr int F_QF = F_WMAX + 16 * R;              // [4][R] 2^-a of the queries' rows
     static constexpr int F_QU = F_QF + 4 * R;                // [4][2] 2^-a of all rows of a unit; whether the rows' differ instead
@@ -818,12 +821,15 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                             const float Mn = fmaxf(M, m);
                             // a row that has seen nothing: the first score it sees passes any limit
                             off[lane] = Mn == -INFINITY ? 1e30f : P_EXP - Mn;
-                            alpha[lane] = M == -INFINITY ? 0.0f : ex2(M - Mn);
+                            alpha[lane] = M == -INFINITY ? 0.0f : ex2(0.5f * (M - Mn));
                             M = Mn;
                         }
                         __syncwarp();
 #pragma unroll
-                        for (int q = 0; q < RH / 2; ++q) l2[q] = mul2(l2[q], *reinterpret_cast<const f32x2*>(alpha + 2 * q));
+                        for (int q = 0; q < RH / 2; ++q) {
+                            const f32x2 al = *reinterpret_cast<const f32x2*>(alpha + 2 * q);
+                            l2[q] = mul2(mul2(l2[q], al), al);
+                        }
                     }
                     float top = -INFINITY;
 #pragma unroll
@@ -853,7 +859,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                             tc_wait_ld();
                             const float* al = alpha + c0 % RH;
 #pragma unroll
-                            for (int q = 0; q < 8; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * al[q]);
+                            for (int q = 0; q < 8; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * (al[q] * al[q]));
                             tc_st_x8(at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
                         }
                         tc_wait_st();
@@ -1118,8 +1124,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                     return (ls[0] + ls[R]) + (ls[2 * R] + ls[3 * R]);
                 };
                 const float M0 = F[C::F_M + u], M1 = F[C::F_M + R + u], M = fmaxf(M0, M1);
-                float f0 = M0 == -INFINITY ? 0.0f : ex2(M0 - M), f1 = M1 == -INFINITY ? 0.0f : ex2(M1 - M);
-                const float L = sum(0) * f0 + sum(1) * f1;            // sums may be NaN
+                float f0 = M0 == -INFINITY ? 0.0f : ex2(0.5f * (M0 - M)), f1 = M1 == -INFINITY ? 0.0f : ex2(0.5f * (M1 - M));
+                const float L = sum(0) * f0 * f0 + sum(1) * f1 * f1;  // sums may be NaN
+                f0 *= f0;
+                f1 *= f1;
                 const int node = (row0 + u) / G, row = node * a.n_q_heads + row0 + u - node * G;      // of the lane and kv head: 2^26 at most
                 if (whole) {
                     // out = O / (L 2^L_EXP); lse = ln 2 (M - P_EXP + L_EXP + log2 L): p carries 2^P_EXP, L 2^-L_EXP
@@ -1476,17 +1484,17 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_attention_join(const Att
             if (k0 + k > u.last) { m[k] = -INFINITY; l[k] = 0.0f; }
             Mn = fmaxf(Mn, m[k]);
         }
-        const float f0 = M == -INFINITY ? 0.0f : ex2(M - Mn);
-        L *= f0;
+        const float f0 = M == -INFINITY ? 0.0f : ex2(0.5f * (M - Mn));
+        L = L * f0 * f0;
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] *= f0;
+        for (int e = 0; e < V; ++e) acc[e] *= f0 * f0;
 #pragma unroll
         for (int k = 0; k < AT_ONCE; ++k) {
-            const float f = m[k] == -INFINITY ? 0.0f : ex2(m[k] - Mn);
-            L += f * l[k];                           // NaN stays, also with a weight of zero
+            const float f = m[k] == -INFINITY ? 0.0f : ex2(0.5f * (m[k] - Mn));
+            L += f * l[k] * f;                       // NaN stays, also with a weight of zero
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                if (k0 + k <= u.last) acc[e] += f * x[k][e];
+                if (k0 + k <= u.last) acc[e] += f * f * x[k][e];
         }
         M = Mn;
     }

@@ -114,3 +114,29 @@ def test_a_value_row_that_is_large_in_one_column():
         c.pool[2][page, :, at], c.pool[3][page, :, at] = 0, 127 + 6
         c.pool[2][page, :, at, 17] = 0x78                                # 256
     check(c, *c.gpu())
+
+
+# ------------------------------------------------------------------ value vectors of very different size
+
+@pytest.mark.parametrize("sizes", [(-91, 58), (58, -91), (-100, 120), (120, -100), (60, -70), (-70, 60)])
+@pytest.mark.parametrize("rows", [256, 700, 9000, 40000])
+def test_tiles_of_values_of_very_different_size(sizes, rows):
+    """Tiles of which all values are tiny before, after or between tiles of which all are huge: the tiny ones' weights
+    still count in full in the sum of weights."""
+    c = Case([(rows - 1, 1), (rows // 2, 1)], 2, 1, 128, 128, tree=False, seed=31)
+    for b, (p, n) in enumerate(c.lanes):
+        for t in range(-(-(p + n) // 128)):
+            c.pool[3][c.table[b, t]] = 127 + sizes[t // 2 % 2 if rows < 1000 else t * 4 // -(-rows // 128) % 2]
+            if max(sizes) == 120:
+                c.pool[2][c.table[b, t]] &= 0x9F                          # codes below 2^-3, so that values stay below 2^118
+    check(c, *c.gpu())
+
+
+@pytest.mark.parametrize("nodes,Hq", [(4, 4), (9, 8), (16, 8)])
+def test_a_few_huge_values_among_tiny_ones(nodes, Hq):
+    c = Case([(1500, nodes), (300, nodes)], Hq, 2, 64, 32, seed=32)
+    c.pool[3][:] = 127 - 95
+    for b, j in ((0, 3), (0, 1400), (1, 200)):
+        page, at = c.row(b, j)
+        c.pool[3][page, :, at] = 127 + 40
+    check(c, *c.gpu())
