@@ -479,7 +479,7 @@ moe_status moe_kv_keep(const moe_kv_cache* cache, const int32_t* page_table, int
  * exactly down to 2^-9 of the largest of its (node, head) row and to 2^-17 of
  * it below (to 2^-13 where a larger row is handled with it); a weight to 2^-9 of
  * itself, or to 2^-28 of the largest p[j] * 2^(scale byte of v[j] - 127) that
- * the node sees, whichever is more.
+ * the node sees (value vectors of zeros aside), whichever is more.
  * q bf16 [n_nodes, n_q_heads, head_dim], last axis contiguous, strides in
  * elements (multiples of 8), 16-byte aligned; query head h reads kv head
  * h / (n_q_heads / n_kv_heads). page_table int32 [lanes, table_width] (entries

@@ -25,6 +25,9 @@
 //     their share, 2^17 of one size to 2^-11 of the peak above them. (Two parts, e5m2 and e4m3, reach 2^-9 of a weight
 //     only down to 2^-8 of the largest, and equal weights below round the same way: up to 11 % of a tail's share was
 //     lost.)
+//   - A value vector of zeros has the scale 2^0 in the cache, far above those of ordinary values. Taken as it is it would
+//     raise m by 8 and more and cost the weights that count as many bits. Rows of that scale byte have their codes looked at,
+//     and zeros count as 2^-100: they add to the sum of weights and to nothing else.
 //   - References hold a value exponent, so two of them can be 2^220 apart where the scores are not. The sum of weights,
 //     which holds the inverse, is taken from one to the other by the root of the factor, twice: 2^-220 is no
 //     fp32, its product with the sum is.
@@ -160,7 +163,7 @@ struct Cfg {
     static constexpr int SA = 8;                              // tiles that scales are under way ahead, and page ids another as many
     static constexpr int PT = 8;                              // tiles that the page ids of keys and values are under way ahead
     static constexpr int NSC = 2 * SA;                        // ring of the rows' scales:
-    static constexpr int SC_BYTES = 2 * TILE + 16;            // key bytes, value bytes, largest and smallest value exponent
+    static constexpr int SC_BYTES = 2 * TILE + 16;            // key bytes, value bytes, largest and smallest value byte (int)
     static constexpr int MB = D == 256 ? 2 : 1;               // M blocks of O^T
     static constexpr int OFF_RING = 0;
     static constexpr int OFF_P = OFF_RING + NS * SLOT;
@@ -224,6 +227,10 @@ constexpr float P_EXP_MAX = 15.9f;               // below fp16's largest, 65,504
 // rows do not overflow), 2^-125 for the largest weight at least. An exponential of its own is taken 2^26 larger, as
 // ex2 has no subnormal results.
 constexpr int L_EXP = 16, L_OWN = 26;
+constexpr uint32_t ZERO_BYTE = 127u, LEAST_BYTE = 27u;      // scale bytes: of a vector of zeros, of the smallest vectors
+// A row's value scale this far (in binades) below the largest so far, or a row that may be one of zeros, is looked after. (p
+// ends at 2^-126: what the sum of weights could miss is 2^-37 of the largest weight.)
+constexpr int WIDE = 100, MAY_BE_ZERO = -1000;
 
 // ------------------------------------------------------------------ small device pieces
 
@@ -626,6 +633,17 @@ __device__ __noinline__ void tell_join(const AttnArgs& a, const int* facts, cons
     reinterpret_cast<JoinUnit*>(a.ws)[blockIdx.x] = u;
 }
 
+// Whether all codes of a value row in its ring slot are zeros. (A function of its own, as it is rare: its instructions within the
+// tile loop cost trees of up to 16 nodes 1 %.)
+template <int D, int ROWB, int PANEL>
+__device__ __noinline__ bool all_zero(const uint8_t* row) {
+    for (int q = 0; q < D / 16; ++q) {
+        const uint4 c = *reinterpret_cast<const uint4*>(row + q / (ROWB / 16) * PANEL + q % (ROWB / 16) * 16);
+        if ((c.x | c.y | c.z | c.w) & 0x7F7F7F7Fu) return false;
+    }
+    return true;
+}
+
 template <int D, int R>
 __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __grid_constant__ AttnMaps maps,
                                                                           const __grid_constant__ AttnArgs a) {
@@ -700,7 +718,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             const int len = ln.len, prefix = ln.len - ln.n;
             const int row0 = w.rt * R + h * RH;      // this warpgroup's tree rows in the lane
             const int live = ln.n * G - row0;        // how many of them there are (more than RH: all; none or less: none)
-            float ev_most = -INFINITY;               // largest value exponent seen so far
+            int ev_most = 0;                         // largest value scale byte so far
             bool set = true;                         // the reference is to be set (a part's first tile)
             const uint32_t i1 = i + nt;              // the part's tiles are taken in turn by the two groups
             int t = w.t + (int)((i ^ (uint32_t)g) & 1);
@@ -743,14 +761,27 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                 const int sc = (int)(i % NSC);
                 if (!warp_wait_at(bar(C::B_SCFULL, sc), (i / NSC) & 1, stop)) { ok = false; break; }
                 const uint8_t* scales = smem + C::OFF_SC + sc * C::SC_BYTES;
-                const uint32_t ks = scales[j], vs = scales[TILE + j];
-                const float2 range = *reinterpret_cast<const float2*>(scales + 2 * TILE);
+                const uint32_t ks = scales[j];
+                uint32_t vs = scales[TILE + j];
+                const int2 range = *reinterpret_cast<const int2*>(scales + 2 * TILE);
                 __syncwarp();
                 if (lane == 0) arrive_at(bar(C::B_SCEMPTY, sc));
-                // Value scales more than 2^104 apart: p could underflow in a row that matters to the sum of
-                // weights, p 2^-ev; its weight then gets an exponential of its own.
-                ev_most = fmaxf(ev_most, range.x);
-                const bool wide = ev_most > range.y + 104.0f;
+                ev_most = max(ev_most, range.x);
+                bool wide = false;
+                if (ev_most > range.y + WIDE) {
+                    if (__any_sync(0xFFFFFFFFu, vs == ZERO_BYTE && sees != 0u)) {
+                        // The values have arrived when their slot's fill is complete. The fill before it in the slot, which the
+                        // parity cannot tell from it, is one of a tile before this group's last or that tile itself.
+                        const uint32_t f = 2 * i + 1;
+                        if (k > 0 && !warp_wait_at(bar(C::B_PFREE, g), (k - 1) & 1, stop)) { ok = false; break; }
+                        if (!warp_wait_at(bar(C::B_FULL, f % NS), (f / NS) & 1, stop)) { ok = false; break; }
+                        if (vs == ZERO_BYTE && all_zero<D, C::ROWB, C::PANEL>(smem + C::OFF_RING + (f % NS) * C::SLOT + j * C::ROWB)) vs = LEAST_BYTE;
+                        __syncwarp();
+                    }
+                    // p could underflow in a row that matters to the sum of weights, p 2^-ev: the warp's weights then get an
+                    // exponential of their own.
+                    wide = __any_sync(0xFFFFFFFFu, sees != 0u && ev_most > (int)vs + WIDE);
+                }
                 const int evi = vs == 255u ? 0 : (int)vs - 127;       // a NaN row that is not seen weighs nothing
                 const float ev = vs == 255u ? __uint_as_float(0x7FC00000u) : (float)evi;
                 const f32x2 ev2 = pack2(ev, ev);
@@ -1397,8 +1428,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                         cp_async_4(dst, a.c.k_scales + row);
                         cp_async_4(dst + TILE, a.c.v_scales + row);
                     } else {
-                        write_at(dst, 0x7F7F7F7Fu);
-                        write_at(dst + TILE, 0x7F7F7F7Fu);
+                        write_at(dst, 0x01010101u * (ZERO_BYTE - 1));              // any scale but that of zeros
+                        write_at(dst + TILE, 0x01010101u * (ZERO_BYTE - 1));
                     }
                     return true;
                 };
@@ -1419,10 +1450,15 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                     if (d < 0) continue;
                     const uint32_t sc = (i + d) % NSC;
                     const uint32_t mine = read_at(sc0 + sc * C::SC_BYTES + TILE);
-                    const uint32_t hi = __vmaxu4(mine, mine >> 16), lo = __vminu4(mine, __byte_perm(mine, 0, 0x1032));
+                    const uint32_t hi = __vmaxu4(mine, mine >> 16);
+                    const uint32_t lo = __vminu4(mine, __byte_perm(mine, 0, 0x1032));
                     const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(hi & 255u, (hi >> 8) & 255u));
-                    const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, min(lo & 255u, (lo >> 8) & 255u));
-                    if (lane == 0) *reinterpret_cast<float2*>(smem + C::OFF_SC + sc * C::SC_BYTES + 2 * TILE) = make_float2((float)most, (float)least);
+                    uint32_t least = __reduce_min_sync(0xFFFFFFFFu, min(lo & 255u, (lo >> 8) & 255u));
+                    if (__any_sync(0xFFFFFFFFu, __vcmpeq4(mine, 0x01010101u * ZERO_BYTE) != 0u)) least = (uint32_t)MAY_BE_ZERO;
+                    if (lane == 0) {
+                        write_at(base + C::OFF_SC + sc * C::SC_BYTES + 2 * TILE, most);
+                        write_at(base + C::OFF_SC + sc * C::SC_BYTES + 2 * TILE + 4, least);
+                    }
                     __syncwarp();
                     if (lane == 0) arrive_at(bar(C::B_SCFULL, sc));
                 }

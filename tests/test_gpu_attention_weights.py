@@ -3,8 +3,8 @@ definition in 64 bits.
 
 Bounds. A weight is held to 2^-9 of itself, or to 2^-28 of the largest weight times its value vector's scale, whichever
 is more; the scores and the sums are fp32 (2^-11 of the weights covers their roundings, and the queries'), and the
-output is rounded to bf16 once (half a unit: 2^-9). So
-  |out - o| <= 2^-9 |o| + (2^-9 + 2^-11) sum p |v| + 2^-28 max(p 2^ev) sum |codes|,
+output is rounded to bf16 once (half a unit: 2^-9, and 2^-134 where bf16's steps end). So
+  |out - o| <= max(2^-9 |o|, 2^-134) + (2^-9 + 2^-11) sum p |v| + 2^-28 max(p 2^ev) sum |codes|,
 each column for itself. A log sum is off by the rounding of the scores and the scale exponents that are
 added to them (at most 2^7: 2^-17 each) and a few 2^-22.
 """
@@ -35,7 +35,7 @@ def definition(q, k, codes, scales, see, scale):
         held = c[j].any(-1)                   # a vector of zeros adds to the sum of weights alone
         most = (p * unit[j])[held].max(initial=0.0)
         out[t], lse[t] = p @ v[j] / total, s.max() + np.log(total)
-        tol[t] = 2.0 ** -9 * np.abs(out[t]) + ((2.0 ** -9 + 2.0 ** -11) * (p @ np.abs(v[j])) + 2.0 ** -28 * most * c[j].sum(0)) / total
+        tol[t] = np.maximum(2.0 ** -9 * np.abs(out[t]), 2.0 ** -134) + ((2.0 ** -9 + 2.0 ** -11) * (p @ np.abs(v[j])) + 2.0 ** -28 * most * c[j].sum(0)) / total
     return out, lse, tol
 
 
@@ -140,3 +140,88 @@ def test_a_few_huge_values_among_tiny_ones(nodes, Hq):
         page, at = c.row(b, j)
         c.pool[3][page, :, at] = 127 + 40
     check(c, *c.gpu())
+
+
+# ------------------------------------------------------------------ value vectors of zeros
+
+def zero_value(c, b, j, head=slice(None), code=0):
+    """As the cache holds a vector of zeros: codes 0 (or of the sign alone) and scale 2^0."""
+    page, at = c.row(b, j)
+    c.pool[2][page, head, at], c.pool[3][page, head, at] = code, 127
+
+
+@pytest.mark.parametrize("size", [0, -7, -16, -24, -90])
+@pytest.mark.parametrize("D,Hq,Hkv,nodes", [(128, 4, 2, 1), (64, 8, 4, 5), (128, 16, 2, 8), (256, 8, 2, 3)])
+def test_zero_value_rows(size, D, Hq, Hkv, nodes):
+    # values of size 2^size; rows of zeros first, in the middle of a tile, in one head alone, a whole tile, among the drafted nodes
+    c = Case([(700, nodes), (7, nodes), (130, nodes), (1900, nodes), (0, nodes)], Hq, Hkv, D, 32, seed=40 + D)
+    c.pool[3][:] = np.clip(c.pool[3].astype(int) + size, 27, 247)
+    for b, j in ((0, 0), (0, 77), (1, 3), (2, 129), (3, 1899), (4, 0)):
+        zero_value(c, b, j)
+    for j in range(256, 384):
+        zero_value(c, 3, j)
+    zero_value(c, 0, 400, head=0, code=0x80)
+    check(c, *c.gpu())
+
+
+@pytest.mark.parametrize("bits", [6.0, 14.0, 16.0, 22.5])
+@pytest.mark.parametrize("at", [0, 130, 511])
+def test_a_zero_value_with_the_highest_score(bits, at):
+    # most of the weight lies on a vector of zeros; what is left keeps its precision
+    c = Case([(511, 1)], 2, 1, 128, 64, tree=False, seed=50)
+    c.pool[0][:], c.pool[1][:] = 0x38, 127 - 8
+    c.q = torch.ones_like(c.q)
+    c.q_host = c.q.cpu().double().numpy()
+    c.scale = float(bits * np.log(2.0) / 0.5)
+    page, row = c.row(0, at)
+    c.pool[1][page, 0, row] = 127 - 7
+    zero_value(c, 0, at)
+    check(c, *c.gpu())
+
+
+def test_zero_values_alone():
+    # nothing else is seen: by single tokens, by a node of a tree, in a lane of a cache that holds nothing yet
+    c = Case([(4, 1), (0, 1), (300, 3), (1300, 2)], 4, 2, 128, 16, seed=60)
+    for b in (0, 1, 3):
+        for j in range(sum(c.lanes[b])):
+            zero_value(c, b, j)
+    c.lanes[2], c.kv_len[2] = (0, 3), 3              # three nodes without a prefix, the second of which sees itself alone
+    zero_value(c, 2, 1)
+    c.mask[3, 0] = 0b010
+    got, lse = c.gpu()
+    check(c, got, lse)
+    assert not got[:2].any() and not got[3].any() and not got[5:].any() and np.isfinite(lse).all() and got[2].any()
+
+
+def test_a_value_row_of_scale_one_is_no_zero():
+    # scale 2^0 with codes that are zero but for the last, and infinities in rows that nobody sees
+    c = Case([(200, 4)], 4, 2, 128, 16, seed=61)
+    for j in (0, 150):
+        zero_value(c, 0, j)
+        page, at = c.row(0, j)
+        c.pool[2][page, :, at, 127] = 0x01
+    c.mask[:, 0] = [0b0001, 0b0001, 0b0101, 0b1001]
+    zero_value(c, 0, 201)
+    check(c, *c.gpu())
+
+
+def test_written_zeros_are_attended_as_zeros():
+    H, page, D = 2, 16, 128
+    cache = moe.KvCache.empty(4, H, page, D)
+    x = torch.randn(40, 2 * H, D, device="cuda").bfloat16()
+    x[:, H:] *= 1e-3
+    x[5:9, H:] = 0.0
+    x[30, H] = -0.0
+    moe.moe_kv_write(x[:, :H], x[:, H:], torch.arange(40, device="cuda"), cache)
+    q = torch.randn(1, 4, D, device="cuda").bfloat16()
+    out, lse = torch.empty_like(q), torch.empty((1, 4), device="cuda")
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = torch.empty(moe.moe_tree_attention_workspace_bytes(1, 4, H, D, 1), dtype=torch.uint8, device="cuda")
+    moe.moe_tree_attention(q, cache, i32(0, 1, 2, 3).view(1, 4), i32(40), i32(0, 1), 1, None, D ** -0.5, out, ws, lse=lse)
+    got, host = out.double().cpu().numpy(), [t.cpu().numpy() for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)]
+    kc, ks, vc, vs = (ref.lane_rows(a, np.arange(4), 40) for a in host)
+    for h in range(4):
+        o, e, tol = definition(q[:, h].double().cpu().numpy(), ref.values(kc, ks)[:, h // 2], vc[:, h // 2], vs[:, h // 2],
+                               np.ones((1, 40), bool), D ** -0.5)
+        assert (np.abs(got[:, h] - o) <= tol).all() and abs(lse[0, h].item() - e[0]) <= 2.0 ** -15
+    assert moe.moe_device_status() == (moe.MOE_OK, 0)
