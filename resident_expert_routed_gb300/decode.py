@@ -120,6 +120,8 @@ class DecodeLayer:
         """hidden bf16 [n_nodes, d] of the step's nodes, lane by lane; returns the layer's bf16 output. tree = False:
         each lane's nodes are a chain (a chunk of its prompt)."""
         n, H, D = tables.n_nodes, self.cache.n_kv_heads, self.cache.head_dim
+        if n == 0:                           # every lane waits
+            return torch.empty_like(hidden)
         qkv = hidden @ self.w_qkv.T
         q, k, v = (x.view(n, -1, D) for x in qkv.split([self.heads * D, H * D, H * D], 1))
         moe_kv_write(k, v, tables.slots, self.cache)

@@ -1,0 +1,22 @@
+"""Host side of a decode step (no GPU needed): steps without work, tables and the host's page table, what the example needs."""
+import types
+
+import torch
+
+from resident_expert_routed_gb300.decode import DecodeLayer, LanePages, Step
+
+
+def layer(d=32, heads=4, kv_heads=2, D=64, lanes=3):
+    """A layer on the host; nothing in it can be launched."""
+    w = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16)  # noqa: E731
+    cache = types.SimpleNamespace(n_kv_heads=kv_heads, head_dim=D)
+    return DecodeLayer(w((heads + 2 * kv_heads) * D, d), w(d, heads * D), cache, heads, lanes, 8, (None,) * 7, None)
+
+
+def test_a_step_in_which_every_lane_waits():
+    pages = LanePages(3, 8, 16, 4)
+    tables = Step(pages, [[], [], []], device="cpu")
+    assert tables.n_nodes == 0 and tables.slots.shape == (0,) and tables.mask.shape == (0, 1)
+    hidden = torch.zeros((0, 32), dtype=torch.bfloat16)
+    out = layer().step(hidden, tables)
+    assert out.shape == (0, 32) and out.dtype == torch.bfloat16
