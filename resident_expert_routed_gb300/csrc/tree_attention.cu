@@ -1389,7 +1389,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             // -------------------------------------------------------- watchdog: stops the block when nothing has moved for the bound
             uint32_t seen = 0;
             uint64_t since = global_timer_ns();
-            while (!try_at_for(bar(C::B_DONE), 0, 20000) && !stopped(stop)) {
+            const bool nap = a.wait_ns >= 40000ull;  // (asleep for some 20 us, whatever less is asked for)
+            while (!(nap ? try_at_for(bar(C::B_DONE), 0, 20000) : test_at(bar(C::B_DONE), 0)) && !stopped(stop)) {
                 const uint32_t now_at = progress[0] + progress[1];
                 const uint64_t now = global_timer_ns();
                 if (now_at != seen) {
