@@ -152,8 +152,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
-    """Handle of a stream, or of the current one of the current device (without building a Stream object: 3 us)."""
-    return _raw_stream(_device()) if stream is None else stream.cuda_stream
+    """Handle of a stream, or of the current one of the current device (without building a Stream object, 3 us, where
+    this torch build has the two calls)."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None or _device is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_device())
 
 
 @dataclass
@@ -443,7 +448,7 @@ def moe_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: K
     if heads != cache.n_kv_heads or dim != cache.head_dim or k1 != 1 or v1 != 1 or not k.is_cuda or not v.is_cuda:
         raise ValueError(f"k and v: expected CUDA tensors [tokens, {cache.n_kv_heads}, {cache.head_dim}] with a contiguous last axis")
     st = (_lib or load()).moe_kv_write(k.data_ptr(), v.data_ptr(), dtype, kt, kh, vt, vh, _at(slots, _I64, (T,), "slots"),
-                                       T, cache._st, _raw_stream(_device()) if stream is None else stream.cuda_stream)
+                                       T, cache._st, _stream(stream))
     if st:
         _check("moe_kv_write", st)
 
