@@ -84,7 +84,7 @@ class Step:
         for n in counts:
             cu.append(cu[-1] + n)
         dev = lambda v, t=torch.int32: torch.tensor(v, dtype=t, device=device)  # noqa: E731
-        self.table = pages.table.to(device, non_blocking=True)
+        self.table = pages.table.to(device, copy=True)       # (complete on return: the host's table may change at once)
         self.prefix, self.cu = dev(pages.rows), dev(cu)
         self.kv_len = dev([r + n for r, n in zip(pages.rows, counts)])
         self.slots = dev([s for b, n in enumerate(counts) for s in pages.slots(b, n)], torch.int64)

@@ -20,3 +20,14 @@ def test_a_step_in_which_every_lane_waits():
     hidden = torch.zeros((0, 32), dtype=torch.bfloat16)
     out = layer().step(hidden, tables)
     assert out.shape == (0, 32) and out.dtype == torch.bfloat16
+
+
+def test_a_step_keeps_its_page_table():
+    """What the host does with its table afterwards (a lane that ends, pages handed to another) is not the step's."""
+    pages = LanePages(2, 8, 16, 4)
+    tables = Step(pages, [[-1, 0, 0], [-1]], device="cpu")
+    was = tables.table.clone()
+    assert was[0, 0] >= 0 and was[1, 0] >= 0
+    pages.release(0)
+    pages.reserve(1, 60)
+    assert torch.equal(tables.table, was)
