@@ -17,27 +17,37 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
+import numpy as np
 import torch
 
 import resident_expert_routed_gb300 as moe
 import synth
 from resident_expert_routed_gb300.decode import DecodeLayer, LanePages, Step
 from resident_expert_routed_gb300.layer import LayerBuffers
-from tests.cases import device_arena, make_case, to_dev
 
 HEADS, KV_HEADS, HEAD_DIM, PAGE = 8, 2, 64, 16
 
 
 def build(lanes: int, max_tokens: int, n_pages: int, seed: int = 0) -> DecodeLayer:
     cfg = synth.TINY
-    case = make_case(cfg, 8)
+    bias = synth.router_bias(cfg.seed, cfg.E, cfg.sigma)
+    resident = synth.resident_set(cfg, bias)
+    slot_of = synth.slot_table(cfg, resident, cfg.resident)
+    owner = np.full(cfg.resident, -1, np.int32)                          # expert of each slot of the arena
+    owner[slot_of[resident]] = resident
+    rec = synth.slot_record(cfg.d, cfg.ffn)
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    slots = torch.zeros(cfg.resident * rec["slot_bytes"], dtype=torch.uint8, device="cuda")
+    synth.fill_slots_device(slots, cfg.d, cfg.ffn, cfg.seed, cfg.E, dev(owner))
+    arena = moe.Arena(slots, rec["slot_bytes"], cfg.resident, cfg.d, cfg.ffn, rec["off_gu_codes"], rec["off_gu_scales"],
+                      rec["off_dn_codes"], rec["off_dn_scales"])
     gen = torch.Generator(device="cuda").manual_seed(seed)
     w = lambda *shape: (torch.randn(shape, generator=gen, device="cuda") * shape[1] ** -0.5).bfloat16()  # noqa: E731
-    moe_args = (to_dev(case.W), to_dev(case.bias), to_dev(case.slot_of), device_arena(cfg, case.owner, case.n_slots),
+    moe_args = (dev(synth.router_weights(cfg.seed, cfg.E, cfg.d)), dev(bias), dev(slot_of), arena,
                 torch.zeros((1, cfg.E), dtype=torch.int64, device="cuda"), torch.zeros((1, cfg.E), device="cuda"), 0)
     return DecodeLayer(w((HEADS + 2 * KV_HEADS) * HEAD_DIM, cfg.d), w(cfg.d, HEADS * HEAD_DIM),
                        moe.KvCache.empty(n_pages, KV_HEADS, PAGE, HEAD_DIM), HEADS, lanes, max_tokens, moe_args,
-                       LayerBuffers(max_tokens, cfg.k, cfg.E, cfg.d, cfg.ffn, case.n_slots))
+                       LayerBuffers(max_tokens, cfg.k, cfg.E, cfg.d, cfg.ffn, cfg.resident))
 
 
 def draft(rng: random.Random, n: int) -> list[int]:

@@ -31,3 +31,13 @@ def test_a_step_keeps_its_page_table():
     pages.release(0)
     pages.reserve(1, 60)
     assert torch.equal(tables.table, was)
+
+
+def test_the_example_does_without_the_test_tree(monkeypatch):
+    import importlib
+    import sys
+    for name in [m for m in sys.modules if m == "tests" or m.startswith("tests.") or m == "examples.tree_decode"]:
+        monkeypatch.delitem(sys.modules, name)
+    monkeypatch.setitem(sys.modules, "tests", None)                      # any import of it fails
+    assert importlib.import_module("examples.tree_decode").HEADS == 8
+    monkeypatch.delitem(sys.modules, "examples.tree_decode")
