@@ -425,7 +425,8 @@ typedef struct {
  * (MOE_EINVAL). slots int64 [T]: token t goes to row slots[t] % page_size of
  * page slots[t] / page_size; -1 skips the token. Another slot outside the
  * cache is skipped and sets MOE_DEV_BAD_PAGE; a vector that is not finite sets
- * MOE_DEV_NAN_KV. Two tokens with one slot: either may win.
+ * MOE_DEV_NAN_KV. No two tokens of a call share a slot: such a row could hold
+ * codes of one and the scale of the other, which stand for neither.
  * T = 0 returns MOE_OK without a launch; T * n_kv_heads <= 2^27.
  */
 moe_status moe_kv_write(const void* k, const void* v, int dtype, int64_t k_token_stride, int64_t k_head_stride,

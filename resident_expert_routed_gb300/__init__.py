@@ -438,7 +438,8 @@ class KvCache:
 
 def moe_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: KvCache, stream=None) -> None:
     """Quantise the keys and values of T tokens [T, n_kv_heads, head_dim] (bf16, fp16 or fp32; any token and head
-    strides of whole 16 bytes) into cache rows slots int64 [T] (page * page_size + row; -1 skips the token)."""
+    strides of whole 16 bytes) into cache rows slots int64 [T] (page * page_size + row; -1 skips the token; no two tokens
+    share a row)."""
     shape, dtype = k.shape, _DTYPES.get(k.dtype)
     if len(shape) != 3 or v.shape != shape or dtype is None or v.dtype is not k.dtype:
         raise ValueError("k and v: one shape [tokens, heads, dim] and one type of bf16, fp16, fp32")
