@@ -1018,44 +1018,37 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             const int rows = walk.rows(wq), row0 = wq.rt * R, n0 = walk.lane(wq.b).n0;
             uint8_t* Q = smem + C::OFF_Q + qb * C::QBUF;
             float* qf = F + C::F_QF + (qpiece & 3) * R;
-            // up to eight rows a lane at a time, all loads under way before the first is used; more are read twice
-            constexpr int BATCH = ITER < 8 ? ITER : 8;
-            const int first = row0 + wl * RPW + sub, node0 = first / G, head0 = first - node0 * G;
-            int node = node0, head = head0;
-            uint4 raw[BATCH];
-            auto fetch = [&](int b0) {
+            static_assert(ITER <= 8, "a lane's rows are held in registers");
+            const int first = row0 + wl * RPW + sub;
+            int node = first / G, head = first - node * G;
+            uint4 raw[ITER];
 #pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                    raw[b] = make_uint4(0u, 0u, 0u, 0u);
-                    if (((b0 + b) * 4 + wl) * RPW + sub < rows)
-                        raw[b] = *reinterpret_cast<const uint4*>(a.q + (n0 + node) * a.q_token_stride + (wq.h * G + head) * a.q_head_stride + part * 8);
-                    node += row_step / G;
-                    head += row_step % G;
-                    if (head >= G) { head -= G; ++node; }
-                }
-            };
+            for (int b = 0; b < ITER; ++b) {
+                raw[b] = make_uint4(0u, 0u, 0u, 0u);
+                if ((b * 4 + wl) * RPW + sub < rows)
+                    raw[b] = *reinterpret_cast<const uint4*>(a.q + (n0 + node) * a.q_token_stride + (wq.h * G + head) * a.q_head_stride + part * 8);
+                node += row_step / G;
+                head += row_step % G;
+                if (head >= G) { head -= G; ++node; }
+            }
             // max |x| of each row (bf16 bits; NaN stays), and of the unit's rows the largest and the smallest but zero
             uint32_t* keys = reinterpret_cast<uint32_t*>(qf);
             uint32_t most = 0, least = 0x7FFFu;
 #pragma unroll
-            for (int b0 = 0; b0 < ITER; b0 += BATCH) {
-                fetch(b0);
+            for (int b = 0; b < ITER; ++b) {
+                auto abs2 = [](uint32_t v) {
+                    v &= 0x7FFF7FFFu;
+                    return *reinterpret_cast<const __nv_bfloat162*>(&v);
+                };
+                __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(abs2(raw[b].x), abs2(raw[b].y)), __hmax2_nan(abs2(raw[b].z), abs2(raw[b].w)));
+                m = __hmax2_nan(m, __lowhigh2highlow(m));
 #pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                    auto abs2 = [](uint32_t v) {
-                        v &= 0x7FFF7FFFu;
-                        return *reinterpret_cast<const __nv_bfloat162*>(&v);
-                    };
-                    __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(abs2(raw[b].x), abs2(raw[b].y)), __hmax2_nan(abs2(raw[b].z), abs2(raw[b].w)));
-                    m = __hmax2_nan(m, __lowhigh2highlow(m));
-#pragma unroll
-                    for (int o = LPR / 2; o > 0; o >>= 1) m = __hmax2_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                    const uint32_t key = *reinterpret_cast<const uint32_t*>(&m) & 0xFFFFu;
-                    const int u = ((b0 + b) * 4 + wl) * RPW + sub;
-                    if (part == 0 && u < R) keys[u] = key;
-                    most = max(most, key);
-                    if (key) least = min(least, key);
-                }
+                for (int o = LPR / 2; o > 0; o >>= 1) m = __hmax2_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                const uint32_t key = *reinterpret_cast<const uint32_t*>(&m) & 0xFFFFu;
+                const int u = (b * 4 + wl) * RPW + sub;
+                if (part == 0 && u < R) keys[u] = key;
+                most = max(most, key);
+                if (key) least = min(least, key);
             }
             uint32_t* qx = reinterpret_cast<uint32_t*>(F + C::F_QX);
             most = __reduce_max_sync(0xFFFFFFFFu, most);
@@ -1083,38 +1076,32 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
             if (wl == 0 && lane == 0)
                 *reinterpret_cast<float2*>(F + C::F_QU + (qpiece & 3) * 2) = make_float2(rowwise ? 1.0f : exp2_int(-unit_up), rowwise ? 1.0f : 0.0f);
             const int byte = part * 8, panel = byte / C::ROWB, in_row = byte % C::ROWB;
-            node = node0;
-            head = head0;
 #pragma unroll
-            for (int b0 = 0; b0 < ITER; b0 += BATCH) {
-                if (ITER > BATCH) fetch(b0);
+            for (int b = 0; b < ITER; ++b) {
+                const int u = (b * 4 + wl) * RPW + sub;
+                const uint32_t key = rowwise && u < R ? keys[u] : 0u;
+                __syncwarp();
+                const int up = rowwise ? up_of(key) : unit_up;
+                const float gain = exp2_int(up);
+                const f32x2 gain2 = pack2(gain, gain);
+                const uint32_t in[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+                uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                    const int u = ((b0 + b) * 4 + wl) * RPW + sub;
-                    const uint32_t key = rowwise && u < R ? keys[u] : 0u;
-                    __syncwarp();
-                    const int up = rowwise ? up_of(key) : unit_up;
-                    const float gain = exp2_int(up);
-                    const f32x2 gain2 = pack2(gain, gain);
-                    const uint32_t in[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        // a scaled bf16 value is exact in fp16 (down to 2^-16, far below what lo resolves)
-                        const float2 x = unpack2(mul2(pack2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xFFFF0000u)), gain2));
-                        const __half2 xh = __floats2half2_rn(x.x, x.y);
-                        hi[e] = __nv_cvt_halfraw2_to_fp8x2(xh, __NV_SATFINITE, __NV_E4M3);
-                        const __half2 rest = __hsub2(xh, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3)));
-                        lo[e] = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
-                    }
-                    if (u < R) {
-                        // a row that is not finite: its scores become NaN
-                        if (rowwise && part == 0) qf[u] = key >= 0x7F80u ? __uint_as_float(0x7FC00000u) : exp2_int(-up);
-                        const int swz = C::ROWB == 128 ? u & 7 : (u >> 1) & 3;     // the same for row R + u
-                        uint8_t* at = Q + panel * C::QROWS * C::ROWB + u * C::ROWB + (((in_row >> 4) ^ swz) << 4) + (in_row & 15);
-                        *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(hi[0], hi[1], 0x5410), __byte_perm(hi[2], hi[3], 0x5410));
-                        *reinterpret_cast<uint2*>(at + R * C::ROWB) = make_uint2(__byte_perm(lo[0], lo[1], 0x5410), __byte_perm(lo[2], lo[3], 0x5410));
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    // a scaled bf16 value is exact in fp16 (down to 2^-16, far below what lo resolves)
+                    const float2 x = unpack2(mul2(pack2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xFFFF0000u)), gain2));
+                    const __half2 xh = __floats2half2_rn(x.x, x.y);
+                    hi[e] = __nv_cvt_halfraw2_to_fp8x2(xh, __NV_SATFINITE, __NV_E4M3);
+                    const __half2 rest = __hsub2(xh, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3)));
+                    lo[e] = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
+                }
+                if (u < R) {
+                    // a row that is not finite: its scores become NaN
+                    if (rowwise && part == 0) qf[u] = key >= 0x7F80u ? __uint_as_float(0x7FC00000u) : exp2_int(-up);
+                    const int swz = C::ROWB == 128 ? u & 7 : (u >> 1) & 3;     // the same for row R + u
+                    uint8_t* at = Q + panel * C::QROWS * C::ROWB + u * C::ROWB + (((in_row >> 4) ^ swz) << 4) + (in_row & 15);
+                    *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(hi[0], hi[1], 0x5410), __byte_perm(hi[2], hi[3], 0x5410));
+                    *reinterpret_cast<uint2*>(at + R * C::ROWB) = make_uint2(__byte_perm(lo[0], lo[1], 0x5410), __byte_perm(lo[2], lo[3], 0x5410));
                 }
             }
             fence_proxy_async_smem();
