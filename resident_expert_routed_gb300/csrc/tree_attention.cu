@@ -173,8 +173,8 @@ struct Cfg {
     static constexpr int OFF_TID = OFF_SID + 2 * SA * 128;    // [PT][8]
     static constexpr int OFF_F = OFF_TID + PT * 32;           // floats from here
     static constexpr int F_O = 0;                             // [2 groups][R] P_EXP - m, as added to s'
-    static constexpr int F_AL = F_O + 2 * R;                  // [2][R] scale-down of what has been added up: its root
-    static constexpr int F_WMAX = F_AL + 2 * R;               // [2 groups][HALVES][2][4 warps][RH]
+    static constexpr int F_AL = F_O + 2 * R;                  // [2: root, whole][2][R] scale-down of what has been added up
+    static constexpr int F_WMAX = F_AL + 4 * R;               // [2 groups][HALVES][2][4 warps][RH]
     static constexpr int F_QF = F_WMAX + 16 * R;              // [4][R] 2^-a of the queries' rows
     static constexpr int F_QU = F_QF + 4 * R;                // [4][2] 2^-a of all rows of a unit; whether the rows' differ instead
     static constexpr int F_QX = F_QU + 8;                     // [largest, smallest][unit parity][4 warps] |q| of the rows, as bits
@@ -852,7 +852,9 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                             const float Mn = fmaxf(M, m);
                             // a row that has seen nothing: the first score it sees passes any limit
                             off[lane] = Mn == -INFINITY ? 1e30f : P_EXP - Mn;
-                            alpha[lane] = M == -INFINITY ? 0.0f : ex2(0.5f * (M - Mn));
+                            const float root = M == -INFINITY ? 0.0f : ex2(0.5f * (M - Mn));
+                            alpha[lane] = root;
+                            alpha[2 * R + lane] = root * root;
                             M = Mn;
                         }
                         __syncwarp();
@@ -888,9 +890,9 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
                             uint32_t o[8];
                             tc_ld_x8(at, o);
                             tc_wait_ld();
-                            const float* al = alpha + c0 % RH;
+                            const float* al = alpha + 2 * R + c0 % RH;
 #pragma unroll
-                            for (int q = 0; q < 8; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * (al[q] * al[q]));
+                            for (int q = 0; q < 8; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * al[q]);
                             tc_st_x8(at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
                         }
                         tc_wait_st();
