@@ -475,12 +475,18 @@ moe_status moe_kv_keep(const moe_kv_cache* cache, const int32_t* page_table, int
  *   out      = sum_j p[j] v[j],    lse = log sum_j exp(score[j])
  * A node that sees no row gets zeros and lse = -inf. Rows that a node does not
  * see never touch its result, whatever they hold.
- * Precision: scores, sums of weights and lse are fp32, out is rounded to bf16
- * once. The products run on 8-bit parts of q and p: a query element is held
- * exactly down to 2^-9 of the largest of its (node, head) row and to 2^-17 of
- * it below (to 2^-13 where a larger row is handled with it); a weight to 2^-9 of
- * itself, or to 2^-28 of the largest p[j] * 2^(scale byte of v[j] - 127) that
- * the node sees (value vectors of zeros aside), whichever is more.
+ * Precision: sums of weights and lse are fp32, out is rounded to bf16 once. The
+ * products run on 8-bit parts of q and p, accumulated in fp32 by truncation:
+ *   - a query element is held exactly down to 2^-9 of the largest of its (node,
+ *     head) row, to 2^-17 of that below (to 2^-13 where a row of up to 2^5 times
+ *     its size is handled with it);
+ *   - a score is off by at most head_dim * 2^-24 of scale * sum |q k|;
+ *   - a weight is held to 2^-9 of itself, or to 2^-28 of the largest
+ *     p[j] * 2^(scale byte of v[j] - 127) that the node sees, whichever is more
+ *     (a value vector of zeros counts as 2^-100 there);
+ *   - weighted values of one sign add up to 2^-11 too little for every 2^20 rows
+ *     that one block adds up (2^-9 with more than 32 rows of nodes and heads to a
+ *     kv head, or more than 16 at head_dim 256).
  * q bf16 [n_nodes, n_q_heads, head_dim], last axis contiguous, strides in
  * elements (multiples of 8), 16-byte aligned; query head h reads kv head
  * h / (n_q_heads / n_kv_heads). page_table int32 [lanes, table_width] (entries

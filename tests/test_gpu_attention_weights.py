@@ -3,7 +3,8 @@ definition in 64 bits.
 
 Bounds. A weight is held to 2^-9 of itself, or to 2^-28 of the largest weight times its value vector's scale, whichever
 is more; the scores and the sums are fp32 (2^-11 of the weights covers their roundings, and the queries'), and the
-output is rounded to bf16 once (half a unit: 2^-9, and 2^-134 where bf16's steps end). So
+output is rounded to bf16 once (half a unit: 2^-9 to 2^-8, of which 2^-9 is asked for, as the weights' bound is hardly
+reached; and 2^-134 where bf16's steps end). So
   |out - o| <= max(2^-9 |o|, 2^-134) + (2^-9 + 2^-11) sum p |v| + 2^-28 max(p 2^ev) sum |codes|,
 each column for itself. A log sum is off by the rounding of the scores and the scale exponents that are
 added to them (at most 2^7: 2^-17 each) and a few 2^-22.
