@@ -48,8 +48,8 @@ struct KvSide {
 // moe_kv_write. D / 16 lanes share a vector: 16 elements a lane, one 16-byte
 // store of codes, the maximum by shuffles within the group, so a vector is read
 // once and stays in registers. blockIdx.y picks keys or values. Measured (calls back
-// to back, 8 heads of 128, bf16): 8,192 rows 8.7 us (50.5 MB, 5.8 TB/s), one
-// row 1.5 us, a launch.
+// to back in a graph, so inputs partly from L2; 8 heads of 128, bf16): 8,192 rows 8.6 us
+// (50.5 MB, 5.8 TB/s), two rows 1.5 us, a launch. Called from Python 20 and 15 us: the host.
 template <typename T, int D>
 __global__ void __launch_bounds__(KV_THREADS) kv_write(const KvSide k, const KvSide v, const int64_t* __restrict__ slots,
                                                        int n_tokens, int H, int page_shift, int64_t n_rows, uint32_t* err) {
@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(KV_THREADS) kv_write(const KvSide k, const KvS
 // binary search over the lanes' row counts) and then every thread converts
 // 16-byte pieces of the output, neighbours next to each other, READ_UNROLL
 // pieces under way (one: 8.4 us for 7.8; eight: no faster). What is written is not read again
-// here, so it is stored as streaming. Measured (8 heads of 128, bf16): 8,192 rows
-// of one lane 7.8 us (50.5 MB, 6.5 TB/s).
+// here, so it is stored as streaming. Measured (as above): 8,191 rows of one lane
+// 7.8 us (50.5 MB, 6.5 TB/s); called from Python 11 us.
 constexpr int READ_ROWS = 32, READ_UNROLL = 4;
 
 template <typename T, int D>

@@ -50,13 +50,15 @@
 // in the workspace and tree_attention_join adds them up in order. One CTA an SM, so one long lane and many uneven
 // ones fill the machine alike.
 //
-// What bounds it (measured, a call's whole time; head_dim 128, 8 kv heads, 2,064 bytes of cache a row): up to 32 tree
-// rows HBM: one token in 64 lanes of uneven lengths up to 8,192 rows 95 us (543 MB, 5.7 TB/s; even lengths 6.4 TB/s,
-// head_dim 256 6.4, head_dim 64 4.1: there the copies' warp, 1,100 clocks a tile for four pages), a tree of 7 nodes in two
-// lanes of 131,072 rows 100 us (541 MB). Of the 95 us the tile loop takes 78, the cut 4, the first tile 4, the last
-// outputs, the join and its launch 6. With 64 tree rows the softmax's instructions and their latency: 2,200 clocks a
-// tile where HBM would allow 1,470 (trees of up to 16 nodes, 64 query heads, 32 lanes of up to 8,001 rows: 139 us).
-// Below some thousand rows the chain of one unit: 8.6 us for a lane of 300.
+// What bounds it (measured, a call's whole time, calls back to back in a graph; head_dim 128, 8 kv heads, 2,064 bytes of
+// cache a row): up to 32 tree rows HBM: one token in 64 lanes of uneven lengths up to 8,192 rows 94.5 us (543 MB, 5.7 TB/s;
+// even lengths 6.5 TB/s, head_dim 256 6.5, head_dim 64 4.3: there the copies' warp, 1,090 clocks a tile for four pages where
+// HBM would allow 780), a tree of 7 nodes in two lanes of 131,072 rows 101 us (541 MB). Of the 95 us the tile loop takes 78,
+// the cut 4, the first tile 4, the last outputs, the join and its launch 6. With 64 tree rows the softmax's instructions and
+// their latency: 2,400 clocks a tile where HBM would allow 1,550 (trees of up to 16 nodes, 64 query heads, 32 lanes of up to
+// 8,001 rows: 148 us; at head_dim 64 2,600 clocks). A chain without a mask (the chunk of a prompt) runs over all its tiles,
+// those that nobody sees too: 8,192 rows, 32 query heads 2.58 ms. Below some thousand rows the chain of one unit: 8.7 us
+// for a lane of 300.
 //
 // Roles: 8 or 16 warps of softmax, then
 //   four warps       the next unit's queries (split and laid out), a finished unit's output
@@ -110,14 +112,14 @@ constexpr int LANE_CACHE = 256;                  // lanes whose facts are kept i
 
 // Units of at most this many tiles are not cut between CTAs, and the join is not launched: a unit's tiles one after the other
 // take less than the join and its launch. Known on the host, from the rows that the page table can hold. (One token, 8 kv
-// heads of 128, us whole / cut: 300 rows 8.6 / 10.7 in one lane, 19.3 / 24.2 in 64; 1,000 rows 12 / 11.7 and 34.5 / 36.0;
-// 2,000 rows 18.0 / 14.0 and 57.0 / 54.8.)
+// heads of 128, us whole / cut: 300 rows 8.7 / 10.8 in one lane, 20.2 / 25.0 in 64; 1,000 rows 12.1 / 11.6 and 33.3 / 35.7;
+// 2,000 rows 17.5 / 13.6 and 54.6 / 53.3.)
 constexpr int WHOLE_TILES = 8;
 
 // The run's measure: what a tile costs, and a tile of which half the unit's tree rows are missing, where the halves are
-// different warps' (the cache is then read as fast, the softmax does half the work; 2, 3, 4: trees of up to 10 nodes 133, 115,
-// 120 us). A unit costs R / 8 tiles beside its own: its queries, its first reference, its output (0, R / 8, R / 4: trees of up to
-// 16 nodes 210, 139, 144 us; 64 uneven lanes of one token 112, 95, 96 us). The parts are cut evenly in this measure; below four
+// different warps' (the cache is then read as fast, the softmax does half the work; 2, 3, 4: trees of up to 10 nodes 147, 125,
+// 128 us). A unit costs R / 8 tiles beside its own: its queries, its first reference, its output (0, R / 8, R / 4: trees of up to
+// 16 nodes 207, 148, 154 us; 64 uneven lanes of one token 110, 94, 92.5 us). The parts are cut evenly in this measure; below four
 // tiles a CTA in tiles alone, as there the longest part counts.
 constexpr int FULL_COST = 4, HALF_COST = 3;
 __host__ __device__ constexpr int unit_cost(int R) { return FULL_COST * R / 8; }
@@ -209,8 +211,8 @@ struct Cfg {
     // Tiles whose S may be under way: the buffers, and (an odd ring) not past a slot whose values are still to be used
     static constexpr int LOOK = NS % 2 && NS / 2 + 1 < SB ? NS / 2 + 1 : SB;
     // O of the three parts of P in columns of their own where TMEM has room (they are added up with the output): one MMA of
-    // N = 3 R takes 32 rows, not three of N = R (us, so / three: one token in 64 uneven lanes 94.7 / 103.2, a tree of 7 nodes
-    // in two lanes of 131,072 rows 100.8 / 107.9).
+    // N = 3 R takes 32 rows, not three of N = R (us, so / three: one token in 64 uneven lanes 93.9 / 103.7, a tree of 7 nodes
+    // in two lanes of 131,072 rows 100.6 / 107.4).
     static constexpr int PARTS = 4 * R + 4 * R * MB * 3 <= 512 ? 3 : 1;
     static constexpr int OC = PARTS * R;                      // columns of one O block
     static constexpr int TMEM_O = 4 * R;                      // after S (4 R columns): O [group][unit parity][MB][PARTS][R]
@@ -1593,11 +1595,12 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
 }
 
 // The tile of tree rows: the smallest that takes a lane's rows of one kv head at once, else the largest. Measured, us,
-// taken / the other: 4 rows, 64 lanes of up to 8,192 rows, 16 / 32: 95 / 106. 28 rows, two lanes of 131,072, 32 / 64:
-// 100 / 110. Up to 128 rows, 32 lanes of up to 8,001, 64 / 32: 139 / 164. Up to 64 rows at head_dim 64, 32 lanes of up
-// to 8,000, 64 / 32: 153 / 187 (nine lanes of up to 2,047, their trees uneven: 35 / 31). Two groups on one tile for
+// taken / the other: 4 rows, 64 lanes of up to 8,192 rows, 16 / 32: 94 / 104. 28 rows, two lanes of 131,072, 32 / 64:
+// 101 / 124. Up to 128 rows, 32 lanes of up to 8,001, 64 / 32: 148 / 171. Up to 64 rows at head_dim 64, 32 lanes of up
+// to 8,000, 64 / 32: 182 / 189 (nine lanes of up to 2,047, their trees uneven: 38 / 33; a second rule, on the rows that the page
+// table can hold, could tell these apart). Two groups on one tile for
 // twice the rows read the cache once where two units read it twice, but above 64 rows the softmax
-// bounds, not the reading: 3 % faster with 128 rows in every lane, 8 % slower with uneven trees.
+// bounds, not the reading: 3 % faster with 128 rows in every lane, 8 % slower with uneven trees (with weights in two parts).
 template <int D>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
     const int64_t rows = (int64_t)(a.max_nodes < a.n_nodes ? a.max_nodes : a.n_nodes) * a.group;
