@@ -62,6 +62,7 @@ typedef enum {
 #define MOE_DEV_RESIDENT    0x10u  /* ring install of an expert that is already resident */
 #define MOE_DEV_BAD_PAGE    0x20u  /* key/value cache: a row, page id, path or lane length out of range */
 #define MOE_DEV_NAN_KV      0x40u  /* moe_kv_write met a key or value vector that is not finite */
+#define MOE_DEV_NO_PAGES    0x80u  /* moe_page_plan refused a lane: no pages, no place in its table or in the batch */
 
 /*
  * The shared slot arena (README item 1: a single arena serves every layer).
@@ -510,6 +511,93 @@ moe_status moe_tree_attention(const void* q, int64_t q_token_stride, int64_t q_h
                               int lanes, const int32_t* kv_len, const int32_t* cu_nodes, int max_nodes,
                               const int32_t* tree_mask, int mask_words, float scale, void* out, float* lse,
                               void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The plan of a batch of new tokens, made on the device: pages from a stack of
+ * free ones into the lanes' page tables, the tokens' positions and cache slots.
+ * n_new int32 [lanes]: how many tokens lane b gets (0: it waits; below 0: it is
+ * done, and its pages go back). State, updated in place:
+ *   rows       int32 [lanes]  rows that the lane has kept; 0 when it is done.
+ *              (The caller moves it on: by n_new after a chunk, by what was kept
+ *              after a draft.)
+ *   held       int32 [lanes]  pages in its table
+ *   page_table int32 [lanes, table_width]; -1 past the held ones
+ *   free_pages int32 [n_pages] a stack of page ids, n_free int32 [1] how many
+ * First the done lanes' pages are put on the stack, in the lanes' order and each
+ * table's; then lane b takes need_b = max(0, ceil((rows + n_new) / page_size) -
+ * held) pages from its top, if the needs of all lanes up to b are there. A lane
+ * for which they are not, or whose rows do not fit its table or tokens the batch,
+ * is refused: its state stays, its kv_len is 0 (attention then gives zeros), its
+ * tokens get no slots, and MOE_DEV_NO_PAGES is set. A refused need counts for the
+ * lanes behind it, so whether a lane is served does not depend on those behind.
+ * Outputs:
+ *   kv_len     int32 [lanes]      rows + n_new; 0 of a done or refused lane
+ *   cu_tokens  int32 [lanes + 1]  the tokens' sums, from 0, at most max_tokens
+ *   positions  int32 [max_tokens] row of the lane that a token becomes; 0 past the last
+ *   slots      int64 [max_tokens] page * page_size + row, for moe_kv_write; -1 past
+ *              the last and for refused lanes
+ * kv_len and cu_tokens go to moe_chunk_attention as they are. Calling again with
+ * the same n_new, before rows has moved on, gives the same answer.
+ * A stack outside 0 .. n_pages, negative rows, held outside the table or a page id
+ * outside the pool set MOE_DEV_BAD_PAGE; such a lane is refused.
+ * No two of the arrays overlap. Limits: lanes <= 4096, table_width <= 2^20,
+ * max_tokens <= 2^24, page_size a power of two, 16..1024, n_pages * page_size < 2^31.
+ */
+moe_status moe_page_plan(const int32_t* n_new, int32_t* rows, int32_t* held, int32_t* page_table, int table_width, int lanes,
+                         int32_t* free_pages, int n_pages, int32_t* n_free, int page_size, int32_t* kv_len, int32_t* cu_tokens,
+                         int32_t* positions, int64_t* slots, int max_tokens, void* stream);
+
+/*
+ * Norms of queries and keys of each head and the rotation by their token's
+ * position, in one pass:
+ *   y = x * weight / sqrt(mean(x^2) + eps)      (y = x where the weight is NULL)
+ * and of the first 2 * n_pairs values of a head every pair (a, b) becomes
+ *   (a cos t - b sin t, b cos t + a sin t) * magnitude,  t = position * f[i];
+ * the others stay y. Pair i is values (i, i + n_pairs), or (2 i, 2 i + 1) where
+ * interleaved is not 0. turns int64 [n_pairs]: f[i] as a whole number of 2^-64
+ * turns, round(f[i] / (2 pi) * 2^64) modulo 2^64: the angle of any position is then
+ * exact to the frequency's last bit. magnitude scales the turned values (1, or the
+ * factor that some rules for long contexts ask for).
+ * q, q_out [n_tokens, n_q_heads, head_dim], k, k_out [n_tokens, n_k_heads,
+ * head_dim] of `dtype` (MOE_BF16 ..), last axis contiguous; strides int64 [8], a
+ * HOST array, elements: token and head strides of q, k, q_out, k_out. Pointers are 16-byte
+ * aligned and strides multiples of 16 bytes. An output may be its input, with the same
+ * strides; otherwise nothing overlaps. positions int32 [n_tokens]; q_weight,
+ * k_weight fp32 [head_dim], 16-byte aligned, or NULL. One of the two head counts may be 0.
+ * Sums are fp32 (values above 2^60 in size overflow the mean square); one rounding.
+ * n_tokens = 0 returns MOE_OK without a launch. Limits: head_dim 64, 128 or 256,
+ * n_pairs a multiple of 8, up to half of head_dim (0: norms alone); heads <= 65,536 each,
+ * n_tokens * (n_q_heads + n_k_heads) <= 2^31.
+ */
+moe_status moe_qk_rotate(const void* q, const void* k, int dtype, const int64_t* strides, int n_tokens, int n_q_heads, int n_k_heads,
+                         int head_dim, const int32_t* positions, const int64_t* turns, int n_pairs, int interleaved, float magnitude,
+                         const float* q_weight, const float* k_weight, float eps, void* q_out, void* k_out, void* stream);
+
+/*
+ * Attention of a chunk of new tokens of every lane over the lane's cache rows:
+ * a whole prompt, the next part of one, a single token, each lane as it likes.
+ * Lane b has n = cu_tokens[b+1] - cu_tokens[b] tokens (none: it waits), whose rows
+ * are the last n of its kv_len[b] rows, already written; token t sees the rows up
+ * to its own, j <= kv_len[b] - n + t.
+ *   score[j] = scale * q . k[j],   p = softmax of the scores of the rows seen
+ *   out      = sum_j p[j] v[j],    lse = log sum_j exp(score[j])
+ * Rows that a token does not see never touch its result, whatever they hold.
+ * Arguments as for moe_tree_attention, without a bound on a lane's tokens and
+ * without a mask. A lane with fewer rows than tokens or more than its table
+ * holds sets MOE_DEV_BAD_PAGE and gets zeros and lse = -inf; a page id outside
+ * the cache sets it too, and page 0 is read in its place. Rows of q and out behind
+ * cu_tokens[lanes] are left as they are.
+ * workspace: >= moe_chunk_attention_workspace_bytes(...), 16-byte aligned; its
+ * contents need not be kept or cleared between calls. Calls that overlap on
+ * the GPU need one each.
+ * scale > 0. n_tokens = 0 returns MOE_OK without a launch. Limits: lanes <= 4096,
+ * n_tokens <= 2^24, n_q_heads a multiple of n_kv_heads, at most 1024 and 128 to a kv head.
+ */
+size_t     moe_chunk_attention_workspace_bytes(int n_tokens, int n_q_heads, int n_kv_heads, int head_dim, int lanes);
+moe_status moe_chunk_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int n_tokens,
+                               int n_q_heads, const moe_kv_cache* cache, const int32_t* page_table, int table_width,
+                               int lanes, const int32_t* kv_len, const int32_t* cu_tokens, float scale, void* out, float* lse,
+                               void* workspace, size_t ws_bytes, void* stream);
 
 /* Workspace sizes (bytes) for the calls above. */
 size_t moe_workspace_bytes(int T, int k, int d, int ffn, int E, int n_slots);

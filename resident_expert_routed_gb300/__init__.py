@@ -26,7 +26,7 @@ LIB_PATH = os.path.join(_PKG, "libmoe_resident.so")
 
 MOE_OK, MOE_EINVAL, MOE_ECUDA, MOE_ENOMEM, MOE_ETIMEOUT, MOE_EDEVICE, MOE_EUNSUPPORTED, MOE_EIO = range(8)
 MOE_DEV_BAD_SLOT, MOE_DEV_NAN_SCALE, MOE_DEV_TIMEOUT, MOE_DEV_BAD_TABLE, MOE_DEV_RESIDENT = 0x1, 0x2, 0x4, 0x8, 0x10
-MOE_DEV_BAD_PAGE, MOE_DEV_NAN_KV = 0x20, 0x40
+MOE_DEV_BAD_PAGE, MOE_DEV_NAN_KV, MOE_DEV_NO_PAGES = 0x20, 0x40, 0x80
 MOE_BF16, MOE_FP16, MOE_FP32 = range(3)
 
 # Every symbol the header declares (checked by the CPU test suite).
@@ -37,7 +37,8 @@ EXPORTS = ("moe_route_resident", "moe_route_resident_noalloc", "moe_demand_accum
            "moe_demand_save", "moe_demand_load", "moe_hot_ring_create", "moe_hot_ring_step", "moe_hot_ring_destroy",
            "moe_hot_read_sync", "moe_renormalise_weights", "moe_expert_ffn_prefetch", "moe_set_wait_limit",
            "moe_get_wait_limit", "moe_wait_selftest", "moe_arena_refill", "moe_kv_write", "moe_kv_read", "moe_kv_keep",
-           "moe_tree_attention", "moe_tree_attention_workspace_bytes")
+           "moe_tree_attention", "moe_tree_attention_workspace_bytes", "moe_page_plan", "moe_qk_rotate",
+           "moe_chunk_attention", "moe_chunk_attention_workspace_bytes")
 
 
 class MoeError(RuntimeError):
@@ -119,13 +120,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.moe_tree_attention_workspace_bytes.restype = _SZ
     L.moe_tree_attention_workspace_bytes.argtypes = [_I, _I, _I, _I, _I]
     L.moe_tree_attention.argtypes = [_P, _I64, _I64, _I, _I, _KV, _P, _I, _I, _P, _P, _I, _P, _I, _F, _P, _P, _P, _SZ, _P]
+    L.moe_page_plan.argtypes = [_P, _P, _P, _P, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _I, _P]
+    L.moe_qk_rotate.argtypes = [_P, _P, _I, ctypes.c_char_p, _I, _I, _I, _I, _P, _P, _I, _I, _F, _P, _P, _F, _P, _P, _P]
+    L.moe_chunk_attention_workspace_bytes.restype = _SZ
+    L.moe_chunk_attention_workspace_bytes.argtypes = [_I, _I, _I, _I, _I]
+    L.moe_chunk_attention.argtypes = [_P, _I64, _I64, _I, _I, _KV, _P, _I, _I, _P, _P, _F, _P, _P, _P, _SZ, _P]
     for name in ("moe_route_resident", "moe_route_resident_noalloc", "moe_demand_accumulate", "moe_hot_miss_select",
                  "moe_expert_ffn_mxfp4",
                  "moe_arena_replan", "moe_ring_install", "moe_device_status", "moe_profile_enable",
                  "moe_profile_read", "moe_demand_decay", "moe_demand_save", "moe_demand_load", "moe_hot_ring_create",
                  "moe_hot_ring_step", "moe_hot_ring_destroy", "moe_hot_read_sync", "moe_renormalise_weights",
                  "moe_expert_ffn_prefetch", "moe_set_wait_limit", "moe_wait_selftest", "moe_arena_refill",
-                 "moe_kv_write", "moe_kv_read", "moe_kv_keep", "moe_tree_attention"):
+                 "moe_kv_write", "moe_kv_read", "moe_kv_keep", "moe_tree_attention", "moe_page_plan", "moe_qk_rotate",
+                 "moe_chunk_attention"):
         L[name].restype = _I
     _lib = L
     return L
@@ -513,3 +520,87 @@ def moe_tree_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor
         _ptr(workspace), workspace.nbytes, _stream(stream))
     if st:
         _check("moe_tree_attention", st)
+
+
+# ------------------------------------------------------------------ a chunk of new tokens: plan, norms and rotation, attention
+
+_STRIDES = struct.Struct("=8q")
+
+
+def moe_page_plan(n_new: torch.Tensor, rows: torch.Tensor, held: torch.Tensor, page_table: torch.Tensor, free_pages: torch.Tensor,
+                  n_free: torch.Tensor, page_size: int, kv_len: torch.Tensor, cu_tokens: torch.Tensor, positions: torch.Tensor,
+                  slots: torch.Tensor, stream=None) -> None:
+    """Plan a batch of n_new[b] new tokens for every lane on the device (see the header): pages from the stack free_pages
+    (int32 [n_pages], n_free int32 [1]) into page_table int32 [lanes, width]; kv_len, cu_tokens [lanes + 1], positions and
+    slots (int64) of the batch's tokens. n_new, rows, held int32 [lanes]; n_new < 0 gives a lane's pages back."""
+    lanes, width = page_table.shape
+    n_pages, T = free_pages.shape[0], slots.shape[0]
+    per_lane = (lanes,)
+    st = (_lib or load()).moe_page_plan(
+        _at(n_new, _I32, per_lane, "n_new"), _at(rows, _I32, per_lane, "rows"), _at(held, _I32, per_lane, "held"),
+        _at(page_table, _I32, (lanes, width), "page_table"), width, lanes, _at(free_pages, _I32, (n_pages,), "free_pages"), n_pages,
+        _at(n_free, _I32, (1,), "n_free"), page_size, _at(kv_len, _I32, per_lane, "kv_len"), _at(cu_tokens, _I32, (lanes + 1,), "cu_tokens"),
+        _at(positions, _I32, (T,), "positions"), _at(slots, _I64, (T,), "slots"), T, _stream(stream))
+    if st:
+        _check("moe_page_plan", st)
+
+
+def _vectors(x: torch.Tensor, dtype: torch.dtype, T: int, dim: int, what: str) -> tuple[int, int, int, int]:
+    """(address, token stride, head stride, heads) of a strided CUDA tensor [T, heads, dim] of this type."""
+    shape = x.shape
+    if len(shape) != 3 or x.dtype is not dtype or not x.is_cuda or shape[0] != T or shape[2] != dim or x.stride(2) != 1:
+        raise ValueError(f"{what}: expected a {dtype} CUDA tensor [{T}, heads, {dim}] with a contiguous last axis")
+    t, h, _ = x.stride()
+    return x.data_ptr(), t, h, shape[1]
+
+
+def moe_qk_rotate(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, turns: torch.Tensor, q_out: torch.Tensor,
+                  k_out: torch.Tensor, q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                  interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
+    """Norm (where a weight is given, fp32 [head_dim]) and rotate queries and keys [tokens, heads, head_dim] by their
+    positions int32 [tokens], in one pass (see the header). bf16, fp16 or fp32, any token and head strides of whole 16 bytes;
+    outputs may be the inputs. turns int64 [pairs] (``rotary.rotary_turns``): 2^-64 turns a position of each pair."""
+    dtype = _DTYPES.get(q.dtype)
+    if dtype is None or len(q.shape) != 3:
+        raise ValueError("q: [tokens, heads, dim] of bf16, fp16 or fp32")
+    T, _, D = q.shape
+    q_at, qt, qh, Q = _vectors(q, q.dtype, T, D, "q")
+    k_at, kt, kh, H = _vectors(k, q.dtype, T, D, "k")
+    qo_at, qot, qoh, Qo = _vectors(q_out, q.dtype, T, D, "q_out")
+    ko_at, kot, koh, Ho = _vectors(k_out, q.dtype, T, D, "k_out")
+    if Q != Qo or H != Ho:
+        raise ValueError(f"q_out, k_out: expected {Q} and {H} heads, got {Qo} and {Ho}")
+    pairs = turns.shape[0]
+    st = (_lib or load()).moe_qk_rotate(
+        q_at, k_at, dtype, _STRIDES.pack(qt, qh, kt, kh, qot, qoh, kot, koh), T, Q, H, D, _at(positions, _I32, (T,), "positions"),
+        _at(turns, _I64, (pairs,), "turns"), pairs, 1 if interleaved else 0, magnitude,
+        None if q_weight is None else _at(q_weight, _F32, (D,), "q_weight"),
+        None if k_weight is None else _at(k_weight, _F32, (D,), "k_weight"), eps, qo_at, ko_at, _stream(stream))
+    if st:
+        _check("moe_qk_rotate", st)
+
+
+def moe_chunk_attention_workspace_bytes(n_tokens: int, n_q_heads: int, n_kv_heads: int, head_dim: int, lanes: int) -> int:
+    return int(load().moe_chunk_attention_workspace_bytes(n_tokens, n_q_heads, n_kv_heads, head_dim, lanes))
+
+
+def moe_chunk_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, kv_len: torch.Tensor, cu_tokens: torch.Tensor,
+                        scale: float, out: torch.Tensor, workspace: torch.Tensor, lse: torch.Tensor | None = None, stream=None) -> None:
+    """Attention of every lane's new tokens over its cache rows up to their own (see the header).
+
+    q bf16 [n_tokens, n_q_heads, head_dim] (strided); kv_len int32 [lanes] (the tokens' rows included); cu_tokens int32
+    [lanes + 1]; out bf16 like q, contiguous; lse fp32 [n_tokens, n_q_heads] or None.
+    """
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError("q: [tokens, heads, dim]")
+    n, heads, _ = shape
+    q_at, qt, qh, _ = _vectors(q, _BF16, n, cache.head_dim, "q")
+    lanes, width = page_table.shape
+    st = (_lib or load()).moe_chunk_attention(
+        q_at, qt, qh, n, heads, cache._st, _at(page_table, _I32, (lanes, width), "page_table"), width, lanes,
+        _at(kv_len, _I32, (lanes,), "kv_len"), _at(cu_tokens, _I32, (lanes + 1,), "cu_tokens"), scale,
+        _at(out, _BF16, shape, "out"), None if lse is None else _at(lse, _F32, (n, heads), "lse"),
+        _ptr(workspace), workspace.nbytes, _stream(stream))
+    if st:
+        _check("moe_chunk_attention", st)

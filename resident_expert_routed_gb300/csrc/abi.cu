@@ -129,7 +129,8 @@ moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_E
 const char* const kKernelNames[MK_COUNT] = {"router_logits_partial", "route_select", "demand_accumulate",
                                             "hot_miss_select", "ffn_plan", "ffn_pack", "ffn_gemm_gate_up",
                                             "ffn_gemm_down", "ffn_combine", "arena_replan", "ring_install", "kv_write",
-                                            "kv_read", "kv_keep", "tree_attention", "tree_attention_join"};
+                                            "kv_read", "kv_keep", "tree_attention", "tree_attention_join", "page_plan",
+                                            "qk_rotate", "chunk_attention", "chunk_attention_join"};
 struct ProfRec {
     int kind;
     cudaEvent_t a, b;

@@ -452,6 +452,7 @@ int moe_sm_count();
 enum MoeKernelKind {
     MK_ROUTER_LOGITS = 0, MK_ROUTE_SELECT, MK_DEMAND, MK_HOT_MISS, MK_PLAN, MK_PACK, MK_GEMM_GATE_UP,
     MK_GEMM_DOWN, MK_COMBINE, MK_REPLAN, MK_RING, MK_KV_WRITE, MK_KV_READ, MK_KV_KEEP, MK_ATTENTION, MK_ATTENTION_JOIN,
+    MK_PAGE_PLAN, MK_QK_ROTATE, MK_CHUNK_ATTENTION, MK_CHUNK_JOIN,
     MK_COUNT
 };
 void moe_prof_begin(int kind, cudaStream_t s);

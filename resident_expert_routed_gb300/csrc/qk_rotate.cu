@@ -1,0 +1,222 @@
+// Queries and keys of each head: root-mean-square norm, then the rotation by the token's position, in one pass.
+//
+//   y = x * w / sqrt(mean(x^2) + eps)                     (without weights: y = x)
+//   (a, b) -> (a cos t - b sin t, b cos t + a sin t) * magnitude,   t = position * f_i,
+// for the pairs of the first 2 n values of a head: (i, i + n), or (2 i, 2 i + 1) where they are interleaved; the others stay y.
+//
+// The frequencies come as whole numbers of 2^-64 turns a position: the product with the position, modulo 2^64, is the
+// exact fraction of a turn, so a far position is as good as a near one and no 64-bit floating point is needed.
+// All else is fp32, rounded once.
+//
+// HBM bounds the large calls: each value is read and written once. D / 8 lanes share a vector (16 bytes a lane of a
+// 16-bit type), one warp takes one token's heads in turn, so a token's sines and cosines are computed once a warp and stay
+// in registers. The partner of a value is on another lane of the same vector (halves) or in the same one (interleaved).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace {
+
+constexpr int ROT_THREADS = 256;
+
+struct RotArgs {
+    const void* q;
+    const void* k;
+    void* q_out;
+    void* k_out;
+    int64_t q_token, q_head, k_token, k_head, qo_token, qo_head, ko_token, ko_head;      // strides, elements
+    int n_tokens, n_q, n_k;                 // heads
+    const int32_t* positions;
+    const int64_t* turns;
+    int pairs;
+    const float* q_weight;
+    const float* k_weight;
+    float eps, magnitude;
+    int per_warp;                           // vectors that a warp's lanes take one after the other
+    int groups;                             // warps to a token
+};
+
+template <typename T> struct Eight;         // eight values as fp32
+template <> struct Eight<float> {
+    static MOE_DEV void load(const void* p, float (&x)[8]) {
+        const float4 a = static_cast<const float4*>(p)[0], b = static_cast<const float4*>(p)[1];
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+    static MOE_DEV void store(void* p, const float (&x)[8]) {
+        static_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        static_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+};
+template <> struct Eight<__nv_bfloat16> {
+    static MOE_DEV void load(const void* p, float (&x)[8]) {
+        const uint4 v = *static_cast<const uint4*>(p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    static MOE_DEV void store(void* p, const float (&x)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <> struct Eight<__half> {
+    static MOE_DEV void load(const void* p, float (&x)[8]) {
+        const uint4 v = *static_cast<const uint4*>(p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+    static MOE_DEV void store(void* p, const float (&x)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+template <typename T, int D, bool PAIRED>   // PAIRED: pairs side by side
+__global__ void __launch_bounds__(ROT_THREADS) qk_rotate(const __grid_constant__ RotArgs a) {
+    constexpr int LPV = D / 8, AT_ONCE = 32 / LPV;             // lanes to a vector, vectors that a warp holds
+    constexpr int N = PAIRED ? 4 : 8;                          // angles a lane needs
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, part = lane % LPV, sub = lane / LPV;
+    const int64_t warp = (int64_t)blockIdx.x * (ROT_THREADS / 32) + (threadIdx.x >> 5);
+    pdl_wait();
+    if (warp >= (int64_t)a.n_tokens * a.groups) return;
+    const int t = (int)(warp / a.groups), group = (int)(warp - (int64_t)t * a.groups);
+    const int at = part * 8, half = a.pairs / 8;               // this lane's first value; lanes to half of the turned part
+    const bool on = at < 2 * a.pairs;
+    const bool second = !PAIRED && part >= half;
+    float c[N], s[N];
+    if (on) {
+        const unsigned long long pos = (unsigned long long)(long long)a.positions[t];
+        const int first = PAIRED ? at / 2 : (second ? at - a.pairs : at);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            // a signed fraction of half a turn: [-1, 1)
+            const int turn = (int)((pos * (unsigned long long)a.turns[first + i]) >> 32);
+            sincospif((float)turn * 0x1p-31f, &s[i], &c[i]);
+            c[i] *= a.magnitude;
+            s[i] *= a.magnitude;
+            if (second) s[i] = -s[i];
+        }
+    }
+    const int partner = (lane - part) + (!on ? part : second ? part - half : part + half);
+    const int heads = a.n_q + a.n_k;
+    const int h0 = group * a.per_warp * AT_ONCE;
+    for (int i = 0; i < a.per_warp; ++i) {
+        const int h = h0 + i * AT_ONCE + sub;
+        const bool there = h < heads;
+        const bool key = h >= a.n_q;
+        const int hh = key ? h - a.n_q : h;
+        float x[8] = {};
+        if (there) {
+            const T* src = key ? static_cast<const T*>(a.k) + t * a.k_token + hh * a.k_head : static_cast<const T*>(a.q) + t * a.q_token + hh * a.q_head;
+            Eight<T>::load(src + at, x);
+        }
+        const float* w = key ? a.k_weight : a.q_weight;
+        float sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
+#pragma unroll
+        for (int o = LPV / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (w) {
+            const float r = 1.0f / sqrtf(sum * (1.0f / D) + a.eps);
+            float wv[8];
+            Eight<float>::load(w + at, wv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= r * wv[e];
+        }
+        if constexpr (PAIRED) {
+            if (on) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float u = x[2 * e], v = x[2 * e + 1];
+                    x[2 * e] = u * c[e] - v * s[e];
+                    x[2 * e + 1] = v * c[e] + u * s[e];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = __shfl_sync(0xFFFFFFFFu, x[e], partner);
+                if (on) x[e] = x[e] * c[e] - v * s[e];
+            }
+        }
+        if (there) {
+            T* dst = key ? static_cast<T*>(a.k_out) + t * a.ko_token + hh * a.ko_head : static_cast<T*>(a.q_out) + t * a.qo_token + hh * a.qo_head;
+            Eight<T>::store(dst + at, x);
+        }
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch(RotArgs a, bool interleaved, cudaStream_t s) {
+    constexpr int AT_ONCE = 32 / (D / 8);
+    const int vectors = (a.n_q + a.n_k + AT_ONCE - 1) / AT_ONCE;        // a token's, in warps' loads
+    // as many vectors a warp as leave 32 warps an SM
+    const int64_t warps = (int64_t)moe_sm_count() * 32;
+    const int64_t per = (int64_t)a.n_tokens * vectors / warps;
+    a.per_warp = (int)(per < 1 ? 1 : per > vectors ? vectors : per);
+    a.groups = (vectors + a.per_warp - 1) / a.per_warp;
+    const int64_t total = (int64_t)a.n_tokens * a.groups;
+    const dim3 grid((unsigned)((total + ROT_THREADS / 32 - 1) / (ROT_THREADS / 32)));
+    return interleaved ? moe_launch(qk_rotate<T, D, true>, grid, dim3(ROT_THREADS), 0, s, a)
+                       : moe_launch(qk_rotate<T, D, false>, grid, dim3(ROT_THREADS), 0, s, a);
+}
+template <typename T>
+cudaError_t launch_dim(const RotArgs& a, int D, bool interleaved, cudaStream_t s) {
+    return D == 64 ? launch<T, 64>(a, interleaved, s) : D == 128 ? launch<T, 128>(a, interleaved, s) : launch<T, 256>(a, interleaved, s);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+
+moe_status moe_qk_rotate(const void* q, const void* k, int dtype, const int64_t* strides, int n_tokens, int n_q_heads, int n_k_heads,
+                         int head_dim, const int32_t* positions, const int64_t* turns, int n_pairs, int interleaved, float magnitude,
+                         const float* q_weight, const float* k_weight, float eps, void* q_out, void* k_out, void* stream) {
+    MOE_RANGE("moe_qk_rotate");
+    if (n_tokens < 0 || n_q_heads < 0 || n_k_heads < 0 || n_q_heads + n_k_heads < 1 || dtype < MOE_BF16 || dtype > MOE_FP32 || !strides) return MOE_EINVAL;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return MOE_EUNSUPPORTED;
+    if (n_pairs < 0 || 2 * (int64_t)n_pairs > head_dim || !(eps >= 0.0f) || eps > 3.0e38f || !(magnitude >= -3.0e38f && magnitude <= 3.0e38f)) return MOE_EINVAL;
+    if (n_pairs % 8 || n_q_heads > 65536 || n_k_heads > 65536) return MOE_EUNSUPPORTED;
+    if (n_tokens == 0) return MOE_OK;
+    if ((n_q_heads && (!q || !q_out)) || (n_k_heads && (!k || !k_out)) || (n_pairs && (!positions || !turns))) return MOE_EINVAL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(q_weight) || !aligned16(k_weight)) return MOE_EINVAL;
+    const int per16 = dtype == MOE_FP32 ? 4 : 8;
+    for (int i = 0; i < 8; ++i)
+        if (strides[i] % per16) return MOE_EINVAL;
+    if ((int64_t)n_tokens * (n_q_heads + n_k_heads) > ((int64_t)1 << 31)) return MOE_EUNSUPPORTED;
+    RotArgs a{};
+    a.q = q; a.k = k; a.q_out = q_out; a.k_out = k_out;
+    a.q_token = strides[0]; a.q_head = strides[1]; a.k_token = strides[2]; a.k_head = strides[3];
+    a.qo_token = strides[4]; a.qo_head = strides[5]; a.ko_token = strides[6]; a.ko_head = strides[7];
+    a.n_tokens = n_tokens; a.n_q = n_q_heads; a.n_k = n_k_heads;
+    a.positions = positions; a.turns = turns; a.pairs = n_pairs;
+    a.q_weight = q_weight; a.k_weight = k_weight; a.eps = eps; a.magnitude = magnitude;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    moe_prof_begin(MK_QK_ROTATE, s);
+    const cudaError_t e = dtype == MOE_BF16   ? launch_dim<__nv_bfloat16>(a, head_dim, interleaved != 0, s)
+                          : dtype == MOE_FP16 ? launch_dim<__half>(a, head_dim, interleaved != 0, s)
+                                              : launch_dim<float>(a, head_dim, interleaved != 0, s);
+    moe_prof_end(MK_QK_ROTATE, s);
+    moe_count_launches(1);
+    return e == cudaSuccess ? MOE_OK : MOE_ECUDA;
+}
