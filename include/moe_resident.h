@@ -591,7 +591,7 @@ moe_status moe_qk_rotate(const void* q, const void* k, int dtype, const int64_t*
  * contents need not be kept or cleared between calls. Calls that overlap on
  * the GPU need one each.
  * scale > 0. n_tokens = 0 returns MOE_OK without a launch. Limits: lanes <= 4096,
- * n_tokens <= 2^24, n_q_heads a multiple of n_kv_heads, at most 1024 and 128 to a kv head.
+ * kv_len <= 2^30 (a lane past it does not fit), n_tokens <= 2^24, n_q_heads a multiple of n_kv_heads, at most 1024 and 128 to a kv head.
  */
 size_t     moe_chunk_attention_workspace_bytes(int n_tokens, int n_q_heads, int n_kv_heads, int head_dim, int lanes);
 moe_status moe_chunk_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int n_tokens,

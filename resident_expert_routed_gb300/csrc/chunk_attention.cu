@@ -1,13 +1,39 @@
-// Attention of a chunk of new tokens over the paged 8-bit key/value cache: a plain kernel.
+// Attention of a chunk of new tokens over the paged 8-bit key/value cache.
 //
-// A block takes 32 rows (token, query head) of one lane and kv head, tiles of
-// 32 cache rows come as fp32 into shared memory, and a running maximum and sum
-// carry the softmax over them. All arithmetic is fp32 on the CUDA cores.
+// For the rows r = (token, query head) of one kv head and the cache rows j up to the token's own:
+//   x[r,j] = scale log2(e) q_r . k_j        (k_j = codes * 2^ek_j)
+//   out[r] = sum_j 2^x[r,j] v_j / sum_j 2^x[r,j]      (v_j = codes * 2^ev_j)
+// The rows are the MMA's M (128 a tile), 128 cache rows its N, fp32 accumulators in TMEM:
+//   S[128, 128] = Q hi K^T + Q lo K^T      kind::f8f6f4 on the cache's codes as TMA brings them; the queries in two e4m3 parts
+//   O[128, D]  += P V                      kind::f16: P in bf16, from TMEM; V in bf16
+//   - A bf16 query has 8 significant bits and e4m3 has 4: with its rows scaled by a power of two to at most 256, hi =
+//     e4m3(q) and lo = e4m3(q - hi) hold it exactly down to 2^-9 of the maximum and within 2^-17 of the maximum below. Two
+//     8-bit products cost what one of 16 bits costs, and no key is converted.
+//   - A key row's scale is the factor of its column of scores: one fused multiply-add takes it and the reference.
+//   - e4m3 codes times a power of two are exact in bf16, and bf16 has the exponents of fp32: weights and values
+//     need no care about their range. Four warps convert each tile of values once for the 256 rows that use it.
+//   - m is a running reference, not each tile's maximum: it stays until a score passes it by 2^8 (p then up to 2^8, in
+//     bf16 as good as below 1), and only then O and the sum are scaled down. A thread has a row to itself, so neither
+//     maximum nor sum needs another thread.
+// Scores, sums, O and the parts that the join adds up are fp32; weights are rounded to bf16, the output once.
+//
+// A unit is a block of 256 rows (128 at head_dim 256, where O fills TMEM) of a lane and kv head, whole tokens with all their
+// heads, so 256 / group tokens share each tile of the cache and the causal edge is as near as can be. Its tiles of cache
+// rows come one after the other; the two tiles of 128 rows take turns: while one's softmax runs, the other's products do.
+// A unit of at most 128 rows (single tokens among them) has one row tile and two buffers of S.
+//
+// Work: the units are laid end to end and cut into equal parts, one per CTA. A unit that one CTA does whole is written at
+// once; the others leave parts (O, reference, sum) in the workspace, and chunk_attention_join adds them up in order.
+//
+// Roles, 16 warps: two softmax groups of four; four that convert values and prepare queries; TMA; MMA issue; scales; a
+// watchdog that bounds all waits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "common.cuh"
+#include <climits>
+
+#include "attention.cuh"
 
 namespace {
 
@@ -15,134 +41,1068 @@ struct ChunkArgs {
     moe_kv_cache c;
     const __nv_bfloat16* q;
     int64_t q_token, q_head;
-    int n_tokens, n_q, group;
+    int n_tokens, n_q, group, block;             // group: query heads to a kv head; block: tokens of a unit
+    uint32_t by_group;                           // ceil(2^16 / group): divides a row of a unit by group
     const int32_t* table;
     int width, lanes, page_shift;
     const int32_t* kv_len;
     const int32_t* cu;
+    int whole;                                   // units are not cut
     float scale_log2;
     __nv_bfloat16* out;
     float* lse;
+    uint8_t* ws;
     uint32_t* err;
+    uint64_t wait_ns;
 };
 
-constexpr int ROWS = 32, TILE = 32, WARPS = 8;
+struct ChunkMaps {
+    CUtensorMap k, v;                            // (head_dim, rows) bytes; boxes: an operand panel of keys, whole rows of values
+};
+
+constexpr int TILE = 128;                        // cache rows a tile, and rows a row tile
+constexpr int WHOLE_TILES = 8;                   // a table of at most so many tiles: units are not cut
+constexpr float NEVER = -1e30f;                  // the reference of a row that has seen nothing
+constexpr float LIMIT = 8.0f;                    // log2 of the largest weight before the reference moves
+
+// The run's measure: a cache row of a unit with two row tiles, of one with one; a unit beside its rows.
+constexpr int FULL_COST = 4, HALF_COST = 3, UNIT_COST = 512;
+constexpr int LEAST_PART = 2048;                 // of a part
+
+struct Pos {                                     // a place in the run
+    int lane, unit, tile, pad;
+};
+MOE_DEV bool same_unit(const Pos& a, const Pos& b) { return a.lane == b.lane && a.unit == b.unit; }
+MOE_DEV bool before(const Pos& a, const Pos& b) {
+    return a.lane != b.lane ? a.lane < b.lane : a.unit != b.unit ? a.unit < b.unit : a.tile < b.tile;
+}
 
 template <int D>
-__global__ void __launch_bounds__(WARPS * 32) chunk_attention(const ChunkArgs a) {
-    extern __shared__ float sm[];
-    float* Q = sm;                          // [ROWS][D]
-    float* K = Q + ROWS * D;                // [TILE][D + 1]
-    float* V = K + TILE * (D + 1);          // [TILE][D]
-    __shared__ int place[4];
-    pdl_trigger();
-    pdl_wait();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y, G = a.group;
-    if (tid == 0) {                         // the lane whose rows this block has
-        int u = blockIdx.x, b = 0;
-        place[0] = -1;
-        for (; b < a.lanes; ++b) {
-            const int n0 = a.cu[b], n = a.cu[b + 1] - n0;
-            if (n0 < 0 || n < 0 || n > a.n_tokens - n0) { if (h == 0) record_error(a.err, MOE_DEV_BAD_PAGE); continue; }
-            const int units = (n * G + ROWS - 1) / ROWS;
-            if (u < units) { place[0] = n0; place[1] = n; place[2] = u * ROWS; place[3] = b; break; }
-            u -= units;
+struct Cfg {
+    static constexpr int NT = D <= 128 ? 2 : 1;               // row tiles of a unit
+    static constexpr int ROWS = NT * TILE;
+    static constexpr int THREADS = 512;
+    static constexpr int ROWB = D >= 128 ? 128 : 64;          // bytes of an operand row of keys and queries: one swizzle atom
+    static constexpr int PANELS = D / ROWB;
+    static constexpr int KPANEL = TILE * ROWB, KSLOT = TILE * D;
+    static constexpr int QPANEL = 2 * TILE * ROWB, QTILE = 2 * TILE * D;      // hi, then lo
+    static constexpr int NK = D == 64 ? 6 : D == 128 ? 3 : 2; // ring of key tiles
+    static constexpr int VR = D == 256 ? 32 : 64;             // values come in pieces of so many rows
+    static constexpr int PIECES = TILE / VR;
+    static constexpr int NR = D == 64 ? 8 : D == 128 ? 4 : 3; // ring of pieces as codes
+    static constexpr int RSLOT = VR * D;
+    static constexpr int NB = D == 64 ? 6 : 4;                // ring of pieces in bf16
+    static constexpr int VPANEL = VR * 128, BSLOT = VR * D * 2;
+    static constexpr int SA = 4, NSC = 2 * SA;                // tiles that scales are under way ahead; their ring:
+    static constexpr int SC_BYTES = 3 * TILE * 2;             // key bytes, value bytes, the columns' factors (float)
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = OFF_Q + NT * QTILE;
+    static constexpr int OFF_R = OFF_K + NK * KSLOT;
+    static constexpr int OFF_B = OFF_R + NR * RSLOT;
+    static constexpr int OFF_SC = OFF_B + NB * BSLOT;
+    static constexpr int OFF_SID = OFF_SC + NSC * SC_BYTES;   // page ids, [2 SA][32]
+    // What the softmax reads of a part's queries: of four parts, as the next parts' queries may be ready before a part of one
+    // tile is begun (its scores wait for those of two items before alone).
+    static constexpr int QB = 4;
+    static constexpr int OFF_QF = OFF_SID + 2 * SA * 128;     // [QB][ROWS] 2^-a of the queries' rows
+    static constexpr int OFF_QU = OFF_QF + QB * ROWS * 4;     // [QB][2] 2^-a of a unit's rows; whether they differ instead
+    static constexpr int OFF_QX = OFF_QU + QB * 8;            // [2][largest, smallest][4 warps]
+    static constexpr int OFF_BAR = OFF_QX + 64;
+    static constexpr int B_KFULL = OFF_BAR;                   // [NK] a tile of keys has arrived
+    static constexpr int B_KEMPTY = B_KFULL + 8 * NK;         // [NK] ... has been used
+    static constexpr int B_RFULL = B_KEMPTY + 8 * NK;         // [NR] a piece of values has arrived
+    static constexpr int B_REMPTY = B_RFULL + 8 * NR;
+    static constexpr int B_BFULL = B_REMPTY + 8 * NR;         // [NB] ... is there in bf16
+    static constexpr int B_BEMPTY = B_BFULL + 8 * NB;
+    static constexpr int B_SCFULL = B_BEMPTY + 8 * NB;        // [NSC] a tile's factors and value bytes are there
+    static constexpr int B_SCEMPTY = B_SCFULL + 8 * NSC;
+    static constexpr int B_SFULL = B_SCEMPTY + 8 * NSC;       // [2] S is ready
+    static constexpr int B_PFULL = B_SFULL + 16;              // [2] P is written (S has been read)
+    static constexpr int B_ODONE = B_PFULL + 16;              // [2] P has been used: a tile is added to O
+    static constexpr int B_QFULL = B_ODONE + 16;              // [QB] the queries of a part are there
+    static constexpr int B_QFREE = B_QFULL + 8 * QB;              // ... have been used
+    static constexpr int B_QMAX = B_QFREE + 8;                // the four warps have their maxima
+    static constexpr int B_DONE = B_QMAX + 8;                 // the block's last output is written
+    static constexpr int B_DRAIN = B_DONE + 8;
+    static constexpr int OFF_MISC = (B_DRAIN + 8 + 15) / 16 * 16;     // tmem slot, abort flag, progress [2], start, end
+    static constexpr int SMEM = OFF_MISC + 16 + 32 + 1024;
+    static constexpr int TMEM_O = 2 * TILE;                   // after S [2]
+    static constexpr int SOFT_REGS = 184, CONV_REGS = 96, REST_REGS = 48;     // 2 x 184 + 96 + 48 <= 4 x 128
+    static_assert(OFF_B % 1024 == 0 && OFF_R % 128 == 0 && OFF_K % 1024 == 0 && BSLOT % 1024 == 0, "alignment");
+    static_assert(OFF_BAR % 8 == 0 && OFF_QF % 16 == 0 && SMEM <= 227 * 1024, "shared memory");
+    static_assert(2 * SOFT_REGS + CONV_REGS + REST_REGS <= 512, "registers");
+    static constexpr size_t PART_FLOATS = (size_t)ROWS * (D + 2);     // O [D / 4][ROWS][4], references, sums
+};
+constexpr size_t parts_offset(int ctas) { return ((size_t)(ctas + 1) * sizeof(Pos) + 255) / 256 * 256; }
+
+// ------------------------------------------------------------------ device pieces
+
+MOE_DEV void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// kind::f16, bf16 x bf16 -> fp32, B with N contiguous.
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+MOE_DEV void tc_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+MOE_DEV void tc_st_x32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
+        "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+          "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+          "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+MOE_DEV uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+MOE_DEV uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+MOE_DEV void arrive_at_n(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+MOE_DEV float4 read4_at(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+    return v;
+}
+
+// ------------------------------------------------------------------ lanes, units, the cut
+
+// A lane that does not fit (see the header): no rows, and its outputs become zeros; one whose tokens would lead out of q
+// has none either.
+struct Lane {
+    int n0, n, len;
+};
+MOE_DEV Lane lane_facts(const ChunkArgs& a, int b, bool* bad) {
+    Lane l;
+    l.n0 = a.cu[b];
+    l.n = a.cu[b + 1] - l.n0;
+    l.len = a.kv_len[b];
+    *bad = false;
+    if (l.n0 < 0 || l.n < 0 || l.n > a.n_tokens - l.n0) {
+        *bad = true;
+        l.n0 = l.n = l.len = 0;
+    } else if (l.n > 0 && (l.len < l.n || l.len > 1 << 30 || (((int64_t)l.len + (1 << a.page_shift) - 1) >> a.page_shift) > a.width)) {
+        *bad = true;
+        l.len = 0;
+    }
+    return l;
+}
+
+struct Unit {
+    int b, h;                                    // lane, kv head
+    int tok0;                                    // the unit's first token, in q
+    int first;                                   // that token's own row in the lane; -2^30 where the lane is refused
+    int rows, nt;                                // rows (token, head) of the unit; row tiles
+    int end, tiles;                              // rows of the lane that it sees at all; tiles of them
+    int units;                                   // of the lane
+};
+template <int D>
+MOE_DEV Unit unit_at(const ChunkArgs& a, int b, int u) {
+    bool bad;
+    const Lane l = lane_facts(a, b, &bad);
+    Unit x;
+    const int blocks = l.n > 0 ? (l.n + a.block - 1) / a.block : 1;
+    x.b = b;
+    x.h = u / blocks;
+    const int rb = u - x.h * blocks, t0 = rb * a.block;
+    const int tokens = min(a.block, l.n - t0);
+    x.tok0 = l.n0 + t0;
+    x.rows = tokens * a.group;
+    x.nt = x.rows > TILE ? 2 : 1;
+    x.first = l.len > 0 ? l.len - l.n + t0 : -(1 << 30);
+    x.end = l.len > 0 ? x.first + tokens : 0;
+    x.tiles = x.end > 0 ? (x.end + TILE - 1) / TILE : 1;
+    x.units = a.c.n_kv_heads * blocks;
+    return x;
+}
+// The unit after p's, at its first tile.
+MOE_DEV Pos after(const ChunkArgs& a, const Pos& p, int units, const Pos& end) {
+    Pos n{p.lane, p.unit + 1, 0, 0};
+    if (n.unit < units) return n;
+    n.unit = 0;
+    bool bad;
+    do ++n.lane; while (n.lane < end.lane && lane_facts(a, n.lane, &bad).n == 0);
+    return n;
+}
+
+// Costs of the units before block rb of a head with n tokens (rb full blocks; the last may be short).
+struct LaneCost {
+    long long base, step;                        // cost of block r: base + step (r + 1), but for the last
+    long long last;                              // of the last block
+    int blocks;
+    MOE_DEV unsigned long long upto(int rb) const { return (unsigned long long)(base * rb + step * rb * (rb + 1) / 2); }
+    MOE_DEV unsigned long long head() const { return blocks ? upto(blocks - 1) + (unsigned long long)last : 0ull; }
+};
+template <int D>
+MOE_DEV LaneCost lane_cost(const ChunkArgs& a, const Lane& l) {
+    LaneCost c{0, 0, 0, 0};
+    if (l.n == 0) return c;
+    c.blocks = (l.n + a.block - 1) / a.block;
+    if (a.whole) {
+        c.base = c.last = 1;
+        return c;
+    }
+    const int left = (l.n - (c.blocks - 1) * a.block) * a.group;
+    const int w = Cfg<D>::NT == 2 && left <= TILE ? HALF_COST : FULL_COST;
+    c.base = c.last = UNIT_COST;
+    if (l.len > 0) {
+        c.base += (long long)FULL_COST * (l.len - l.n);
+        c.step = (long long)FULL_COST * a.block;
+        c.last += (long long)w * l.len;
+    }
+    return c;
+}
+
+// Every CTA adds up all lanes' costs and finds where its part begins and ends.
+template <int D>
+__device__ __noinline__ void cut_run(const ChunkArgs& a, unsigned long long* scratch, Pos* here) {
+    const int tid = threadIdx.x, H = a.c.n_kv_heads;
+    unsigned long long all = 0, at = 0, size = 0;
+    Lane l{0, 0, 0};
+    LaneCost c{0, 0, 0, 0};
+    auto scan_lanes = [&](int b0, bool tell) {
+        const int b = b0 + tid;
+        l = Lane{0, 0, 0};
+        if (b < a.lanes) {
+            bool bad;
+            l = lane_facts(a, b, &bad);
+            if (bad && tell && blockIdx.x == 0) record_error(a.err, MOE_DEV_BAD_PAGE);
+        }
+        c = lane_cost<D>(a, l);
+        size = (unsigned long long)H * c.head();
+        unsigned long long x = size, y = 0, tx, ty;
+        scan2(x, y, scratch, &tx, &ty);
+        at = all + x - size;
+        all += tx;
+    };
+    for (int b0 = 0; b0 < a.lanes; b0 += (int)blockDim.x) scan_lanes(b0, true);
+    const unsigned long long total = all;
+    unsigned long long most = a.whole ? total : total / LEAST_PART;
+    if (most < 1) most = 1;
+    const int parts = most < gridDim.x ? (int)most : (int)gridDim.x;
+    const unsigned long long first = (int)blockIdx.x < parts ? (unsigned long long)part_begin(total, parts, blockIdx.x) : total;
+    const unsigned long long next = (int)blockIdx.x < parts ? (unsigned long long)part_begin(total, parts, blockIdx.x + 1) : total;
+    if (tid < 2) here[tid] = Pos{a.lanes, 0, 0, 0};
+    auto locate = [&](int b0) {                  // by the thread whose lane it is in
+        for (int z = 0; z < 2; ++z) {
+            const unsigned long long x = z ? next : first;
+            if (x < at || x >= at + size) continue;
+            const unsigned long long off = x - at, head = c.head();
+            const int h = (int)(off / head);
+            const unsigned long long rest = off - h * head;
+            int lo = 0, hi = c.blocks - 1;       // the last block that begins at or before rest
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (c.upto(mid) <= rest) lo = mid; else hi = mid - 1;
+            }
+            int tile = 0;
+            const unsigned long long in = rest - c.upto(lo);
+            if (!a.whole && in > UNIT_COST) {
+                const int left = (l.n - lo * a.block) * a.group;
+                const int w = Cfg<D>::NT == 2 && left <= TILE ? HALF_COST : FULL_COST;
+                tile = (int)((in - UNIT_COST) / (unsigned long long)(w * TILE));
+            }
+            here[z] = Pos{b0 + tid, h * c.blocks + lo, tile, 0};
+        }
+    };
+    __syncthreads();
+    if (a.lanes <= (int)blockDim.x) {
+        locate(0);
+    } else {
+        all = 0;
+        for (int b0 = 0; b0 < a.lanes; b0 += (int)blockDim.x) {
+            scan_lanes(b0, false);
+            locate(b0);
         }
     }
     __syncthreads();
-    if (place[0] < 0) return;
-    const int n0 = place[0], n = place[1], row0 = place[2], b = place[3];
-    const int rows = min(ROWS, n * G - row0);
-    int len = a.kv_len[b];
-    bool refused = len < n || (((int64_t)len + (1 << a.page_shift) - 1) >> a.page_shift) > a.width;
-    if (refused) { if (tid == 0) record_error(a.err, MOE_DEV_BAD_PAGE); len = 0; }
-    const int prefix = len - n;
-    for (int i = tid; i < rows * D; i += WARPS * 32) {
-        const int r = i / D, d = i % D, t = (row0 + r) / G, g = (row0 + r) % G;
-        Q[i] = __bfloat162float(a.q[(n0 + t) * a.q_token + (h * G + g) * a.q_head + d]) * a.scale_log2;
-    }
-    constexpr int V_ = D / 32, RW = ROWS / WARPS;
-    float o[RW][V_] = {}, m[RW], l[RW];
-    for (int r = 0; r < RW; ++r) { m[r] = -INFINITY; l[r] = 0.0f; }
-    const int end = refused ? 0 : prefix + (row0 + rows - 1) / G + 1;
-    for (int j0 = 0; j0 < end; j0 += TILE) {
-        __syncthreads();
-        for (int i = tid; i < TILE * D; i += WARPS * 32) {
-            const int j = j0 + i / D, d = i % D;
-            float kf = 0.0f, vf = 0.0f;
-            if (j < end) {
-                int page = a.table[(int64_t)b * a.width + (j >> a.page_shift)];
-                if (page < 0 || page >= a.c.n_pages) { record_error(a.err, MOE_DEV_BAD_PAGE); page = 0; }
-                const int64_t row = (((int64_t)page * a.c.n_kv_heads + h) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
-                auto value = [&](const void* codes, const uint8_t* scales) {
-                    const uint32_t s = scales[row];
-                    const __nv_fp8_storage_t code = static_cast<const uint8_t*>(codes)[row * D + d];
-                    return __half2float(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3))) * e8m0_to_float(s);
-                };
-                kf = value(a.c.k_codes, a.c.k_scales);
-                vf = value(a.c.v_codes, a.c.v_scales);
-            }
-            K[(i / D) * (D + 1) + d] = kf;
-            V[i] = vf;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < RW; ++r) {
-            const int row = warp * RW + r;
-            if (row >= rows) continue;
-            const int limit = prefix + (row0 + row) / G;         // the last row it sees
-            float s = 0.0f;
-            for (int d = 0; d < D; ++d) s = fmaf(Q[row * D + d], K[lane * (D + 1) + d], s);
-            const bool sees = j0 + lane <= limit;
-            if (!sees) s = -INFINITY;
-            float top = s;
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-            top = fmaxf(top, m[r]);
-            const float base = top == -INFINITY ? 0.0f : top;
-            const float p = exp2f(s - base), f = exp2f(m[r] - base);
-            float sum = p;
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-            l[r] = l[r] * f + sum;
-            m[r] = top;
-#pragma unroll
-            for (int e = 0; e < V_; ++e) o[r][e] *= f;
-            const int seen = min(TILE, limit + 1 - j0);
-            for (int j = 0; j < seen; ++j) {
-                const float pj = __shfl_sync(0xFFFFFFFFu, p, j);
-#pragma unroll
-                for (int e = 0; e < V_; ++e) o[r][e] = fmaf(pj, V[j * D + e * 32 + lane], o[r][e]);
-            }
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < RW; ++r) {
-        const int row = warp * RW + r;
-        if (row >= rows) continue;
-        const int t = (row0 + row) / G, g = (row0 + row) % G;
-        const int64_t at = (int64_t)(n0 + t) * a.n_q + h * G + g;
-        for (int e = 0; e < V_; ++e) a.out[at * D + e * 32 + lane] = __float2bfloat16_rn(refused ? 0.0f : o[r][e] / l[r]);
-        if (a.lse && lane == 0) a.lse[at] = refused ? -INFINITY : (m[r] + log2f(l[r])) * 0.69314718055994531f;
+    if (tid == 0 && !a.whole) {
+        Pos* to = reinterpret_cast<Pos*>(a.ws);
+        to[blockIdx.x] = here[0];
+        if (blockIdx.x == gridDim.x - 1) to[gridDim.x] = here[1];
     }
 }
 
 template <int D>
-cudaError_t launch(const ChunkArgs& a, cudaStream_t s) {
-    const size_t smem = (size_t)(ROWS * D + TILE * (D + 1) + TILE * D) * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(chunk_attention<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    const int64_t units = (int64_t)a.n_tokens * a.group / ROWS + a.lanes;
-    return moe_launch(chunk_attention<D>, dim3((unsigned)units, (unsigned)a.c.n_kv_heads), dim3(WARPS * 32), smem, s, a);
+__global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkArgs a) {
+    using C = Cfg<D>;
+    constexpr int NK = C::NK, NR = C::NR, NB = C::NB, NSC = C::NSC, QB = C::QB, ROWS = C::ROWS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const uint32_t base = smem_u32(smem), stop = base + C::OFF_MISC + 4;
+    auto bar = [&](int offset, uint32_t i = 0) { return base + offset + 8 * i; };
+    auto bar_ptr = [&](int offset) { return reinterpret_cast<uint64_t*>(smem + offset); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+    volatile uint32_t* progress = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 8);      // tiles added; parts out
+    Pos* ends = reinterpret_cast<Pos*>(smem + C::OFF_MISC + 16);
+
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
+    const int G = a.group;
+    pdl_trigger();
+    if (tid == 0) {
+        auto init = [&](int offset, int n, int arrivals) {
+            for (int i = 0; i < n; ++i) mbar_init(bar_ptr(offset) + i, arrivals);
+        };
+        init(C::B_KFULL, NK, 1); init(C::B_KEMPTY, NK, 1); init(C::B_RFULL, NR, 1); init(C::B_REMPTY, NR, 4);
+        init(C::B_BFULL, NB, 4); init(C::B_BEMPTY, NB, 1); init(C::B_SCFULL, NSC, 1); init(C::B_SCEMPTY, NSC, 12);
+        init(C::B_SFULL, 2, 1); init(C::B_PFULL, 2, 4); init(C::B_ODONE, 2, 1); init(C::B_QFULL, QB, 4); init(C::B_QFREE, 1, 1);
+        init(C::B_QMAX, 1, 4); init(C::B_DONE, 1, 8); init(C::B_DRAIN, 1, 1);
+        *abort_flag = 0;
+        progress[0] = progress[1] = 0;
+        fence_barrier_init();
+        prefetch_tmap(&maps.k);
+        prefetch_tmap(&maps.v);
+    }
+    if (warp == 13) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
+    pdl_wait();
+    cut_run<D>(a, reinterpret_cast<unsigned long long*>(smem + C::OFF_Q), ends);      // (the queries' room, not yet in use)
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Pos end = ends[1];
+    Pos at = ends[0];
+    uint32_t issued_k = 0, issued_r = 0;             // ring fills, by the producer
+    // tiles [at.tile, last) of unit x belong to this CTA
+    auto last_tile = [&](const Unit& x) { return same_unit(at, end) ? min(end.tile, x.tiles) : x.tiles; };
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ softmax: a thread is a row
+        regs_up<C::SOFT_REGS>();
+        const int g = warp >> 2, wl = warp & 3, j = tid & 127;
+        const uint32_t trow = tmem + ((uint32_t)(wl * 32) << 16);
+        uint32_t items = 0, tiles = 0, piece = 0;    // of the CTA: items (tile, row tile), tiles, parts
+        bool ok = true;
+        while (ok && before(at, end)) {
+            const Unit x = unit_at<D>(a, at.lane, at.unit);
+            const int t0 = at.tile, t1 = last_tile(x), nt = t1 - t0;
+            if (nt > 0) {
+                // (a group that has no rows here waits too: it may not run ahead of barriers whose phases it does not see)
+                if (!warp_wait_at(bar(C::B_QFULL, piece % QB), (piece / QB) & 1, stop)) break;
+                if (g < x.nt) {
+                    const uint32_t o_at = trow + C::TMEM_O + g * (C::NT == 2 ? D : 0);
+                    const int row = g * TILE + j;
+                    const int u = row < x.rows ? row : x.rows - 1;
+                    const int t = (int)((uint32_t)u * a.by_group >> 16);
+                    const int limit = x.first + t;                   // the last cache row that this row sees
+                    const int open = x.first + (int)((uint32_t)(g * TILE) * a.by_group >> 16);       // that every row of the tile sees
+                    const float2 unit = *reinterpret_cast<const float2*>(smem + C::OFF_QU + (piece % QB) * 8);
+                    const bool rowwise = unit.y != 0.0f;
+                    const float rf = rowwise ? *reinterpret_cast<const float*>(smem + C::OFF_QF + ((piece % QB) * ROWS + row) * 4) : 1.0f;
+                    const f32x2 rf2 = pack2(rf, rf);
+                    float m = NEVER, l = 0.0f;
+                    for (int i = 0; i < nt; ++i) {
+                        const uint32_t item = items + i * x.nt + g, buf = item & 1, sc = (tiles + i) % NSC;
+                        const uint32_t s_at = trow + buf * TILE, k_at = base + C::OFF_SC + sc * C::SC_BYTES + 2 * TILE;
+                        const int j0 = (t0 + i) * TILE;
+                        const bool masked = j0 + TILE - 1 > open;
+                        const int rel = limit - j0;                  // columns up to rel are seen
+                        if (!warp_wait_at(bar(C::B_SCFULL, sc), ((tiles + i) / NSC) & 1, stop)) { ok = false; break; }
+                        if (!warp_wait_at(bar(C::B_SFULL, buf), (item >> 1) & 1, stop)) { ok = false; break; }
+                        tc_fence_after();
+                        uint32_t P[64];
+                        for (bool moved = false;; moved = true) {
+                            const f32x2 m2 = pack2(-m, -m);
+                            float top = -INFINITY;
+                            f32x2 sum0 = 0ull, sum1 = 0ull;
+                            uint32_t s[2][32];
+                            tc_ld_x32(s_at, s[0]);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                tc_wait_ld();
+                                // (the loads' registers are complete only past the wait: nothing that reads them may move above it)
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(s[c & 1][e]));
+                                if (c < 3) tc_ld_x32(s_at + (c + 1) * 32, s[(c + 1) & 1]);
+                                f32x2 y[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) y[e] = pack2(__uint_as_float(s[c & 1][2 * e]), __uint_as_float(s[c & 1][2 * e + 1]));
+                                if (rowwise) {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) y[e] = mul2(y[e], rf2);
+                                }
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const float4 k = read4_at(k_at + c * 128 + e * 16);
+                                    y[2 * e] = fma2(y[2 * e], pack2(k.x, k.y), m2);
+                                    y[2 * e + 1] = fma2(y[2 * e + 1], pack2(k.z, k.w), m2);
+                                }
+                                if (masked) {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        const float2 v = unpack2(y[e]);
+                                        y[e] = pack2(c * 32 + 2 * e <= rel ? v.x : -INFINITY, c * 32 + 2 * e + 1 <= rel ? v.y : -INFINITY);
+                                    }
+                                }
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    const float2 v = unpack2(y[e]);
+                                    top = max3(top, v.x, v.y);
+                                    const float p0 = ex2(v.x), p1 = ex2(v.y);
+                                    if (e & 1) sum1 = add2(sum1, pack2(p0, p1));
+                                    else sum0 = add2(sum0, pack2(p0, p1));
+                                    P[c * 16 + e] = pack_bf16(p0, p1);
+                                }
+                            }
+                            // (scores of 2^27 and more may pass the limit by their rounding alone)
+                            if (moved || !__any_sync(0xFFFFFFFFu, top > LIMIT)) {
+                                const float2 p = unpack2(add2(sum0, sum1));
+                                l += p.x + p.y;
+                                break;
+                            }
+                            // the reference moves to the largest score so far, what has been added up with it
+                            float most = -INFINITY;
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t s1[32];
+                                tc_load(s_at + c * 32, s1);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const float k = __uint_as_float((uint32_t)read_at(k_at + c * 128 + e * 4));
+                                    const float v = __uint_as_float(s1[e]) * rf * k;
+                                    if (c * 32 + e <= rel) most = fmaxf(most, v);
+                                }
+                            }
+                            const float mn = fmaxf(m, most);
+                            const float alpha = ex2(m - mn);
+                            l *= alpha;
+                            m = mn;
+                            if (i > 0) {
+                                if (!warp_wait_at(bar(C::B_ODONE, (item - x.nt) & 1), ((item - x.nt) >> 1) & 1, stop)) { ok = false; break; }
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int c = 0; c < D / 32; ++c) {
+                                    uint32_t o[32];
+                                    tc_load(o_at + c * 32, o);
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                    tc_st_x32(o_at + c * 32, o);
+                                }
+                                tc_wait_st();
+                            }
+                        }
+                        if (!ok) break;
+                        tc_st_x32(s_at, P);
+                        tc_st_x32(s_at + 32, P + 32);
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            arrive_at(bar(C::B_PFULL, buf));
+                            arrive_at_n(bar(C::B_SCEMPTY, sc), x.nt == 2 ? 1 : 2);
+                        }
+                    }
+                    if (!ok) break;
+                    // ---- the part's output
+                    const uint32_t ended = items + (nt - 1) * x.nt + g;
+                    if (!warp_wait_at(bar(C::B_ODONE, ended & 1), (ended >> 1) & 1, stop)) break;
+                    tc_fence_after();
+                    const bool live = row < x.rows;
+                    if (t0 == 0 && t1 == x.tiles) {
+                        const int64_t to = (int64_t)(x.tok0 + t) * a.n_q + x.h * G + u - t * G;
+                        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                        if (a.lse && live) a.lse[to] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + to * D);
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tc_load(o_at + c * 32, o);
+                            uint32_t v[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) v[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                            if (live)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) dst[c * 4 + e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                        }
+                    } else {
+                        float* part = reinterpret_cast<float*>(a.ws + parts_offset(gridDim.x)) + (size_t)(2 * blockIdx.x + (t0 > 0 ? 0 : 1)) * C::PART_FLOATS;
+                        part[ROWS * D + row] = m;
+                        part[ROWS * D + ROWS + row] = l;
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tc_load(o_at + c * 32, o);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<uint4*>(part + ((size_t)(c * 8 + e) * ROWS + row) * 4) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                    }
+                    tc_fence_before();
+                    if (lane == 0 && wl == 0 && g == 0) progress[1] = piece + 1;
+                }
+                items += nt * x.nt;
+                tiles += nt;
+                ++piece;
+            }
+            at = after(a, at, x.units, end);
+        }
+        __syncwarp();
+        if (lane == 0) arrive_at(bar(C::B_DONE));
+    } else if (warp < 12) {
+        // ------------------------------------------------------------ queries in two parts; values in bf16
+        regs_down<C::CONV_REGS>();
+        const int wl = warp & 3, ct = tid & 127;
+        // A unit's queries: their largest size first, then the parts.
+        auto prepare = [&](const Unit& x, uint32_t piece) -> bool {
+            constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = 4 * RPW;        // lanes a row, rows a warp takes at once, all four
+            constexpr int BATCH = 8;
+            const int part = lane % LPR, mine = wl * RPW + lane / LPR;
+            const int rounds = x.nt * TILE / STEP;
+            const __nv_bfloat16* q = a.q + (int64_t)x.tok0 * a.q_token + (int64_t)x.h * G * a.q_head + part * 8;
+            auto load = [&](int u) {
+                if (u >= x.rows) return make_uint4(0u, 0u, 0u, 0u);
+                const int t = (int)((uint32_t)u * a.by_group >> 16);
+                return *reinterpret_cast<const uint4*>(q + t * a.q_token + (u - t * G) * a.q_head);
+            };
+            float* qf = reinterpret_cast<float*>(smem + C::OFF_QF) + (piece % QB) * ROWS;
+            uint32_t* keys = reinterpret_cast<uint32_t*>(qf);
+            if (piece > 0 && !warp_wait_at(bar(C::B_QFREE), (piece - 1) & 1, stop)) return false;
+            uint32_t most = 0, least = 0x7FFFu;
+#pragma unroll 1
+            for (int r0 = 0; r0 < rounds; r0 += BATCH) {
+                uint4 raw[BATCH];
+#pragma unroll
+                for (int b = 0; b < BATCH; ++b) raw[b] = load((r0 + b) * STEP + mine);
+#pragma unroll
+                for (int b = 0; b < BATCH; ++b) {
+                    auto abs2 = [](uint32_t v) {
+                        v &= 0x7FFF7FFFu;
+                        return *reinterpret_cast<const __nv_bfloat162*>(&v);
+                    };
+                    __nv_bfloat162 v = __hmax2_nan(__hmax2_nan(abs2(raw[b].x), abs2(raw[b].y)), __hmax2_nan(abs2(raw[b].z), abs2(raw[b].w)));
+                    v = __hmax2_nan(v, __lowhigh2highlow(v));
+#pragma unroll
+                    for (int o = LPR / 2; o > 0; o >>= 1) v = __hmax2_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+                    const uint32_t key = *reinterpret_cast<const uint32_t*>(&v) & 0xFFFFu;
+                    if (part == 0) keys[(r0 + b) * STEP + mine] = key;
+                    most = max(most, key);
+                    if (key) least = min(least, key);
+                }
+            }
+            uint32_t* qx = reinterpret_cast<uint32_t*>(smem + C::OFF_QX) + (piece & 1) * 8;
+            most = __reduce_max_sync(0xFFFFFFFFu, most);
+            least = __reduce_min_sync(0xFFFFFFFFu, least);
+            if (lane == 0) {
+                qx[wl] = most;
+                qx[4 + wl] = least;
+                arrive_at(bar(C::B_QMAX));
+            }
+            if (!warp_wait_at(bar(C::B_QMAX), piece & 1, stop)) return false;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                most = max(most, qx[w]);
+                least = min(least, qx[4 + w]);
+            }
+            // Rows within 2^4 of one another share one power of two, and the scores need no factor of their row's; the
+            // smallest rows' low parts then end 2^-13 below their own maximum. (Subnormal rows count as 2^-126.)
+            auto up_of = [](uint32_t k) {            // 2^up * maximum is in [128, 256)
+                const int up = k ? 134 - (int)(k >> 7) : 0;
+                return up > 120 ? 120 : (up < -120 ? -120 : up);
+            };
+            const int unit_up = up_of(most);
+            const bool rowwise = most >= 0x7F80u || (least < most && up_of(least) - unit_up > 4);
+            if (wl == 0 && lane == 0)
+                *reinterpret_cast<float2*>(smem + C::OFF_QU + (piece % QB) * 8) = make_float2(rowwise ? 1.0f : exp2_int(-unit_up), rowwise ? 1.0f : 0.0f);
+            const int panel = part * 8 / C::ROWB, chunk = part * 8 % C::ROWB / 16;
+#pragma unroll 1
+            for (int r0 = 0; r0 < rounds; r0 += BATCH) {
+                uint4 raw[BATCH];
+#pragma unroll
+                for (int b = 0; b < BATCH; ++b) raw[b] = load((r0 + b) * STEP + mine);
+#pragma unroll
+                for (int b = 0; b < BATCH; ++b) {
+                    const int u = (r0 + b) * STEP + mine;
+                    const uint32_t key = rowwise ? keys[u] : 0u;
+                    __syncwarp();
+                    const int up = rowwise ? up_of(key) : unit_up;
+                    const float gain = exp2_int(up);
+                    const f32x2 gain2 = pack2(gain, gain);
+                    const uint32_t in[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        // a scaled bf16 value is exact in fp16 (down to 2^-16, far below what lo resolves)
+                        const float2 v = unpack2(mul2(pack2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xFFFF0000u)), gain2));
+                        const __half2 vh = __floats2half2_rn(v.x, v.y);
+                        hi[e] = __nv_cvt_halfraw2_to_fp8x2(vh, __NV_SATFINITE, __NV_E4M3);
+                        const __half2 rest = __hsub2(vh, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3)));
+                        lo[e] = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
+                    }
+                    // a row that is not finite: its scores become NaN
+                    if (rowwise && part == 0) qf[u] = key >= 0x7F80u ? __uint_as_float(0x7FC00000u) : exp2_int(-up);
+                    const int ur = u & (TILE - 1), swz = C::ROWB == 128 ? ur & 7 : (ur >> 1) & 3;
+                    uint8_t* to = smem + C::OFF_Q + (u >> 7) * C::QTILE + panel * C::QPANEL + ur * C::ROWB + ((chunk ^ swz) << 4) + (part & 1) * 8;
+                    *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(hi[0], hi[1], 0x5410), __byte_perm(hi[2], hi[3], 0x5410));
+                    *reinterpret_cast<uint2*>(to + TILE * C::ROWB) = make_uint2(__byte_perm(lo[0], lo[1], 0x5410), __byte_perm(lo[2], lo[3], 0x5410));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_at(bar(C::B_QFULL, piece % QB));
+            return true;
+        };
+        uint32_t tiles = 0, pieces = 0, piece = 0;
+        bool ok = true;
+        while (ok && before(at, end)) {
+            const Unit x = unit_at<D>(a, at.lane, at.unit);
+            const int t0 = at.tile, t1 = last_tile(x);
+            if (t1 > t0) {
+                if (!prepare(x, piece)) break;
+                ++piece;
+                for (int t = t0; t < t1 && ok; ++t, ++tiles) {
+                    const uint32_t sc = tiles % NSC;
+                    if (!warp_wait_at(bar(C::B_SCFULL, sc), (tiles / NSC) & 1, stop)) { ok = false; break; }
+                    const uint8_t* bytes = smem + C::OFF_SC + sc * C::SC_BYTES + TILE;
+#pragma unroll 1
+                    for (int pc = 0; pc < C::PIECES; ++pc, ++pieces) {
+                        const uint32_t rs = pieces % NR, bs = pieces % NB;
+                        if (!warp_wait_at(bar(C::B_RFULL, rs), (pieces / NR) & 1, stop)) { ok = false; break; }
+                        if (!warp_wait_at(bar(C::B_BEMPTY, bs), ((pieces / NB) & 1) ^ 1, stop)) { ok = false; break; }
+                        constexpr int CPR = D / 16, EACH = C::VR * CPR / 128;        // 16-byte pieces of a row, of a thread
+                        const int left = x.end - t * TILE - pc * C::VR;      // rows that somebody sees; what lies behind is anything
+#pragma unroll
+                        for (int e = 0; e < EACH; ++e) {
+                            const int i = e * 128 + ct, row = i / CPR, c = i % CPR;
+                            const uint4 raw = *reinterpret_cast<const uint4*>(smem + C::OFF_R + rs * C::RSLOT + i * 16);
+                            const uint32_t s = bytes[pc * C::VR + row];
+                            // e4m3's bits, moved to bf16's places, stand for the code times 2^-120
+                            uint32_t f = s <= 134u ? (s + 120u) << 7 : 0x7F00u;
+                            f |= f << 16;
+                            const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+                            uint32_t v[8];
+#pragma unroll
+                            for (int w = 0; w < 8; ++w) {
+                                const uint32_t two = __byte_perm(in[w / 2], 0u, w & 1 ? 0x3424 : 0x1404);
+                                v[w] = mul_bf16x2(((two >> 4) & 0x07F007F0u) | (two & 0x80008000u), f);
+                            }
+                            if (s > 134u) {
+                                const uint32_t f2 = ((s - 7u) << 7) * 0x10001u;
+#pragma unroll
+                                for (int w = 0; w < 8; ++w) v[w] = mul_bf16x2(v[w], f2);
+                            }
+                            if (s == 0u || row >= left)
+#pragma unroll
+                                for (int w = 0; w < 8; ++w) v[w] = 0u;
+                            // the two halves in an order that keeps neighbours' panels on different banks
+                            const int flip = (c >> 2) & 1, q0 = (c & 3) * 2;
+                            uint8_t* to = smem + C::OFF_B + bs * C::BSLOT + (c >> 2) * C::VPANEL + row * 128;
+                            const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]), hi = make_uint4(v[4], v[5], v[6], v[7]);
+                            *reinterpret_cast<uint4*>(to + (((q0 + flip) ^ (row & 7)) << 4)) = flip ? hi : lo;
+                            *reinterpret_cast<uint4*>(to + (((q0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? lo : hi;
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            arrive_at(bar(C::B_BFULL, bs));
+                            arrive_at(bar(C::B_REMPTY, rs));
+                        }
+                    }
+                    if (ok && lane == 0) arrive_at(bar(C::B_SCEMPTY, sc));
+                }
+            }
+            at = after(a, at, x.units, end);
+        }
+    } else {
+        regs_down<C::REST_REGS>();
+        const int P = 1 << a.page_shift;
+        auto checked = [&](int page, bool tell) {
+            if (page >= 0 && page < a.c.n_pages) return page;
+            if (tell) record_error(a.err, MOE_DEV_BAD_PAGE);
+            return 0;
+        };
+        if (warp == 12) {
+            // -------------------------------------------------------- TMA: lane l < 8 looks up the page of the tile's rows 16 l ..
+            const int rk = P < TILE ? P : TILE, rv = P < C::VR ? P : C::VR;          // rows a copy
+            bool ok = true;
+            while (ok && before(at, end)) {
+                const Unit x = unit_at<D>(a, at.lane, at.unit);
+                const int t0 = at.tile, t1 = last_tile(x), hp = x.h * P;
+                const int32_t* table = a.table + (int64_t)x.b * a.width;
+                auto look = [&](int t) {
+                    const int j = t * TILE + lane * 16;
+                    return lane < 8 && t < t1 && j < x.end ? table[j >> a.page_shift] : 0;
+                };
+                int id = look(t0);
+                for (int t = t0; t < t1 && ok; ++t) {
+                    const int next = look(t + 1);
+                    const int j = t * TILE + lane * 16;
+                    int row = 0;                     // this lane's first cache row
+                    if (lane < 8 && j < x.end) row = checked(id, true) * a.c.n_kv_heads * P + hp + (j & (P - 1));
+                    id = next;
+                    {
+                        const uint32_t s = issued_k % NK;
+                        const int r = __shfl_sync(0xFFFFFFFFu, row, lane * rk / 16 & 31);
+                        const bool some = lane * rk < TILE && t * TILE + lane * rk < x.end;
+                        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, some)) * rk * D;
+                        if (!warp_wait_at(bar(C::B_KEMPTY, s), ((issued_k / NK) & 1) ^ 1, stop)) { ok = false; break; }
+                        if (lane == 0) arrive_expect_tx_at(bar(C::B_KFULL, s), bytes);
+                        ++issued_k;
+                        __syncwarp();
+                        if (some)
+#pragma unroll
+                            for (int q = 0; q < C::PANELS; ++q)
+                                tma_load_at(base + C::OFF_K + s * C::KSLOT + q * C::KPANEL + lane * rk * C::ROWB, &maps.k, bar(C::B_KFULL, s), q * 128, r);
+                    }
+                    for (int pc = 0; pc < C::PIECES; ++pc) {
+                        const uint32_t s = issued_r % NR;
+                        const int in = pc * C::VR + lane * rv;
+                        const int first = __shfl_sync(0xFFFFFFFFu, row, in / 16 & 7);        // (a page of 1024 rows: the same one, further down)
+                        const bool some = lane * rv < C::VR && t * TILE + in < x.end;
+                        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, some)) * rv * D;
+                        if (!warp_wait_at(bar(C::B_REMPTY, s), ((issued_r / NR) & 1) ^ 1, stop)) { ok = false; break; }
+                        if (lane == 0) arrive_expect_tx_at(bar(C::B_RFULL, s), bytes);
+                        ++issued_r;
+                        __syncwarp();
+                        if (some) tma_load_at(base + C::OFF_R + s * C::RSLOT + lane * rv * D, &maps.v, bar(C::B_RFULL, s), 0, first);
+                    }
+                }
+                at = after(a, at, x.units, end);
+            }
+        } else if (warp == 13) {
+            // -------------------------------------------------------- MMA issue: whatever is ready, outputs first
+            constexpr uint64_t KD = desc_base(C::ROWB == 128 ? 2 : 4, 8 * C::ROWB, 8 * C::ROWB);
+            constexpr uint64_t VD = desc_base(2, C::VPANEL, 1024);
+            constexpr uint32_t ID_S = idesc_f8(TILE, TILE, 0, 0, 0), ID_PV = idesc_bf16(TILE, D);
+            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+            const uint64_t qd = desc_at(KD, base + C::OFF_Q), kd = desc_at(KD, base + C::OFF_K), vd = desc_at(VD, base + C::OFF_B);
+            auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(0xFFFFFFFFu, test_at(b, parity)) != 0; };
+            // Two ways through the parts: of the scores and, behind it, of the outputs.
+            struct Way { Pos at; int units, nt, left; };             // left: tiles of the part that are still to be done
+            auto enter = [&](Way& w, bool go_on) {                   // the next part that has tiles; false: there is none
+                if (go_on) w.at = after(a, w.at, w.units, end);
+                while (before(w.at, end)) {
+                    const Unit x = unit_at<D>(a, w.at.lane, w.at.unit);
+                    const int last = same_unit(w.at, end) ? min(end.tile, x.tiles) : x.tiles;
+                    w.units = x.units;
+                    w.nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0);
+                    w.left = __shfl_sync(0xFFFFFFFFu, last - w.at.tile, 0);
+                    if (w.left > 0) return true;
+                    w.at = after(a, w.at, w.units, end);
+                }
+                w.left = 0;
+                return false;
+            };
+            Way ws{at, 0, 1, 0}, wo{at, 0, 1, 0};
+            bool more_s = enter(ws, false), more_o = enter(wo, false), fresh = true;
+            uint32_t si = 0, oi = 0, ks = 0, piece = 0, bi = 0;      // items of scores and outputs, tiles of keys, parts, pieces of values
+            int sr = 0, orow = 0;                                    // row tiles
+            while (more_o) {
+                bool moved = false;
+                if (oi < si && ready(bar(C::B_PFULL, oi & 1), (oi >> 1) & 1)) {
+                    bool there = true;
+#pragma unroll
+                    for (int pc = 0; pc < C::PIECES; ++pc) there = there && ready(bar(C::B_BFULL, (bi + pc) % NB), ((bi + pc) / NB) & 1);
+                    if (there) {
+                        tc_fence_after();
+                        const uint32_t o = tm + C::TMEM_O + orow * D, p = tm + (oi & 1) * TILE;
+                        const bool done = orow == wo.nt - 1;         // with this tile of values
+                        if (elect_one()) {
+#pragma unroll
+                            for (int pc = 0; pc < C::PIECES; ++pc) {
+                                const uint32_t bs = (bi + pc) % NB;
+                                const uint64_t v = vd + (uint64_t)(bs * (C::BSLOT >> 4));
+#pragma unroll
+                                for (int kk = 0; kk < C::VR / 16; ++kk)
+                                    tc_mma_f16_ts(o, p + pc * (C::VR / 2) + kk * 8, v + kk * (2048 >> 4), ID_PV, fresh && pc == 0 && kk == 0 ? 0u : 1u);
+                                if (done) commit_at(bar(C::B_BEMPTY, bs));
+                            }
+                            commit_at(bar(C::B_ODONE, oi & 1));
+                        }
+                        __syncwarp();
+                        progress[0] = ++oi;
+                        if (done) {
+                            orow = 0;
+                            bi += C::PIECES;
+                            fresh = false;
+                            if (--wo.left == 0) {
+                                more_o = enter(wo, true);
+                                fresh = true;
+                            }
+                        } else {
+                            ++orow;
+                        }
+                        moved = true;
+                    }
+                }
+                // the buffer's P has been read: by the output issued two items ago
+                if (more_s && si < oi + 2 && ready(bar(C::B_KFULL, ks % NK), (ks / NK) & 1) && ready(bar(C::B_QFULL, piece % QB), (piece / QB) & 1)) {
+                    tc_fence_after();
+                    const uint32_t s = ks % NK, d = tm + (si & 1) * TILE;
+                    const uint64_t k = kd + (uint64_t)(s * (C::KSLOT >> 4)), q = qd + (uint64_t)(sr * (C::QTILE >> 4));
+                    const bool done = sr == ws.nt - 1;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 2 * D / 32; ++kk) {
+                            constexpr int STEPS = C::ROWB / 32, HALF = D / 32;
+                            const int kq = kk % HALF;
+                            tc_mma_f8(d, q + (((kq / STEPS) * C::QPANEL + (kk / HALF) * TILE * C::ROWB + (kq % STEPS) * 32) >> 4),
+                                      k + (((kq / STEPS) * C::KPANEL + (kq % STEPS) * 32) >> 4), ID_S, kk ? 1u : 0u);
+                        }
+                        commit_at(bar(C::B_SFULL, si & 1));
+                        if (done) commit_at(bar(C::B_KEMPTY, s));
+                        if (done && ws.left == 1) commit_at(bar(C::B_QFREE));
+                    }
+                    __syncwarp();
+                    ++si;
+                    if (done) {
+                        sr = 0;
+                        ++ks;
+                        if (--ws.left == 0) {
+                            ++piece;
+                            more_s = enter(ws, true);
+                        }
+                    } else {
+                        ++sr;
+                    }
+                    moved = true;
+                }
+                if (!moved && __any_sync(0xFFFFFFFFu, stopped(stop))) break;
+            }
+        } else if (warp == 15) {
+            // -------------------------------------------------------- watchdog: stops the block when nothing has moved for the bound
+            uint32_t seen = 0;
+            uint64_t since = global_timer_ns();
+            const bool nap = a.wait_ns >= 40000ull;  // (asleep for some 20 us, whatever less is asked for)
+            while (!(nap ? try_at_for(bar(C::B_DONE), 0, 20000) : test_at(bar(C::B_DONE), 0)) && !stopped(stop)) {
+                const uint32_t now_at = progress[0] + progress[1];
+                const uint64_t now = global_timer_ns();
+                if (now_at != seen) {
+                    seen = now_at;
+                    since = now;
+                } else if (now - since >= a.wait_ns) {
+                    stop_all(stop);
+                    break;
+                }
+            }
+        } else {
+            // -------------------------------------------------------- scales: a lane takes four rows; scales are under way SA tiles
+            // ahead and page ids another SA, both into shared memory (a register handed on would wait for its load)
+            constexpr int A = C::SA;
+            const uint32_t ids = base + C::OFF_SID + lane * 4, sc0 = base + C::OFF_SC + lane * 4;
+            uint32_t tiles = 0, piece = 0;
+            bool ok = true;
+            while (ok && before(at, end)) {
+                const Unit x = unit_at<D>(a, at.lane, at.unit);
+                const int t0 = at.tile, nt = last_tile(x) - t0, hp = x.h * P;
+                const int first = t0 * TILE + lane * 4;
+                const int32_t* table = a.table + (int64_t)x.b * a.width;
+                auto look = [&](int d) {
+                    const int j = first + d * TILE;
+                    if (d < nt && j < x.end) cp_async_4(ids + (d % (2 * A)) * 128, table + (j >> a.page_shift));
+                };
+                auto load = [&](int d) {                     // its id has arrived
+                    if (d >= nt) return true;
+                    const uint32_t e = tiles + d, sc = e % NSC;
+                    if (!warp_wait_at(bar(C::B_SCEMPTY, sc), ((e / NSC) & 1) ^ 1, stop)) return false;
+                    const int j = first + d * TILE;
+                    const uint32_t dst = sc0 + sc * C::SC_BYTES;
+                    if (j < x.end) {
+                        const int row = checked(read_at(ids + (d % (2 * A)) * 128), false) * a.c.n_kv_heads * P + hp + (j & (P - 1));
+                        cp_async_4(dst, a.c.k_scales + row);
+                        cp_async_4(dst + TILE, a.c.v_scales + row);
+                    } else {
+                        write_at(dst, 0x7F7F7F7Fu);
+                        write_at(dst + TILE, 0x7F7F7F7Fu);
+                    }
+                    return true;
+                };
+                const int ahead = nt < A ? nt : A;
+#pragma unroll 1
+                for (int d = 0; d < ahead; ++d) look(d);
+                cp_async_commit();
+                cp_async_wait<0>();
+                float unit = 0.0f;
+#pragma unroll 1
+                for (int d = -ahead; d < nt; ++d) {
+                    if (d >= 0) {
+                        if (nt < A) cp_async_wait<0>(); else cp_async_wait<A - 1>();
+                    }
+                    if (!load(d + ahead)) { ok = false; break; }
+                    look(d + 2 * A);
+                    cp_async_commit();
+                    if (d < 0) continue;
+                    if (d == 0) {
+                        if (!warp_wait_at(bar(C::B_QFULL, piece % QB), (piece / QB) & 1, stop)) { ok = false; break; }
+                        unit = *reinterpret_cast<const float*>(smem + C::OFF_QU + (piece % QB) * 8) * a.scale_log2;
+                    }
+                    const uint32_t sc = (tiles + d) % NSC, dst = sc0 + sc * C::SC_BYTES;
+                    const uint32_t ks = read_at(dst);
+                    uint32_t vs = read_at(dst + TILE);
+                    float f[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t k = (ks >> (8 * e)) & 255u, v = (vs >> (8 * e)) & 255u;
+                        // scores stay finite where they can; values past bf16's range, and NaN, make a NaN of the weight and count as zeros
+                        f[e] = fminf(e8m0_to_float(k) * unit, 0x1p126f);
+                        if (k == 255u || v > 246u) f[e] = __uint_as_float(0x7FC00000u);
+                        if (v > 246u) vs &= ~(255u << (8 * e));
+                    }
+                    write_at(dst + TILE, vs);
+                    *reinterpret_cast<float4*>(smem + C::OFF_SC + sc * C::SC_BYTES + 2 * TILE + lane * 16) = make_float4(f[0], f[1], f[2], f[3]);
+                    __syncwarp();
+                    if (lane == 0) arrive_at(bar(C::B_SCFULL, sc));
+                }
+                if (nt > 0) {
+                    tiles += nt;
+                    ++piece;
+                }
+                at = after(a, at, x.units, end);
+            }
+            cp_async_wait<0>();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {                               // final after the barrier: nothing new is issued past it
+        if (warp == 12 && lane == 0) {
+            drain_stage_fills(bar_ptr(C::B_KFULL), NK, issued_k);
+            drain_stage_fills(bar_ptr(C::B_RFULL), NR, issued_r);
+        }
+        if (warp == 13 && elect_one()) tc_drain(bar_ptr(C::B_DRAIN));
+        tc_fence_before();
+        __syncthreads();
+    }
+    if (warp == 13) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (tid == 0 && *abort_flag) record_error(a.err, MOE_DEV_TIMEOUT);
 }
 
-int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
+// ------------------------------------------------------------------ join
+
+// The parts of a unit that several CTAs share, added in the order of the cache rows. blockIdx.x + 1 is the first CTA whose
+// part begins inside the unit; 32 rows a block, a lane a row, a warp every eighth group of four columns.
+constexpr int JOIN_WARPS = 8, JOIN_ROWS = 32;
+
+template <int D>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_attention_join(const __grid_constant__ ChunkArgs a, int ctas) {
+    using C = Cfg<D>;
+    constexpr int ROWS = C::ROWS;
+    pdl_trigger();
+    pdl_wait();
+    const Pos* places = reinterpret_cast<const Pos*>(a.ws);
+    const int k = blockIdx.x + 1;
+    const Pos p = places[k], q = places[k - 1];
+    if (p.lane >= a.lanes || p.tile == 0 || (same_unit(p, q) && q.tile > 0)) return;
+    const Unit x = unit_at<D>(a, p.lane, p.unit);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y * JOIN_ROWS + lane;
+    if ((int)blockIdx.y * JOIN_ROWS >= x.rows) return;
+    const float* parts = reinterpret_cast<const float*>(a.ws + parts_offset(ctas));
+    constexpr int N = D / 4 / JOIN_WARPS;            // groups of columns of a thread
+    float4 acc[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float m = NEVER, l = 0.0f;
+    Pos here = p;
+    for (int c = k - 1; c < ctas; ++c) {
+        if (c >= k) {
+            here = places[c];
+            if (!same_unit(here, p)) break;
+            const Pos next = places[c + 1];
+            if (same_unit(next, here) && next.tile == here.tile) continue;           // a CTA without tiles
+        }
+        const float* part = parts + (size_t)(2 * c + (c == k - 1 ? 1 : 0)) * C::PART_FLOATS;
+        const float mc = part[ROWS * D + row], lc = part[ROWS * D + ROWS + row];
+        const float mn = fmaxf(m, mc), f0 = ex2(m - mn), f1 = ex2(mc - mn);
+        l = l * f0 + lc * f1;
+        m = mn;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float4 v = *reinterpret_cast<const float4*>(part + ((size_t)(warp + e * JOIN_WARPS) * ROWS + row) * 4);
+            acc[e].x = acc[e].x * f0 + v.x * f1;
+            acc[e].y = acc[e].y * f0 + v.y * f1;
+            acc[e].z = acc[e].z * f0 + v.z * f1;
+            acc[e].w = acc[e].w * f0 + v.w * f1;
+        }
+    }
+    if (row >= x.rows) return;
+    const int t = (int)((uint32_t)row * a.by_group >> 16);
+    const int64_t to = (int64_t)(x.tok0 + t) * a.n_q + x.h * a.group + row - t * a.group;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        *reinterpret_cast<uint2*>(a.out + to * D + (warp + e * JOIN_WARPS) * 4) =
+            make_uint2(pack_bf16(acc[e].x * inv, acc[e].y * inv), pack_bf16(acc[e].z * inv, acc[e].w * inv));
+    if (a.lse && warp == 0) a.lse[to] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// ------------------------------------------------------------------ host side
+
+cudaError_t codes_map(CUtensorMap* m, const void* base, const moe_kv_cache& c, int box_bytes, int box_rows, CUtensorMapSwizzle swizzle) {
+    auto enc = encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.n_pages * c.n_kv_heads * c.page_size};
+    const cuuint64_t strides[1] = {(cuuint64_t)c.head_dim};
+    const cuuint32_t box[2] = {(cuuint32_t)box_bytes, (cuuint32_t)(c.page_size < box_rows ? c.page_size : box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D>
+cudaError_t launch(ChunkArgs a, cudaStream_t s) {
+    using C = Cfg<D>;
+    a.block = C::ROWS / a.group;
+    ChunkMaps maps;
+    cudaError_t e = codes_map(&maps.k, a.c.k_codes, a.c, C::ROWB, TILE, C::ROWB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess) e = codes_map(&maps.v, a.c.v_codes, a.c, D, C::VR, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e != cudaSuccess) return e;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+        e = cudaFuncSetAttribute(chunk_attention<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
+    const int ctas = moe_sm_count();
+    moe_prof_begin(MK_CHUNK_ATTENTION, s);
+    e = moe_launch(chunk_attention<D>, dim3((unsigned)ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
+    moe_prof_end(MK_CHUNK_ATTENTION, s);
+    moe_count_launches(1);
+    if (e != cudaSuccess || ctas < 2 || a.whole) return e;
+    moe_prof_begin(MK_CHUNK_JOIN, s);
+    e = moe_launch(chunk_attention_join<D>, dim3((unsigned)(ctas - 1), C::ROWS / JOIN_ROWS), dim3(JOIN_WARPS * 32), 0, s, a, ctas);
+    moe_prof_end(MK_CHUNK_JOIN, s);
+    moe_count_launches(1);
+    return e;
+}
 
 }  // namespace
 
 size_t moe_chunk_attention_workspace_bytes(int n_tokens, int n_q_heads, int n_kv_heads, int head_dim, int lanes) {
     if (n_tokens < 1 || n_q_heads < 1 || n_kv_heads < 1 || head_dim < 1 || lanes < 1) return 0;
-    return 16;
+    const int ctas = moe_sm_count();
+    const size_t part = head_dim == 256 ? Cfg<256>::PART_FLOATS : head_dim == 64 ? Cfg<64>::PART_FLOATS : Cfg<128>::PART_FLOATS;
+    return parts_offset(ctas) + (size_t)2 * ctas * part * sizeof(float);
 }
 
 moe_status moe_chunk_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int n_tokens, int n_q_heads,
@@ -171,19 +1131,20 @@ moe_status moe_chunk_attention(const void* q, int64_t q_token_stride, int64_t q_
     a.n_tokens = n_tokens;
     a.n_q = n_q_heads;
     a.group = n_q_heads / cache->n_kv_heads;
+    a.by_group = (65536u + a.group - 1) / a.group;
     a.table = page_table;
     a.width = table_width;
     a.lanes = lanes;
     a.page_shift = log2_of(cache->page_size);
     a.kv_len = kv_len;
     a.cu = cu_tokens;
+    a.whole = (int64_t)table_width * cache->page_size <= WHOLE_TILES * TILE;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
+    a.ws = static_cast<uint8_t*>(workspace);
     a.err = err;
-    moe_prof_begin(MK_CHUNK_ATTENTION, s);
+    a.wait_ns = moe_wait_limit_ns();
     const cudaError_t e = cache->head_dim == 64 ? launch<64>(a, s) : cache->head_dim == 128 ? launch<128>(a, s) : launch<256>(a, s);
-    moe_prof_end(MK_CHUNK_ATTENTION, s);
-    moe_count_launches(1);
     return e == cudaSuccess ? MOE_OK : MOE_ECUDA;
 }

@@ -129,6 +129,33 @@ MOE_DEV unsigned long long block_inclusive_scan_u64(unsigned long long v, unsign
     return v;
 }
 
+// Inclusive sums over the block's threads of two values, and their totals. scratch: 64 values. One barrier, after one that
+// lets scratch be written again.
+MOE_DEV void scan2(unsigned long long& x, unsigned long long& y, unsigned long long* scratch, unsigned long long* tx, unsigned long long* ty) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long a = __shfl_up_sync(0xFFFFFFFFu, x, o), b = __shfl_up_sync(0xFFFFFFFFu, y, o);
+        if (lane >= o) { x += a; y += b; }
+    }
+    __syncthreads();
+    if (lane == 31) { scratch[wid] = x; scratch[32 + wid] = y; }
+    __syncthreads();
+    unsigned long long sx = lane < nw ? scratch[lane] : 0ull, sy = lane < nw ? scratch[32 + lane] : 0ull;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long a = __shfl_up_sync(0xFFFFFFFFu, sx, o), b = __shfl_up_sync(0xFFFFFFFFu, sy, o);
+        if (lane >= o) { sx += a; sy += b; }
+    }
+    *tx = __shfl_sync(0xFFFFFFFFu, sx, 31);
+    *ty = __shfl_sync(0xFFFFFFFFu, sy, 31);
+    const unsigned long long bx = __shfl_sync(0xFFFFFFFFu, sx, wid - 1 & 31), by = __shfl_sync(0xFFFFFFFFu, sy, wid - 1 & 31);
+    if (wid > 0) { x += bx; y += by; }
+}
+
+// Of a power of two.
+inline int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
+
 MOE_DEV void record_error(uint32_t* err, uint32_t bits) {
     if (err) atomicOr(err, bits);
 }

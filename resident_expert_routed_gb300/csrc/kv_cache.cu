@@ -264,8 +264,6 @@ __global__ void __launch_bounds__(KV_THREADS) kv_keep(const moe_kv_cache c, cons
     }
 }
 
-int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
-
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ECUDA; }
 
 template <typename T>

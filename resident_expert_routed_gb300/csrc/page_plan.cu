@@ -38,29 +38,6 @@ struct PlanArgs {
 
 typedef unsigned long long u64;
 
-// Inclusive sums over the block's threads of two values, and their totals; scratch: 64 values. Barriers within.
-MOE_DEV void scan_two(u64& x, u64& y, u64* scratch, u64* tx, u64* ty) {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const u64 a = __shfl_up_sync(0xFFFFFFFFu, x, o), b = __shfl_up_sync(0xFFFFFFFFu, y, o);
-        if (lane >= o) { x += a; y += b; }
-    }
-    __syncthreads();
-    if (lane == 31) { scratch[wid] = x; scratch[32 + wid] = y; }
-    __syncthreads();
-    u64 sx = lane < nw ? scratch[lane] : 0ull, sy = lane < nw ? scratch[32 + lane] : 0ull;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const u64 a = __shfl_up_sync(0xFFFFFFFFu, sx, o), b = __shfl_up_sync(0xFFFFFFFFu, sy, o);
-        if (lane >= o) { sx += a; sy += b; }
-    }
-    *tx = __shfl_sync(0xFFFFFFFFu, sx, 31);
-    *ty = __shfl_sync(0xFFFFFFFFu, sy, 31);
-    const u64 bx = __shfl_sync(0xFFFFFFFFu, sx, (wid - 1) & 31), by = __shfl_sync(0xFFFFFFFFu, sy, (wid - 1) & 31);
-    if (wid > 0) { x += bx; y += by; }
-}
-
 MOE_DEV void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -103,7 +80,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan(const PlanArgs a) {
         if (!fine) { bad |= MOE_DEV_BAD_PAGE; h = h < 0 ? 0 : (h > a.width ? a.width : h); }
         const u64 own = n > 0 ? n : 0, gone = n < 0 ? h : 0;
         u64 x = own, y = gone, tx, ty;
-        scan_two(x, y, scratch, &tx, &ty);
+        scan2(x, y, scratch, &tx, &ty);
         x += tok_all;
         y += back_all;
         tok_all += tx;
@@ -127,13 +104,13 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan(const PlanArgs a) {
         const int b = b0 + tid;
         const int need = b < B ? got[b] : 0;
         u64 x = need, y = 0, tx, ty;
-        scan_two(x, y, scratch, &tx, &ty);
+        scan2(x, y, scratch, &tx, &ty);
         x += need_all;
         need_all += tx;
         bool served = true;
         if (b < B && need > 0 && x > (u64)there) served = false;
         u64 g = served ? need : 0, z = 0, tg, tz;
-        scan_two(g, z, scratch, &tg, &tz);
+        scan2(g, z, scratch, &tg, &tz);
         g += given;
         given += tg;
         if (b < B) {
@@ -200,8 +177,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan(const PlanArgs a) {
     }
     if (lost) record_error(a.err, MOE_DEV_BAD_PAGE);
 }
-
-int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
 
 }  // namespace
 

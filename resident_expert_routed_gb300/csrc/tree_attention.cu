@@ -74,11 +74,8 @@
 #include <cuda_fp8.h>
 
 #include <climits>
-#include <mutex>
 
-#include <cudaTypedefs.h>
-
-#include "common.cuh"
+#include "attention.cuh"
 
 namespace {
 
@@ -135,12 +132,6 @@ struct JoinUnit {
 __host__ __device__ constexpr size_t part_floats(int R, int D) { return (size_t)R * (D + 2); }
 __host__ __device__ inline size_t parts_offset(int ctas) { return ((size_t)ctas * sizeof(JoinUnit) + 255) / 256 * 256; }
 
-// Where part k begins: total / parts each, one more in the first total % parts. (64-bit divisions only where needed.)
-MOE_DEV int64_t part_begin(unsigned long long total, int parts, int k) {
-    const unsigned long long each = total >> 32 ? total / parts : (uint32_t)total / (uint32_t)parts;
-    const int more = (int)(total - each * parts);
-    return (int64_t)(each * k) + (k < more ? k : more);
-}
 // The part that x is in.
 MOE_DEV int part_of(unsigned long long total, int parts, unsigned long long x) {
     const unsigned long long each = total / parts, more = total - each * parts;
@@ -234,187 +225,6 @@ constexpr uint32_t ZERO_BYTE = 127u, LEAST_BYTE = 27u;      // scale bytes: of a
 // ends at 2^-126: what the sum of weights could miss is 2^-37 of the largest weight.)
 constexpr int WIDE = 100, MAY_BE_ZERO = -1000;
 
-// ------------------------------------------------------------------ small device pieces
-
-MOE_DEV float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-MOE_DEV float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-typedef unsigned long long f32x2;
-MOE_DEV f32x2 pack2(float a, float b) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-MOE_DEV float2 unpack2(f32x2 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-MOE_DEV f32x2 add2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-MOE_DEV f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-MOE_DEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-// The barrier and copy instructions of common.cuh on 32-bit shared-memory addresses: one register holds the base, the
-// rest is an immediate. (Registers bound this kernel; a table of 64-bit pointers costs it dozens.)
-MOE_DEV bool test_at(uint32_t bar, uint32_t parity) {         // without waiting
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-MOE_DEV bool try_at(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-MOE_DEV bool try_at_for(uint32_t bar, uint32_t parity, uint32_t ns) {       // asleep for about ns at most
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(ns)
-        : "memory");
-    return ok != 0;
-}
-MOE_DEV void cp_async_4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-MOE_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> MOE_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-MOE_DEV int read_at(uint32_t at) {
-    int v;
-    asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    return v;
-}
-MOE_DEV void write_at(uint32_t at, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
-MOE_DEV uint32_t stopped(uint32_t stop) {
-    uint32_t v;
-    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(stop) : "memory");
-    return v;
-}
-MOE_DEV void stop_all(uint32_t stop) { asm volatile("st.volatile.shared.u32 [%0], 1;" ::"r"(stop) : "memory"); }
-// A wait of a whole warp, with the same outcome in every lane: false when the block has been stopped. The watchdog warp bounds all
-// of a block's waits in one place: a bound in each of some thirty inlined waits drives the kernel out of the instruction cache.
-MOE_DEV bool warp_wait_at(uint32_t bar, uint32_t parity, uint32_t stop) {
-    while (!__all_sync(0xFFFFFFFFu, try_at(bar, parity)))
-        if (__any_sync(0xFFFFFFFFu, stopped(stop))) return false;
-    return true;
-}
-MOE_DEV void arrive_at(uint32_t bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory"); }
-MOE_DEV void arrive_expect_tx_at(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-MOE_DEV void commit_at(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-MOE_DEV void tma_load_at(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-        : "memory");
-}
-
-MOE_DEV void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// Moves registers between warpgroups: of 768 threads launched with 80 each (R = 64), 4 x 96 + 56 + 40 = 6 x 80.
-template <int N> MOE_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> MOE_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-// kind::f8f6f4, e4m3 x e4m3 (or x e5m2) -> fp32; a_mn, b_mn: whether A and B lie with M and N (instead of K) contiguous.
-__host__ __device__ constexpr uint32_t idesc_f8(int m, int n, int a_mn, int b_mn, int b_e5m2) {
-    return (1u << 4) | ((uint32_t)b_e5m2 << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
-           ((uint32_t)(m >> 4) << 24);
-}
-
-// 2^p down to the smallest subnormal, 2^-149.
-MOE_DEV float exp2_whole(int p) { return p >= -126 ? exp2_int(p) : __uint_as_float(p >= -149 ? 1u << (p + 149) : 0u); }
-
-// One lane of the (converged) warp.
-MOE_DEV bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
-MOE_DEV void tc_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
-
-// N consecutive columns of this lane of TMEM, complete on return. One wide load, not several: beside running
-// MMAs each wait costs 250 to 400 clocks.
-MOE_DEV void tc_load(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
-        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-MOE_DEV void tc_load(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-}
-
-// Shared-memory matrix descriptor without its address: swizzle 2 = 128 B, 4 = 64 B, 6 = 32 B, 0 = none; the two
-// strides in bytes. With a swizzle `lead` is from one atom of the contiguous axis to the next and `group` from one group of
-// eight rows (of the strided axis) to the next, without one the other way round. Operands that are one atom wide on
-// their contiguous axis hold the group stride in both.
-__host__ __device__ constexpr uint64_t desc_base(int swizzle, int lead, int group) {
-    return ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(group >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)swizzle << 61);
-}
-MOE_DEV uint64_t desc_at(uint64_t base, uint32_t saddr) { return base + (uint64_t)(saddr >> 4); }   // below 256 KB: no carry
-
 // A lane's facts. A lane that does not fit (see the header) has no rows, and its outputs become zeros.
 struct Lane {
     int n0, n, len;
@@ -443,30 +253,6 @@ struct Cut {
     unsigned long long total;                        // of the run
     int cost, weight, parts;                         // of a unit beside its tiles, of a tile of that unit; parts of the run
 };
-
-// Inclusive sums over the block's threads of two values, and their totals. scratch: 64 values. One barrier, after one that
-// lets scratch be written again.
-MOE_DEV void scan2(unsigned long long& x, unsigned long long& y, unsigned long long* scratch, unsigned long long* tx, unsigned long long* ty) {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long a = __shfl_up_sync(0xFFFFFFFFu, x, o), b = __shfl_up_sync(0xFFFFFFFFu, y, o);
-        if (lane >= o) { x += a; y += b; }
-    }
-    __syncthreads();
-    if (lane == 31) { scratch[wid] = x; scratch[32 + wid] = y; }
-    __syncthreads();
-    unsigned long long sx = lane < nw ? scratch[lane] : 0ull, sy = lane < nw ? scratch[32 + lane] : 0ull;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long a = __shfl_up_sync(0xFFFFFFFFu, sx, o), b = __shfl_up_sync(0xFFFFFFFFu, sy, o);
-        if (lane >= o) { sx += a; sy += b; }
-    }
-    *tx = __shfl_sync(0xFFFFFFFFu, sx, 31);
-    *ty = __shfl_sync(0xFFFFFFFFu, sy, 31);
-    const unsigned long long bx = __shfl_sync(0xFFFFFFFFu, sx, wid - 1 & 31), by = __shfl_sync(0xFFFFFFFFu, sy, wid - 1 & 31);
-    if (wid > 0) { x += bx; y += by; }
-}
 
 // One CTA's way through its part of the run: the unit it is in and the tile within it.
 struct Walk {
@@ -700,7 +486,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, 1) tree_attention(const __
 
     if (warp < SW) {
         // ------------------------------------------------------------ softmax
-        if constexpr (R == 64) regs_up<96>();
+        if constexpr (R == 64) regs_up<96>();        // of 768 threads launched with 80 each: 4 x 96 + 56 + 40 = 6 x 80
         const int wg = warp >> 2, wl = warp & 3;     // warpgroup, warp in it
         const int g = wg / C::HALVES, h = wg % C::HALVES;             // group, which of its tree rows
         const int j = tid & 127;                     // this thread's row of the tile
@@ -1535,21 +1321,6 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_attention_join(const Att
 }
 
 // ------------------------------------------------------------------ host side
-
-int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
-
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
 
 cudaError_t codes_map(CUtensorMap* m, const void* base, const moe_kv_cache& c) {
     auto enc = encoder();
