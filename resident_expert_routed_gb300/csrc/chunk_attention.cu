@@ -117,8 +117,9 @@ struct Cfg {
     static constexpr int B_SCFULL = B_BEMPTY + 8 * NB;        // [NSC] a tile's factors and value bytes are there
     static constexpr int B_SCEMPTY = B_SCFULL + 8 * NSC;
     static constexpr int B_SFULL = B_SCEMPTY + 8 * NSC;       // [2] S is ready
-    static constexpr int B_PFULL = B_SFULL + 16;              // [2] P is written (S has been read)
-    static constexpr int B_ODONE = B_PFULL + 16;              // [2] P has been used: a tile is added to O
+    static constexpr int B_PFULL = B_SFULL + 16;              // [2][2] half of P is written (that half of S has been read)
+    static constexpr int B_OHALF = B_PFULL + 32;              // [2] the first half of P has been used
+    static constexpr int B_ODONE = B_OHALF + 16;              // [2] both: a tile is added to O
     static constexpr int B_QFULL = B_ODONE + 16;              // [QB] the queries of a part are there
     static constexpr int B_QFREE = B_QFULL + 8 * QB;              // ... have been used
     static constexpr int B_QMAX = B_QFREE + 8;                // the four warps have their maxima
@@ -127,7 +128,7 @@ struct Cfg {
     static constexpr int OFF_MISC = (B_DRAIN + 8 + 15) / 16 * 16;     // tmem slot, abort flag, progress [2], start, end
     static constexpr int SMEM = OFF_MISC + 16 + 32 + 1024;
     static constexpr int TMEM_O = 2 * TILE;                   // after S [2]
-    static constexpr int SOFT_REGS = 184, CONV_REGS = 96, REST_REGS = 48;     // 2 x 184 + 96 + 48 <= 4 x 128
+    static constexpr int SOFT_REGS = 168, CONV_REGS = 88, REST_REGS = 88;     // 2 x 168 + 88 + 88 = 4 x 128
     static_assert(OFF_B % 1024 == 0 && OFF_R % 128 == 0 && OFF_K % 1024 == 0 && BSLOT % 1024 == 0, "alignment");
     static_assert(OFF_BAR % 8 == 0 && OFF_QF % 16 == 0 && SMEM <= 227 * 1024, "shared memory");
     static_assert(2 * SOFT_REGS + CONV_REGS + REST_REGS <= 512, "registers");
@@ -183,11 +184,6 @@ MOE_DEV uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 }
 MOE_DEV void arrive_at_n(uint32_t bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
-}
-MOE_DEV float4 read4_at(uint32_t at) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
-    return v;
 }
 
 // ------------------------------------------------------------------ lanes, units, the cut
@@ -369,9 +365,9 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
         auto init = [&](int offset, int n, int arrivals) {
             for (int i = 0; i < n; ++i) mbar_init(bar_ptr(offset) + i, arrivals);
         };
-        init(C::B_KFULL, NK, 1); init(C::B_KEMPTY, NK, 1); init(C::B_RFULL, NR, 1); init(C::B_REMPTY, NR, 4);
-        init(C::B_BFULL, NB, 4); init(C::B_BEMPTY, NB, 1); init(C::B_SCFULL, NSC, 1); init(C::B_SCEMPTY, NSC, 12);
-        init(C::B_SFULL, 2, 1); init(C::B_PFULL, 2, 4); init(C::B_ODONE, 2, 1); init(C::B_QFULL, QB, 4); init(C::B_QFREE, 1, 1);
+        init(C::B_KFULL, NK, 1); init(C::B_KEMPTY, NK, 2); init(C::B_RFULL, NR, 1); init(C::B_REMPTY, NR, 4);
+        init(C::B_BFULL, NB, 4); init(C::B_BEMPTY, NB, 2); init(C::B_SCFULL, NSC, 1); init(C::B_SCEMPTY, NSC, 12);
+        init(C::B_SFULL, 2, 1); init(C::B_PFULL, 4, 4); init(C::B_OHALF, 2, 1); init(C::B_ODONE, 2, 1); init(C::B_QFULL, QB, 4); init(C::B_QFREE, 1, 2);
         init(C::B_QMAX, 1, 4); init(C::B_DONE, 1, 8); init(C::B_DRAIN, 1, 1);
         *abort_flag = 0;
         progress[0] = progress[1] = 0;
@@ -419,104 +415,130 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                     float m = NEVER, l = 0.0f;
                     for (int i = 0; i < nt; ++i) {
                         const uint32_t item = items + i * x.nt + g, buf = item & 1, sc = (tiles + i) % NSC;
-                        const uint32_t s_at = trow + buf * TILE, k_at = base + C::OFF_SC + sc * C::SC_BYTES + 2 * TILE;
+                        const uint32_t s_at = trow + buf * TILE;
                         const int j0 = (t0 + i) * TILE;
                         const bool masked = j0 + TILE - 1 > open;
                         const int rel = limit - j0;                  // columns up to rel are seen
                         if (!warp_wait_at(bar(C::B_SCFULL, sc), ((tiles + i) / NSC) & 1, stop)) { ok = false; break; }
                         if (!warp_wait_at(bar(C::B_SFULL, buf), (item >> 1) & 1, stop)) { ok = false; break; }
                         tc_fence_after();
-                        uint32_t P[64];
-                        for (bool moved = false;; moved = true) {
-                            const f32x2 m2 = pack2(-m, -m);
-                            float top = -INFINITY;
-                            f32x2 sum0 = 0ull, sum1 = 0ull;
-                            uint32_t s[2][32];
-                            tc_ld_x32(s_at, s[0]);
+                        const uint4* kf = reinterpret_cast<const uint4*>(smem + C::OFF_SC + sc * C::SC_BYTES + 2 * TILE);
+                        uint32_t s[2][32];
+                        tc_ld_x32(s_at, s[0]);
+                        // half a tile at a time, so that its weights are at work while the other half's are made
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            const int seen = rel - 64 * h;           // columns of this half up to here are seen
+                            const uint4* kh = kf + 16 * h;
+                            uint32_t P[32];
+                            bool move = i == 0 && h == 0;
+                            for (bool moved = false;; moved = true) {
+                                if (move) {
+                                    tc_wait_ld();                    // (what is under way goes to registers that are used again)
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                tc_wait_ld();
-                                // (the loads' registers are complete only past the wait: nothing that reads them may move above it)
+                                    for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(s[0][e]));
+                                    // the reference moves to the largest score so far, and what has been added up with it
+                                    float most = -INFINITY;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(s[c & 1][e]));
-                                if (c < 3) tc_ld_x32(s_at + (c + 1) * 32, s[(c + 1) & 1]);
-                                f32x2 y[16];
+                                    for (int c = 0; c < 2; ++c) {
+                                        uint32_t s1[32];
+                                        tc_load(s_at + h * 64 + c * 32, s1);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) y[e] = pack2(__uint_as_float(s[c & 1][2 * e]), __uint_as_float(s[c & 1][2 * e + 1]));
-                                if (rowwise) {
+                                        for (int e = 0; e < 8; ++e) {
+                                            const uint4 k = kh[c * 8 + e];
+                                            const uint32_t k4[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e) y[e] = mul2(y[e], rf2);
+                                            for (int z = 0; z < 4; ++z) {
+                                                const float v = __uint_as_float(s1[4 * e + z]) * rf * __uint_as_float(k4[z]);
+                                                if (c * 32 + 4 * e + z <= seen) most = fmaxf(most, v);
+                                            }
+                                        }
+                                    }
+                                    const float mn = fmaxf(m, most);
+                                    const float alpha = ex2(m - mn);
+                                    l *= alpha;
+                                    m = mn;
+                                    if (i > 0 || h > 0) {
+                                        const uint32_t before_it = item - x.nt;
+                                        if (h > 0 ? !warp_wait_at(bar(C::B_OHALF, buf), (item >> 1) & 1, stop)
+                                                  : !warp_wait_at(bar(C::B_ODONE, before_it & 1), (before_it >> 1) & 1, stop)) { ok = false; break; }
+                                        tc_fence_after();
+#pragma unroll 1
+                                        for (int c = 0; c < D / 32; ++c) {
+                                            uint32_t o[32];
+                                            tc_load(o_at + c * 32, o);
+#pragma unroll
+                                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                            tc_st_x32(o_at + c * 32, o);
+                                        }
+                                        tc_wait_st();
+                                    }
+                                    tc_ld_x32(s_at + h * 64, s[0]);
                                 }
+                                const f32x2 m2 = pack2(-m, -m);
+                                float top0 = -INFINITY, top1 = -INFINITY;
+                                f32x2 sum0 = 0ull, sum1 = 0ull;
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const float4 k = read4_at(k_at + c * 128 + e * 16);
-                                    y[2 * e] = fma2(y[2 * e], pack2(k.x, k.y), m2);
-                                    y[2 * e + 1] = fma2(y[2 * e + 1], pack2(k.z, k.w), m2);
-                                }
-                                if (masked) {
+                                for (int c = 0; c < 2; ++c) {
+                                    uint4 k[8];
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) k[e] = kh[c * 8 + e];
+                                    tc_wait_ld();
+                                    // (the loads' registers are complete only past the wait: nothing that reads them may move above it)
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(s[c][e]));
+                                    if (c == 0) tc_ld_x32(s_at + h * 64 + 32, s[1]);
+                                    else if (h == 0) tc_ld_x32(s_at + 64, s[0]);
+                                    f32x2 y[16];
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) y[e] = pack2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
+                                    if (rowwise) {
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e) y[e] = mul2(y[e], rf2);
+                                    }
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) {
+                                        y[2 * e] = fma2(y[2 * e], pack2(__uint_as_float(k[e].x), __uint_as_float(k[e].y)), m2);
+                                        y[2 * e + 1] = fma2(y[2 * e + 1], pack2(__uint_as_float(k[e].z), __uint_as_float(k[e].w)), m2);
+                                    }
+                                    if (masked) {
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e) {
+                                            const float2 v = unpack2(y[e]);
+                                            y[e] = pack2(c * 32 + 2 * e <= seen ? v.x : -INFINITY, c * 32 + 2 * e + 1 <= seen ? v.y : -INFINITY);
+                                        }
+                                    }
 #pragma unroll
                                     for (int e = 0; e < 16; ++e) {
                                         const float2 v = unpack2(y[e]);
-                                        y[e] = pack2(c * 32 + 2 * e <= rel ? v.x : -INFINITY, c * 32 + 2 * e + 1 <= rel ? v.y : -INFINITY);
+                                        const float p0 = ex2(v.x), p1 = ex2(v.y);
+                                        if (e & 1) {
+                                            top1 = max3(top1, v.x, v.y);
+                                            sum1 = add2(sum1, pack2(p0, p1));
+                                        } else {
+                                            top0 = max3(top0, v.x, v.y);
+                                            sum0 = add2(sum0, pack2(p0, p1));
+                                        }
+                                        P[c * 16 + e] = pack_bf16(p0, p1);
                                     }
                                 }
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    const float2 v = unpack2(y[e]);
-                                    top = max3(top, v.x, v.y);
-                                    const float p0 = ex2(v.x), p1 = ex2(v.y);
-                                    if (e & 1) sum1 = add2(sum1, pack2(p0, p1));
-                                    else sum0 = add2(sum0, pack2(p0, p1));
-                                    P[c * 16 + e] = pack_bf16(p0, p1);
+                                // (scores of 2^27 and more may pass the limit by their rounding alone)
+                                move = __any_sync(0xFFFFFFFFu, fmaxf(top0, top1) > LIMIT);
+                                if (moved || !move) {
+                                    const float2 p = unpack2(add2(sum0, sum1));
+                                    l += p.x + p.y;
+                                    break;
                                 }
                             }
-                            // (scores of 2^27 and more may pass the limit by their rounding alone)
-                            if (moved || !__any_sync(0xFFFFFFFFu, top > LIMIT)) {
-                                const float2 p = unpack2(add2(sum0, sum1));
-                                l += p.x + p.y;
-                                break;
-                            }
-                            // the reference moves to the largest score so far, what has been added up with it
-                            float most = -INFINITY;
-#pragma unroll 1
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t s1[32];
-                                tc_load(s_at + c * 32, s1);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const float k = __uint_as_float((uint32_t)read_at(k_at + c * 128 + e * 4));
-                                    const float v = __uint_as_float(s1[e]) * rf * k;
-                                    if (c * 32 + e <= rel) most = fmaxf(most, v);
-                                }
-                            }
-                            const float mn = fmaxf(m, most);
-                            const float alpha = ex2(m - mn);
-                            l *= alpha;
-                            m = mn;
-                            if (i > 0) {
-                                if (!warp_wait_at(bar(C::B_ODONE, (item - x.nt) & 1), ((item - x.nt) >> 1) & 1, stop)) { ok = false; break; }
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int c = 0; c < D / 32; ++c) {
-                                    uint32_t o[32];
-                                    tc_load(o_at + c * 32, o);
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                    tc_st_x32(o_at + c * 32, o);
-                                }
-                                tc_wait_st();
-                            }
+                            if (!ok) break;
+                            tc_st_x32(s_at + 32 * h, P);
+                            tc_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_at(bar(C::B_PFULL, 2 * buf + h));
                         }
                         if (!ok) break;
-                        tc_st_x32(s_at, P);
-                        tc_st_x32(s_at + 32, P + 32);
-                        tc_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            arrive_at(bar(C::B_PFULL, buf));
-                            arrive_at_n(bar(C::B_SCEMPTY, sc), x.nt == 2 ? 1 : 2);
-                        }
+                        if (lane == 0) arrive_at_n(bar(C::B_SCEMPTY, sc), x.nt == 2 ? 1 : 2);
                     }
                     if (!ok) break;
                     // ---- the part's output
@@ -562,6 +584,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             }
             at = after(a, at, x.units, end);
         }
+        tc_wait_ld();
         __syncwarp();
         if (lane == 0) arrive_at(bar(C::B_DONE));
     } else if (warp < 12) {
@@ -575,8 +598,8 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             const int part = lane % LPR, mine = wl * RPW + lane / LPR;
             const int rounds = x.nt * TILE / STEP;
             const __nv_bfloat16* q = a.q + (int64_t)x.tok0 * a.q_token + (int64_t)x.h * G * a.q_head + part * 8;
-            auto load = [&](int u) {
-                if (u >= x.rows) return make_uint4(0u, 0u, 0u, 0u);
+            auto load = [&](int u) {                 // (rows past the unit's last are its last again, and their results nobody's)
+                u = min(u, x.rows - 1);
                 const int t = (int)((uint32_t)u * a.by_group >> 16);
                 return *reinterpret_cast<const uint4*>(q + t * a.q_token + (u - t * G) * a.q_head);
             };
@@ -684,37 +707,44 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                         const uint32_t rs = pieces % NR, bs = pieces % NB;
                         if (!warp_wait_at(bar(C::B_RFULL, rs), (pieces / NR) & 1, stop)) { ok = false; break; }
                         if (!warp_wait_at(bar(C::B_BEMPTY, bs), ((pieces / NB) & 1) ^ 1, stop)) { ok = false; break; }
-                        constexpr int CPR = D / 16, EACH = C::VR * CPR / 128;        // 16-byte pieces of a row, of a thread
+                        constexpr int EACH = C::VR * D / 16 / 128;       // 16 codes at once, of a thread
                         const int left = x.end - t * TILE - pc * C::VR;      // rows that somebody sees; what lies behind is anything
 #pragma unroll
                         for (int e = 0; e < EACH; ++e) {
-                            const int i = e * 128 + ct, row = i / CPR, c = i % CPR;
-                            const uint4 raw = *reinterpret_cast<const uint4*>(smem + C::OFF_R + rs * C::RSLOT + i * 16);
+                            // Eight neighbours take four places of a row in one panel of 64 columns and four of the next row in the
+                            // next panel: all on different banks, where they read and where they write.
+                            const int i = e * 128 + ct;
+                            int row = i >> 2, panel = 0;
+                            if constexpr (D > 64) {
+                                constexpr int HP = D / 128;
+                                const int rest = i >> 4, odd = (i >> 2) & 1;
+                                row = rest / HP * 2 + odd;
+                                panel = rest % HP * 2 + (((i >> 3) & 1) ^ odd);
+                            }
+                            const uint4 raw = *reinterpret_cast<const uint4*>(smem + C::OFF_R + rs * C::RSLOT + row * D + panel * 64 + (i & 3) * 16);
                             const uint32_t s = bytes[pc * C::VR + row];
                             // e4m3's bits, moved to bf16's places, stand for the code times 2^-120
                             uint32_t f = s <= 134u ? (s + 120u) << 7 : 0x7F00u;
+                            if (s == 0u || row >= left) f = 0u;
                             f |= f << 16;
                             const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
                             uint32_t v[8];
 #pragma unroll
-                            for (int w = 0; w < 8; ++w) {
-                                const uint32_t two = __byte_perm(in[w / 2], 0u, w & 1 ? 0x3424 : 0x1404);
-                                v[w] = mul_bf16x2(((two >> 4) & 0x07F007F0u) | (two & 0x80008000u), f);
+                            for (int w = 0; w < 4; ++w) {
+                                // the upper bytes (sign, upper exponent bits) and the lower ones (last exponent bit, mantissa) of four values
+                                const uint32_t hi = (in[w] & 0x80808080u) | ((in[w] >> 4) & 0x07070707u), lo = (in[w] & 0x0F0F0F0Fu) * 16u;
+                                v[2 * w] = mul_bf16x2(__byte_perm(lo, hi, 0x5140), f);
+                                v[2 * w + 1] = mul_bf16x2(__byte_perm(lo, hi, 0x7362), f);
                             }
                             if (s > 134u) {
                                 const uint32_t f2 = ((s - 7u) << 7) * 0x10001u;
 #pragma unroll
                                 for (int w = 0; w < 8; ++w) v[w] = mul_bf16x2(v[w], f2);
                             }
-                            if (s == 0u || row >= left)
-#pragma unroll
-                                for (int w = 0; w < 8; ++w) v[w] = 0u;
-                            // the two halves in an order that keeps neighbours' panels on different banks
-                            const int flip = (c >> 2) & 1, q0 = (c & 3) * 2;
-                            uint8_t* to = smem + C::OFF_B + bs * C::BSLOT + (c >> 2) * C::VPANEL + row * 128;
-                            const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]), hi = make_uint4(v[4], v[5], v[6], v[7]);
-                            *reinterpret_cast<uint4*>(to + (((q0 + flip) ^ (row & 7)) << 4)) = flip ? hi : lo;
-                            *reinterpret_cast<uint4*>(to + (((q0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? lo : hi;
+                            uint8_t* to = smem + C::OFF_B + bs * C::BSLOT + panel * C::VPANEL + row * 128;
+                            const int q0 = (i & 3) * 2;
+                            *reinterpret_cast<uint4*>(to + ((q0 ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                            *reinterpret_cast<uint4*>(to + (((q0 + 1) ^ (row & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
@@ -792,95 +822,112 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             const uint64_t qd = desc_at(KD, base + C::OFF_Q), kd = desc_at(KD, base + C::OFF_K), vd = desc_at(VD, base + C::OFF_B);
             auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(0xFFFFFFFFu, test_at(b, parity)) != 0; };
-            // Two ways through the parts: of the scores and, behind it, of the outputs.
-            struct Way { Pos at; int units, nt, left; };             // left: tiles of the part that are still to be done
-            auto enter = [&](Way& w, bool go_on) {                   // the next part that has tiles; false: there is none
-                if (go_on) w.at = after(a, w.at, w.units, end);
+            // Items (tile, row tile) go in turn to the two buffers of S. Each buffer has its own way through them: scores of an
+            // item, both halves of its output, scores of the item after the next. Whatever is ready is issued.
+            struct Way {
+                Pos at;
+                int units, nt, left, r;          // row tiles; tiles of the part still to be done; row tile
+                uint32_t item, tile, piece;      // of the CTA: items, tiles, parts
+                int stage;                       // 0 scores, 1 and 2 halves of the output, 3 the end
+                bool fresh;                      // a part's first tile
+            };
+            auto enter = [&](Way& w) {                               // w.at or the next part that has tiles
+                w.fresh = true;
+                w.r = 0;
                 while (before(w.at, end)) {
                     const Unit x = unit_at<D>(a, w.at.lane, w.at.unit);
                     const int last = same_unit(w.at, end) ? min(end.tile, x.tiles) : x.tiles;
                     w.units = x.units;
                     w.nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0);
                     w.left = __shfl_sync(0xFFFFFFFFu, last - w.at.tile, 0);
-                    if (w.left > 0) return true;
+                    if (w.left > 0) return;
                     w.at = after(a, w.at, w.units, end);
                 }
                 w.left = 0;
-                return false;
+                w.stage = 3;
             };
-            Way ws{at, 0, 1, 0}, wo{at, 0, 1, 0};
-            bool more_s = enter(ws, false), more_o = enter(wo, false), fresh = true;
-            uint32_t si = 0, oi = 0, ks = 0, piece = 0, bi = 0;      // items of scores and outputs, tiles of keys, parts, pieces of values
-            int sr = 0, orow = 0;                                    // row tiles
-            while (more_o) {
+            auto next_item = [&](Way& w) {
+                if (w.stage == 3) return;
+                ++w.item;
+                if (++w.r < w.nt) return;
+                w.r = 0;
+                ++w.tile;
+                w.fresh = false;
+                if (--w.left > 0) return;
+                ++w.piece;
+                w.at = after(a, w.at, w.units, end);
+                enter(w);
+            };
+            Way way[2];
+            way[0] = Way{at, 0, 1, 0, 0, 0u, 0u, 0u, 0, true};
+            enter(way[0]);
+            way[1] = way[0];
+            next_item(way[1]);
+            uint32_t done = 0;
+            while (way[0].stage < 3 || way[1].stage < 3) {
                 bool moved = false;
-                if (oi < si && ready(bar(C::B_PFULL, oi & 1), (oi >> 1) & 1)) {
-                    bool there = true;
 #pragma unroll
-                    for (int pc = 0; pc < C::PIECES; ++pc) there = there && ready(bar(C::B_BFULL, (bi + pc) % NB), ((bi + pc) / NB) & 1);
-                    if (there) {
+                for (int b = 0; b < 2; ++b) {
+                    Way& w = way[b];
+                    if (w.stage == 0) {
+                        // (this buffer's last P has been used by an output issued before)
+                        if (!ready(bar(C::B_KFULL, w.tile % NK), (w.tile / NK) & 1) || !ready(bar(C::B_QFULL, w.piece % QB), (w.piece / QB) & 1)) continue;
                         tc_fence_after();
-                        const uint32_t o = tm + C::TMEM_O + orow * D, p = tm + (oi & 1) * TILE;
-                        const bool done = orow == wo.nt - 1;         // with this tile of values
+                        const uint32_t s = w.tile % NK, d = tm + b * TILE;
+                        const uint64_t k = kd + (uint64_t)(s * (C::KSLOT >> 4)), q = qd + (uint64_t)(w.r * (C::QTILE >> 4));
                         if (elect_one()) {
 #pragma unroll
-                            for (int pc = 0; pc < C::PIECES; ++pc) {
+                            for (int kk = 0; kk < 2 * D / 32; ++kk) {
+                                constexpr int STEPS = C::ROWB / 32, HALF = D / 32;
+                                const int kq = kk % HALF;
+                                tc_mma_f8(d, q + (((kq / STEPS) * C::QPANEL + (kk / HALF) * TILE * C::ROWB + (kq % STEPS) * 32) >> 4),
+                                          k + (((kq / STEPS) * C::KPANEL + (kq % STEPS) * 32) >> 4), ID_S, kk ? 1u : 0u);
+                            }
+                            commit_at(bar(C::B_SFULL, b));
+                            for (int z = w.nt; z < 3; ++z) {         // one row tile arrives for two
+                                commit_at(bar(C::B_KEMPTY, s));
+                                if (w.left == 1) commit_at(bar(C::B_QFREE));
+                            }
+                        }
+                        __syncwarp();
+                        w.stage = 1;
+                        moved = true;
+                    } else if (w.stage < 3) {
+                        constexpr int PH = C::PIECES / 2;
+                        const int h = w.stage - 1;
+                        // one row tile's outputs go in order: the first of them clears O
+                        if (w.nt == 1 && way[1 - b].stage < 3 && way[1 - b].item < w.item) continue;
+                        if (!ready(bar(C::B_PFULL, 2 * b + h), (w.item >> 1) & 1)) continue;
+                        const uint32_t bi = w.tile * C::PIECES + h * PH;
+                        bool there = true;
+#pragma unroll
+                        for (int pc = 0; pc < PH; ++pc) there = there && ready(bar(C::B_BFULL, (bi + pc) % NB), ((bi + pc) / NB) & 1);
+                        if (!there) continue;
+                        tc_fence_after();
+                        const uint32_t o = tm + C::TMEM_O + w.r * D, p = tm + b * TILE + h * 32;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int pc = 0; pc < PH; ++pc) {
                                 const uint32_t bs = (bi + pc) % NB;
                                 const uint64_t v = vd + (uint64_t)(bs * (C::BSLOT >> 4));
 #pragma unroll
                                 for (int kk = 0; kk < C::VR / 16; ++kk)
-                                    tc_mma_f16_ts(o, p + pc * (C::VR / 2) + kk * 8, v + kk * (2048 >> 4), ID_PV, fresh && pc == 0 && kk == 0 ? 0u : 1u);
-                                if (done) commit_at(bar(C::B_BEMPTY, bs));
+                                    tc_mma_f16_ts(o, p + pc * (C::VR / 2) + kk * 8, v + kk * (2048 >> 4), ID_PV, w.fresh && h == 0 && pc == 0 && kk == 0 ? 0u : 1u);
+                                for (int z = w.nt; z < 3; ++z) commit_at(bar(C::B_BEMPTY, bs));
                             }
-                            commit_at(bar(C::B_ODONE, oi & 1));
+                            commit_at(bar(h ? C::B_ODONE : C::B_OHALF, b));
                         }
                         __syncwarp();
-                        progress[0] = ++oi;
-                        if (done) {
-                            orow = 0;
-                            bi += C::PIECES;
-                            fresh = false;
-                            if (--wo.left == 0) {
-                                more_o = enter(wo, true);
-                                fresh = true;
-                            }
+                        progress[0] = ++done;
+                        if (h == 0) {
+                            w.stage = 2;
                         } else {
-                            ++orow;
+                            w.stage = 0;
+                            next_item(w);
+                            next_item(w);
                         }
                         moved = true;
                     }
-                }
-                // the buffer's P has been read: by the output issued two items ago
-                if (more_s && si < oi + 2 && ready(bar(C::B_KFULL, ks % NK), (ks / NK) & 1) && ready(bar(C::B_QFULL, piece % QB), (piece / QB) & 1)) {
-                    tc_fence_after();
-                    const uint32_t s = ks % NK, d = tm + (si & 1) * TILE;
-                    const uint64_t k = kd + (uint64_t)(s * (C::KSLOT >> 4)), q = qd + (uint64_t)(sr * (C::QTILE >> 4));
-                    const bool done = sr == ws.nt - 1;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < 2 * D / 32; ++kk) {
-                            constexpr int STEPS = C::ROWB / 32, HALF = D / 32;
-                            const int kq = kk % HALF;
-                            tc_mma_f8(d, q + (((kq / STEPS) * C::QPANEL + (kk / HALF) * TILE * C::ROWB + (kq % STEPS) * 32) >> 4),
-                                      k + (((kq / STEPS) * C::KPANEL + (kq % STEPS) * 32) >> 4), ID_S, kk ? 1u : 0u);
-                        }
-                        commit_at(bar(C::B_SFULL, si & 1));
-                        if (done) commit_at(bar(C::B_KEMPTY, s));
-                        if (done && ws.left == 1) commit_at(bar(C::B_QFREE));
-                    }
-                    __syncwarp();
-                    ++si;
-                    if (done) {
-                        sr = 0;
-                        ++ks;
-                        if (--ws.left == 0) {
-                            ++piece;
-                            more_s = enter(ws, true);
-                        }
-                    } else {
-                        ++sr;
-                    }
-                    moved = true;
                 }
                 if (!moved && __any_sync(0xFFFFFFFFu, stopped(stop))) break;
             }
