@@ -32,6 +32,7 @@
 #include <cuda_fp8.h>
 
 #include <climits>
+#include <type_traits>
 
 #include "attention.cuh"
 
@@ -77,6 +78,15 @@ MOE_DEV bool before(const Pos& a, const Pos& b) {
     return a.lane != b.lane ? a.lane < b.lane : a.unit != b.unit ? a.unit < b.unit : a.tile < b.tile;
 }
 
+// A CTA's way through its part of the run: a unit, and its tiles [t0, t1) that are this CTA's. One warp walks and tells the
+// others (six copies of the walk would crowd the softmax out of the instruction cache).
+struct alignas(16) Part {
+    int b, h, tok0, first;                       // lane, kv head, first token, its own row (as in Unit)
+    int rows, nt, end, tiles;
+    int t0, t1;                                  // t1 = 0: there are no more
+    int pad[2];
+};
+
 template <int D>
 struct Cfg {
     static constexpr int NT = D <= 128 ? 2 : 1;               // row tiles of a unit
@@ -86,12 +96,12 @@ struct Cfg {
     static constexpr int PANELS = D / ROWB;
     static constexpr int KPANEL = TILE * ROWB, KSLOT = TILE * D;
     static constexpr int QPANEL = 2 * TILE * ROWB, QTILE = 2 * TILE * D;      // hi, then lo
-    static constexpr int NK = D == 64 ? 6 : D == 128 ? 3 : 2; // ring of key tiles
+    static constexpr int NK = D == 64 ? 8 : D == 128 ? 3 : 2; // ring of key tiles
     static constexpr int VR = D == 256 ? 32 : 64;             // values come in pieces of so many rows
     static constexpr int PIECES = TILE / VR;
     static constexpr int NR = D == 64 ? 8 : D == 128 ? 4 : 3; // ring of pieces as codes
     static constexpr int RSLOT = VR * D;
-    static constexpr int NB = D == 64 ? 6 : 4;                // ring of pieces in bf16
+    static constexpr int NB = D == 64 ? 8 : 4;                // ring of pieces in bf16
     static constexpr int VPANEL = VR * 128, BSLOT = VR * D * 2;
     static constexpr int SA = 4, NSC = 2 * SA;                // tiles that scales are under way ahead; their ring:
     static constexpr int SC_BYTES = 3 * TILE * 2;             // key bytes, value bytes, the columns' factors (float)
@@ -107,7 +117,9 @@ struct Cfg {
     static constexpr int OFF_QF = OFF_SID + 2 * SA * 128;     // [QB][ROWS] 2^-a of the queries' rows
     static constexpr int OFF_QU = OFF_QF + QB * ROWS * 4;     // [QB][2] 2^-a of a unit's rows; whether they differ instead
     static constexpr int OFF_QX = OFF_QU + QB * 8;            // [2][largest, smallest][4 warps]
-    static constexpr int OFF_BAR = OFF_QX + 64;
+    static constexpr int NPD = 4;                             // parts that are told ahead
+    static constexpr int OFF_PD = OFF_QX + 64;
+    static constexpr int OFF_BAR = OFF_PD + NPD * (int)sizeof(Part);
     static constexpr int B_KFULL = OFF_BAR;                   // [NK] a tile of keys has arrived
     static constexpr int B_KEMPTY = B_KFULL + 8 * NK;         // [NK] ... has been used
     static constexpr int B_RFULL = B_KEMPTY + 8 * NK;         // [NR] a piece of values has arrived
@@ -123,12 +135,14 @@ struct Cfg {
     static constexpr int B_QFULL = B_ODONE + 16;              // [QB] the queries of a part are there
     static constexpr int B_QFREE = B_QFULL + 8 * QB;              // ... have been used
     static constexpr int B_QMAX = B_QFREE + 8;                // the four warps have their maxima
-    static constexpr int B_DONE = B_QMAX + 8;                 // the block's last output is written
+    static constexpr int B_PDFULL = B_QMAX + 8;               // [NPD] a part is told
+    static constexpr int B_PDEMPTY = B_PDFULL + 8 * NPD;      // [NPD] ... and read: by fourteen warps and, for its second way, MMA issue once more
+    static constexpr int B_DONE = B_PDEMPTY + 8 * NPD;                 // the block's last output is written
     static constexpr int B_DRAIN = B_DONE + 8;
     static constexpr int OFF_MISC = (B_DRAIN + 8 + 15) / 16 * 16;     // tmem slot, abort flag, progress [2], start, end
     static constexpr int SMEM = OFF_MISC + 16 + 32 + 1024;
     static constexpr int TMEM_O = 2 * TILE;                   // after S [2]
-    static constexpr int SOFT_REGS = 168, CONV_REGS = 88, REST_REGS = 88;     // 2 x 168 + 88 + 88 = 4 x 128
+    static constexpr int SOFT_REGS = 184, CONV_REGS = 80, REST_REGS = 64;     // 2 x 184 + 80 + 64 = 4 x 128
     static_assert(OFF_B % 1024 == 0 && OFF_R % 128 == 0 && OFF_K % 1024 == 0 && BSLOT % 1024 == 0, "alignment");
     static_assert(OFF_BAR % 8 == 0 && OFF_QF % 16 == 0 && SMEM <= 227 * 1024, "shared memory");
     static_assert(2 * SOFT_REGS + CONV_REGS + REST_REGS <= 512, "registers");
@@ -160,6 +174,17 @@ MOE_DEV void tc_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
+}
+// What reads the registers of a tcgen05.ld under way: volatile, so that it stays behind the wait, which is too.
+MOE_DEV f32x2 fma2_loaded(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm volatile("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+MOE_DEV f32x2 mul2_loaded(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm volatile("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 MOE_DEV void tc_st_x32(uint32_t taddr, const uint32_t* r) {
     asm volatile(
@@ -236,14 +261,21 @@ MOE_DEV Unit unit_at(const ChunkArgs& a, int b, int u) {
     x.units = a.c.n_kv_heads * blocks;
     return x;
 }
-// The unit after p's, at its first tile.
-MOE_DEV Pos after(const ChunkArgs& a, const Pos& p, int units, const Pos& end) {
-    Pos n{p.lane, p.unit + 1, 0, 0};
-    if (n.unit < units) return n;
-    n.unit = 0;
-    bool bad;
-    do ++n.lane; while (n.lane < end.lane && lane_facts(a, n.lane, &bad).n == 0);
-    return n;
+template <int D>
+MOE_DEV Part next_part(const ChunkArgs& a, const Pos& end, Pos& at, int& units) {      // units: of the lane; 0 before the first part
+    for (;;) {
+        if (units > 0 && ++at.unit >= units) {
+            at.unit = 0;
+            bool bad;
+            do ++at.lane; while (at.lane < end.lane && lane_facts(a, at.lane, &bad).n == 0);
+        }
+        if (units > 0) at.tile = 0;
+        if (!before(at, end)) return Part{};
+        const Unit x = unit_at<D>(a, at.lane, at.unit);
+        units = x.units;
+        const int t1 = same_unit(at, end) ? min(end.tile, x.tiles) : x.tiles;
+        if (t1 > at.tile) return Part{x.b, x.h, x.tok0, x.first, x.rows, x.nt, x.end, x.tiles, at.tile, t1, {0, 0}};
+    }
 }
 
 // Costs of the units before block rb of a head with n tokens (rb full blocks; the last may be short).
@@ -368,7 +400,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
         init(C::B_KFULL, NK, 1); init(C::B_KEMPTY, NK, 2); init(C::B_RFULL, NR, 1); init(C::B_REMPTY, NR, 4);
         init(C::B_BFULL, NB, 4); init(C::B_BEMPTY, NB, 2); init(C::B_SCFULL, NSC, 1); init(C::B_SCEMPTY, NSC, 12);
         init(C::B_SFULL, 2, 1); init(C::B_PFULL, 4, 4); init(C::B_OHALF, 2, 1); init(C::B_ODONE, 2, 1); init(C::B_QFULL, QB, 4); init(C::B_QFREE, 1, 2);
-        init(C::B_QMAX, 1, 4); init(C::B_DONE, 1, 8); init(C::B_DRAIN, 1, 1);
+        init(C::B_QMAX, 1, 4); init(C::B_PDFULL, C::NPD, 1); init(C::B_PDEMPTY, C::NPD, 16); init(C::B_DONE, 1, 8); init(C::B_DRAIN, 1, 1);
         *abort_flag = 0;
         progress[0] = progress[1] = 0;
         fence_barrier_init();
@@ -382,11 +414,18 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const Pos end = ends[1];
-    Pos at = ends[0];
+    // The n-th part of this CTA, for a whole warp; false: there is none, or the block has been stopped.
+    auto part_at = [&](uint32_t n, Part& p) -> bool {
+        if (!warp_wait_at(bar(C::B_PDFULL, n % C::NPD), (n / C::NPD) & 1, stop)) return false;
+        const int4* from = reinterpret_cast<const int4*>(smem + C::OFF_PD + (n % C::NPD) * sizeof(Part));
+        *reinterpret_cast<int4*>(&p.b) = from[0];
+        *reinterpret_cast<int4*>(&p.rows) = from[1];
+        *reinterpret_cast<int2*>(&p.t0) = *reinterpret_cast<const int2*>(from + 2);
+        __syncwarp();
+        if (lane == 0) arrive_at(bar(C::B_PDEMPTY, n % C::NPD));
+        return p.t1 > 0;
+    };
     uint32_t issued_k = 0, issued_r = 0;             // ring fills, by the producer
-    // tiles [at.tile, last) of unit x belong to this CTA
-    auto last_tile = [&](const Unit& x) { return same_unit(at, end) ? min(end.tile, x.tiles) : x.tiles; };
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax: a thread is a row
@@ -395,10 +434,10 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
         const uint32_t trow = tmem + ((uint32_t)(wl * 32) << 16);
         uint32_t items = 0, tiles = 0, piece = 0;    // of the CTA: items (tile, row tile), tiles, parts
         bool ok = true;
-        while (ok && before(at, end)) {
-            const Unit x = unit_at<D>(a, at.lane, at.unit);
-            const int t0 = at.tile, t1 = last_tile(x), nt = t1 - t0;
-            if (nt > 0) {
+        Part x;
+        while (ok && part_at(piece, x)) {
+            const int t0 = x.t0, t1 = x.t1, nt = t1 - t0;
+            {
                 // (a group that has no rows here waits too: it may not run ahead of barriers whose phases it does not see)
                 if (!warp_wait_at(bar(C::B_QFULL, piece % QB), (piece / QB) & 1, stop)) break;
                 if (g < x.nt) {
@@ -423,34 +462,30 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                         if (!warp_wait_at(bar(C::B_SFULL, buf), (item >> 1) & 1, stop)) { ok = false; break; }
                         tc_fence_after();
                         const uint4* kf = reinterpret_cast<const uint4*>(smem + C::OFF_SC + sc * C::SC_BYTES + 2 * TILE);
-                        uint32_t s[2][32];
-                        tc_ld_x32(s_at, s[0]);
                         // half a tile at a time, so that its weights are at work while the other half's are made
 #pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
-                            const int seen = rel - 64 * h;           // columns of this half up to here are seen
+                            const int seen = masked ? rel - 64 * h : TILE;   // columns of this half up to here are seen
+                            const uint32_t sh = s_at + h * 64;
                             const uint4* kh = kf + 16 * h;
                             uint32_t P[32];
                             bool move = i == 0 && h == 0;
                             for (bool moved = false;; moved = true) {
                                 if (move) {
-                                    tc_wait_ld();                    // (what is under way goes to registers that are used again)
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(s[0][e]));
                                     // the reference moves to the largest score so far, and what has been added up with it
                                     float most = -INFINITY;
+#pragma unroll 1
+                                    for (int c = 0; c < 4; ++c) {
+                                        uint32_t s1[16];
+                                        tc_load(sh + c * 16, s1);
 #pragma unroll
-                                    for (int c = 0; c < 2; ++c) {
-                                        uint32_t s1[32];
-                                        tc_load(s_at + h * 64 + c * 32, s1);
-#pragma unroll
-                                        for (int e = 0; e < 8; ++e) {
-                                            const uint4 k = kh[c * 8 + e];
+                                        for (int e = 0; e < 4; ++e) {
+                                            const uint4 k = kh[c * 4 + e];
                                             const uint32_t k4[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
                                             for (int z = 0; z < 4; ++z) {
                                                 const float v = __uint_as_float(s1[4 * e + z]) * rf * __uint_as_float(k4[z]);
-                                                if (c * 32 + 4 * e + z <= seen) most = fmaxf(most, v);
+                                                if (c * 16 + 4 * e + z <= seen) most = fmaxf(most, v);
                                             }
                                         }
                                     }
@@ -464,64 +499,54 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                                                   : !warp_wait_at(bar(C::B_ODONE, before_it & 1), (before_it >> 1) & 1, stop)) { ok = false; break; }
                                         tc_fence_after();
 #pragma unroll 1
-                                        for (int c = 0; c < D / 32; ++c) {
-                                            uint32_t o[32];
-                                            tc_load(o_at + c * 32, o);
+                                        for (int c = 0; c < D / 8; ++c) {
+                                            uint32_t o[8];
+                                            tc_ld_x8(o_at + c * 8, o);
+                                            tc_wait_ld();
 #pragma unroll
-                                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                            tc_st_x32(o_at + c * 32, o);
+                                            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                            tc_st_x8(o_at + c * 8, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
                                         }
                                         tc_wait_st();
                                     }
-                                    tc_ld_x32(s_at + h * 64, s[0]);
                                 }
                                 const f32x2 m2 = pack2(-m, -m);
                                 float top0 = -INFINITY, top1 = -INFINITY;
                                 f32x2 sum0 = 0ull, sum1 = 0ull;
-#pragma unroll
-                                for (int c = 0; c < 2; ++c) {
-                                    uint4 k[8];
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) k[e] = kh[c * 8 + e];
+                                // Weights of the half. A form of its own for tiles that need no more than the reference: branches within would
+                                // have the scores copied from where the loads leave them (two moves a pair).
+                                auto weights = [&](auto plain) {
+                                    uint32_t s[2][32];
+                                    tc_ld_x32(sh, s[0]);
+                                    tc_ld_x32(sh + 32, s[1]);
                                     tc_wait_ld();
-                                    // (the loads' registers are complete only past the wait: nothing that reads them may move above it)
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(s[c][e]));
-                                    if (c == 0) tc_ld_x32(s_at + h * 64 + 32, s[1]);
-                                    else if (h == 0) tc_ld_x32(s_at + 64, s[0]);
-                                    f32x2 y[16];
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) y[e] = pack2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
-                                    if (rowwise) {
-#pragma unroll
-                                        for (int e = 0; e < 16; ++e) y[e] = mul2(y[e], rf2);
-                                    }
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) {
-                                        y[2 * e] = fma2(y[2 * e], pack2(__uint_as_float(k[e].x), __uint_as_float(k[e].y)), m2);
-                                        y[2 * e + 1] = fma2(y[2 * e + 1], pack2(__uint_as_float(k[e].z), __uint_as_float(k[e].w)), m2);
-                                    }
-                                    if (masked) {
+                                    for (int c = 0; c < 2; ++c) {
 #pragma unroll
                                         for (int e = 0; e < 16; ++e) {
-                                            const float2 v = unpack2(y[e]);
-                                            y[e] = pack2(c * 32 + 2 * e <= seen ? v.x : -INFINITY, c * 32 + 2 * e + 1 <= seen ? v.y : -INFINITY);
+                                            const uint4 kk = kh[c * 8 + e / 2];
+                                            f32x2 y = pack2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
+                                            if constexpr (!plain) y = mul2_loaded(y, rf2);
+                                            y = fma2_loaded(y, e & 1 ? pack2(__uint_as_float(kk.z), __uint_as_float(kk.w)) : pack2(__uint_as_float(kk.x), __uint_as_float(kk.y)), m2);
+                                            float2 v = unpack2(y);
+                                            if constexpr (!plain) {
+                                                if (c * 32 + 2 * e > seen) v.x = -INFINITY;
+                                                if (c * 32 + 2 * e + 1 > seen) v.y = -INFINITY;
+                                            }
+                                            const float p0 = ex2(v.x), p1 = ex2(v.y);
+                                            if (e & 1) {
+                                                top1 = max3(top1, v.x, v.y);
+                                                sum1 = add2(sum1, pack2(p0, p1));
+                                            } else {
+                                                top0 = max3(top0, v.x, v.y);
+                                                sum0 = add2(sum0, pack2(p0, p1));
+                                            }
+                                            P[c * 16 + e] = pack_bf16(p0, p1);
                                         }
                                     }
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) {
-                                        const float2 v = unpack2(y[e]);
-                                        const float p0 = ex2(v.x), p1 = ex2(v.y);
-                                        if (e & 1) {
-                                            top1 = max3(top1, v.x, v.y);
-                                            sum1 = add2(sum1, pack2(p0, p1));
-                                        } else {
-                                            top0 = max3(top0, v.x, v.y);
-                                            sum0 = add2(sum0, pack2(p0, p1));
-                                        }
-                                        P[c * 16 + e] = pack_bf16(p0, p1);
-                                    }
-                                }
+                                };
+                                if (rowwise || masked) weights(std::false_type{});
+                                else weights(std::true_type{});
                                 // (scores of 2^27 and more may pass the limit by their rounding alone)
                                 move = __any_sync(0xFFFFFFFFu, fmaxf(top0, top1) > LIMIT);
                                 if (moved || !move) {
@@ -582,7 +607,6 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                 tiles += nt;
                 ++piece;
             }
-            at = after(a, at, x.units, end);
         }
         tc_wait_ld();
         __syncwarp();
@@ -592,9 +616,9 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
         regs_down<C::CONV_REGS>();
         const int wl = warp & 3, ct = tid & 127;
         // A unit's queries: their largest size first, then the parts.
-        auto prepare = [&](const Unit& x, uint32_t piece) -> bool {
+        auto prepare = [&](const Part& x, uint32_t piece) -> bool {
             constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = 4 * RPW;        // lanes a row, rows a warp takes at once, all four
-            constexpr int BATCH = 8;
+            constexpr int BATCH = 4;
             const int part = lane % LPR, mine = wl * RPW + lane / LPR;
             const int rounds = x.nt * TILE / STEP;
             const __nv_bfloat16* q = a.q + (int64_t)x.tok0 * a.q_token + (int64_t)x.h * G * a.q_head + part * 8;
@@ -692,10 +716,10 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
         };
         uint32_t tiles = 0, pieces = 0, piece = 0;
         bool ok = true;
-        while (ok && before(at, end)) {
-            const Unit x = unit_at<D>(a, at.lane, at.unit);
-            const int t0 = at.tile, t1 = last_tile(x);
-            if (t1 > t0) {
+        Part x;
+        while (ok && part_at(piece, x)) {
+            const int t0 = x.t0, t1 = x.t1;
+            {
                 if (!prepare(x, piece)) break;
                 ++piece;
                 for (int t = t0; t < t1 && ok; ++t, ++tiles) {
@@ -709,7 +733,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                         if (!warp_wait_at(bar(C::B_BEMPTY, bs), ((pieces / NB) & 1) ^ 1, stop)) { ok = false; break; }
                         constexpr int EACH = C::VR * D / 16 / 128;       // 16 codes at once, of a thread
                         const int left = x.end - t * TILE - pc * C::VR;      // rows that somebody sees; what lies behind is anything
-#pragma unroll
+#pragma unroll 2
                         for (int e = 0; e < EACH; ++e) {
                             // Eight neighbours take four places of a row in one panel of 64 columns and four of the next row in the
                             // next panel: all on different banks, where they read and where they write.
@@ -756,7 +780,6 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                     if (ok && lane == 0) arrive_at(bar(C::B_SCEMPTY, sc));
                 }
             }
-            at = after(a, at, x.units, end);
         }
     } else {
         regs_down<C::REST_REGS>();
@@ -770,9 +793,9 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             // -------------------------------------------------------- TMA: lane l < 8 looks up the page of the tile's rows 16 l ..
             const int rk = P < TILE ? P : TILE, rv = P < C::VR ? P : C::VR;          // rows a copy
             bool ok = true;
-            while (ok && before(at, end)) {
-                const Unit x = unit_at<D>(a, at.lane, at.unit);
-                const int t0 = at.tile, t1 = last_tile(x), hp = x.h * P;
+            Part x;
+            for (uint32_t n = 0; ok && part_at(n, x); ++n) {
+                const int t0 = x.t0, t1 = x.t1, hp = x.h * P;
                 const int32_t* table = a.table + (int64_t)x.b * a.width;
                 auto look = [&](int t) {
                     const int j = t * TILE + lane * 16;
@@ -799,6 +822,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                             for (int q = 0; q < C::PANELS; ++q)
                                 tma_load_at(base + C::OFF_K + s * C::KSLOT + q * C::KPANEL + lane * rk * C::ROWB, &maps.k, bar(C::B_KFULL, s), q * 128, r);
                     }
+#pragma unroll 1
                     for (int pc = 0; pc < C::PIECES; ++pc) {
                         const uint32_t s = issued_r % NR;
                         const int in = pc * C::VR + lane * rv;
@@ -812,7 +836,6 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                         if (some) tma_load_at(base + C::OFF_R + s * C::RSLOT + lane * rv * D, &maps.v, bar(C::B_RFULL, s), 0, first);
                     }
                 }
-                at = after(a, at, x.units, end);
             }
         } else if (warp == 13) {
             // -------------------------------------------------------- MMA issue: whatever is ready, outputs first
@@ -820,31 +843,32 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             constexpr uint64_t VD = desc_base(2, C::VPANEL, 1024);
             constexpr uint32_t ID_S = idesc_f8(TILE, TILE, 0, 0, 0), ID_PV = idesc_bf16(TILE, D);
             const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-            const uint64_t qd = desc_at(KD, base + C::OFF_Q), kd = desc_at(KD, base + C::OFF_K), vd = desc_at(VD, base + C::OFF_B);
-            auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(0xFFFFFFFFu, test_at(b, parity)) != 0; };
+            // A descriptor's lower word changes, its upper one is constant. Lower words go through a shuffle, which leaves them
+            // in uniform registers: an MMA then costs its issue and no moves of its operands (four words each, 80 clocks).
+            auto lower = [&](uint64_t kind, uint32_t at_byte) { return __shfl_sync(0xFFFFFFFFu, (uint32_t)kind + (at_byte >> 4), 0); };
+            auto desc = [](uint64_t kind, uint32_t lo) {
+                uint64_t d;
+                asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"((uint32_t)(kind >> 32)));
+                return d;
+            };
             // Items (tile, row tile) go in turn to the two buffers of S. Each buffer has its own way through them: scores of an
             // item, both halves of its output, scores of the item after the next. Whatever is ready is issued.
             struct Way {
-                Pos at;
-                int units, nt, left, r;          // row tiles; tiles of the part still to be done; row tile
+                int b, nt, left, r;              // buffer; row tiles; tiles of the part still to be done; row tile
                 uint32_t item, tile, piece;      // of the CTA: items, tiles, parts
                 int stage;                       // 0 scores, 1 and 2 halves of the output, 3 the end
                 bool fresh;                      // a part's first tile
             };
-            auto enter = [&](Way& w) {                               // w.at or the next part that has tiles
+            auto enter = [&](Way& w) {
                 w.fresh = true;
                 w.r = 0;
-                while (before(w.at, end)) {
-                    const Unit x = unit_at<D>(a, w.at.lane, w.at.unit);
-                    const int last = same_unit(w.at, end) ? min(end.tile, x.tiles) : x.tiles;
-                    w.units = x.units;
+                Part x;
+                if (part_at(w.piece, x)) {
                     w.nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0);
-                    w.left = __shfl_sync(0xFFFFFFFFu, last - w.at.tile, 0);
-                    if (w.left > 0) return;
-                    w.at = after(a, w.at, w.units, end);
+                    w.left = __shfl_sync(0xFFFFFFFFu, x.t1 - x.t0, 0);
+                } else {
+                    w.stage = 3;
                 }
-                w.left = 0;
-                w.stage = 3;
             };
             auto next_item = [&](Way& w) {
                 if (w.stage == 3) return;
@@ -855,33 +879,53 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                 w.fresh = false;
                 if (--w.left > 0) return;
                 ++w.piece;
-                w.at = after(a, w.at, w.units, end);
                 enter(w);
             };
-            Way way[2];
-            way[0] = Way{at, 0, 1, 0, 0, 0u, 0u, 0u, 0, true};
-            enter(way[0]);
-            way[1] = way[0];
-            next_item(way[1]);
+            Way now{0, 1, 0, 0, 0u, 0u, 0u, 0, true}, other{1, 1, 0, 0, 0u, 0u, 0u, 0, true};
+            enter(now);
+            enter(other);
+            next_item(other);
+            // What the next step of buffer b waits for is tested by lanes 8 b ..: all at once.
+            constexpr int PH = C::PIECES / 2;                        // pieces of values of half a tile
+            uint32_t my_bar = 0, my_parity = 0;
+            const int my_b = (lane >> 3) & 1, my_k = lane & 7;
+            auto aim = [&]() {
+                const Way& w = my_b == now.b ? now : other;
+                if (w.stage == 0) {
+                    my_bar = my_k == 0 ? bar(C::B_KFULL, w.tile % NK) : bar(C::B_QFULL, w.piece % QB);
+                    my_parity = my_k == 0 ? w.tile / NK : w.piece / QB;
+                } else {
+                    const uint32_t bi = w.tile * C::PIECES + (w.stage - 1) * PH + (my_k > 1 ? PH - 1 : 0);
+                    my_bar = my_k == 0 ? bar(C::B_PFULL, 2 * my_b + w.stage - 1) : bar(C::B_BFULL, bi % NB);
+                    my_parity = my_k == 0 ? w.item >> 1 : bi / NB;
+                }
+                my_parity &= 1;
+            };
+            aim();
             uint32_t done = 0;
-            while (way[0].stage < 3 || way[1].stage < 3) {
+            while (now.stage < 3 || other.stage < 3) {
+                const uint32_t there = __ballot_sync(0xFFFFFFFFu, test_at(my_bar, my_parity));
                 bool moved = false;
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    Way& w = way[b];
+#pragma unroll 1
+                for (int turn = 0; turn < 2; ++turn) {
+                    const Way swap = now;
+                    now = other;
+                    other = swap;
+                    Way& w = now;
+                    const int b = w.b;
+                    if (((there >> (8 * b)) & 255u) != 255u || w.stage == 3) continue;
                     if (w.stage == 0) {
                         // (this buffer's last P has been used by an output issued before)
-                        if (!ready(bar(C::B_KFULL, w.tile % NK), (w.tile / NK) & 1) || !ready(bar(C::B_QFULL, w.piece % QB), (w.piece / QB) & 1)) continue;
                         tc_fence_after();
-                        const uint32_t s = w.tile % NK, d = tm + b * TILE;
-                        const uint64_t k = kd + (uint64_t)(s * (C::KSLOT >> 4)), q = qd + (uint64_t)(w.r * (C::QTILE >> 4));
+                        const uint32_t s = w.tile % NK, d = __shfl_sync(0xFFFFFFFFu, tm + b * TILE, 0);
+                        const uint32_t k = lower(KD, base + C::OFF_K + s * C::KSLOT), q = lower(KD, base + C::OFF_Q + w.r * C::QTILE);
                         if (elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < 2 * D / 32; ++kk) {
                                 constexpr int STEPS = C::ROWB / 32, HALF = D / 32;
                                 const int kq = kk % HALF;
-                                tc_mma_f8(d, q + (((kq / STEPS) * C::QPANEL + (kk / HALF) * TILE * C::ROWB + (kq % STEPS) * 32) >> 4),
-                                          k + (((kq / STEPS) * C::KPANEL + (kq % STEPS) * 32) >> 4), ID_S, kk ? 1u : 0u);
+                                tc_mma_f8(d, desc(KD, q + (((kq / STEPS) * C::QPANEL + (kk / HALF) * TILE * C::ROWB + (kq % STEPS) * 32) >> 4)),
+                                          desc(KD, k + (((kq / STEPS) * C::KPANEL + (kq % STEPS) * 32) >> 4)), ID_S, kk ? 1u : 0u);
                             }
                             commit_at(bar(C::B_SFULL, b));
                             for (int z = w.nt; z < 3; ++z) {         // one row tile arrives for two
@@ -891,29 +935,24 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                         }
                         __syncwarp();
                         w.stage = 1;
-                        moved = true;
-                    } else if (w.stage < 3) {
-                        constexpr int PH = C::PIECES / 2;
+                    } else {
                         const int h = w.stage - 1;
                         // one row tile's outputs go in order: the first of them clears O
-                        if (w.nt == 1 && way[1 - b].stage < 3 && way[1 - b].item < w.item) continue;
-                        if (!ready(bar(C::B_PFULL, 2 * b + h), (w.item >> 1) & 1)) continue;
-                        const uint32_t bi = w.tile * C::PIECES + h * PH;
-                        bool there = true;
-#pragma unroll
-                        for (int pc = 0; pc < PH; ++pc) there = there && ready(bar(C::B_BFULL, (bi + pc) % NB), ((bi + pc) / NB) & 1);
-                        if (!there) continue;
+                        if (w.nt == 1 && other.stage < 3 && other.item < w.item) continue;
                         tc_fence_after();
-                        const uint32_t o = tm + C::TMEM_O + w.r * D, p = tm + b * TILE + h * 32;
+                        const uint32_t bi = w.tile * C::PIECES + h * PH;
+                        const uint32_t o = __shfl_sync(0xFFFFFFFFu, tm + C::TMEM_O + w.r * D, 0), p = __shfl_sync(0xFFFFFFFFu, tm + b * TILE + h * 32, 0);
+                        const uint32_t add = __shfl_sync(0xFFFFFFFFu, w.fresh && h == 0 ? 0u : 1u, 0);
+                        uint32_t v[PH];
+#pragma unroll
+                        for (int pc = 0; pc < PH; ++pc) v[pc] = lower(VD, base + C::OFF_B + (bi + pc) % NB * C::BSLOT);
                         if (elect_one()) {
 #pragma unroll
                             for (int pc = 0; pc < PH; ++pc) {
-                                const uint32_t bs = (bi + pc) % NB;
-                                const uint64_t v = vd + (uint64_t)(bs * (C::BSLOT >> 4));
 #pragma unroll
                                 for (int kk = 0; kk < C::VR / 16; ++kk)
-                                    tc_mma_f16_ts(o, p + pc * (C::VR / 2) + kk * 8, v + kk * (2048 >> 4), ID_PV, w.fresh && h == 0 && pc == 0 && kk == 0 ? 0u : 1u);
-                                for (int z = w.nt; z < 3; ++z) commit_at(bar(C::B_BEMPTY, bs));
+                                    tc_mma_f16_ts(o, p + pc * (C::VR / 2) + kk * 8, desc(VD, v[pc] + kk * (2048 >> 4)), ID_PV, pc == 0 && kk == 0 ? add : 1u);
+                                for (int z = w.nt; z < 3; ++z) commit_at(bar(C::B_BEMPTY, (bi + pc) % NB));
                             }
                             commit_at(bar(h ? C::B_ODONE : C::B_OHALF, b));
                         }
@@ -926,17 +965,37 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                             next_item(w);
                             next_item(w);
                         }
-                        moved = true;
                     }
+                    moved = true;
                 }
-                if (!moved && __any_sync(0xFFFFFFFFu, stopped(stop))) break;
+                if (moved) aim();
+                else if (__any_sync(0xFFFFFFFFu, stopped(stop))) break;
             }
         } else if (warp == 15) {
-            // -------------------------------------------------------- watchdog: stops the block when nothing has moved for the bound
-            uint32_t seen = 0;
+            // -------------------------------------------------------- tells the parts, and stops the block when nothing has
+            // moved for the bound
+            const Pos end = ends[1];
+            Pos at = ends[0];
+            int units = 0;
+            uint32_t told = 0, seen = 0;
+            bool more = true;
             uint64_t since = global_timer_ns();
             const bool nap = a.wait_ns >= 40000ull;  // (asleep for some 20 us, whatever less is asked for)
-            while (!(nap ? try_at_for(bar(C::B_DONE), 0, 20000) : test_at(bar(C::B_DONE), 0)) && !stopped(stop)) {
+            auto look = [&](uint32_t b, uint32_t parity) { return __all_sync(0xFFFFFFFFu, nap ? try_at_for(b, parity, 20000) : test_at(b, parity)) != 0; };
+            while (!__any_sync(0xFFFFFFFFu, stopped(stop))) {
+                const uint32_t slot = told % C::NPD;
+                if (more && look(bar(C::B_PDEMPTY, slot), ((told / C::NPD) & 1) ^ 1)) {
+                    const Part p = next_part<D>(a, end, at, units);
+                    if (lane == 0) {
+                        *reinterpret_cast<Part*>(smem + C::OFF_PD + slot * sizeof(Part)) = p;
+                        arrive_at(bar(C::B_PDFULL, slot));
+                    }
+                    __syncwarp();
+                    more = p.t1 > 0;
+                    ++told;
+                    continue;
+                }
+                if (!more && look(bar(C::B_DONE), 0)) break;
                 const uint32_t now_at = progress[0] + progress[1];
                 const uint64_t now = global_timer_ns();
                 if (now_at != seen) {
@@ -954,9 +1013,9 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             const uint32_t ids = base + C::OFF_SID + lane * 4, sc0 = base + C::OFF_SC + lane * 4;
             uint32_t tiles = 0, piece = 0;
             bool ok = true;
-            while (ok && before(at, end)) {
-                const Unit x = unit_at<D>(a, at.lane, at.unit);
-                const int t0 = at.tile, nt = last_tile(x) - t0, hp = x.h * P;
+            Part x;
+            while (ok && part_at(piece, x)) {
+                const int t0 = x.t0, nt = x.t1 - t0, hp = x.h * P;
                 const int first = t0 * TILE + lane * 4;
                 const int32_t* table = a.table + (int64_t)x.b * a.width;
                 auto look = [&](int d) {
@@ -1015,11 +1074,8 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                     __syncwarp();
                     if (lane == 0) arrive_at(bar(C::B_SCFULL, sc));
                 }
-                if (nt > 0) {
-                    tiles += nt;
-                    ++piece;
-                }
-                at = after(a, at, x.units, end);
+                tiles += nt;
+                ++piece;
             }
             cp_async_wait<0>();
         }
