@@ -25,8 +25,8 @@
 // Work: the units are laid end to end and cut into equal parts, one per CTA. A unit that one CTA does whole is written at
 // once; the others leave parts (O, reference, sum) in the workspace, and chunk_attention_join adds them up in order.
 //
-// Roles, 16 warps: two softmax groups of four; four that convert values and prepare queries; TMA; MMA issue; scales; a
-// watchdog that bounds all waits.
+// Roles, 16 warps: two softmax groups of four; four that convert values and prepare queries; one that walks the run and
+// issues TMA; one of MMA issue for each buffer of S; one of scales, which also bounds all waits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -136,11 +136,11 @@ struct Cfg {
     static constexpr int B_QFREE = B_QFULL + 8 * QB;              // ... have been used
     static constexpr int B_QMAX = B_QFREE + 8;                // the four warps have their maxima
     static constexpr int B_PDFULL = B_QMAX + 8;               // [NPD] a part is told
-    static constexpr int B_PDEMPTY = B_PDFULL + 8 * NPD;      // [NPD] ... and read: by fourteen warps and, for its second way, MMA issue once more
+    static constexpr int B_PDEMPTY = B_PDFULL + 8 * NPD;      // [NPD] ... and read by the other fifteen warps
     static constexpr int B_DONE = B_PDEMPTY + 8 * NPD;                 // the block's last output is written
     static constexpr int B_DRAIN = B_DONE + 8;
-    static constexpr int OFF_MISC = (B_DRAIN + 8 + 15) / 16 * 16;     // tmem slot, abort flag, progress [2], start, end
-    static constexpr int SMEM = OFF_MISC + 16 + 32 + 1024;
+    static constexpr int OFF_MISC = (B_DRAIN + 16 + 15) / 16 * 16;    // tmem slot, abort flag, progress [3] and one more, start, end
+    static constexpr int SMEM = OFF_MISC + 32 + 32 + 1024;
     static constexpr int TMEM_O = 2 * TILE;                   // after S [2]
     static constexpr int SOFT_REGS = 184, CONV_REGS = 80, REST_REGS = 64;     // 2 x 184 + 80 + 64 = 4 x 128
     static_assert(OFF_B % 1024 == 0 && OFF_R % 128 == 0 && OFF_K % 1024 == 0 && BSLOT % 1024 == 0, "alignment");
@@ -387,8 +387,8 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
     auto bar_ptr = [&](int offset) { return reinterpret_cast<uint64_t*>(smem + offset); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-    volatile uint32_t* progress = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 8);      // tiles added; parts out
-    Pos* ends = reinterpret_cast<Pos*>(smem + C::OFF_MISC + 16);
+    volatile uint32_t* progress = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 8);      // items of the two buffers; parts out
+    Pos* ends = reinterpret_cast<Pos*>(smem + C::OFF_MISC + 32);
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const int G = a.group;
@@ -400,9 +400,9 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
         init(C::B_KFULL, NK, 1); init(C::B_KEMPTY, NK, 2); init(C::B_RFULL, NR, 1); init(C::B_REMPTY, NR, 4);
         init(C::B_BFULL, NB, 4); init(C::B_BEMPTY, NB, 2); init(C::B_SCFULL, NSC, 1); init(C::B_SCEMPTY, NSC, 12);
         init(C::B_SFULL, 2, 1); init(C::B_PFULL, 4, 4); init(C::B_OHALF, 2, 1); init(C::B_ODONE, 2, 1); init(C::B_QFULL, QB, 4); init(C::B_QFREE, 1, 2);
-        init(C::B_QMAX, 1, 4); init(C::B_PDFULL, C::NPD, 1); init(C::B_PDEMPTY, C::NPD, 16); init(C::B_DONE, 1, 8); init(C::B_DRAIN, 1, 1);
+        init(C::B_QMAX, 1, 4); init(C::B_PDFULL, C::NPD, 1); init(C::B_PDEMPTY, C::NPD, 15); init(C::B_DONE, 1, 8); init(C::B_DRAIN, 2, 1);
         *abort_flag = 0;
-        progress[0] = progress[1] = 0;
+        progress[0] = progress[1] = progress[2] = 0;
         fence_barrier_init();
         prefetch_tmap(&maps.k);
         prefetch_tmap(&maps.v);
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                         }
                     }
                     tc_fence_before();
-                    if (lane == 0 && wl == 0 && g == 0) progress[1] = piece + 1;
+                    if (lane == 0 && wl == 0 && g == 0) progress[2] = piece + 1;
                 }
                 items += nt * x.nt;
                 tiles += nt;
@@ -792,9 +792,19 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
         if (warp == 12) {
             // -------------------------------------------------------- TMA: lane l < 8 looks up the page of the tile's rows 16 l ..
             const int rk = P < TILE ? P : TILE, rv = P < C::VR ? P : C::VR;          // rows a copy
+            const Pos end = ends[1];
+            Pos at = ends[0];
+            int units = 0;
             bool ok = true;
-            Part x;
-            for (uint32_t n = 0; ok && part_at(n, x); ++n) {
+            for (uint32_t n = 0; ok; ++n) {
+                const Part x = next_part<D>(a, end, at, units);
+                if (!warp_wait_at(bar(C::B_PDEMPTY, n % C::NPD), ((n / C::NPD) & 1) ^ 1, stop)) break;
+                if (lane == 0) {
+                    *reinterpret_cast<Part*>(smem + C::OFF_PD + (n % C::NPD) * sizeof(Part)) = x;
+                    arrive_at(bar(C::B_PDFULL, n % C::NPD));
+                }
+                __syncwarp();
+                if (x.t1 == 0) break;
                 const int t0 = x.t0, t1 = x.t1, hp = x.h * P;
                 const int32_t* table = a.table + (int64_t)x.b * a.width;
                 auto look = [&](int t) {
@@ -837,8 +847,10 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                     }
                 }
             }
-        } else if (warp == 13) {
-            // -------------------------------------------------------- MMA issue: whatever is ready, outputs first
+        } else if (warp < 15) {
+            // -------------------------------------------------------- MMA issue: a warp for each buffer of S. Scores of an item (tile,
+            // row tile), both halves of its output, scores of the item after the next. (One warp for both has more to decide a
+            // step than the step's products take.)
             constexpr uint64_t KD = desc_base(C::ROWB == 128 ? 2 : 4, 8 * C::ROWB, 8 * C::ROWB);
             constexpr uint64_t VD = desc_base(2, C::VPANEL, 1024);
             constexpr uint32_t ID_S = idesc_f8(TILE, TILE, 0, 0, 0), ID_PV = idesc_bf16(TILE, D);
@@ -851,160 +863,72 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                 asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"((uint32_t)(kind >> 32)));
                 return d;
             };
-            // Items (tile, row tile) go in turn to the two buffers of S. Each buffer has its own way through them: scores of an
-            // item, both halves of its output, scores of the item after the next. Whatever is ready is issued.
-            struct Way {
-                int b, nt, left, r;              // buffer; row tiles; tiles of the part still to be done; row tile
-                uint32_t item, tile, piece;      // of the CTA: items, tiles, parts
-                int stage;                       // 0 scores, 1 and 2 halves of the output, 3 the end
-                bool fresh;                      // a part's first tile
-            };
-            auto enter = [&](Way& w) {
-                w.fresh = true;
-                w.r = 0;
-                Part x;
-                if (part_at(w.piece, x)) {
-                    w.nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0);
-                    w.left = __shfl_sync(0xFFFFFFFFu, x.t1 - x.t0, 0);
-                } else {
-                    w.stage = 3;
-                }
-            };
-            auto next_item = [&](Way& w) {
-                if (w.stage == 3) return;
-                ++w.item;
-                if (++w.r < w.nt) return;
-                w.r = 0;
-                ++w.tile;
-                w.fresh = false;
-                if (--w.left > 0) return;
-                ++w.piece;
-                enter(w);
-            };
-            Way now{0, 1, 0, 0, 0u, 0u, 0u, 0, true}, other{1, 1, 0, 0, 0u, 0u, 0u, 0, true};
-            enter(now);
-            enter(other);
-            next_item(other);
-            // What the next step of buffer b waits for is tested by lanes 8 b ..: all at once.
-            constexpr int PH = C::PIECES / 2;                        // pieces of values of half a tile
-            uint32_t my_bar = 0, my_parity = 0;
-            const int my_b = (lane >> 3) & 1, my_k = lane & 7;
-            auto aim = [&]() {
-                const Way& w = my_b == now.b ? now : other;
-                if (w.stage == 0) {
-                    my_bar = my_k == 0 ? bar(C::B_KFULL, w.tile % NK) : bar(C::B_QFULL, w.piece % QB);
-                    my_parity = my_k == 0 ? w.tile / NK : w.piece / QB;
-                } else {
-                    const uint32_t bi = w.tile * C::PIECES + (w.stage - 1) * PH + (my_k > 1 ? PH - 1 : 0);
-                    my_bar = my_k == 0 ? bar(C::B_PFULL, 2 * my_b + w.stage - 1) : bar(C::B_BFULL, bi % NB);
-                    my_parity = my_k == 0 ? w.item >> 1 : bi / NB;
-                }
-                my_parity &= 1;
-            };
-            aim();
-            uint32_t done = 0;
-            while (now.stage < 3 || other.stage < 3) {
-                const uint32_t there = __ballot_sync(0xFFFFFFFFu, test_at(my_bar, my_parity));
-                bool moved = false;
-#pragma unroll 1
-                for (int turn = 0; turn < 2; ++turn) {
-                    const Way swap = now;
-                    now = other;
-                    other = swap;
-                    Way& w = now;
-                    const int b = w.b;
-                    if (((there >> (8 * b)) & 255u) != 255u || w.stage == 3) continue;
-                    if (w.stage == 0) {
-                        // (this buffer's last P has been used by an output issued before)
-                        tc_fence_after();
-                        const uint32_t s = w.tile % NK, d = __shfl_sync(0xFFFFFFFFu, tm + b * TILE, 0);
-                        const uint32_t k = lower(KD, base + C::OFF_K + s * C::KSLOT), q = lower(KD, base + C::OFF_Q + w.r * C::QTILE);
-                        if (elect_one()) {
+            constexpr int PH = C::PIECES / 2;        // pieces of values of half a tile
+            const int b = warp - 13;
+            uint32_t item = 0, tile = 0, piece = 0;  // of the CTA: the first item of the part, its first tile, part
+            uint32_t mine = b;                       // this buffer's next item
+            bool ok = true;
+            Part x;
+            for (; ok && part_at(piece, x); ++piece) {
+                const int nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0), tiles = __shfl_sync(0xFFFFFFFFu, x.t1 - x.t0, 0);
+                const uint32_t last = item + tiles * nt;
+                for (; mine < last; mine += 2) {
+                    const int i = nt == 2 ? (int)(mine - item) >> 1 : (int)(mine - item), r = nt == 2 ? (int)(mine - item) & 1 : 0;
+                    const uint32_t t = tile + i, ks = t % NK;
+                    // (the buffer's last P has been used by an output that this warp has issued before)
+                    const uint32_t d = __shfl_sync(0xFFFFFFFFu, tm + b * TILE, 0);
+                    const uint32_t k = lower(KD, base + C::OFF_K + ks * C::KSLOT), q = lower(KD, base + C::OFF_Q + r * C::QTILE);
+                    // Q is free when all scores of the part are made, of both buffers
+                    const int frees = nt == 2 ? i == tiles - 1 : (i == tiles - 1) + (i == tiles - 2 || tiles == 1);
+                    if (!warp_wait_at(bar(C::B_QFULL, piece % QB), (piece / QB) & 1, stop) ||
+                        !warp_wait_at(bar(C::B_KFULL, ks), (t / NK) & 1, stop)) { ok = false; break; }
+                    tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < 2 * D / 32; ++kk) {
-                                constexpr int STEPS = C::ROWB / 32, HALF = D / 32;
-                                const int kq = kk % HALF;
-                                tc_mma_f8(d, desc(KD, q + (((kq / STEPS) * C::QPANEL + (kk / HALF) * TILE * C::ROWB + (kq % STEPS) * 32) >> 4)),
-                                          desc(KD, k + (((kq / STEPS) * C::KPANEL + (kq % STEPS) * 32) >> 4)), ID_S, kk ? 1u : 0u);
-                            }
-                            commit_at(bar(C::B_SFULL, b));
-                            for (int z = w.nt; z < 3; ++z) {         // one row tile arrives for two
-                                commit_at(bar(C::B_KEMPTY, s));
-                                if (w.left == 1) commit_at(bar(C::B_QFREE));
-                            }
+                        for (int kk = 0; kk < 2 * D / 32; ++kk) {
+                            constexpr int STEPS = C::ROWB / 32, HALF = D / 32;
+                            const int kq = kk % HALF;
+                            tc_mma_f8(d, desc(KD, q + (((kq / STEPS) * C::QPANEL + (kk / HALF) * TILE * C::ROWB + (kq % STEPS) * 32) >> 4)),
+                                      desc(KD, k + (((kq / STEPS) * C::KPANEL + (kq % STEPS) * 32) >> 4)), ID_S, kk ? 1u : 0u);
                         }
-                        __syncwarp();
-                        w.stage = 1;
-                    } else {
-                        const int h = w.stage - 1;
-                        // one row tile's outputs go in order: the first of them clears O
-                        if (w.nt == 1 && other.stage < 3 && other.item < w.item) continue;
-                        tc_fence_after();
-                        const uint32_t bi = w.tile * C::PIECES + h * PH;
-                        const uint32_t o = __shfl_sync(0xFFFFFFFFu, tm + C::TMEM_O + w.r * D, 0), p = __shfl_sync(0xFFFFFFFFu, tm + b * TILE + h * 32, 0);
-                        const uint32_t add = __shfl_sync(0xFFFFFFFFu, w.fresh && h == 0 ? 0u : 1u, 0);
+                        commit_at(bar(C::B_SFULL, b));
+                        for (int z = nt; z < 3; ++z) commit_at(bar(C::B_KEMPTY, ks));        // one row tile arrives for two
+                        for (int z = 0; z < frees; ++z) commit_at(bar(C::B_QFREE));
+                    }
+                    __syncwarp();
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t bi = t * C::PIECES + h * PH;
+                        const uint32_t o = __shfl_sync(0xFFFFFFFFu, tm + C::TMEM_O + r * D, 0), p = __shfl_sync(0xFFFFFFFFu, tm + b * TILE + h * 32, 0);
+                        const uint32_t add = __shfl_sync(0xFFFFFFFFu, i == 0 && h == 0 ? 0u : 1u, 0);
                         uint32_t v[PH];
 #pragma unroll
                         for (int pc = 0; pc < PH; ++pc) v[pc] = lower(VD, base + C::OFF_B + (bi + pc) % NB * C::BSLOT);
+                        if (!warp_wait_at(bar(C::B_PFULL, 2 * b + h), (mine >> 1) & 1, stop)) { ok = false; break; }
+                        // Outputs of one row tile add up in order: the other buffer's last is complete. (Its values then have arrived,
+                        // without which the parity of the next ones' barriers would say nothing.)
+                        if (nt == 1 && h == 0 && mine > 0 && !warp_wait_at(bar(C::B_ODONE, 1 - b), ((mine - 1) >> 1) & 1, stop)) { ok = false; break; }
+#pragma unroll
+                        for (int pc = 0; pc < PH; ++pc) ok = ok && warp_wait_at(bar(C::B_BFULL, (bi + pc) % NB), ((bi + pc) / NB) & 1, stop);
+                        if (!ok) break;
+                        tc_fence_after();
                         if (elect_one()) {
 #pragma unroll
                             for (int pc = 0; pc < PH; ++pc) {
 #pragma unroll
                                 for (int kk = 0; kk < C::VR / 16; ++kk)
                                     tc_mma_f16_ts(o, p + pc * (C::VR / 2) + kk * 8, desc(VD, v[pc] + kk * (2048 >> 4)), ID_PV, pc == 0 && kk == 0 ? add : 1u);
-                                for (int z = w.nt; z < 3; ++z) commit_at(bar(C::B_BEMPTY, (bi + pc) % NB));
+                                for (int z = nt; z < 3; ++z) commit_at(bar(C::B_BEMPTY, (bi + pc) % NB));
                             }
                             commit_at(bar(h ? C::B_ODONE : C::B_OHALF, b));
                         }
                         __syncwarp();
-                        progress[0] = ++done;
-                        if (h == 0) {
-                            w.stage = 2;
-                        } else {
-                            w.stage = 0;
-                            next_item(w);
-                            next_item(w);
-                        }
                     }
-                    moved = true;
+                    if (!ok) break;
+                    progress[b] = mine;
                 }
-                if (moved) aim();
-                else if (__any_sync(0xFFFFFFFFu, stopped(stop))) break;
-            }
-        } else if (warp == 15) {
-            // -------------------------------------------------------- tells the parts, and stops the block when nothing has
-            // moved for the bound
-            const Pos end = ends[1];
-            Pos at = ends[0];
-            int units = 0;
-            uint32_t told = 0, seen = 0;
-            bool more = true;
-            uint64_t since = global_timer_ns();
-            const bool nap = a.wait_ns >= 40000ull;  // (asleep for some 20 us, whatever less is asked for)
-            auto look = [&](uint32_t b, uint32_t parity) { return __all_sync(0xFFFFFFFFu, nap ? try_at_for(b, parity, 20000) : test_at(b, parity)) != 0; };
-            while (!__any_sync(0xFFFFFFFFu, stopped(stop))) {
-                const uint32_t slot = told % C::NPD;
-                if (more && look(bar(C::B_PDEMPTY, slot), ((told / C::NPD) & 1) ^ 1)) {
-                    const Part p = next_part<D>(a, end, at, units);
-                    if (lane == 0) {
-                        *reinterpret_cast<Part*>(smem + C::OFF_PD + slot * sizeof(Part)) = p;
-                        arrive_at(bar(C::B_PDFULL, slot));
-                    }
-                    __syncwarp();
-                    more = p.t1 > 0;
-                    ++told;
-                    continue;
-                }
-                if (!more && look(bar(C::B_DONE), 0)) break;
-                const uint32_t now_at = progress[0] + progress[1];
-                const uint64_t now = global_timer_ns();
-                if (now_at != seen) {
-                    seen = now_at;
-                    since = now;
-                } else if (now - since >= a.wait_ns) {
-                    stop_all(stop);
-                    break;
-                }
+                item = last;
+                tile += tiles;
             }
         } else {
             // -------------------------------------------------------- scales: a lane takes four rows; scales are under way SA tiles
@@ -1012,9 +936,29 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             constexpr int A = C::SA;
             const uint32_t ids = base + C::OFF_SID + lane * 4, sc0 = base + C::OFF_SC + lane * 4;
             uint32_t tiles = 0, piece = 0;
+            // This warp's waits bound those of all: where the pipeline stands, it waits, and stops the block when nothing has moved for
+            // the bound.
+            uint32_t seen = 0;
+            uint64_t since = global_timer_ns();
+            const bool nap = a.wait_ns >= 40000ull;  // (asleep for some 20 us, whatever less is asked for)
+            auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+                while (!__all_sync(0xFFFFFFFFu, nap ? try_at_for(b, parity, 20000) : test_at(b, parity))) {
+                    if (__any_sync(0xFFFFFFFFu, stopped(stop))) return false;
+                    const uint32_t now_at = progress[0] + progress[1] + progress[2];
+                    const uint64_t now = global_timer_ns();
+                    if (now_at != seen) {
+                        seen = now_at;
+                        since = now;
+                    } else if (__any_sync(0xFFFFFFFFu, now - since >= a.wait_ns)) {
+                        stop_all(stop);
+                        return false;
+                    }
+                }
+                return true;
+            };
             bool ok = true;
             Part x;
-            while (ok && part_at(piece, x)) {
+            while (ok && wait(bar(C::B_PDFULL, piece % C::NPD), (piece / C::NPD) & 1) && part_at(piece, x)) {
                 const int t0 = x.t0, nt = x.t1 - t0, hp = x.h * P;
                 const int first = t0 * TILE + lane * 4;
                 const int32_t* table = a.table + (int64_t)x.b * a.width;
@@ -1025,7 +969,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                 auto load = [&](int d) {                     // its id has arrived
                     if (d >= nt) return true;
                     const uint32_t e = tiles + d, sc = e % NSC;
-                    if (!warp_wait_at(bar(C::B_SCEMPTY, sc), ((e / NSC) & 1) ^ 1, stop)) return false;
+                    if (!wait(bar(C::B_SCEMPTY, sc), ((e / NSC) & 1) ^ 1)) return false;
                     const int j = first + d * TILE;
                     const uint32_t dst = sc0 + sc * C::SC_BYTES;
                     if (j < x.end) {
@@ -1054,7 +998,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                     cp_async_commit();
                     if (d < 0) continue;
                     if (d == 0) {
-                        if (!warp_wait_at(bar(C::B_QFULL, piece % QB), (piece / QB) & 1, stop)) { ok = false; break; }
+                        if (!wait(bar(C::B_QFULL, piece % QB), (piece / QB) & 1)) { ok = false; break; }
                         unit = *reinterpret_cast<const float*>(smem + C::OFF_QU + (piece % QB) * 8) * a.scale_log2;
                     }
                     const uint32_t sc = (tiles + d) % NSC, dst = sc0 + sc * C::SC_BYTES;
@@ -1078,6 +1022,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                 ++piece;
             }
             cp_async_wait<0>();
+            if (ok) (void)wait(bar(C::B_DONE), 0);
         }
     }
     tc_fence_before();
@@ -1087,7 +1032,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             drain_stage_fills(bar_ptr(C::B_KFULL), NK, issued_k);
             drain_stage_fills(bar_ptr(C::B_RFULL), NR, issued_r);
         }
-        if (warp == 13 && elect_one()) tc_drain(bar_ptr(C::B_DRAIN));
+        if ((warp == 13 || warp == 14) && elect_one()) tc_drain(bar_ptr(C::B_DRAIN) + (warp - 13));
         tc_fence_before();
         __syncthreads();
     }
