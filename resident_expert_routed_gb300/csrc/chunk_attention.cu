@@ -67,7 +67,7 @@ constexpr float NEVER = -1e30f;                  // the reference of a row that 
 constexpr float LIMIT = 8.0f;                    // log2 of the largest weight before the reference moves
 
 // The run's measure: a cache row of a unit with two row tiles, of one with one; a unit beside its rows.
-constexpr int FULL_COST = 4, HALF_COST = 3, UNIT_COST = 512;
+constexpr int FULL_COST = 4, HALF_COST = 3, UNIT_COST = 1024;
 constexpr int LEAST_PART = 2048;                 // of a part
 
 struct Pos {                                     // a place in the run
@@ -96,12 +96,12 @@ struct Cfg {
     static constexpr int PANELS = D / ROWB;
     static constexpr int KPANEL = TILE * ROWB, KSLOT = TILE * D;
     static constexpr int QPANEL = 2 * TILE * ROWB, QTILE = 2 * TILE * D;      // hi, then lo
-    static constexpr int NK = D == 64 ? 8 : D == 128 ? 3 : 2; // ring of key tiles
+    static constexpr int NK = D == 64 ? 8 : D == 128 ? 4 : 2; // ring of key tiles (even: see MMA issue)
     static constexpr int VR = D == 256 ? 32 : 64;             // values come in pieces of so many rows
     static constexpr int PIECES = TILE / VR;
     static constexpr int NR = D == 64 ? 8 : D == 128 ? 4 : 3; // ring of pieces as codes
     static constexpr int RSLOT = VR * D;
-    static constexpr int NB = D == 64 ? 8 : 4;                // ring of pieces in bf16
+    static constexpr int NB = D == 64 ? 8 : D == 128 ? 3 : 4;                // ring of pieces in bf16
     static constexpr int VPANEL = VR * 128, BSLOT = VR * D * 2;
     static constexpr int SA = 4, NSC = 2 * SA;                // tiles that scales are under way ahead; their ring:
     static constexpr int SC_BYTES = 3 * TILE * 2;             // key bytes, value bytes, the columns' factors (float)
@@ -137,7 +137,9 @@ struct Cfg {
     static constexpr int B_QMAX = B_QFREE + 8;                // the four warps have their maxima
     static constexpr int B_PDFULL = B_QMAX + 8;               // [NPD] a part is told
     static constexpr int B_PDEMPTY = B_PDFULL + 8 * NPD;      // [NPD] ... and read by the other fifteen warps
-    static constexpr int B_DONE = B_PDEMPTY + 8 * NPD;                 // the block's last output is written
+    static constexpr int B_MERGE = B_PDEMPTY + 8 * NPD;       // group 1's share of a unit with one row tile is laid down
+    static constexpr int B_MFREE = B_MERGE + 8;               // ... and read
+    static constexpr int B_DONE = B_MFREE + 8;                 // the block's last output is written
     static constexpr int B_DRAIN = B_DONE + 8;
     static constexpr int OFF_MISC = (B_DRAIN + 16 + 15) / 16 * 16;    // tmem slot, abort flag, progress [3] and one more, start, end
     static constexpr int SMEM = OFF_MISC + 32 + 32 + 1024;
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
         init(C::B_KFULL, NK, 1); init(C::B_KEMPTY, NK, 2); init(C::B_RFULL, NR, 1); init(C::B_REMPTY, NR, 4);
         init(C::B_BFULL, NB, 4); init(C::B_BEMPTY, NB, 2); init(C::B_SCFULL, NSC, 1); init(C::B_SCEMPTY, NSC, 12);
         init(C::B_SFULL, 2, 1); init(C::B_PFULL, 4, 4); init(C::B_OHALF, 2, 1); init(C::B_ODONE, 2, 1); init(C::B_QFULL, QB, 4); init(C::B_QFREE, 1, 2);
-        init(C::B_QMAX, 1, 4); init(C::B_PDFULL, C::NPD, 1); init(C::B_PDEMPTY, C::NPD, 15); init(C::B_DONE, 1, 8); init(C::B_DRAIN, 2, 1);
+        init(C::B_QMAX, 1, 4); init(C::B_PDFULL, C::NPD, 1); init(C::B_PDEMPTY, C::NPD, 15); init(C::B_MERGE, 1, 4); init(C::B_MFREE, 1, 4); init(C::B_DONE, 1, 8); init(C::B_DRAIN, 2, 1);
         *abort_flag = 0;
         progress[0] = progress[1] = progress[2] = 0;
         fence_barrier_init();
@@ -433,6 +435,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
         const int g = warp >> 2, wl = warp & 3, j = tid & 127;
         const uint32_t trow = tmem + ((uint32_t)(wl * 32) << 16);
         uint32_t items = 0, tiles = 0, piece = 0;    // of the CTA: items (tile, row tile), tiles, parts
+        uint32_t merges = 0;                         // units whose O the groups have added up
         bool ok = true;
         Part x;
         while (ok && part_at(piece, x)) {
@@ -440,20 +443,26 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             {
                 // (a group that has no rows here waits too: it may not run ahead of barriers whose phases it does not see)
                 if (!warp_wait_at(bar(C::B_QFULL, piece % QB), (piece / QB) & 1, stop)) break;
-                if (g < x.nt) {
+                // Two row tiles: one a group. One: the groups take its tiles in turn, each with an O of its own, which are added up
+                // at the end (at head_dim 256 there is room for one O: group 0 takes them all).
+                const bool split = C::NT == 2 && x.nt == 1;
+                if (split || g < x.nt) {
                     const uint32_t o_at = trow + C::TMEM_O + g * (C::NT == 2 ? D : 0);
-                    const int row = g * TILE + j;
+                    const int tile_row = split ? 0 : g * TILE, row = tile_row + j;
                     const int u = row < x.rows ? row : x.rows - 1;
                     const int t = (int)((uint32_t)u * a.by_group >> 16);
                     const int limit = x.first + t;                   // the last cache row that this row sees
-                    const int open = x.first + (int)((uint32_t)(g * TILE) * a.by_group >> 16);       // that every row of the tile sees
+                    const int open = x.first + (int)((uint32_t)tile_row * a.by_group >> 16);         // that every row of the tile sees
                     const float2 unit = *reinterpret_cast<const float2*>(smem + C::OFF_QU + (piece % QB) * 8);
                     const bool rowwise = unit.y != 0.0f;
                     const float rf = rowwise ? *reinterpret_cast<const float*>(smem + C::OFF_QF + ((piece % QB) * ROWS + row) * 4) : 1.0f;
                     const f32x2 rf2 = pack2(rf, rf);
                     float m = NEVER, l = 0.0f;
-                    for (int i = 0; i < nt; ++i) {
-                        const uint32_t item = items + i * x.nt + g, buf = item & 1, sc = (tiles + i) % NSC;
+                    bool fresh = true;               // nothing has been added to O
+                    uint32_t item = 0;
+                    for (int i = split ? (int)((items ^ (uint32_t)g) & 1) : 0; i < nt; i += split ? 2 : 1) {
+                        item = split ? items + i : items + i * x.nt + g;
+                        const uint32_t buf = item & 1, sc = (tiles + i) % NSC;
                         const uint32_t s_at = trow + buf * TILE;
                         const int j0 = (t0 + i) * TILE;
                         const bool masked = j0 + TILE - 1 > open;
@@ -469,7 +478,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                             const uint32_t sh = s_at + h * 64;
                             const uint4* kh = kf + 16 * h;
                             uint32_t P[32];
-                            bool move = i == 0 && h == 0;
+                            bool move = fresh;
                             for (bool moved = false;; moved = true) {
                                 if (move) {
                                     // the reference moves to the largest score so far, and what has been added up with it
@@ -493,8 +502,8 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                                     const float alpha = ex2(m - mn);
                                     l *= alpha;
                                     m = mn;
-                                    if (i > 0 || h > 0) {
-                                        const uint32_t before_it = item - x.nt;
+                                    if (!fresh) {
+                                        const uint32_t before_it = item - C::NT;
                                         if (h > 0 ? !warp_wait_at(bar(C::B_OHALF, buf), (item >> 1) & 1, stop)
                                                   : !warp_wait_at(bar(C::B_ODONE, before_it & 1), (before_it >> 1) & 1, stop)) { ok = false; break; }
                                         tc_fence_after();
@@ -561,45 +570,85 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) arrive_at(bar(C::B_PFULL, 2 * buf + h));
+                            fresh = false;
                         }
                         if (!ok) break;
                         if (lane == 0) arrive_at_n(bar(C::B_SCEMPTY, sc), x.nt == 2 ? 1 : 2);
                     }
                     if (!ok) break;
                     // ---- the part's output
-                    const uint32_t ended = items + (nt - 1) * x.nt + g;
-                    if (!warp_wait_at(bar(C::B_ODONE, ended & 1), (ended >> 1) & 1, stop)) break;
+                    if (!fresh && !warp_wait_at(bar(C::B_ODONE, item & 1), (item >> 1) & 1, stop)) break;
                     tc_fence_after();
-                    const bool live = row < x.rows;
-                    if (t0 == 0 && t1 == x.tiles) {
+                    const bool live = row < x.rows, whole = t0 == 0 && t1 == x.tiles;
+                    // where this thread's row lies in a part, in the workspace
+                    float* part = reinterpret_cast<float*>(a.ws + parts_offset(gridDim.x)) + (size_t)(2 * blockIdx.x + (t0 > 0 ? 0 : 1)) * C::PART_FLOATS;
+                    const int at = split ? g * TILE + j : row;
+                    if (whole && (!split || g == 0)) {
+                        float f0 = 1.0f, f1 = 0.0f;
+                        if (split) {
+                            if (!warp_wait_at(bar(C::B_MERGE), merges & 1, stop)) break;
+                            const float m1 = part[ROWS * D + TILE + j], l1 = part[ROWS * D + ROWS + TILE + j];
+                            const float mn = fmaxf(m, m1);
+                            f0 = ex2(m - mn);
+                            f1 = m1 == NEVER && l1 == 0.0f ? 0.0f : ex2(m1 - mn);
+                            l = l * f0 + l1 * f1;
+                            m = mn;
+                        }
                         const int64_t to = (int64_t)(x.tok0 + t) * a.n_q + x.h * G + u - t * G;
                         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                         if (a.lse && live) a.lse[to] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                        f0 *= inv;
+                        f1 *= inv;
                         uint4* dst = reinterpret_cast<uint4*>(a.out + to * D);
+                        if (!split || __any_sync(0xFFFFFFFFu, live))
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t o[32];
-                            tc_load(o_at + c * 32, o);
-                            uint32_t v[16];
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t o[16];
+                                tc_load(o_at + c * 16, o);
+                                float v[16];
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-                            if (live)
+                                for (int e = 0; e < 16; ++e) v[e] = fresh ? 0.0f : __uint_as_float(o[e]) * f0;
+                                if (split && f1 != 0.0f) {
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) dst[c * 4 + e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                                    for (int e = 0; e < 4; ++e) {
+                                        const float4 w = *reinterpret_cast<const float4*>(part + ((size_t)(c * 4 + e) * ROWS + TILE + j) * 4);
+                                        v[4 * e] += w.x * f1;
+                                        v[4 * e + 1] += w.y * f1;
+                                        v[4 * e + 2] += w.z * f1;
+                                        v[4 * e + 3] += w.w * f1;
+                                    }
+                                }
+                                if (live) {
+                                    dst[c * 2] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+                                    dst[c * 2 + 1] = make_uint4(pack_bf16(v[8], v[9]), pack_bf16(v[10], v[11]), pack_bf16(v[12], v[13]), pack_bf16(v[14], v[15]));
+                                }
+                            }
+                        if (split) {
+                            __syncwarp();
+                            if (lane == 0) arrive_at(bar(C::B_MFREE));
                         }
                     } else {
-                        float* part = reinterpret_cast<float*>(a.ws + parts_offset(gridDim.x)) + (size_t)(2 * blockIdx.x + (t0 > 0 ? 0 : 1)) * C::PART_FLOATS;
-                        part[ROWS * D + row] = m;
-                        part[ROWS * D + ROWS + row] = l;
+                        if (whole && merges > 0 && !warp_wait_at(bar(C::B_MFREE), (merges - 1) & 1, stop)) break;
+                        if (live) {
+                            part[ROWS * D + at] = m;
+                            part[ROWS * D + ROWS + at] = l;
+                        }
+                        if (!fresh && (!split || __any_sync(0xFFFFFFFFu, live)))
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t o[32];
-                            tc_load(o_at + c * 32, o);
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tc_load(o_at + c * 32, o);
+                                if (live)
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                *reinterpret_cast<uint4*>(part + ((size_t)(c * 8 + e) * ROWS + row) * 4) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                                    for (int e = 0; e < 8; ++e)
+                                        *reinterpret_cast<uint4*>(part + ((size_t)(c * 8 + e) * ROWS + at) * 4) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                            }
+                        if (whole) {
+                            __syncwarp();
+                            if (lane == 0) arrive_at(bar(C::B_MERGE));
                         }
                     }
+                    if (whole && split) ++merges;
                     tc_fence_before();
                     if (lane == 0 && wl == 0 && g == 0) progress[2] = piece + 1;
                 }
@@ -615,44 +664,38 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
         // ------------------------------------------------------------ queries in two parts; values in bf16
         regs_down<C::CONV_REGS>();
         const int wl = warp & 3, ct = tid & 127;
-        // A unit's queries: their largest size first, then the parts.
-        auto prepare = [&](const Part& x, uint32_t piece) -> bool {
-            constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = 4 * RPW;        // lanes a row, rows a warp takes at once, all four
-            constexpr int BATCH = 4;
-            const int part = lane % LPR, mine = wl * RPW + lane / LPR;
-            const int rounds = x.nt * TILE / STEP;
-            const __nv_bfloat16* q = a.q + (int64_t)x.tok0 * a.q_token + (int64_t)x.h * G * a.q_head + part * 8;
-            auto load = [&](int u) {                 // (rows past the unit's last are its last again, and their results nobody's)
-                u = min(u, x.rows - 1);
-                const int t = (int)((uint32_t)u * a.by_group >> 16);
-                return *reinterpret_cast<const uint4*>(q + t * a.q_token + (u - t * G) * a.q_head);
-            };
-            float* qf = reinterpret_cast<float*>(smem + C::OFF_QF) + (piece % QB) * ROWS;
-            uint32_t* keys = reinterpret_cast<uint32_t*>(qf);
-            if (piece > 0 && !warp_wait_at(bar(C::B_QFREE), (piece - 1) & 1, stop)) return false;
-            uint32_t most = 0, least = 0x7FFFu;
-#pragma unroll 1
-            for (int r0 = 0; r0 < rounds; r0 += BATCH) {
-                uint4 raw[BATCH];
+        // A unit's queries go through twice: for the largest size of each row (while the part before is at work, a few rows
+        // with each piece of its values), then for the parts.
+        constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = 4 * RPW;            // lanes a row, rows a warp takes at once, all four
+        constexpr int BATCH = 4;                                              // loads under way
+        const int part = lane % LPR, mine = wl * RPW + lane / LPR;
+        auto load = [&](const Part& x, int u) {      // (rows past the unit's last are its last again, and their results nobody's)
+            u = min(u, x.rows - 1);
+            const int t = (int)((uint32_t)u * a.by_group >> 16);
+            return *reinterpret_cast<const uint4*>(a.q + (int64_t)(x.tok0 + t) * a.q_token + (int64_t)(x.h * G + u - t * G) * a.q_head + part * 8);
+        };
+        auto row_factors = [&](uint32_t n) { return reinterpret_cast<float*>(smem + C::OFF_QF) + (n % QB) * ROWS; };
+        uint32_t most = 0, least = 0x7FFFu;          // sizes of the next part's rows, as bf16 bits
+        auto sizes = [&](const uint4 (&raw)[BATCH], uint32_t n, int r0) {
+            uint32_t* keys = reinterpret_cast<uint32_t*>(row_factors(n));
 #pragma unroll
-                for (int b = 0; b < BATCH; ++b) raw[b] = load((r0 + b) * STEP + mine);
+            for (int b = 0; b < BATCH; ++b) {
+                auto abs2 = [](uint32_t v) {
+                    v &= 0x7FFF7FFFu;
+                    return *reinterpret_cast<const __nv_bfloat162*>(&v);
+                };
+                __nv_bfloat162 v = __hmax2_nan(__hmax2_nan(abs2(raw[b].x), abs2(raw[b].y)), __hmax2_nan(abs2(raw[b].z), abs2(raw[b].w)));
+                v = __hmax2_nan(v, __lowhigh2highlow(v));
 #pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                    auto abs2 = [](uint32_t v) {
-                        v &= 0x7FFF7FFFu;
-                        return *reinterpret_cast<const __nv_bfloat162*>(&v);
-                    };
-                    __nv_bfloat162 v = __hmax2_nan(__hmax2_nan(abs2(raw[b].x), abs2(raw[b].y)), __hmax2_nan(abs2(raw[b].z), abs2(raw[b].w)));
-                    v = __hmax2_nan(v, __lowhigh2highlow(v));
-#pragma unroll
-                    for (int o = LPR / 2; o > 0; o >>= 1) v = __hmax2_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-                    const uint32_t key = *reinterpret_cast<const uint32_t*>(&v) & 0xFFFFu;
-                    if (part == 0) keys[(r0 + b) * STEP + mine] = key;
-                    most = max(most, key);
-                    if (key) least = min(least, key);
-                }
+                for (int o = LPR / 2; o > 0; o >>= 1) v = __hmax2_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+                const uint32_t key = *reinterpret_cast<const uint32_t*>(&v) & 0xFFFFu;
+                if (part == 0) keys[(r0 + b) * STEP + mine] = key;
+                most = max(most, key);
+                if (key) least = min(least, key);
             }
-            uint32_t* qx = reinterpret_cast<uint32_t*>(smem + C::OFF_QX) + (piece & 1) * 8;
+        };
+        auto prepare = [&](const Part& x, uint32_t n) -> bool {
+            uint32_t* qx = reinterpret_cast<uint32_t*>(smem + C::OFF_QX) + (n & 1) * 8;
             most = __reduce_max_sync(0xFFFFFFFFu, most);
             least = __reduce_min_sync(0xFFFFFFFFu, least);
             if (lane == 0) {
@@ -660,7 +703,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                 qx[4 + wl] = least;
                 arrive_at(bar(C::B_QMAX));
             }
-            if (!warp_wait_at(bar(C::B_QMAX), piece & 1, stop)) return false;
+            if (!warp_wait_at(bar(C::B_QMAX), n & 1, stop)) return false;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 most = max(most, qx[w]);
@@ -674,14 +717,26 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             };
             const int unit_up = up_of(most);
             const bool rowwise = most >= 0x7F80u || (least < most && up_of(least) - unit_up > 4);
+            most = 0;
+            least = 0x7FFFu;
+            float* qf = row_factors(n);
+            const uint32_t* keys = reinterpret_cast<const uint32_t*>(qf);
             if (wl == 0 && lane == 0)
-                *reinterpret_cast<float2*>(smem + C::OFF_QU + (piece % QB) * 8) = make_float2(rowwise ? 1.0f : exp2_int(-unit_up), rowwise ? 1.0f : 0.0f);
+                *reinterpret_cast<float2*>(smem + C::OFF_QU + (n % QB) * 8) = make_float2(rowwise ? 1.0f : exp2_int(-unit_up), rowwise ? 1.0f : 0.0f);
+            const int rounds = x.nt * TILE / STEP;
             const int panel = part * 8 / C::ROWB, chunk = part * 8 % C::ROWB / 16;
+            uint4 next[BATCH];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) next[b] = load(x, b * STEP + mine);
+            if (n > 0 && !warp_wait_at(bar(C::B_QFREE), (n - 1) & 1, stop)) return false;
 #pragma unroll 1
             for (int r0 = 0; r0 < rounds; r0 += BATCH) {
                 uint4 raw[BATCH];
 #pragma unroll
-                for (int b = 0; b < BATCH; ++b) raw[b] = load((r0 + b) * STEP + mine);
+                for (int b = 0; b < BATCH; ++b) {
+                    raw[b] = next[b];
+                    next[b] = load(x, (r0 + BATCH + b) * STEP + mine);
+                }
 #pragma unroll
                 for (int b = 0; b < BATCH; ++b) {
                     const int u = (r0 + b) * STEP + mine;
@@ -711,75 +766,84 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) arrive_at(bar(C::B_QFULL, piece % QB));
+            if (lane == 0) arrive_at(bar(C::B_QFULL, n % QB));
             return true;
         };
-        uint32_t tiles = 0, pieces = 0, piece = 0;
-        bool ok = true;
-        Part x;
-        while (ok && part_at(piece, x)) {
-            const int t0 = x.t0, t1 = x.t1;
-            {
-                if (!prepare(x, piece)) break;
-                ++piece;
-                for (int t = t0; t < t1 && ok; ++t, ++tiles) {
-                    const uint32_t sc = tiles % NSC;
-                    if (!warp_wait_at(bar(C::B_SCFULL, sc), (tiles / NSC) & 1, stop)) { ok = false; break; }
-                    const uint8_t* bytes = smem + C::OFF_SC + sc * C::SC_BYTES + TILE;
-#pragma unroll 1
-                    for (int pc = 0; pc < C::PIECES; ++pc, ++pieces) {
-                        const uint32_t rs = pieces % NR, bs = pieces % NB;
-                        if (!warp_wait_at(bar(C::B_RFULL, rs), (pieces / NR) & 1, stop)) { ok = false; break; }
-                        if (!warp_wait_at(bar(C::B_BEMPTY, bs), ((pieces / NB) & 1) ^ 1, stop)) { ok = false; break; }
-                        constexpr int EACH = C::VR * D / 16 / 128;       // 16 codes at once, of a thread
-                        const int left = x.end - t * TILE - pc * C::VR;      // rows that somebody sees; what lies behind is anything
+        // One piece of values (the part's i-th): codes to bf16.
+        uint32_t pieces = 0;
+        auto convert = [&](const Part& x, int i) -> bool {
+            const int pc = i % C::PIECES, t = x.t0 + i / C::PIECES;
+            const uint32_t tile = pieces / C::PIECES, sc = tile % NSC, rs = pieces % NR, bs = pieces % NB;
+            if (pc == 0 && !warp_wait_at(bar(C::B_SCFULL, sc), (tile / NSC) & 1, stop)) return false;
+            if (!warp_wait_at(bar(C::B_RFULL, rs), (pieces / NR) & 1, stop)) return false;
+            if (!warp_wait_at(bar(C::B_BEMPTY, bs), ((pieces / NB) & 1) ^ 1, stop)) return false;
+            const uint8_t* bytes = smem + C::OFF_SC + sc * C::SC_BYTES + TILE + pc * C::VR;
+            constexpr int EACH = C::VR * D / 16 / 128;                       // 16 codes at once, of a thread
+            const int left = x.end - t * TILE - pc * C::VR;                  // rows that somebody sees; what lies behind is anything
 #pragma unroll 2
-                        for (int e = 0; e < EACH; ++e) {
-                            // Eight neighbours take four places of a row in one panel of 64 columns and four of the next row in the
-                            // next panel: all on different banks, where they read and where they write.
-                            const int i = e * 128 + ct;
-                            int row = i >> 2, panel = 0;
-                            if constexpr (D > 64) {
-                                constexpr int HP = D / 128;
-                                const int rest = i >> 4, odd = (i >> 2) & 1;
-                                row = rest / HP * 2 + odd;
-                                panel = rest % HP * 2 + (((i >> 3) & 1) ^ odd);
-                            }
-                            const uint4 raw = *reinterpret_cast<const uint4*>(smem + C::OFF_R + rs * C::RSLOT + row * D + panel * 64 + (i & 3) * 16);
-                            const uint32_t s = bytes[pc * C::VR + row];
-                            // e4m3's bits, moved to bf16's places, stand for the code times 2^-120
-                            uint32_t f = s <= 134u ? (s + 120u) << 7 : 0x7F00u;
-                            if (s == 0u || row >= left) f = 0u;
-                            f |= f << 16;
-                            const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-                            uint32_t v[8];
-#pragma unroll
-                            for (int w = 0; w < 4; ++w) {
-                                // the upper bytes (sign, upper exponent bits) and the lower ones (last exponent bit, mantissa) of four values
-                                const uint32_t hi = (in[w] & 0x80808080u) | ((in[w] >> 4) & 0x07070707u), lo = (in[w] & 0x0F0F0F0Fu) * 16u;
-                                v[2 * w] = mul_bf16x2(__byte_perm(lo, hi, 0x5140), f);
-                                v[2 * w + 1] = mul_bf16x2(__byte_perm(lo, hi, 0x7362), f);
-                            }
-                            if (s > 134u) {
-                                const uint32_t f2 = ((s - 7u) << 7) * 0x10001u;
-#pragma unroll
-                                for (int w = 0; w < 8; ++w) v[w] = mul_bf16x2(v[w], f2);
-                            }
-                            uint8_t* to = smem + C::OFF_B + bs * C::BSLOT + panel * C::VPANEL + row * 128;
-                            const int q0 = (i & 3) * 2;
-                            *reinterpret_cast<uint4*>(to + ((q0 ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-                            *reinterpret_cast<uint4*>(to + (((q0 + 1) ^ (row & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            arrive_at(bar(C::B_BFULL, bs));
-                            arrive_at(bar(C::B_REMPTY, rs));
-                        }
-                    }
-                    if (ok && lane == 0) arrive_at(bar(C::B_SCEMPTY, sc));
+            for (int e = 0; e < EACH; ++e) {
+                // Eight neighbours take four places of a row in one panel of 64 columns and four of the next row in the
+                // next panel: all on different banks, where they read and where they write.
+                const int i = e * 128 + ct;
+                int row = i >> 2, panel = 0;
+                if constexpr (D > 64) {
+                    constexpr int HP = D / 128;
+                    const int rest = i >> 4, odd = (i >> 2) & 1;
+                    row = rest / HP * 2 + odd;
+                    panel = rest % HP * 2 + (((i >> 3) & 1) ^ odd);
                 }
+                const uint4 raw = *reinterpret_cast<const uint4*>(smem + C::OFF_R + rs * C::RSLOT + row * D + panel * 64 + (i & 3) * 16);
+                const uint32_t s = bytes[row];
+                // e4m3's bits, moved to bf16's places, stand for the code times 2^-120
+                uint32_t f = s <= 134u ? (s + 120u) << 7 : 0x7F00u;
+                if (s == 0u || row >= left) f = 0u;
+                f |= f << 16;
+                const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+                uint32_t v[8];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    // the upper bytes (sign, upper exponent bits) and the lower ones (last exponent bit, mantissa) of four values
+                    const uint32_t hi = (in[w] & 0x80808080u) | ((in[w] >> 4) & 0x07070707u), lo = (in[w] & 0x0F0F0F0Fu) * 16u;
+                    v[2 * w] = mul_bf16x2(__byte_perm(lo, hi, 0x5140), f);
+                    v[2 * w + 1] = mul_bf16x2(__byte_perm(lo, hi, 0x7362), f);
+                }
+                if (s > 134u) {
+                    const uint32_t f2 = ((s - 7u) << 7) * 0x10001u;
+#pragma unroll
+                    for (int w = 0; w < 8; ++w) v[w] = mul_bf16x2(v[w], f2);
+                }
+                uint8_t* to = smem + C::OFF_B + bs * C::BSLOT + panel * C::VPANEL + row * 128;
+                const int q0 = (i & 3) * 2;
+                *reinterpret_cast<uint4*>(to + ((q0 ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<uint4*>(to + (((q0 + 1) ^ (row & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                arrive_at(bar(C::B_BFULL, bs));
+                arrive_at(bar(C::B_REMPTY, rs));
+                if (pc == C::PIECES - 1) arrive_at(bar(C::B_SCEMPTY, sc));
+            }
+            ++pieces;
+            return true;
+        };
+        Part x{}, nx;
+        bool ok = true, more = part_at(0, nx);
+        for (uint32_t n = 0; ok; ++n) {              // the values of part n - 1 (none), with them the next queries' sizes; then these
+            const int todo = (x.t1 - x.t0) * C::PIECES, batches = more ? nx.nt * TILE / STEP / BATCH : 0;
+#pragma unroll 1
+            for (int i = 0; i < todo || i < batches; ++i) {
+                uint4 raw[BATCH];
+                if (i < batches)
+#pragma unroll
+                    for (int b = 0; b < BATCH; ++b) raw[b] = load(nx, (i * BATCH + b) * STEP + mine);
+                if (i < todo && !convert(x, i)) { ok = false; break; }
+                if (i < batches) sizes(raw, n, i * BATCH);
+            }
+            if (!ok || !more) break;
+            x = nx;
+            if (!prepare(x, n)) break;
+            more = part_at(n + 1, nx);
         }
     } else {
         regs_down<C::REST_REGS>();
@@ -796,15 +860,22 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             Pos at = ends[0];
             int units = 0;
             bool ok = true;
-            for (uint32_t n = 0; ok; ++n) {
-                const Part x = next_part<D>(a, end, at, units);
-                if (!warp_wait_at(bar(C::B_PDEMPTY, n % C::NPD), ((n / C::NPD) & 1) ^ 1, stop)) break;
-                if (lane == 0) {
-                    *reinterpret_cast<Part*>(smem + C::OFF_PD + (n % C::NPD) * sizeof(Part)) = x;
-                    arrive_at(bar(C::B_PDFULL, n % C::NPD));
+            Part x{}, nx{};
+            for (uint32_t n = 0; ok; ++n) {          // tells part n, then copies part n - 1: the next queries are looked at early
+                if (n == 0 || x.t1 > 0) {
+                    nx = next_part<D>(a, end, at, units);
+                    if (!warp_wait_at(bar(C::B_PDEMPTY, n % C::NPD), ((n / C::NPD) & 1) ^ 1, stop)) break;
+                    if (lane == 0) {
+                        *reinterpret_cast<Part*>(smem + C::OFF_PD + (n % C::NPD) * sizeof(Part)) = nx;
+                        arrive_at(bar(C::B_PDFULL, n % C::NPD));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (x.t1 == 0) break;
+                if (n == 0) {
+                    x = nx;
+                    if (x.t1 == 0) break;
+                    continue;
+                }
                 const int t0 = x.t0, t1 = x.t1, hp = x.h * P;
                 const int32_t* table = a.table + (int64_t)x.b * a.width;
                 auto look = [&](int t) {
@@ -846,11 +917,14 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                         if (some) tma_load_at(base + C::OFF_R + s * C::RSLOT + lane * rv * D, &maps.v, bar(C::B_RFULL, s), 0, first);
                     }
                 }
+                x = nx;
+                if (x.t1 == 0) break;
             }
         } else if (warp < 15) {
             // -------------------------------------------------------- MMA issue: a warp for each buffer of S. Scores of an item (tile,
             // row tile), both halves of its output, scores of the item after the next. (One warp for both has more to decide a
-            // step than the step's products take.)
+            // step than the step's products take.) With one row tile a warp sees every second tile only: the ring of keys has an
+            // even number of slots, so that the slot's fill before, from whose parity the next one's differs, was its own too.
             constexpr uint64_t KD = desc_base(C::ROWB == 128 ? 2 : 4, 8 * C::ROWB, 8 * C::ROWB);
             constexpr uint64_t VD = desc_base(2, C::VPANEL, 1024);
             constexpr uint32_t ID_S = idesc_f8(TILE, TILE, 0, 0, 0), ID_PV = idesc_bf16(TILE, D);
@@ -899,15 +973,15 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t bi = t * C::PIECES + h * PH;
-                        const uint32_t o = __shfl_sync(0xFFFFFFFFu, tm + C::TMEM_O + r * D, 0), p = __shfl_sync(0xFFFFFFFFu, tm + b * TILE + h * 32, 0);
-                        const uint32_t add = __shfl_sync(0xFFFFFFFFu, i == 0 && h == 0 ? 0u : 1u, 0);
+                        const uint32_t o = __shfl_sync(0xFFFFFFFFu, tm + C::TMEM_O + (C::NT == 2 && nt == 1 ? b : r) * D, 0), p = __shfl_sync(0xFFFFFFFFu, tm + b * TILE + h * 32, 0);
+                        const uint32_t add = __shfl_sync(0xFFFFFFFFu, (C::NT == 2 ? mine - item < 2 : i == 0) && h == 0 ? 0u : 1u, 0);
                         uint32_t v[PH];
 #pragma unroll
                         for (int pc = 0; pc < PH; ++pc) v[pc] = lower(VD, base + C::OFF_B + (bi + pc) % NB * C::BSLOT);
                         if (!warp_wait_at(bar(C::B_PFULL, 2 * b + h), (mine >> 1) & 1, stop)) { ok = false; break; }
-                        // Outputs of one row tile add up in order: the other buffer's last is complete. (Its values then have arrived,
+                        // Outputs of one O add up in order: the other buffer's last is complete. (Its values then have arrived,
                         // without which the parity of the next ones' barriers would say nothing.)
-                        if (nt == 1 && h == 0 && mine > 0 && !warp_wait_at(bar(C::B_ODONE, 1 - b), ((mine - 1) >> 1) & 1, stop)) { ok = false; break; }
+                        if (C::NT == 1 && h == 0 && mine > 0 && !warp_wait_at(bar(C::B_ODONE, 1 - b), ((mine - 1) >> 1) & 1, stop)) { ok = false; break; }
 #pragma unroll
                         for (int pc = 0; pc < PH; ++pc) ok = ok && warp_wait_at(bar(C::B_BFULL, (bi + pc) % NB), ((bi + pc) / NB) & 1, stop);
                         if (!ok) break;
@@ -1077,17 +1151,22 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_attention_join(const __
             if (same_unit(next, here) && next.tile == here.tile) continue;           // a CTA without tiles
         }
         const float* part = parts + (size_t)(2 * c + (c == k - 1 ? 1 : 0)) * C::PART_FLOATS;
-        const float mc = part[ROWS * D + row], lc = part[ROWS * D + ROWS + row];
-        const float mn = fmaxf(m, mc), f0 = ex2(m - mn), f1 = ex2(mc - mn);
-        l = l * f0 + lc * f1;
-        m = mn;
+        // one row tile: what each of the two groups has added up
+        for (int z = 0; z < (C::NT == 2 && x.nt == 1 ? 2 : 1); ++z) {
+            const int at = row + z * TILE;
+            const float mc = part[ROWS * D + at], lc = part[ROWS * D + ROWS + at];
+            if (row >= x.rows || (mc == NEVER && lc == 0.0f)) continue;      // nothing seen: no O either
+            const float mn = fmaxf(m, mc), f0 = ex2(m - mn), f1 = ex2(mc - mn);
+            l = l * f0 + lc * f1;
+            m = mn;
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const float4 v = *reinterpret_cast<const float4*>(part + ((size_t)(warp + e * JOIN_WARPS) * ROWS + row) * 4);
-            acc[e].x = acc[e].x * f0 + v.x * f1;
-            acc[e].y = acc[e].y * f0 + v.y * f1;
-            acc[e].z = acc[e].z * f0 + v.z * f1;
-            acc[e].w = acc[e].w * f0 + v.w * f1;
+            for (int e = 0; e < N; ++e) {
+                const float4 v = *reinterpret_cast<const float4*>(part + ((size_t)(warp + e * JOIN_WARPS) * ROWS + at) * 4);
+                acc[e].x = acc[e].x * f0 + v.x * f1;
+                acc[e].y = acc[e].y * f0 + v.y * f1;
+                acc[e].z = acc[e].z * f0 + v.z * f1;
+                acc[e].w = acc[e].w * f0 + v.w * f1;
+            }
         }
     }
     if (row >= x.rows) return;
