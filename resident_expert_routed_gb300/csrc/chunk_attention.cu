@@ -471,9 +471,82 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                         if (!warp_wait_at(bar(C::B_SFULL, buf), (item >> 1) & 1, stop)) { ok = false; break; }
                         tc_fence_after();
                         const uint4* kf = reinterpret_cast<const uint4*>(smem + C::OFF_SC + sc * C::SC_BYTES + 2 * TILE);
-                        // half a tile at a time, so that its weights are at work while the other half's are made
+                        // Half a tile at a time, so that its weights are at work while the other half's are made.
+                        auto publish = [&](int h, const uint32_t (&P)[32]) {
+                            tc_st_x32(s_at + 32 * h, P);
+                            tc_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_at(bar(C::B_PFULL, 2 * buf + h));
+                        };
+                        // 32 columns of scores to weights
+                        f32x2 sum0, sum1;
+                        float top0, top1;
+                        auto weights = [&](auto plain, uint32_t (&s)[32], uint32_t* P, const uint4* k8, float m, int seen) {
+                            const f32x2 m2 = pack2(-m, -m);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const uint4 kk = k8[e / 2];
+                                f32x2 y = pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+                                if constexpr (!plain) y = mul2_loaded(y, rf2);
+                                y = fma2_loaded(y, e & 1 ? pack2(__uint_as_float(kk.z), __uint_as_float(kk.w)) : pack2(__uint_as_float(kk.x), __uint_as_float(kk.y)), m2);
+                                float2 v = unpack2(y);
+                                if constexpr (!plain) {
+                                    if (2 * e > seen) v.x = -INFINITY;
+                                    if (2 * e + 1 > seen) v.y = -INFINITY;
+                                }
+                                const float p0 = ex2(v.x), p1 = ex2(v.y);
+                                if (e & 1) {
+                                    top1 = max3(top1, v.x, v.y);
+                                    sum1 = add2(sum1, pack2(p0, p1));
+                                } else {
+                                    top0 = max3(top0, v.x, v.y);
+                                    sum0 = add2(sum0, pack2(p0, p1));
+                                }
+                                P[e] = pack_bf16(p0, p1);
+                            }
+                        };
+                        auto clear = [&]() {
+                            top0 = top1 = -INFINITY;
+                            sum0 = sum1 = 0ull;
+                        };
+                        auto passes = [&]() { return __any_sync(0xFFFFFFFFu, fmaxf(top0, top1) > LIMIT); };
+                        auto add_up = [&]() {
+                            const float2 p = unpack2(add2(sum0, sum1));
+                            l += p.x + p.y;
+                        };
+                        int h = 0;                   // the half that is to be done
+                        if (!fresh && !masked && !rowwise) {
+                            // Most tiles: no edge, no factor of the row's, the reference stays. The second half's scores come while the
+                            // first half's are at work. (A form of its own: with branches, and in a loop, the scores are copied from
+                            // where the loads leave them, two moves a pair.)
+                            uint32_t sa[32], sb[32], P[32];
+                            tc_ld_x32(s_at, sa);
+                            tc_ld_x32(s_at + 32, sb);
+                            tc_wait_ld();
+                            clear();
+                            weights(std::true_type{}, sa, P, kf, m, 0);
+                            tc_ld_x32(s_at + 64, sa);
+                            weights(std::true_type{}, sb, P + 16, kf + 8, m, 0);
+                            if (!passes()) {
+                                add_up();
+                                publish(0, P);
+                                h = 1;
+                                tc_ld_x32(s_at + 96, sb);
+                                tc_wait_ld();
+                                clear();
+                                weights(std::true_type{}, sa, P, kf + 16, m, 0);
+                                weights(std::true_type{}, sb, P + 16, kf + 24, m, 0);
+                                if (!passes()) {
+                                    add_up();
+                                    publish(1, P);
+                                    h = 2;
+                                }
+                            }
+                            tc_wait_ld();            // (what is under way goes to registers that are used again)
+                        }
 #pragma unroll 1
-                        for (int h = 0; h < 2; ++h) {
+                        for (; h < 2; ++h) {
                             const int seen = masked ? rel - 64 * h : TILE;   // columns of this half up to here are seen
                             const uint32_t sh = s_at + h * 64;
                             const uint4* kh = kf + 16 * h;
@@ -519,57 +592,22 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                                         tc_wait_st();
                                     }
                                 }
-                                const f32x2 m2 = pack2(-m, -m);
-                                float top0 = -INFINITY, top1 = -INFINITY;
-                                f32x2 sum0 = 0ull, sum1 = 0ull;
-                                // Weights of the half. A form of its own for tiles that need no more than the reference: branches within would
-                                // have the scores copied from where the loads leave them (two moves a pair).
-                                auto weights = [&](auto plain) {
-                                    uint32_t s[2][32];
-                                    tc_ld_x32(sh, s[0]);
-                                    tc_ld_x32(sh + 32, s[1]);
-                                    tc_wait_ld();
-#pragma unroll
-                                    for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                                        for (int e = 0; e < 16; ++e) {
-                                            const uint4 kk = kh[c * 8 + e / 2];
-                                            f32x2 y = pack2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
-                                            if constexpr (!plain) y = mul2_loaded(y, rf2);
-                                            y = fma2_loaded(y, e & 1 ? pack2(__uint_as_float(kk.z), __uint_as_float(kk.w)) : pack2(__uint_as_float(kk.x), __uint_as_float(kk.y)), m2);
-                                            float2 v = unpack2(y);
-                                            if constexpr (!plain) {
-                                                if (c * 32 + 2 * e > seen) v.x = -INFINITY;
-                                                if (c * 32 + 2 * e + 1 > seen) v.y = -INFINITY;
-                                            }
-                                            const float p0 = ex2(v.x), p1 = ex2(v.y);
-                                            if (e & 1) {
-                                                top1 = max3(top1, v.x, v.y);
-                                                sum1 = add2(sum1, pack2(p0, p1));
-                                            } else {
-                                                top0 = max3(top0, v.x, v.y);
-                                                sum0 = add2(sum0, pack2(p0, p1));
-                                            }
-                                            P[c * 16 + e] = pack_bf16(p0, p1);
-                                        }
-                                    }
-                                };
-                                if (rowwise || masked) weights(std::false_type{});
-                                else weights(std::true_type{});
+                                uint32_t sa[32], sb[32];
+                                tc_ld_x32(sh, sa);
+                                tc_ld_x32(sh + 32, sb);
+                                tc_wait_ld();
+                                clear();
+                                weights(std::false_type{}, sa, P, kh, m, seen);
+                                weights(std::false_type{}, sb, P + 16, kh + 8, m, seen - 32);
                                 // (scores of 2^27 and more may pass the limit by their rounding alone)
-                                move = __any_sync(0xFFFFFFFFu, fmaxf(top0, top1) > LIMIT);
+                                move = passes();
                                 if (moved || !move) {
-                                    const float2 p = unpack2(add2(sum0, sum1));
-                                    l += p.x + p.y;
+                                    add_up();
                                     break;
                                 }
                             }
                             if (!ok) break;
-                            tc_st_x32(s_at + 32 * h, P);
-                            tc_wait_st();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) arrive_at(bar(C::B_PFULL, 2 * buf + h));
+                            publish(h, P);
                             fresh = false;
                         }
                         if (!ok) break;
@@ -780,7 +818,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             const uint8_t* bytes = smem + C::OFF_SC + sc * C::SC_BYTES + TILE + pc * C::VR;
             constexpr int EACH = C::VR * D / 16 / 128;                       // 16 codes at once, of a thread
             const int left = x.end - t * TILE - pc * C::VR;                  // rows that somebody sees; what lies behind is anything
-#pragma unroll 2
+#pragma unroll
             for (int e = 0; e < EACH; ++e) {
                 // Eight neighbours take four places of a row in one panel of 64 columns and four of the next row in the
                 // next panel: all on different banks, where they read and where they write.
@@ -939,6 +977,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             };
             constexpr int PH = C::PIECES / 2;        // pieces of values of half a tile
             const int b = warp - 13;
+            const uint32_t s_tm = __shfl_sync(0xFFFFFFFFu, tm + b * TILE, 0);        // this buffer's S
             uint32_t item = 0, tile = 0, piece = 0;  // of the CTA: the first item of the part, its first tile, part
             uint32_t mine = b;                       // this buffer's next item
             bool ok = true;
@@ -946,45 +985,65 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             for (; ok && part_at(piece, x); ++piece) {
                 const int nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0), tiles = __shfl_sync(0xFFFFFFFFu, x.t1 - x.t0, 0);
                 const uint32_t last = item + tiles * nt;
-                for (; mine < last; mine += 2) {
-                    const int i = nt == 2 ? (int)(mine - item) >> 1 : (int)(mine - item), r = nt == 2 ? (int)(mine - item) & 1 : 0;
-                    const uint32_t t = tile + i, ks = t % NK;
-                    // (the buffer's last P has been used by an output that this warp has issued before)
-                    const uint32_t d = __shfl_sync(0xFFFFFFFFu, tm + b * TILE, 0);
-                    const uint32_t k = lower(KD, base + C::OFF_K + ks * C::KSLOT), q = lower(KD, base + C::OFF_Q + r * C::QTILE);
+                if (mine < last && !warp_wait_at(bar(C::B_QFULL, piece % QB), (piece / QB) & 1, stop)) break;
+                // Scores of item n of the part (its tile of keys has arrived).
+                auto scores = [&](uint32_t n, uint32_t k, uint32_t q) {
+                    const int i = nt == 2 ? (int)n >> 1 : (int)n;
                     // Q is free when all scores of the part are made, of both buffers
                     const int frees = nt == 2 ? i == tiles - 1 : (i == tiles - 1) + (i == tiles - 2 || tiles == 1);
-                    if (!warp_wait_at(bar(C::B_QFULL, piece % QB), (piece / QB) & 1, stop) ||
-                        !warp_wait_at(bar(C::B_KFULL, ks), (t / NK) & 1, stop)) { ok = false; break; }
-                    tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 2 * D / 32; ++kk) {
                             constexpr int STEPS = C::ROWB / 32, HALF = D / 32;
                             const int kq = kk % HALF;
-                            tc_mma_f8(d, desc(KD, q + (((kq / STEPS) * C::QPANEL + (kk / HALF) * TILE * C::ROWB + (kq % STEPS) * 32) >> 4)),
+                            tc_mma_f8(s_tm, desc(KD, q + (((kq / STEPS) * C::QPANEL + (kk / HALF) * TILE * C::ROWB + (kq % STEPS) * 32) >> 4)),
                                       desc(KD, k + (((kq / STEPS) * C::KPANEL + (kq % STEPS) * 32) >> 4)), ID_S, kk ? 1u : 0u);
                         }
                         commit_at(bar(C::B_SFULL, b));
-                        for (int z = nt; z < 3; ++z) commit_at(bar(C::B_KEMPTY, ks));        // one row tile arrives for two
+                        for (int z = nt; z < 3; ++z) commit_at(bar(C::B_KEMPTY, (tile + i) % NK));       // one row tile arrives for two
                         for (int z = 0; z < frees; ++z) commit_at(bar(C::B_QFREE));
                     }
                     __syncwarp();
+                };
+                // Waits for the keys of item n, and finds its operands.
+                uint32_t k = 0, q = 0;
+                auto keys = [&](uint32_t n) {
+                    const uint32_t t = tile + (nt == 2 ? n >> 1 : n);
+                    k = lower(KD, base + C::OFF_K + t % NK * C::KSLOT);
+                    q = lower(KD, base + C::OFF_Q + (nt == 2 ? n & 1 : 0) * C::QTILE);
+                    return warp_wait_at(bar(C::B_KFULL, t % NK), (t / NK) & 1, stop);
+                };
+                if (mine < last) {
+                    // the second row tile begins when the first one's scores are there: the groups then take turns at the softmax
+                    if (nt == 2 && mine > item && !warp_wait_at(bar(C::B_SFULL, 1 - b), (item >> 1) & 1, stop)) break;
+                    if (!keys(mine - item)) break;
+                    tc_fence_after();
+                    scores(mine - item, k, q);
+                }
+                for (; mine < last; mine += 2) {
+                    const uint32_t n = mine - item;
+                    const int r = nt == 2 ? (int)n & 1 : 0;
+                    const uint32_t t = tile + (nt == 2 ? n >> 1 : n);
+                    const uint32_t o = __shfl_sync(0xFFFFFFFFu, tm + C::TMEM_O + (C::NT == 2 && nt == 1 ? b : r) * D, 0);
+                    const bool first = C::NT == 2 ? n < 2 : n == 0;
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t bi = t * C::PIECES + h * PH;
-                        const uint32_t o = __shfl_sync(0xFFFFFFFFu, tm + C::TMEM_O + (C::NT == 2 && nt == 1 ? b : r) * D, 0), p = __shfl_sync(0xFFFFFFFFu, tm + b * TILE + h * 32, 0);
-                        const uint32_t add = __shfl_sync(0xFFFFFFFFu, (C::NT == 2 ? mine - item < 2 : i == 0) && h == 0 ? 0u : 1u, 0);
+                        const uint32_t p = __shfl_sync(0xFFFFFFFFu, s_tm + h * 32, 0), add = __shfl_sync(0xFFFFFFFFu, first && h == 0 ? 0u : 1u, 0);
                         uint32_t v[PH];
 #pragma unroll
                         for (int pc = 0; pc < PH; ++pc) v[pc] = lower(VD, base + C::OFF_B + (bi + pc) % NB * C::BSLOT);
-                        if (!warp_wait_at(bar(C::B_PFULL, 2 * b + h), (mine >> 1) & 1, stop)) { ok = false; break; }
+                        // What the next scores need is found before the wait that the softmax ends. (With a ring of two tiles those keys come
+                        // when this output is done.)
+                        if (C::NT == 2 && h == 1 && mine + 2 < last && !keys(n + 2)) { ok = false; break; }
                         // Outputs of one O add up in order: the other buffer's last is complete. (Its values then have arrived,
                         // without which the parity of the next ones' barriers would say nothing.)
-                        if (C::NT == 1 && h == 0 && mine > 0 && !warp_wait_at(bar(C::B_ODONE, 1 - b), ((mine - 1) >> 1) & 1, stop)) { ok = false; break; }
+                        if (C::NT == 1 && h == 0 && mine > 0 &&
+                            (!warp_wait_at(bar(C::B_PFULL, 2 * b), (mine >> 1) & 1, stop) ||
+                             !warp_wait_at(bar(C::B_ODONE, 1 - b), ((mine - 1) >> 1) & 1, stop))) { ok = false; break; }
 #pragma unroll
                         for (int pc = 0; pc < PH; ++pc) ok = ok && warp_wait_at(bar(C::B_BFULL, (bi + pc) % NB), ((bi + pc) / NB) & 1, stop);
-                        if (!ok) break;
+                        if (!ok || !warp_wait_at(bar(C::B_PFULL, 2 * b + h), (mine >> 1) & 1, stop)) { ok = false; break; }
                         tc_fence_after();
                         if (elect_one()) {
 #pragma unroll
@@ -999,6 +1058,11 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                         __syncwarp();
                     }
                     if (!ok) break;
+                    // (the buffer's P has been used by the output just issued)
+                    if (mine + 2 < last) {
+                        if (C::NT == 1 && !keys(n + 2)) { ok = false; break; }
+                        scores(n + 2, k, q);
+                    }
                     progress[b] = mine;
                 }
                 item = last;
