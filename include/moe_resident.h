@@ -583,7 +583,7 @@ moe_status moe_qk_rotate(const void* q, const void* k, int dtype, const int64_t*
  *   out      = sum_j p[j] v[j],    lse = log sum_j exp(score[j])
  * Rows that a token does not see never touch its result, whatever they hold.
  * Arguments as for moe_tree_attention, without a bound on a lane's tokens and
- * without a mask. A lane with fewer rows than tokens or more than its table
+ * without a mask; out is 32-byte aligned. A lane with fewer rows than tokens or more than its table
  * holds sets MOE_DEV_BAD_PAGE and gets zeros and lse = -inf; a page id outside
  * the cache sets it too, and page 0 is read in its place. Rows of q and out behind
  * cu_tokens[lanes] are left as they are.

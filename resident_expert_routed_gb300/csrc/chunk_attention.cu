@@ -25,8 +25,9 @@
 // Work: the units are laid end to end and cut into equal parts, one per CTA. A unit that one CTA does whole is written at
 // once; the others leave parts (O, reference, sum) in the workspace, and chunk_attention_join adds them up in order.
 //
-// Roles, 16 warps: two softmax groups of four; four that convert values and prepare queries; one that walks the run and
-// issues TMA; one of MMA issue for each buffer of S; one of scales, which also bounds all waits.
+// Roles, 20 warps: two softmax groups of four; two groups of four that convert pieces of values in turn and together prepare
+// queries; one warp that walks the run and issues TMA; one of MMA issue for each buffer of S; one of scales, which also
+// bounds all waits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -68,6 +69,7 @@ constexpr float LIMIT = 8.0f;                    // log2 of the largest weight b
 
 // The run's measure: a cache row of a unit with two row tiles, of one with one; a unit beside its rows.
 constexpr int FULL_COST = 4, HALF_COST = 3, UNIT_COST = 1024;
+constexpr int STAGGER = 20;                      // looks
 constexpr int LEAST_PART = 2048;                 // of a part
 
 struct Pos {                                     // a place in the run
@@ -91,17 +93,18 @@ template <int D>
 struct Cfg {
     static constexpr int NT = D <= 128 ? 2 : 1;               // row tiles of a unit
     static constexpr int ROWS = NT * TILE;
-    static constexpr int THREADS = 512;
+    static constexpr int THREADS = 640;
     static constexpr int ROWB = D >= 128 ? 128 : 64;          // bytes of an operand row of keys and queries: one swizzle atom
     static constexpr int PANELS = D / ROWB;
     static constexpr int KPANEL = TILE * ROWB, KSLOT = TILE * D;
     static constexpr int QPANEL = 2 * TILE * ROWB, QTILE = 2 * TILE * D;      // hi, then lo
-    static constexpr int NK = D == 64 ? 8 : D == 128 ? 4 : 2; // ring of key tiles (even: see MMA issue)
+    // Rings have even numbers of slots: see MMA issue, and the groups that convert, of which each takes every second piece.
+    static constexpr int NK = D == 64 ? 8 : 2;                // ring of key tiles
     static constexpr int VR = D == 256 ? 32 : 64;             // values come in pieces of so many rows
     static constexpr int PIECES = TILE / VR;
-    static constexpr int NR = D == 64 ? 8 : D == 128 ? 4 : 3; // ring of pieces as codes
+    static constexpr int NR = D == 64 ? 8 : D == 128 ? 6 : 2; // ring of pieces as codes
     static constexpr int RSLOT = VR * D;
-    static constexpr int NB = D == 64 ? 8 : D == 128 ? 3 : 4;                // ring of pieces in bf16
+    static constexpr int NB = D == 64 ? 8 : 4;                // ring of pieces in bf16
     static constexpr int VPANEL = VR * 128, BSLOT = VR * D * 2;
     static constexpr int SA = 4, NSC = 2 * SA;                // tiles that scales are under way ahead; their ring:
     static constexpr int SC_BYTES = 3 * TILE * 2;             // key bytes, value bytes, the columns' factors (float)
@@ -116,9 +119,9 @@ struct Cfg {
     static constexpr int QB = 4;
     static constexpr int OFF_QF = OFF_SID + 2 * SA * 128;     // [QB][ROWS] 2^-a of the queries' rows
     static constexpr int OFF_QU = OFF_QF + QB * ROWS * 4;     // [QB][2] 2^-a of a unit's rows; whether they differ instead
-    static constexpr int OFF_QX = OFF_QU + QB * 8;            // [2][largest, smallest][4 warps]
+    static constexpr int OFF_QX = OFF_QU + QB * 8;            // [2][largest, smallest][8 warps]
     static constexpr int NPD = 4;                             // parts that are told ahead
-    static constexpr int OFF_PD = OFF_QX + 64;
+    static constexpr int OFF_PD = OFF_QX + 128;
     static constexpr int OFF_BAR = OFF_PD + NPD * (int)sizeof(Part);
     static constexpr int B_KFULL = OFF_BAR;                   // [NK] a tile of keys has arrived
     static constexpr int B_KEMPTY = B_KFULL + 8 * NK;         // [NK] ... has been used
@@ -136,7 +139,7 @@ struct Cfg {
     static constexpr int B_QFREE = B_QFULL + 8 * QB;              // ... have been used
     static constexpr int B_QMAX = B_QFREE + 8;                // the four warps have their maxima
     static constexpr int B_PDFULL = B_QMAX + 8;               // [NPD] a part is told
-    static constexpr int B_PDEMPTY = B_PDFULL + 8 * NPD;      // [NPD] ... and read by the other fifteen warps
+    static constexpr int B_PDEMPTY = B_PDFULL + 8 * NPD;      // [NPD] ... and read by the other nineteen warps
     static constexpr int B_MERGE = B_PDEMPTY + 8 * NPD;       // group 1's share of a unit with one row tile is laid down
     static constexpr int B_MFREE = B_MERGE + 8;               // ... and read
     static constexpr int B_DONE = B_MFREE + 8;                 // the block's last output is written
@@ -144,10 +147,10 @@ struct Cfg {
     static constexpr int OFF_MISC = (B_DRAIN + 16 + 15) / 16 * 16;    // tmem slot, abort flag, progress [3] and one more, start, end
     static constexpr int SMEM = OFF_MISC + 32 + 32 + 1024;
     static constexpr int TMEM_O = 2 * TILE;                   // after S [2]
-    static constexpr int SOFT_REGS = 184, CONV_REGS = 80, REST_REGS = 64;     // 2 x 184 + 80 + 64 = 4 x 128
+    static constexpr int SOFT_REGS = 152, CONV_REGS = 56, REST_REGS = 64;     // 2 x 152 + 2 x 56 + 64 = 5 x 96
     static_assert(OFF_B % 1024 == 0 && OFF_R % 128 == 0 && OFF_K % 1024 == 0 && BSLOT % 1024 == 0, "alignment");
     static_assert(OFF_BAR % 8 == 0 && OFF_QF % 16 == 0 && SMEM <= 227 * 1024, "shared memory");
-    static_assert(2 * SOFT_REGS + CONV_REGS + REST_REGS <= 512, "registers");
+    static_assert(2 * SOFT_REGS + 2 * CONV_REGS + REST_REGS <= 5 * 96, "registers");
     static constexpr size_t PART_FLOATS = (size_t)ROWS * (D + 2);     // O [D / 4][ROWS][4], references, sums
 };
 constexpr size_t parts_offset(int ctas) { return ((size_t)(ctas + 1) * sizeof(Pos) + 255) / 256 * 256; }
@@ -203,6 +206,14 @@ MOE_DEV uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+// 32 bytes, a whole sector, of a thread.
+MOE_DEV void store_32(void* to, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f, uint32_t g, uint32_t h) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(to), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h) : "memory");
+}
+MOE_DEV void cp_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 MOE_DEV uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -379,7 +390,7 @@ __device__ __noinline__ void cut_run(const ChunkArgs& a, unsigned long long* scr
 }
 
 template <int D>
-__global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkArgs a) {
     using C = Cfg<D>;
     constexpr int NK = C::NK, NR = C::NR, NB = C::NB, NSC = C::NSC, QB = C::QB, ROWS = C::ROWS;
     extern __shared__ uint8_t smem_raw[];
@@ -400,16 +411,16 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             for (int i = 0; i < n; ++i) mbar_init(bar_ptr(offset) + i, arrivals);
         };
         init(C::B_KFULL, NK, 1); init(C::B_KEMPTY, NK, 2); init(C::B_RFULL, NR, 1); init(C::B_REMPTY, NR, 4);
-        init(C::B_BFULL, NB, 4); init(C::B_BEMPTY, NB, 2); init(C::B_SCFULL, NSC, 1); init(C::B_SCEMPTY, NSC, 12);
-        init(C::B_SFULL, 2, 1); init(C::B_PFULL, 4, 4); init(C::B_OHALF, 2, 1); init(C::B_ODONE, 2, 1); init(C::B_QFULL, QB, 4); init(C::B_QFREE, 1, 2);
-        init(C::B_QMAX, 1, 4); init(C::B_PDFULL, C::NPD, 1); init(C::B_PDEMPTY, C::NPD, 15); init(C::B_MERGE, 1, 4); init(C::B_MFREE, 1, 4); init(C::B_DONE, 1, 8); init(C::B_DRAIN, 2, 1);
+        init(C::B_BFULL, NB, 4); init(C::B_BEMPTY, NB, 2); init(C::B_SCFULL, NSC, 1); init(C::B_SCEMPTY, NSC, 16);
+        init(C::B_SFULL, 2, 1); init(C::B_PFULL, 4, 4); init(C::B_OHALF, 2, 1); init(C::B_ODONE, 2, 1); init(C::B_QFULL, QB, 8); init(C::B_QFREE, 1, 2);
+        init(C::B_QMAX, 1, 8); init(C::B_PDFULL, C::NPD, 1); init(C::B_PDEMPTY, C::NPD, 19); init(C::B_MERGE, 1, 4); init(C::B_MFREE, 1, 4); init(C::B_DONE, 1, 8); init(C::B_DRAIN, 2, 1);
         *abort_flag = 0;
         progress[0] = progress[1] = progress[2] = 0;
         fence_barrier_init();
         prefetch_tmap(&maps.k);
         prefetch_tmap(&maps.v);
     }
-    if (warp == 13) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
+    if (warp == 17) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
     pdl_wait();
     cut_run<D>(a, reinterpret_cast<unsigned long long*>(smem + C::OFF_Q), ends);      // (the queries' room, not yet in use)
     tc_fence_before();
@@ -656,17 +667,17 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                                         v[4 * e + 3] += w.w * f1;
                                     }
                                 }
-                                if (live) {
-                                    dst[c * 2] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-                                    dst[c * 2 + 1] = make_uint4(pack_bf16(v[8], v[9]), pack_bf16(v[10], v[11]), pack_bf16(v[12], v[13]), pack_bf16(v[14], v[15]));
-                                }
+                                if (live)
+                                    store_32(dst + c * 2, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]),
+                                             pack_bf16(v[8], v[9]), pack_bf16(v[10], v[11]), pack_bf16(v[12], v[13]), pack_bf16(v[14], v[15]));
                             }
                         if (split) {
                             __syncwarp();
                             if (lane == 0) arrive_at(bar(C::B_MFREE));
                         }
                     } else {
-                        if (whole && merges > 0 && !warp_wait_at(bar(C::B_MFREE), (merges - 1) & 1, stop)) break;
+                        // (group 1's rows may still be read for the last unit that was added up)
+                        if (g == 1 && merges > 0 && !warp_wait_at(bar(C::B_MFREE), (merges - 1) & 1, stop)) break;
                         if (live) {
                             part[ROWS * D + at] = m;
                             part[ROWS * D + ROWS + at] = l;
@@ -698,19 +709,19 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
         tc_wait_ld();
         __syncwarp();
         if (lane == 0) arrive_at(bar(C::B_DONE));
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ------------------------------------------------------------ queries in two parts; values in bf16
         regs_down<C::CONV_REGS>();
-        const int wl = warp & 3, ct = tid & 127;
+        const int wl = warp - 8, cg = wl >> 2, ct = tid & 127;       // of both groups; group
         // A unit's queries go through twice: for the largest size of each row (while the part before is at work, a few rows
         // with each piece of its values), then for the parts.
-        constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = 4 * RPW;            // lanes a row, rows a warp takes at once, all four
+        constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = 8 * RPW;            // lanes a row, rows a warp takes at once, all eight
         constexpr int BATCH = 4;                                              // loads under way
         const int part = lane % LPR, mine = wl * RPW + lane / LPR;
-        auto load = [&](const Part& x, int u) {      // (rows past the unit's last are its last again, and their results nobody's)
+        auto place = [&](const Part& x, int u) {     // (rows past the unit's last are its last again, and their results nobody's)
             u = min(u, x.rows - 1);
             const int t = (int)((uint32_t)u * a.by_group >> 16);
-            return *reinterpret_cast<const uint4*>(a.q + (int64_t)(x.tok0 + t) * a.q_token + (int64_t)(x.h * G + u - t * G) * a.q_head + part * 8);
+            return reinterpret_cast<const uint4*>(a.q + (int64_t)(x.tok0 + t) * a.q_token + (int64_t)(x.h * G + u - t * G) * a.q_head + part * 8);
         };
         auto row_factors = [&](uint32_t n) { return reinterpret_cast<float*>(smem + C::OFF_QF) + (n % QB) * ROWS; };
         uint32_t most = 0, least = 0x7FFFu;          // sizes of the next part's rows, as bf16 bits
@@ -733,19 +744,19 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             }
         };
         auto prepare = [&](const Part& x, uint32_t n) -> bool {
-            uint32_t* qx = reinterpret_cast<uint32_t*>(smem + C::OFF_QX) + (n & 1) * 8;
+            uint32_t* qx = reinterpret_cast<uint32_t*>(smem + C::OFF_QX) + (n & 1) * 16;
             most = __reduce_max_sync(0xFFFFFFFFu, most);
             least = __reduce_min_sync(0xFFFFFFFFu, least);
             if (lane == 0) {
                 qx[wl] = most;
-                qx[4 + wl] = least;
+                qx[8 + wl] = least;
                 arrive_at(bar(C::B_QMAX));
             }
             if (!warp_wait_at(bar(C::B_QMAX), n & 1, stop)) return false;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < 8; ++w) {
                 most = max(most, qx[w]);
-                least = min(least, qx[4 + w]);
+                least = min(least, qx[8 + w]);
             }
             // Rows within 2^4 of one another share one power of two, and the scores need no factor of their row's; the
             // smallest rows' low parts then end 2^-13 below their own maximum. (Subnormal rows count as 2^-126.)
@@ -763,62 +774,65 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                 *reinterpret_cast<float2*>(smem + C::OFF_QU + (n % QB) * 8) = make_float2(rowwise ? 1.0f : exp2_int(-unit_up), rowwise ? 1.0f : 0.0f);
             const int rounds = x.nt * TILE / STEP;
             const int panel = part * 8 / C::ROWB, chunk = part * 8 % C::ROWB / 16;
-            uint4 next[BATCH];
-#pragma unroll
-            for (int b = 0; b < BATCH; ++b) next[b] = load(x, b * STEP + mine);
             if (n > 0 && !warp_wait_at(bar(C::B_QFREE), (n - 1) & 1, stop)) return false;
+            // A row's bf16 values take as many bytes as its two parts: they come asynchronously, all at once, to where the parts
+            // will lie (an eighth of the segments to a lane), and the row's lanes then replace them.
+            constexpr int SEG = C::ROWB / 16;        // lanes a segment
+            auto row_at = [&](int u) { return C::OFF_Q + (u >> 7) * C::QTILE + (u & (TILE - 1)) * C::ROWB; };
+            const int raw_at = part / SEG / 2 * C::QPANEL + (part / SEG & 1) * TILE * C::ROWB + part % SEG * 16;
 #pragma unroll 1
-            for (int r0 = 0; r0 < rounds; r0 += BATCH) {
-                uint4 raw[BATCH];
+            for (int r = 0; r < rounds; ++r) {
+                const int u = r * STEP + mine;
+                cp_async_16(base + row_at(u) + raw_at, place(x, u));
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+#pragma unroll 1
+            for (int r = 0; r < rounds; ++r) {
+                const int u = r * STEP + mine;
+                const uint4 raw = *reinterpret_cast<const uint4*>(smem + row_at(u) + raw_at);
+                const uint32_t key = rowwise ? keys[u] : 0u;
+                __syncwarp();
+                const int up = rowwise ? up_of(key) : unit_up;
+                const float gain = exp2_int(up);
+                const f32x2 gain2 = pack2(gain, gain);
+                const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+                uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                    raw[b] = next[b];
-                    next[b] = load(x, (r0 + BATCH + b) * STEP + mine);
+                for (int e = 0; e < 4; ++e) {
+                    // a scaled bf16 value is exact in fp16 (down to 2^-16, far below what lo resolves)
+                    const float2 v = unpack2(mul2(pack2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xFFFF0000u)), gain2));
+                    const __half2 vh = __floats2half2_rn(v.x, v.y);
+                    hi[e] = __nv_cvt_halfraw2_to_fp8x2(vh, __NV_SATFINITE, __NV_E4M3);
+                    const __half2 rest = __hsub2(vh, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3)));
+                    lo[e] = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
                 }
-#pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                    const int u = (r0 + b) * STEP + mine;
-                    const uint32_t key = rowwise ? keys[u] : 0u;
-                    __syncwarp();
-                    const int up = rowwise ? up_of(key) : unit_up;
-                    const float gain = exp2_int(up);
-                    const f32x2 gain2 = pack2(gain, gain);
-                    const uint32_t in[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        // a scaled bf16 value is exact in fp16 (down to 2^-16, far below what lo resolves)
-                        const float2 v = unpack2(mul2(pack2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xFFFF0000u)), gain2));
-                        const __half2 vh = __floats2half2_rn(v.x, v.y);
-                        hi[e] = __nv_cvt_halfraw2_to_fp8x2(vh, __NV_SATFINITE, __NV_E4M3);
-                        const __half2 rest = __hsub2(vh, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3)));
-                        lo[e] = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
-                    }
-                    // a row that is not finite: its scores become NaN
-                    if (rowwise && part == 0) qf[u] = key >= 0x7F80u ? __uint_as_float(0x7FC00000u) : exp2_int(-up);
-                    const int ur = u & (TILE - 1), swz = C::ROWB == 128 ? ur & 7 : (ur >> 1) & 3;
-                    uint8_t* to = smem + C::OFF_Q + (u >> 7) * C::QTILE + panel * C::QPANEL + ur * C::ROWB + ((chunk ^ swz) << 4) + (part & 1) * 8;
-                    *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(hi[0], hi[1], 0x5410), __byte_perm(hi[2], hi[3], 0x5410));
-                    *reinterpret_cast<uint2*>(to + TILE * C::ROWB) = make_uint2(__byte_perm(lo[0], lo[1], 0x5410), __byte_perm(lo[2], lo[3], 0x5410));
-                }
+                // a row that is not finite: its scores become NaN
+                if (rowwise && part == 0) qf[u] = key >= 0x7F80u ? __uint_as_float(0x7FC00000u) : exp2_int(-up);
+                const int swz = C::ROWB == 128 ? u & 7 : (u >> 1) & 3;
+                uint8_t* to = smem + row_at(u) + panel * C::QPANEL + ((chunk ^ swz) << 4) + (part & 1) * 8;
+                *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(hi[0], hi[1], 0x5410), __byte_perm(hi[2], hi[3], 0x5410));
+                *reinterpret_cast<uint2*>(to + TILE * C::ROWB) = make_uint2(__byte_perm(lo[0], lo[1], 0x5410), __byte_perm(lo[2], lo[3], 0x5410));
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) arrive_at(bar(C::B_QFULL, n % QB));
             return true;
         };
-        // One piece of values (the part's i-th): codes to bf16.
-        uint32_t pieces = 0;
+        // One piece of values (of the part's, the group's i-th): codes to bf16.
+        constexpr int MINE = C::PIECES / 2;          // pieces of a tile that are this group's
+        uint32_t tile = 0;                           // of the CTA
         auto convert = [&](const Part& x, int i) -> bool {
-            const int pc = i % C::PIECES, t = x.t0 + i / C::PIECES;
-            const uint32_t tile = pieces / C::PIECES, sc = tile % NSC, rs = pieces % NR, bs = pieces % NB;
-            if (pc == 0 && !warp_wait_at(bar(C::B_SCFULL, sc), (tile / NSC) & 1, stop)) return false;
+            const int pc = i % MINE * 2 + cg, t = x.t0 + i / MINE;
+            const uint32_t pieces = tile * C::PIECES + pc, sc = tile % NSC, rs = pieces % NR, bs = pieces % NB;
+            if (pc < 2 && !warp_wait_at(bar(C::B_SCFULL, sc), (tile / NSC) & 1, stop)) return false;
             if (!warp_wait_at(bar(C::B_RFULL, rs), (pieces / NR) & 1, stop)) return false;
             if (!warp_wait_at(bar(C::B_BEMPTY, bs), ((pieces / NB) & 1) ^ 1, stop)) return false;
             const uint8_t* bytes = smem + C::OFF_SC + sc * C::SC_BYTES + TILE + pc * C::VR;
             constexpr int EACH = C::VR * D / 16 / 128;                       // 16 codes at once, of a thread
             const int left = x.end - t * TILE - pc * C::VR;                  // rows that somebody sees; what lies behind is anything
-#pragma unroll
+            // (one after the other: two or four at once cost more in instruction fetches than they save)
+#pragma unroll 1
             for (int e = 0; e < EACH; ++e) {
                 // Eight neighbours take four places of a row in one panel of 64 columns and four of the next row in the
                 // next panel: all on different banks, where they read and where they write.
@@ -860,21 +874,21 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             if (lane == 0) {
                 arrive_at(bar(C::B_BFULL, bs));
                 arrive_at(bar(C::B_REMPTY, rs));
-                if (pc == C::PIECES - 1) arrive_at(bar(C::B_SCEMPTY, sc));
+                if (pc >= C::PIECES - 2) arrive_at(bar(C::B_SCEMPTY, sc));
             }
-            ++pieces;
+            if (pc >= C::PIECES - 2) ++tile;
             return true;
         };
         Part x{}, nx;
         bool ok = true, more = part_at(0, nx);
         for (uint32_t n = 0; ok; ++n) {              // the values of part n - 1 (none), with them the next queries' sizes; then these
-            const int todo = (x.t1 - x.t0) * C::PIECES, batches = more ? nx.nt * TILE / STEP / BATCH : 0;
+            const int todo = (x.t1 - x.t0) * MINE, batches = more ? nx.nt * TILE / STEP / BATCH : 0;
 #pragma unroll 1
             for (int i = 0; i < todo || i < batches; ++i) {
                 uint4 raw[BATCH];
                 if (i < batches)
 #pragma unroll
-                    for (int b = 0; b < BATCH; ++b) raw[b] = load(nx, (i * BATCH + b) * STEP + mine);
+                    for (int b = 0; b < BATCH; ++b) raw[b] = *place(nx, (i * BATCH + b) * STEP + mine);
                 if (i < todo && !convert(x, i)) { ok = false; break; }
                 if (i < batches) sizes(raw, n, i * BATCH);
             }
@@ -891,7 +905,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
             if (tell) record_error(a.err, MOE_DEV_BAD_PAGE);
             return 0;
         };
-        if (warp == 12) {
+        if (warp == 16) {
             // -------------------------------------------------------- TMA: lane l < 8 looks up the page of the tile's rows 16 l ..
             const int rk = P < TILE ? P : TILE, rv = P < C::VR ? P : C::VR;          // rows a copy
             const Pos end = ends[1];
@@ -958,7 +972,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                 x = nx;
                 if (x.t1 == 0) break;
             }
-        } else if (warp < 15) {
+        } else if (warp < 19) {
             // -------------------------------------------------------- MMA issue: a warp for each buffer of S. Scores of an item (tile,
             // row tile), both halves of its output, scores of the item after the next. (One warp for both has more to decide a
             // step than the step's products take.) With one row tile a warp sees every second tile only: the ring of keys has an
@@ -976,7 +990,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                 return d;
             };
             constexpr int PH = C::PIECES / 2;        // pieces of values of half a tile
-            const int b = warp - 13;
+            const int b = warp - 17;
             const uint32_t s_tm = __shfl_sync(0xFFFFFFFFu, tm + b * TILE, 0);        // this buffer's S
             uint32_t item = 0, tile = 0, piece = 0;  // of the CTA: the first item of the part, its first tile, part
             uint32_t mine = b;                       // this buffer's next item
@@ -986,11 +1000,26 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                 const int nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0), tiles = __shfl_sync(0xFFFFFFFFu, x.t1 - x.t0, 0);
                 const uint32_t last = item + tiles * nt;
                 if (mine < last && !warp_wait_at(bar(C::B_QFULL, piece % QB), (piece / QB) & 1, stop)) break;
-                // Scores of item n of the part (its tile of keys has arrived).
-                auto scores = [&](uint32_t n, uint32_t k, uint32_t q) {
+                // Waits for the keys of item n, and finds its operands.
+                uint32_t k = 0, q = 0;
+                auto keys = [&](uint32_t n) {
+                    const uint32_t t = tile + (nt == 2 ? n >> 1 : n);
+                    k = lower(KD, base + C::OFF_K + t % NK * C::KSLOT);
+                    q = lower(KD, base + C::OFF_Q + (nt == 2 ? n & 1 : 0) * C::QTILE);
+                    return warp_wait_at(bar(C::B_KFULL, t % NK), (t / NK) & 1, stop);
+                };
+                // The second row tile begins when half of the first one's weights are there, and the groups then take turns at the
+                // softmax. (A few looks: whether it has begun, and not how often since, is all that the barrier can tell.)
+                if (nt == 2 && mine == item + 1)
+                    for (int z = 0; z < STAGGER && !__all_sync(0xFFFFFFFFu, test_at(bar(C::B_PFULL, 2 * (1 - b)), (item >> 1) & 1)); ++z) {}
+                if (mine < last && !keys(mine - item)) break;
+                for (; mine < last; mine += 2) {
+                    const uint32_t n = mine - item;
                     const int i = nt == 2 ? (int)n >> 1 : (int)n;
                     // Q is free when all scores of the part are made, of both buffers
                     const int frees = nt == 2 ? i == tiles - 1 : (i == tiles - 1) + (i == tiles - 2 || tiles == 1);
+                    tc_fence_after();
+                    // (the buffer's last P has been used by an output that this warp has issued before)
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 2 * D / 32; ++kk) {
@@ -1004,26 +1033,8 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                         for (int z = 0; z < frees; ++z) commit_at(bar(C::B_QFREE));
                     }
                     __syncwarp();
-                };
-                // Waits for the keys of item n, and finds its operands.
-                uint32_t k = 0, q = 0;
-                auto keys = [&](uint32_t n) {
-                    const uint32_t t = tile + (nt == 2 ? n >> 1 : n);
-                    k = lower(KD, base + C::OFF_K + t % NK * C::KSLOT);
-                    q = lower(KD, base + C::OFF_Q + (nt == 2 ? n & 1 : 0) * C::QTILE);
-                    return warp_wait_at(bar(C::B_KFULL, t % NK), (t / NK) & 1, stop);
-                };
-                if (mine < last) {
-                    // the second row tile begins when the first one's scores are there: the groups then take turns at the softmax
-                    if (nt == 2 && mine > item && !warp_wait_at(bar(C::B_SFULL, 1 - b), (item >> 1) & 1, stop)) break;
-                    if (!keys(mine - item)) break;
-                    tc_fence_after();
-                    scores(mine - item, k, q);
-                }
-                for (; mine < last; mine += 2) {
-                    const uint32_t n = mine - item;
                     const int r = nt == 2 ? (int)n & 1 : 0;
-                    const uint32_t t = tile + (nt == 2 ? n >> 1 : n);
+                    const uint32_t t = tile + i;
                     const uint32_t o = __shfl_sync(0xFFFFFFFFu, tm + C::TMEM_O + (C::NT == 2 && nt == 1 ? b : r) * D, 0);
                     const bool first = C::NT == 2 ? n < 2 : n == 0;
 #pragma unroll 1
@@ -1058,11 +1069,7 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
                         __syncwarp();
                     }
                     if (!ok) break;
-                    // (the buffer's P has been used by the output just issued)
-                    if (mine + 2 < last) {
-                        if (C::NT == 1 && !keys(n + 2)) { ok = false; break; }
-                        scores(n + 2, k, q);
-                    }
+                    if (C::NT == 1 && mine + 2 < last && !keys(n + 2)) { ok = false; break; }
                     progress[b] = mine;
                 }
                 item = last;
@@ -1166,15 +1173,15 @@ __global__ void __launch_bounds__(512, 1) chunk_attention(const __grid_constant_
     tc_fence_before();
     __syncthreads();
     if (*abort_flag) {                               // final after the barrier: nothing new is issued past it
-        if (warp == 12 && lane == 0) {
+        if (warp == 16 && lane == 0) {
             drain_stage_fills(bar_ptr(C::B_KFULL), NK, issued_k);
             drain_stage_fills(bar_ptr(C::B_RFULL), NR, issued_r);
         }
-        if ((warp == 13 || warp == 14) && elect_one()) tc_drain(bar_ptr(C::B_DRAIN) + (warp - 13));
+        if ((warp == 17 || warp == 18) && elect_one()) tc_drain(bar_ptr(C::B_DRAIN) + (warp - 17));
         tc_fence_before();
         __syncthreads();
     }
-    if (warp == 13) {
+    if (warp == 17) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -1306,7 +1313,7 @@ moe_status moe_chunk_attention(const void* q, int64_t q_token_stride, int64_t q_
     if (n_tokens < 0) return MOE_EINVAL;
     if (n_tokens == 0) return MOE_OK;
     if (!q || !page_table || !kv_len || !cu_tokens || !out || !workspace) return MOE_EINVAL;
-    if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) & 15) return MOE_EINVAL;
+    if ((((uintptr_t)q | (uintptr_t)workspace) & 15) || ((uintptr_t)out & 31)) return MOE_EINVAL;
     if (lanes < 1 || table_width < 1 || n_q_heads < 1 || n_q_heads % cache->n_kv_heads) return MOE_EINVAL;
     if (q_token_stride % 8 || q_head_stride % 8 || !(scale > 0.0f) || scale > 3.0e38f) return MOE_EINVAL;
     if (lanes > 4096 || n_q_heads > 1024 || n_q_heads / cache->n_kv_heads > 128 || n_tokens > (1 << 24)) return MOE_EUNSUPPORTED;
