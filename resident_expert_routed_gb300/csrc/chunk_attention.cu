@@ -68,7 +68,7 @@ constexpr float NEVER = -1e30f;                  // the reference of a row that 
 constexpr float LIMIT = 8.0f;                    // log2 of the largest weight before the reference moves
 
 // The run's measure: a cache row of a unit with two row tiles, of one with one; a unit beside its rows.
-constexpr int FULL_COST = 4, HALF_COST = 3, UNIT_COST = 1024;
+constexpr int FULL_COST = 4, HALF_COST = 3, UNIT_COST = 1536;
 constexpr int STAGGER = 20;                      // looks
 constexpr int LEAST_PART = 2048;                 // of a part
 
@@ -354,7 +354,7 @@ __device__ __noinline__ void cut_run(const ChunkArgs& a, unsigned long long* scr
             const unsigned long long x = z ? next : first;
             if (x < at || x >= at + size) continue;
             const unsigned long long off = x - at, head = c.head();
-            const int h = (int)(off / head);
+            const int h = (off | head) >> 32 ? (int)(off / head) : (int)((uint32_t)off / (uint32_t)head);
             const unsigned long long rest = off - h * head;
             int lo = 0, hi = c.blocks - 1;       // the last block that begins at or before rest
             while (lo < hi) {
@@ -366,7 +366,7 @@ __device__ __noinline__ void cut_run(const ChunkArgs& a, unsigned long long* scr
             if (!a.whole && in > UNIT_COST) {
                 const int left = (l.n - lo * a.block) * a.group;
                 const int w = Cfg<D>::NT == 2 && left <= TILE ? HALF_COST : FULL_COST;
-                tile = (int)((in - UNIT_COST) / (unsigned long long)(w * TILE));
+                tile = (int)((uint32_t)((in - UNIT_COST) / TILE) / (uint32_t)w);
             }
             here[z] = Pos{b0 + tid, h * c.blocks + lo, tile, 0};
         }
@@ -527,61 +527,48 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                             l += p.x + p.y;
                         };
                         int h = 0;                   // the half that is to be done
-                        if (!fresh && !masked && !rowwise) {
-                            // Most tiles: no edge, no factor of the row's, the reference stays. The second half's scores come while the
-                            // first half's are at work. (A form of its own: with branches, and in a loop, the scores are copied from
-                            // where the loads leave them, two moves a pair.)
-                            uint32_t sa[32], sb[32], P[32];
-                            tc_ld_x32(s_at, sa);
-                            tc_ld_x32(s_at + 32, sb);
-                            tc_wait_ld();
-                            clear();
-                            weights(std::true_type{}, sa, P, kf, m, 0);
-                            tc_ld_x32(s_at + 64, sa);
-                            weights(std::true_type{}, sb, P + 16, kf + 8, m, 0);
-                            if (!passes()) {
-                                add_up();
-                                publish(0, P);
-                                h = 1;
-                                tc_ld_x32(s_at + 96, sb);
+                        // Most tiles: no edge, no factor of the row's, the reference stays. (A form of its own: with branches within, the
+                        // scores are copied from where the loads leave them, two moves a pair. A loop, though the second half's scores
+                        // could come ahead: the instructions' cache is as scarce.)
+                        if (!fresh && !masked && !rowwise)
+#pragma unroll 1
+                            for (; h < 2; ++h) {
+                                uint32_t sa[32], sb[32], P[32];
+                                tc_ld_x32(s_at + h * 64, sa);
+                                tc_ld_x32(s_at + h * 64 + 32, sb);
                                 tc_wait_ld();
                                 clear();
-                                weights(std::true_type{}, sa, P, kf + 16, m, 0);
-                                weights(std::true_type{}, sb, P + 16, kf + 24, m, 0);
-                                if (!passes()) {
-                                    add_up();
-                                    publish(1, P);
-                                    h = 2;
-                                }
+                                weights(std::true_type{}, sa, P, kf + 16 * h, m, 0);
+                                weights(std::true_type{}, sb, P + 16, kf + 16 * h + 8, m, 0);
+                                if (passes()) break;
+                                add_up();
+                                publish(h, P);
                             }
-                            tc_wait_ld();            // (what is under way goes to registers that are used again)
-                        }
 #pragma unroll 1
                         for (; h < 2; ++h) {
                             const int seen = masked ? rel - 64 * h : TILE;   // columns of this half up to here are seen
                             const uint32_t sh = s_at + h * 64;
                             const uint4* kh = kf + 16 * h;
-                            uint32_t P[32];
+                            uint32_t sa[32], sb[32], P[32];
+                            tc_ld_x32(sh, sa);
+                            tc_ld_x32(sh + 32, sb);
+                            tc_wait_ld();
                             bool move = fresh;
                             for (bool moved = false;; moved = true) {
                                 if (move) {
                                     // the reference moves to the largest score so far, and what has been added up with it
                                     float most = -INFINITY;
-#pragma unroll 1
-                                    for (int c = 0; c < 4; ++c) {
-                                        uint32_t s1[16];
-                                        tc_load(sh + c * 16, s1);
+                                    auto largest = [&](const uint32_t (&s)[32], const uint4* k8, int seen) {
 #pragma unroll
-                                        for (int e = 0; e < 4; ++e) {
-                                            const uint4 k = kh[c * 4 + e];
-                                            const uint32_t k4[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-                                            for (int z = 0; z < 4; ++z) {
-                                                const float v = __uint_as_float(s1[4 * e + z]) * rf * __uint_as_float(k4[z]);
-                                                if (c * 16 + 4 * e + z <= seen) most = fmaxf(most, v);
-                                            }
+                                        for (int e = 0; e < 16; ++e) {
+                                            const uint4 kk = k8[e / 2];
+                                            const f32x2 y = mul2_loaded(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), rf2);
+                                            const float2 v = unpack2(mul2(y, e & 1 ? pack2(__uint_as_float(kk.z), __uint_as_float(kk.w)) : pack2(__uint_as_float(kk.x), __uint_as_float(kk.y))));
+                                            most = max3(most, 2 * e <= seen ? v.x : -INFINITY, 2 * e + 1 <= seen ? v.y : -INFINITY);
                                         }
-                                    }
+                                    };
+                                    largest(sa, kh, seen);
+                                    largest(sb, kh + 8, seen - 32);
                                     const float mn = fmaxf(m, most);
                                     const float alpha = ex2(m - mn);
                                     l *= alpha;
@@ -592,21 +579,17 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                                                   : !warp_wait_at(bar(C::B_ODONE, before_it & 1), (before_it >> 1) & 1, stop)) { ok = false; break; }
                                         tc_fence_after();
 #pragma unroll 1
-                                        for (int c = 0; c < D / 8; ++c) {
-                                            uint32_t o[8];
-                                            tc_ld_x8(o_at + c * 8, o);
-                                            tc_wait_ld();
+                                        for (int c = 0; c < D / 16; ++c) {
+                                            uint32_t o[16];
+                                            tc_load(o_at + c * 16, o);
 #pragma unroll
-                                            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                            tc_st_x8(o_at + c * 8, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
+                                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                            tc_st_x8(o_at + c * 16, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
+                                            tc_st_x8(o_at + c * 16 + 8, make_uint4(o[8], o[9], o[10], o[11]), make_uint4(o[12], o[13], o[14], o[15]));
                                         }
                                         tc_wait_st();
                                     }
                                 }
-                                uint32_t sa[32], sb[32];
-                                tc_ld_x32(sh, sa);
-                                tc_ld_x32(sh + 32, sb);
-                                tc_wait_ld();
                                 clear();
                                 weights(std::false_type{}, sa, P, kh, m, seen);
                                 weights(std::false_type{}, sb, P + 16, kh + 8, m, seen - 32);
@@ -651,16 +634,16 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                         uint4* dst = reinterpret_cast<uint4*>(a.out + to * D);
                         if (!split || __any_sync(0xFFFFFFFFu, live))
 #pragma unroll 1
-                            for (int c = 0; c < D / 16; ++c) {
-                                uint32_t o[16];
-                                tc_load(o_at + c * 16, o);
-                                float v[16];
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tc_load(o_at + c * 32, o);
+                                float v[32];
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) v[e] = fresh ? 0.0f : __uint_as_float(o[e]) * f0;
+                                for (int e = 0; e < 32; ++e) v[e] = fresh ? 0.0f : __uint_as_float(o[e]) * f0;
                                 if (split && f1 != 0.0f) {
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const float4 w = *reinterpret_cast<const float4*>(part + ((size_t)(c * 4 + e) * ROWS + TILE + j) * 4);
+                                    for (int e = 0; e < 8; ++e) {
+                                        const float4 w = *reinterpret_cast<const float4*>(part + ((size_t)(c * 8 + e) * ROWS + TILE + j) * 4);
                                         v[4 * e] += w.x * f1;
                                         v[4 * e + 1] += w.y * f1;
                                         v[4 * e + 2] += w.z * f1;
@@ -668,8 +651,11 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                                     }
                                 }
                                 if (live)
-                                    store_32(dst + c * 2, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]),
-                                             pack_bf16(v[8], v[9]), pack_bf16(v[10], v[11]), pack_bf16(v[12], v[13]), pack_bf16(v[14], v[15]));
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 16)
+                                        store_32(dst + c * 4 + e / 8, pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]), pack_bf16(v[e + 4], v[e + 5]),
+                                                 pack_bf16(v[e + 6], v[e + 7]), pack_bf16(v[e + 8], v[e + 9]), pack_bf16(v[e + 10], v[e + 11]),
+                                                 pack_bf16(v[e + 12], v[e + 13]), pack_bf16(v[e + 14], v[e + 15]));
                             }
                         if (split) {
                             __syncwarp();
@@ -723,6 +709,17 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
             const int t = (int)((uint32_t)u * a.by_group >> 16);
             return reinterpret_cast<const uint4*>(a.q + (int64_t)(x.tok0 + t) * a.q_token + (int64_t)(x.h * G + u - t * G) * a.q_head + part * 8);
         };
+        // A row's bf16 values take as many bytes as its two parts: they come asynchronously, all at once, to where the parts
+        // will lie (an eighth of the segments to a lane), and the row's lanes then replace them.
+        constexpr int SEG = C::ROWB / 16;            // lanes a segment
+        auto row_at = [&](int u) { return C::OFF_Q + (u >> 7) * C::QTILE + (u & (TILE - 1)) * C::ROWB; };
+        const int raw_at = part / SEG / 2 * C::QPANEL + (part / SEG & 1) * TILE * C::ROWB + part % SEG * 16;
+        auto fetch = [&](const Part& x) {
+#pragma unroll 1
+            for (int u = mine; u < x.nt * TILE; u += STEP) cp_async_16(base + row_at(u) + raw_at, place(x, u));
+            cp_async_commit();
+            cp_async_wait<0>();
+        };
         auto row_factors = [&](uint32_t n) { return reinterpret_cast<float*>(smem + C::OFF_QF) + (n % QB) * ROWS; };
         uint32_t most = 0, least = 0x7FFFu;          // sizes of the next part's rows, as bf16 bits
         auto sizes = [&](const uint4 (&raw)[BATCH], uint32_t n, int r0) {
@@ -774,19 +771,10 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                 *reinterpret_cast<float2*>(smem + C::OFF_QU + (n % QB) * 8) = make_float2(rowwise ? 1.0f : exp2_int(-unit_up), rowwise ? 1.0f : 0.0f);
             const int rounds = x.nt * TILE / STEP;
             const int panel = part * 8 / C::ROWB, chunk = part * 8 % C::ROWB / 16;
-            if (n > 0 && !warp_wait_at(bar(C::B_QFREE), (n - 1) & 1, stop)) return false;
-            // A row's bf16 values take as many bytes as its two parts: they come asynchronously, all at once, to where the parts
-            // will lie (an eighth of the segments to a lane), and the row's lanes then replace them.
-            constexpr int SEG = C::ROWB / 16;        // lanes a segment
-            auto row_at = [&](int u) { return C::OFF_Q + (u >> 7) * C::QTILE + (u & (TILE - 1)) * C::ROWB; };
-            const int raw_at = part / SEG / 2 * C::QPANEL + (part / SEG & 1) * TILE * C::ROWB + part % SEG * 16;
-#pragma unroll 1
-            for (int r = 0; r < rounds; ++r) {
-                const int u = r * STEP + mine;
-                cp_async_16(base + row_at(u) + raw_at, place(x, u));
+            if (n > 0) {
+                if (!warp_wait_at(bar(C::B_QFREE), (n - 1) & 1, stop)) return false;
+                fetch(x);
             }
-            cp_async_commit();
-            cp_async_wait<0>();
 #pragma unroll 1
             for (int r = 0; r < rounds; ++r) {
                 const int u = r * STEP + mine;
@@ -881,6 +869,7 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
         };
         Part x{}, nx;
         bool ok = true, more = part_at(0, nx);
+        if (more) fetch(nx);                         // (of the first part from where they will lie)
         for (uint32_t n = 0; ok; ++n) {              // the values of part n - 1 (none), with them the next queries' sizes; then these
             const int todo = (x.t1 - x.t0) * MINE, batches = more ? nx.nt * TILE / STEP / BATCH : 0;
 #pragma unroll 1
@@ -888,7 +877,10 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                 uint4 raw[BATCH];
                 if (i < batches)
 #pragma unroll
-                    for (int b = 0; b < BATCH; ++b) raw[b] = *place(nx, (i * BATCH + b) * STEP + mine);
+                    for (int b = 0; b < BATCH; ++b) {
+                        const int u = (i * BATCH + b) * STEP + mine;
+                        raw[b] = *(n == 0 ? reinterpret_cast<const uint4*>(smem + row_at(u) + raw_at) : place(nx, u));
+                    }
                 if (i < todo && !convert(x, i)) { ok = false; break; }
                 if (i < batches) sizes(raw, n, i * BATCH);
             }
@@ -1268,7 +1260,9 @@ cudaError_t codes_map(CUtensorMap* m, const void* base, const moe_kv_cache& c, i
 template <int D>
 cudaError_t launch(ChunkArgs a, cudaStream_t s) {
     using C = Cfg<D>;
-    a.block = C::ROWS / a.group;
+    // Few units that are not cut: of one row tile each, for twice as many CTAs.
+    const int64_t heads = a.c.n_kv_heads, rows = (int64_t)a.n_tokens * a.group;
+    a.block = (C::NT == 2 && a.whole && (rows + C::ROWS - 1) / C::ROWS * heads * 2 <= moe_sm_count() ? TILE : C::ROWS) / a.group;
     ChunkMaps maps;
     cudaError_t e = codes_map(&maps.k, a.c.k_codes, a.c, C::ROWB, TILE, C::ROWB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     if (e == cudaSuccess) e = codes_map(&maps.v, a.c.v_codes, a.c, D, C::VR, CU_TENSOR_MAP_SWIZZLE_NONE);
