@@ -8,9 +8,9 @@
 // exact fraction of a turn, so a far position is as good as a near one and no 64-bit floating point is needed.
 // All else is fp32, rounded once.
 //
-// HBM bounds the large calls: each value is read and written once. D / 8 lanes share a vector (16 bytes a lane of a
-// 16-bit type), one warp takes one token's heads in turn, so a token's sines and cosines are computed once a warp and stay
-// in registers. The partner of a value is on another lane of the same vector (halves) or in the same one (interleaved).
+// HBM bounds the large calls: each value is read and written once. A lane holds eight whole pairs (so that no value has to be
+// fetched from a neighbour), D / 16 lanes a vector; a warp takes a token's heads in turn, with the token's sines and cosines
+// computed once and kept in registers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -18,7 +18,8 @@
 
 namespace {
 
-constexpr int ROT_THREADS = 256;
+constexpr int ROT_THREADS = 128;
+constexpr int WARPS = 16;                   // warps an SM, before a warp takes more than one
 
 struct RotArgs {
     const void* q;
@@ -37,20 +38,22 @@ struct RotArgs {
     int groups;                             // warps to a token
 };
 
-template <typename T> struct Eight;         // eight values as fp32
+template <typename T> struct Eight;         // eight values: as they lie in memory, and as fp32
 template <> struct Eight<float> {
-    static MOE_DEV void load(const void* p, float (&x)[8]) {
-        const float4 a = static_cast<const float4*>(p)[0], b = static_cast<const float4*>(p)[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    struct Raw { float4 a, b; };
+    static MOE_DEV Raw load(const void* p) { return Raw{static_cast<const float4*>(p)[0], static_cast<const float4*>(p)[1]}; }
+    static MOE_DEV void expand(const Raw& r, float* x) {
+        x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w; x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
     }
-    static MOE_DEV void store(void* p, const float (&x)[8]) {
+    static MOE_DEV void store(void* p, const float* x) {
         static_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
         static_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
     }
 };
 template <> struct Eight<__nv_bfloat16> {
-    static MOE_DEV void load(const void* p, float (&x)[8]) {
-        const uint4 v = *static_cast<const uint4*>(p);
+    typedef uint4 Raw;
+    static MOE_DEV Raw load(const void* p) { return *static_cast<const uint4*>(p); }
+    static MOE_DEV void expand(const Raw& v, float* x) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -58,7 +61,7 @@ template <> struct Eight<__nv_bfloat16> {
             x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
     }
-    static MOE_DEV void store(void* p, const float (&x)[8]) {
+    static MOE_DEV void store(void* p, const float* x) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -69,8 +72,9 @@ template <> struct Eight<__nv_bfloat16> {
     }
 };
 template <> struct Eight<__half> {
-    static MOE_DEV void load(const void* p, float (&x)[8]) {
-        const uint4 v = *static_cast<const uint4*>(p);
+    typedef uint4 Raw;
+    static MOE_DEV Raw load(const void* p) { return *static_cast<const uint4*>(p); }
+    static MOE_DEV void expand(const Raw& v, float* x) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -79,7 +83,7 @@ template <> struct Eight<__half> {
             x[2 * i + 1] = f.y;
         }
     }
-    static MOE_DEV void store(void* p, const float (&x)[8]) {
+    static MOE_DEV void store(void* p, const float* x) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -92,86 +96,107 @@ template <> struct Eight<__half> {
 
 template <typename T, int D, bool PAIRED>   // PAIRED: pairs side by side
 __global__ void __launch_bounds__(ROT_THREADS) qk_rotate(const __grid_constant__ RotArgs a) {
-    constexpr int LPV = D / 8, AT_ONCE = 32 / LPV;             // lanes to a vector, vectors that a warp holds
-    constexpr int N = PAIRED ? 4 : 8;                          // angles a lane needs
+    constexpr int LPV = D / 16, AT_ONCE = 32 / LPV;            // lanes to a vector, vectors that a warp holds
+    __shared__ __align__(16) float2 turned[ROT_THREADS / 32][D / 2];
     pdl_trigger();
     const int lane = threadIdx.x & 31, part = lane % LPV, sub = lane / LPV;
     const int64_t warp = (int64_t)blockIdx.x * (ROT_THREADS / 32) + (threadIdx.x >> 5);
     pdl_wait();
     if (warp >= (int64_t)a.n_tokens * a.groups) return;
     const int t = (int)(warp / a.groups), group = (int)(warp - (int64_t)t * a.groups);
-    const int at = part * 8, half = a.pairs / 8;               // this lane's first value; lanes to half of the turned part
-    const bool on = at < 2 * a.pairs;
-    const bool second = !PAIRED && part >= half;
-    float c[N], s[N];
+    // This lane's eight pairs, or sixteen of the values that are not turned: two pieces of eight, the first members of the
+    // pairs and the second ones, or what lies side by side.
+    const bool on = part < a.pairs / 8;
+    const int at0 = PAIRED ? part * 16 : on ? part * 8 : part * 16;        // (half layout: 2 pairs + 16 (part - pairs / 8))
+    const int at1 = PAIRED || !on ? at0 + 8 : a.pairs + at0;
+    const int heads = a.n_q + a.n_k;
+    const T* q = static_cast<const T*>(a.q) + t * a.q_token;
+    const T* k = static_cast<const T*>(a.k) + t * a.k_token;
+    T* qo = static_cast<T*>(a.q_out) + t * a.qo_token;
+    T* ko = static_cast<T*>(a.k_out) + t * a.ko_token;
+    const int h0 = group * a.per_warp * AT_ONCE + sub;
+    typename Eight<T>::Raw next[2];                            // the next vector's values, under way (the first's beside the angles)
+    auto load = [&](int i) {
+        const int h = h0 + i * AT_ONCE;
+        if (i >= a.per_warp || h >= heads) return;
+        const T* from = h < a.n_q ? q + h * a.q_head : k + (h - a.n_q) * a.k_head;
+        next[0] = Eight<T>::load(from + at0);
+        next[1] = Eight<T>::load(from + at1);
+    };
+    load(0);
+    // the token's cosines and sines, each once
+    float2* mine = turned[threadIdx.x >> 5];
+    const unsigned long long pos = a.pairs ? (unsigned long long)(long long)a.positions[t] : 0ull;
+#pragma unroll 1
+    for (int i = lane; i < a.pairs; i += 32) {
+        // a signed fraction of half a turn: [-1, 1)
+        const int turn = (int)((pos * (unsigned long long)a.turns[i]) >> 32);
+        float sn, cs;
+        sincospif((float)turn * 0x1p-31f, &sn, &cs);
+        mine[i] = make_float2(cs * a.magnitude, sn * a.magnitude);
+    }
+    __syncwarp();
+    float c[8], s[8];
     if (on) {
-        const unsigned long long pos = (unsigned long long)(long long)a.positions[t];
-        const int first = PAIRED ? at / 2 : (second ? at - a.pairs : at);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            // a signed fraction of half a turn: [-1, 1)
-            const int turn = (int)((pos * (unsigned long long)a.turns[first + i]) >> 32);
-            sincospif((float)turn * 0x1p-31f, &s[i], &c[i]);
-            c[i] *= a.magnitude;
-            s[i] *= a.magnitude;
-            if (second) s[i] = -s[i];
+        for (int i = 0; i < 8; i += 2) {
+            const float4 two = *reinterpret_cast<const float4*>(mine + part * 8 + i);
+            c[i] = two.x; s[i] = two.y;
+            c[i + 1] = two.z; s[i + 1] = two.w;
         }
     }
-    const int partner = (lane - part) + (!on ? part : second ? part - half : part + half);
-    const int heads = a.n_q + a.n_k;
-    const int h0 = group * a.per_warp * AT_ONCE;
+    int have = -1;                                             // whose weights w holds: 0 queries', 1 keys'
+    float w[16];
+#pragma unroll 1
     for (int i = 0; i < a.per_warp; ++i) {
-        const int h = h0 + i * AT_ONCE + sub;
-        const bool there = h < heads;
-        const bool key = h >= a.n_q;
-        const int hh = key ? h - a.n_q : h;
-        float x[8] = {};
-        if (there) {
-            const T* src = key ? static_cast<const T*>(a.k) + t * a.k_token + hh * a.k_head : static_cast<const T*>(a.q) + t * a.q_token + hh * a.q_head;
-            Eight<T>::load(src + at, x);
-        }
-        const float* w = key ? a.k_weight : a.q_weight;
-        float sum = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
-#pragma unroll
-        for (int o = LPV / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (w) {
-            const float r = 1.0f / sqrtf(sum * (1.0f / D) + a.eps);
-            float wv[8];
-            Eight<float>::load(w + at, wv);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= r * wv[e];
-        }
-        if constexpr (PAIRED) {
-            if (on) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float u = x[2 * e], v = x[2 * e + 1];
-                    x[2 * e] = u * c[e] - v * s[e];
-                    x[2 * e + 1] = v * c[e] + u * s[e];
-                }
+        const int h = h0 + i * AT_ONCE, key = h >= a.n_q;
+        float y[16];
+        Eight<T>::expand(next[0], y);
+        Eight<T>::expand(next[1], y + 8);
+        load(i + 1);
+        if (h >= heads) continue;                              // (whole vectors' lanes; nothing below needs the others)
+        const float* weight = key ? a.k_weight : a.q_weight;
+        if (weight) {
+            if (key != have) {
+                Eight<float>::expand(Eight<float>::load(weight + at0), w);
+                Eight<float>::expand(Eight<float>::load(weight + at1), w + 8);
+                have = key;
             }
-        } else {
+            float even = 0.0f, odd = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                even = fmaf(y[e], y[e], even);
+                odd = fmaf(y[e + 1], y[e + 1], odd);
+            }
+            float sum = even + odd;
+            constexpr uint32_t GROUP = (1u << LPV) - 1u;
+#pragma unroll
+            for (int o = LPV / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(GROUP << (lane - part), sum, o);
+            const float r = rsqrtf(sum * (1.0f / D) + a.eps);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] *= r * w[e];
+        }
+        if (on) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float v = __shfl_sync(0xFFFFFFFFu, x[e], partner);
-                if (on) x[e] = x[e] * c[e] - v * s[e];
+                const int m = PAIRED ? 2 * e : e, n = PAIRED ? 2 * e + 1 : e + 8;
+                const float first = y[m], second = y[n];
+                y[m] = first * c[e] - second * s[e];
+                y[n] = second * c[e] + first * s[e];
             }
         }
-        if (there) {
-            T* dst = key ? static_cast<T*>(a.k_out) + t * a.ko_token + hh * a.ko_head : static_cast<T*>(a.q_out) + t * a.qo_token + hh * a.qo_head;
-            Eight<T>::store(dst + at, x);
-        }
+        T* to = key ? ko + (h - a.n_q) * a.ko_head : qo + h * a.qo_head;
+        Eight<T>::store(to + at0, y);
+        Eight<T>::store(to + at1, y + 8);
     }
 }
 
 template <typename T, int D>
 cudaError_t launch(RotArgs a, bool interleaved, cudaStream_t s) {
-    constexpr int AT_ONCE = 32 / (D / 8);
+    constexpr int AT_ONCE = 32 / (D / 16);
     const int vectors = (a.n_q + a.n_k + AT_ONCE - 1) / AT_ONCE;        // a token's, in warps' loads
-    // as many vectors a warp as leave 32 warps an SM
-    const int64_t warps = (int64_t)moe_sm_count() * 32;
+    // as many vectors a warp as leave WARPS warps an SM
+    const int64_t warps = (int64_t)moe_sm_count() * WARPS;
     const int64_t per = (int64_t)a.n_tokens * vectors / warps;
     a.per_warp = (int)(per < 1 ? 1 : per > vectors ? vectors : per);
     a.groups = (vectors + a.per_warp - 1) / a.per_warp;
