@@ -28,7 +28,7 @@ from resident_expert_routed_gb300.layer import LayerBuffers
 HEADS, KV_HEADS, HEAD_DIM, PAGE = 8, 2, 64, 16
 
 
-def build(lanes: int, max_tokens: int, n_pages: int, seed: int = 0) -> DecodeLayer:
+def build(lanes: int, max_tokens: int, n_pages: int, seed: int = 0, norms=None) -> DecodeLayer:
     cfg = synth.TINY
     bias = synth.router_bias(cfg.seed, cfg.E, cfg.sigma)
     resident = synth.resident_set(cfg, bias)
@@ -47,7 +47,7 @@ def build(lanes: int, max_tokens: int, n_pages: int, seed: int = 0) -> DecodeLay
                 torch.zeros((1, cfg.E), dtype=torch.int64, device="cuda"), torch.zeros((1, cfg.E), device="cuda"), 0)
     return DecodeLayer(w((HEADS + 2 * KV_HEADS) * HEAD_DIM, cfg.d), w(cfg.d, HEADS * HEAD_DIM),
                        moe.KvCache.empty(n_pages, KV_HEADS, PAGE, HEAD_DIM), HEADS, lanes, max_tokens, moe_args,
-                       LayerBuffers(max_tokens, cfg.k, cfg.E, cfg.d, cfg.ffn, cfg.resident))
+                       LayerBuffers(max_tokens, cfg.k, cfg.E, cfg.d, cfg.ffn, cfg.resident), norms)
 
 
 def draft(rng: random.Random, n: int) -> list[int]:

@@ -1,18 +1,23 @@
-"""One decode layer of drafted tokens: attention over the paged 8-bit cache, then the routed-MoE layer step.
+"""One layer of a served model: attention over the paged 8-bit cache, then the routed-MoE layer step.
 
-``LanePages`` keeps, on the host, which pages of a cache each lane holds. ``DecodeLayer`` is a layer's weights and
-buffers; ``step`` runs it for the tree nodes (or single tokens) of all lanes: the projection of queries, keys and
-values (a plain library product), ``moe_kv_write``, ``moe_tree_attention``, the output projection and ``layer_step``.
-``keep`` moves the rows of each lane's accepted path together once the nodes have been checked. No arithmetic of the
-cache, the attention or the experts is done here.
+``LanePages`` keeps, on the host, which pages of a cache each lane holds; ``DevicePages`` keeps the same on the device
+(``moe_page_plan``), so that a batch of new tokens is planned without the host's lists. ``DecodeLayer`` is a layer's
+weights and buffers; ``step`` runs it for the tree nodes (or single tokens) of all lanes: the projection of queries, keys
+and values (a plain library product), ``moe_qk_rotate`` where the layer has norms or rotary positions, ``moe_kv_write``,
+``moe_tree_attention``, the output projection and ``layer_step``. ``chunk`` runs it for a chunk of new tokens of every lane
+(a prompt, the next part of one, a single token), with ``moe_chunk_attention``. ``keep`` moves the rows of each lane's
+accepted path together once the nodes have been checked. No arithmetic of the cache, the attention or the experts is done
+here.
 """
 from __future__ import annotations
 
 import copy
+from dataclasses import dataclass
 
 import torch
 
-from . import KvCache, moe_kv_keep, moe_kv_write, moe_tree_attention, moe_tree_attention_workspace_bytes
+from . import (KvCache, moe_chunk_attention, moe_chunk_attention_workspace_bytes, moe_kv_keep, moe_kv_write, moe_page_plan,
+               moe_qk_rotate, moe_tree_attention, moe_tree_attention_workspace_bytes)
 from .layer import LayerBuffers, layer_step
 
 
@@ -59,6 +64,46 @@ class LanePages:
         self.table[lane] = -1
 
 
+class DevicePages:
+    """Pages of a cache by lane, kept on the device: the state and the outputs of ``moe_page_plan``.
+
+    ``plan`` gives every lane room for its new tokens; ``kv_len``, ``cu``, ``positions`` and ``slots`` (of `max_tokens`
+    tokens) then belong to that batch, and ``advance`` keeps its rows. ``table`` int32 [lanes, width]; every layer's cache uses
+    the same one. Nothing here waits for the device."""
+
+    def __init__(self, lanes: int, n_pages: int, page_size: int, width: int, max_tokens: int, device="cuda"):
+        i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
+        self.page_size = page_size
+        self.rows, self.held, self.kv_len, self.cu = i32(lanes), i32(lanes), i32(lanes), i32(lanes + 1)
+        self.table = torch.full((lanes, width), -1, dtype=torch.int32, device=device)
+        self.free = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)       # page 0 on top
+        self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=device)
+        self.positions = i32(max_tokens)
+        self.slots = torch.full((max_tokens,), -1, dtype=torch.int64, device=device)
+
+    def plan(self, n_new: torch.Tensor) -> None:
+        """n_new int32 [lanes] on the device: new tokens of each lane; 0: it waits; below 0: it is done, and its pages are free.
+        A lane that cannot be served (no pages, no place) gets kv_len 0 and no slots, and the device status says so."""
+        moe_page_plan(n_new, self.rows, self.held, self.table, self.free, self.n_free, self.page_size, self.kv_len, self.cu,
+                      self.positions, self.slots)
+
+    def advance(self) -> None:
+        """The rows of the batch planned last are kept (those of lanes that were not served stay as they were)."""
+        self.rows.copy_(torch.maximum(self.rows, self.kv_len))
+
+
+@dataclass
+class HeadNorms:
+    """What ``moe_qk_rotate`` does with a layer's queries and keys: `turns` (``rotary.rotary_turns``) of its positions; weights
+    fp32 [head_dim] of the norms, or None."""
+    turns: torch.Tensor
+    q_weight: torch.Tensor | None = None
+    k_weight: torch.Tensor | None = None
+    eps: float = 1e-6
+    interleaved: bool = False
+    magnitude: float = 1.0
+
+
 def tree_mask(parents: list[int]) -> list[int]:
     """Ancestor bits of each node (its own among them) from the parents' indices, -1 for a root."""
     bits: list[int] = []
@@ -88,6 +133,8 @@ class Step:
         self.prefix, self.cu = dev(pages.rows), dev(cu)
         self.kv_len = dev([r + n for r, n in zip(pages.rows, counts)])
         self.slots = dev([s for b, n in enumerate(counts) for s in pages.slots(b, n)], torch.int64)
+        # a node's place in its lane's text: behind the prefix, as deep as it stands in the tree
+        self.positions = dev([r + bits.bit_count() - 1 for r, p in zip(pages.rows, parents) for bits in tree_mask(p)])
         self.mask = dev(mask).view(-1, words)
 
 
@@ -105,13 +152,14 @@ class DecodeLayer:
 
     w_qkv bf16 [(n_q_heads + 2 * n_kv_heads) * head_dim, d], w_out bf16 [d, n_q_heads * head_dim]; moe_args: (w_router,
     bias, slot_of, arena, demand, miss_max, layer) as for ``layer_step``; buf: its LayerBuffers, for at least
-    `max_tokens` tokens.
+    `max_tokens` tokens; norms: the norms and rotary positions of its queries and keys, or None.
     """
 
     def __init__(self, w_qkv: torch.Tensor, w_out: torch.Tensor, cache: KvCache, n_q_heads: int, lanes: int, max_tokens: int,
-                 moe_args: tuple, buf: LayerBuffers):
+                 moe_args: tuple, buf: LayerBuffers, norms: HeadNorms | None = None):
         self.w_qkv, self.w_out, self.cache, self.moe_args, self.buf = w_qkv, w_out, cache, moe_args, buf
-        self.heads, self.scale = n_q_heads, cache.head_dim ** -0.5
+        self.heads, self.scale, self.norms, self.lanes = n_q_heads, cache.head_dim ** -0.5, norms, lanes
+        self.chunk_workspace = None          # of the first chunk on
         self.out = torch.empty((max_tokens, n_q_heads, cache.head_dim), dtype=torch.bfloat16, device=w_qkv.device)
         self.workspace = torch.empty(moe_tree_attention_workspace_bytes(max_tokens, n_q_heads, cache.n_kv_heads, cache.head_dim, lanes),
                                      dtype=torch.uint8, device=w_qkv.device)
@@ -119,15 +167,43 @@ class DecodeLayer:
     def step(self, hidden: torch.Tensor, tables: Step, tree: bool = True) -> torch.Tensor:
         """hidden bf16 [n_nodes, d] of the step's nodes, lane by lane; returns the layer's bf16 output. tree = False:
         each lane's nodes are a chain (a chunk of its prompt)."""
-        n, H, D = tables.n_nodes, self.cache.n_kv_heads, self.cache.head_dim
+        n = tables.n_nodes
         if n == 0:                           # every lane waits
             return torch.empty_like(hidden)
-        qkv = hidden @ self.w_qkv.T
-        q, k, v = (x.view(n, -1, D) for x in qkv.split([self.heads * D, H * D, H * D], 1))
-        moe_kv_write(k, v, tables.slots, self.cache)
+        q = self._write(hidden, tables.positions, tables.slots)
         out = self.out[:n]
         moe_tree_attention(q, self.cache, tables.table, tables.kv_len, tables.cu, tables.max_nodes, tables.mask if tree else None,
                            self.scale, out, self.workspace)
+        return self._experts(hidden, out)
+
+    def chunk(self, hidden: torch.Tensor, pages: DevicePages) -> torch.Tensor:
+        """hidden bf16 [n, d] of the n new tokens that `pages` has planned last, lane by lane; returns the layer's bf16
+        output. (Tokens of lanes that were not served attend to nothing.)"""
+        n, H, D = hidden.shape[0], self.cache.n_kv_heads, self.cache.head_dim
+        if n == 0:
+            return torch.empty_like(hidden)
+        if self.chunk_workspace is None:
+            size = moe_chunk_attention_workspace_bytes(self.out.shape[0], self.heads, H, D, self.lanes)
+            self.chunk_workspace = torch.empty(size, dtype=torch.uint8, device=hidden.device)
+        q = self._write(hidden, pages.positions[:n], pages.slots[:n])
+        out = self.out[:n]
+        moe_chunk_attention(q, self.cache, pages.table, pages.kv_len, pages.cu, self.scale, out, self.chunk_workspace)
+        return self._experts(hidden, out)
+
+    def _write(self, hidden: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
+        """Queries of the tokens; their keys and values are in the cache."""
+        n, H, D = hidden.shape[0], self.cache.n_kv_heads, self.cache.head_dim
+        qkv = hidden @ self.w_qkv.T
+        q, k, v = (x.view(n, -1, D) for x in qkv.split([self.heads * D, H * D, H * D], 1))
+        if self.norms is not None:
+            c = self.norms
+            moe_qk_rotate(q, k, positions, c.turns, q, k, q_weight=c.q_weight, k_weight=c.k_weight, eps=c.eps, interleaved=c.interleaved,
+                          magnitude=c.magnitude)
+        moe_kv_write(k, v, slots, self.cache)
+        return q
+
+    def _experts(self, hidden: torch.Tensor, out: torch.Tensor) -> torch.Tensor:
+        n = hidden.shape[0]
         x = hidden + out.view(n, -1) @ self.w_out.T
         w_router, bias, slot_of, arena, demand, miss_max, layer = self.moe_args
         return (x + layer_step(x, w_router, bias, slot_of, arena, demand, miss_max, layer, _first_rows(self.buf, n))).to(torch.bfloat16)
