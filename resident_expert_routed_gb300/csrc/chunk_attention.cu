@@ -131,8 +131,8 @@ struct Cfg {
     static constexpr int B_BEMPTY = B_BFULL + 8 * NB;
     static constexpr int B_SCFULL = B_BEMPTY + 8 * NB;        // [NSC] a tile's factors and value bytes are there
     static constexpr int B_SCEMPTY = B_SCFULL + 8 * NSC;
-    static constexpr int B_SFULL = B_SCEMPTY + 8 * NSC;       // [2] S is ready
-    static constexpr int B_PFULL = B_SFULL + 16;              // [2][2] half of P is written (that half of S has been read)
+    static constexpr int B_SFULL = B_SCEMPTY + 8 * NSC;       // [2][2] half of S is ready
+    static constexpr int B_PFULL = B_SFULL + 32;              // [2][2] half of P is written (that half of S has been read)
     static constexpr int B_OHALF = B_PFULL + 32;              // [2] the first half of P has been used
     static constexpr int B_ODONE = B_OHALF + 16;              // [2] both: a tile is added to O
     static constexpr int B_QFULL = B_ODONE + 16;              // [QB] the queries of a part are there
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
         };
         init(C::B_KFULL, NK, 1); init(C::B_KEMPTY, NK, 2); init(C::B_RFULL, NR, 1); init(C::B_REMPTY, NR, 4);
         init(C::B_BFULL, NB, 4); init(C::B_BEMPTY, NB, 2); init(C::B_SCFULL, NSC, 1); init(C::B_SCEMPTY, NSC, 16);
-        init(C::B_SFULL, 2, 1); init(C::B_PFULL, 4, 4); init(C::B_OHALF, 2, 1); init(C::B_ODONE, 2, 1); init(C::B_QFULL, QB, 8); init(C::B_QFREE, 1, 2);
+        init(C::B_SFULL, 4, 1); init(C::B_PFULL, 4, 4); init(C::B_OHALF, 2, 1); init(C::B_ODONE, 2, 1); init(C::B_QFULL, QB, 8); init(C::B_QFREE, 1, 2);
         init(C::B_QMAX, 1, 8); init(C::B_PDFULL, C::NPD, 1); init(C::B_PDEMPTY, C::NPD, 19); init(C::B_MERGE, 1, 4); init(C::B_MFREE, 1, 4); init(C::B_DONE, 1, 8); init(C::B_DRAIN, 2, 1);
         *abort_flag = 0;
         progress[0] = progress[1] = progress[2] = 0;
@@ -479,12 +479,16 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                         const bool masked = j0 + TILE - 1 > open;
                         const int rel = limit - j0;                  // columns up to rel are seen
                         if (!warp_wait_at(bar(C::B_SCFULL, sc), ((tiles + i) / NSC) & 1, stop)) { ok = false; break; }
-                        if (!warp_wait_at(bar(C::B_SFULL, buf), (item >> 1) & 1, stop)) { ok = false; break; }
-                        tc_fence_after();
+                        auto scores_at = [&](int h) {
+                            if (!warp_wait_at(bar(C::B_SFULL, 2 * buf + h), (item >> 1) & 1, stop)) return ok = false;
+                            tc_fence_after();
+                            return true;
+                        };
                         const uint4* kf = reinterpret_cast<const uint4*>(smem + C::OFF_SC + sc * C::SC_BYTES + 2 * TILE);
-                        // Half a tile at a time, so that its weights are at work while the other half's are made.
+                        // Half a tile at a time: its weights are at work, and the next tile's scores of that half are made, beside the
+                        // other half's softmax.
                         auto publish = [&](int h, const uint32_t (&P)[32]) {
-                            tc_st_x32(s_at + 32 * h, P);
+                            tc_st_x32(s_at + 64 * h, P);
                             tc_wait_st();
                             tc_fence_before();
                             __syncwarp();
@@ -533,6 +537,7 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                         if (!fresh && !masked && !rowwise)
 #pragma unroll 1
                             for (; h < 2; ++h) {
+                                if (!scores_at(h)) break;
                                 uint32_t sa[32], sb[32], P[32];
                                 tc_ld_x32(s_at + h * 64, sa);
                                 tc_ld_x32(s_at + h * 64 + 32, sb);
@@ -544,11 +549,13 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                                 add_up();
                                 publish(h, P);
                             }
+                        if (!ok) break;
 #pragma unroll 1
                         for (; h < 2; ++h) {
                             const int seen = masked ? rel - 64 * h : TILE;   // columns of this half up to here are seen
                             const uint32_t sh = s_at + h * 64;
                             const uint4* kh = kf + 16 * h;
+                            if (!scores_at(h)) break;
                             uint32_t sa[32], sb[32], P[32];
                             tc_ld_x32(sh, sa);
                             tc_ld_x32(sh + 32, sb);
@@ -965,13 +972,12 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                 if (x.t1 == 0) break;
             }
         } else if (warp < 19) {
-            // -------------------------------------------------------- MMA issue: a warp for each buffer of S. Scores of an item (tile,
-            // row tile), both halves of its output, scores of the item after the next. (One warp for both has more to decide a
-            // step than the step's products take.) With one row tile a warp sees every second tile only: the ring of keys has an
+            // -------------------------------------------------------- MMA issue: a warp for each buffer of S, which items (tile, row tile)
+            // use in turn, half by half. (One warp for both has more to decide a step than the step's products take.) With one row tile a warp sees every second tile only: the ring of keys has an
             // even number of slots, so that the slot's fill before, from whose parity the next one's differs, was its own too.
             constexpr uint64_t KD = desc_base(C::ROWB == 128 ? 2 : 4, 8 * C::ROWB, 8 * C::ROWB);
             constexpr uint64_t VD = desc_base(2, C::VPANEL, 1024);
-            constexpr uint32_t ID_S = idesc_f8(TILE, TILE, 0, 0, 0), ID_PV = idesc_bf16(TILE, D);
+            constexpr uint32_t ID_S = idesc_f8(TILE, TILE / 2, 0, 0, 0), ID_PV = idesc_bf16(TILE, D);
             const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             // A descriptor's lower word changes, its upper one is constant. Lower words go through a shuffle, which leaves them
             // in uniform registers: an MMA then costs its issue and no moves of its operands (four words each, 80 clocks).
@@ -992,61 +998,42 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                 const int nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0), tiles = __shfl_sync(0xFFFFFFFFu, x.t1 - x.t0, 0);
                 const uint32_t last = item + tiles * nt;
                 if (mine < last && !warp_wait_at(bar(C::B_QFULL, piece % QB), (piece / QB) & 1, stop)) break;
-                // Waits for the keys of item n, and finds its operands.
+                // This buffer's halves of the part in a row: half z's output, then the scores of half z + 2, which take its place in TMEM.
+                const int halves = mine < last ? ((int)(last - mine) + 1) / 2 * 2 : 0;
+                const uint32_t n0 = mine - item;
+                // The second row tile begins when half of the first one's weights are there, and the groups then take turns at the
+                // softmax. (A few looks: whether it has begun, and not how often since, is all that the barrier can tell.)
+                if (nt == 2 && n0 == 1)
+                    for (int z = 0; z < STAGGER && !__all_sync(0xFFFFFFFFu, test_at(bar(C::B_PFULL, 2 * (1 - b)), (item >> 1) & 1)); ++z) {}
                 uint32_t k = 0, q = 0;
-                auto keys = [&](uint32_t n) {
+                auto keys = [&](uint32_t n) {        // waits for the keys of item n, and finds its operands
                     const uint32_t t = tile + (nt == 2 ? n >> 1 : n);
                     k = lower(KD, base + C::OFF_K + t % NK * C::KSLOT);
                     q = lower(KD, base + C::OFF_Q + (nt == 2 ? n & 1 : 0) * C::QTILE);
                     return warp_wait_at(bar(C::B_KFULL, t % NK), (t / NK) & 1, stop);
                 };
-                // The second row tile begins when half of the first one's weights are there, and the groups then take turns at the
-                // softmax. (A few looks: whether it has begun, and not how often since, is all that the barrier can tell.)
-                if (nt == 2 && mine == item + 1)
-                    for (int z = 0; z < STAGGER && !__all_sync(0xFFFFFFFFu, test_at(bar(C::B_PFULL, 2 * (1 - b)), (item >> 1) & 1)); ++z) {}
-                if (mine < last && !keys(mine - item)) break;
-                for (; mine < last; mine += 2) {
-                    const uint32_t n = mine - item;
-                    const int i = nt == 2 ? (int)n >> 1 : (int)n;
-                    // Q is free when all scores of the part are made, of both buffers
-                    const int frees = nt == 2 ? i == tiles - 1 : (i == tiles - 1) + (i == tiles - 2 || tiles == 1);
-                    tc_fence_after();
-                    // (the buffer's last P has been used by an output that this warp has issued before)
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < 2 * D / 32; ++kk) {
-                            constexpr int STEPS = C::ROWB / 32, HALF = D / 32;
-                            const int kq = kk % HALF;
-                            tc_mma_f8(s_tm, desc(KD, q + (((kq / STEPS) * C::QPANEL + (kk / HALF) * TILE * C::ROWB + (kq % STEPS) * 32) >> 4)),
-                                      desc(KD, k + (((kq / STEPS) * C::KPANEL + (kq % STEPS) * 32) >> 4)), ID_S, kk ? 1u : 0u);
-                        }
-                        commit_at(bar(C::B_SFULL, b));
-                        for (int z = nt; z < 3; ++z) commit_at(bar(C::B_KEMPTY, (tile + i) % NK));       // one row tile arrives for two
-                        for (int z = 0; z < frees; ++z) commit_at(bar(C::B_QFREE));
-                    }
-                    __syncwarp();
-                    const int r = nt == 2 ? (int)n & 1 : 0;
-                    const uint32_t t = tile + i;
-                    const uint32_t o = __shfl_sync(0xFFFFFFFFu, tm + C::TMEM_O + (C::NT == 2 && nt == 1 ? b : r) * D, 0);
-                    const bool first = C::NT == 2 ? n < 2 : n == 0;
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t bi = t * C::PIECES + h * PH;
-                        const uint32_t p = __shfl_sync(0xFFFFFFFFu, s_tm + h * 32, 0), add = __shfl_sync(0xFFFFFFFFu, first && h == 0 ? 0u : 1u, 0);
+                for (int z = -2; z < halves; ++z) {
+                    const int h = z & 1;
+                    // what the next scores need is found before the wait that the softmax ends
+                    if (C::NT == 2 && h == 0 && z + 2 < halves && !keys(n0 + z + 2)) { ok = false; break; }
+                    if (z >= 0) {
+                        const uint32_t n = n0 + (z & ~1), at = mine + (z & ~1);
+                        const uint32_t bi = (tile + (nt == 2 ? n >> 1 : n)) * C::PIECES + h * PH;
+                        const uint32_t o = __shfl_sync(0xFFFFFFFFu, tm + C::TMEM_O + (C::NT == 2 && nt == 1 ? b : nt == 2 ? n & 1 : 0) * D, 0);
+                        const uint32_t p = __shfl_sync(0xFFFFFFFFu, s_tm + h * 64, 0);
+                        const uint32_t add = __shfl_sync(0xFFFFFFFFu, (C::NT == 2 ? n < 2 : n == 0) && h == 0 ? 0u : 1u, 0);
                         uint32_t v[PH];
 #pragma unroll
                         for (int pc = 0; pc < PH; ++pc) v[pc] = lower(VD, base + C::OFF_B + (bi + pc) % NB * C::BSLOT);
-                        // What the next scores need is found before the wait that the softmax ends. (With a ring of two tiles those keys come
-                        // when this output is done.)
-                        if (C::NT == 2 && h == 1 && mine + 2 < last && !keys(n + 2)) { ok = false; break; }
                         // Outputs of one O add up in order: the other buffer's last is complete. (Its values then have arrived,
                         // without which the parity of the next ones' barriers would say nothing.)
-                        if (C::NT == 1 && h == 0 && mine > 0 &&
-                            (!warp_wait_at(bar(C::B_PFULL, 2 * b), (mine >> 1) & 1, stop) ||
-                             !warp_wait_at(bar(C::B_ODONE, 1 - b), ((mine - 1) >> 1) & 1, stop))) { ok = false; break; }
+                        if (C::NT == 1 && h == 0 && at > 0 &&
+                            (!warp_wait_at(bar(C::B_PFULL, 2 * b), (at >> 1) & 1, stop) ||
+                             !warp_wait_at(bar(C::B_ODONE, 1 - b), ((at - 1) >> 1) & 1, stop))) { ok = false; break; }
 #pragma unroll
                         for (int pc = 0; pc < PH; ++pc) ok = ok && warp_wait_at(bar(C::B_BFULL, (bi + pc) % NB), ((bi + pc) / NB) & 1, stop);
-                        if (!ok || !warp_wait_at(bar(C::B_PFULL, 2 * b + h), (mine >> 1) & 1, stop)) { ok = false; break; }
+                        if (!ok || !warp_wait_at(bar(C::B_PFULL, 2 * b + h), (at >> 1) & 1, stop)) { ok = false; break; }
                         tc_fence_after();
                         if (elect_one()) {
 #pragma unroll
@@ -1054,16 +1041,42 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
 #pragma unroll
                                 for (int kk = 0; kk < C::VR / 16; ++kk)
                                     tc_mma_f16_ts(o, p + pc * (C::VR / 2) + kk * 8, desc(VD, v[pc] + kk * (2048 >> 4)), ID_PV, pc == 0 && kk == 0 ? add : 1u);
-                                for (int z = nt; z < 3; ++z) commit_at(bar(C::B_BEMPTY, (bi + pc) % NB));
+                                for (int w = nt; w < 3; ++w) commit_at(bar(C::B_BEMPTY, (bi + pc) % NB));
                             }
                             commit_at(bar(h ? C::B_ODONE : C::B_OHALF, b));
                         }
                         __syncwarp();
+                        if (h) progress[b] = at;
+                    }
+                    // (With a ring of two tiles the next keys come when this output is done: both halves' scores after the second's.)
+                    const int end = z + 2 < halves ? z + 2 : -1;
+#pragma unroll 1
+                    for (int y = C::NT == 2 ? z + 2 : h ? z + 1 : z + 3; y <= end; ++y) {
+                        if (C::NT == 1 && !(y & 1) && !keys(n0 + y)) { ok = false; break; }
+                        const int n = (int)n0 + (y & ~1), i = nt == 2 ? n >> 1 : n;
+                        // Q is free when all scores of the part are made, of both buffers
+                        const int frees = nt == 2 ? i == tiles - 1 : (i == tiles - 1) + (i == tiles - 2 || tiles == 1);
+                        const uint32_t s_half = __shfl_sync(0xFFFFFFFFu, s_tm + (y & 1) * 64, 0), k_half = __shfl_sync(0xFFFFFFFFu, k + ((y & 1) * (64 * C::ROWB) >> 4), 0);
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < 2 * D / 32; ++kk) {
+                                constexpr int STEPS = C::ROWB / 32, HALF = D / 32;
+                                const int kq = kk % HALF;
+                                tc_mma_f8(s_half, desc(KD, q + (((kq / STEPS) * C::QPANEL + (kk / HALF) * TILE * C::ROWB + (kq % STEPS) * 32) >> 4)),
+                                          desc(KD, k_half + (((kq / STEPS) * C::KPANEL + (kq % STEPS) * 32) >> 4)), ID_S, kk ? 1u : 0u);
+                            }
+                            commit_at(bar(C::B_SFULL, 2 * b + (y & 1)));
+                            if (y & 1) {
+                                for (int w = nt; w < 3; ++w) commit_at(bar(C::B_KEMPTY, (tile + i) % NK));       // one row tile arrives for two
+                                for (int w = 0; w < frees; ++w) commit_at(bar(C::B_QFREE));
+                            }
+                        }
+                        __syncwarp();
                     }
                     if (!ok) break;
-                    if (C::NT == 1 && mine + 2 < last && !keys(n + 2)) { ok = false; break; }
-                    progress[b] = mine;
                 }
+                mine += halves;
                 item = last;
                 tile += tiles;
             }
