@@ -1196,7 +1196,8 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
 // ------------------------------------------------------------------ join
 
 // The parts of a unit that several CTAs share, added in the order of the cache rows. blockIdx.x + 1 is the first CTA whose
-// part begins inside the unit; 32 rows a block, a lane a row, a warp every eighth group of four columns.
+// part begins inside the unit; 32 rows a block, a lane a row, a warp an eighth of the columns: a lane's output is whole
+// sectors where it has 16 columns or more. The references come first, of all parts, and the sums need not wait for one another.
 constexpr int JOIN_WARPS = 8, JOIN_ROWS = 32;
 
 template <int D>
@@ -1207,52 +1208,82 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_attention_join(const __
     pdl_wait();
     const Pos* places = reinterpret_cast<const Pos*>(a.ws);
     const int k = blockIdx.x + 1;
-    const Pos p = places[k], q = places[k - 1];
-    if (p.lane >= a.lanes || p.tile == 0 || (same_unit(p, q) && q.tile > 0)) return;
-    const Unit x = unit_at<D>(a, p.lane, p.unit);
+    const Pos p = places[k], before_p = places[k - 1];
+    if (p.lane >= a.lanes || p.tile == 0 || (same_unit(p, before_p) && before_p.tile > 0)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y * JOIN_ROWS + lane;
+    // CTA k - 1 + i holds a part: one more in which the unit begins, and those that begin in it, but for CTAs without tiles
+    auto parts_from = [&](int i0, bool* more) {
+        const int c = k - 1 + i0 + lane;
+        bool in = i0 + lane == 0, some = in;
+        if (!in && c < ctas) {
+            const Pos here = places[c], next = places[c + 1];
+            in = same_unit(here, p);
+            some = in && !(same_unit(next, here) && next.tile == here.tile);
+        }
+        *more = __all_sync(0xFFFFFFFFu, in);
+        return __ballot_sync(0xFFFFFFFFu, some);
+    };
+    bool more;
+    const uint32_t first = parts_from(0, &more);
+    const Unit x = unit_at<D>(a, p.lane, p.unit);
     if ((int)blockIdx.y * JOIN_ROWS >= x.rows) return;
     const float* parts = reinterpret_cast<const float*>(a.ws + parts_offset(ctas));
-    constexpr int N = D / 4 / JOIN_WARPS;            // groups of columns of a thread
+    const int pieces = C::NT == 2 && x.nt == 1 ? 2 : 1;      // one row tile: what each of the two groups has added up
+    // f(references and sums of a part's piece, this row's place in it)
+    auto each = [&](auto f) {
+        uint32_t some = first;
+        bool on = more;
+        for (int i0 = 0;;) {
+            for (; some; some &= some - 1) {
+                const int c = k - 1 + i0 + __ffs(some) - 1;
+                const float* part = parts + (size_t)(2 * c + (c == k - 1 ? 1 : 0)) * C::PART_FLOATS;
+                for (int z = 0; z < pieces; ++z) f(part, row + z * TILE);
+            }
+            if (!on) break;
+            i0 += 32;
+            some = parts_from(i0, &on);
+        }
+    };
+    float m = NEVER;
+    each([&](const float* part, int at) { m = fmaxf(m, part[ROWS * D + at]); });
+    constexpr int N = D / 4 / JOIN_WARPS;            // groups of four columns of a thread
     float4 acc[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float m = NEVER, l = 0.0f;
-    Pos here = p;
-    for (int c = k - 1; c < ctas; ++c) {
-        if (c >= k) {
-            here = places[c];
-            if (!same_unit(here, p)) break;
-            const Pos next = places[c + 1];
-            if (same_unit(next, here) && next.tile == here.tile) continue;           // a CTA without tiles
-        }
-        const float* part = parts + (size_t)(2 * c + (c == k - 1 ? 1 : 0)) * C::PART_FLOATS;
-        // one row tile: what each of the two groups has added up
-        for (int z = 0; z < (C::NT == 2 && x.nt == 1 ? 2 : 1); ++z) {
-            const int at = row + z * TILE;
-            const float mc = part[ROWS * D + at], lc = part[ROWS * D + ROWS + at];
-            if (row >= x.rows || (mc == NEVER && lc == 0.0f)) continue;      // nothing seen: no O either
-            const float mn = fmaxf(m, mc), f0 = ex2(m - mn), f1 = ex2(mc - mn);
-            l = l * f0 + lc * f1;
-            m = mn;
+    float l = 0.0f;
+    each([&](const float* part, int at) {
+        const float mc = part[ROWS * D + at], lc = part[ROWS * D + ROWS + at];
+        if (row >= x.rows || (mc == NEVER && lc == 0.0f)) return;            // nothing seen: no O either
+        float4 v[N];
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float4 v = *reinterpret_cast<const float4*>(part + ((size_t)(warp + e * JOIN_WARPS) * ROWS + at) * 4);
-                acc[e].x = acc[e].x * f0 + v.x * f1;
-                acc[e].y = acc[e].y * f0 + v.y * f1;
-                acc[e].z = acc[e].z * f0 + v.z * f1;
-                acc[e].w = acc[e].w * f0 + v.w * f1;
-            }
+        for (int e = 0; e < N; ++e) v[e] = *reinterpret_cast<const float4*>(part + ((size_t)(warp * N + e) * ROWS + at) * 4);
+        const float f = ex2(mc - m);
+        l += lc * f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            acc[e].x += v[e].x * f;
+            acc[e].y += v[e].y * f;
+            acc[e].z += v[e].z * f;
+            acc[e].w += v[e].w * f;
         }
-    }
+    });
     if (row >= x.rows) return;
     const int t = (int)((uint32_t)row * a.by_group >> 16);
     const int64_t to = (int64_t)(x.tok0 + t) * a.n_q + x.h * a.group + row - t * a.group;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint32_t o[2 * N];
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-        *reinterpret_cast<uint2*>(a.out + to * D + (warp + e * JOIN_WARPS) * 4) =
-            make_uint2(pack_bf16(acc[e].x * inv, acc[e].y * inv), pack_bf16(acc[e].z * inv, acc[e].w * inv));
+    for (int e = 0; e < N; ++e) {
+        o[2 * e] = pack_bf16(acc[e].x * inv, acc[e].y * inv);
+        o[2 * e + 1] = pack_bf16(acc[e].z * inv, acc[e].w * inv);
+    }
+    __nv_bfloat16* dst = a.out + to * D + warp * N * 4;
+    if constexpr (N == 2) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 2 * N; e += 8) store_32(dst + 2 * e, o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
+    }
     if (a.lse && warp == 0) a.lse[to] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
