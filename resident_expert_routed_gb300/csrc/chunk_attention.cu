@@ -557,6 +557,12 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                             const uint4* kh = kf + 16 * h;
                             if (!scores_at(h)) break;
                             uint32_t sa[32], sb[32], P[32];
+                            if (!fresh && __all_sync(0xFFFFFFFFu, seen < 0)) {       // behind the edge of all 32 rows
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) P[e] = 0u;
+                                publish(h, P);
+                                continue;
+                            }
                             tc_ld_x32(sh, sa);
                             tc_ld_x32(sh + 32, sb);
                             tc_wait_ld();
