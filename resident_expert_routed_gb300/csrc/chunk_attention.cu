@@ -788,32 +788,42 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                 if (!warp_wait_at(bar(C::B_QFREE), (n - 1) & 1, stop)) return false;
                 fetch(x);
             }
+            constexpr int AT_ONCE = D > 64 ? 2 : 1;      // prompts of 8192, 1 / 2 / 4: head_dim 128 484 / 479 / 518 us, 256 1060 / 1031 / 1049, 64 (24 of 1024) 158 / 167 / 175
 #pragma unroll 1
-            for (int r = 0; r < rounds; ++r) {
-                const int u = r * STEP + mine;
-                const uint4 raw = *reinterpret_cast<const uint4*>(smem + row_at(u) + raw_at);
-                const uint32_t key = rowwise ? keys[u] : 0u;
-                __syncwarp();
-                const int up = rowwise ? up_of(key) : unit_up;
-                const float gain = exp2_int(up);
-                const f32x2 gain2 = pack2(gain, gain);
-                const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-                uint32_t hi[4], lo[4];
+            for (int r = 0; r < rounds; r += AT_ONCE) {
+                uint4 raw[AT_ONCE];
+                uint32_t key[AT_ONCE];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // a scaled bf16 value is exact in fp16 (down to 2^-16, far below what lo resolves)
-                    const float2 v = unpack2(mul2(pack2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xFFFF0000u)), gain2));
-                    const __half2 vh = __floats2half2_rn(v.x, v.y);
-                    hi[e] = __nv_cvt_halfraw2_to_fp8x2(vh, __NV_SATFINITE, __NV_E4M3);
-                    const __half2 rest = __hsub2(vh, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3)));
-                    lo[e] = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
+                for (int z = 0; z < AT_ONCE; ++z) {
+                    const int u = (r + z) * STEP + mine;
+                    raw[z] = *reinterpret_cast<const uint4*>(smem + row_at(u) + raw_at);
+                    key[z] = rowwise ? keys[u] : 0u;
                 }
-                // a row that is not finite: its scores become NaN
-                if (rowwise && part == 0) qf[u] = key >= 0x7F80u ? __uint_as_float(0x7FC00000u) : exp2_int(-up);
-                const int swz = C::ROWB == 128 ? u & 7 : (u >> 1) & 3;
-                uint8_t* to = smem + row_at(u) + panel * C::QPANEL + ((chunk ^ swz) << 4) + (part & 1) * 8;
-                *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(hi[0], hi[1], 0x5410), __byte_perm(hi[2], hi[3], 0x5410));
-                *reinterpret_cast<uint2*>(to + TILE * C::ROWB) = make_uint2(__byte_perm(lo[0], lo[1], 0x5410), __byte_perm(lo[2], lo[3], 0x5410));
+                __syncwarp();
+#pragma unroll
+                for (int z = 0; z < AT_ONCE; ++z) {
+                    const int u = (r + z) * STEP + mine;
+                    const int up = rowwise ? up_of(key[z]) : unit_up;
+                    const float gain = exp2_int(up);
+                    const f32x2 gain2 = pack2(gain, gain);
+                    const uint32_t in[4] = {raw[z].x, raw[z].y, raw[z].z, raw[z].w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        // a scaled bf16 value is exact in fp16 (down to 2^-16, far below what lo resolves)
+                        const float2 v = unpack2(mul2(pack2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xFFFF0000u)), gain2));
+                        const __half2 vh = __floats2half2_rn(v.x, v.y);
+                        hi[e] = __nv_cvt_halfraw2_to_fp8x2(vh, __NV_SATFINITE, __NV_E4M3);
+                        const __half2 rest = __hsub2(vh, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3)));
+                        lo[e] = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
+                    }
+                    // a row that is not finite: its scores become NaN
+                    if (rowwise && part == 0) qf[u] = key[z] >= 0x7F80u ? __uint_as_float(0x7FC00000u) : exp2_int(-up);
+                    const int swz = C::ROWB == 128 ? u & 7 : (u >> 1) & 3;
+                    uint8_t* to = smem + row_at(u) + panel * C::QPANEL + ((chunk ^ swz) << 4) + (part & 1) * 8;
+                    *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(hi[0], hi[1], 0x5410), __byte_perm(hi[2], hi[3], 0x5410));
+                    *reinterpret_cast<uint2*>(to + TILE * C::ROWB) = make_uint2(__byte_perm(lo[0], lo[1], 0x5410), __byte_perm(lo[2], lo[3], 0x5410));
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
