@@ -67,10 +67,11 @@ constexpr int WHOLE_TILES = 8;                   // a table of at most so many t
 constexpr float NEVER = -1e30f;                  // the reference of a row that has seen nothing
 constexpr float LIMIT = 8.0f;                    // log2 of the largest weight before the reference moves
 
-// The run's measure: a cache row of a unit with two row tiles, of one with one; a unit beside its rows.
-constexpr int FULL_COST = 4, HALF_COST = 3, UNIT_COST = 1536;
+// The run's measure: a cache row of a unit with two row tiles, of one with one (200 single tokens beside three chunks of 500,
+// 64 query heads, for 2 / 3 / 4: 642 / 615 / 759 us). A unit beside its rows: see Cfg.
+constexpr int FULL_COST = 4, HALF_COST = 3;
 constexpr int STAGGER = 20;                      // looks
-constexpr int LEAST_PART = 2048;                 // of a part
+constexpr int LEAST_PART = 2048;                 // of a part (half or twice as much: no difference)
 
 struct Pos {                                     // a place in the run
     int lane, unit, tile, pad;
@@ -94,6 +95,9 @@ struct Cfg {
     static constexpr int NT = D <= 128 ? 2 : 1;               // row tiles of a unit
     static constexpr int ROWS = NT * TILE;
     static constexpr int THREADS = 640;
+    // For 1536 / 2048 / 2560, us: head_dim 128, a prompt of 8192 tokens 480 / 456 / 459, 22 single tokens and 11 chunks over
+    // prefixes 264 / 238 / 234; head_dim 64, a prompt 361 / 366 / 369; head_dim 256, 1033 / 1056 / 1074. (1024: 517, 388, 1115)
+    static constexpr int UNIT_COST = D == 128 ? 2560 : 1536;
     static constexpr int ROWB = D >= 128 ? 128 : 64;          // bytes of an operand row of keys and queries: one swizzle atom
     static constexpr int PANELS = D / ROWB;
     static constexpr int KPANEL = TILE * ROWB, KSLOT = TILE * D;
@@ -310,7 +314,7 @@ MOE_DEV LaneCost lane_cost(const ChunkArgs& a, const Lane& l) {
     }
     const int left = (l.n - (c.blocks - 1) * a.block) * a.group;
     const int w = Cfg<D>::NT == 2 && left <= TILE ? HALF_COST : FULL_COST;
-    c.base = c.last = UNIT_COST;
+    c.base = c.last = Cfg<D>::UNIT_COST;
     if (l.len > 0) {
         c.base += (long long)FULL_COST * (l.len - l.n);
         c.step = (long long)FULL_COST * a.block;
@@ -363,10 +367,10 @@ __device__ __noinline__ void cut_run(const ChunkArgs& a, unsigned long long* scr
             }
             int tile = 0;
             const unsigned long long in = rest - c.upto(lo);
-            if (!a.whole && in > UNIT_COST) {
+            if (!a.whole && in > Cfg<D>::UNIT_COST) {
                 const int left = (l.n - lo * a.block) * a.group;
                 const int w = Cfg<D>::NT == 2 && left <= TILE ? HALF_COST : FULL_COST;
-                tile = (int)((uint32_t)((in - UNIT_COST) / TILE) / (uint32_t)w);
+                tile = (int)((uint32_t)((in - Cfg<D>::UNIT_COST) / TILE) / (uint32_t)w);
             }
             here[z] = Pos{b0 + tid, h * c.blocks + lo, tile, 0};
         }
