@@ -126,7 +126,8 @@ struct Cfg {
     static constexpr int OFF_QX = OFF_QU + QB * 8;            // [2][largest, smallest][8 warps]
     static constexpr int NPD = 4;                             // parts that are told ahead
     static constexpr int OFF_PD = OFF_QX + 128;
-    static constexpr int OFF_BAR = OFF_PD + NPD * (int)sizeof(Part);
+    static constexpr int OFF_ML = OFF_PD + NPD * (int)sizeof(Part);       // [2][TILE] references and sums that the groups tell one another
+    static constexpr int OFF_BAR = OFF_ML + (NT == 2 ? 2 * TILE * 8 : 0);
     static constexpr int B_KFULL = OFF_BAR;                   // [NK] a tile of keys has arrived
     static constexpr int B_KEMPTY = B_KFULL + 8 * NK;         // [NK] ... has been used
     static constexpr int B_RFULL = B_KEMPTY + 8 * NK;         // [NR] a piece of values has arrived
@@ -144,9 +145,8 @@ struct Cfg {
     static constexpr int B_QMAX = B_QFREE + 8;                // the four warps have their maxima
     static constexpr int B_PDFULL = B_QMAX + 8;               // [NPD] a part is told
     static constexpr int B_PDEMPTY = B_PDFULL + 8 * NPD;      // [NPD] ... and read by the other nineteen warps
-    static constexpr int B_MERGE = B_PDEMPTY + 8 * NPD;       // group 1's share of a unit with one row tile is laid down
-    static constexpr int B_MFREE = B_MERGE + 8;               // ... and read
-    static constexpr int B_DONE = B_MFREE + 8;                 // the block's last output is written
+    static constexpr int B_MERGE = B_PDEMPTY + 8 * NPD;       // of a part with one row tile: both groups' O stands; it is read
+    static constexpr int B_DONE = B_MERGE + 8;                // the block's last output is written
     static constexpr int B_DRAIN = B_DONE + 8;
     static constexpr int OFF_MISC = (B_DRAIN + 16 + 15) / 16 * 16;    // tmem slot, abort flag, progress [3] and one more, start, end
     static constexpr int SMEM = OFF_MISC + 32 + 32 + 1024;
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
         init(C::B_KFULL, NK, 1); init(C::B_KEMPTY, NK, 2); init(C::B_RFULL, NR, 1); init(C::B_REMPTY, NR, 4);
         init(C::B_BFULL, NB, 4); init(C::B_BEMPTY, NB, 2); init(C::B_SCFULL, NSC, 1); init(C::B_SCEMPTY, NSC, 16);
         init(C::B_SFULL, 4, 1); init(C::B_PFULL, 4, 4); init(C::B_OHALF, 2, 1); init(C::B_ODONE, 2, 1); init(C::B_QFULL, QB, 8); init(C::B_QFREE, 1, 2);
-        init(C::B_QMAX, 1, 8); init(C::B_PDFULL, C::NPD, 1); init(C::B_PDEMPTY, C::NPD, 19); init(C::B_MERGE, 1, 4); init(C::B_MFREE, 1, 4); init(C::B_DONE, 1, 8); init(C::B_DRAIN, 2, 1);
+        init(C::B_QMAX, 1, 8); init(C::B_PDFULL, C::NPD, 1); init(C::B_PDEMPTY, C::NPD, 19); init(C::B_MERGE, 1, 8); init(C::B_DONE, 1, 8); init(C::B_DRAIN, 2, 1);
         *abort_flag = 0;
         progress[0] = progress[1] = progress[2] = 0;
         fence_barrier_init();
@@ -450,7 +450,6 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
         const int g = warp >> 2, wl = warp & 3, j = tid & 127;
         const uint32_t trow = tmem + ((uint32_t)(wl * 32) << 16);
         uint32_t items = 0, tiles = 0, piece = 0;    // of the CTA: items (tile, row tile), tiles, parts
-        uint32_t merges = 0;                         // units whose O the groups have added up
         bool ok = true;
         Part x;
         while (ok && part_at(piece, x)) {
@@ -629,78 +628,76 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                     if (!fresh && !warp_wait_at(bar(C::B_ODONE, item & 1), (item >> 1) & 1, stop)) break;
                     tc_fence_after();
                     const bool live = row < x.rows, whole = t0 == 0 && t1 == x.tiles;
-                    // where this thread's row lies in a part, in the workspace
-                    float* part = reinterpret_cast<float*>(a.ws + parts_offset(gridDim.x)) + (size_t)(2 * blockIdx.x + (t0 > 0 ? 0 : 1)) * C::PART_FLOATS;
-                    const int at = split ? g * TILE + j : row;
-                    if (whole && (!split || g == 0)) {
-                        float f0 = 1.0f, f1 = 0.0f;
-                        if (split) {
-                            if (!warp_wait_at(bar(C::B_MERGE), merges & 1, stop)) break;
-                            const float m1 = part[ROWS * D + TILE + j], l1 = part[ROWS * D + ROWS + TILE + j];
-                            const float mn = fmaxf(m, m1);
-                            f0 = ex2(m - mn);
-                            f1 = m1 == NEVER && l1 == 0.0f ? 0.0f : ex2(m1 - mn);
-                            l = l * f0 + l1 * f1;
-                            m = mn;
-                        }
+                    float f0 = fresh ? 0.0f : 1.0f, f1 = 0.0f;       // factors of this group's O and of the other's
+                    if (split) {
+                        // One row, two O: in the same lanes of TMEM, where each group reads both, of half the columns.
+                        float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+                        ml[g * TILE + j] = make_float2(m, l);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_at(bar(C::B_MERGE));
+                        if (!warp_wait_at(bar(C::B_MERGE), 0, stop)) break;
+                        tc_fence_after();
+                        const float2 other = ml[(1 - g) * TILE + j];
+                        const float mn = fmaxf(m, other.x);
+                        if (m != NEVER || l != 0.0f) f0 = ex2(m - mn);
+                        if (other.x != NEVER || other.y != 0.0f) f1 = ex2(other.x - mn);
+                        const float mine = l * f0, theirs = other.y * f1;
+                        l = mine + theirs;
+                        m = mn;
+                    }
+                    float* part = nullptr;           // where this thread's row lies in a part, in the workspace
+                    uint4* dst = nullptr;            // or in the output
+                    if (whole) {
                         const int64_t to = (int64_t)(x.tok0 + t) * a.n_q + x.h * G + u - t * G;
                         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                        if (a.lse && live) a.lse[to] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                        if (a.lse && live && (!split || g == 0)) a.lse[to] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
                         f0 *= inv;
                         f1 *= inv;
-                        uint4* dst = reinterpret_cast<uint4*>(a.out + to * D);
-                        if (!split || __any_sync(0xFFFFFFFFu, live))
-#pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tc_load(o_at + c * 32, o);
-                                float v[32];
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) v[e] = fresh ? 0.0f : __uint_as_float(o[e]) * f0;
-                                if (split && f1 != 0.0f) {
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) {
-                                        const float4 w = *reinterpret_cast<const float4*>(part + ((size_t)(c * 8 + e) * ROWS + TILE + j) * 4);
-                                        v[4 * e] += w.x * f1;
-                                        v[4 * e + 1] += w.y * f1;
-                                        v[4 * e + 2] += w.z * f1;
-                                        v[4 * e + 3] += w.w * f1;
-                                    }
-                                }
-                                if (live)
-#pragma unroll
-                                    for (int e = 0; e < 32; e += 16)
-                                        store_32(dst + c * 4 + e / 8, pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]), pack_bf16(v[e + 4], v[e + 5]),
-                                                 pack_bf16(v[e + 6], v[e + 7]), pack_bf16(v[e + 8], v[e + 9]), pack_bf16(v[e + 10], v[e + 11]),
-                                                 pack_bf16(v[e + 12], v[e + 13]), pack_bf16(v[e + 14], v[e + 15]));
-                            }
-                        if (split) {
-                            __syncwarp();
-                            if (lane == 0) arrive_at(bar(C::B_MFREE));
-                        }
+                        dst = reinterpret_cast<uint4*>(a.out + to * D);
                     } else {
-                        // (group 1's rows may still be read for the last unit that was added up)
-                        if (g == 1 && merges > 0 && !warp_wait_at(bar(C::B_MFREE), (merges - 1) & 1, stop)) break;
-                        if (live) {
-                            part[ROWS * D + at] = m;
-                            part[ROWS * D + ROWS + at] = l;
-                        }
-                        if (!fresh && (!split || __any_sync(0xFFFFFFFFu, live)))
-#pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tc_load(o_at + c * 32, o);
-                                if (live)
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e)
-                                        *reinterpret_cast<uint4*>(part + ((size_t)(c * 8 + e) * ROWS + at) * 4) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                            }
-                        if (whole) {
-                            __syncwarp();
-                            if (lane == 0) arrive_at(bar(C::B_MERGE));
+                        part = reinterpret_cast<float*>(a.ws + parts_offset(gridDim.x)) + (size_t)(2 * blockIdx.x + (t0 > 0 ? 0 : 1)) * C::PART_FLOATS;
+                        if (live && (!split || g == 0)) {
+                            part[ROWS * D + row] = m;
+                            part[ROWS * D + ROWS + row] = l;
                         }
                     }
-                    if (whole && split) ++merges;
+                    // (A factor of 0: nothing has been added up there. A row without a weight has zeros.)
+                    const int cn = split ? D / 64 : D / 32, c0 = split ? g * cn : 0;
+                    if (__any_sync(0xFFFFFFFFu, live))
+#pragma unroll 1
+                        for (int c = c0; c < c0 + cn; ++c) {
+                            uint32_t o[32];
+                            __syncwarp();
+                            tc_load(o_at + c * 32, o);
+                            float v[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = f0 == 0.0f ? 0.0f : __uint_as_float(o[e]) * f0;
+                            if (split) {
+                                tc_load(trow + C::TMEM_O + (1 - g) * D + c * 32, o);
+                                if (f1 != 0.0f)
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(o[e]), f1, v[e]);
+                            }
+                            if (live && whole) {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 16)
+                                    store_32(dst + c * 4 + e / 8, pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]), pack_bf16(v[e + 4], v[e + 5]),
+                                             pack_bf16(v[e + 6], v[e + 7]), pack_bf16(v[e + 8], v[e + 9]), pack_bf16(v[e + 10], v[e + 11]),
+                                             pack_bf16(v[e + 12], v[e + 13]), pack_bf16(v[e + 14], v[e + 15]));
+                            } else if (live) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    *reinterpret_cast<float4*>(part + ((size_t)(c * 8 + e) * ROWS + row) * 4) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                            }
+                        }
+                    if (split) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_at(bar(C::B_MERGE));
+                        if (!warp_wait_at(bar(C::B_MERGE), 1, stop)) break;
+                        tc_fence_after();
+                    }
                     tc_fence_before();
                     if (lane == 0 && wl == 0 && g == 0) progress[2] = piece + 1;
                 }
@@ -1248,8 +1245,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_attention_join(const __
     const Unit x = unit_at<D>(a, p.lane, p.unit);
     if ((int)blockIdx.y * JOIN_ROWS >= x.rows) return;
     const float* parts = reinterpret_cast<const float*>(a.ws + parts_offset(ctas));
-    const int pieces = C::NT == 2 && x.nt == 1 ? 2 : 1;      // one row tile: what each of the two groups has added up
-    // f(references and sums of a part's piece, this row's place in it)
+    // f(each part)
     auto each = [&](auto f) {
         uint32_t some = first;
         bool on = more;
@@ -1257,7 +1253,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_attention_join(const __
             for (; some; some &= some - 1) {
                 const int c = k - 1 + i0 + __ffs(some) - 1;
                 const float* part = parts + (size_t)(2 * c + (c == k - 1 ? 1 : 0)) * C::PART_FLOATS;
-                for (int z = 0; z < pieces; ++z) f(part, row + z * TILE);
+                f(part);
             }
             if (!on) break;
             i0 += 32;
@@ -1265,18 +1261,18 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_attention_join(const __
         }
     };
     float m = NEVER;
-    each([&](const float* part, int at) { m = fmaxf(m, part[ROWS * D + at]); });
+    each([&](const float* part) { m = fmaxf(m, part[ROWS * D + row]); });
     constexpr int N = D / 4 / JOIN_WARPS;            // groups of four columns of a thread
     float4 acc[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float l = 0.0f;
-    each([&](const float* part, int at) {
-        const float mc = part[ROWS * D + at], lc = part[ROWS * D + ROWS + at];
+    each([&](const float* part) {
+        const float mc = part[ROWS * D + row], lc = part[ROWS * D + ROWS + row];
         if (row >= x.rows || (mc == NEVER && lc == 0.0f)) return;            // nothing seen: no O either
         float4 v[N];
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = *reinterpret_cast<const float4*>(part + ((size_t)(warp * N + e) * ROWS + at) * 4);
+        for (int e = 0; e < N; ++e) v[e] = *reinterpret_cast<const float4*>(part + ((size_t)(warp * N + e) * ROWS + row) * 4);
         const float f = ex2(mc - m);
         l += lc * f;
 #pragma unroll
