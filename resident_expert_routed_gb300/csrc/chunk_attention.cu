@@ -994,7 +994,7 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
             // even number of slots, so that the slot's fill before, from whose parity the next one's differs, was its own too.
             constexpr uint64_t KD = desc_base(C::ROWB == 128 ? 2 : 4, 8 * C::ROWB, 8 * C::ROWB);
             constexpr uint64_t VD = desc_base(2, C::VPANEL, 1024);
-            constexpr uint32_t ID_S = idesc_f8(TILE, TILE / 2, 0, 0, 0), ID_PV = idesc_bf16(TILE, D);
+            constexpr uint32_t ID_S = idesc_f8(TILE, C::NT == 2 ? TILE / 2 : TILE, 0, 0, 0), ID_PV = idesc_bf16(TILE, D);
             const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             // A descriptor's lower word changes, its upper one is constant. Lower words go through a shuffle, which leaves them
             // in uniform registers: an MMA then costs its issue and no moves of its operands (four words each, 80 clocks).
@@ -1065,15 +1065,16 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                         __syncwarp();
                         if (h) progress[b] = at;
                     }
-                    // (With a ring of two tiles the next keys come when this output is done: both halves' scores after the second's.)
-                    const int end = z + 2 < halves ? z + 2 : -1;
-#pragma unroll 1
-                    for (int y = C::NT == 2 ? z + 2 : h ? z + 1 : z + 3; y <= end; ++y) {
-                        if (C::NT == 1 && !(y & 1) && !keys(n0 + y)) { ok = false; break; }
+                    // (With one row tile to a unit the next keys come when this output is done: the scores of a whole tile after its
+                    // second half's. Products of 128 columns read the queries once, of 64 twice.)
+                    const int y = z + 2;
+                    if (y < halves && (C::NT == 2 || h)) {
                         const int n = (int)n0 + (y & ~1), i = nt == 2 ? n >> 1 : n;
+                        if (C::NT == 1 && !keys(n)) { ok = false; break; }
                         // Q is free when all scores of the part are made, of both buffers
                         const int frees = nt == 2 ? i == tiles - 1 : (i == tiles - 1) + (i == tiles - 2 || tiles == 1);
-                        const uint32_t s_half = __shfl_sync(0xFFFFFFFFu, s_tm + (y & 1) * 64, 0), k_half = __shfl_sync(0xFFFFFFFFu, k + ((y & 1) * (64 * C::ROWB) >> 4), 0);
+                        const uint32_t s_half = __shfl_sync(0xFFFFFFFFu, s_tm + (C::NT == 2 ? h * 64 : 0), 0);
+                        const uint32_t k_half = __shfl_sync(0xFFFFFFFFu, k + (C::NT == 2 ? h * (64 * C::ROWB) >> 4 : 0), 0);
                         tc_fence_after();
                         if (elect_one()) {
 #pragma unroll
@@ -1083,15 +1084,15 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                                 tc_mma_f8(s_half, desc(KD, q + (((kq / STEPS) * C::QPANEL + (kk / HALF) * TILE * C::ROWB + (kq % STEPS) * 32) >> 4)),
                                           desc(KD, k_half + (((kq / STEPS) * C::KPANEL + (kq % STEPS) * 32) >> 4)), ID_S, kk ? 1u : 0u);
                             }
-                            commit_at(bar(C::B_SFULL, 2 * b + (y & 1)));
-                            if (y & 1) {
+                            if (C::NT == 1) commit_at(bar(C::B_SFULL, 2 * b));
+                            commit_at(bar(C::B_SFULL, 2 * b + h));
+                            if (h) {
                                 for (int w = nt; w < 3; ++w) commit_at(bar(C::B_KEMPTY, (tile + i) % NK));       // one row tile arrives for two
                                 for (int w = 0; w < frees; ++w) commit_at(bar(C::B_QFREE));
                             }
                         }
                         __syncwarp();
                     }
-                    if (!ok) break;
                 }
                 mine += halves;
                 item = last;
