@@ -63,7 +63,10 @@ struct ChunkMaps {
 };
 
 constexpr int TILE = 128;                        // cache rows a tile, and rows a row tile
-constexpr int WHOLE_TILES = 8;                   // a table of at most so many tiles: units are not cut
+// Units are not cut, and no parts joined, where the table has at most SHORT_TILES tiles (cut / whole: 40 prompts of 300 tokens
+// 134 / 132 us, 9 of 600 87 / 83), or WHOLE_TILES and there are at most two full units an SM (a prompt of 1024 43 / 33, two
+// 56 / 54, 200 single tokens over 1000 182 / 165; but three prompts 66 / 74, eight 134 / 144; a prompt of 2048 67 / 81).
+constexpr int SHORT_TILES = 5, WHOLE_TILES = 8;
 constexpr float NEVER = -1e30f;                  // the reference of a row that has seen nothing
 constexpr float LIMIT = 8.0f;                    // log2 of the largest weight before the reference moves
 
@@ -103,7 +106,7 @@ struct Cfg {
     static constexpr int KPANEL = TILE * ROWB, KSLOT = TILE * D;
     static constexpr int QPANEL = 2 * TILE * ROWB, QTILE = 2 * TILE * D;      // hi, then lo
     // Rings have even numbers of slots: see MMA issue, and the groups that convert, of which each takes every second piece.
-    static constexpr int NK = D == 64 ? 8 : 2;                // ring of key tiles
+    static constexpr int NK = D == 64 ? 4 : 2;                // ring of key tiles
     static constexpr int VR = D == 256 ? 32 : 64;             // values come in pieces of so many rows
     static constexpr int PIECES = TILE / VR;
     static constexpr int NR = D == 64 ? 8 : D == 128 ? 6 : 2; // ring of pieces as codes
@@ -843,8 +846,11 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
             const uint8_t* bytes = smem + C::OFF_SC + sc * C::SC_BYTES + TILE + pc * C::VR;
             constexpr int EACH = C::VR * D / 16 / 128;                       // 16 codes at once, of a thread
             const int left = x.end - t * TILE - pc * C::VR;                  // rows that somebody sees; what lies behind is anything
-            // (one after the other: two or four at once cost more in instruction fetches than they save)
-#pragma unroll 1
+            // One after the other: two or four at once cost more in instruction fetches than they save (1 / 2 / 4: a prompt of 8192 tokens
+            // 457 / 459 / 468 us, 24 prompts of 1024 at head_dim 64 158 / 163 / 163). Not so at head_dim 256, where a tile of values serves
+            // 128 rows alone: 1057 / 1074 / 988, 1024 tokens over 30,000 1125 / 1145 / 1053.
+            constexpr int AT_ONCE = D == 256 ? 4 : 1;
+#pragma unroll AT_ONCE
             for (int e = 0; e < EACH; ++e) {
                 // Eight neighbours take four places of a row in one panel of 64 columns and four of the next row in the
                 // next panel: all on different banks, where they read and where they write.
@@ -1321,9 +1327,11 @@ cudaError_t codes_map(CUtensorMap* m, const void* base, const moe_kv_cache& c, i
 template <int D>
 cudaError_t launch(ChunkArgs a, cudaStream_t s) {
     using C = Cfg<D>;
-    // Few units that are not cut: of one row tile each, for twice as many CTAs.
-    const int64_t heads = a.c.n_kv_heads, rows = (int64_t)a.n_tokens * a.group;
-    a.block = (C::NT == 2 && a.whole && (rows + C::ROWS - 1) / C::ROWS * heads * 2 <= moe_sm_count() ? TILE : C::ROWS) / a.group;
+    const int64_t tiles = ((int64_t)a.width * a.c.page_size + TILE - 1) / TILE;
+    const int64_t units = ((int64_t)a.n_tokens * a.group + C::ROWS - 1) / C::ROWS * a.c.n_kv_heads;      // if they are full
+    a.whole = tiles <= SHORT_TILES || (tiles <= WHOLE_TILES && units <= 2 * moe_sm_count());
+    // Few units that are not cut: of one row tile each, for twice as many CTAs (300 tokens, 8 kv heads: 19 us, not 23).
+    a.block = (C::NT == 2 && a.whole && units * 2 <= moe_sm_count() ? TILE : C::ROWS) / a.group;
     ChunkMaps maps;
     cudaError_t e = codes_map(&maps.k, a.c.k_codes, a.c, C::ROWB, TILE, C::ROWB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     if (e == cudaSuccess) e = codes_map(&maps.v, a.c.v_codes, a.c, D, C::VR, CU_TENSOR_MAP_SWIZZLE_NONE);
@@ -1391,7 +1399,6 @@ moe_status moe_chunk_attention(const void* q, int64_t q_token_stride, int64_t q_
     a.page_shift = log2_of(cache->page_size);
     a.kv_len = kv_len;
     a.cu = cu_tokens;
-    a.whole = (int64_t)table_width * cache->page_size <= WHOLE_TILES * TILE;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
