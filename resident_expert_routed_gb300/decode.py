@@ -123,18 +123,20 @@ class Step:
             pages.reserve(b, n)
         self.counts, self.n_nodes, self.max_nodes = counts, sum(counts), max(1, max(counts))
         words = -(-self.max_nodes // 32)
+        trees = [tree_mask(p) for p in parents]
         mask = [[(bits >> 32 * w & 0xFFFFFFFF) - ((bits >> 32 * w & 0x80000000) << 1) for w in range(words)]
-                for p in parents for bits in tree_mask(p)]
+                for tree in trees for bits in tree]
         cu = [0]
         for n in counts:
             cu.append(cu[-1] + n)
         dev = lambda v, t=torch.int32: torch.tensor(v, dtype=t, device=device)  # noqa: E731
         self.table = pages.table.to(device, copy=True)       # (complete on return: the host's table may change at once)
-        self.prefix, self.cu = dev(pages.rows), dev(cu)
-        self.kv_len = dev([r + n for r, n in zip(pages.rows, counts)])
-        self.slots = dev([s for b, n in enumerate(counts) for s in pages.slots(b, n)], torch.int64)
         # a node's place in its lane's text: behind the prefix, as deep as it stands in the tree
-        self.positions = dev([r + bits.bit_count() - 1 for r, p in zip(pages.rows, parents) for bits in tree_mask(p)])
+        places = [r + bits.bit_count() - 1 for r, tree in zip(pages.rows, trees) for bits in tree]
+        lens = [r + n for r, n in zip(pages.rows, counts)]
+        self.prefix, self.kv_len, self.positions = dev(pages.rows + lens + places).split([len(lens), len(lens), len(places)])
+        self.cu = dev(cu)
+        self.slots = dev([s for b, n in enumerate(counts) for s in pages.slots(b, n)], torch.int64)
         self.mask = dev(mask).view(-1, words)
 
 
