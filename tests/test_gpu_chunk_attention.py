@@ -172,6 +172,20 @@ def test_a_long_prefix(D):
     run_and_check(Chunks([(30000, 140)], 4, 2, D, 128, seed=2), heads=[1, 2], tokens=30)
 
 
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64), (256, 128)])
+def test_units_of_one_row_tile_and_of_two_beside_one_another(D, page):
+    """Several units a block, of one tile of cache rows and of more, odd and even numbers of them."""
+    lanes = [((53 * i) % 700, (1, 70, 33, 140, 2, 129, 0, 64)[(3 * i + i // 8) % 8]) for i in range(150)]
+    run_and_check(Chunks(lanes, 8, 2, D, page, seed=24), heads=[0, 7], tokens=4)
+
+
+@pytest.mark.parametrize("lanes", [[(0, 1024)] * 3, [(0, 900)] * 4, [(0, 640)] * 5, [(0, 1024)] * 2])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_several_prompts(lanes, D):
+    """Of five to eight tiles, more and fewer units than twice the SMs: cut and not cut."""
+    run_and_check(Chunks(lanes, 32, 8, D, 128, seed=25), heads=[0, 13, 31], tokens=6)
+
+
 def test_a_whole_prompt():
     run_and_check(Chunks([(0, 3000)], 8, 2, 128, 64, seed=3), heads=[0, 5], tokens=200)
 
