@@ -560,10 +560,11 @@ moe_status moe_page_plan(const int32_t* n_new, int32_t* rows, int32_t* held, int
  * factor that some rules for long contexts ask for).
  * q, q_out [n_tokens, n_q_heads, head_dim], k, k_out [n_tokens, n_k_heads,
  * head_dim] of `dtype` (MOE_BF16 ..), last axis contiguous; strides int64 [8], a
- * HOST array, elements: token and head strides of q, k, q_out, k_out. Pointers are 16-byte
- * aligned and strides multiples of 16 bytes. An output may be its input, with the same
- * strides; otherwise nothing overlaps. positions int32 [n_tokens]; q_weight,
- * k_weight fp32 [head_dim], 16-byte aligned, or NULL. One of the two head counts may be 0.
+ * HOST array, elements: token and head strides of q, k, q_out, k_out. Pointers are
+ * 16-byte aligned and strides multiples of 16 bytes. An output may be its input,
+ * with the same strides; otherwise nothing overlaps. positions int32 [n_tokens];
+ * q_weight, k_weight fp32 [head_dim], 16-byte aligned, or NULL. One of the two head
+ * counts may be 0.
  * Sums are fp32 (values above 2^60 in size overflow the mean square); one rounding.
  * n_tokens = 0 returns MOE_OK without a launch. Limits: head_dim 64, 128 or 256,
  * n_pairs a multiple of 8, up to half of head_dim (0: norms alone); heads <= 65,536 each,
@@ -582,16 +583,27 @@ moe_status moe_qk_rotate(const void* q, const void* k, int dtype, const int64_t*
  *   score[j] = scale * q . k[j],   p = softmax of the scores of the rows seen
  *   out      = sum_j p[j] v[j],    lse = log sum_j exp(score[j])
  * Rows that a token does not see never touch its result, whatever they hold.
+ * Precision: scores, sums and lse are fp32, out is rounded to bf16 once.
+ *   - A query element is held exactly down to 2^-9 of the largest of its (token,
+ *     head) row, to 2^-17 of that below (to 2^-13 where rows of up to 2^4 times
+ *     its size are handled with it).
+ *   - A weight p[j] is rounded to bf16 for its product with v[j], by at most 2^-8
+ *     of itself; the sum takes it unrounded.
+ *   - A key or value vector marked as not finite (scale byte 255), and a value
+ *     vector with a scale byte above 246 (2^119; its values may pass bf16's range),
+ *     make NaN of the results that see it.
  * Arguments as for moe_tree_attention, without a bound on a lane's tokens and
- * without a mask; out is 32-byte aligned. A lane with fewer rows than tokens or more than its table
- * holds sets MOE_DEV_BAD_PAGE and gets zeros and lse = -inf; a page id outside
- * the cache sets it too, and page 0 is read in its place. Rows of q and out behind
- * cu_tokens[lanes] are left as they are.
- * workspace: >= moe_chunk_attention_workspace_bytes(...), 16-byte aligned; its
- * contents need not be kept or cleared between calls. Calls that overlap on
- * the GPU need one each.
+ * without a mask; out is 32-byte aligned. A lane with fewer rows than tokens or
+ * more than its table holds sets MOE_DEV_BAD_PAGE and gets zeros and lse = -inf; a
+ * page id outside the cache sets it too, and page 0 is read in its place; so does
+ * a lane whose tokens lead out of q, of which nothing is written. Rows of q and out
+ * behind cu_tokens[lanes] are left as they are.
+ * workspace: >= moe_chunk_attention_workspace_bytes(...) (20 MB at head_dim 64, 41
+ * MB at 128 and 256, on 152 SMs), 16-byte aligned; its contents need not be kept or
+ * cleared between calls. Calls that overlap on the GPU need one each.
  * scale > 0. n_tokens = 0 returns MOE_OK without a launch. Limits: lanes <= 4096,
- * kv_len <= 2^30 (a lane past it does not fit), n_tokens <= 2^24, n_q_heads a multiple of n_kv_heads, at most 1024 and 128 to a kv head.
+ * kv_len <= 2^30 (a lane past it does not fit), n_tokens <= 2^24, n_q_heads a
+ * multiple of n_kv_heads, at most 1024 and 128 to a kv head.
  */
 size_t     moe_chunk_attention_workspace_bytes(int n_tokens, int n_q_heads, int n_kv_heads, int head_dim, int lanes);
 moe_status moe_chunk_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int n_tokens,

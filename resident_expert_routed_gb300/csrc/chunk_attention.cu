@@ -11,16 +11,19 @@
 //     8-bit products cost what one of 16 bits costs, and no key is converted.
 //   - A key row's scale is the factor of its column of scores: one fused multiply-add takes it and the reference.
 //   - e4m3 codes times a power of two are exact in bf16, and bf16 has the exponents of fp32: weights and values
-//     need no care about their range. Four warps convert each tile of values once for the 256 rows that use it.
+//     need no care about their range. Eight warps convert each tile of values once for the 256 rows that use it.
 //   - m is a running reference, not each tile's maximum: it stays until a score passes it by 2^8 (p then up to 2^8, in
 //     bf16 as good as below 1), and only then O and the sum are scaled down. A thread has a row to itself, so neither
 //     maximum nor sum needs another thread.
-// Scores, sums, O and the parts that the join adds up are fp32; weights are rounded to bf16, the output once.
+// Scores, sums, O and the parts that the join adds up are fp32. Weights are rounded to bf16 for the second product, by at most
+// 2^-8 of each (the sum takes them before), far less than a value's own 2^-4; the output is rounded once.
 //
 // A unit is a block of 256 rows (128 at head_dim 256, where O fills TMEM) of a lane and kv head, whole tokens with all their
 // heads, so 256 / group tokens share each tile of the cache and the causal edge is as near as can be. Its tiles of cache
-// rows come one after the other; the two tiles of 128 rows take turns: while one's softmax runs, the other's products do.
-// A unit of at most 128 rows (single tokens among them) has one row tile and two buffers of S.
+// rows come one after the other; the two tiles of 128 rows take turns: while one's softmax runs, the other's products do, and
+// each works by halves of 64 cache rows: half's weights at work beside the other half's softmax, the next tile's scores of that
+// half behind them. A unit of at most 128 rows (single tokens among them) has one row tile and two buffers of S, which the two
+// groups of the softmax take in turn, each with an O of its own; the two are added up from TMEM at the end.
 //
 // Work: the units are laid end to end and cut into equal parts, one per CTA. A unit that one CTA does whole is written at
 // once; the others leave parts (O, reference, sum) in the workspace, and chunk_attention_join adds them up in order.
@@ -28,6 +31,16 @@
 // Roles, 20 warps: two softmax groups of four; two groups of four that convert pieces of values in turn and together prepare
 // queries; one warp that walks the run and issues TMA; one of MMA issue for each buffer of S; one of scales, which also
 // bounds all waits.
+//
+// What bounds it at head_dim 128: 128 cache rows take the two row tiles about 3,300 clocks, of which the tensor cores work
+// 2,050; shared memory moves 340 KB for them (2,650 clocks: keys for each row tile and half, values once in and out of the
+// conversion and for each row tile), and the softmax issues for 2,000 on each of the SM's four schedulers. 1,024 tokens over
+// 65,536 rows (32 / 8 heads) take 767 us, 1,445 TFLOP/s; over and over they draw 1.4 kW and the clock falls: 860 us. A prompt
+// of 8,192 takes 457 us, 1,200 TFLOP/s: the edge, a unit's first tile, its queries and its output, some 9 us a unit, are what
+// its 6.7 units a CTA pay. At head_dim 64 the softmax's and the issue's instructions bound it (a prompt 355 us), at 256 the conversion,
+// which serves 128 rows there, and shared memory (978 us). Single tokens over 8,192 rows, 64 lanes: 310 us, 3.5 TB/s, the conversion.
+// 300 tokens take 14 us, of which 3 to find the parts, 4 to bring and split the queries and 2 for a first tile's scores.
+// The instructions' cache is as scarce as anything: loops that are not unrolled, and code in one place, are faster in most places.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -68,12 +81,12 @@ constexpr int TILE = 128;                        // cache rows a tile, and rows 
 // 56 / 54, 200 single tokens over 1000 182 / 165; but three prompts 66 / 74, eight 134 / 144; a prompt of 2048 67 / 81).
 constexpr int SHORT_TILES = 5, WHOLE_TILES = 8;
 constexpr float NEVER = -1e30f;                  // the reference of a row that has seen nothing
-constexpr float LIMIT = 8.0f;                    // log2 of the largest weight before the reference moves
+constexpr float LIMIT = 8.0f;                    // log2 of the largest weight before the reference moves (4 or 16: no difference)
 
 // The run's measure: a cache row of a unit with two row tiles, of one with one (200 single tokens beside three chunks of 500,
 // 64 query heads, for 2 / 3 / 4: 642 / 615 / 759 us). A unit beside its rows: see Cfg.
 constexpr int FULL_COST = 4, HALF_COST = 3;
-constexpr int STAGGER = 20;                      // looks
+constexpr int STAGGER = 20;                      // looks (0 / 20 / 64: a prompt at head_dim 64 367 / 359 / 368 us, 24 of 1,024 152 / 158 / 171)
 constexpr int LEAST_PART = 2048;                 // of a part (half or twice as much: no difference)
 
 struct Pos {                                     // a place in the run
@@ -105,7 +118,10 @@ struct Cfg {
     static constexpr int PANELS = D / ROWB;
     static constexpr int KPANEL = TILE * ROWB, KSLOT = TILE * D;
     static constexpr int QPANEL = 2 * TILE * ROWB, QTILE = 2 * TILE * D;      // hi, then lo
-    // Rings have even numbers of slots: see MMA issue, and the groups that convert, of which each takes every second piece.
+    // Rings have even numbers of slots: see MMA issue, and the groups that convert, of which each takes every second piece. What
+    // fits beside the queries: at head_dim 128 four slots of codes instead of six 480 us a prompt for 457, pieces of 32 rows 491; at
+    // 64 eight key tiles 158 us for 24 prompts of 1,024, for 150, four pieces in bf16 367 a prompt for 359; at 256 pieces of 16 rows 1203
+    // for 1025, three slots of codes for both groups together 1176.
     static constexpr int NK = D == 64 ? 4 : 2;                // ring of key tiles
     static constexpr int VR = D == 256 ? 32 : 64;             // values come in pieces of so many rows
     static constexpr int PIECES = TILE / VR;
@@ -145,7 +161,7 @@ struct Cfg {
     static constexpr int B_ODONE = B_OHALF + 16;              // [2] both: a tile is added to O
     static constexpr int B_QFULL = B_ODONE + 16;              // [QB] the queries of a part are there
     static constexpr int B_QFREE = B_QFULL + 8 * QB;              // ... have been used
-    static constexpr int B_QMAX = B_QFREE + 8;                // the four warps have their maxima
+    static constexpr int B_QMAX = B_QFREE + 8;                // the eight warps have their maxima
     static constexpr int B_PDFULL = B_QMAX + 8;               // [NPD] a part is told
     static constexpr int B_PDEMPTY = B_PDFULL + 8 * NPD;      // [NPD] ... and read by the other nineteen warps
     static constexpr int B_MERGE = B_PDEMPTY + 8 * NPD;       // of a part with one row tile: both groups' O stands; it is read
@@ -792,7 +808,8 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                 if (!warp_wait_at(bar(C::B_QFREE), (n - 1) & 1, stop)) return false;
                 fetch(x);
             }
-            constexpr int AT_ONCE = D > 64 ? 2 : 1;      // prompts of 8192, 1 / 2 / 4: head_dim 128 484 / 479 / 518 us, 256 1060 / 1031 / 1049, 64 (24 of 1024) 158 / 167 / 175
+            // 1 / 2 / 4: a prompt of 8192 tokens 484 / 479 / 518 us, at head_dim 256 1060 / 1031 / 1049; 24 of 1024 at 64 158 / 167 / 175
+            constexpr int AT_ONCE = D > 64 ? 2 : 1;
 #pragma unroll 1
             for (int r = 0; r < rounds; r += AT_ONCE) {
                 uint4 raw[AT_ONCE];
@@ -996,8 +1013,9 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
             }
         } else if (warp < 19) {
             // -------------------------------------------------------- MMA issue: a warp for each buffer of S, which items (tile, row tile)
-            // use in turn, half by half. (One warp for both has more to decide a step than the step's products take.) With one row tile a warp sees every second tile only: the ring of keys has an
-            // even number of slots, so that the slot's fill before, from whose parity the next one's differs, was its own too.
+            // use in turn, half by half. (One warp for both has more to decide a step than the step's products take.) With one row
+            // tile a warp sees every second tile only: the ring of keys has an even number of slots, so that the slot's fill before,
+            // from whose parity the next one's differs, was its own too.
             constexpr uint64_t KD = desc_base(C::ROWB == 128 ? 2 : 4, 8 * C::ROWB, 8 * C::ROWB);
             constexpr uint64_t VD = desc_base(2, C::VPANEL, 1024);
             constexpr uint32_t ID_S = idesc_f8(TILE, C::NT == 2 ? TILE / 2 : TILE, 0, 0, 0), ID_PV = idesc_bf16(TILE, D);

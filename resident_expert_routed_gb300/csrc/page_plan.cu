@@ -11,7 +11,8 @@
 // Nothing here is large (12 bytes a token), so the launch and the chain of
 // dependent steps bound it. One launch: a cluster of up to eight CTAs, each of which
 // does the sums for itself and takes its share of the tokens; the cluster's barriers
-// keep the state's old values until all have read them.
+// keep the state's old values until all have read them. One after the other in a
+// graph: two lanes of one token 3.1 us, 256 lanes of 9 tokens 6.3, 48 of 1,000 8.6.
 #include <climits>
 
 #include "common.cuh"
@@ -19,7 +20,8 @@
 namespace {
 
 constexpr int PLAN_THREADS = 1024;
-constexpr int PLAN_MAX_LANES = 4096, PLAN_MAX_CTAS = 8;
+constexpr int PLAN_MAX_LANES = 4096;
+constexpr int PLAN_MAX_CTAS = 8;            // 1 / 4 / 8: 48 lanes of 1,000 tokens 32.3 / 12.4 / 8.6 us, 4,096 lanes of 4 28.3 / 17.7 / 15.9
 
 struct PlanArgs {
     const int32_t* n_new;
