@@ -32,14 +32,15 @@
 // queries; one warp that walks the run and issues TMA; one of MMA issue for each buffer of S; one of scales, which also
 // bounds all waits.
 //
-// What bounds it at head_dim 128: 128 cache rows take the two row tiles about 3,300 clocks, of which the tensor cores work
-// 2,050; shared memory moves 340 KB for them (2,650 clocks: keys for each row tile and half, values once in and out of the
-// conversion and for each row tile), and the softmax issues for 2,000 on each of the SM's four schedulers. 1,024 tokens over
-// 65,536 rows (32 / 8 heads) take 767 us, 1,445 TFLOP/s; over and over they draw 1.4 kW and the clock falls: 860 us. A prompt
-// of 8,192 takes 457 us, 1,200 TFLOP/s: the edge, a unit's first tile, its queries and its output, some 9 us a unit, are what
-// its 6.7 units a CTA pay. At head_dim 64 the softmax's and the issue's instructions bound it (a prompt 355 us), at 256 the conversion,
-// which serves 128 rows there, and shared memory (978 us). Single tokens over 8,192 rows, 64 lanes: 310 us, 3.5 TB/s, the conversion.
-// 300 tokens take 14 us, of which 3 to find the parts, 4 to bring and split the queries and 2 for a first tile's scores.
+// What bounds it at head_dim 128: 128 cache rows take the two row tiles about 3,300 clocks, and shared memory is busy for nearly
+// all of them: 336 KB of operands (2,690 clocks: the queries and keys once for each row tile and half 192 KB, values for each row
+// tile 64, through the conversion 48, copies 32) and 512 reads of the columns' factors. The tensor cores work 2,050 of them, the
+// softmax issues for 2,000 on each of the SM's four schedulers. 1,024 tokens over 65,536 rows (32 / 8 heads) take 767 us, 1,445
+// TFLOP/s; over and over they draw 1.4 kW and the clock falls: 855 us. A prompt of 8,192 takes 457 us, 1,200 TFLOP/s: the edge,
+// a unit's first tile, its queries and its output, some 9 us a unit, are what its 6.7 units a CTA pay. At head_dim 64 the
+// instructions of softmax and issue bound it (a prompt 355 us), at 256 the conversion, which serves 128 rows there, and shared
+// memory (978 us). Single tokens over 8,192 rows, 64 lanes: 310 us, 3.5 TB/s, the conversion. 300 tokens take 14 us, of which 3 to
+// find the parts, 4 to bring and split the queries and 2 for a first tile's scores.
 // The instructions' cache is as scarce as anything: loops that are not unrolled, and code in one place, are faster in most places.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
