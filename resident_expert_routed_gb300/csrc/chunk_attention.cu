@@ -16,7 +16,8 @@
 //     bf16 as good as below 1), and only then O and the sum are scaled down. A thread has a row to itself, so neither
 //     maximum nor sum needs another thread.
 // Scores, sums, O and the parts that the join adds up are fp32. Weights are rounded to bf16 for the second product, by at most
-// 2^-8 of each (the sum takes them before), far less than a value's own 2^-4; the output is rounded once.
+// 2^-8 of each (the sum takes them before), far less than a value's own 2^-4; calls of few rows take what is left of them as a
+// second part (FEW_ROWS), to 2^-16. The output is rounded once.
 //
 // A unit is a block of 256 rows (128 at head_dim 256, where O fills TMEM) of a lane and kv head, whole tokens with all their
 // heads, so 256 / group tokens share each tile of the cache and the causal edge is as near as can be. Its tiles of cache
@@ -81,6 +82,11 @@ constexpr int TILE = 128;                        // cache rows a tile, and rows 
 // 134 / 132 us, 9 of 600 87 / 83), or WHOLE_TILES and there are at most two full units an SM (a prompt of 1024 43 / 33, two
 // 56 / 54, 200 single tokens over 1000 182 / 165; but three prompts 66 / 74, eight 134 / 144; a prompt of 2048 67 / 81).
 constexpr int SHORT_TILES = 5, WHOLE_TILES = 8;
+// Calls with at most so many rows (token, query head) have their weights in two bf16 parts: with so few, one part's roundings, which
+// are as large as the output's own, do not always average out to less (error against 64 bits up to 1.55 times that of fp32
+// rounded once, over 60 rows; 1.3 to 1.4 over many). One token in 30 lanes, 2 heads of 64 over 10,476 rows: 53 us in two
+// parts, 46 in one; 32 / 8 heads of 128 over 8,192 rows 165 / 145; 8 tokens over 300 rows 14 / 14.
+constexpr int FEW_ROWS = 1024;
 constexpr float NEVER = -1e30f;                  // the reference of a row that has seen nothing
 constexpr float LIMIT = 8.0f;                    // log2 of the largest weight before the reference moves (4 or 16: no difference)
 
@@ -413,7 +419,7 @@ __device__ __noinline__ void cut_run(const ChunkArgs& a, unsigned long long* scr
     }
 }
 
-template <int D>
+template <int D, bool TWO>                       // TWO: weights in two parts
 __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkArgs a) {
     using C = Cfg<D>;
     constexpr int NK = C::NK, NR = C::NR, NB = C::NB, NSC = C::NSC, QB = C::QB, ROWS = C::ROWS;
@@ -510,8 +516,7 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                         const uint4* kf = reinterpret_cast<const uint4*>(smem + C::OFF_SC + sc * C::SC_BYTES + 2 * TILE);
                         // Half a tile at a time: its weights are at work, and the next tile's scores of that half are made, beside the
                         // other half's softmax.
-                        auto publish = [&](int h, const uint32_t (&P)[32]) {
-                            tc_st_x32(s_at + 64 * h, P);
+                        auto publish = [&](int h) {
                             tc_wait_st();
                             tc_fence_before();
                             __syncwarp();
@@ -542,6 +547,7 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                                     sum0 = add2(sum0, pack2(p0, p1));
                                 }
                                 P[e] = pack_bf16(p0, p1);
+                                if constexpr (TWO) P[16 + e] = pack_bf16(p0 - __uint_as_float(P[e] << 16), p1 - __uint_as_float(P[e] & 0xFFFF0000u));
                             }
                         };
                         auto clear = [&]() {
@@ -557,20 +563,32 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                         // Most tiles: no edge, no factor of the row's, the reference stays. (A form of its own: with branches within, the
                         // scores are copied from where the loads leave them, two moves a pair. A loop, though the second half's scores
                         // could come ahead: the instructions' cache is as scarce.)
+                        // 32 columns' weights, with their second parts behind
+                        auto store_two = [&](const uint32_t* P, uint32_t to) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+                                tc_st_x8(to + (e & 8) + (e & 16) * 2, make_uint4(P[e], P[e + 1], P[e + 2], P[e + 3]), make_uint4(P[e + 4], P[e + 5], P[e + 6], P[e + 7]));
+                        };
                         if (!fresh && !masked && !rowwise)
 #pragma unroll 1
                             for (; h < 2; ++h) {
                                 if (!scores_at(h)) break;
-                                uint32_t sa[32], sb[32], P[32];
+                                uint32_t sa[32], sb[32], P[TWO ? 64 : 32];
                                 tc_ld_x32(s_at + h * 64, sa);
                                 tc_ld_x32(s_at + h * 64 + 32, sb);
                                 tc_wait_ld();
                                 clear();
                                 weights(std::true_type{}, sa, P, kf + 16 * h, m, 0);
-                                weights(std::true_type{}, sb, P + 16, kf + 16 * h + 8, m, 0);
+                                weights(std::true_type{}, sb, P + (TWO ? 32 : 16), kf + 16 * h + 8, m, 0);
                                 if (passes()) break;
                                 add_up();
-                                publish(h, P);
+                                if constexpr (TWO) {
+                                    store_two(P, s_at + 64 * h);
+                                    store_two(P + 32, s_at + 64 * h + 16);
+                                } else {
+                                    tc_st_x32(s_at + 64 * h, P);
+                                }
+                                publish(h);
                             }
                         if (!ok) break;
 #pragma unroll 1
@@ -583,7 +601,9 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                             if (!fresh && __all_sync(0xFFFFFFFFu, seen < 0)) {       // behind the edge of all 32 rows
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) P[e] = 0u;
-                                publish(h, P);
+                                tc_st_x32(sh, P);
+                                if constexpr (TWO) tc_st_x32(sh + 32, P);
+                                publish(h);
                                 continue;
                             }
                             tc_ld_x32(sh, sa);
@@ -628,7 +648,15 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                                 }
                                 clear();
                                 weights(std::false_type{}, sa, P, kh, m, seen);
-                                weights(std::false_type{}, sb, P + 16, kh + 8, m, seen - 32);
+                                if constexpr (TWO) {
+                                    // (the scores are in registers: their place may be taken before it is known that these weights stay)
+                                    store_two(P, sh);
+                                    weights(std::false_type{}, sb, P, kh + 8, m, seen - 32);
+                                    store_two(P, sh + 16);
+                                } else {
+                                    weights(std::false_type{}, sb, P + 16, kh + 8, m, seen - 32);
+                                    tc_st_x32(sh, P);
+                                }
                                 // (scores of 2^27 and more may pass the limit by their rounding alone)
                                 move = passes();
                                 if (moved || !move) {
@@ -637,7 +665,7 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                                 }
                             }
                             if (!ok) break;
-                            publish(h, P);
+                            publish(h);
                             fresh = false;
                         }
                         if (!ok) break;
@@ -1083,6 +1111,10 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
 #pragma unroll
                                 for (int kk = 0; kk < C::VR / 16; ++kk)
                                     tc_mma_f16_ts(o, p + pc * (C::VR / 2) + kk * 8, desc(VD, v[pc] + kk * (2048 >> 4)), ID_PV, pc == 0 && kk == 0 ? add : 1u);
+                                if constexpr (TWO)
+#pragma unroll
+                                    for (int kk = 0; kk < C::VR / 16; ++kk)
+                                        tc_mma_f16_ts(o, p + 32 + pc * (C::VR / 2) + kk * 8, desc(VD, v[pc] + kk * (2048 >> 4)), ID_PV, 1u);
                                 for (int w = nt; w < 3; ++w) commit_at(bar(C::B_BEMPTY, (bi + pc) % NB));
                             }
                             commit_at(bar(h ? C::B_ODONE : C::B_OHALF, b));
@@ -1355,17 +1387,19 @@ cudaError_t launch(ChunkArgs a, cudaStream_t s) {
     cudaError_t e = codes_map(&maps.k, a.c.k_codes, a.c, C::ROWB, TILE, C::ROWB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     if (e == cudaSuccess) e = codes_map(&maps.v, a.c.v_codes, a.c, D, C::VR, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e != cudaSuccess) return e;
-    static bool attr_set[64] = {};
+    const bool few = (int64_t)a.n_tokens * a.n_q <= FEW_ROWS;
+    const auto kernel = few ? chunk_attention<D, true> : chunk_attention<D, false>;
+    static bool attr_set[2][64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
-    if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        e = cudaFuncSetAttribute(chunk_attention<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (dev >= 0 && dev < 64 && !attr_set[few][dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
-        attr_set[dev] = true;
+        attr_set[few][dev] = true;
     }
     const int ctas = moe_sm_count();
     moe_prof_begin(MK_CHUNK_ATTENTION, s);
-    e = moe_launch(chunk_attention<D>, dim3((unsigned)ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
+    e = moe_launch(kernel, dim3((unsigned)ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
     moe_prof_end(MK_CHUNK_ATTENTION, s);
     moe_count_launches(1);
     if (e != cudaSuccess || ctas < 2 || a.whole) return e;

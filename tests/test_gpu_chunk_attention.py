@@ -73,7 +73,8 @@ class Chunks:
         codes, scales = (ref.lane_rows(x, self.table[b], n)[:, h] for x in self.pool[i:i + 2])
         return ref.values(codes, scales)
 
-    def check(self, out, lse=None, heads=None, tokens=None):
+    def check(self, out, lse=None, heads=None, tokens=None, weight=2.0 ** -8):
+        """weight: half a step of a weight's rounding; in two parts, half a step of what the first leaves, and twice the sums."""
         G = self.Hq // self.Hkv
         for b, (p, n) in enumerate(self.lanes):
             if not n:
@@ -103,7 +104,7 @@ class Chunks:
                     d = held + (self.D + 8) * U * mags + 8 * U
                 got = out[rows, h].double().cpu().numpy()
                 assert np.array_equal(np.isnan(got), np.isnan(o)), (b, h)
-                tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2 * d[:, None] + (p + n) / 16 * U) * mass * (1 + 2.0 ** -6) + 1e-30
+                tol = 2.0 ** -8 * np.abs(o) + (weight + 2 * d[:, None] + (p + n) / 16 * U * (1 if weight == 2.0 ** -8 else 2)) * mass * (1 + 2.0 ** -6) + 1e-30
                 off = np.abs(got - o)
                 fine = ~np.isnan(o)
                 assert (off[fine] <= tol[fine]).all(), (b, h, np.nanmax(off / tol))
@@ -184,6 +185,13 @@ def test_units_of_one_row_tile_and_of_two_beside_one_another(D, page):
 def test_several_prompts(lanes, D):
     """Of five to eight tiles, more and fewer units than twice the SMs: cut and not cut."""
     run_and_check(Chunks(lanes, 32, 8, D, 128, seed=25), heads=[0, 13, 31], tokens=6)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lanes,Hq,Hkv", [([(5000, 1)] * 30, 2, 2), ([(9000, 1), (70, 3), (0, 2)], 32, 8), ([(300, 100)], 8, 2), ([(0, 1024)], 1, 1),
+                                          ([(1500, 200)], 5, 1)])
+def test_few_rows_hold_their_weights_in_two_parts(lanes, Hq, Hkv, D):
+    run_and_check(Chunks(lanes, Hq, Hkv, D, 64, seed=26), weight=2.0 ** -16)
 
 
 def test_a_whole_prompt():
