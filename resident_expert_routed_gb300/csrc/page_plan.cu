@@ -198,7 +198,8 @@ moe_status moe_page_plan(const int32_t* n_new, int32_t* rows, int32_t* held, int
                      kv_len, cu_tokens, positions, slots, err};
     const size_t smem = (size_t)5 * lanes * sizeof(int);
     cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(page_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, 5 * PLAN_MAX_LANES * (int)sizeof(int));
+    // (48 KB need no opt-in, but the block's static shared memory is among them)
+    if (smem > 40 * 1024) e = cudaFuncSetAttribute(page_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, 5 * PLAN_MAX_LANES * (int)sizeof(int));
     if (e != cudaSuccess) return MOE_ECUDA;
     // threads for the lanes and the tokens; more CTAs where a thread would take more than two tokens
     int threads = (lanes > max_tokens ? lanes : max_tokens) + 31;
