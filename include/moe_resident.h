@@ -538,8 +538,12 @@ moe_status moe_tree_attention(const void* q, int64_t q_token_stride, int64_t q_h
  *              the last and for refused lanes
  * kv_len and cu_tokens go to moe_chunk_attention as they are. Calling again with
  * the same n_new, before rows has moved on, gives the same answer.
- * A stack outside 0 .. n_pages, negative rows, held outside the table or a page id
- * outside the pool set MOE_DEV_BAD_PAGE; such a lane is refused.
+ * A stack outside 0 .. n_pages, negative rows and held outside the table set
+ * MOE_DEV_BAD_PAGE; such a lane is refused. So does a page id outside the pool that
+ * a lane's new tokens would come to lie on, of its table or of the stack: the lane's
+ * kv_len is 0, none of its tokens gets a slot and its rows stay, but pages that it
+ * took stay with it until it is done. (Pages of rows before are not looked at here;
+ * the attention checks those that it reads.)
  * No two of the arrays overlap. Limits: lanes <= 4096, table_width <= 2^20,
  * max_tokens <= 2^24, page_size a power of two, 16..1024, n_pages * page_size < 2^31.
  */

@@ -10,9 +10,11 @@
 //
 // Nothing here is large (12 bytes a token), so the launch and the chain of
 // dependent steps bound it. One launch: a cluster of up to eight CTAs, each of which
-// does the sums for itself and takes its share of the tokens; the cluster's barriers
-// keep the state's old values until all have read them. One after the other in a
-// graph: two lanes of one token 3.1 us, 256 lanes of 9 tokens 6.3, 48 of 1,000 8.6.
+// does the sums for itself and takes its share of the tokens; the cluster's first
+// barrier keeps the state's old values until all have read them, the second (0.1 to
+// 0.5 us) tells all whether a lane has met a page id outside the pool. One after the
+// other in a graph: two lanes of one token 3.2 us, 256 lanes of 9 tokens 6.8, 48 of
+// 1,000 9.1.
 #include <climits>
 
 #include "common.cuh"
@@ -21,7 +23,7 @@ namespace {
 
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_MAX_LANES = 4096;
-constexpr int PLAN_MAX_CTAS = 8;            // 1 / 4 / 8: 48 lanes of 1,000 tokens 32.3 / 12.4 / 8.6 us, 4,096 lanes of 4 28.3 / 17.7 / 15.9
+constexpr int PLAN_MAX_CTAS = 8;            // 1 / 4 / 8, before the second barrier: 48 lanes of 1,000 tokens 32.3 / 12.4 / 8.6 us, 4,096 lanes of 4 28.3 / 17.7 / 15.9
 
 struct PlanArgs {
     const int32_t* n_new;
@@ -41,7 +43,16 @@ struct PlanArgs {
 typedef unsigned long long u64;
 
 MOE_DEV void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Sets a flag in shared memory of a block of the cluster.
+MOE_DEV void tell_block(int* flag, int rank) {
+    asm volatile(
+        "{\n\t.reg .u32 at;\n\t"
+        "mapa.shared::cluster.u32 at, %0, %1;\n\t"
+        "st.shared::cluster.u32 [at], 1;\n\t}" ::"r"(smem_u32(flag)), "r"(rank) : "memory");
 }
 
 // The first index in [0, n) with upto[index] > x; n where there is none.
@@ -64,6 +75,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan(const PlanArgs a) {
     int* rows = back + B;                   // [B] the lane's rows; ~rows where it is refused
     int* held = rows + B;                   // [B]
     __shared__ u64 scratch[64];
+    __shared__ int spoilt;                  // some token's page is none of the pool's
+    if (tid == 0) spoilt = 0;
     pdl_trigger();
     pdl_wait();
     int n_free = a.n_free[0];
@@ -119,6 +132,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan(const PlanArgs a) {
             if (!served) rows[b] = ~rows[b];
             if (rows[b] < 0 && a.n_new[b] > 0) bad |= MOE_DEV_NO_PAGES;
             got[b] = (int)g;                                                    // pages given to the lanes up to this one
+            if (rank == 0) a.kv_len[b] = a.n_new[b] < 0 || rows[b] < 0 ? 0 : rows[b] + a.n_new[b];
         }
     }
     if (bad && rank == 0) record_error(a.err, bad);
@@ -134,9 +148,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan(const PlanArgs a) {
     // ---- from here on the state changes, and nobody reads its old values
     if (rank == 0) {
         for (int b = tid; b < B; b += nt) {
-            const int n = a.n_new[b], h = held[b], r = rows[b];
+            const int n = a.n_new[b], h = held[b];
             a.cu[b + 1] = tok[b];
-            a.kv_len[b] = n < 0 || r < 0 ? 0 : r + n;
             if (n < 0) {
                 a.rows[b] = 0;
                 a.held[b] = 0;
@@ -170,14 +183,27 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan(const PlanArgs a) {
             if (r >= 0) {
                 const int p = pos >> a.page_shift, h = held[b];
                 const int id = p < h ? a.table[(int64_t)b * a.width + p] : a.free_pages[there - 1 - ((b ? got[b - 1] : 0) + p - h)];
-                if (id >= 0 && id < a.n_pages) slot = (int64_t)id * page + (pos & (page - 1));
-                else lost = true;
+                if (id >= 0 && id < a.n_pages) {
+                    slot = (int64_t)id * page + (pos & (page - 1));
+                } else {
+                    lost = true;
+                    a.kv_len[b] = 0;
+                }
             }
         }
         a.positions[t] = pos;
         a.slots[t] = slot;
     }
-    if (lost) record_error(a.err, MOE_DEV_BAD_PAGE);
+    // A lane with an id outside the pool among its tokens' pages is refused as a whole: whichever block met it, those of its
+    // tokens that have got slots on other pages lose them.
+    if (lost) {
+        record_error(a.err, MOE_DEV_BAD_PAGE);
+        for (int r = 0; r < ranks; ++r) tell_block(&spoilt, r);
+    }
+    if (ranks > 1) cluster_sync(); else __syncthreads();
+    if (spoilt)
+        for (int t = first; t < tokens; t += step)
+            if (__ldcg(a.kv_len + lane_of(tok, B, t)) == 0) a.slots[t] = -1;
 }
 
 }  // namespace

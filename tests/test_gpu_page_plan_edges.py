@@ -1,9 +1,13 @@
-"""Plans at the edges of their workspace."""
+"""Plans at the edges of their workspace, and states that cannot be served."""
 import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
+import torch
+
+from tests.test_gpu_page_plan import State
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +30,59 @@ print("planned")
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, env=dict(os.environ, PYTHONPATH=ROOT), capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "planned" in r.stdout, r.stdout + r.stderr
+
+
+def planned(s, new, T):
+    """(outputs and state as lists, status) of a call."""
+    got = s.gpu(new, T)
+    bits = moe.moe_device_status()[1]
+    return {k: v.cpu().numpy() for k, v in got.items()}, bits, got
+
+
+@pytest.mark.parametrize("n,held", [(5, True), (48, False), (3000, True), (3000, False)])
+def test_a_page_id_outside_the_pool_refuses_its_lane(n, held):
+    """In the lane's table, or on the stack when the lane takes it; few tokens and so many that several blocks plan them. The lane
+    gets kv_len 0 and no slots at all, though its other pages are good; the lanes around it are served."""
+    page, T = 16, 4 * n + 9
+    width = (20 + n) // page + 2
+    s = State(4, width, 4 * width + 4, page, seed=n, most=0)
+    ids = s.rng.permutation(4 * width + 4).astype(np.int32)
+    s.held[:], s.rows[:] = 2, 20                               # the second page is half full
+    s.table[:, :2] = ids[:8].reshape(4, 2)
+    s.free[:], s.n_free = -7, 4 * width - 4
+    s.free[:s.n_free] = ids[8:8 + s.n_free]
+    need = -(-(20 + n) // page) - 2
+    if held:
+        s.table[1, 1] = 4 * width + 4                          # the first id past the pool
+    else:
+        s.free[s.n_free - 1 - need - need // 2] = -2           # one that lane 1 takes
+    want, bits, got = planned(s, [n] * 4, T)
+    assert bits == moe.MOE_DEV_BAD_PAGE
+    assert want["kv_len"].tolist() == [20 + n, 0, 20 + n, 20 + n] and want["rows"].tolist() == [20] * 4
+    assert want["cu"].tolist() == [n * i for i in range(5)]
+    slots = want["slots"]
+    assert (slots[n:2 * n] == -1).all() and (slots[4 * n:] == -1).all()
+    for b in (0, 2, 3):
+        at = 20 + np.arange(n)
+        assert np.array_equal(slots[b * n:(b + 1) * n], want["table"][b, at // page].astype(np.int64) * page + at % page)
+        assert np.array_equal(want["positions"][b * n:(b + 1) * n], at)
+    # the pages that it took stay with it: again the same answer, and each page is in one place
+    assert want["held"].tolist() == [2 + need] * 4 and want["n_free"].tolist() == [s.n_free - 4 * need]
+    s.call(got)
+    torch.cuda.synchronize()
+    assert moe.moe_device_status()[1] == moe.MOE_DEV_BAD_PAGE
+    for name in ("rows", "held", "table", "n_free", "kv_len", "cu", "positions", "slots"):
+        assert np.array_equal(got[name].cpu().numpy(), want[name]), name
+
+
+def test_rows_of_a_lane_refused_for_its_pages_do_not_move_on():
+    from resident_expert_routed_gb300.decode import DevicePages
+    pages = DevicePages(3, 12, 16, 4, 64)
+    new = torch.tensor([10, 10, 10], dtype=torch.int32, device="cuda")
+    pages.plan(new)
+    pages.advance()
+    pages.table[1, 0] = 12
+    pages.plan(new)
+    assert moe.moe_device_status()[1] == moe.MOE_DEV_BAD_PAGE
+    pages.advance()
+    assert pages.rows.tolist() == [20, 10, 20] and pages.kv_len.tolist() == [20, 0, 20]
