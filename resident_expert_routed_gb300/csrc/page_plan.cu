@@ -104,10 +104,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan(const PlanArgs a) {
             tok[b] = (int)min(x, (u64)a.max_tokens);
             back[b] = (int)min(y, (u64)INT_MAX);
             held[b] = h;
-            fine &= x <= (u64)a.max_tokens;
+            if (n > 0) fine &= x <= (u64)a.max_tokens;                          // (a lane that waits fits any batch)
             const int64_t pages = ((int64_t)(fine ? r : 0) + (int64_t)own + (1 << a.page_shift) - 1) >> a.page_shift;
-            fine &= pages <= a.width;
-            rows[b] = fine || n <= 0 ? r : ~(r < 0 ? 0 : r);
+            if (n > 0) fine &= pages <= a.width;
+            rows[b] = fine ? r : ~(r < 0 ? 0 : r);
             got[b] = fine && n > 0 && pages > h ? (int)(pages - h) : 0;          // the need, for now
         }
     }

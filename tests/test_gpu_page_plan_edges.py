@@ -86,3 +86,20 @@ def test_rows_of_a_lane_refused_for_its_pages_do_not_move_on():
     assert moe.moe_device_status()[1] == moe.MOE_DEV_BAD_PAGE
     pages.advance()
     assert pages.rows.tolist() == [20, 10, 20] and pages.kv_len.tolist() == [20, 0, 20]
+
+
+def test_a_waiting_lane_whose_state_is_bad_is_refused_too():
+    """Pages outside the table, or negative rows: kv_len 0, as for a lane that gets tokens. A waiting lane behind tokens that do not
+    fit the batch is not refused: it has none."""
+    for rows, held in ((20, 9), (20, -1), (-4, 2)):
+        s = State(3, 4, 20, 16, seed=2, most=2)
+        s.rows[:], s.held[:] = 20, 2
+        s.table[:, :2] = np.arange(6).reshape(3, 2)
+        s.free[:14], s.n_free = np.arange(6, 20), 14
+        s.rows[1], s.held[1] = rows, held
+        want, bits, _ = planned(s, [3, 0, 0], 8)
+        assert bits == moe.MOE_DEV_BAD_PAGE and want["kv_len"].tolist() == [23, 0, 20], (rows, held)
+        assert want["rows"][1] == rows and want["held"][1] == held
+    s.rows[:], s.held[:] = 20, 2
+    want, bits, _ = planned(s, [3, 30, 0], 8)
+    assert bits == moe.MOE_DEV_NO_PAGES and want["kv_len"].tolist() == [23, 0, 20]
