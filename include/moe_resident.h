@@ -598,10 +598,11 @@ moe_status moe_qk_rotate(const void* q, const void* k, int dtype, const int64_t*
  *     vector with a scale byte above 246 (2^119; its values may pass bf16's range),
  *     make NaN of the results that see it.
  * Arguments as for moe_tree_attention, without a bound on a lane's tokens and
- * without a mask; out is 32-byte aligned. A lane with fewer rows than tokens or
- * more than its table holds sets MOE_DEV_BAD_PAGE and gets zeros and lse = -inf; a
- * page id outside the cache sets it too, and page 0 is read in its place; so does
- * a lane whose tokens lead out of q, of which nothing is written. Rows of q and out
+ * without a mask; out is 32-byte aligned. A lane with tokens and kv_len 0 (one that
+ * moe_page_plan refused) gets zeros and lse = -inf; that is no error. Any other lane
+ * with fewer rows than tokens, or more than its table holds, gets them too and sets
+ * MOE_DEV_BAD_PAGE. So do a page id outside the cache, in whose place page 0 is read,
+ * and a lane whose tokens lead out of q, of which nothing is written. Rows of q and out
  * behind cu_tokens[lanes] are left as they are.
  * workspace: >= moe_chunk_attention_workspace_bytes(...) (20 MB at head_dim 64, 41
  * MB at 128 and 256, on 152 SMs), 16-byte aligned; its contents need not be kept or

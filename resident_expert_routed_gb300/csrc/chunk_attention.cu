@@ -256,8 +256,8 @@ MOE_DEV void arrive_at_n(uint32_t bar, uint32_t n) {
 
 // ------------------------------------------------------------------ lanes, units, the cut
 
-// A lane that does not fit (see the header): no rows, and its outputs become zeros; one whose tokens would lead out of q
-// has none either.
+// A lane that does not fit (see the header): no rows, and its outputs become zeros; so too, though not bad, one of no rows
+// with tokens, as a plan refuses it. One whose tokens would lead out of q has none of them either.
 struct Lane {
     int n0, n, len;
 };
@@ -270,7 +270,7 @@ MOE_DEV Lane lane_facts(const ChunkArgs& a, int b, bool* bad) {
     if (l.n0 < 0 || l.n < 0 || l.n > a.n_tokens - l.n0) {
         *bad = true;
         l.n0 = l.n = l.len = 0;
-    } else if (l.n > 0 && (l.len < l.n || l.len > 1 << 30 || (((int64_t)l.len + (1 << a.page_shift) - 1) >> a.page_shift) > a.width)) {
+    } else if (l.n > 0 && l.len != 0 && (l.len < l.n || l.len > 1 << 30 || (((int64_t)l.len + (1 << a.page_shift) - 1) >> a.page_shift) > a.width)) {
         *bad = true;
         l.len = 0;
     }
