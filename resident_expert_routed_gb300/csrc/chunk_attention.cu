@@ -87,7 +87,7 @@ constexpr int SHORT_TILES = 5, WHOLE_TILES = 8;
 // rounded once, over 60 rows; 1.3 to 1.4 over many). One token in 30 lanes, 2 heads of 64 over 10,476 rows: 53 us in two
 // parts, 46 in one; 32 / 8 heads of 128 over 8,192 rows 165 / 145; 8 tokens over 300 rows 14 / 14.
 constexpr int FEW_ROWS = 1024;
-constexpr float NEVER = -1e30f;                  // the reference of a row that has seen nothing
+constexpr float NEVER = -3.402823466e38f;        // the reference of a row that has seen nothing: below any finite score
 constexpr float LIMIT = 8.0f;                    // log2 of the largest weight before the reference moves (4 or 16: no difference)
 
 // The run's measure: a cache row of a unit with two row tiles, of one with one (200 single tokens beside three chunks of 500,
