@@ -153,7 +153,8 @@ struct Cfg {
     static constexpr int NPD = 4;                             // parts that are told ahead
     static constexpr int OFF_PD = OFF_QX + 128;
     static constexpr int OFF_ML = OFF_PD + NPD * (int)sizeof(Part);       // [2][TILE] references and sums that the groups tell one another
-    static constexpr int OFF_BAR = OFF_ML + (NT == 2 ? 2 * TILE * 8 : 0);
+    static constexpr int OFF_ONE = OFF_ML + (NT == 2 ? 2 * TILE * 8 : 0);        // [32] 1
+    static constexpr int OFF_BAR = OFF_ONE + 128;
     static constexpr int B_KFULL = OFF_BAR;                   // [NK] a tile of keys has arrived
     static constexpr int B_KEMPTY = B_KFULL + 8 * NK;         // [NK] ... has been used
     static constexpr int B_RFULL = B_KEMPTY + 8 * NK;         // [NR] a piece of values has arrived
@@ -451,6 +452,7 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
         prefetch_tmap(&maps.v);
     }
     if (warp == 17) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
+    if (tid < 32) *reinterpret_cast<float*>(smem + C::OFF_ONE + tid * 4) = 1.0f;
     pdl_wait();
     cut_run<D>(a, reinterpret_cast<unsigned long long*>(smem + C::OFF_Q), ends);      // (the queries' room, not yet in use)
     tc_fence_before();
@@ -525,13 +527,13 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                         // 32 columns of scores to weights
                         f32x2 sum0, sum1;
                         float top0, top1;
-                        auto weights = [&](auto plain, uint32_t (&s)[32], uint32_t* P, const uint4* k8, float m, int seen) {
+                        auto weights = [&](auto plain, uint32_t (&s)[32], uint32_t* P, const uint4* k8, f32x2 f2, float m, int seen) {
                             const f32x2 m2 = pack2(-m, -m);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 const uint4 kk = k8[e / 2];
                                 f32x2 y = pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-                                if constexpr (!plain) y = mul2_loaded(y, rf2);
+                                if constexpr (!plain) y = mul2_loaded(y, f2);
                                 y = fma2_loaded(y, e & 1 ? pack2(__uint_as_float(kk.z), __uint_as_float(kk.w)) : pack2(__uint_as_float(kk.x), __uint_as_float(kk.y)), m2);
                                 float2 v = unpack2(y);
                                 if constexpr (!plain) {
@@ -578,8 +580,8 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                                 tc_ld_x32(s_at + h * 64 + 32, sb);
                                 tc_wait_ld();
                                 clear();
-                                weights(std::true_type{}, sa, P, kf + 16 * h, m, 0);
-                                weights(std::true_type{}, sb, P + (TWO ? 32 : 16), kf + 16 * h + 8, m, 0);
+                                weights(std::true_type{}, sa, P, kf + 16 * h, 0ull, m, 0);
+                                weights(std::true_type{}, sb, P + (TWO ? 32 : 16), kf + 16 * h + 8, 0ull, m, 0);
                                 if (passes()) break;
                                 add_up();
                                 if constexpr (TWO) {
@@ -595,7 +597,9 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                         for (; h < 2; ++h) {
                             const int seen = masked ? rel - 64 * h : TILE;   // columns of this half up to here are seen
                             const uint32_t sh = s_at + h * 64;
-                            const uint4* kh = kf + 16 * h;
+                            const uint4* kh = kf + 16 * h;           // the factors of the columns' scores,
+                            int next8 = 8;
+                            f32x2 f2 = rf2;                          // and of the row's
                             if (!scores_at(h)) break;
                             uint32_t sa[32], sb[32], P[32];
                             if (!fresh && __all_sync(0xFFFFFFFFu, seen < 0)) {       // behind the edge of all 32 rows
@@ -614,17 +618,24 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                                 if (move) {
                                     // the reference moves to the largest score so far, and what has been added up with it
                                     float most = -INFINITY;
-                                    auto largest = [&](const uint32_t (&s)[32], const uint4* k8, int seen) {
+                                    auto largest = [&](uint32_t (&s)[32], const uint4* k8, int seen) {
 #pragma unroll
                                         for (int e = 0; e < 16; ++e) {
                                             const uint4 kk = k8[e / 2];
-                                            const f32x2 y = mul2_loaded(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), rf2);
+                                            const f32x2 y = mul2_loaded(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), f2);
                                             const float2 v = unpack2(mul2(y, e & 1 ? pack2(__uint_as_float(kk.z), __uint_as_float(kk.w)) : pack2(__uint_as_float(kk.x), __uint_as_float(kk.y))));
+                                            s[2 * e] = __float_as_uint(v.x);
+                                            s[2 * e + 1] = __float_as_uint(v.y);
                                             most = max3(most, 2 * e <= seen ? v.x : -INFINITY, 2 * e + 1 <= seen ? v.y : -INFINITY);
                                         }
                                     };
                                     largest(sa, kh, seen);
                                     largest(sb, kh + 8, seen - 32);
+                                    // They are rounded now, and their difference to the largest is exact: a fused one would leave the product's
+                                    // last bits, which of scores past 2^31 alone make a weight infinite.
+                                    kh = reinterpret_cast<const uint4*>(smem + C::OFF_ONE);
+                                    next8 = 0;
+                                    f2 = pack2(1.0f, 1.0f);
                                     const float mn = fmaxf(m, most);
                                     const float alpha = ex2(m - mn);
                                     l *= alpha;
@@ -647,17 +658,16 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                                     }
                                 }
                                 clear();
-                                weights(std::false_type{}, sa, P, kh, m, seen);
+                                weights(std::false_type{}, sa, P, kh, f2, m, seen);
                                 if constexpr (TWO) {
                                     // (the scores are in registers: their place may be taken before it is known that these weights stay)
                                     store_two(P, sh);
-                                    weights(std::false_type{}, sb, P, kh + 8, m, seen - 32);
+                                    weights(std::false_type{}, sb, P, kh + next8, f2, m, seen - 32);
                                     store_two(P, sh + 16);
                                 } else {
-                                    weights(std::false_type{}, sb, P + 16, kh + 8, m, seen - 32);
+                                    weights(std::false_type{}, sb, P + 16, kh + next8, f2, m, seen - 32);
                                     tc_st_x32(sh, P);
                                 }
-                                // (scores of 2^27 and more may pass the limit by their rounding alone)
                                 move = passes();
                                 if (moved || !move) {
                                     add_up();
