@@ -592,8 +592,8 @@ moe_status moe_qk_rotate(const void* q, const void* k, int dtype, const int64_t*
  *     head) row, to 2^-17 of that below (to 2^-13 where rows of up to 2^4 times
  *     its size are handled with it).
  *   - A weight p[j] is rounded to bf16 for its product with v[j], by at most 2^-8
- *     of itself (2^-16 in calls with n_tokens * n_q_heads <= 1,024); the sum takes
- *     it unrounded.
+ *     of itself (2^-16 in a lane with n * n_q_heads <= 1,024, whatever else is in
+ *     the call); the sum takes it unrounded.
  *   - A key or value vector marked as not finite (scale byte 255), and a value
  *     vector with a scale byte above 246 (2^119; its values may pass bf16's range),
  *     make NaN of the results that see it.

@@ -16,7 +16,7 @@
 //     bf16 as good as below 1), and only then O and the sum are scaled down. A thread has a row to itself, so neither
 //     maximum nor sum needs another thread.
 // Scores, sums, O and the parts that the join adds up are fp32. Weights are rounded to bf16 for the second product, by at most
-// 2^-8 of each (the sum takes them before), far less than a value's own 2^-4; calls of few rows take what is left of them as a
+// 2^-8 of each (the sum takes them before), far less than a value's own 2^-4; lanes of few rows take what is left of them as a
 // second part (FEW_ROWS), to 2^-16. The output is rounded once.
 //
 // A unit is a block of 256 rows (128 at head_dim 256, where O fills TMEM) of a lane and kv head, whole tokens with all their
@@ -82,10 +82,13 @@ constexpr int TILE = 128;                        // cache rows a tile, and rows 
 // 134 / 132 us, 9 of 600 87 / 83), or WHOLE_TILES and there are at most two full units an SM (a prompt of 1024 43 / 33, two
 // 56 / 54, 200 single tokens over 1000 182 / 165; but three prompts 66 / 74, eight 134 / 144; a prompt of 2048 67 / 81).
 constexpr int SHORT_TILES = 5, WHOLE_TILES = 8;
-// Calls with at most so many rows (token, query head) have their weights in two bf16 parts: with so few, one part's roundings, which
-// are as large as the output's own, do not always average out to less (error against 64 bits up to 1.55 times that of fp32
-// rounded once, over 60 rows; 1.3 to 1.4 over many). One token in 30 lanes, 2 heads of 64 over 10,476 rows: 53 us in two
-// parts, 46 in one; 32 / 8 heads of 128 over 8,192 rows 165 / 145; 8 tokens over 300 rows 14 / 14.
+// Lanes with at most so many rows (new tokens times query heads) have their weights in two bf16 parts. One part is as coarse as the
+// output's own rounding, and over few rows that does not average out to less (error against 64 bits up to 1.55 times that of fp32
+// rounded once, over 60 rows; 1.3 to 1.4 over many). By the lane, so that what a token gets does not depend on the others in the call.
+// One / two parts: one token in 30 lanes, 2 heads of 64 over 10,476 rows 46 / 55 us; 64 lanes, 32 / 8 heads of 128 over 8,192 rows
+// 310 / 345; 33 lanes, of which 22 take one token, 233 / 243; 8 tokens over 300 rows 14 / 14. That the second form is there costs the
+// others too, in registers and instruction fetches (without it / with it: a prompt of 8,192 457 / 461, at head_dim 64 357 / 365, 24
+// prompts of 1,024 there 151 / 160).
 constexpr int FEW_ROWS = 1024;
 constexpr float NEVER = -3.402823466e38f;        // the reference of a row that has seen nothing: below any finite score
 constexpr float LIMIT = 8.0f;                    // log2 of the largest weight before the reference moves (4 or 16: no difference)
@@ -110,7 +113,7 @@ struct alignas(16) Part {
     int b, h, tok0, first;                       // lane, kv head, first token, its own row (as in Unit)
     int rows, nt, end, tiles;
     int t0, t1;                                  // t1 = 0: there are no more
-    int pad[2];
+    int two, pad;                                // whether its weights are in two parts (FEW_ROWS)
 };
 
 template <int D>
@@ -285,6 +288,7 @@ struct Unit {
     int rows, nt;                                // rows (token, head) of the unit; row tiles
     int end, tiles;                              // rows of the lane that it sees at all; tiles of them
     int units;                                   // of the lane
+    int two;                                     // whether its weights are in two parts (FEW_ROWS)
 };
 template <int D>
 MOE_DEV Unit unit_at(const ChunkArgs& a, int b, int u) {
@@ -303,6 +307,7 @@ MOE_DEV Unit unit_at(const ChunkArgs& a, int b, int u) {
     x.end = l.len > 0 ? x.first + tokens : 0;
     x.tiles = x.end > 0 ? (x.end + TILE - 1) / TILE : 1;
     x.units = a.c.n_kv_heads * blocks;
+    x.two = (int64_t)l.n * a.n_q <= FEW_ROWS;
     return x;
 }
 template <int D>
@@ -318,7 +323,7 @@ MOE_DEV Part next_part(const ChunkArgs& a, const Pos& end, Pos& at, int& units) 
         const Unit x = unit_at<D>(a, at.lane, at.unit);
         units = x.units;
         const int t1 = same_unit(at, end) ? min(end.tile, x.tiles) : x.tiles;
-        if (t1 > at.tile) return Part{x.b, x.h, x.tok0, x.first, x.rows, x.nt, x.end, x.tiles, at.tile, t1, {0, 0}};
+        if (t1 > at.tile) return Part{x.b, x.h, x.tok0, x.first, x.rows, x.nt, x.end, x.tiles, at.tile, t1, x.two, 0};
     }
 }
 
@@ -420,7 +425,7 @@ __device__ __noinline__ void cut_run(const ChunkArgs& a, unsigned long long* scr
     }
 }
 
-template <int D, bool TWO>                       // TWO: weights in two parts
+template <int D>
 __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkArgs a) {
     using C = Cfg<D>;
     constexpr int NK = C::NK, NR = C::NR, NB = C::NB, NSC = C::NSC, QB = C::QB, ROWS = C::ROWS;
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
         const int4* from = reinterpret_cast<const int4*>(smem + C::OFF_PD + (n % C::NPD) * sizeof(Part));
         *reinterpret_cast<int4*>(&p.b) = from[0];
         *reinterpret_cast<int4*>(&p.rows) = from[1];
-        *reinterpret_cast<int2*>(&p.t0) = *reinterpret_cast<const int2*>(from + 2);
+        *reinterpret_cast<int4*>(&p.t0) = from[2];
         __syncwarp();
         if (lane == 0) arrive_at(bar(C::B_PDEMPTY, n % C::NPD));
         return p.t1 > 0;
@@ -502,185 +507,226 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
                     float m = NEVER, l = 0.0f;
                     bool fresh = true;               // nothing has been added to O
                     uint32_t item = 0;
-                    for (int i = split ? (int)((items ^ (uint32_t)g) & 1) : 0; i < nt; i += split ? 2 : 1) {
-                        item = split ? items + i : items + i * x.nt + g;
-                        const uint32_t buf = item & 1, sc = (tiles + i) % NSC;
-                        const uint32_t s_at = trow + buf * TILE;
-                        const int j0 = (t0 + i) * TILE;
-                        const bool masked = j0 + TILE - 1 > open;
-                        const int rel = limit - j0;                  // columns up to rel are seen
-                        if (!warp_wait_at(bar(C::B_SCFULL, sc), ((tiles + i) / NSC) & 1, stop)) { ok = false; break; }
-                        auto scores_at = [&](int h) {
-                            if (!warp_wait_at(bar(C::B_SFULL, 2 * buf + h), (item >> 1) & 1, stop)) return ok = false;
-                            tc_fence_after();
-                            return true;
-                        };
-                        const uint4* kf = reinterpret_cast<const uint4*>(smem + C::OFF_SC + sc * C::SC_BYTES + 2 * TILE);
-                        // Half a tile at a time: its weights are at work, and the next tile's scores of that half are made, beside the
-                        // other half's softmax.
-                        auto publish = [&](int h) {
-                            tc_wait_st();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) arrive_at(bar(C::B_PFULL, 2 * buf + h));
-                        };
-                        // 32 columns of scores to weights
-                        f32x2 sum0, sum1;
-                        float top0, top1;
-                        auto weights = [&](auto plain, uint32_t (&s)[32], uint32_t* P, const uint4* k8, f32x2 f2, float m, int seen) {
-                            const f32x2 m2 = pack2(-m, -m);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const uint4 kk = k8[e / 2];
-                                f32x2 y = pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-                                if constexpr (!plain) y = mul2_loaded(y, f2);
-                                y = fma2_loaded(y, e & 1 ? pack2(__uint_as_float(kk.z), __uint_as_float(kk.w)) : pack2(__uint_as_float(kk.x), __uint_as_float(kk.y)), m2);
-                                float2 v = unpack2(y);
-                                if constexpr (!plain) {
-                                    if (2 * e > seen) v.x = -INFINITY;
-                                    if (2 * e + 1 > seen) v.y = -INFINITY;
-                                }
-                                const float p0 = ex2(v.x), p1 = ex2(v.y);
-                                if (e & 1) {
-                                    top1 = max3(top1, v.x, v.y);
-                                    sum1 = add2(sum1, pack2(p0, p1));
-                                } else {
-                                    top0 = max3(top0, v.x, v.y);
-                                    sum0 = add2(sum0, pack2(p0, p1));
-                                }
-                                P[e] = pack_bf16(p0, p1);
-                                if constexpr (TWO) P[16 + e] = pack_bf16(p0 - __uint_as_float(P[e] << 16), p1 - __uint_as_float(P[e] & 0xFFFF0000u));
-                            }
-                        };
-                        auto clear = [&]() {
-                            top0 = top1 = -INFINITY;
-                            sum0 = sum1 = 0ull;
-                        };
-                        auto passes = [&]() { return __any_sync(0xFFFFFFFFu, fmaxf(top0, top1) > LIMIT); };
-                        auto add_up = [&]() {
-                            const float2 p = unpack2(add2(sum0, sum1));
-                            l += p.x + p.y;
-                        };
-                        int h = 0;                   // the half that is to be done
-                        // Most tiles: no edge, no factor of the row's, the reference stays. (A form of its own: with branches within, the
-                        // scores are copied from where the loads leave them, two moves a pair. A loop, though the second half's scores
-                        // could come ahead: the instructions' cache is as scarce.)
-                        // 32 columns' weights, with their second parts behind
-                        auto store_two = [&](const uint32_t* P, uint32_t to) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 8)
-                                tc_st_x8(to + (e & 8) + (e & 16) * 2, make_uint4(P[e], P[e + 1], P[e + 2], P[e + 3]), make_uint4(P[e + 4], P[e + 5], P[e + 6], P[e + 7]));
-                        };
-                        if (!fresh && !masked && !rowwise)
+                    auto weigh = [&](auto two) {
+                        for (int i = split ? (int)((items ^ (uint32_t)g) & 1) : 0; i < nt; i += split ? 2 : 1) {
+                            item = split ? items + i : items + i * x.nt + g;
+                            const uint32_t buf = item & 1, sc = (tiles + i) % NSC;
+                            const uint32_t s_at = trow + buf * TILE;
+                            const int j0 = (t0 + i) * TILE;
+                            const bool masked = j0 + TILE - 1 > open;
+                            const int rel = limit - j0;                  // columns up to rel are seen
+                            if (!warp_wait_at(bar(C::B_SCFULL, sc), ((tiles + i) / NSC) & 1, stop)) { ok = false; break; }
+                            auto scores_at = [&](int h) {
+                                if (!warp_wait_at(bar(C::B_SFULL, 2 * buf + h), (item >> 1) & 1, stop)) return ok = false;
+                                tc_fence_after();
+                                return true;
+                            };
+                            const uint4* kf = reinterpret_cast<const uint4*>(smem + C::OFF_SC + sc * C::SC_BYTES + 2 * TILE);
+                            // Half a tile at a time: its weights are at work, and the next tile's scores of that half are made, beside the
+                            // other half's softmax.
+                            auto publish = [&](int h) {
+                                tc_wait_st();
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) arrive_at(bar(C::B_PFULL, 2 * buf + h));
+                            };
+                            // The reference moves to `most`, the largest score so far, and what has been added up with it.
+                            auto refer = [&](float most, int h) {
+                                const float mn = fmaxf(m, most);
+                                const float alpha = ex2(m - mn);
+                                l *= alpha;
+                                m = mn;
+                                if (fresh) return true;
+                                const uint32_t before_it = item - C::NT;
+                                if (h > 0 ? !warp_wait_at(bar(C::B_OHALF, buf), (item >> 1) & 1, stop)
+                                          : !warp_wait_at(bar(C::B_ODONE, before_it & 1), (before_it >> 1) & 1, stop)) return ok = false;
+                                tc_fence_after();
 #pragma unroll 1
-                            for (; h < 2; ++h) {
-                                if (!scores_at(h)) break;
-                                uint32_t sa[32], sb[32], P[TWO ? 64 : 32];
-                                tc_ld_x32(s_at + h * 64, sa);
-                                tc_ld_x32(s_at + h * 64 + 32, sb);
-                                tc_wait_ld();
-                                clear();
-                                weights(std::true_type{}, sa, P, kf + 16 * h, 0ull, m, 0);
-                                weights(std::true_type{}, sb, P + (TWO ? 32 : 16), kf + 16 * h + 8, 0ull, m, 0);
-                                if (passes()) break;
-                                add_up();
-                                if constexpr (TWO) {
-                                    store_two(P, s_at + 64 * h);
-                                    store_two(P + 32, s_at + 64 * h + 16);
-                                } else {
-                                    tc_st_x32(s_at + 64 * h, P);
+                                for (int c = 0; c < D / 16; ++c) {
+                                    uint32_t o[16];
+                                    tc_load(o_at + c * 16, o);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                    tc_st_x8(o_at + c * 16, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
+                                    tc_st_x8(o_at + c * 16 + 8, make_uint4(o[8], o[9], o[10], o[11]), make_uint4(o[12], o[13], o[14], o[15]));
                                 }
-                                publish(h);
-                            }
-                        if (!ok) break;
-#pragma unroll 1
-                        for (; h < 2; ++h) {
-                            const int seen = masked ? rel - 64 * h : TILE;   // columns of this half up to here are seen
-                            const uint32_t sh = s_at + h * 64;
-                            const uint4* kh = kf + 16 * h;           // the factors of the columns' scores,
-                            int next8 = 8;
-                            f32x2 f2 = rf2;                          // and of the row's
-                            if (!scores_at(h)) break;
-                            uint32_t sa[32], sb[32], P[32];
-                            if (!fresh && __all_sync(0xFFFFFFFFu, seen < 0)) {       // behind the edge of all 32 rows
+                                tc_wait_st();
+                                return true;
+                            };
+                            // 32 columns of scores to weights
+                            f32x2 sum0, sum1;
+                            float top0, top1;
+                            auto weights = [&](auto plain, uint32_t (&s)[32], uint32_t* P, const uint4* k8, f32x2 f2, float m, int seen) {
+                                const f32x2 m2 = pack2(-m, -m);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) P[e] = 0u;
-                                tc_st_x32(sh, P);
-                                if constexpr (TWO) tc_st_x32(sh + 32, P);
-                                publish(h);
-                                continue;
-                            }
-                            tc_ld_x32(sh, sa);
-                            tc_ld_x32(sh + 32, sb);
-                            tc_wait_ld();
-                            bool move = fresh;
-                            for (bool moved = false;; moved = true) {
-                                if (move) {
-                                    // the reference moves to the largest score so far, and what has been added up with it
-                                    float most = -INFINITY;
-                                    auto largest = [&](uint32_t (&s)[32], const uint4* k8, int seen) {
-#pragma unroll
-                                        for (int e = 0; e < 16; ++e) {
-                                            const uint4 kk = k8[e / 2];
-                                            const f32x2 y = mul2_loaded(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), f2);
-                                            const float2 v = unpack2(mul2(y, e & 1 ? pack2(__uint_as_float(kk.z), __uint_as_float(kk.w)) : pack2(__uint_as_float(kk.x), __uint_as_float(kk.y))));
-                                            s[2 * e] = __float_as_uint(v.x);
-                                            s[2 * e + 1] = __float_as_uint(v.y);
-                                            most = max3(most, 2 * e <= seen ? v.x : -INFINITY, 2 * e + 1 <= seen ? v.y : -INFINITY);
-                                        }
-                                    };
-                                    largest(sa, kh, seen);
-                                    largest(sb, kh + 8, seen - 32);
-                                    // They are rounded now, and their difference to the largest is exact: a fused one would leave the product's
-                                    // last bits, which of scores past 2^31 alone make a weight infinite.
-                                    kh = reinterpret_cast<const uint4*>(smem + C::OFF_ONE);
-                                    next8 = 0;
-                                    f2 = pack2(1.0f, 1.0f);
-                                    const float mn = fmaxf(m, most);
-                                    const float alpha = ex2(m - mn);
-                                    l *= alpha;
-                                    m = mn;
-                                    if (!fresh) {
-                                        const uint32_t before_it = item - C::NT;
-                                        if (h > 0 ? !warp_wait_at(bar(C::B_OHALF, buf), (item >> 1) & 1, stop)
-                                                  : !warp_wait_at(bar(C::B_ODONE, before_it & 1), (before_it >> 1) & 1, stop)) { ok = false; break; }
-                                        tc_fence_after();
-#pragma unroll 1
-                                        for (int c = 0; c < D / 16; ++c) {
-                                            uint32_t o[16];
-                                            tc_load(o_at + c * 16, o);
-#pragma unroll
-                                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                            tc_st_x8(o_at + c * 16, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
-                                            tc_st_x8(o_at + c * 16 + 8, make_uint4(o[8], o[9], o[10], o[11]), make_uint4(o[12], o[13], o[14], o[15]));
-                                        }
-                                        tc_wait_st();
+                                for (int e = 0; e < 16; ++e) {
+                                    const uint4 kk = k8[e / 2];
+                                    f32x2 y = pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+                                    if constexpr (!plain) y = mul2_loaded(y, f2);
+                                    y = fma2_loaded(y, e & 1 ? pack2(__uint_as_float(kk.z), __uint_as_float(kk.w)) : pack2(__uint_as_float(kk.x), __uint_as_float(kk.y)), m2);
+                                    float2 v = unpack2(y);
+                                    if constexpr (!plain) {
+                                        if (2 * e > seen) v.x = -INFINITY;
+                                        if (2 * e + 1 > seen) v.y = -INFINITY;
                                     }
+                                    const float p0 = ex2(v.x), p1 = ex2(v.y);
+                                    if (e & 1) {
+                                        top1 = max3(top1, v.x, v.y);
+                                        sum1 = add2(sum1, pack2(p0, p1));
+                                    } else {
+                                        top0 = max3(top0, v.x, v.y);
+                                        sum0 = add2(sum0, pack2(p0, p1));
+                                    }
+                                    P[e] = pack_bf16(p0, p1);
                                 }
-                                clear();
-                                weights(std::false_type{}, sa, P, kh, f2, m, seen);
-                                if constexpr (TWO) {
-                                    // (the scores are in registers: their place may be taken before it is known that these weights stay)
-                                    store_two(P, sh);
-                                    weights(std::false_type{}, sb, P, kh + next8, f2, m, seen - 32);
-                                    store_two(P, sh + 16);
-                                } else {
-                                    weights(std::false_type{}, sb, P + 16, kh + next8, f2, m, seen - 32);
-                                    tc_st_x32(sh, P);
-                                }
-                                move = passes();
-                                if (moved || !move) {
+                            };
+                            auto clear = [&]() {
+                                top0 = top1 = -INFINITY;
+                                sum0 = sum1 = 0ull;
+                            };
+                            auto passes = [&]() { return __any_sync(0xFFFFFFFFu, fmaxf(top0, top1) > LIMIT); };
+                            auto add_up = [&]() {
+                                const float2 p = unpack2(add2(sum0, sum1));
+                                l += p.x + p.y;
+                            };
+                            int h = 0;                   // the half that is to be done
+                            if constexpr (two) {
+                                // Weights in two parts, in one form: the scores in place of what the MMA left, their largest, then the weights, eight
+                                // columns' first and second parts at a time (all at once would not fit the registers).
+#pragma unroll 1
+                                for (; h < 2; ++h) {
+                                    const uint32_t sh = s_at + h * 64;
+                                    const uint4* kh = kf + 16 * h;
+                                    if (!scores_at(h)) break;
+                                    uint32_t s[64];
+                                    tc_ld_x32(sh, *reinterpret_cast<uint32_t (*)[32]>(s));
+                                    tc_ld_x32(sh + 32, *reinterpret_cast<uint32_t (*)[32]>(s + 32));
+                                    tc_wait_ld();
+                                    clear();
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) {
+                                        const uint4 kk = kh[e / 2];
+                                        const f32x2 y = mul2_loaded(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), rf2);
+                                        const float2 v = unpack2(mul2(y, e & 1 ? pack2(__uint_as_float(kk.z), __uint_as_float(kk.w)) : pack2(__uint_as_float(kk.x), __uint_as_float(kk.y))));
+                                        s[2 * e] = __float_as_uint(v.x);
+                                        s[2 * e + 1] = __float_as_uint(v.y);
+                                    }
+                                    if (masked) {
+                                        const int seen = rel - 64 * h;
+#pragma unroll
+                                        for (int e = 0; e < 64; ++e)
+                                            if (e > seen) s[e] = 0xFF800000u;
+                                    }
+#pragma unroll
+                                    for (int e = 0; e < 64; e += 4) {
+                                        top0 = max3(top0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                                        top1 = max3(top1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+                                    }
+                                    const float most = fmaxf(top0, top1);
+                                    if ((fresh || __any_sync(0xFFFFFFFFu, most > m + LIMIT)) && !refer(most, h)) break;
+                                    const f32x2 m2 = pack2(-m, -m);
+#pragma unroll
+                                    for (int e = 0; e < 64; e += 16) {
+                                        uint32_t P[16];
+#pragma unroll
+                                        for (int z = 0; z < 8; ++z) {
+                                            const float2 v = unpack2(add2(pack2(__uint_as_float(s[e + 2 * z]), __uint_as_float(s[e + 2 * z + 1])), m2));
+                                            const float p0 = ex2(v.x), p1 = ex2(v.y);
+                                            if (z & 1) sum1 = add2(sum1, pack2(p0, p1)); else sum0 = add2(sum0, pack2(p0, p1));
+                                            P[z] = pack_bf16(p0, p1);
+                                            P[8 + z] = pack_bf16(p0 - __uint_as_float(P[z] << 16), p1 - __uint_as_float(P[z] & 0xFFFF0000u));
+                                        }
+                                        tc_st_x8(sh + e / 2, make_uint4(P[0], P[1], P[2], P[3]), make_uint4(P[4], P[5], P[6], P[7]));
+                                        tc_st_x8(sh + 32 + e / 2, make_uint4(P[8], P[9], P[10], P[11]), make_uint4(P[12], P[13], P[14], P[15]));
+                                    }
                                     add_up();
-                                    break;
+                                    publish(h);
+                                    fresh = false;
+                                }
+                            } else {
+                                // Most tiles: no edge, no factor of the row's, the reference stays. (A form of its own: with branches within, the
+                                // scores are copied from where the loads leave them, two moves a pair. A loop, though the second half's scores
+                                // could come ahead: the instructions' cache is as scarce.)
+                                if (!fresh && !masked && !rowwise)
+#pragma unroll 1
+                                    for (; h < 2; ++h) {
+                                        if (!scores_at(h)) break;
+                                        uint32_t sa[32], sb[32], P[32];
+                                        tc_ld_x32(s_at + h * 64, sa);
+                                        tc_ld_x32(s_at + h * 64 + 32, sb);
+                                        tc_wait_ld();
+                                        clear();
+                                        weights(std::true_type{}, sa, P, kf + 16 * h, 0ull, m, 0);
+                                        weights(std::true_type{}, sb, P + 16, kf + 16 * h + 8, 0ull, m, 0);
+                                        if (passes()) break;
+                                        add_up();
+                                        tc_st_x32(s_at + 64 * h, P);
+                                        publish(h);
+                                    }
+                                if (!ok) break;
+#pragma unroll 1
+                                for (; h < 2; ++h) {
+                                    const int seen = masked ? rel - 64 * h : TILE;   // columns of this half up to here are seen
+                                    const uint32_t sh = s_at + h * 64;
+                                    const uint4* kh = kf + 16 * h;           // the factors of the columns' scores,
+                                    int next8 = 8;
+                                    f32x2 f2 = rf2;                          // and of the row's
+                                    if (!scores_at(h)) break;
+                                    uint32_t sa[32], sb[32], P[32];
+                                    if (!fresh && __all_sync(0xFFFFFFFFu, seen < 0)) {       // behind the edge of all 32 rows
+#pragma unroll
+                                        for (int e = 0; e < 32; ++e) P[e] = 0u;
+                                        tc_st_x32(sh, P);
+                                        publish(h);
+                                        continue;
+                                    }
+                                    tc_ld_x32(sh, sa);
+                                    tc_ld_x32(sh + 32, sb);
+                                    tc_wait_ld();
+                                    bool move = fresh;
+                                    for (bool moved = false;; moved = true) {
+                                        if (move) {
+                                            float most = -INFINITY;
+                                            auto largest = [&](uint32_t (&s)[32], const uint4* k8, int seen) {
+#pragma unroll
+                                                for (int e = 0; e < 16; ++e) {
+                                                    const uint4 kk = k8[e / 2];
+                                                    const f32x2 y = mul2_loaded(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), f2);
+                                                    const float2 v = unpack2(mul2(y, e & 1 ? pack2(__uint_as_float(kk.z), __uint_as_float(kk.w)) : pack2(__uint_as_float(kk.x), __uint_as_float(kk.y))));
+                                                    s[2 * e] = __float_as_uint(v.x);
+                                                    s[2 * e + 1] = __float_as_uint(v.y);
+                                                    most = max3(most, 2 * e <= seen ? v.x : -INFINITY, 2 * e + 1 <= seen ? v.y : -INFINITY);
+                                                }
+                                            };
+                                            largest(sa, kh, seen);
+                                            largest(sb, kh + 8, seen - 32);
+                                            // They are rounded now, and their difference to the largest is exact: a fused one would leave the product's
+                                            // last bits, which of scores past 2^31 alone make a weight infinite.
+                                            kh = reinterpret_cast<const uint4*>(smem + C::OFF_ONE);
+                                            next8 = 0;
+                                            f2 = pack2(1.0f, 1.0f);
+                                            if (!refer(most, h)) break;
+                                        }
+                                        clear();
+                                        weights(std::false_type{}, sa, P, kh, f2, m, seen);
+                                        weights(std::false_type{}, sb, P + 16, kh + next8, f2, m, seen - 32);
+                                        tc_st_x32(sh, P);
+                                        move = passes();
+                                        if (moved || !move) {
+                                            add_up();
+                                            break;
+                                        }
+                                    }
+                                    if (!ok) break;
+                                    publish(h);
+                                    fresh = false;
                                 }
                             }
                             if (!ok) break;
-                            publish(h);
-                            fresh = false;
+                            if (lane == 0) arrive_at_n(bar(C::B_SCEMPTY, sc), x.nt == 2 ? 1 : 2);
                         }
-                        if (!ok) break;
-                        if (lane == 0) arrive_at_n(bar(C::B_SCEMPTY, sc), x.nt == 2 ? 1 : 2);
-                    }
+                    };
+                    if (__builtin_expect(x.two, 0)) weigh(std::true_type{}); else weigh(std::false_type{});
                     if (!ok) break;
                     // ---- the part's output
                     if (!fresh && !warp_wait_at(bar(C::B_ODONE, item & 1), (item >> 1) & 1, stop)) break;
@@ -1076,6 +1122,7 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
             Part x;
             for (; ok && part_at(piece, x); ++piece) {
                 const int nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0), tiles = __shfl_sync(0xFFFFFFFFu, x.t1 - x.t0, 0);
+                const int two = __shfl_sync(0xFFFFFFFFu, x.two, 0);
                 const uint32_t last = item + tiles * nt;
                 if (mine < last && !warp_wait_at(bar(C::B_QFULL, piece % QB), (piece / QB) & 1, stop)) break;
                 // This buffer's halves of the part in a row: half z's output, then the scores of half z + 2, which take its place in TMEM.
@@ -1121,7 +1168,7 @@ __global__ void __launch_bounds__(640, 1) chunk_attention(const __grid_constant_
 #pragma unroll
                                 for (int kk = 0; kk < C::VR / 16; ++kk)
                                     tc_mma_f16_ts(o, p + pc * (C::VR / 2) + kk * 8, desc(VD, v[pc] + kk * (2048 >> 4)), ID_PV, pc == 0 && kk == 0 ? add : 1u);
-                                if constexpr (TWO)
+                                if (two)
 #pragma unroll
                                     for (int kk = 0; kk < C::VR / 16; ++kk)
                                         tc_mma_f16_ts(o, p + 32 + pc * (C::VR / 2) + kk * 8, desc(VD, v[pc] + kk * (2048 >> 4)), ID_PV, 1u);
@@ -1397,19 +1444,17 @@ cudaError_t launch(ChunkArgs a, cudaStream_t s) {
     cudaError_t e = codes_map(&maps.k, a.c.k_codes, a.c, C::ROWB, TILE, C::ROWB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     if (e == cudaSuccess) e = codes_map(&maps.v, a.c.v_codes, a.c, D, C::VR, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e != cudaSuccess) return e;
-    const bool few = (int64_t)a.n_tokens * a.n_q <= FEW_ROWS;
-    const auto kernel = few ? chunk_attention<D, true> : chunk_attention<D, false>;
-    static bool attr_set[2][64] = {};
+    static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
-    if (dev >= 0 && dev < 64 && !attr_set[few][dev]) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+        e = cudaFuncSetAttribute(chunk_attention<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
-        attr_set[few][dev] = true;
+        attr_set[dev] = true;
     }
     const int ctas = moe_sm_count();
     moe_prof_begin(MK_CHUNK_ATTENTION, s);
-    e = moe_launch(kernel, dim3((unsigned)ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
+    e = moe_launch(chunk_attention<D>, dim3((unsigned)ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
     moe_prof_end(MK_CHUNK_ATTENTION, s);
     moe_count_launches(1);
     if (e != cudaSuccess || ctas < 2 || a.whole) return e;
