@@ -67,9 +67,9 @@ class LanePages:
 class DevicePages:
     """Pages of a cache by lane, kept on the device: the state and the outputs of ``moe_page_plan``.
 
-    ``plan`` gives every lane room for its new tokens; ``kv_len``, ``cu``, ``positions`` and ``slots`` (of `max_tokens`
-    tokens) then belong to that batch, and ``advance`` keeps its rows. ``table`` int32 [lanes, width]; every layer's cache uses
-    the same one. Nothing here waits for the device."""
+    ``plan`` gives every lane room for its new tokens; ``kv_len``, ``cu``, ``positions``, ``slots`` and ``idle`` (of `max_tokens`
+    tokens; idle: past the last token, or of a lane that was not served) then belong to that batch, and ``advance`` keeps its rows.
+    ``table`` int32 [lanes, width]; every layer's cache uses the same one. Nothing here waits for the device."""
 
     def __init__(self, lanes: int, n_pages: int, page_size: int, width: int, max_tokens: int, device="cuda"):
         i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
@@ -80,12 +80,14 @@ class DevicePages:
         self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=device)
         self.positions = i32(max_tokens)
         self.slots = torch.full((max_tokens,), -1, dtype=torch.int64, device=device)
+        self.idle = torch.ones(max_tokens, dtype=torch.bool, device=device)
 
     def plan(self, n_new: torch.Tensor) -> None:
         """n_new int32 [lanes] on the device: new tokens of each lane; 0: it waits; below 0: it is done, and its pages are free.
         A lane that cannot be served (no pages, no place) gets kv_len 0 and no slots, and the device status says so."""
         moe_page_plan(n_new, self.rows, self.held, self.table, self.free, self.n_free, self.page_size, self.kv_len, self.cu,
                       self.positions, self.slots)
+        torch.lt(self.slots, 0, out=self.idle)
 
     def advance(self) -> None:
         """The rows of the batch planned last are kept (those of lanes that were not served stay as they were)."""
@@ -162,7 +164,7 @@ class DecodeLayer:
         self.w_qkv, self.w_out, self.cache, self.moe_args, self.buf = w_qkv, w_out, cache, moe_args, buf
         self.heads, self.scale, self.norms, self.lanes = n_q_heads, cache.head_dim ** -0.5, norms, lanes
         self.chunk_workspace = None          # of the first chunk on
-        self.out = torch.empty((max_tokens, n_q_heads, cache.head_dim), dtype=torch.bfloat16, device=w_qkv.device)
+        self.out = torch.zeros((max_tokens, n_q_heads, cache.head_dim), dtype=torch.bfloat16, device=w_qkv.device)
         self.workspace = torch.empty(moe_tree_attention_workspace_bytes(max_tokens, n_q_heads, cache.n_kv_heads, cache.head_dim, lanes),
                                      dtype=torch.uint8, device=w_qkv.device)
 
@@ -179,9 +181,12 @@ class DecodeLayer:
         return self._experts(hidden, out)
 
     def chunk(self, hidden: torch.Tensor, pages: DevicePages) -> torch.Tensor:
-        """hidden bf16 [n, d] of the n new tokens that `pages` has planned last, lane by lane; returns the layer's bf16
-        output. (Tokens of lanes that were not served attend to nothing.)"""
+        """hidden bf16 [n, d] of the new tokens that `pages` has planned last, lane by lane; returns the layer's bf16 output.
+        It may have rows behind them (a batch of one size, for a captured graph): what comes out there means nothing, nor what
+        comes out for lanes that were not served, whose tokens attend to nothing; neither is counted as demand."""
         n, H, D = hidden.shape[0], self.cache.n_kv_heads, self.cache.head_dim
+        if n > min(self.out.shape[0], pages.slots.shape[0]):
+            raise ValueError(f"{n} tokens: the layer has places for {self.out.shape[0]}, the plan for {pages.slots.shape[0]}")
         if n == 0:
             return torch.empty_like(hidden)
         if self.chunk_workspace is None:
@@ -190,7 +195,7 @@ class DecodeLayer:
         q = self._write(hidden, pages.positions[:n], pages.slots[:n])
         out = self.out[:n]
         moe_chunk_attention(q, self.cache, pages.table, pages.kv_len, pages.cu, self.scale, out, self.chunk_workspace)
-        return self._experts(hidden, out)
+        return self._experts(hidden, out, pages.idle[:n])
 
     def _write(self, hidden: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
         """Queries of the tokens; their keys and values are in the cache."""
@@ -204,11 +209,12 @@ class DecodeLayer:
         moe_kv_write(k, v, slots, self.cache)
         return q
 
-    def _experts(self, hidden: torch.Tensor, out: torch.Tensor) -> torch.Tensor:
+    def _experts(self, hidden: torch.Tensor, out: torch.Tensor, idle: torch.Tensor | None = None) -> torch.Tensor:
         n = hidden.shape[0]
         x = hidden + out.view(n, -1) @ self.w_out.T
         w_router, bias, slot_of, arena, demand, miss_max, layer = self.moe_args
-        return (x + layer_step(x, w_router, bias, slot_of, arena, demand, miss_max, layer, _first_rows(self.buf, n))).to(torch.bfloat16)
+        y = layer_step(x, w_router, bias, slot_of, arena, demand, miss_max, layer, _first_rows(self.buf, n), idle=idle)
+        return (x + y).to(torch.bfloat16)
 
     def keep(self, tables: Step, path: torch.Tensor, n_keep: torch.Tensor) -> None:
         """Keep the accepted nodes path[b, :n_keep[b]] (ascending) of every lane in this layer's cache."""

@@ -36,7 +36,7 @@ class LayerBuffers:
 
 def layer_step(hidden: torch.Tensor, w_router: torch.Tensor, bias, slot_of: torch.Tensor, arena: Arena,
                demand: torch.Tensor, miss_max: torch.Tensor, layer: int, buf: LayerBuffers, stream=None,
-               side=None, out: torch.Tensor | None = None, prefetch: bool = False) -> torch.Tensor:
+               side=None, out: torch.Tensor | None = None, prefetch: bool = False, idle: torch.Tensor | None = None) -> torch.Tensor:
     """route -> demand -> expert FFN; returns the output (fp32 [T, d]): buf.out, or `out` when given.
 
     `hidden` and `out` may be pinned host tensors: the kernels then read the
@@ -52,10 +52,17 @@ def layer_step(hidden: torch.Tensor, w_router: torch.Tensor, bias, slot_of: torc
     single token through one layer with a cold L2 (about 1 us of 50); from
     two tokens on, and through consecutive layers, it competes with the
     gate/up GEMM for HBM and the step is slower.
+
+    `idle` bool [T]: tokens that stand for nothing (the rest of a padded batch,
+    those of a lane that was not served). Their picks are no demand: their
+    rows of ``buf.want_e`` become -1.
     """
     main = torch.cuda.current_stream() if stream is None else stream
     moe_route_resident(hidden, w_router, bias, slot_of, buf.k, buf.want_e, buf.want_s, buf.sel_e, buf.sel_slot,
                        buf.sel_w, buf.workspace, main)
+    if idle is not None:
+        with torch.cuda.stream(main):
+            buf.want_e.masked_fill_(idle.unsqueeze(1), -1)
     if side is None:
         moe_demand_accumulate(buf.want_e, buf.want_s, slot_of, layer, demand, miss_max, main)
     else:
