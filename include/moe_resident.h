@@ -569,7 +569,8 @@ moe_status moe_page_plan(const int32_t* n_new, int32_t* rows, int32_t* held, int
  * with the same strides; otherwise nothing overlaps. positions int32 [n_tokens];
  * q_weight, k_weight fp32 [head_dim], 16-byte aligned, or NULL. One of the two head
  * counts may be 0.
- * Sums are fp32 (values above 2^60 in size overflow the mean square); one rounding.
+ * Sums are fp32 (values above 2^60 in size overflow the mean square, and those below
+ * 2^-63 are lost from it); one rounding.
  * n_tokens = 0 returns MOE_OK without a launch. Limits: head_dim 64, 128 or 256,
  * n_pairs a multiple of 8, up to half of head_dim (0: norms alone); heads <= 65,536 each,
  * n_tokens * (n_q_heads + n_k_heads) <= 2^31.

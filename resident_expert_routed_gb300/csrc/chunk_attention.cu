@@ -36,12 +36,14 @@
 // What bounds it at head_dim 128: 128 cache rows take the two row tiles about 3,300 clocks, and shared memory is busy for nearly
 // all of them: 336 KB of operands (2,690 clocks: the queries and keys once for each row tile and half 192 KB, values for each row
 // tile 64, through the conversion 48, copies 32) and 512 reads of the columns' factors. The tensor cores work 2,050 of them, the
-// softmax issues for 2,000 on each of the SM's four schedulers. 1,024 tokens over 65,536 rows (32 / 8 heads) take 767 us, 1,445
-// TFLOP/s; over and over they draw 1.4 kW and the clock falls: 855 us. A prompt of 8,192 takes 457 us, 1,200 TFLOP/s: the edge,
-// a unit's first tile, its queries and its output, some 9 us a unit, are what its 6.7 units a CTA pay. At head_dim 64 the
-// instructions of softmax and issue bound it (a prompt 355 us), at 256 the conversion, which serves 128 rows there, and shared
-// memory (978 us). Single tokens over 8,192 rows, 64 lanes: 310 us, 3.5 TB/s, the conversion. 300 tokens take 14 us, of which 3 to
-// find the parts, 4 to bring and split the queries and 2 for a first tile's scores.
+// softmax issues for 2,000 on each of the SM's four schedulers. 1,024 tokens over 65,536 rows (32 / 8 heads) take 778 us, 1,425
+// TFLOP/s; over and over they draw 1.4 kW and the clock falls: 870 us. A prompt of 8,192 takes 461 us, 1,195 TFLOP/s: the edge,
+// a unit's first tile, its queries and its output, some 9 us a unit, are what its 6.7 units a CTA pay. At head_dim 64 nothing is
+// near its limit (issue slots 64 %, tensor cores 33 %, a prompt 365 us): softmax and issue wait for one another, and for short prompts
+// one instruction fetch in six misses its cache. At 256 (990 us) the conversion serves 128 rows only, and the tensor cores are at 49 %.
+// Single tokens over 8,192 rows, 64 lanes: 345 us, 3.2 TB/s, the conversion of a tile for the 4 rows that use it; issue slots 71 %,
+// tensor cores 53 % (without the softmax of warps whose rows are nobody's 343). 300 tokens take 14.6 us in a table of as many rows, of which 3 to find the parts, 4 to bring and split the
+// queries and 2 for a first tile's scores; in a table for 8,192 rows 23 us (SHORT_TILES).
 // The instructions' cache is as scarce as anything: loops that are not unrolled, and code in one place, are faster in most places.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -80,7 +82,9 @@ struct ChunkMaps {
 constexpr int TILE = 128;                        // cache rows a tile, and rows a row tile
 // Units are not cut, and no parts joined, where the table has at most SHORT_TILES tiles (cut / whole: 40 prompts of 300 tokens
 // 134 / 132 us, 9 of 600 87 / 83), or WHOLE_TILES and there are at most two full units an SM (a prompt of 1024 43 / 33, two
-// 56 / 54, 200 single tokens over 1000 182 / 165; but three prompts 66 / 74, eight 134 / 144; a prompt of 2048 67 / 81).
+// 56 / 54, 200 single tokens over 1000 182 / 165; but three prompts 66 / 74, eight 134 / 144; a prompt of 2048 67 / 81). The host
+// has the table's width and not the lanes' lengths, so a short prompt in a wide table is cut: 300 tokens 23 us for 14.6, 1024 35 for 28,
+// 16 tokens 13.0 for 10.8, 40 prompts of 300 132 for 128 (back to back in a graph; tables of 8,192 and of 131,072 rows alike).
 constexpr int SHORT_TILES = 5, WHOLE_TILES = 8;
 // Lanes with at most so many rows (new tokens times query heads) have their weights in two bf16 parts. One part is as coarse as the
 // output's own rounding, and over few rows that does not average out to less (error against 64 bits up to 1.55 times that of fp32
@@ -88,7 +92,7 @@ constexpr int SHORT_TILES = 5, WHOLE_TILES = 8;
 // One / two parts: one token in 30 lanes, 2 heads of 64 over 10,476 rows 46 / 55 us; 64 lanes, 32 / 8 heads of 128 over 8,192 rows
 // 310 / 345; 33 lanes, of which 22 take one token, 233 / 243; 8 tokens over 300 rows 14 / 14. That the second form is there costs the
 // others too, in registers and instruction fetches (without it / with it: a prompt of 8,192 457 / 461, at head_dim 64 357 / 365, 24
-// prompts of 1,024 there 151 / 160).
+// prompts of 1,024 there 151 / 160; at 256 980 / 990). Figures beside the other choices of this file were taken without it.
 constexpr int FEW_ROWS = 1024;
 constexpr float NEVER = -3.402823466e38f;        // the reference of a row that has seen nothing: below any finite score
 constexpr float LIMIT = 8.0f;                    // log2 of the largest weight before the reference moves (4 or 16: no difference)

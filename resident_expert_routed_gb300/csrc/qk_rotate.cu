@@ -10,9 +10,11 @@
 //
 // HBM bounds the large calls: each value is read and written once. A lane holds eight whole pairs (so that no value has to be
 // fetched from a neighbour), D / 16 lanes a vector; a warp takes a token's heads in turn, with the token's sines and cosines
-// computed once (through shared memory: a pair's by one lane) and kept in registers. One vector more is under way a lane; the
-// loads in flight, and not the arithmetic, are what is left: 8,192 tokens of 32 + 8 heads of 128, bf16, with norms take 36.1 us
-// in a graph, 4.65 TB/s (without norms 33.0), in fp32 4,096 tokens 31.2 us, 5.4 TB/s; two tokens take 2.1 us.
+// computed once (through shared memory: a pair's by one lane) and kept in registers. One vector more is under way a lane, in
+// registers, of which 91 a thread leave 16.5 warps an SM (issue slots 49 %, DRAM 43 % as counted, part of it in L2): 8,192 tokens of
+// 32 + 8 heads of 128, bf16, with norms take 36.1 us in a graph, 4.65 TB/s (without norms 33.0), in fp32, where a lane has twice the
+// bytes under way, 4,096 tokens 31.2 us, 5.4 TB/s; two tokens take 2.1 us. More bytes under way in 16 bits, through shared
+// memory, were not tried.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -21,8 +21,9 @@ def rotary_frequencies(turned: int, base: float = 10000.0, stretch: float = 1.0,
 
     stretch > 1 reaches that many times the trained length. rule "linear": every frequency divided by it. "base": the
     base raised so that the slowest frequency is divided by it and the fastest stays. "ramp": pairs that turn less than
-    `slow` times in the trained length are divided, those of more than `fast` turns stay, a linear ramp between (the
-    factor for the turned values that goes with it is ``rotary_magnitude``)."""
+    `slow` times in the trained length are divided, those of more than `fast` turns stay, between them a ramp that is linear
+    in the turns (the factor for the turned values that goes with it is ``rotary_magnitude``). Checkpoints whose ramp is
+    linear in the pair's index have other frequencies between the two: ``rotary_turns`` takes any list."""
     if turned < 2 or turned % 2 or not base > 1.0 or not stretch >= 1.0 or rule not in ("linear", "base", "ramp") or not fast > slow:
         raise ValueError("turned: an even number from 2; base > 1; stretch >= 1; rule linear, base or ramp; fast > slow")
     if rule == "base" and stretch > 1.0:
